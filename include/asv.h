@@ -69,7 +69,8 @@ typedef enum {
   ASV_ERR_CUDA = 7       /* a CUDA runtime call or the launch failed (see asv_last_cuda_error) */
 } asv_status;
 
-typedef enum { ASV_F32 = 0, ASV_BF16 = 1 } asv_dtype;
+/* ASV_F16 is an element type of the paged cache only (the logits of the verification are fp32 or bf16). */
+typedef enum { ASV_F32 = 0, ASV_BF16 = 1, ASV_F16 = 2 } asv_dtype;
 
 typedef enum {
   ASV_MODE_ASYMSPEC = 0,
@@ -85,6 +86,9 @@ typedef enum {
 #define ASV_REQ_TIMEOUT 4u   /* a bounded wait of the staged kernel expired (its launch keeps every CTA
                                 resident, so this marks a fault, not a load condition): the request's
                                 outputs are unspecified and the workspace must be zero-filled again */
+#define ASV_REQ_BAD_PAGE 8u  /* a block-table entry the request needs lies outside [0, num_pages) */
+#define ASV_REQ_BAD_LEN 16u  /* indptr is not 0 <= start <= end <= N, cache_len is negative, or the tokens go
+                                past the block table's last page or the rotation table's last row */
 
 /* Human-readable name of a status code (static string). */
 const char* asv_status_string(asv_status s);
@@ -391,6 +395,103 @@ asv_status asymspec_sci_verify(const void* a, const void* b, const void* t, int 
                                float* out_lse, int32_t* out_sci_accept_len, int32_t* out_sci_tokens, float* out_jsd,
                                float* out_T, uint32_t* out_req_status, void* workspace, size_t ws_bytes,
                                cudaStream_t stream);
+
+/* ------------------------------------------------------------------ paged key/value cache
+ *
+ * The forwards whose logits the verification takes see a chunk of new tokens per request (K drafts
+ * and one more; one token in plain decoding; a piece of a prompt) next to the tokens the request has
+ * in its cache.  paged_kv_append writes the chunk's keys and values into the cache, paged_attention
+ * lets the chunk's queries attend over it.  Both take the batch in the same form and read all lengths
+ * on the device, so a decoding loop advances cache_len by accept_len + 1 without a host round trip and
+ * can be captured in a CUDA graph; rejected drafts' slots are written over by the next append.
+ *
+ * Both OR their ASV_REQ_* bits into out_req_status [B], which the caller zero-fills once and reads when
+ * it likes.  A request flagged ASV_REQ_BAD_LEN is left out: nothing of it is appended, its attention
+ * outputs are 0 and its log-sum-exps -inf (if its rows lie within [0, N)).  A token whose page is bad
+ * is not appended; the attention of a request with a bad page is unspecified (no access leaves the
+ * cache).  Rows that belong to no request have no outputs.
+ */
+
+/* The cache: k and v [num_pages, page_size, kv_heads, head_dim] of `dtype` (ASV_BF16 or ASV_F16), each
+ * head's row contiguous, the other dimensions at any positive strides (in elements; multiples of 8, the
+ * stride of a dimension of extent 1 is not looked at), so caches with the heads outside the slots need
+ * no copy.  page_size is a multiple of 8; head_dim a multiple of 8, at most 128; the base addresses are
+ * 16-byte aligned. */
+typedef struct {
+  void* k;
+  void* v;
+  int dtype;
+  int num_pages, page_size, kv_heads, head_dim;
+  int64_t k_stride_page, k_stride_slot, k_stride_head;
+  int64_t v_stride_page, v_stride_slot, v_stride_head;
+} asv_paged_cache;
+
+/* The batch: B requests whose N new tokens are packed, request b's in rows indptr[b] .. indptr[b + 1] - 1;
+ * before them the request has cache_len[b] tokens in the cache, so its token i has position
+ * cache_len[b] + i.  Position p lives in slot p % page_size of page block_table[b, p / page_size]; block
+ * table rows are `block_table_stride` elements apart and hold max_pages entries (entries past a request's
+ * last token are not looked at).  All device pointers. */
+typedef struct {
+  int B, N;
+  const int32_t* indptr;    /* [B + 1] */
+  const int32_t* cache_len; /* [B] */
+  const int32_t* block_table;
+  int max_pages;
+  int64_t block_table_stride;
+} asv_paged_batch;
+
+/* Packed rows [N, heads, head_dim] of the cache's element type: each head's row contiguous, strides in
+ * elements, positive multiples of 8; the base address is 16-byte aligned.  (q, k and v may be views of
+ * one projection's output.) */
+typedef struct {
+  void* data;
+  int64_t stride_token, stride_head;
+} asv_rows;
+
+/* Position rotation: row p of `table` ([max_position, dim] fp32, contiguous) holds cos of the dim / 2
+ * angles of position p, then their sines; dim is even, at most head_dim, and the head's entries from dim
+ * on pass unchanged.  Pair j is (x_j, x_{j + dim/2}), or (x_{2j}, x_{2j+1}) with `interleaved`; it becomes
+ * (a cos - b sin, b cos + a sin), formed in fp32 and rounded once. */
+typedef struct {
+  const float* table;
+  int dim, max_position;
+  int interleaved;
+} asv_rotary;
+
+/*
+ * paged_kv_append -- the chunk's keys (rotated) and values (as they are) into their slots of the cache,
+ * and the rotated queries to out_q.  rotary NULL: no rotation.  q and out_q both NULL: keys and values
+ * only (q_heads is then not looked at); out_q must not overlap q.  Two requests that share a page must not write
+ * the same slot.  One launch.
+ * Checks, in this order, before anything is queued: sizes (ASV_ERR_SHAPE), element type
+ * (ASV_ERR_DTYPE), for B > 0 and N > 0: the rotation's sizes (ASV_ERR_PARAM), alignment of pointers
+ * and strides (ASV_ERR_ALIGN; NULL counts as aligned), the required pointers (ASV_ERR_NULL).
+ */
+asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* k,
+                           const asv_rows* v, const asv_rows* q, const asv_rows* out_q, int q_heads,
+                           const asv_rotary* rotary, uint32_t* out_req_status, cudaStream_t stream);
+
+/*
+ * paged_attention -- attention of the chunk's queries over the cache, the chunk's own tokens (already
+ * appended) included.  Token i of request b, at position p = cache_len[b] + i, attends to positions
+ * j <= p, with window > 0 only to j > p - window; query head h reads key head h / (q_heads / kv_heads).
+ *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j)
+ * Products take the 16-bit inputs exactly and accumulate in fp32; the softmax is fp32, its weights are
+ * rounded to the cache's type for the product with v (their sum is not), and out is rounded once.
+ * What a slot outside every attended position holds (a page's unwritten tail, an evicted page's entry)
+ * does not matter, NaN included.
+ * q_heads is a multiple of kv_heads, at most 128 to one key head; scale is finite and > 0; window >= 0
+ * (0: none).  out_lse [N, q_heads] may be NULL.
+ * workspace: asv_paged_workspace_bytes(...) bytes, 256-byte aligned, zero-filled before its first use
+ * (asv_workspace_init); every call leaves it ready for the next.  Calls that may run at the same time
+ * must not share it.  One launch.
+ * Checks in the order of paged_kv_append's (scale and window are ASV_ERR_PARAM), then the workspace
+ * (ASV_ERR_WORKSPACE).
+ */
+size_t asv_paged_workspace_bytes(int q_heads, int kv_heads, int head_dim);
+asv_status paged_attention(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* q,
+                           const asv_rows* out, int q_heads, float scale, int window, float* out_lse,
+                           uint32_t* out_req_status, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -17,11 +17,15 @@ Entry points (same names as the C ABI):
                          Inference with Retrieval-Augmented Speculative Decoding", Key designs 2-4)
   sci_verify             E2-SCI JSD test against an adaptive threshold ("E2-SCI: Elastic
                          Edge-Cloud Speculative Decoding via Credit Inertia", Key design 3)
+  paged_kv_append        the new tokens' keys and values into a paged cache, rotated on the way
+  paged_attention        attention of a chunk of new tokens (one, K + 1 drafts, a prompt) over that
+                         cache: the forwards whose logits the verification takes
 """
 from __future__ import annotations
 
 from ._binding import (  # noqa: F401
     ASV_BF16,
+    ASV_F16,
     ASV_F32,
     DELTA_A,
     DELTA_A_MINUS_B,
@@ -35,7 +39,11 @@ from ._binding import (  # noqa: F401
     SweepOutput,
     asymspec_sci_verify,
     asymspec_verify_sweep,
+    PagedAppendOutput,
+    PagedAttentionOutput,
     REQ_BAD_DRAFT,
+    REQ_BAD_LEN,
+    REQ_BAD_PAGE,
     REQ_NONFINITE,
     REQ_TIMEOUT,
     AsvError,
@@ -51,6 +59,9 @@ from ._binding import (  # noqa: F401
     host_arena_bytes,
     library,
     library_path,
+    paged_attention,
+    paged_kv_append,
+    paged_workspace_bytes,
     query_plan,
     rapid_verify,
     sci_state_decode,

@@ -13,12 +13,15 @@ from . import nvcc_build as _build
 
 ASV_F32 = 0
 ASV_BF16 = 1
+ASV_F16 = 2  # paged cache only
 ASV_MODE_ASYMSPEC = 0
 ASV_MODE_RAPID = 1
 ASV_MODE_SCI = 2
 REQ_NONFINITE = 1
 REQ_BAD_DRAFT = 2
 REQ_TIMEOUT = 4
+REQ_BAD_PAGE = 8
+REQ_BAD_LEN = 16
 
 _STATUS = {0: "ASV_OK", 1: "ASV_ERR_NULL", 2: "ASV_ERR_SHAPE", 3: "ASV_ERR_ALIGN", 4: "ASV_ERR_DTYPE",
            5: "ASV_ERR_PARAM", 6: "ASV_ERR_WORKSPACE", 7: "ASV_ERR_CUDA"}
@@ -80,6 +83,25 @@ class _SciParamsC(C.Structure):
                 ("T_min", C.c_double), ("T_max", C.c_double), ("ewma_beta", C.c_double)]
 
 
+class _PagedCacheC(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int), ("num_pages", C.c_int),
+                ("page_size", C.c_int), ("kv_heads", C.c_int), ("head_dim", C.c_int)] + [
+                    (f"{t}_stride_{d}", C.c_int64) for t in "kv" for d in ("page", "slot", "head")]
+
+
+class _PagedBatchC(C.Structure):
+    _fields_ = [("B", C.c_int), ("N", C.c_int), ("indptr", C.c_void_p), ("cache_len", C.c_void_p),
+                ("block_table", C.c_void_p), ("max_pages", C.c_int), ("block_table_stride", C.c_int64)]
+
+
+class _RowsC(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_token", C.c_int64), ("stride_head", C.c_int64)]
+
+
+class _RotaryC(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("dim", C.c_int), ("max_position", C.c_int), ("interleaved", C.c_int)]
+
+
 def _declare(L):
     L.asv_status_string.argtypes = [_i]
     L.asv_status_string.restype = C.c_char_p
@@ -125,6 +147,13 @@ def _declare(L):
     L.sci_verify_ex.argtypes = [_vp, _vp, _i, _vp, _i, _i, _i, C.POINTER(_SciParamsC), C.POINTER(_SciStabC), _vp,
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     L.sci_verify_ex.restype = _i
+    rows, cache, batch = C.POINTER(_RowsC), C.POINTER(_PagedCacheC), C.POINTER(_PagedBatchC)
+    L.paged_kv_append.argtypes = [cache, batch, rows, rows, rows, rows, _i, C.POINTER(_RotaryC), _vp, _vp]
+    L.paged_kv_append.restype = _i
+    L.asv_paged_workspace_bytes.argtypes = [_i, _i, _i]
+    L.asv_paged_workspace_bytes.restype = _sz
+    L.paged_attention.argtypes = [cache, batch, rows, rows, _i, _f, _i, _vp, _vp, _vp, _sz, _vp]
+    L.paged_attention.restype = _i
 
 
 def _check(status: int, what: str):
@@ -515,4 +544,170 @@ def sci_verify(draft: torch.Tensor, target: torch.Tensor, draft_ids: torch.Tenso
                                  _ptr(r_hat), _ptr(state), _ptr(out.accept_len), _ptr(out.tokens), _ptr(out.jsd),
                                  _ptr(out.T), _ptr(out.req_status), _ptr(ws), ws.numel(), sh)
     _check(st, "sci_verify_ex")
+    return out
+
+
+# ------------------------------------------------------------------ paged key/value cache
+
+@dataclass
+class PagedAppendOutput:
+    q: Optional[torch.Tensor]  # [N, q_heads, head_dim] rotated queries (None without q)
+    req_status: torch.Tensor   # [B] int32 (ASV_REQ_* bits, ORed in)
+
+
+@dataclass
+class PagedAttentionOutput:
+    out: torch.Tensor            # [N, q_heads, head_dim]
+    lse: Optional[torch.Tensor]  # [N, q_heads] float32 (natural log; may be None)
+    req_status: torch.Tensor     # [B] int32 (ASV_REQ_* bits, ORed in)
+
+
+def _rows(t: torch.Tensor) -> _RowsC:
+    return _RowsC(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N):
+    """Checks the cache and the batch and returns their C forms."""
+    _need_cuda(k_cache, v_cache, block_table, cache_len, indptr)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise AsvError(2, "k_cache and v_cache must share one [num_pages, page_size, kv_heads, head_dim] shape")
+    if k_cache.dtype not in (torch.bfloat16, torch.float16) or k_cache.dtype != v_cache.dtype:
+        raise AsvError(4, f"the caches must share bfloat16 or float16, got {k_cache.dtype} and {v_cache.dtype}")
+    if any(x.dtype != torch.int32 for x in (block_table, cache_len, indptr)):
+        raise AsvError(4, "block_table, cache_len and indptr must be int32")
+    if block_table.dim() != 2 or cache_len.dim() != 1 or indptr.dim() != 1:
+        raise AsvError(2, "block_table must be [B, max_pages], cache_len [B], indptr [B + 1]")
+    B = block_table.shape[0]
+    if cache_len.shape[0] != B or indptr.shape[0] != B + 1:
+        raise AsvError(2, "block_table must be [B, max_pages], cache_len [B], indptr [B + 1]")
+    _contig(cache_len, "cache_len")
+    _contig(indptr, "indptr")
+    if any(x.shape[-1] > 1 and x.stride(-1) != 1 for x in (k_cache, v_cache, block_table)):
+        raise AsvError(3, "the last dimension of k_cache, v_cache and block_table must be contiguous")
+    P, page, H, D = k_cache.shape
+    cache = _PagedCacheC(k_cache.data_ptr(), v_cache.data_ptr(),
+                         ASV_BF16 if k_cache.dtype == torch.bfloat16 else ASV_F16, P, page, H, D,
+                         *k_cache.stride()[:3], *v_cache.stride()[:3])
+    batch = _PagedBatchC(B, N, indptr.data_ptr(), cache_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                         block_table.stride(0))
+    return cache, batch, B
+
+
+def _check_packed(x: torch.Tensor, name: str, N: int, heads: Optional[int], cache: torch.Tensor):
+    _need_cuda(x)
+    D = cache.shape[3]
+    if x.dim() != 3 or x.shape[0] != N or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
+        raise AsvError(2, f"{name} must be [{N}, {'heads' if heads is None else heads}, {D}], got {tuple(x.shape)}")
+    if x.dtype != cache.dtype:
+        raise AsvError(4, f"{name} must have the cache's type {cache.dtype}, got {x.dtype}")
+    if x.shape[0] and x.stride(2) != 1:
+        raise AsvError(3, f"the last dimension of {name} must be contiguous")
+
+
+def _check_status(req_status: torch.Tensor, B: int):
+    _need_cuda(req_status)
+    if req_status.dtype != torch.int32 or tuple(req_status.shape) != (B,):
+        raise AsvError(2, "req_status must be int32 [B]")
+    _contig(req_status, "req_status")
+
+
+def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, cache_len: torch.Tensor, indptr: torch.Tensor, *,
+                    q: Optional[torch.Tensor] = None, rotary: Optional[torch.Tensor] = None,
+                    interleaved: bool = False, out: Optional[PagedAppendOutput] = None,
+                    stream=None) -> PagedAppendOutput:
+    """Appends the packed new tokens' keys and values ([N, kv_heads, head_dim]; request b's are rows
+    indptr[b]..indptr[b+1]) to the paged caches at positions cache_len[b] onwards; with `rotary`
+    ([max_position, dim] float32: cos of the dim/2 angles of each position, then their sines) the keys
+    are rotated on the way, and the queries `q` into out.q (paged_kv_append in include/asv.h).
+    cache_len is not advanced.  The caches take any strides with head rows contiguous."""
+    _need_cuda(k, v, q, rotary)
+    if k.dim() != 3:
+        raise AsvError(2, "k and v must be [N, kv_heads, head_dim]")
+    N = k.shape[0]
+    cache, batch, B = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
+    for name, x in (("k", k), ("v", v)):
+        _check_packed(x, name, N, k_cache.shape[2], k_cache)
+    if q is not None:
+        _check_packed(q, "q", N, None, k_cache)
+    rc = None
+    if rotary is not None:
+        if rotary.dim() != 2 or rotary.dtype != torch.float32:
+            raise AsvError(2, "rotary must be a float32 [max_position, dim] table")
+        _contig(rotary, "rotary")
+        rc = C.byref(_RotaryC(rotary.data_ptr(), rotary.shape[1], rotary.shape[0], int(bool(interleaved))))
+    dev = k_cache.device
+    sh = _stream_handle(dev, stream)
+    if out is None:
+        out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
+                                torch.zeros(B, dtype=torch.int32, device=dev))
+    _check_status(out.req_status, B)
+    qr = oq = None
+    q_heads = 0
+    if q is not None:
+        if out.q is None:
+            raise AsvError(1, "out.q is missing")
+        _check_packed(out.q, "out.q", N, q.shape[1], k_cache)
+        q_heads = q.shape[1]
+        qr, oq = C.byref(_rows(q)), C.byref(_rows(out.q))
+    st = library().paged_kv_append(C.byref(cache), C.byref(batch), C.byref(_rows(k)), C.byref(_rows(v)), qr, oq,
+                                   q_heads, rc, _ptr(out.req_status), sh)
+    _check(st, "paged_kv_append")
+    return out
+
+
+# Workspaces of paged_attention, one per (device, stream): their partial results are not zeroed by a
+# call, so they are kept apart from the verification's.
+_paged_ws_cache: dict = {}
+
+
+def paged_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(library().asv_paged_workspace_bytes(q_heads, kv_heads, head_dim))
+
+
+def _paged_workspace(device: torch.device, stream, nbytes: int) -> torch.Tensor:
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    key = (device.index, s.cuda_stream)
+    with _ws_lock:
+        ws = _paged_ws_cache.get(key)
+        if ws is None or ws.numel() < nbytes:
+            with torch.cuda.stream(s):
+                ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            _paged_ws_cache[key] = ws
+    return ws
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    cache_len: torch.Tensor, indptr: torch.Tensor, *, scale: Optional[float] = None,
+                    window: int = 0, out: Optional[PagedAttentionOutput] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> PagedAttentionOutput:
+    """Attention of the packed chunks of new tokens q [N, q_heads, head_dim] over the paged caches, the
+    chunk's own tokens (appended before, see paged_kv_append) included: causal, grouped heads, with
+    `window` > 0 only the last `window` positions of each token (paged_attention in include/asv.h).
+    cache_len [B] counts the tokens before the chunk; scale defaults to head_dim ** -0.5."""
+    _need_cuda(q)
+    if q.dim() != 3:
+        raise AsvError(2, "q must be [N, q_heads, head_dim]")
+    N, Hq = q.shape[:2]
+    cache, batch, B = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
+    _check_packed(q, "q", N, None, k_cache)
+    dev = q.device
+    sh = _stream_handle(dev, stream)
+    if out is None:
+        out = PagedAttentionOutput(torch.empty(q.shape, dtype=q.dtype, device=dev),
+                                   torch.empty(N, Hq, dtype=torch.float32, device=dev),
+                                   torch.zeros(B, dtype=torch.int32, device=dev))
+    _check_packed(out.out, "out.out", N, Hq, k_cache)
+    _check_status(out.req_status, B)
+    if out.lse is not None:
+        _need_cuda(out.lse)
+        if out.lse.dtype != torch.float32 or tuple(out.lse.shape) != (N, Hq):
+            raise AsvError(2, "out.lse must be float32 [N, q_heads]")
+        _contig(out.lse, "out.lse")
+    need = paged_workspace_bytes(Hq, k_cache.shape[2], q.shape[2])
+    ws = workspace if workspace is not None else _paged_workspace(dev, stream, need)
+    st = library().paged_attention(C.byref(cache), C.byref(batch), C.byref(_rows(q)), C.byref(_rows(out.out)), Hq,
+                                   float(q.shape[2] ** -0.5 if scale is None else scale), int(window), _ptr(out.lse),
+                                   _ptr(out.req_status), _ptr(ws), ws.numel() * ws.element_size(), sh)
+    _check(st, "paged_attention")
     return out

@@ -10,6 +10,7 @@
 
 #include "asv.h"
 #include "asv_internal.h"
+#include "asv_paged.h"
 
 static_assert(sizeof(asv_sci_state) == sizeof(asv::SciState), "asv_sci_state layout");
 
@@ -180,6 +181,8 @@ int elem_size(int dt) { return dt == ASV_F32 ? 4 : 2; }
 }  // namespace
 
 namespace asv {
+
+asv_status record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
 // Argument checks of asymspec_verify, in the order they are applied: shapes and element type, then
 // (for B > 0) the scalar parameters, the alignment of every pointer given (NULL counts as

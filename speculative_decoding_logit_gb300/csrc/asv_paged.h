@@ -1,0 +1,59 @@
+// asv_paged.h -- host-side declarations shared by the paged-cache entry points and their kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "asv.h"
+#include "asv_internal.h"
+
+namespace asv {
+
+struct RowsView {
+  uint16_t* p;
+  long long tok, head;  // strides in elements
+};
+
+// The cache and the batch as the kernels take them (strides of extent-1 dimensions zeroed).
+struct PagedView {
+  uint16_t* k;
+  uint16_t* v;
+  int num_pages, page_size, kv_heads, head_dim;
+  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
+  int B, N;
+  const int32_t* indptr;
+  const int32_t* cache_len;
+  const int32_t* table;
+  int max_pages;
+  long long table_stride;
+};
+
+struct AppendArgs {
+  PagedView c;
+  RowsView k, v, q, out_q;  // q.p == nullptr: keys and values only
+  int q_heads;
+  const float* rotary;  // nullptr: no rotation
+  int rot_dim, max_position, interleaved;
+  uint32_t* status;
+  uint32_t* check_log;  // always nullptr: the append has no workspace to keep a log in
+};
+
+struct AttendArgs {
+  PagedView c;
+  RowsView q, out;
+  int q_heads, group;
+  float scale;
+  int window;
+  float* lse;
+  uint32_t* status;
+  uint32_t* check_log;
+};
+
+cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_paged_attention(const AttendArgs& a, int dtype, cudaStream_t s);
+
+// ASV_ERR_CUDA, with `e` kept for asv_last_cuda_error (asv_api.cu).
+asv_status record_cuda_error(cudaError_t e);
+
+}  // namespace asv
