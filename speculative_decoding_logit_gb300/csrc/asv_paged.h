@@ -47,8 +47,22 @@ struct AttendArgs {
   int window;
   float* lse;
   uint32_t* status;
+  int box;             // slots one copy of keys or values takes (a power of two that divides the page)
+  int tile_tokens;     // tokens of one row tile
+  uint32_t* tickets;   // workspace: [kMaxGrid * 2], zero between calls
+  float* parts;        // workspace: partial results of split items
   uint32_t* check_log;
 };
+
+// paged_attention's workspace: tickets (zero between calls), then each CTA's two partial results of up
+// to two row tiles (unnormalised outputs, then row maxima and sums).
+constexpr int kPagedMaxGrid = 152;
+constexpr int kPagedTicketBytes = 4096;
+constexpr int kPagedSlots = 2 * kPagedMaxGrid;
+inline size_t paged_part_floats(int dim_padded) { return size_t(128) * dim_padded + 2 * 128; }
+inline size_t paged_workspace_bytes(int head_dim) {
+  return kPagedTicketBytes + kPagedSlots * 2 * paged_part_floats(head_dim <= 64 ? 64 : 128) * sizeof(float);
+}
 
 cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_paged_attention(const AttendArgs& a, int dtype, cudaStream_t s);

@@ -12,7 +12,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 // Sizes of the cache and the batch, then the element type.
 asv_status check_sizes(const asv_paged_cache& c, const asv_paged_batch& b) {
-  if (b.B < 0 || b.N < 0 || b.max_pages < 0 || c.num_pages < 0) return ASV_ERR_SHAPE;
+  if (b.B < 0 || b.N < 0 || b.max_pages < 0 || c.num_pages < 1) return ASV_ERR_SHAPE;
   if (c.page_size < 8 || c.page_size % 8 != 0 || c.kv_heads < 1 || c.kv_heads > 1024) return ASV_ERR_SHAPE;
   if (c.head_dim < 8 || c.head_dim % 8 != 0 || c.head_dim > 128) return ASV_ERR_SHAPE;
   // positions are 32-bit
@@ -37,7 +37,7 @@ bool cache_ok(const asv_paged_cache& c, const asv_paged_batch& b) {
 }
 
 bool cache_given(const asv_paged_cache& c, const asv_paged_batch& b) {
-  return (c.num_pages == 0 || (c.k && c.v)) && b.indptr && b.cache_len && (b.max_pages == 0 || b.block_table);
+  return c.k && c.v && b.indptr && b.cache_len && (b.max_pages == 0 || b.block_table);
 }
 
 asv::RowsView rows_view(const asv_rows& r, int N, int heads) {
@@ -112,8 +112,8 @@ asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* 
 }
 
 size_t asv_paged_workspace_bytes(int q_heads, int kv_heads, int head_dim) {
-  if (kv_heads < 1 || q_heads < kv_heads || head_dim < 1) return 0;
-  return 4096 + asv::kCheckLogBytes;
+  if (kv_heads < 1 || q_heads < kv_heads || head_dim < 1 || head_dim > 128) return 0;
+  return asv::paged_workspace_bytes(head_dim) + asv::kCheckLogBytes;
 }
 
 asv_status paged_attention(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* q,
@@ -142,6 +142,10 @@ asv_status paged_attention(const asv_paged_cache* cache, const asv_paged_batch* 
   a.window = window;
   a.lse = out_lse;
   a.status = out_req_status;
+  a.tickets = static_cast<uint32_t*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + asv::kPagedTicketBytes);
+  if (asv::kCheckLogBytes)
+    a.check_log = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + asv::paged_workspace_bytes(c.head_dim));
   cudaError_t e = asv::launch_paged_attention(a, c.dtype, stream);
   return e == cudaSuccess ? ASV_OK : asv::record_cuda_error(e);
 }
