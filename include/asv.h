@@ -482,12 +482,13 @@ asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* 
  * does not matter, NaN included.
  * q_heads is a multiple of kv_heads, at most 128 to one key head; scale is finite and > 0; window >= 0
  * (0: none).  out_lse [N, q_heads] may be NULL.
- * workspace: asv_paged_workspace_bytes(...) bytes, 256-byte aligned, zero-filled before its first use
- * (asv_workspace_init); every call leaves it ready for the next.  Calls that may run at the same time
+ * workspace: asv_paged_workspace_bytes(...) bytes, 256-byte aligned, its first ASV_PAGED_WORKSPACE_ZEROED
+ * bytes zero-filled before its first use (asv_workspace_init); every call leaves them zero.  Calls that may run at the same time
  * must not share it.  One launch.
  * Checks in the order of paged_kv_append's (scale and window are ASV_ERR_PARAM), then the workspace
  * (ASV_ERR_WORKSPACE).
  */
+#define ASV_PAGED_WORKSPACE_ZEROED 4096
 size_t asv_paged_workspace_bytes(int q_heads, int kv_heads, int head_dim);
 asv_status paged_attention(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* q,
                            const asv_rows* out, int q_heads, float scale, int window, float* out_lse,

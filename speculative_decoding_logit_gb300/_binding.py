@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -102,6 +103,14 @@ class _RotaryC(C.Structure):
     _fields_ = [("table", C.c_void_p), ("dim", C.c_int), ("max_position", C.c_int), ("interleaved", C.c_int)]
 
 
+# The same layouts packed from Python values: a structure's constructor takes several microseconds, and
+# the paged calls are made for every layer of every step.
+_pack_cache = struct.Struct("@QQiiiii4xqqqqqq").pack
+_pack_batch = struct.Struct("@iiQQQi4xq").pack
+_pack_rows = struct.Struct("@Qqq").pack
+_pack_rotary = struct.Struct("@Qiii4x").pack
+
+
 def _declare(L):
     L.asv_status_string.argtypes = [_i]
     L.asv_status_string.restype = C.c_char_p
@@ -147,12 +156,11 @@ def _declare(L):
     L.sci_verify_ex.argtypes = [_vp, _vp, _i, _vp, _i, _i, _i, C.POINTER(_SciParamsC), C.POINTER(_SciStabC), _vp,
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     L.sci_verify_ex.restype = _i
-    rows, cache, batch = C.POINTER(_RowsC), C.POINTER(_PagedCacheC), C.POINTER(_PagedBatchC)
-    L.paged_kv_append.argtypes = [cache, batch, rows, rows, rows, rows, _i, C.POINTER(_RotaryC), _vp, _vp]
+    L.paged_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp]
     L.paged_kv_append.restype = _i
     L.asv_paged_workspace_bytes.argtypes = [_i, _i, _i]
     L.asv_paged_workspace_bytes.restype = _sz
-    L.paged_attention.argtypes = [cache, batch, rows, rows, _i, _f, _i, _vp, _vp, _vp, _sz, _vp]
+    L.paged_attention.argtypes = [_vp, _vp, _vp, _vp, _i, _f, _i, _vp, _vp, _vp, _sz, _vp]
     L.paged_attention.restype = _i
 
 
@@ -562,53 +570,61 @@ class PagedAttentionOutput:
     req_status: torch.Tensor     # [B] int32 (ASV_REQ_* bits, ORed in)
 
 
-def _rows(t: torch.Tensor) -> _RowsC:
-    return _RowsC(t.data_ptr(), t.stride(0), t.stride(1))
+_CACHE_TYPES = {torch.bfloat16: ASV_BF16, torch.float16: ASV_F16}
 
 
 def _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N):
-    """Checks the cache and the batch and returns their C forms."""
-    _need_cuda(k_cache, v_cache, block_table, cache_len, indptr)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    """Checks the cache and the batch; returns their packed forms, B, the caches' type and shape."""
+    if not (k_cache.is_cuda and v_cache.is_cuda and block_table.is_cuda and cache_len.is_cuda and indptr.is_cuda):
+        _need_cuda(k_cache, v_cache, block_table, cache_len, indptr)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape:
         raise AsvError(2, "k_cache and v_cache must share one [num_pages, page_size, kv_heads, head_dim] shape")
-    if k_cache.dtype not in (torch.bfloat16, torch.float16) or k_cache.dtype != v_cache.dtype:
-        raise AsvError(4, f"the caches must share bfloat16 or float16, got {k_cache.dtype} and {v_cache.dtype}")
-    if any(x.dtype != torch.int32 for x in (block_table, cache_len, indptr)):
+    dtype = k_cache.dtype
+    code = _CACHE_TYPES.get(dtype)
+    if code is None or v_cache.dtype != dtype:
+        raise AsvError(4, f"the caches must share bfloat16 or float16, got {dtype} and {v_cache.dtype}")
+    i32 = torch.int32
+    if block_table.dtype != i32 or cache_len.dtype != i32 or indptr.dtype != i32:
         raise AsvError(4, "block_table, cache_len and indptr must be int32")
-    if block_table.dim() != 2 or cache_len.dim() != 1 or indptr.dim() != 1:
+    table = block_table.shape
+    if len(table) != 2 or cache_len.shape != table[:1] or indptr.shape != (table[0] + 1,):
         raise AsvError(2, "block_table must be [B, max_pages], cache_len [B], indptr [B + 1]")
-    B = block_table.shape[0]
-    if cache_len.shape[0] != B or indptr.shape[0] != B + 1:
-        raise AsvError(2, "block_table must be [B, max_pages], cache_len [B], indptr [B + 1]")
-    _contig(cache_len, "cache_len")
-    _contig(indptr, "indptr")
-    if any(x.shape[-1] > 1 and x.stride(-1) != 1 for x in (k_cache, v_cache, block_table)):
+    B, width = table
+    if B > 1 and cache_len.stride(0) != 1 or indptr.shape[0] > 1 and indptr.stride(0) != 1:
+        raise AsvError(2, "cache_len and indptr must be contiguous")
+    ks, vs, ts = k_cache.stride(), v_cache.stride(), block_table.stride()
+    if (shape[3] > 1 and (ks[3] != 1 or vs[3] != 1)) or (width > 1 and ts[1] != 1):
         raise AsvError(3, "the last dimension of k_cache, v_cache and block_table must be contiguous")
-    P, page, H, D = k_cache.shape
-    cache = _PagedCacheC(k_cache.data_ptr(), v_cache.data_ptr(),
-                         ASV_BF16 if k_cache.dtype == torch.bfloat16 else ASV_F16, P, page, H, D,
-                         *k_cache.stride()[:3], *v_cache.stride()[:3])
-    batch = _PagedBatchC(B, N, indptr.data_ptr(), cache_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                         block_table.stride(0))
-    return cache, batch, B
+    try:
+        cache = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), code, *shape, *ks[:3], *vs[:3])
+        batch = _pack_batch(B, N, indptr.data_ptr(), cache_len.data_ptr(), block_table.data_ptr(), width, ts[0])
+    except struct.error as e:
+        raise AsvError(2, f"an extent does not fit 32 bits ({e})") from None
+    return cache, batch, B, dtype, shape
 
 
-def _check_packed(x: torch.Tensor, name: str, N: int, heads: Optional[int], cache: torch.Tensor):
-    _need_cuda(x)
-    D = cache.shape[3]
-    if x.dim() != 3 or x.shape[0] != N or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
-        raise AsvError(2, f"{name} must be [{N}, {'heads' if heads is None else heads}, {D}], got {tuple(x.shape)}")
-    if x.dtype != cache.dtype:
-        raise AsvError(4, f"{name} must have the cache's type {cache.dtype}, got {x.dtype}")
-    if x.shape[0] and x.stride(2) != 1:
+def _packed_rows(x: torch.Tensor, name: str, shape, dtype) -> bytes:
+    """Packed form of q, k, v or out, [N, heads, head_dim] of the cache's type."""
+    if x.shape != shape:
+        raise AsvError(2, f"{name} must be {tuple(shape)}, got {tuple(x.shape)}")
+    if x.dtype != dtype:
+        raise AsvError(4, f"{name} must have the cache's type {dtype}, got {x.dtype}")
+    if not x.is_cuda:
+        _need_cuda(x)
+    s = x.stride()
+    if s[2] != 1 and x.numel():
         raise AsvError(3, f"the last dimension of {name} must be contiguous")
+    return _pack_rows(x.data_ptr(), s[0], s[1])
 
 
 def _check_status(req_status: torch.Tensor, B: int):
-    _need_cuda(req_status)
-    if req_status.dtype != torch.int32 or tuple(req_status.shape) != (B,):
+    if req_status.dtype != torch.int32 or req_status.shape != (B,):
         raise AsvError(2, "req_status must be int32 [B]")
-    _contig(req_status, "req_status")
+    if not req_status.is_cuda:
+        _need_cuda(req_status)
+    if B > 1 and req_status.stride(0) != 1:
+        raise AsvError(2, "req_status must be contiguous")
 
 
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -621,58 +637,67 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     ([max_position, dim] float32: cos of the dim/2 angles of each position, then their sines) the keys
     are rotated on the way, and the queries `q` into out.q (paged_kv_append in include/asv.h).
     cache_len is not advanced.  The caches take any strides with head rows contiguous."""
-    _need_cuda(k, v, q, rotary)
-    if k.dim() != 3:
+    shape = k.shape
+    if len(shape) != 3:
         raise AsvError(2, "k and v must be [N, kv_heads, head_dim]")
-    N = k.shape[0]
-    cache, batch, B = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
-    for name, x in (("k", k), ("v", v)):
-        _check_packed(x, name, N, k_cache.shape[2], k_cache)
-    if q is not None:
-        _check_packed(q, "q", N, None, k_cache)
+    N = shape[0]
+    cache, batch, B, dtype, cs = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
+    kv_shape = (N, cs[2], cs[3])
+    kr, vr = _packed_rows(k, "k", kv_shape, dtype), _packed_rows(v, "v", kv_shape, dtype)
     rc = None
     if rotary is not None:
         if rotary.dim() != 2 or rotary.dtype != torch.float32:
             raise AsvError(2, "rotary must be a float32 [max_position, dim] table")
+        if not rotary.is_cuda:
+            _need_cuda(rotary)
         _contig(rotary, "rotary")
-        rc = C.byref(_RotaryC(rotary.data_ptr(), rotary.shape[1], rotary.shape[0], int(bool(interleaved))))
-    dev = k_cache.device
-    sh = _stream_handle(dev, stream)
+        positions, dim = rotary.shape
+        rc = _pack_rotary(rotary.data_ptr(), dim, min(positions, 0x7fffffff), 1 if interleaved else 0)
     if out is None:
-        out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
+        dev = k_cache.device
+        out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=dtype, device=dev),
                                 torch.zeros(B, dtype=torch.int32, device=dev))
-    _check_status(out.req_status, B)
+    status = out.req_status
+    _check_status(status, B)
     qr = oq = None
     q_heads = 0
     if q is not None:
         if out.q is None:
             raise AsvError(1, "out.q is missing")
-        _check_packed(out.q, "out.q", N, q.shape[1], k_cache)
+        if q.dim() != 3:
+            raise AsvError(2, "q must be [N, q_heads, head_dim]")
         q_heads = q.shape[1]
-        qr, oq = C.byref(_rows(q)), C.byref(_rows(out.q))
-    st = library().paged_kv_append(C.byref(cache), C.byref(batch), C.byref(_rows(k)), C.byref(_rows(v)), qr, oq,
-                                   q_heads, rc, _ptr(out.req_status), sh)
-    _check(st, "paged_kv_append")
+        q_shape = (N, q_heads, cs[3])
+        qr, oq = _packed_rows(q, "q", q_shape, dtype), _packed_rows(out.q, "out.q", q_shape, dtype)
+    st = library().paged_kv_append(cache, batch, kr, vr, qr, oq, q_heads, rc, status.data_ptr(),
+                                   _raw_stream(k_cache, stream))
+    if st:
+        _check(st, "paged_kv_append")
     return out
 
 
 # Workspaces of paged_attention, one per (device, stream): their partial results are not zeroed by a
-# call, so they are kept apart from the verification's.
+# call, so they are kept apart from the verification's.  Only their first bytes have to start at zero.
 _paged_ws_cache: dict = {}
+PAGED_WORKSPACE_ZEROED = 4096
+
+
+def _raw_stream(t: torch.Tensor, stream) -> int:
+    """The CUDA stream handle of `stream`, or of the current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def paged_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(library().asv_paged_workspace_bytes(q_heads, kv_heads, head_dim))
 
 
-def _paged_workspace(device: torch.device, stream, nbytes: int) -> torch.Tensor:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device.index, s.cuda_stream)
-    with _ws_lock:
-        ws = _paged_ws_cache.get(key)
-        if ws is None or ws.numel() < nbytes:
-            with torch.cuda.stream(s):
-                ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+def _paged_workspace(q: torch.Tensor, handle: int, stream, nbytes: int) -> torch.Tensor:
+    key = (q.get_device(), handle)
+    ws = _paged_ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with _ws_lock, torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(q.device)):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            ws[:PAGED_WORKSPACE_ZEROED].zero_()
             _paged_ws_cache[key] = ws
     return ws
 
@@ -685,29 +710,36 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     chunk's own tokens (appended before, see paged_kv_append) included: causal, grouped heads, with
     `window` > 0 only the last `window` positions of each token (paged_attention in include/asv.h).
     cache_len [B] counts the tokens before the chunk; scale defaults to head_dim ** -0.5."""
-    _need_cuda(q)
     if q.dim() != 3:
         raise AsvError(2, "q must be [N, q_heads, head_dim]")
-    N, Hq = q.shape[:2]
-    cache, batch, B = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
-    _check_packed(q, "q", N, None, k_cache)
-    dev = q.device
-    sh = _stream_handle(dev, stream)
+    N, Hq, D = q.shape
+    cache, batch, B, dtype, cs = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
+    shape = (N, Hq, cs[3])
+    qr = _packed_rows(q, "q", shape, dtype)
     if out is None:
-        out = PagedAttentionOutput(torch.empty(q.shape, dtype=q.dtype, device=dev),
+        dev = q.device
+        out = PagedAttentionOutput(torch.empty(q.shape, dtype=dtype, device=dev),
                                    torch.empty(N, Hq, dtype=torch.float32, device=dev),
                                    torch.zeros(B, dtype=torch.int32, device=dev))
-    _check_packed(out.out, "out.out", N, Hq, k_cache)
-    _check_status(out.req_status, B)
-    if out.lse is not None:
-        _need_cuda(out.lse)
-        if out.lse.dtype != torch.float32 or tuple(out.lse.shape) != (N, Hq):
+    rows = _packed_rows(out.out, "out.out", shape, dtype)
+    status, lse = out.req_status, out.lse
+    _check_status(status, B)
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (N, Hq):
             raise AsvError(2, "out.lse must be float32 [N, q_heads]")
-        _contig(out.lse, "out.lse")
-    need = paged_workspace_bytes(Hq, k_cache.shape[2], q.shape[2])
-    ws = workspace if workspace is not None else _paged_workspace(dev, stream, need)
-    st = library().paged_attention(C.byref(cache), C.byref(batch), C.byref(_rows(q)), C.byref(_rows(out.out)), Hq,
-                                   float(q.shape[2] ** -0.5 if scale is None else scale), int(window), _ptr(out.lse),
-                                   _ptr(out.req_status), _ptr(ws), ws.numel() * ws.element_size(), sh)
-    _check(st, "paged_attention")
+        if not lse.is_cuda:
+            _need_cuda(lse)
+        _contig(lse, "out.lse")
+        lse = lse.data_ptr()
+    L = library()
+    handle = _raw_stream(q, stream)
+    if workspace is None:
+        workspace = _paged_workspace(q, handle, stream, L.asv_paged_workspace_bytes(Hq, cs[2], D))
+    try:
+        st = L.paged_attention(cache, batch, qr, rows, Hq, D ** -0.5 if scale is None else scale, window, lse,
+                               status.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle)
+    except (C.ArgumentError, TypeError) as e:
+        raise AsvError(5, f"scale must be a number and window a 32-bit whole number ({e})") from None
+    if st:
+        _check(st, "paged_attention")
     return out

@@ -57,7 +57,7 @@ struct AttendArgs {
 // paged_attention's workspace: tickets (zero between calls), then each CTA's two partial results of up
 // to two row tiles (unnormalised outputs, then row maxima and sums).
 constexpr int kPagedMaxGrid = 152;
-constexpr int kPagedTicketBytes = 4096;
+constexpr int kPagedTicketBytes = ASV_PAGED_WORKSPACE_ZEROED;
 constexpr int kPagedSlots = 2 * kPagedMaxGrid;
 inline size_t paged_part_floats(int dim_padded) { return size_t(128) * dim_padded + 2 * 128; }
 inline size_t paged_workspace_bytes(int head_dim) {

@@ -440,27 +440,38 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     bool have_prev = false, prev_first = false, prev_last = false;
     bool run = true;
 
-    // S of row tile x (buffer sb) of the key tile at `slot`
-    auto qk = [&](int sb, uint32_t q, int slot) {
-      const uint32_t k = ring + slot * kTileBytes;
-      for (int i = 0; i < k_steps; ++i) {
-        const uint32_t off = (i / 4) * kHalfBytes + (i % 4) * 32;
-        mma_ss(tmem + sb * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), id_qk, i > 0);
+    // An instruction runs 64 cycles and blocks its issue until there is room, so its operands must be there
+    // by then: descriptors are those of the first tiles plus constants (in 16-byte units), unrolled, in a
+    // branch of one elected lane (formed by a lane picked by its number, from vector registers, an
+    // instruction took about 130 cycles).
+    const uint64_t q_desc = smem_desc(q_tiles, 16, 1024), k_desc = smem_desc(ring, 16, 1024);
+    const uint64_t v_desc = smem_desc(ring, kHalfBytes, 1024);
+    // S (buffer sb) of the queries of Q tile q and the keys at `slot`
+    auto qk = [&](int sb, int q, int slot) {
+      const uint64_t qd = q_desc + q * (kTileBytes / 16), kd = k_desc + slot * (kTileBytes / 16);
+      auto step = [&](int i) {
+        const uint32_t off = ((i / 4) * kHalfBytes + (i % 4) * 32) / 16;
+        mma_ss(tmem + sb * 128, qd + off, kd + off, id_qk, i > 0);
+      };
+      if (k_steps == DP / 16) {
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) step(i);
+      } else {
+        for (int i = 0; i < k_steps; ++i) step(i);
       }
     };
     auto pv = [&](int ob, int sb, int slot, bool first) {
-      const uint32_t v = ring + slot * kTileBytes;
+      const uint64_t vd = v_desc + slot * (kTileBytes / 16);
 #pragma unroll
       for (int i = 0; i < kTile / 16; ++i)
-        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, smem_desc(v + i * 2048, kHalfBytes, 1024), id_pv,
-               !(first && i == 0));
+        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, !(first && i == 0));
     };
     // out += P V of the previous tile, row tile x
     auto pv_tile = [&](int x, int v_slot, bool last_tile) {
       const int sb = NT == 1 ? prev_sb : x, ob = NT == 1 ? prev_ob : x;
       if (!warp_wait(at(ms.p_full, sb), (used[sb] & 1) ^ 1, abort)) return false;
       fence_after();
-      if (lane == 0) {
+      if (elect()) {
         pv(ob, sb, v_slot, prev_first);
         if (NT == 1) commit(at(ms.pv_done, sb));
         if (last_tile) commit(at(ms.kv_empty, v_slot));
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       if (!run) break;
       const int tiles = NT == 1 ? 1 : (p.ntok + a.tile_tokens - 1) / a.tile_tokens;
       int k_slot = 0, v_slot = 0;
-      uint32_t q = q_tiles;
+      int q = 0;
       auto begin_tile = [&]() {  // keys (and queries) of the next tile are there
         if (!warp_wait(at(ms.kv_full, ring_kv.slot), ring_kv.phase, abort)) return false;
         k_slot = ring_kv.slot;
@@ -528,14 +539,14 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
           cur_ob = next_ob;
           if (NT == 1) next_ob ^= 1;
         }
-        if (NT == 1) q = q_tiles + ring_q.slot * kTileBytes;
+        if (NT == 1) q = ring_q.slot;
         fence_after();
         return true;
       };
       auto qk_tile = [&](int x) {
         const int sb = NT == 1 ? tile_no & 1 : x;
-        if (lane == 0) {
-          qk(sb, q + (NT == 2 ? x * kTileBytes : 0), k_slot);
+        if (elect()) {
+          qk(sb, NT == 2 ? x : q, k_slot);
           commit(at(ms.s_full, sb));
           if (x == tiles - 1) {
             commit(at(ms.kv_empty, k_slot));
@@ -629,30 +640,34 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         if (any) {
           fence_after();
           __syncwarp();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + i * 32, s[i]);
-          tmem_wait_ld();
           const int base = t * kTile;
-          if (base + kTile > all_hi || base < all_lo) {
-            const int h = hi - base, l = lo - base;
+          const bool masked = base + kTile > all_hi || base < all_lo;
+          const int h = hi - base, l = lo - base;
+          // Both passes over the row read S from tensor memory, 64 columns at a time: reading it twice costs
+          // less than holding 128 registers of it, and the loops' code stays small.
+          auto load_s = [&](int half, uint32_t (&s)[64]) {
+            tmem_ld32(s_addr + half * 64, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+            tmem_ld32(s_addr + half * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+            tmem_wait_ld();
+            if (masked) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int col = i * 32 + j;
-                if (col >= h || col < l) s[i][j] = 0xff800000u;
+              for (int j = 0; j < 64; ++j) {
+                const int col = half * 64 + j;
+                if (col >= h || col < l) s[j] = 0xff800000u;
               }
-          }
-          float m[4];
+            }
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            uint32_t s[64];
+            load_s(half, s);
+            float m[2] = {top, __uint_as_float(s[63])};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            m[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-            for (int j = 1; j < 31; j += 2) m[i] = max3(m[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
-            m[i] = fmaxf(m[i], __uint_as_float(s[i][31]));
+            for (int j = 0; j < 62; j += 2) m[(j / 2) & 1] = max3(m[(j / 2) & 1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            top = max3(m[0], m[1], __uint_as_float(s[62]));
           }
-          const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale2;
+          top *= scale2;
           const bool move = top > ref + kLazy;
           if (__any_sync(0xffffffffu, move)) {
             const float keep = move ? ex2_approx(ref - top) : 1.0f;
@@ -686,19 +701,19 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
           const float shift = ref == -INFINITY ? 0.0f : -ref;
           const float2 sc = make_float2(scale2, scale2), sh = make_float2(shift, shift);
           float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t w[32];
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            uint32_t s[64], w[32];
+            load_s(half, s);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const uint32_t* src = &s[2 * i + j / 16][2 * (j % 16)];
-              float2 x = ffma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), sc, sh);
+              float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sc, sh);
               x.x = ex2_approx(x.x);
               x.y = ex2_approx(x.y);
               part[j & 1] = fadd2(part[j & 1], x);
               w[j] = pack2<BF16>(x.x, x.y);
             }
-            tmem_st32(s_addr + i * 32, w);
+            tmem_st32(s_addr + half * 32, w);
           }
           const float2 both = fadd2(part[0], part[1]);
           sum += both.x + both.y;

@@ -173,6 +173,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// True in one lane of a converged warp, always the same one.  A branch on it is known to the compiler to
+// be taken by one lane, so what is uniform in the warp stays in uniform registers inside it, where the
+// matrix instructions take their operands from.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // One arrival on `bar` when every matrix instruction this thread has issued is complete.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");

@@ -35,15 +35,17 @@ def _batch(m, **kw):
 
 
 def _append(m, cache=None, batch=None, k=None, v=None, q=None, oq=None, heads=4, rot=None):
-    ref = lambda x: None if x is None else C.byref(x)
-    return m.library().paged_kv_append(C.byref(cache or _cache(m)), C.byref(batch or _batch(m)), ref(k), ref(v),
-                                       ref(q), ref(oq), heads, ref(rot), None, None)
+    ref = lambda x: None if x is None else C.addressof(x)
+    cache, batch = cache or _cache(m), batch or _batch(m)
+    return m.library().paged_kv_append(C.addressof(cache), C.addressof(batch), ref(k), ref(v), ref(q), ref(oq), heads,
+                                       ref(rot), None, None)
 
 
 def _attend(m, cache=None, batch=None, q=None, out=None, heads=4, scale=0.125, window=0, lse=None, ws=None, n=0):
-    ref = lambda x: None if x is None else C.byref(x)
-    return m.library().paged_attention(C.byref(cache or _cache(m)), C.byref(batch or _batch(m)), ref(q), ref(out),
-                                       heads, scale, window, lse, None, ws, n, None)
+    ref = lambda x: None if x is None else C.addressof(x)
+    cache, batch = cache or _cache(m), batch or _batch(m)
+    return m.library().paged_attention(C.addressof(cache), C.addressof(batch), ref(q), ref(out), heads, scale, window,
+                                       lse, None, ws, n, None)
 
 
 SIZES = [("page_size", 0), ("page_size", 4), ("page_size", 12), ("kv_heads", 0), ("kv_heads", 2000), ("head_dim", 0),
@@ -128,6 +130,16 @@ def test_attention_scalars(m):
     assert _attend(m) == NULL
     assert m.library().paged_attention(None, None, None, None, 4, 1.0, 0, None, None, None, 0, None) == NULL
     assert m.library().paged_kv_append(None, None, None, None, None, None, 4, None, None, None) == NULL
+
+
+def test_packed_forms_match_the_structures(m):
+    cache = (BASE, BASE + 16, 1, 4, 16, 2, 64, 1, 2, 3, 4, 5, 1 << 40)
+    batch = (2, 3, BASE, BASE + 4, BASE + 8, 5, 1 << 33)
+    for cls, pack, values in ((m._PagedCacheC, m._pack_cache, cache), (m._PagedBatchC, m._pack_batch, batch),
+                              (m._RowsC, m._pack_rows, (BASE, -5, 1 << 35)), (m._RotaryC, m._pack_rotary, (BASE, 64, 9, 1))):
+        got = cls.from_buffer_copy(pack(*values))
+        assert len(pack(*values)) == C.sizeof(cls)
+        assert tuple(getattr(got, f[0]) for f in cls._fields_) == values
 
 
 def test_workspace_size(m):
