@@ -40,6 +40,9 @@ using namespace tc;
 constexpr int kTile = 128;  // rows of a row tile; positions of a key tile
 constexpr int kQueue = 4;
 constexpr uint32_t kTmemColumns = 512;  // S buffers at 0 and 128, outputs at 256 and 384
+// Key tiles that an item's own work (queries in, outputs out, the pipeline's fill) is worth in the split.
+template <int NT>
+constexpr int kItemCost = NT == 1 ? 2 : 4;
 constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
 
 template <int DP>
@@ -118,8 +121,10 @@ struct Items {
     }
     return sum;
   }
-  __device__ long long units(int window, int kv_heads) const {
-    return n == 0 ? 0 : kv_heads * (tiles_before(window, n - 1) + tiles(window, n - 1));
+  // units of one key head before item i
+  __device__ long long before(int window, int cost, int i) const { return tiles_before(window, i) + (long long)cost * i; }
+  __device__ long long units(int window, int cost, int kv_heads) const {
+    return n == 0 ? 0 : kv_heads * (before(window, cost, n - 1) + tiles(window, n - 1) + cost);
   }
 };
 
@@ -149,11 +154,16 @@ __device__ __forceinline__ uint32_t at(const uint64_t* bars, int i) { return sme
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// Any 16-bit element of the words with all exponent bits set.
+// 0 * x + acc for both 16-bit elements: NaN from the first x that is not finite on.
 template <bool BF16>
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
-  return (w & kExp) == kExp || ((w >> 16) & kExp) == kExp;
+__device__ __forceinline__ uint32_t probe2(uint32_t x, uint32_t acc) {
+  uint32_t r;
+  if constexpr (BF16) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  } else {
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  }
+  return r;
 }
 
 template <bool BF16>
@@ -164,45 +174,105 @@ __device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
   return w;
 }
 
-// Makes a tile of values (rows = positions base .. base + 127) safe to multiply by weights of zero: rows
-// outside [lo, hi), which no row of the item attends to, are zeroed where a copied box reaches past the
-// bounds; in the rows that only some attend to, [zone, hi) and [lo, wzone), elements that are not finite
-// are zeroed and reported (the epilogue adds them to the rows that do attend to them).  By one warp.
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 x) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
+// Rows [r0, r1) of a tile of keys or values, 16 bytes a time over the lanes of a warp: f(address).
+template <int DP, class F>
+__device__ __forceinline__ void each_vec(uint32_t tile, int r0, int r1, int lane, F f) {
+  constexpr int kVecs = DP / 8, kRows = 32 / kVecs;  // vectors of a row, rows of a step
+  const int vec = lane % kVecs;
+  uint32_t p = tile + (vec / 8) * (kTile * 128) + (r0 + lane / kVecs) * 128 + (vec % 8) * 16;
+  const uint32_t end = tile + (vec / 8) * (kTile * 128) + r1 * 128;
+#pragma unroll 4
+  for (; p < end; p += kRows * 128) f(p);
+}
+
 template <bool BF16, int DP>
-__device__ bool clean_values(uint32_t tile, int base, int lo, int hi, int zone, int wzone, int box, int lane) {
-  constexpr int kVecs = DP / 8;
-  auto addr = [&](int row, int vec) { return tile + (vec / 8) * (kTile * 128) + row * 128 + (vec % 8) * 16; };
-  bool touched = false, found = false;
-  auto zero = [&](int r0, int r1) {
-    for (int i = r0 * kVecs + lane; i < r1 * kVecs; i += 32)
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr(i / kVecs, i % kVecs)), "r"(0) : "memory");
-    touched |= r1 > r0;
+__device__ __noinline__ void zero_nonfinite(uint32_t tile, int r0, int r1, int lane) {
+  each_vec<DP>(tile, r0, r1, lane, [](uint32_t p) {
+    const uint4 x = lds16(p);
+    sts16(p, make_uint4(finite_or_zero2<BF16>(x.x), finite_or_zero2<BF16>(x.y), finite_or_zero2<BF16>(x.z),
+                        finite_or_zero2<BF16>(x.w)));
+  });
+}
+
+// Makes a tile of values (rows = positions base .. base + 127) safe to multiply by weights of zero.  The
+// product takes rows in steps of 16, those that reach into [lo, hi): the rest of the first and the last
+// step, which no row of the item attends to, is zeroed.  In the rows that only some attend to, [zone, hi)
+// and [lo, wzone), elements that are not finite are zeroed and reported (the epilogue adds them to the rows
+// that do attend to them).  By one warp.
+template <bool BF16, int DP>
+__device__ bool clean_values(uint32_t tile, int base, int lo, int hi, int zone, int wzone, int lane) {
+  const int first = max(lo - base, 0), end = min(hi - base, kTile);
+  auto zero = [](uint32_t p) { sts16(p, make_uint4(0, 0, 0, 0)); };
+  each_vec<DP>(tile, first & ~15, first, lane, zero);
+  each_vec<DP>(tile, end, (end + 15) & ~15, lane, zero);
+  const int w1 = max(min(wzone - base, end), first), z0 = max(max(zone - base, first), w1);
+  uint32_t acc[4] = {0, 0, 0, 0};
+  auto probe = [&](uint32_t p) {
+    const uint4 x = lds16(p);
+    acc[0] = probe2<BF16>(x.x, acc[0]);
+    acc[1] = probe2<BF16>(x.y, acc[1]);
+    acc[2] = probe2<BF16>(x.z, acc[2]);
+    acc[3] = probe2<BF16>(x.w, acc[3]);
   };
-  auto scan = [&](int r0, int r1) {
-    for (int i = r0 * kVecs + lane; i < r1 * kVecs; i += 32) {
-      const uint32_t p = addr(i / kVecs, i % kVecs);
-      uint4 x;
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(p));
-      if (nonfinite2<BF16>(x.x) || nonfinite2<BF16>(x.y) || nonfinite2<BF16>(x.z) || nonfinite2<BF16>(x.w)) {
-        found = true;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(finite_or_zero2<BF16>(x.x)),
-                     "r"(finite_or_zero2<BF16>(x.y)), "r"(finite_or_zero2<BF16>(x.z)), "r"(finite_or_zero2<BF16>(x.w))
-                     : "memory");
+  each_vec<DP>(tile, first, w1, lane, probe);
+  each_vec<DP>(tile, z0, end, lane, probe);
+  // sums of products with zero: +-0 unless one was not finite
+  const bool found = __any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0);
+  if (found) {
+    zero_nonfinite<BF16, DP>(tile, first, w1, lane);
+    zero_nonfinite<BF16, DP>(tile, z0, end, lane);
+  }
+  fence_async_shared();
+  __syncwarp();
+  return found;
+}
+
+// Eight 16-byte vectors of each lane (its row) exchanged among groups of eight lanes, so that lane i of a
+// group ends with vector i of the group's eight rows and a store covers whole 128-byte lines.
+__device__ __forceinline__ void transpose8(uint32_t (&w)[32], int lane) {
+#pragma unroll
+  for (int m = 1; m < 8; m *= 2) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      if (a & m) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t mine = w[4 * a + e], theirs = w[4 * (a | m) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? mine : theirs, m);
+        w[4 * a + e] = up ? got : mine;
+        w[4 * (a | m) + e] = up ? theirs : got;
       }
     }
-  };
-  const int first = max(lo - base, 0), end = min(hi - base, kTile);
-  zero(first / box * box, first);
-  zero(end, min(kTile, (end + box - 1) / box * box));
-  const int w1 = min(wzone - base, end);
-  scan(first, w1);
-  scan(max(max(zone - base, first), w1), end);
-  found = __any_sync(0xffffffffu, found);
-  if (found || touched) {
-    fence_async_shared();
-    __syncwarp();
   }
-  return found;
+}
+
+// Adds to entries d0 .. d0 + N - 1 of a row's outputs the values that are not finite among those it attends
+// to at positions [lo, hi) and the item's other rows may not (all but [skip_lo, skip_hi)).  Out of line: only
+// rows next to such values come here.
+template <bool BF16, int N>
+__device__ __noinline__ void add_poison(const PagedView& c, int request, int head, int lo, int hi, int skip_lo,
+                                        int skip_hi, int d0, float* o) {
+  for (int k = lo; k < hi; ++k) {
+    if (k >= skip_lo && k < skip_hi) continue;
+    const int page = c.table[request * c.table_stride + k / c.page_size];
+    if (page < 0 || page >= c.num_pages) continue;
+    const uint16_t* v = c.v + page * c.v_page + (k % c.page_size) * c.v_slot + head * c.v_head;
+    for (int d = 0; d < N && d0 + d < c.head_dim; ++d) {
+      const float x = unpack1<BF16>(v[d0 + d]);
+      if (!(fabsf(x) < INFINITY)) o[d] += x;
+    }
+  }
 }
 
 template <bool BF16, int DP, int NT>
@@ -210,6 +280,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr int kThreads = 32 * (4 * NT + 3);
+  constexpr int kCost = kItemCost<NT>;
   constexpr int kRing = kRingSlots<DP>;
   constexpr int kHalves = DP / 64;                // 64-element column blocks, 128 bytes a row
   constexpr uint32_t kTileBytes = kTile * DP * 2;
@@ -260,7 +331,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
   for (int b = b0; b < b1; ++b) {
     const Items it = load_items(c, b, T);
     if (!it.r.ok && blockIdx.x == 0) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
-    own += it.units(a.window, c.kv_heads);
+    own += it.units(a.window, kCost, c.kv_heads);
   }
   long long incl = own;
 #pragma unroll
@@ -281,7 +352,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
   if (u0 >= before && u0 < before + own) {
     long long x = before;
     for (int b = b0; b < b1; ++b) {
-      const long long n = load_items(c, b, T).units(a.window, c.kv_heads);
+      const long long n = load_items(c, b, T).units(a.window, kCost, c.kv_heads);
       if (u0 < x + n) {
         ms.start_request = b;
         ms.start_units = x;
@@ -306,40 +377,44 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       int i = 0;  // the item that holds unit u0: the last with no more than rel units before it
       for (int hi = it.n; hi - i > 1;) {
         const int mid = (i + hi) / 2;
-        if (c.kv_heads * it.tiles_before(a.window, mid) <= rel) i = mid;
+        if (c.kv_heads * it.before(a.window, kCost, mid) <= rel) i = mid;
         else hi = mid;
       }
       int n = it.tiles(a.window, i);
-      const long long off = rel - c.kv_heads * it.tiles_before(a.window, i);
-      int h = int(off / n), t = int(off % n);
+      const long long off = rel - c.kv_heads * it.before(a.window, kCost, i);
+      int h = int(off / (n + kCost));
+      long long item0 = u0 - off % (n + kCost);  // units before the item
       Ring ring_p;
-      for (long long u = u0;;) {
-        if (!bar_wait(at(ms.piece_empty, ring_p.slot), ring_p.phase ^ 1, abort)) break;
-        Piece& p = ms.piece[ring_p.slot];
-        if (u >= u1) {
-          p.kind = 1;
+      for (bool end = false; !end;) {
+        // its first kCost units are its own, then one for each key tile
+        const int ta = int(max(u0 - item0 - kCost, 0ll));
+        const int tb = int(min(max(u1 - item0 - kCost, 0ll), (long long)n));
+        end = b >= c.B || item0 >= u1;
+        if (end || tb > ta) {
+          if (!bar_wait(at(ms.piece_empty, ring_p.slot), ring_p.phase ^ 1, abort)) break;
+          Piece& p = ms.piece[ring_p.slot];
+          p.kind = end;
+          if (!end) {
+            p.request = b;
+            p.tok0 = it.r.start + i * T;
+            p.ntok = min(T, it.r.end - p.tok0);
+            p.head = h;
+            p.pos0 = it.r.past + i * T;
+            p.kv_lo = it.lo(a.window, i);
+            const int tile0 = p.kv_lo / kTile;
+            p.t0 = it.r.ok ? tile0 + ta : 0;
+            p.t1 = it.r.ok ? tile0 + tb : 0;
+            p.part = -1;
+            if (tb - ta < n) {
+              p.first_cta = int((item0 + kCost) / per_cta);
+              p.n_parts = int((item0 + kCost + n - 1) / per_cta) - p.first_cta + 1;
+              p.part = 2 * int(blockIdx.x) + (ta == 0 ? 1 : 0);
+            }
+          }
           bar_arrive(at(ms.piece_full, ring_p.slot));
-          break;
+          ring_p.next(kQueue);
         }
-        const int take = int(min((long long)(n - t), u1 - u));
-        const long long item0 = u - t;
-        p.kind = 0;
-        p.request = b;
-        p.tok0 = it.r.start + i * T;
-        p.ntok = min(T, it.r.end - p.tok0);
-        p.head = h;
-        p.pos0 = it.r.past + i * T;
-        p.kv_lo = it.lo(a.window, i);
-        const int tile0 = p.kv_lo / kTile;
-        p.t0 = it.r.ok ? tile0 + t : 0;
-        p.t1 = it.r.ok ? tile0 + t + take : 0;
-        p.first_cta = int(item0 / per_cta);
-        p.n_parts = int((item0 + n - 1) / per_cta) - p.first_cta + 1;
-        p.part = p.n_parts == 1 ? -1 : 2 * int(blockIdx.x) + (item0 >= u0 ? 1 : 0);
-        bar_arrive(at(ms.piece_full, ring_p.slot));
-        ring_p.next(kQueue);
-        u += take;
-        t = 0;
+        item0 += n + kCost;
         if (++h == c.kv_heads) {
           h = 0;
           if (++i == it.n) {
@@ -355,68 +430,106 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     }
   } else if (warp == kCopyWarp) {
     // ---- copies
+    // 32 lanes hold the pages of up to 32 boxes, a window of one or more tiles; the next window's entries of
+    // the block table are on their way while this one's tiles are copied.
     Ring ring_p, ring_kv, ring_q;
-    const int boxes = kTile / a.box;
-    Piece prev = {};
-    int prev_tile = 0, prev_page = 0;
-    bool have_prev = false, run = true;
-    // this lane's box of a tile of keys (or values) into the next slot of the ring
-    auto copy_tile = [&](const CUtensorMap* map, int head, int tile, int page) {
+    const int boxes = kTile / a.box, shift = 31 - __clz(boxes);
+    const int group = lane >> shift, in_tile = (lane & (boxes - 1)) * a.box;  // this lane's tile and box
+    struct Window {
+      int head, tok0, ntok, request, t0, n, entry, slot;
+      bool first, need;
+    };
+    Piece p;
+    p.kind = p.t1 = 0;
+    int t = 0;
+    // the next window; `block`: wait for its piece.  n = 0: none (yet).
+    auto next_window = [&](bool block, Window& w) {
+      w.n = 0;
+      while (t == p.t1) {
+        if (p.kind == 1) return true;
+        const uint32_t bar = at(ms.piece_full, ring_p.slot);
+        if (block ? !warp_wait(bar, ring_p.phase, abort) : !__all_sync(0xffffffffu, bar_try(bar, ring_p.phase)))
+          return !block;
+        p = ms.piece[ring_p.slot];
+        __syncwarp();
+        if (lane == 0) bar_arrive(at(ms.piece_empty, ring_p.slot));
+        ring_p.next(kQueue);
+        if (p.kind == 1) {
+          t = p.t1;
+          return true;
+        }
+        t = p.t0;
+      }
+      w.head = p.head;
+      w.tok0 = p.tok0;
+      w.ntok = p.ntok;
+      w.request = p.request;
+      w.first = t == p.t0;
+      w.t0 = t;
+      w.n = min(32 >> shift, p.t1 - t);
+      // what no row attends to is filled with zeros (a page past the last)
+      const int pos = (t + group) * kTile + in_tile;
+      w.need = group < w.n && pos < p.pos0 + p.ntok && pos + a.box > p.kv_lo;
+      const int page = pos / c.page_size;
+      w.slot = pos - page * c.page_size;
+      w.entry = w.need ? c.table[p.request * c.table_stride + page] : -1;
+      t += w.n;
+      return true;
+    };
+    // one tile of keys (or values) into the next slot of the ring: the lanes of `g` copy their boxes
+    auto copy_tile = [&](const CUtensorMap* map, int head, int g, int page, int slot) {
       if (!warp_wait(at(ms.kv_empty, ring_kv.slot), ring_kv.phase ^ 1, abort)) return false;
       const uint32_t bar = at(ms.kv_full, ring_kv.slot);
       if (lane == 0) bar_expect(bar, kTileBytes);
       __syncwarp();
-      if (lane < boxes) {
-        const int slot = (tile * kTile + lane * a.box) % c.page_size;
-        const uint32_t dst = ring + ring_kv.slot * kTileBytes + lane * a.box * 128;
+      if (group == g) {
+        const uint32_t dst = ring + ring_kv.slot * kTileBytes + in_tile * 128;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) copy_4d(dst + h * kHalfBytes, map, h * 64, head, slot, page, bar);
       }
+      __syncwarp();
       ring_kv.next(kRing);
       return true;
     };
-    while (run) {
-      if (!warp_wait(at(ms.piece_full, ring_p.slot), ring_p.phase, abort)) break;
-      const Piece p = ms.piece[ring_p.slot];
+    auto copy_queries = [&](const Window& w) {
+      if (!warp_wait(at(ms.q_empty, ring_q.slot), ring_q.phase ^ 1, abort)) return false;
+      if (lane == 0) {
+        const int tiles = NT == 1 || w.ntok <= a.tile_tokens ? 1 : 2;
+        const uint32_t bar = at(ms.q_full, ring_q.slot);
+        bar_expect(bar, tiles * kHalves * a.tile_tokens * a.group * 128);
+        for (int i = 0; i < tiles; ++i)
+          for (int h = 0; h < kHalves; ++h)
+            copy_3d(q_tiles + (NT == 1 ? ring_q.slot : i) * kTileBytes + h * kHalfBytes, &map_q, h * 64,
+                    w.head * a.group, w.tok0 + i * a.tile_tokens, bar);
+      }
       __syncwarp();
-      if (lane == 0) bar_arrive(at(ms.piece_empty, ring_p.slot));
-      ring_p.next(kQueue);
-      if (p.kind == 1) break;
-      const int kv_hi = p.pos0 + p.ntok;
-      for (int t = p.t0; t < p.t1; ++t) {
-        // this lane's page; what no row attends to is filled with zeros (a page past the last)
-        int page = c.num_pages;
-        const int pos = t * kTile + lane * a.box;
-        if (lane < boxes && pos < kv_hi && pos + a.box > p.kv_lo) {
-          const int id = c.table[p.request * c.table_stride + pos / c.page_size];
-          if (id >= 0 && id < c.num_pages) page = id;
-          else atomicOr(a.status + p.request, ASV_REQ_BAD_PAGE);
-        }
-        if (NT == 2 && have_prev) run = run && copy_tile(&map_v, prev.head, prev_tile, prev_page);
-        run = run && copy_tile(&map_k, p.head, t, page);
-        if (run && t == p.t0) {
-          if (!warp_wait(at(ms.q_empty, ring_q.slot), ring_q.phase ^ 1, abort)) {
-            run = false;
-          } else if (lane == 0) {
-            const int tiles = NT == 1 ? 1 : (p.ntok + a.tile_tokens - 1) / a.tile_tokens;
-            const uint32_t bar = at(ms.q_full, ring_q.slot);
-            bar_expect(bar, tiles * kHalves * a.tile_tokens * a.group * 128);
-            for (int i = 0; i < tiles; ++i)
-              for (int h = 0; h < kHalves; ++h)
-                copy_3d(q_tiles + (NT == 1 ? ring_q.slot : i) * kTileBytes + h * kHalfBytes, &map_q, h * 64,
-                        p.head * a.group, p.tok0 + i * a.tile_tokens, bar);
-          }
-          ring_q.next(3 - NT);
-        }
-        if (NT == 1 && have_prev) run = run && copy_tile(&map_v, prev.head, prev_tile, prev_page);
-        if (!run) break;
-        prev = p;
-        prev_tile = t;
-        prev_page = page;
-        have_prev = true;
+      ring_q.next(3 - NT);
+      return true;
+    };
+    Window w, ahead;
+    ahead.n = 0;
+    int v_head = 0, v_group = -1, v_page = 0, v_slot = 0;  // the previous tile, whose values are copied next
+    bool run = true;
+    while (run) {
+      if (ahead.n == 0 && (!next_window(true, ahead) || ahead.n == 0)) break;
+      w = ahead;
+      const bool ok = w.need && w.entry >= 0 && w.entry < c.num_pages;
+      if (w.need && !ok) atomicOr(a.status + w.request, ASV_REQ_BAD_PAGE);
+      const int page = ok ? w.entry : c.num_pages;
+      next_window(false, ahead);
+      for (int i = 0; i < w.n && run; ++i) {
+        // the order the tensor cores take them in
+        if (NT == 2 && v_group >= 0) run = copy_tile(&map_v, v_head, v_group, v_page, v_slot);
+        run = run && copy_tile(&map_k, w.head, i, page, w.slot);
+        if (i == 0 && w.first) run = run && copy_queries(w);
+        if (NT == 1 && v_group >= 0) run = run && copy_tile(&map_v, v_head, v_group, v_page, v_slot);
+        v_head = w.head;
+        v_group = i;
+        v_page = page;
+        v_slot = w.slot;
       }
     }
-    if (have_prev && run) copy_tile(&map_v, prev.head, prev_tile, prev_page);
+    if (v_group >= 0 && run) copy_tile(&map_v, v_head, v_group, v_page, v_slot);
     if (*abort) {  // leave with no copy in flight: every slot of the ring once more
       for (int i = 0; i < kRing; ++i) {
         const unsigned long long t0 = now_ns();
@@ -435,8 +548,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     int items[2] = {0, 0};  // output buffer uses so far
     int cur_ob = 0, next_ob = 0;
     int tile_no = 0;  // NT = 1: tiles so far
-    Piece prev = {};
-    int prev_tile = 0, prev_ob = 0, prev_sb = 0, prev_tiles = 0;
+    int prev_pos0 = 0, prev_ntok = 0, prev_lo = 0, prev_tile = 0, prev_ob = 0, prev_sb = 0, prev_tiles = 0;
     bool have_prev = false, prev_first = false, prev_last = false;
     bool run = true;
 
@@ -460,11 +572,19 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         for (int i = 0; i < k_steps; ++i) step(i);
       }
     };
-    auto pv = [&](int ob, int sb, int slot, bool first) {
+    // out (buffer ob) += P V over the 16-position steps [i0, i1)
+    auto pv = [&](int ob, int sb, int slot, bool first, int i0, int i1) {
       const uint64_t vd = v_desc + slot * (kTileBytes / 16);
+      auto step = [&](int i, bool add) {
+        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, add);
+      };
+      if (i1 - i0 == kTile / 16) {
+        step(0, !first);
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, !(first && i == 0));
+        for (int i = 1; i < kTile / 16; ++i) step(i, true);
+      } else {
+        for (int i = i0; i < i1; ++i) step(i, !(first && i == i0));
+      }
     };
     // out += P V of the previous tile, row tile x
     auto pv_tile = [&](int x, int v_slot, bool last_tile) {
@@ -472,7 +592,8 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       if (!warp_wait(at(ms.p_full, sb), (used[sb] & 1) ^ 1, abort)) return false;
       fence_after();
       if (elect()) {
-        pv(ob, sb, v_slot, prev_first);
+        pv(ob, sb, v_slot, prev_first, max(prev_lo - prev_tile * kTile, 0) / 16,
+           (min(prev_pos0 + prev_ntok - prev_tile * kTile, kTile) + 15) / 16);
         if (NT == 1) commit(at(ms.pv_done, sb));
         if (last_tile) commit(at(ms.kv_empty, v_slot));
         if (prev_last) commit(at(ms.o_full, ob));
@@ -482,19 +603,17 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       return true;
     };
     // the values of the previous tile are next in the ring: wait for them, make them safe
-    auto take_values = [&](int* v_slot) {
+    auto take_values = [&](int v_slot, uint32_t v_phase) {
       if (prev_first)  // its output buffers (and their poison marks) are free
         for (int x = 0; x < prev_tiles; ++x) {
           const int ob = NT == 1 ? prev_ob : x;
           if (!warp_wait(at(ms.o_empty, ob), (items[ob] & 1) ^ 1, abort)) return false;
         }
-      if (!warp_wait(at(ms.kv_full, ring_kv.slot), ring_kv.phase, abort)) return false;
-      *v_slot = ring_kv.slot;
-      ring_kv.next(kRing);
-      const int base = prev_tile * kTile, hi = prev.pos0 + prev.ntok;
+      if (!warp_wait(at(ms.kv_full, v_slot), v_phase, abort)) return false;
+      const int base = prev_tile * kTile, hi = prev_pos0 + prev_ntok;
       const int last_lo = a.window > 0 ? max(0, hi - a.window) : 0;
-      if (base + kTile > prev.pos0 + 1 || base < last_lo) {
-        if (clean_values<BF16, DP>(ring + *v_slot * kTileBytes, base, prev.kv_lo, hi, prev.pos0 + 1, last_lo, a.box,
+      if (base + kTile > prev_pos0 + 1 || base < last_lo) {
+        if (clean_values<BF16, DP>(ring + v_slot * kTileBytes, base, prev_lo, hi, prev_pos0 + 1, last_lo,
                                    lane)) {
           if (lane < 2 && (NT == 2 || lane == prev_ob)) *reinterpret_cast<volatile int*>(&ms.poison[lane]) = 1;
           __threadfence_block();
@@ -527,14 +646,18 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         }
       }
       if (!run) break;
-      const int tiles = NT == 1 ? 1 : (p.ntok + a.tile_tokens - 1) / a.tile_tokens;
-      int k_slot = 0, v_slot = 0;
+      const int tiles = NT == 1 || p.ntok <= a.tile_tokens ? 1 : 2;
+      // their slots of the ring, in the order of the copies
+      Ring key = ring_kv, value = ring_kv;
+      if (NT == 1 && more) value.next(kRing);
+      if (NT == 2 && have_prev) key.next(kRing);
+      if (more) ring_kv.next(kRing);
+      if (have_prev) ring_kv.next(kRing);
+      const bool first = t == p.t0;
       int q = 0;
       auto begin_tile = [&]() {  // keys (and queries) of the next tile are there
-        if (!warp_wait(at(ms.kv_full, ring_kv.slot), ring_kv.phase, abort)) return false;
-        k_slot = ring_kv.slot;
-        ring_kv.next(kRing);
-        if (t == p.t0) {
+        if (!warp_wait(at(ms.kv_full, key.slot), key.phase, abort)) return false;
+        if (first) {
           if (!warp_wait(at(ms.q_full, ring_q.slot), ring_q.phase, abort)) return false;
           cur_ob = next_ob;
           if (NT == 1) next_ob ^= 1;
@@ -545,42 +668,61 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       };
       auto qk_tile = [&](int x) {
         const int sb = NT == 1 ? tile_no & 1 : x;
+        const bool last_x = x == tiles - 1, last_q = last_x && t == p.t1 - 1;
         if (elect()) {
-          qk(sb, NT == 2 ? x : q, k_slot);
+          qk(sb, NT == 2 ? x : q, key.slot);
           commit(at(ms.s_full, sb));
-          if (x == tiles - 1) {
-            commit(at(ms.kv_empty, k_slot));
-            if (t == p.t1 - 1) commit(at(ms.q_empty, ring_q.slot));
-          }
+          if (last_x) commit(at(ms.kv_empty, key.slot));
+          if (last_q) commit(at(ms.q_empty, ring_q.slot));
         }
         __syncwarp();
         ++used[sb];
-        if (x == tiles - 1 && t == p.t1 - 1) ring_q.next(3 - NT);
+        if (last_q) ring_q.next(3 - NT);
       };
+      bool ok = true;
       if (NT == 1) {
+        // S of the next tile before the product of this one, unless a new item's keys are still on their way
         const int sb = tile_no & 1;
-        if (more) {
-          if (!begin_tile()) break;
-          qk_tile(0);
+        const bool early = more && (!first || __all_sync(0xffffffffu, bar_try(at(ms.kv_full, key.slot), key.phase) &&
+                                                                          bar_try(at(ms.q_full, ring_q.slot), ring_q.phase)));
+        if (early) {
+          ok = begin_tile();
+          if (ok) qk_tile(0);
         }
-        // `used` of the other buffer is not moved by the line above, so prev's parity is its own
-        if (have_prev) {
-          if (!take_values(&v_slot) || !pv_tile(0, v_slot, true)) break;
+        if (ok && have_prev) {
+          // qk_tile counts a use of the other buffer, so prev's parity is its own
+          ok = take_values(value.slot, value.phase) && pv_tile(0, value.slot, true);
+        }
+        if (ok && more && !early) {
+          ok = begin_tile();
+          if (ok) qk_tile(0);
         }
         prev_sb = sb;
         if (more) ++tile_no;
-      } else {
-        if (have_prev && !take_values(&v_slot)) break;
-        if (more && !begin_tile()) break;
-        bool ok = true;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (have_prev && x < prev_tiles) ok = pv_tile(x, v_slot, x == prev_tiles - 1);
-          if (ok && more && x < tiles) qk_tile(x);
+      } else if (first || !more) {
+        // the item before is finished first: the new one's queries wait for it
+        if (have_prev) {
+          ok = take_values(value.slot, value.phase);
+          for (int x = 0; x < prev_tiles && ok; ++x) ok = pv_tile(x, value.slot, x == prev_tiles - 1);
         }
-        if (!ok) break;
+        if (ok && more) {
+          ok = begin_tile();
+          for (int x = 0; x < tiles && ok; ++x) qk_tile(x);
+        }
+      } else {
+        ok = take_values(value.slot, value.phase) && begin_tile();
+        for (int x = 0; x < tiles && ok; ++x) {
+          ok = pv_tile(x, value.slot, x == tiles - 1);
+          if (ok) qk_tile(x);
+        }
       }
+      if (!ok) break;
       if (!more) break;
-      prev = p;
+      if (first) {
+        prev_pos0 = p.pos0;
+        prev_ntok = p.ntok;
+        prev_lo = p.kv_lo;
+      }
       prev_tile = t;
       prev_tiles = tiles;
       prev_ob = cur_ob;
@@ -736,20 +878,18 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       }
       // values that are not finite and that not all rows attend to: this row's own
       const bool poison = p.t1 > p.t0 && *reinterpret_cast<volatile int*>(&ms.poison[ob]) != 0;
-      auto add_poison = [&](float* o, int d0, int n) {
-        if (!valid) return;
+      auto poisoned = [&](auto& y, int d0) {
+        constexpr int kN = sizeof(y) / sizeof(float);
+        float z[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) z[j] = y[j];
         const int hi_all = p.pos0 + p.ntok;
-        const int last_lo = a.window > 0 ? max(0, hi_all - a.window) : 0;
-        for (int k = max(lo, p.t0 * kTile); k < min(hi, p.t1 * kTile); ++k) {
-          if (k < p.pos0 + 1 && k >= last_lo) continue;
-          const int page = c.table[p.request * c.table_stride + k / c.page_size];
-          if (page < 0 || page >= c.num_pages) continue;
-          const uint16_t* v = c.v + page * c.v_page + (k % c.page_size) * c.v_slot + p.head * c.v_head;
-          for (int d = 0; d < n && d0 + d < c.head_dim; ++d) {
-            const float x = unpack1<BF16>(v[d0 + d]);
-            if (!(fabsf(x) < INFINITY)) o[d] += x;
-          }
-        }
+        if (valid)
+          add_poison<BF16, kN>(c, p.request, p.head, max(lo, p.t0 * kTile), min(hi, p.t1 * kTile),
+                               a.window > 0 ? max(0, hi_all - a.window) : 0, p.pos0 + 1, d0, z);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) y[j] = z[j];
+        __syncwarp();
       };
       const size_t part_floats = size_t(kTile) * DP + 2 * kTile;
       if (p.part < 0) {
@@ -758,23 +898,39 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         uint16_t* out = a.out.p + tok_row * a.out.tok + head * a.out.head;
         if (any) {
 #pragma unroll 1
-          for (int i = 0; i < DP / 32; ++i) {
+          for (int i = 0; i < DP / 64; ++i) {
             __syncwarp();
-            uint32_t o[32];
+            uint32_t o[64];
             if (p.t1 > p.t0) {
-              tmem_ld32(o_addr + i * 32, o);
+              tmem_ld32(o_addr + i * 64, reinterpret_cast<uint32_t(&)[32]>(o[0]));
+              tmem_ld32(o_addr + i * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(o[32]));
               tmem_wait_ld();
             }
-            float y[32];
+            float y[64];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = p.t1 > p.t0 ? __uint_as_float(o[j]) * inv : 0.0f;
-            if (poison) add_poison(y, i * 32, 32);
+            for (int j = 0; j < 64; ++j) y[j] = p.t1 > p.t0 ? __uint_as_float(o[j]) * inv : 0.0f;
+            if (poison) poisoned(y, i * 64);
+            uint32_t v[32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (store && i * 32 + j * 8 < c.head_dim)
-                *reinterpret_cast<uint4*>(out + i * 32 + j * 8) =
-                    make_uint4(pack2<BF16>(y[8 * j], y[8 * j + 1]), pack2<BF16>(y[8 * j + 2], y[8 * j + 3]),
-                               pack2<BF16>(y[8 * j + 4], y[8 * j + 5]), pack2<BF16>(y[8 * j + 6], y[8 * j + 7]));
+            for (int j = 0; j < 32; ++j) v[j] = pack2<BF16>(y[2 * j], y[2 * j + 1]);
+            if (NT == 1) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (store && i * 64 + j * 8 < c.head_dim)
+                  *reinterpret_cast<uint4*>(out + i * 64 + j * 8) =
+                      make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else {
+              // full tiles: a lane's own row to 16 bytes of 32 lines a store took 512 cycles of the L1 each
+              transpose8(v, lane);
+              const int d = i * 64 + (lane & 7) * 8;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const unsigned long long to = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), (lane & ~7) + j);
+                const bool ok = __shfl_sync(0xffffffffu, int(store), (lane & ~7) + j) != 0;
+                if (ok && d < c.head_dim)
+                  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(to) + d) =
+                      make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              }
             }
           }
           if (store && a.lse != nullptr)
@@ -793,7 +949,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
             float y[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]);
-            if (poison) add_poison(y, i * 32, 32);
+            if (poison) poisoned(y, i * 32);
             if (valid) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
