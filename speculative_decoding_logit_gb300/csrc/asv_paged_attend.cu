@@ -63,7 +63,7 @@ struct Piece {
 
 struct Misc {
   uint64_t kv_full[10], kv_empty[10];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[4], pv_done[2], o_full[2], o_empty[2];
   uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
   Piece piece[kQueue];
   long long warp_sum[12];
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       bar_init(at(ms.q_full, i), 1);
       bar_init(at(ms.q_empty, i), 1);
       bar_init(at(ms.s_full, i), 1);
-      bar_init(at(ms.p_full, i), 4);
+      bar_init(at(ms.p_full, 2 * i), 4);
+      bar_init(at(ms.p_full, 2 * i + 1), 4);
       bar_init(at(ms.pv_done, i), 1);
       bar_init(at(ms.o_full, i), 1);
       bar_init(at(ms.o_empty, i), 4);
@@ -572,28 +573,35 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         for (int i = 0; i < k_steps; ++i) step(i);
       }
     };
-    // out (buffer ob) += P V over the 16-position steps [i0, i1)
-    auto pv = [&](int ob, int sb, int slot, bool first, int i0, int i1) {
-      const uint64_t vd = v_desc + slot * (kTileBytes / 16);
-      auto step = [&](int i, bool add) {
-        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, add);
-      };
-      if (i1 - i0 == kTile / 16) {
-        step(0, !first);
+    // out (buffer ob) += P V: one half of the tile's 16-position steps, or those of [i0, i1)
+    auto pv_half = [&](int ob, int sb, int slot, int half, bool first) {
+      const uint64_t vd = v_desc + slot * (kTileBytes / 16) + half * (4 * 2048 / 16);
 #pragma unroll
-        for (int i = 1; i < kTile / 16; ++i) step(i, true);
-      } else {
-        for (int i = i0; i < i1; ++i) step(i, !(first && i == i0));
-      }
+      for (int i = 0; i < 4; ++i)
+        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + half * 32 + i * 8, vd + i * (2048 / 16), id_pv, i > 0 || !first);
+    };
+    auto pv_steps = [&](int ob, int sb, int slot, bool first, int i0, int i1) {
+      const uint64_t vd = v_desc + slot * (kTileBytes / 16);
+      for (int i = i0; i < i1; ++i)
+        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, !(first && i == i0));
     };
     // out += P V of the previous tile, row tile x
     auto pv_tile = [&](int x, int v_slot, bool last_tile) {
       const int sb = NT == 1 ? prev_sb : x, ob = NT == 1 ? prev_ob : x;
-      if (!warp_wait(at(ms.p_full, sb), (used[sb] & 1) ^ 1, abort)) return false;
+      // the weights come in two halves
+      const uint32_t p_phase = (used[sb] & 1) ^ 1;
+      const int i0 = max(prev_lo - prev_tile * kTile, 0) / 16;
+      const int i1 = (min(prev_pos0 + prev_ntok - prev_tile * kTile, kTile) + 15) / 16;
+      const bool whole = i0 == 0 && i1 == kTile / 16;
+      if (!warp_wait(at(ms.p_full, 2 * sb), p_phase, abort)) return false;
+      fence_after();
+      if (whole && elect()) pv_half(ob, sb, v_slot, 0, prev_first);
+      __syncwarp();
+      if (!warp_wait(at(ms.p_full, 2 * sb + 1), p_phase, abort)) return false;
       fence_after();
       if (elect()) {
-        pv(ob, sb, v_slot, prev_first, max(prev_lo - prev_tile * kTile, 0) / 16,
-           (min(prev_pos0 + prev_ntok - prev_tile * kTile, kTile) + 15) / 16);
+        if (whole) pv_half(ob, sb, v_slot, 1, false);
+        else pv_steps(ob, sb, v_slot, prev_first, i0, i1);
         if (NT == 1) commit(at(ms.pv_done, sb));
         if (last_tile) commit(at(ms.kv_empty, v_slot));
         if (prev_last) commit(at(ms.o_full, ob));
@@ -710,9 +718,9 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
           for (int x = 0; x < tiles && ok; ++x) qk_tile(x);
         }
       } else {
-        ok = take_values(value.slot, value.phase) && begin_tile();
+        ok = take_values(value.slot, value.phase);
         for (int x = 0; x < tiles && ok; ++x) {
-          ok = pv_tile(x, value.slot, x == tiles - 1);
+          ok = pv_tile(x, value.slot, x == tiles - 1) && (x > 0 || begin_tile());
           if (ok) qk_tile(x);
         }
       }
@@ -786,16 +794,21 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
           const bool masked = base + kTile > all_hi || base < all_lo;
           const int h = hi - base, l = lo - base;
           // Both passes over the row read S from tensor memory, 64 columns at a time: reading it twice costs
-          // less than holding 128 registers of it, and the loops' code stays small.
+          // less than holding 128 registers of it, and the loops are kept rolled and the masks short because the
+          // warps' roles together are about as much code as the instruction cache holds.
           auto load_s = [&](int half, uint32_t (&s)[64]) {
             tmem_ld32(s_addr + half * 64, reinterpret_cast<uint32_t(&)[32]>(s[0]));
             tmem_ld32(s_addr + half * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-            tmem_wait_ld();
+            tmem_wait_ld(s);
             if (masked) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                const int col = half * 64 + j;
-                if (col >= h || col < l) s[j] = 0xff800000u;
+              for (int i = 0; i < 2; ++i) {
+                const int b0 = l - half * 64 - i * 32, b1 = h - half * 64 - i * 32;  // columns [b0, b1) stay
+                const uint32_t from = b0 <= 0 ? ~0u : b0 >= 32 ? 0u : ~0u << b0;
+                const uint32_t keep = b1 >= 32 ? from : b1 <= 0 ? 0u : from & ((1u << b1) - 1);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((keep >> j) & 1u)) s[i * 32 + j] = 0xff800000u;
               }
             }
           };
@@ -828,11 +841,11 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
                 }
                 fence_after();
               }
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < DP / 32; ++i) {
                 uint32_t o[32];
                 tmem_ld32(o_addr + i * 32, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
                 tmem_st32(o_addr + i * 32, o);
@@ -856,14 +869,17 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
               w[j] = pack2<BF16>(x.x, x.y);
             }
             tmem_st32(s_addr + half * 32, w);
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(at(ms.p_full, 2 * sb + half));
           }
           const float2 both = fadd2(part[0], part[1]);
           sum += both.x + both.y;
-          tmem_wait_st();
-          fence_before();
+        } else if (lane == 0) {
+          bar_arrive(at(ms.p_full, 2 * sb));
+          bar_arrive(at(ms.p_full, 2 * sb + 1));
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(at(ms.p_full, sb));
         ++used;
       }
       if (!run) break;
@@ -904,7 +920,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
             if (p.t1 > p.t0) {
               tmem_ld32(o_addr + i * 64, reinterpret_cast<uint32_t(&)[32]>(o[0]));
               tmem_ld32(o_addr + i * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(o[32]));
-              tmem_wait_ld();
+              tmem_wait_ld(o);
             }
             float y[64];
 #pragma unroll
@@ -945,7 +961,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
             __syncwarp();
             uint32_t o[32];
             tmem_ld32(o_addr + i * 32, o);
-            tmem_wait_ld();
+            tmem_wait_ld(o);
             float y[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]);
