@@ -7,9 +7,13 @@
 // dependent loads (indptr, cache_len, block table and table row, each an L2 or HBM latency) for short
 // ones.
 //
-// One CTA per token.  Its threads first take their vectors of q, k and v (independent of the chain, so
-// their latency overlaps it), then find the token's request by counting the requests that end before
-// it, one load per thread and 256 requests, and share one copy of the table's row.
+// A CTA takes kTokens consecutive tokens: its first threads find their requests (all threads count the
+// requests that end before the first token, 256 a step; the others are at most a few further), pages and
+// slots, and the rows of the table come to shared memory once for all heads.  Then a task is one or two
+// 16-byte vectors: where a pair's elements are dim / 2 apart and that is whole vectors, one thread has
+// both, so every element is loaded once.
+#include <algorithm>
+
 #include "asv_paged_device.cuh"
 
 namespace asv {
@@ -18,83 +22,168 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The rotated element of a pair: a cos - b sin for its first element, a cos + b sin for its second (a
-// the element, b its partner).
-__device__ __forceinline__ float turn(float a, float b, float c, float s, bool second) {
-  return second ? fmaf(a, c, b * s) : fmaf(a, c, -(b * s));
-}
+// How a head's vectors are made tasks of.
+enum Pairing {
+  kPlain,     // a vector a task; pairs lie within it (interleaved), or nothing is rotated
+  kHalves,    // vectors j and j + dim / 2 a task, and the vectors from dim on one by one
+  kScattered  // a vector a task, its partners fetched one by one (dim / 2 not whole vectors)
+};
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a) {
-  __shared__ float s_cs[128];  // cos of the position's angles, then their sines
+struct TokenPlace {
+  int request, pos, page, slot;  // page < 0: not appended; request < 0: no token
+};
+
+// The elements of a pair turned: (a cos - b sin, b cos + a sin).
+__device__ __forceinline__ float first_of(float a, float b, float c, float s) { return fmaf(a, c, -(b * s)); }
+__device__ __forceinline__ float second_of(float a, float b, float c, float s) { return fmaf(b, c, a * s); }
+
+template <bool BF16, int PAIRING, int TOKENS>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ __align__(16) float s_cs[TOKENS][128];  // cos of the positions' angles, then their sines
+  __shared__ TokenPlace s_place[TOKENS];
   const PagedView& c = a.c;
-  const int token = blockIdx.x, tid = threadIdx.x;
-  const int vecs = c.head_dim / 8;
-  const int n_rot = (a.q_heads + c.kv_heads) * vecs;
-  const int items = n_rot + c.kv_heads * vecs;
-
-  // the request: the first whose rows end after this token
-  int before = 0;
-  for (int i = 0; i < c.B; i += kThreads) {
-    const bool ends = i + tid < c.B && c.indptr[i + tid + 1] <= token;
-    before += __syncthreads_count(ends);
-  }
+  const int tid = threadIdx.x, token0 = blockIdx.x * TOKENS;
   const long long limit = a.rotary != nullptr ? min((long long)a.max_position, table_positions(c)) : table_positions(c);
-  if (token == 0)  // one CTA looks every request over
-    for (int b = tid; b < c.B; b += kThreads)
-      if (!load_request(c, b, limit).ok) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
-  if (before >= c.B) return;
-  const Request r = load_request(c, before, limit);
-  if (!r.ok || token < r.start || token >= r.end) return;
-  const int pos = r.past + (token - r.start);
-  const int entry = pos / c.page_size, slot = pos % c.page_size;
-  const int page = c.table[before * c.table_stride + entry];
-  const bool page_ok = page >= 0 && page < c.num_pages;
-  if (!page_ok && tid == 0) atomicOr(a.status + before, ASV_REQ_BAD_PAGE);
-  if (a.rotary != nullptr && tid < a.rot_dim) s_cs[tid] = a.rotary[(long long)pos * a.rot_dim + tid];
-  __syncthreads();
-  const int half = a.rot_dim / 2;
 
-  for (int i = tid; i < items; i += kThreads) {
-    const int head = i / vecs, d0 = (i - head * vecs) * 8;
-    const bool is_q = head < a.q_heads, is_k = !is_q && head < a.q_heads + c.kv_heads;
-    const int h = is_q ? head : is_k ? head - a.q_heads : head - a.q_heads - c.kv_heads;
-    const RowsView& in = is_q ? a.q : is_k ? a.k : a.v;
-    const uint16_t* row = in.p + token * in.tok + h * in.head;
-    uint4 x = *reinterpret_cast<const uint4*>(row + d0);
-    uint16_t* dst;
-    if (is_q) dst = a.out_q.p + token * a.out_q.tok + h * a.out_q.head;
-    else if (is_k) dst = c.k + page * c.k_page + slot * c.k_slot + h * c.k_head;
-    else dst = c.v + page * c.v_page + slot * c.v_slot + h * c.v_head;
-    if (!is_q && !page_ok) continue;
-    if ((is_q || is_k) && d0 < a.rot_dim) {
-      uint32_t* w = &x.x;
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = d0 + e;
-        const float2 pair = unpack2<BF16>(w[e / 2]);
-        const float self = e % 2 ? pair.y : pair.x;
-        y[e] = self;
-        if (d < a.rot_dim) {
-          const bool second = a.interleaved ? d % 2 : d >= half;
-          const int partner = a.interleaved ? d ^ 1 : second ? d - half : d + half;
-          const int j = a.interleaved ? d / 2 : second ? d - half : d;
-          y[e] = turn(self, unpack1<BF16>(row[partner]), s_cs[j], s_cs[half + j], second);
+  // ---- the tokens' requests and places
+  int before = 0;
+  for (int i = 0; i < c.B; i += kThreads) before += __syncthreads_count(i + tid < c.B && c.indptr[i + tid + 1] <= token0);
+  if (tid < TOKENS) {
+    const int token = token0 + tid;
+    TokenPlace p = {-1, 0, -1, 0};
+    int b = before;
+    while (b < c.B && c.indptr[b + 1] <= token) ++b;
+    if (token < c.N && b < c.B) {
+      const Request r = load_request(c, b, limit);
+      if (r.ok && token >= r.start && token < r.end) {
+        p.request = b;
+        p.pos = r.past + (token - r.start);
+        const int entry = p.pos / c.page_size;
+        p.slot = p.pos - entry * c.page_size;
+        p.page = c.table[b * c.table_stride + entry];
+        if (p.page < 0 || p.page >= c.num_pages) {
+          atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
+          p.page = -1;
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = pack2<BF16>(y[2 * e], y[2 * e + 1]);
     }
-    *reinterpret_cast<uint4*>(dst + d0) = x;
+    s_place[tid] = p;
   }
+  if (blockIdx.x == 0)  // one CTA looks every request over
+    for (int b = tid; b < c.B; b += kThreads)
+      if (!load_request(c, b, limit).ok) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
+  __syncthreads();
+  if (a.rotary != nullptr) {
+    for (int i = tid; i < TOKENS * a.rot_dim; i += kThreads) {
+      const int t = i / a.rot_dim, j = i - t * a.rot_dim;
+      if (s_place[t].request >= 0) s_cs[t][j] = a.rotary[(long long)s_place[t].pos * a.rot_dim + j];
+    }
+    __syncthreads();
+  }
+
+  // ---- the rows: a thread keeps its place within a head (no division per vector) and goes through the heads of
+  // all tokens, kRows rows of the CTA's threads at a time
+  const int half = a.rot_dim / 2, vecs = c.head_dim / 8;
+  const int pairs = PAIRING == kHalves ? half / 8 : 0;  // tasks of two vectors
+  const int tasks = vecs - pairs;
+  {
+    const int heads = a.q_heads + c.kv_heads;
+    const int rows = kThreads / tasks, j = tid % tasks;
+    const bool pair = j < pairs;
+    const int d = (PAIRING == kHalves && !pair ? j + pairs : j) * 8;  // (the pairs take 2 * pairs vectors)
+    int t = 0, h = tid / tasks;
+    if (h >= rows) t = TOKENS;
+#pragma unroll PAIRING == kHalves ? 2 : 4
+    for (;; h += rows) {
+      while (h >= heads && t < TOKENS) {
+        h -= heads;
+        ++t;
+      }
+      if (t >= TOKENS) break;
+      const TokenPlace p = s_place[t];
+      const bool is_q = h < a.q_heads;
+      if (p.request < 0 || (!is_q && p.page < 0)) continue;
+      const long long token = token0 + t;
+      const uint16_t* src = is_q ? a.q.p + token * a.q.tok + h * a.q.head
+                                 : a.k.p + token * a.k.tok + (h - a.q_heads) * a.k.head;
+      uint16_t* dst = is_q ? a.out_q.p + token * a.out_q.tok + h * a.out_q.head
+                           : c.k + p.page * c.k_page + p.slot * c.k_slot + (h - a.q_heads) * c.k_head;
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + d));
+      uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      const float* cs = s_cs[t];
+      if (PAIRING == kHalves && pair) {
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(src + half + d));
+        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 co = *reinterpret_cast<const float2*>(cs + d + 2 * e);
+          const float2 si = *reinterpret_cast<const float2*>(cs + half + d + 2 * e);
+          const float2 p0 = unpack2<BF16>(u[e]), p1 = unpack2<BF16>(w[e]);
+          u[e] = pack2<BF16>(first_of(p0.x, p1.x, co.x, si.x), first_of(p0.y, p1.y, co.y, si.y));
+          w[e] = pack2<BF16>(second_of(p0.x, p1.x, co.x, si.x), second_of(p0.y, p1.y, co.y, si.y));
+        }
+        *reinterpret_cast<uint4*>(dst + half + d) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if (PAIRING != kHalves && d < a.rot_dim) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpack2<BF16>(u[e]);
+          const int d0 = d + 2 * e;
+          float2 z = v;
+          if (PAIRING == kPlain) {
+            if (d0 < a.rot_dim) {
+              const float co = cs[d0 / 2], si = cs[half + d0 / 2];
+              z = make_float2(first_of(v.x, v.y, co, si), second_of(v.x, v.y, co, si));
+            }
+          } else {
+            auto turn = [&](int at, float own) {
+              if (at >= a.rot_dim) return own;
+              const int q = at < half ? at : at - half;
+              const float other = unpack1<BF16>(src[at < half ? at + half : q]);
+              return at < half ? first_of(own, other, cs[q], cs[half + q]) : second_of(other, own, cs[q], cs[half + q]);
+            };
+            z = make_float2(turn(d0, v.x), turn(d0 + 1, v.y));
+          }
+          u[e] = pack2<BF16>(z.x, z.y);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + d) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+  // values
+  const int rows = kThreads / vecs, d = (tid % vecs) * 8;
+  int t = 0, h = tid / vecs;
+  if (h >= rows) return;
+#pragma unroll 4
+  for (;; h += rows) {
+    while (h >= c.kv_heads && t < TOKENS) {
+      h -= c.kv_heads;
+      ++t;
+    }
+    if (t >= TOKENS) break;
+    const TokenPlace p = s_place[t];
+    if (p.request < 0 || p.page < 0) continue;
+    *reinterpret_cast<uint4*>(c.v + p.page * c.v_page + p.slot * c.v_slot + h * c.v_head + d) =
+        __ldg(reinterpret_cast<const uint4*>(a.v.p + (long long)(token0 + t) * a.v.tok + h * a.v.head + d));
+  }
+}
+
+template <bool BF16, int PAIRING>
+void launch(const AppendArgs& a, cudaStream_t s) {
+  // one token to a CTA until every SM has eight, then more of them share the search and the chain of loads
+  if (a.c.N <= 2048) paged_append_kernel<BF16, PAIRING, 1><<<a.c.N, kThreads, 0, s>>>(a);
+  else paged_append_kernel<BF16, PAIRING, 8><<<(a.c.N + 7) / 8, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == ASV_BF16) paged_append_kernel<true><<<a.c.N, kThreads, 0, s>>>(a);
-  else paged_append_kernel<false><<<a.c.N, kThreads, 0, s>>>(a);
+  const int pairing = a.rotary == nullptr || a.interleaved ? kPlain : a.rot_dim % 16 == 0 ? kHalves : kScattered;
+  const bool bf16 = dtype == ASV_BF16;
+  switch (pairing) {
+    case kPlain: bf16 ? launch<true, kPlain>(a, s) : launch<false, kPlain>(a, s); break;
+    case kHalves: bf16 ? launch<true, kHalves>(a, s) : launch<false, kHalves>(a, s); break;
+    default: bf16 ? launch<true, kScattered>(a, s) : launch<false, kScattered>(a, s);
+  }
   return cudaGetLastError();
 }
 
