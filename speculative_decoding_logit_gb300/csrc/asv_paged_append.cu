@@ -45,6 +45,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   const int tid = threadIdx.x, token0 = blockIdx.x * TOKENS;
   const long long limit = a.rotary != nullptr ? min((long long)a.max_position, table_positions(c)) : table_positions(c);
 
+  // What came before on the stream is needed from here on; what comes after may set itself up.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // ---- the tokens' requests and places
   int before = 0;
   for (int i = 0; i < c.B; i += kThreads) before += __syncthreads_count(i + tid < c.B && c.indptr[i + tid + 1] <= token0);
@@ -168,10 +172,22 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
 }
 
 template <bool BF16, int PAIRING>
-void launch(const AppendArgs& a, cudaStream_t s) {
-  // one token to a CTA until every SM has eight, then more of them share the search and the chain of loads
-  if (a.c.N <= 2048) paged_append_kernel<BF16, PAIRING, 1><<<a.c.N, kThreads, 0, s>>>(a);
-  else paged_append_kernel<BF16, PAIRING, 8><<<(a.c.N + 7) / 8, kThreads, 0, s>>>(a);
+cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
+  // a programmatic launch: the CTAs start while the launch before it ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // one token to a CTA until every SM has a dozen, then more of them share the search and the chain of loads
+  // (9216 tokens: 37 us at eight to a CTA, 45 at one)
+  const int tokens = a.c.N <= 2048 ? 1 : 8;
+  cfg.gridDim = dim3(unsigned((a.c.N + tokens - 1) / tokens), 1, 1);
+  return tokens == 1 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 1>, a)
+                     : cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 8>, a);
 }
 
 }  // namespace
@@ -180,11 +196,10 @@ cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s) 
   const int pairing = a.rotary == nullptr || a.interleaved ? kPlain : a.rot_dim % 16 == 0 ? kHalves : kScattered;
   const bool bf16 = dtype == ASV_BF16;
   switch (pairing) {
-    case kPlain: bf16 ? launch<true, kPlain>(a, s) : launch<false, kPlain>(a, s); break;
-    case kHalves: bf16 ? launch<true, kHalves>(a, s) : launch<false, kHalves>(a, s); break;
-    default: bf16 ? launch<true, kScattered>(a, s) : launch<false, kScattered>(a, s);
+    case kPlain: return bf16 ? launch<true, kPlain>(a, s) : launch<false, kPlain>(a, s);
+    case kHalves: return bf16 ? launch<true, kHalves>(a, s) : launch<false, kHalves>(a, s);
+    default: return bf16 ? launch<true, kScattered>(a, s) : launch<false, kScattered>(a, s);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace asv

@@ -27,6 +27,7 @@
 // NT = 1 keeps two S and two output buffers, so the next tile's S is formed while the softmax runs; NT = 2
 // gives each row tile one, and the two tiles alternate.
 #include <algorithm>
+#include <atomic>
 
 #include "asv_paged_device.cuh"
 #include "asv_tcgen05.cuh"
@@ -67,12 +68,12 @@ struct Misc {
   uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
   Piece piece[kQueue];
   long long warp_sum[12];
-  long long start_units;  // units before the run's first request
-  int start_request;
+  long long start_item0;  // the run's first item: units before it, request, place, key tiles, head
+  int start_request, start_i, start_n, start_h;
   uint32_t tmem;
   int abort;
   int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
-  int last[2];
+  int last[2][2];
 };
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0: each round takes out the whole parts of a / m and b / m
@@ -136,6 +137,11 @@ __device__ Items load_items(const PagedView& c, int b, int T) {
   const bool rows = it.r.start >= 0 && it.r.start <= it.r.end && it.r.end <= c.N;
   it.n = rows ? (it.r.end - it.r.start + T - 1) / T : 0;
   return it;
+}
+
+// a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
 // Counters of a ring of `n` barriers: slot and phase of the i-th use.
@@ -325,6 +331,9 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     prefetch_map(&map_k);
     prefetch_map(&map_v);
   }
+  // What came before on the stream is needed from here on; what comes after may set itself up.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // units of this thread's requests, and of all
   const int per_thread = (c.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per_thread, c.B), b1 = min(b0 + per_thread, c.B);
@@ -348,15 +357,29 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     if (w < warp) before += ms.warp_sum[w];
     total += ms.warp_sum[w];
   }
-  const long long per_cta = max((total + gridDim.x - 1) / (long long)gridDim.x, 1ll);
+  const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
   const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
   if (u0 >= before && u0 < before + own) {
     long long x = before;
     for (int b = b0; b < b1; ++b) {
-      const long long n = load_items(c, b, T).units(a.window, kCost, c.kv_heads);
+      const Items it = load_items(c, b, T);
+      const long long n = it.units(a.window, kCost, c.kv_heads);
       if (u0 < x + n) {
+        const long long rel = u0 - x;
+        int i = 0;  // the item that holds unit u0: the last with no more than rel units before it
+        for (int hi = it.n; hi - i > 1;) {
+          const int mid = (i + hi) / 2;
+          if (c.kv_heads * it.before(a.window, kCost, mid) <= rel) i = mid;
+          else hi = mid;
+        }
+        const int tiles = it.tiles(a.window, i);
+        const long long item = x + c.kv_heads * it.before(a.window, kCost, i);
+        const int h = int(quotient(u0 - item, tiles + kCost));
         ms.start_request = b;
-        ms.start_units = x;
+        ms.start_i = i;
+        ms.start_n = tiles;
+        ms.start_h = h;
+        ms.start_item0 = item + (long long)h * (tiles + kCost);
         break;
       }
       x += n;
@@ -372,19 +395,9 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
   } else if (warp == kWalkWarp) {
     // ---- scheduler
     if (lane == 0) {
-      int b = ms.start_request;
+      int b = ms.start_request, i = ms.start_i, n = ms.start_n, h = ms.start_h;
+      long long item0 = ms.start_item0;
       Items it = load_items(c, b, T);
-      const long long rel = u0 - ms.start_units;
-      int i = 0;  // the item that holds unit u0: the last with no more than rel units before it
-      for (int hi = it.n; hi - i > 1;) {
-        const int mid = (i + hi) / 2;
-        if (c.kv_heads * it.before(a.window, kCost, mid) <= rel) i = mid;
-        else hi = mid;
-      }
-      int n = it.tiles(a.window, i);
-      const long long off = rel - c.kv_heads * it.before(a.window, kCost, i);
-      int h = int(off / (n + kCost));
-      long long item0 = u0 - off % (n + kCost);  // units before the item
       Ring ring_p;
       for (bool end = false; !end;) {
         // its first kCost units are its own, then one for each key tile
@@ -407,8 +420,8 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
             p.t1 = it.r.ok ? tile0 + tb : 0;
             p.part = -1;
             if (tb - ta < n) {
-              p.first_cta = int((item0 + kCost) / per_cta);
-              p.n_parts = int((item0 + kCost + n - 1) / per_cta) - p.first_cta + 1;
+              p.first_cta = int(quotient(item0 + kCost, per_cta));
+              p.n_parts = int(quotient(item0 + kCost + n - 1, per_cta)) - p.first_cta + 1;
               p.part = 2 * int(blockIdx.x) + (ta == 0 ? 1 : 0);
             }
           }
@@ -989,25 +1002,23 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       }
       if (p.part < 0) continue;
 
-      // the last to file joins the parts, in CTA order
-      __threadfence();
+      // The last to file joins the parts, in CTA order.  The warps' writes come before the ticket through the
+      // barrier and the ticket's release, the other CTAs' before the reads through its acquire and the barrier.
       if (!wg_sync()) break;
       if (row == 0) {
         const uint32_t old = atom_add_acq_rel_gpu(a.tickets + 2 * p.first_cta + wg, 1u);
-        ms.last[wg] = old == uint32_t(p.n_parts - 1);
+        ms.last[wg][sync_phase] = old == uint32_t(p.n_parts - 1);
       }
+      const uint32_t which = sync_phase;
       if (!wg_sync()) break;
-      const bool last = *reinterpret_cast<volatile int*>(&ms.last[wg]) != 0;
-      if (!wg_sync()) break;
-      if (!last) continue;
-      __threadfence();
+      if (*reinterpret_cast<volatile int*>(&ms.last[wg][which]) == 0) continue;
       if (row == 0) a.tickets[2 * p.first_cta + wg] = 0;
       const int cols4 = c.head_dim / 4;
       for (int i = row; i < n_rows * cols4; i += kTile) {
         const int c4 = i / n_rows, r = i - c4 * n_rows;
         float m = -INFINITY, l = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 0; k < p.n_parts; ++k) {
           const int slot = k == 0 ? 2 * p.first_cta + 1 : 2 * (p.first_cta + k);
           const float* part = a.parts + (size_t(slot) * 2 + wg) * part_floats;
@@ -1072,14 +1083,30 @@ cudaError_t make_map(CUtensorMap* m, bool bf16, void* base, int rank, const cuui
 }
 
 template <bool BF16, int DP, int NT>
-cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, cudaStream_t s) {
+cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, int dev, cudaStream_t s) {
   auto kernel = paged_attention_kernel<BF16, DP, NT>;
   constexpr int kSmem = 1024 + (2 + kRingSlots<DP>) * kTile * DP * 2 + int(sizeof(Misc));
   static_assert(kSmem <= 232448, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  kernel<<<grid, 32 * (4 * NT + 3), kSmem, s>>>(a, maps[0], maps[1], maps[2]);
-  return cudaGetLastError();
+  // the limit is raised once per device
+  static std::atomic<uint64_t> raised{0};
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  // a programmatic launch: the set-up runs while the launch before it ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(32 * (4 * NT + 3), 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, maps[0], maps[1], maps[2]);
 }
 
 }  // namespace
@@ -1092,6 +1119,7 @@ cudaError_t launch_paged_attention(const AttendArgs& args, int dtype, cudaStream
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
   a.tile_tokens = kTile / a.group;
   a.box = std::min(kTile, c.page_size & -c.page_size);
   CUtensorMap maps[3];
@@ -1110,14 +1138,14 @@ cudaError_t launch_paged_attention(const AttendArgs& args, int dtype, cudaStream
   const bool two = (long long)c.N * a.group > (long long)kTile * c.B;
   const int which = (bf16 ? 4 : 0) + (c.head_dim > 64 ? 2 : 0) + (two ? 1 : 0);
   switch (which) {
-    case 0: return launch<false, 64, 1>(a, maps, grid, s);
-    case 1: return launch<false, 64, 2>(a, maps, grid, s);
-    case 2: return launch<false, 128, 1>(a, maps, grid, s);
-    case 3: return launch<false, 128, 2>(a, maps, grid, s);
-    case 4: return launch<true, 64, 1>(a, maps, grid, s);
-    case 5: return launch<true, 64, 2>(a, maps, grid, s);
-    case 6: return launch<true, 128, 1>(a, maps, grid, s);
-    default: return launch<true, 128, 2>(a, maps, grid, s);
+    case 0: return launch<false, 64, 1>(a, maps, grid, dev, s);
+    case 1: return launch<false, 64, 2>(a, maps, grid, dev, s);
+    case 2: return launch<false, 128, 1>(a, maps, grid, dev, s);
+    case 3: return launch<false, 128, 2>(a, maps, grid, dev, s);
+    case 4: return launch<true, 64, 1>(a, maps, grid, dev, s);
+    case 5: return launch<true, 64, 2>(a, maps, grid, dev, s);
+    case 6: return launch<true, 128, 1>(a, maps, grid, dev, s);
+    default: return launch<true, 128, 2>(a, maps, grid, dev, s);
   }
 }
 
