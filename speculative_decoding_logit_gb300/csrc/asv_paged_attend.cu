@@ -46,6 +46,10 @@ template <int NT>
 constexpr int kItemCost = NT == 1 ? 2 : 4;
 constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
 
+// Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler.
+template <int NT>
+constexpr int kThreadsOf = 32 * (4 * NT + 4);
+
 template <int DP>
 constexpr int kRingSlots = DP == 128 ? 5 : 10;
 
@@ -148,9 +152,10 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 struct Ring {
   int slot = 0;
   uint32_t phase = 0;
-  __device__ void next(int n) {
-    if (++slot == n) {
-      slot = 0;
+  __device__ void next(int n, int by = 1) {
+    slot += by;
+    if (slot >= n) {
+      slot -= n;
       phase ^= 1;
     }
   }
@@ -282,10 +287,10 @@ __device__ __noinline__ void add_poison(const PagedView& c, int request, int hea
 }
 
 template <bool BF16, int DP, int NT>
-__global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
+__global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  constexpr int kThreads = 32 * (4 * NT + 3);
+  constexpr int kThreads = kThreadsOf<NT>;
   constexpr int kCost = kItemCost<NT>;
   constexpr int kRing = kRingSlots<DP>;
   constexpr int kHalves = DP / 64;                // 64-element column blocks, 128 bytes a row
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
   Misc& ms = *reinterpret_cast<Misc*>(smem_raw + (smem0 - smem_addr(smem_raw)) + (2 + kRing) * kTileBytes);
   const PagedView& c = a.c;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  constexpr int kMmaWarp = 4 * NT, kCopyWarp = 4 * NT + 1, kWalkWarp = 4 * NT + 2;
+  constexpr int kMmaWarp = 4 * NT, kCopyWarp = 4 * NT + 1, kWalkWarp = 4 * NT + 3;
   const int T = NT * a.tile_tokens;  // tokens of an item
   volatile int* abort = &ms.abort;
 
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       bar_init(at(ms.piece_full, i), 1);
-      bar_init(at(ms.piece_empty, i), 2 + 4 * NT);
+      bar_init(at(ms.piece_empty, i), 3 + 4 * NT);
     }
     ms.abort = 0;
     fence_barrier_init();
@@ -442,8 +447,9 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         }
       }
     }
-  } else if (warp == kCopyWarp) {
-    // ---- copies
+  } else if (warp == kCopyWarp || warp == kCopyWarp + 1) {
+    // ---- copies: one warp for keys and queries, one for values; a copy takes its warp about 50 cycles
+    const bool values = warp == kCopyWarp + 1;
     // 32 lanes hold the pages of up to 32 boxes, a window of one or more tiles; the next window's entries of
     // the block table are on their way while this one's tiles are copied.
     Ring ring_p, ring_kv, ring_q;
@@ -490,8 +496,11 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       t += w.n;
       return true;
     };
-    // one tile of keys (or values) into the next slot of the ring: the lanes of `g` copy their boxes
-    auto copy_tile = [&](const CUtensorMap* map, int head, int g, int page, int slot) {
+    // A tile's keys and values take two slots of the ring, one after the other.
+    if (values) ring_kv.next(kRing);
+    const CUtensorMap* map = values ? &map_v : &map_k;
+    // one tile of keys (or values) into its slot: the lanes of `g` copy their boxes
+    auto copy_tile = [&](int head, int g, int page, int slot) {
       if (!warp_wait(at(ms.kv_empty, ring_kv.slot), ring_kv.phase ^ 1, abort)) return false;
       const uint32_t bar = at(ms.kv_full, ring_kv.slot);
       if (lane == 0) bar_expect(bar, kTileBytes);
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
         for (int h = 0; h < kHalves; ++h) copy_4d(dst + h * kHalfBytes, map, h * 64, head, slot, page, bar);
       }
       __syncwarp();
-      ring_kv.next(kRing);
+      ring_kv.next(kRing, 2);
       return true;
     };
     auto copy_queries = [&](const Window& w) {
@@ -522,7 +531,6 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     };
     Window w, ahead;
     ahead.n = 0;
-    int v_head = 0, v_group = -1, v_page = 0, v_slot = 0;  // the previous tile, whose values are copied next
     bool run = true;
     while (run) {
       if (ahead.n == 0 && (!next_window(true, ahead) || ahead.n == 0)) break;
@@ -532,19 +540,11 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       const int page = ok ? w.entry : c.num_pages;
       next_window(false, ahead);
       for (int i = 0; i < w.n && run; ++i) {
-        // the order the tensor cores take them in
-        if (NT == 2 && v_group >= 0) run = copy_tile(&map_v, v_head, v_group, v_page, v_slot);
-        run = run && copy_tile(&map_k, w.head, i, page, w.slot);
-        if (i == 0 && w.first) run = run && copy_queries(w);
-        if (NT == 1 && v_group >= 0) run = run && copy_tile(&map_v, v_head, v_group, v_page, v_slot);
-        v_head = w.head;
-        v_group = i;
-        v_page = page;
-        v_slot = w.slot;
+        run = copy_tile(w.head, i, page, w.slot);
+        if (i == 0 && w.first && !values) run = run && copy_queries(w);
       }
     }
-    if (v_group >= 0 && run) copy_tile(&map_v, v_head, v_group, v_page, v_slot);
-    if (*abort) {  // leave with no copy in flight: every slot of the ring once more
+    if (*abort) {  // leave with no copy in flight: the slots still being written, for a while
       for (int i = 0; i < kRing; ++i) {
         const unsigned long long t0 = now_ns();
         const uint32_t parity = i < ring_kv.slot ? ring_kv.phase : ring_kv.phase ^ 1;
@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
     }
   } else if (warp == kMmaWarp) {
     // ---- matrices
-    Ring ring_p, ring_kv, ring_q;
+    Ring ring_p, ring_k, ring_v, ring_q;
+    ring_v.next(kRing);
     const uint32_t id_qk = instr_desc(BF16, false, kTile);
     const uint32_t id_pv = instr_desc(BF16, true, (c.head_dim + 15) / 16 * 16);
     const int k_steps = (c.head_dim + 15) / 16;
@@ -668,12 +669,10 @@ __global__ void __launch_bounds__(32 * (4 * NT + 3), 1)
       }
       if (!run) break;
       const int tiles = NT == 1 || p.ntok <= a.tile_tokens ? 1 : 2;
-      // their slots of the ring, in the order of the copies
-      Ring key = ring_kv, value = ring_kv;
-      if (NT == 1 && more) value.next(kRing);
-      if (NT == 2 && have_prev) key.next(kRing);
-      if (more) ring_kv.next(kRing);
-      if (have_prev) ring_kv.next(kRing);
+      // slots of the ring: the next tile's keys, the previous one's values
+      const Ring key = ring_k, value = ring_v;
+      if (more) ring_k.next(kRing, 2);
+      if (have_prev) ring_v.next(kRing, 2);
       const bool first = t == p.t0;
       int q = 0;
       auto begin_tile = [&]() {  // keys (and queries) of the next tile are there
@@ -1098,7 +1097,7 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, int d
   // a programmatic launch: the set-up runs while the launch before it ends
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid), 1, 1);
-  cfg.blockDim = dim3(32 * (4 * NT + 3), 1, 1);
+  cfg.blockDim = dim3(kThreadsOf<NT>, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
