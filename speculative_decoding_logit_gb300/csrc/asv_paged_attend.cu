@@ -80,33 +80,54 @@ struct Misc {
   int last[2][2];
 };
 
+// a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0: each round takes out the whole parts of a / m and b / m
 // and counts the lattice points left under the line with the axes exchanged.
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+__device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long sum = 0;
   for (;;) {
     if (a >= m) {
-      sum += n * (n - 1) / 2 * (a / m);
-      a %= m;
+      const long long q = quotient(a, m);
+      sum += n * (n - 1) / 2 * q;
+      a -= q * m;
     }
     if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
+      const long long q = quotient(b, m);
+      sum += n * q;
+      b -= q * m;
     }
     const long long top = a * n + b;
     if (top < m) return sum;
-    n = top / m;
-    b = top % m;
+    n = quotient(top, m);
+    b = top - n * m;
     const long long t = m;
     m = a;
     a = t;
   }
 }
 
+// sum_{i < n} floor((T i + b) / 128) for b >= 0; `shift` is log2 T where T is a power of two, else -1.
+__device__ __forceinline__ long long tile_sum(long long n, int T, int shift, long long b) {
+  if (shift < 0) return floor_sum(n, kTile, T, b);
+  if (shift >= 7) return n * (b >> 7) + ((n * (n - 1) / 2) << (shift - 7));
+  // floor((floor(b / T) + i) / r), r = 128 / T: differences of sum_{m < x} floor(m / r)
+  const int s = 7 - shift;
+  auto below = [&](long long x) {
+    const long long q = x >> s;
+    return ((q * (q - 1) / 2) << s) + q * (x - (q << s));
+  };
+  const long long c = b >> shift;
+  return below(c + n) - below(c);
+}
+
 // A request's items of one key head: n of them, item r with the tokens from r * T.
 struct Items {
   Request r;
-  int T, n;
+  int T, shift, n;
   __device__ int lo(int window, int i) const { return window > 0 ? max(0, r.past + i * T - window + 1) : 0; }
   // key tiles (1 for a request that is left out)
   __device__ int tiles(int window, int i) const {
@@ -118,11 +139,11 @@ struct Items {
   __device__ long long tiles_before(int window, int i) const {
     if (i == 0) return 0;
     if (!r.ok) return i;
-    long long sum = floor_sum(i, kTile, T, (long long)r.past + T + kTile - 1);
+    long long sum = tile_sum(i, T, shift, (long long)r.past + T + kTile - 1);
     if (window > 0) {
       // items before z start at position 0
-      const long long z = r.past >= window - 1 ? 0 : ((long long)window - 1 - r.past + T - 1) / T;
-      if (i > z) sum -= floor_sum(i - z, kTile, T, r.past + z * T - window + 1);
+      const long long z = r.past >= window - 1 ? 0 : quotient((long long)window - 1 - r.past + T - 1, T);
+      if (i > z) sum -= tile_sum(i - z, T, shift, r.past + z * T - window + 1);
     }
     return sum;
   }
@@ -137,15 +158,11 @@ __device__ Items load_items(const PagedView& c, int b, int T) {
   Items it;
   it.r = load_request(c, b, table_positions(c));
   it.T = T;
+  it.shift = (T & (T - 1)) == 0 ? 31 - __clz(T) : -1;
   // the rows of a request that is left out are still zeroed, where they are rows
   const bool rows = it.r.start >= 0 && it.r.start <= it.r.end && it.r.end <= c.N;
   it.n = rows ? (it.r.end - it.r.start + T - 1) / T : 0;
   return it;
-}
-
-// a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
 // Counters of a ring of `n` barriers: slot and phase of the i-th use.
@@ -1012,32 +1029,103 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       if (!wg_sync()) break;
       if (*reinterpret_cast<volatile int*>(&ms.last[wg][which]) == 0) continue;
       if (row == 0) a.tickets[2 * p.first_cta + wg] = 0;
-      const int cols4 = c.head_dim / 4;
-      for (int i = row; i < n_rows * cols4; i += kTile) {
-        const int c4 = i / n_rows, r = i - c4 * n_rows;
-        float m = -INFINITY, l = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int k = 0; k < p.n_parts; ++k) {
-          const int slot = k == 0 ? 2 * p.first_cta + 1 : 2 * (p.first_cta + k);
-          const float* part = a.parts + (size_t(slot) * 2 + wg) * part_floats;
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + kTile * DP) + r);
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + c4 * kTile + r);
-          const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
-          const float wa = ex2_approx(m - base), wb = ex2_approx(ml.x - base);
+      // A thread keeps one row: `span` threads side by side have the rows, the others further columns.
+      const int span = n_rows <= 1 ? 1 : 1 << (32 - __clz(n_rows - 1)), r = row & (span - 1);
+      const int cols4 = c.head_dim / 4, step = kTile / span;
+      if (r >= n_rows) continue;
+      auto part_of = [&](int k) {
+        const int slot = k == 0 ? 2 * p.first_cta + 1 : 2 * (p.first_cta + k);
+        return a.parts + (size_t(slot) * 2 + wg) * part_floats;
+      };
+      auto stats_of = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part_of(k) + kTile * DP) + r); };
+      const int tk = r / a.group, hd = p.head * a.group + (r - tk * a.group);
+      const int dst = p.tok0 + first_tok + tk;
+      if (!ASV_GUARD(a, dst >= 0 && dst < c.N && hd < a.q_heads)) continue;
+      uint16_t* out = a.out.p + dst * a.out.tok + hd * a.out.head;
+      const int col0 = row / span;
+      auto put = [&](int col, float4 y) {
+        *reinterpret_cast<uint2*>(out + col * 4) = make_uint2(pack2<BF16>(y.x, y.y), pack2<BF16>(y.z, y.w));
+      };
+      auto add = [](float4 acc, float4 o, float w) {
+        return make_float4(fmaf(o.x, w, acc.x), fmaf(o.y, w, acc.y), fmaf(o.z, w, acc.z), fmaf(o.w, w, acc.w));
+      };
+      const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float m = -INFINITY, l = 0.0f;
+      // The parts in order, `kIn` at a time with all their loads in flight.  Few rows: a thread has one vector of
+      // four columns and everything of a part at once.  Many: the rows' sums first, then eight vectors a time.
+      constexpr int kIn = 8, kCols = 8;
+      if (cols4 <= step) {
+        float4 acc = zero;
+        for (int k0 = 0; k0 < p.n_parts; k0 += kIn) {
+          float2 ml[kIn];
+          float4 o[kIn];
+#pragma unroll
+          for (int k = 0; k < kIn; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.0f);
+            o[k] = zero;
+            if (k0 + k < p.n_parts && col0 < cols4) {
+              ml[k] = stats_of(k0 + k);
+              o[k] = __ldcg(reinterpret_cast<const float4*>(part_of(k0 + k)) + col0 * kTile + r);
+            }
+          }
+          float top = m;
+#pragma unroll
+          for (int k = 0; k < kIn; ++k) top = fmaxf(top, ml[k].x);
+          const float base = top == -INFINITY ? 0.0f : top, keep = ex2_approx(m - base);
           m = top;
-          l = l * wa + ml.y * wb;
-          acc = make_float4(acc.x * wa + o.x * wb, acc.y * wa + o.y * wb, acc.z * wa + o.z * wb, acc.w * wa + o.w * wb);
+          l *= keep;
+          acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+          for (int k = 0; k < kIn; ++k) {
+            const float w = ex2_approx(ml[k].x - base);
+            l = fmaf(ml[k].y, w, l);
+            acc = add(acc, o[k], w);
+          }
         }
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        const int tk = r / a.group, hd = p.head * a.group + (r - tk * a.group);
-        const int dst = p.tok0 + first_tok + tk;
-        if (!ASV_GUARD(a, dst >= 0 && dst < c.N && hd < a.q_heads)) continue;
-        *reinterpret_cast<uint2*>(a.out.p + dst * a.out.tok + hd * a.out.head + c4 * 4) =
-            make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-        if (c4 == 0 && a.lse != nullptr)
-          a.lse[(long long)dst * a.q_heads + hd] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
+        if (col0 < cols4) put(col0, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      } else {
+#pragma unroll 8
+        for (int k = 0; k < p.n_parts; ++k) {
+          const float2 ml = stats_of(k);
+          const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
+          l = l * ex2_approx(m - base) + ml.y * ex2_approx(ml.x - base);
+          m = top;
+        }
+        const float base = m == -INFINITY ? 0.0f : m, inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        for (int c0 = col0 * kCols; c0 < cols4; c0 += kCols * step) {
+          float4 acc[kCols];
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) acc[i] = zero;
+          for (int k = 0; k < p.n_parts; k += 2) {
+            float4 o[2][kCols];
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // (what is past the last is read again, with no weight)
+              const int at = min(k + e, p.n_parts - 1);
+              const float4* part = reinterpret_cast<const float4*>(part_of(at)) + r;
+              w[e] = k + e < p.n_parts ? stats_of(at).x : -INFINITY;
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) o[e][i] = ld_cg_f4(part + min(c0 + i, cols4 - 1) * kTile);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              w[e] = ex2_approx(w[e] - base) * inv;
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) acc[i] = add(acc[i], o[e][i], w[e]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2)
+            if (c0 + i < cols4)
+              *reinterpret_cast<uint4*>(out + (c0 + i) * 4) =
+                  make_uint4(pack2<BF16>(acc[i].x, acc[i].y), pack2<BF16>(acc[i].z, acc[i].w),
+                             pack2<BF16>(acc[i + 1].x, acc[i + 1].y), pack2<BF16>(acc[i + 1].z, acc[i + 1].w));
+        }
       }
+      if (row < span && a.lse != nullptr)
+        a.lse[(long long)dst * a.q_heads + hd] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
     }
     if (*abort && lane == 0) {
       for (int b = 0; b < c.B; ++b) atomicOr(a.status + b, ASV_REQ_TIMEOUT);
