@@ -28,6 +28,7 @@
 // gives each row tile one, and the two tiles alternate.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "asv_paged_device.cuh"
 #include "asv_tcgen05.cuh"
@@ -43,7 +44,7 @@ constexpr int kQueue = 4;
 constexpr uint32_t kTmemColumns = 512;  // S buffers at 0 and 128, outputs at 256 and 384
 // Key tiles that an item's own work (queries in, outputs out, the pipeline's fill) is worth in the split.
 template <int NT>
-constexpr int kItemCost = NT == 1 ? 2 : 4;
+constexpr int kItemCost = 2;
 constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
 
 // Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler.
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       while (t == p.t1) {
         if (p.kind == 1) return true;
         const uint32_t bar = at(ms.piece_full, ring_p.slot);
-        if (block ? !warp_wait(bar, ring_p.phase, abort) : !__all_sync(0xffffffffu, bar_try(bar, ring_p.phase)))
+        if (block ? !warp_wait(bar, ring_p.phase, abort) : !__all_sync(0xffffffffu, bar_test(bar, ring_p.phase)))
           return !block;
         p = ms.piece[ring_p.slot];
         __syncwarp();
@@ -571,18 +572,11 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     }
   } else if (warp == kMmaWarp) {
     // ---- matrices
-    Ring ring_p, ring_k, ring_v, ring_q;
+    Ring ring_p, ring_k, ring_v, ring_q;  // a tile's keys and values take two slots of the ring, one after the other
     ring_v.next(kRing);
     const uint32_t id_qk = instr_desc(BF16, false, kTile);
     const uint32_t id_pv = instr_desc(BF16, true, (c.head_dim + 15) / 16 * 16);
     const int k_steps = (c.head_dim + 15) / 16;
-    int used[2] = {0, 0};   // S / P buffer uses so far
-    int items[2] = {0, 0};  // output buffer uses so far
-    int cur_ob = 0, next_ob = 0;
-    int tile_no = 0;  // NT = 1: tiles so far
-    int prev_pos0 = 0, prev_ntok = 0, prev_lo = 0, prev_tile = 0, prev_ob = 0, prev_sb = 0, prev_tiles = 0;
-    bool have_prev = false, prev_first = false, prev_last = false;
-    bool run = true;
 
     // An instruction runs 64 cycles and blocks its issue until there is room, so its operands must be there
     // by then: descriptors are those of the first tiles plus constants (in 16-byte units), unrolled, in a
@@ -604,169 +598,182 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         for (int i = 0; i < k_steps; ++i) step(i);
       }
     };
-    // out (buffer ob) += P V: one half of the tile's 16-position steps, or those of [i0, i1)
-    auto pv_half = [&](int ob, int sb, int slot, int half, bool first) {
-      const uint64_t vd = v_desc + slot * (kTileBytes / 16) + half * (4 * 2048 / 16);
+    // out (buffer ob) += P V over N of the tile's 16-position steps from i0, or over those of [i0, i1)
+    auto pv_run = [&](int ob, int sb, int slot, int i0, bool first, auto n) {
+      const uint64_t vd = v_desc + slot * (kTileBytes / 16) + i0 * (2048 / 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + half * 32 + i * 8, vd + i * (2048 / 16), id_pv, i > 0 || !first);
+      for (int i = 0; i < decltype(n)::value; ++i)
+        mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + (i0 + i) * 8, vd + i * (2048 / 16), id_pv, i > 0 || !first);
     };
     auto pv_steps = [&](int ob, int sb, int slot, bool first, int i0, int i1) {
       const uint64_t vd = v_desc + slot * (kTileBytes / 16);
       for (int i = i0; i < i1; ++i)
         mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, !(first && i == i0));
     };
-    // out += P V of the previous tile, row tile x
-    auto pv_tile = [&](int x, int v_slot, bool last_tile) {
-      const int sb = NT == 1 ? prev_sb : x, ob = NT == 1 ? prev_ob : x;
-      // the weights come in two halves
-      const uint32_t p_phase = (used[sb] & 1) ^ 1;
-      const int i0 = max(prev_lo - prev_tile * kTile, 0) / 16;
-      const int i1 = (min(prev_pos0 + prev_ntok - prev_tile * kTile, kTile) + 15) / 16;
-      const bool whole = i0 == 0 && i1 == kTile / 16;
-      if (!warp_wait(at(ms.p_full, 2 * sb), p_phase, abort)) return false;
-      fence_after();
-      if (whole && elect()) pv_half(ob, sb, v_slot, 0, prev_first);
-      __syncwarp();
-      if (!warp_wait(at(ms.p_full, 2 * sb + 1), p_phase, abort)) return false;
-      fence_after();
-      if (elect()) {
-        if (whole) pv_half(ob, sb, v_slot, 1, false);
-        else pv_steps(ob, sb, v_slot, prev_first, i0, i1);
-        if (NT == 1) commit(at(ms.pv_done, sb));
-        if (last_tile) commit(at(ms.kv_empty, v_slot));
-        if (prev_last) commit(at(ms.o_full, ob));
-      }
-      __syncwarp();
-      if (prev_last) ++items[ob];
-      return true;
+    // A tile's values: there, and safe to multiply by weights of zero.
+    struct Span {
+      int base, pos0, lo, hi;  // the tile's first position; the item's first token's, and the bounds of its rows'
+      __device__ bool whole() const { return lo <= base && base + kTile <= hi; }
+      __device__ int first_step() const { return max(lo - base, 0) / 16; }
+      __device__ int end_step() const { return (min(hi - base, kTile) + 15) / 16; }
     };
-    // the values of the previous tile are next in the ring: wait for them, make them safe
-    auto take_values = [&](int v_slot, uint32_t v_phase) {
-      if (prev_first)  // its output buffers (and their poison marks) are free
-        for (int x = 0; x < prev_tiles; ++x) {
-          const int ob = NT == 1 ? prev_ob : x;
-          if (!warp_wait(at(ms.o_empty, ob), (items[ob] & 1) ^ 1, abort)) return false;
-        }
-      if (!warp_wait(at(ms.kv_full, v_slot), v_phase, abort)) return false;
-      const int base = prev_tile * kTile, hi = prev_pos0 + prev_ntok;
-      const int last_lo = a.window > 0 ? max(0, hi - a.window) : 0;
-      if (base + kTile > prev_pos0 + 1 || base < last_lo) {
-        if (clean_values<BF16, DP>(ring + v_slot * kTileBytes, base, prev_lo, hi, prev_pos0 + 1, last_lo,
-                                   lane)) {
-          if (lane < 2 && (NT == 2 || lane == prev_ob)) *reinterpret_cast<volatile int*>(&ms.poison[lane]) = 1;
+    auto take_values = [&](const Ring& value, const Span& g, int poison0, int poison1) {
+      if (!warp_wait(at(ms.kv_full, value.slot), value.phase, abort)) return false;
+      const int last_lo = a.window > 0 ? max(0, g.hi - a.window) : 0;
+      if (g.base + kTile > g.pos0 + 1 || g.base < last_lo) {
+        if (clean_values<BF16, DP>(ring + value.slot * kTileBytes, g.base, g.lo, g.hi, g.pos0 + 1, last_lo, lane)) {
+          if (lane >= poison0 && lane <= poison1) *reinterpret_cast<volatile int*>(&ms.poison[lane]) = 1;
           __threadfence_block();
           __syncwarp();
         }
       }
       return true;
     };
+    auto next_piece = [&](Piece& p) {
+      if (!warp_wait(at(ms.piece_full, ring_p.slot), ring_p.phase, abort)) return false;
+      p = ms.piece[ring_p.slot];
+      __syncwarp();
+      if (lane == 0) bar_arrive(at(ms.piece_empty, ring_p.slot));
+      ring_p.next(kQueue);
+      return true;
+    };
 
-    Piece p;
-    int t = 0;
-    p.t0 = p.t1 = 0;
-    p.kind = 0;
-    for (; run;) {
-      // the next tile of the run
-      bool more = true;
-      while (t == p.t1) {
-        if (!warp_wait(at(ms.piece_full, ring_p.slot), ring_p.phase, abort)) {
-          run = false;
-          break;
-        }
-        p = ms.piece[ring_p.slot];
-        __syncwarp();
-        if (lane == 0) bar_arrive(at(ms.piece_empty, ring_p.slot));
-        ring_p.next(kQueue);
-        t = p.t0;
-        if (p.kind == 1) {
-          more = false;
-          break;
-        }
-      }
-      if (!run) break;
-      const int tiles = NT == 1 || p.ntok <= a.tile_tokens ? 1 : 2;
-      // slots of the ring: the next tile's keys, the previous one's values
-      const Ring key = ring_k, value = ring_v;
-      if (more) ring_k.next(kRing, 2);
-      if (have_prev) ring_v.next(kRing, 2);
-      const bool first = t == p.t0;
-      int q = 0;
-      auto begin_tile = [&]() {  // keys (and queries) of the next tile are there
-        if (!warp_wait(at(ms.kv_full, key.slot), key.phase, abort)) return false;
-        if (first) {
-          if (!warp_wait(at(ms.q_full, ring_q.slot), ring_q.phase, abort)) return false;
-          cur_ob = next_ob;
-          if (NT == 1) next_ob ^= 1;
-        }
-        if (NT == 1) q = ring_q.slot;
+    if constexpr (NT == 2) {
+      // Piece by piece; the two row tiles in turn, each tile's product and then its next S, which goes where the
+      // weights were.
+      uint32_t p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
+      Piece p;
+      for (bool ok = true; ok && next_piece(p) && p.kind == 0;) {
+        if (p.t0 == p.t1) continue;
+        const int tiles = p.ntok <= a.tile_tokens ? 1 : 2;
+        Span g = {p.t0 * kTile, p.pos0, p.kv_lo, p.pos0 + p.ntok};
+        ok = warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort) && warp_wait(at(ms.q_full, 0), ring_q.phase, abort);
+        if (!ok) break;
         fence_after();
-        return true;
-      };
-      auto qk_tile = [&](int x) {
-        const int sb = NT == 1 ? tile_no & 1 : x;
-        const bool last_x = x == tiles - 1, last_q = last_x && t == p.t1 - 1;
         if (elect()) {
-          qk(sb, NT == 2 ? x : q, key.slot);
-          commit(at(ms.s_full, sb));
-          if (last_x) commit(at(ms.kv_empty, key.slot));
-          if (last_q) commit(at(ms.q_empty, ring_q.slot));
+          for (int x = 0; x < tiles; ++x) {
+            qk(x, x, ring_k.slot);
+            commit(at(ms.s_full, x));
+          }
+          commit(at(ms.kv_empty, ring_k.slot));
+          if (p.t0 + 1 == p.t1) commit(at(ms.q_empty, 0));
         }
         __syncwarp();
-        ++used[sb];
-        if (last_q) ring_q.next(3 - NT);
-      };
-      bool ok = true;
-      if (NT == 1) {
-        // S of the next tile before the product of this one, unless a new item's keys are still on their way
+        ring_k.next(kRing, 2);
+        for (int x = 0; x < tiles && ok; ++x) {  // the output buffers (and their poison marks) are free
+          ok = warp_wait(at(ms.o_empty, x), o_phase[x], abort);
+          o_phase[x] ^= 1;
+        }
+        for (int t = p.t0; ok && t < p.t1; ++t, g.base += kTile) {
+          const bool more = t + 1 < p.t1, first = t == p.t0, whole = g.whole();
+          ok = take_values(ring_v, g, 0, 1);
+          if (ok && more) ok = warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x == tiles || !ok) break;
+            ok = warp_wait(at(ms.p_full, 2 * x + 1), p_phase[x], abort);
+            p_phase[x] ^= 1;
+            if (!ok) break;
+            fence_after();
+            if (elect()) {
+              if (whole) pv_run(x, x, ring_v.slot, 0, first, std::integral_constant<int, kTile / 16>());
+              else pv_steps(x, x, ring_v.slot, first, g.first_step(), g.end_step());
+              if (more) {
+                qk(x, x, ring_k.slot);
+                commit(at(ms.s_full, x));
+              } else {
+                commit(at(ms.o_full, x));
+              }
+              if (x == tiles - 1) {
+                commit(at(ms.kv_empty, ring_v.slot));
+                if (more) commit(at(ms.kv_empty, ring_k.slot));
+                if (t + 2 == p.t1) commit(at(ms.q_empty, 0));
+              }
+            }
+            __syncwarp();
+          }
+          ring_v.next(kRing, 2);
+          if (more) ring_k.next(kRing, 2);
+        }
+        ring_q.next(1);
+      }
+    } else {
+      // Tile by tile over the pieces: S of the next tile before the product of this one, unless a new item's keys
+      // are still on their way.
+      int used[2] = {0, 0};   // S / P buffer uses so far
+      int items[2] = {0, 0};  // output buffer uses so far
+      int ob = 1, tile_no = 0;
+      Span prev = {0, 0, 0, 0};
+      int prev_ob = 0, prev_sb = 0;
+      bool have_prev = false, prev_first = false, prev_last = false, ok = true;
+      Piece p;
+      p.t0 = p.t1 = p.kind = 0;
+      int t = 0;
+      while (ok) {
+        while (t == p.t1 && p.kind == 0 && ok) {
+          ok = next_piece(p);
+          t = p.t0;
+        }
+        if (!ok) break;
+        const bool more = p.kind == 0, first = t == p.t0, last = t == p.t1 - 1;
         const int sb = tile_no & 1;
-        const bool early = more && (!first || __all_sync(0xffffffffu, bar_try(at(ms.kv_full, key.slot), key.phase) &&
-                                                                          bar_try(at(ms.q_full, ring_q.slot), ring_q.phase)));
-        if (early) {
-          ok = begin_tile();
-          if (ok) qk_tile(0);
-        }
+        auto qk_tile = [&]() {
+          if (!warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort)) return false;
+          if (first) {
+            if (!warp_wait(at(ms.q_full, ring_q.slot), ring_q.phase, abort)) return false;
+            ob ^= 1;
+          }
+          fence_after();
+          if (elect()) {
+            qk(sb, ring_q.slot, ring_k.slot);
+            commit(at(ms.s_full, sb));
+            commit(at(ms.kv_empty, ring_k.slot));
+            if (last) commit(at(ms.q_empty, ring_q.slot));
+          }
+          __syncwarp();
+          ++used[sb];
+          ring_k.next(kRing, 2);
+          if (last) ring_q.next(2);
+          return true;
+        };
+        const bool early = more && (!first || __all_sync(0xffffffffu, bar_test(at(ms.kv_full, ring_k.slot), ring_k.phase) &&
+                                                                          bar_test(at(ms.q_full, ring_q.slot), ring_q.phase)));
+        if (early) ok = qk_tile();
         if (ok && have_prev) {
-          // qk_tile counts a use of the other buffer, so prev's parity is its own
-          ok = take_values(value.slot, value.phase) && pv_tile(0, value.slot, true);
+          // the output buffer (and its poison mark) is free; the weights come in two halves (qk_tile counted a use
+          // of the other buffer, so prev's parity is its own)
+          if (prev_first) ok = warp_wait(at(ms.o_empty, prev_ob), (items[prev_ob] & 1) ^ 1, abort);
+          ok = ok && take_values(ring_v, prev, prev_ob, prev_ob);
+          const uint32_t p_phase = (used[prev_sb] & 1) ^ 1;
+          const bool whole = prev.whole();
+          if (!ok || !warp_wait(at(ms.p_full, 2 * prev_sb), p_phase, abort)) break;
+          fence_after();
+          if (whole && elect()) pv_run(prev_ob, prev_sb, ring_v.slot, 0, prev_first, std::integral_constant<int, 4>());
+          __syncwarp();
+          if (!warp_wait(at(ms.p_full, 2 * prev_sb + 1), p_phase, abort)) break;
+          fence_after();
+          if (elect()) {
+            if (whole) pv_run(prev_ob, prev_sb, ring_v.slot, 4, false, std::integral_constant<int, 4>());
+            else pv_steps(prev_ob, prev_sb, ring_v.slot, prev_first, prev.first_step(), prev.end_step());
+            commit(at(ms.pv_done, prev_sb));
+            commit(at(ms.kv_empty, ring_v.slot));
+            if (prev_last) commit(at(ms.o_full, prev_ob));
+          }
+          __syncwarp();
+          if (prev_last) ++items[prev_ob];
+          ring_v.next(kRing, 2);
         }
-        if (ok && more && !early) {
-          ok = begin_tile();
-          if (ok) qk_tile(0);
-        }
+        if (ok && more && !early) ok = qk_tile();
+        if (!more) break;
+        prev = Span{t * kTile, p.pos0, p.kv_lo, p.pos0 + p.ntok};
         prev_sb = sb;
-        if (more) ++tile_no;
-      } else if (first || !more) {
-        // the item before is finished first: the new one's queries wait for it
-        if (have_prev) {
-          ok = take_values(value.slot, value.phase);
-          for (int x = 0; x < prev_tiles && ok; ++x) ok = pv_tile(x, value.slot, x == prev_tiles - 1);
-        }
-        if (ok && more) {
-          ok = begin_tile();
-          for (int x = 0; x < tiles && ok; ++x) qk_tile(x);
-        }
-      } else {
-        ok = take_values(value.slot, value.phase);
-        for (int x = 0; x < tiles && ok; ++x) {
-          ok = pv_tile(x, value.slot, x == tiles - 1) && (x > 0 || begin_tile());
-          if (ok) qk_tile(x);
-        }
+        prev_ob = ob;
+        prev_first = first;
+        prev_last = last;
+        have_prev = true;
+        ++tile_no;
+        ++t;
       }
-      if (!ok) break;
-      if (!more) break;
-      if (first) {
-        prev_pos0 = p.pos0;
-        prev_ntok = p.ntok;
-        prev_lo = p.kv_lo;
-      }
-      prev_tile = t;
-      prev_tiles = tiles;
-      prev_ob = cur_ob;
-      prev_first = t == p.t0;
-      prev_last = t == p.t1 - 1;
-      have_prev = true;
-      ++t;
     }
   } else {
     // ---- softmax: thread = row
@@ -901,12 +908,12 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
             tmem_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(at(ms.p_full, 2 * sb + half));
+            if (lane == 0 && (NT == 1 || half == 1)) bar_arrive(at(ms.p_full, 2 * sb + half));
           }
           const float2 both = fadd2(part[0], part[1]);
           sum += both.x + both.y;
         } else if (lane == 0) {
-          bar_arrive(at(ms.p_full, 2 * sb));
+          if (NT == 1) bar_arrive(at(ms.p_full, 2 * sb));
           bar_arrive(at(ms.p_full, 2 * sb + 1));
         }
         ++used;

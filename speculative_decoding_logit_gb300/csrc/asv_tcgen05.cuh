@@ -36,6 +36,19 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without the wait that the hardware may put into a try.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -60,13 +73,17 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (bar_try(bar, parity)) return true;
-  if (bar_try(bar, parity)) return true;
   return bar_wait_slow(bar, parity, abort);
 }
 
 // The same by a whole warp, one answer for every lane.
+__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, bar_wait_slow(bar, parity, abort));
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+  if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+  return warp_wait_slow(bar, parity, abort);
 }
 
 __device__ __forceinline__ void fence_barrier_init() {
