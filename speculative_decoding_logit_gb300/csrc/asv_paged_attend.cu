@@ -664,10 +664,15 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           ok = warp_wait(at(ms.o_empty, x), o_phase[x], abort);
           o_phase[x] ^= 1;
         }
-        for (int t = p.t0; ok && t < p.t1; ++t, g.base += kTile) {
-          const bool more = t + 1 < p.t1, first = t == p.t0, whole = g.whole();
-          ok = take_values(ring_v, g, 0, 1);
-          if (ok && more) ok = warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort);
+        // What a tile's instructions need is waited for behind the ones before (a wait that is over takes about a
+        // hundred cycles, the pipe holds three instructions): the values after the first row tile's, the keys after
+        // the last's.
+        auto keys_there = [&]() { return warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort); };
+        ok = ok && take_values(ring_v, g, 0, 1) && (p.t0 + 1 == p.t1 || keys_there());
+        Ring next_v = ring_v;
+        Span next_g = g;
+        for (int left = p.t1 - p.t0, first = 1; left > 0 && ok; --left, first = 0) {
+          const bool more = left > 1, whole = g.whole();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (x == tiles || !ok) break;
@@ -687,13 +692,22 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
               if (x == tiles - 1) {
                 commit(at(ms.kv_empty, ring_v.slot));
                 if (more) commit(at(ms.kv_empty, ring_k.slot));
-                if (t + 2 == p.t1) commit(at(ms.q_empty, 0));
+                if (left == 2) commit(at(ms.q_empty, 0));
               }
             }
             __syncwarp();
+            if (x == 0) {
+              next_v = ring_v;
+              next_v.next(kRing, 2);
+              next_g = g;
+              next_g.base += kTile;
+              if (more) ok = take_values(next_v, next_g, 0, 1);
+            }
           }
-          ring_v.next(kRing, 2);
+          ring_v = next_v;
+          g = next_g;
           if (more) ring_k.next(kRing, 2);
+          if (ok && left > 2) ok = keys_there();
         }
         ring_q.next(1);
       }
@@ -853,10 +867,11 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           for (int half = 0; half < 2; ++half) {
             uint32_t s[64];
             load_s(half, s);
-            float m[2] = {top, __uint_as_float(s[63])};
+            float m[4] = {top, __uint_as_float(s[61]), __uint_as_float(s[62]), __uint_as_float(s[63])};
 #pragma unroll
-            for (int j = 0; j < 62; j += 2) m[(j / 2) & 1] = max3(m[(j / 2) & 1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            top = max3(m[0], m[1], __uint_as_float(s[62]));
+            for (int j = 0; j < 60; j += 2)
+              m[(j / 2) & 3] = max3(m[(j / 2) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            top = fmaxf(max3(m[0], m[1], __uint_as_float(s[60])), fmaxf(m[2], m[3]));
           }
           top *= scale2;
           const bool move = top > ref + kLazy;
@@ -905,10 +920,12 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
               w[j] = pack2<BF16>(x.x, x.y);
             }
             tmem_st32(s_addr + half * 32, w);
-            tmem_wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0 && (NT == 1 || half == 1)) bar_arrive(at(ms.p_full, 2 * sb + half));
+            if (NT == 1 || half == 1) {
+              tmem_wait_st();
+              fence_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(at(ms.p_full, 2 * sb + half));
+            }
           }
           const float2 both = fadd2(part[0], part[1]);
           sum += both.x + both.y;
