@@ -67,20 +67,6 @@ struct Piece {
   int kind;        // 0: a piece; 1: the end of the run
 };
 
-struct Misc {
-  uint64_t kv_full[10], kv_empty[10];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[4], pv_done[2], o_full[2], o_empty[2];
-  uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
-  Piece piece[kQueue];
-  long long warp_sum[12];
-  long long start_item0;  // the run's first item: units before it, request, place, key tiles, head
-  int start_request, start_i, start_n, start_h;
-  uint32_t tmem;
-  int abort;
-  int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
-  int last[2][2];
-};
-
 // a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
@@ -165,6 +151,26 @@ __device__ Items load_items(const PagedView& c, int b, int T) {
   it.n = rows ? (it.r.end - it.r.start + T - 1) / T : 0;
   return it;
 }
+
+// The item that a run starts in: units before it, its request, its place among the request's, head and key tiles.
+struct Start {
+  long long item0;
+  Items it;
+  int request, i, h, n;
+};
+
+struct Misc {
+  uint64_t kv_full[10], kv_empty[10];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[4], pv_done[2], o_full[2], o_empty[2];
+  uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
+  Piece piece[kQueue];
+  long long warp_sum[12];
+  Start start;
+  uint32_t tmem;
+  int abort;
+  int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
+  int last[2][2];
+};
 
 // Counters of a ring of `n` barriers: slot and phase of the i-th use.
 struct Ring {
@@ -361,8 +367,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
   const int per_thread = (c.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per_thread, c.B), b1 = min(b0 + per_thread, c.B);
   long long own = 0;
+  Items it;
   for (int b = b0; b < b1; ++b) {
-    const Items it = load_items(c, b, T);
+    it = load_items(c, b, T);
     if (!it.r.ok && blockIdx.x == 0) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
     own += it.units(a.window, kCost, c.kv_heads);
   }
@@ -385,8 +392,8 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
   if (u0 >= before && u0 < before + own) {
     long long x = before;
     for (int b = b0; b < b1; ++b) {
-      const Items it = load_items(c, b, T);
-      const long long n = it.units(a.window, kCost, c.kv_heads);
+      if (per_thread > 1) it = load_items(c, b, T);
+      const long long n = per_thread > 1 ? it.units(a.window, kCost, c.kv_heads) : own;
       if (u0 < x + n) {
         const long long rel = u0 - x;
         int i = 0;  // the item that holds unit u0: the last with no more than rel units before it
@@ -398,11 +405,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         const int tiles = it.tiles(a.window, i);
         const long long item = x + c.kv_heads * it.before(a.window, kCost, i);
         const int h = int(quotient(u0 - item, tiles + kCost));
-        ms.start_request = b;
-        ms.start_i = i;
-        ms.start_n = tiles;
-        ms.start_h = h;
-        ms.start_item0 = item + (long long)h * (tiles + kCost);
+        ms.start = Start{item + (long long)h * (tiles + kCost), it, b, i, h, tiles};
         break;
       }
       x += n;
@@ -418,9 +421,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
   } else if (warp == kWalkWarp) {
     // ---- scheduler
     if (lane == 0) {
-      int b = ms.start_request, i = ms.start_i, n = ms.start_n, h = ms.start_h;
-      long long item0 = ms.start_item0;
-      Items it = load_items(c, b, T);
+      int b = ms.start.request, i = ms.start.i, n = ms.start.n, h = ms.start.h;
+      long long item0 = ms.start.item0;
+      Items it = ms.start.it;
       Ring ring_p;
       for (bool end = false; !end;) {
         // its first kCost units are its own, then one for each key tile
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     };
     Window w, ahead;
     ahead.n = 0;
-    bool run = true;
+    bool run = true, begun = false;
     while (run) {
       if (ahead.n == 0 && (!next_window(true, ahead) || ahead.n == 0)) break;
       w = ahead;
@@ -558,8 +561,11 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       const int page = ok ? w.entry : c.num_pages;
       next_window(false, ahead);
       for (int i = 0; i < w.n && run; ++i) {
-        run = copy_tile(w.head, i, page, w.slot);
-        if (i == 0 && w.first && !values) run = run && copy_queries(w);
+        // an item's queries after its first keys, which need not wait for the item before (the run's first: before)
+        if (!begun && !values) run = copy_queries(w);
+        run = run && copy_tile(w.head, i, page, w.slot);
+        if (i == 0 && w.first && begun && !values) run = run && copy_queries(w);
+        begun = true;
       }
     }
     if (*abort) {  // leave with no copy in flight: the slots still being written, for a while
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         // hundred cycles, the pipe holds three instructions): the values after the first row tile's, the keys after
         // the last's.
         auto keys_there = [&]() { return warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort); };
-        ok = ok && take_values(ring_v, g, 0, 1) && (p.t0 + 1 == p.t1 || keys_there());
+        ok = ok && take_values(ring_v, g, 0, tiles - 1) && (p.t0 + 1 == p.t1 || keys_there());
         Ring next_v = ring_v;
         Span next_g = g;
         for (int left = p.t1 - p.t0, first = 1; left > 0 && ok; --left, first = 0) {
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
               next_v.next(kRing, 2);
               next_g = g;
               next_g.base += kTile;
-              if (more) ok = take_values(next_v, next_g, 0, 1);
+              if (more) ok = take_values(next_v, next_g, 0, tiles - 1);
             }
           }
           ring_v = next_v;
@@ -966,32 +972,36 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         const bool store = valid && ASV_GUARD(a, tok_row >= 0 && tok_row < c.N && head < a.q_heads);
         uint16_t* out = a.out.p + tok_row * a.out.tok + head * a.out.head;
         if (any) {
+          constexpr int kCols = NT == 1 ? 32 : 64;
 #pragma unroll 1
-          for (int i = 0; i < DP / 64; ++i) {
+          for (int i = 0; i < DP; i += kCols) {
             __syncwarp();
-            uint32_t o[64];
+            float y[kCols];
             if (p.t1 > p.t0) {
-              tmem_ld32(o_addr + i * 64, reinterpret_cast<uint32_t(&)[32]>(o[0]));
-              tmem_ld32(o_addr + i * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(o[32]));
+              uint32_t o[kCols];
+#pragma unroll
+              for (int j = 0; j < kCols; j += 32) tmem_ld32(o_addr + i + j, reinterpret_cast<uint32_t(&)[32]>(o[j]));
               tmem_wait_ld(o);
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) y[j] = __uint_as_float(o[j]) * inv;
+            } else {
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) y[j] = 0.0f;
             }
-            float y[64];
+            if (poison) poisoned(y, i);
+            uint32_t v[kCols / 2];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) y[j] = p.t1 > p.t0 ? __uint_as_float(o[j]) * inv : 0.0f;
-            if (poison) poisoned(y, i * 64);
-            uint32_t v[32];
+            for (int j = 0; j < kCols / 2; ++j) v[j] = pack2<BF16>(y[2 * j], y[2 * j + 1]);
+            if constexpr (NT == 1) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = pack2<BF16>(y[2 * j], y[2 * j + 1]);
-            if (NT == 1) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (store && i * 64 + j * 8 < c.head_dim)
-                  *reinterpret_cast<uint4*>(out + i * 64 + j * 8) =
+              for (int j = 0; j < kCols / 8; ++j)
+                if (store && i + j * 8 < c.head_dim)
+                  *reinterpret_cast<uint4*>(out + i + j * 8) =
                       make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             } else {
               // full tiles: a lane's own row to 16 bytes of 32 lines a store took 512 cycles of the L1 each
               transpose8(v, lane);
-              const int d = i * 64 + (lane & 7) * 8;
+              const int d = i + (lane & 7) * 8;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const unsigned long long to = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), (lane & ~7) + j);

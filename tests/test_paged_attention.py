@@ -144,6 +144,51 @@ def test_nan_where_no_token_looks(asv):
             assert_within(got.out[other], want[0][other], want[2][other], "the other request")
 
 
+@pytest.mark.parametrize("heads,q_lens", [((4, 1), [300, 20, 150]), ((2, 2), [260, 257, 5, 390])])
+def test_nan_in_later_tokens_of_long_chunks(asv, heads, q_lens):
+    """The last third of every chunk holds NaN keys and values: the tokens before it are left alone, whichever
+    row tiles and items they share with it, and every one from there on is NaN."""
+    b = Batch(q_lens, [70, 0, 200, 11][:len(q_lens)], heads=heads, dim=64, page=32, seed=21).fill()
+    want = attention64(b)
+    clean, bad = [], []
+    for r, (a, n) in enumerate(zip(b.past, b.q_lens)):
+        cut = n - n // 3
+        for j in range(a + cut, a + n):
+            for c in (b.k_cache, b.v_cache):
+                c[b.rows[r][j // 32], j % 32] = math.nan
+        clean += range(b.starts[r], b.starts[r] + cut)
+        bad += range(b.starts[r] + cut, b.starts[r] + n)
+    got = _run(asv, b)
+    assert not got.req_status.any()
+    assert_within(got.out[clean], want[0][clean], want[2][clean], "out")
+    assert_within(got.lse[clean], want[1][clean], want[3][clean], "lse")
+    assert bool(got.out[bad].isnan().all())
+
+
+def test_infinite_values_stay_with_their_rows_and_columns(asv):
+    """Infinities of both signs among the values of a chunk's own tokens: a row that sees one of a column is
+    infinite there, NaN where it sees both signs, and the others are left alone."""
+    b = Batch([90], [140], heads=(2, 1), dim=64, seed=22)
+    b.v[0][150, 0, 3] = math.inf
+    b.v[0][171, 0, 3] = -math.inf
+    b.v[0][171, 0, 9] = -math.inf
+    b.fill()
+    keep = b.v[0].clone()
+    b.v[0] = torch.where(keep.isinf(), 0, keep)
+    want = attention64(b)
+    got = _run(asv, b)
+    pos = torch.arange(140, 230)[:, None]
+    col = torch.arange(64)[None]
+    plus, minus = (col == 3) & (pos >= 150), ((col == 3) | (col == 9)) & (pos >= 171)
+    out = got.out.float().cpu()
+    for h in range(2):
+        o = out[:, h]
+        assert torch.equal(o.isnan(), plus & minus)
+        assert torch.equal(o == math.inf, plus & ~minus) and torch.equal(o == -math.inf, minus & ~plus)
+        ok = ~(plus | minus)
+        assert bool(((o.double() - want[0][:, h]).abs() <= want[2][:, h])[ok].all())
+
+
 def test_nan_among_the_keys_reaches_its_rows(asv):
     b = Batch([4], [100], heads=(2, 2), dim=64, seed=14).fill()
     b.v_cache[b.rows[0][102 // 16], 102 % 16, 1, 5] = math.nan
