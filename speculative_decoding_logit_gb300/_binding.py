@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import struct
 import threading
@@ -612,19 +613,20 @@ def _packed_rows(x: torch.Tensor, name: str, shape, dtype) -> bytes:
         raise AsvError(4, f"{name} must have the cache's type {dtype}, got {x.dtype}")
     if not x.is_cuda:
         _need_cuda(x)
-    s = x.stride()
-    if s[2] != 1 and x.numel():
+    token, head, one = x.stride()
+    if one != 1 and x.numel():
         raise AsvError(3, f"the last dimension of {name} must be contiguous")
-    return _pack_rows(x.data_ptr(), s[0], s[1])
+    return _pack_rows(x.data_ptr(), token, head)
 
 
-def _check_status(req_status: torch.Tensor, B: int):
+def _status_ptr(req_status: torch.Tensor, B: int) -> int:
     if req_status.dtype != torch.int32 or req_status.shape != (B,):
         raise AsvError(2, "req_status must be int32 [B]")
     if not req_status.is_cuda:
         _need_cuda(req_status)
     if B > 1 and req_status.stride(0) != 1:
         raise AsvError(2, "req_status must be contiguous")
+    return req_status.data_ptr()
 
 
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -657,8 +659,7 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         dev = k_cache.device
         out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=dtype, device=dev),
                                 torch.zeros(B, dtype=torch.int32, device=dev))
-    status = out.req_status
-    _check_status(status, B)
+    status = _status_ptr(out.req_status, B)
     qr = oq = None
     q_heads = 0
     if q is not None:
@@ -669,8 +670,8 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         q_heads = q.shape[1]
         q_shape = (N, q_heads, cs[3])
         qr, oq = _packed_rows(q, "q", q_shape, dtype), _packed_rows(out.q, "out.q", q_shape, dtype)
-    st = library().paged_kv_append(cache, batch, kr, vr, qr, oq, q_heads, rc, status.data_ptr(),
-                                   _raw_stream(k_cache, stream))
+    st = (_lib or library()).paged_kv_append(cache, batch, kr, vr, qr, oq, q_heads, rc, status,
+                                             _raw_stream(k_cache, stream))
     if st:
         _check(st, "paged_kv_append")
     return out
@@ -687,7 +688,9 @@ def _raw_stream(t: torch.Tensor, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
+@functools.lru_cache(maxsize=64)
 def paged_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace one paged_attention call with these heads needs, for any batch."""
     return int(library().asv_paged_workspace_bytes(q_heads, kv_heads, head_dim))
 
 
@@ -722,8 +725,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                                    torch.empty(N, Hq, dtype=torch.float32, device=dev),
                                    torch.zeros(B, dtype=torch.int32, device=dev))
     rows = _packed_rows(out.out, "out.out", shape, dtype)
-    status, lse = out.req_status, out.lse
-    _check_status(status, B)
+    status, lse = _status_ptr(out.req_status, B), out.lse
     if lse is not None:
         if lse.dtype != torch.float32 or lse.shape != (N, Hq):
             raise AsvError(2, "out.lse must be float32 [N, q_heads]")
@@ -731,13 +733,13 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             _need_cuda(lse)
         _contig(lse, "out.lse")
         lse = lse.data_ptr()
-    L = library()
+    L = _lib or library()
     handle = _raw_stream(q, stream)
     if workspace is None:
-        workspace = _paged_workspace(q, handle, stream, L.asv_paged_workspace_bytes(Hq, cs[2], D))
+        workspace = _paged_workspace(q, handle, stream, paged_workspace_bytes(Hq, cs[2], D))
     try:
         st = L.paged_attention(cache, batch, qr, rows, Hq, D ** -0.5 if scale is None else scale, window, lse,
-                               status.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle)
+                               status, workspace.data_ptr(), workspace.nbytes, handle)
     except (C.ArgumentError, TypeError) as e:
         raise AsvError(5, f"scale must be a number and window a 32-bit whole number ({e})") from None
     if st:

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     while (b < c.B && c.indptr[b + 1] <= token) ++b;
     if (token < c.N && b < c.B) {
       const Request r = load_request(c, b, limit);
-      if (r.ok && token >= r.start && token < r.end) {
+      if (r.ok && token >= r.start && token < r.end && ASV_GUARD(a, token < c.N)) {
         p.request = b;
         p.pos = r.past + (token - r.start);
         const int entry = p.pos / c.page_size;

@@ -513,7 +513,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       w.need = group < w.n && pos < p.pos0 + p.ntok && pos + a.box > p.kv_lo;
       const int page = pos / c.page_size;
       w.slot = pos - page * c.page_size;
-      w.entry = w.need ? c.table[p.request * c.table_stride + page] : -1;
+      w.entry = w.need && ASV_GUARD(a, page >= 0 && page < c.max_pages && p.request < c.B)
+                    ? c.table[p.request * c.table_stride + page]
+                    : -1;
       t += w.n;
       return true;
     };
@@ -1029,14 +1031,15 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]);
             if (poison) poisoned(y, i * 32);
-            if (valid) {
+            if (valid && ASV_GUARD(a, p.part < kPagedSlots)) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 __stcg(reinterpret_cast<float4*>(part) + (i * 8 + j) * kTile + row,
                        make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]));
             }
           }
-          if (valid) __stcg(reinterpret_cast<float2*>(part + kTile * DP) + row, make_float2(ref, sum));
+          if (valid && ASV_GUARD(a, p.part < kPagedSlots))
+            __stcg(reinterpret_cast<float2*>(part + kTile * DP) + row, make_float2(ref, sum));
         }
       }
       if (p.t1 > p.t0) {
@@ -1055,7 +1058,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       // The last to file joins the parts, in CTA order.  The warps' writes come before the ticket through the
       // barrier and the ticket's release, the other CTAs' before the reads through its acquire and the barrier.
       if (!wg_sync()) break;
-      if (row == 0) {
+      if (row == 0 && ASV_GUARD(a, p.first_cta + p.n_parts <= int(gridDim.x))) {
         const uint32_t old = atom_add_acq_rel_gpu(a.tickets + 2 * p.first_cta + wg, 1u);
         ms.last[wg][sync_phase] = old == uint32_t(p.n_parts - 1);
       }
