@@ -61,8 +61,9 @@ extern "C" {
 typedef enum {
   ASV_OK = 0,
   ASV_ERR_NULL = 1,      /* a required pointer is NULL */
-  ASV_ERR_SHAPE = 2,     /* B < 0, K < 0 (K < 1 for SCI), V < 2, or V too large for one cluster */
-  ASV_ERR_ALIGN = 3,     /* a pointer is not aligned to its element size */
+  ASV_ERR_SHAPE = 2,     /* B < 0, K < 0 (K < 1 for SCI), V < 2, or V too large for one cluster;
+                            a size of the paged cache, its batch or heads out of range */
+  ASV_ERR_ALIGN = 3,     /* a pointer (a stride of the paged cache or its rows) is not aligned */
   ASV_ERR_DTYPE = 4,     /* unknown element type, or a type the mode does not take */
   ASV_ERR_PARAM = 5,     /* a scalar parameter is non-finite or out of range */
   ASV_ERR_WORKSPACE = 6, /* workspace NULL or smaller than asv_workspace_bytes() */
@@ -480,7 +481,7 @@ asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* 
  * rounded to the cache's type for the product with v (their sum is not), and out is rounded once.
  * What a slot outside every attended position holds (a page's unwritten tail, an evicted page's entry)
  * does not matter, NaN included.
- * q_heads is a multiple of kv_heads, at most 128 to one key head; scale is finite and > 0; window >= 0
+ * out must not overlap q or the cache.  q_heads is a multiple of kv_heads, at most 128 to one key head; scale is finite and > 0; window >= 0
  * (0: none).  out_lse [N, q_heads] may be NULL.
  * workspace: asv_paged_workspace_bytes(...) bytes, 256-byte aligned, its first ASV_PAGED_WORKSPACE_ZEROED
  * bytes zero-filled before its first use (asv_workspace_init); every call leaves them zero.  Calls that may run at the same time

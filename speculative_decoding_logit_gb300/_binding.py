@@ -2,9 +2,9 @@
 from __future__ import annotations
 
 import ctypes as C
-import functools
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -102,14 +102,6 @@ class _RowsC(C.Structure):
 
 class _RotaryC(C.Structure):
     _fields_ = [("table", C.c_void_p), ("dim", C.c_int), ("max_position", C.c_int), ("interleaved", C.c_int)]
-
-
-# The same layouts packed from Python values: a structure's constructor takes several microseconds, and
-# the paged calls are made for every layer of every step.
-_pack_cache = struct.Struct("@QQiiiii4xqqqqqq").pack
-_pack_batch = struct.Struct("@iiQQQi4xq").pack
-_pack_rows = struct.Struct("@Qqq").pack
-_pack_rotary = struct.Struct("@Qiii4x").pack
 
 
 def _declare(L):
@@ -571,62 +563,33 @@ class PagedAttentionOutput:
     req_status: torch.Tensor     # [B] int32 (ASV_REQ_* bits, ORed in)
 
 
-_CACHE_TYPES = {torch.bfloat16: ASV_BF16, torch.float16: ASV_F16}
+_ext = None
 
 
-def _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N):
-    """Checks the cache and the batch; returns their packed forms, B, the caches' type and shape."""
-    if not (k_cache.is_cuda and v_cache.is_cuda and block_table.is_cuda and cache_len.is_cuda and indptr.is_cuda):
-        _need_cuda(k_cache, v_cache, block_table, cache_len, indptr)
-    shape = k_cache.shape
-    if len(shape) != 4 or shape != v_cache.shape:
-        raise AsvError(2, "k_cache and v_cache must share one [num_pages, page_size, kv_heads, head_dim] shape")
-    dtype = k_cache.dtype
-    code = _CACHE_TYPES.get(dtype)
-    if code is None or v_cache.dtype != dtype:
-        raise AsvError(4, f"the caches must share bfloat16 or float16, got {dtype} and {v_cache.dtype}")
-    i32 = torch.int32
-    if block_table.dtype != i32 or cache_len.dtype != i32 or indptr.dtype != i32:
-        raise AsvError(4, "block_table, cache_len and indptr must be int32")
-    table = block_table.shape
-    if len(table) != 2 or cache_len.shape != table[:1] or indptr.shape != (table[0] + 1,):
-        raise AsvError(2, "block_table must be [B, max_pages], cache_len [B], indptr [B + 1]")
-    B, width = table
-    if B > 1 and cache_len.stride(0) != 1 or indptr.shape[0] > 1 and indptr.stride(0) != 1:
-        raise AsvError(2, "cache_len and indptr must be contiguous")
-    ks, vs, ts = k_cache.stride(), v_cache.stride(), block_table.stride()
-    if (shape[3] > 1 and (ks[3] != 1 or vs[3] != 1)) or (width > 1 and ts[1] != 1):
-        raise AsvError(3, "the last dimension of k_cache, v_cache and block_table must be contiguous")
-    try:
-        cache = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), code, *shape, *ks[:3], *vs[:3])
-        batch = _pack_batch(B, N, indptr.data_ptr(), cache_len.data_ptr(), block_table.data_ptr(), width, ts[0])
-    except struct.error as e:
-        raise AsvError(2, f"an extent does not fit 32 bits ({e})") from None
-    return cache, batch, B, dtype, shape
+def _paged_ext():
+    """The binding's compiled module, bound to the library's paged entry points."""
+    global _ext
+    L = library()
+    with _lib_lock:
+        if _ext is None:
+            if not os.path.exists(_build.TORCH_EXT):
+                raise AsvError(-1, f"asv_torch.so not built ({_build.TORCH_EXT}); call speculative_decoding_logit_gb300.build()")
+            loader = importlib.machinery.ExtensionFileLoader("asv_torch", _build.TORCH_EXT)
+            ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("asv_torch", loader))
+            loader.exec_module(ext)
+            ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append,
+                                                                        L.asv_status_string, L.asv_last_cuda_error)))
+            _ext = ext
+    return _ext
 
 
-def _packed_rows(x: torch.Tensor, name: str, shape, dtype) -> bytes:
-    """Packed form of q, k, v or out, [N, heads, head_dim] of the cache's type."""
-    if x.shape != shape:
-        raise AsvError(2, f"{name} must be {tuple(shape)}, got {tuple(x.shape)}")
-    if x.dtype != dtype:
-        raise AsvError(4, f"{name} must have the cache's type {dtype}, got {x.dtype}")
-    if not x.is_cuda:
-        _need_cuda(x)
-    token, head, one = x.stride()
-    if one != 1 and x.numel():
-        raise AsvError(3, f"the last dimension of {name} must be contiguous")
-    return _pack_rows(x.data_ptr(), token, head)
-
-
-def _status_ptr(req_status: torch.Tensor, B: int) -> int:
-    if req_status.dtype != torch.int32 or req_status.shape != (B,):
-        raise AsvError(2, "req_status must be int32 [B]")
-    if not req_status.is_cuda:
-        _need_cuda(req_status)
-    if B > 1 and req_status.stride(0) != 1:
-        raise AsvError(2, "req_status must be contiguous")
-    return req_status.data_ptr()
+def _raw_stream(t: torch.Tensor, stream) -> int:
+    """The CUDA stream handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not t.is_cuda:
+        _need_cuda(t)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -639,41 +602,13 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     ([max_position, dim] float32: cos of the dim/2 angles of each position, then their sines) the keys
     are rotated on the way, and the queries `q` into out.q (paged_kv_append in include/asv.h).
     cache_len is not advanced.  The caches take any strides with head rows contiguous."""
-    shape = k.shape
-    if len(shape) != 3:
-        raise AsvError(2, "k and v must be [N, kv_heads, head_dim]")
-    N = shape[0]
-    cache, batch, B, dtype, cs = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
-    kv_shape = (N, cs[2], cs[3])
-    kr, vr = _packed_rows(k, "k", kv_shape, dtype), _packed_rows(v, "v", kv_shape, dtype)
-    rc = None
-    if rotary is not None:
-        if rotary.dim() != 2 or rotary.dtype != torch.float32:
-            raise AsvError(2, "rotary must be a float32 [max_position, dim] table")
-        if not rotary.is_cuda:
-            _need_cuda(rotary)
-        _contig(rotary, "rotary")
-        positions, dim = rotary.shape
-        rc = _pack_rotary(rotary.data_ptr(), dim, min(positions, 0x7fffffff), 1 if interleaved else 0)
+    handle = _raw_stream(k, stream)
     if out is None:
-        dev = k_cache.device
-        out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=dtype, device=dev),
-                                torch.zeros(B, dtype=torch.int32, device=dev))
-    status = _status_ptr(out.req_status, B)
-    qr = oq = None
-    q_heads = 0
-    if q is not None:
-        if out.q is None:
-            raise AsvError(1, "out.q is missing")
-        if q.dim() != 3:
-            raise AsvError(2, "q must be [N, q_heads, head_dim]")
-        q_heads = q.shape[1]
-        q_shape = (N, q_heads, cs[3])
-        qr, oq = _packed_rows(q, "q", q_shape, dtype), _packed_rows(out.q, "out.q", q_shape, dtype)
-    st = (_lib or library()).paged_kv_append(cache, batch, kr, vr, qr, oq, q_heads, rc, status,
-                                             _raw_stream(k_cache, stream))
-    if st:
-        _check(st, "paged_kv_append")
+        dev = k.device
+        out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
+                                torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))
+    (_ext or _paged_ext()).paged_kv_append(k, v, k_cache, v_cache, block_table, cache_len, indptr, q, rotary,
+                                           interleaved, out.q, out.req_status, handle)
     return out
 
 
@@ -683,25 +618,19 @@ _paged_ws_cache: dict = {}
 PAGED_WORKSPACE_ZEROED = 4096
 
 
-def _raw_stream(t: torch.Tensor, stream) -> int:
-    """The CUDA stream handle of `stream`, or of the current stream of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
-
-
-@functools.lru_cache(maxsize=64)
 def paged_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
     """Bytes of workspace one paged_attention call with these heads needs, for any batch."""
     return int(library().asv_paged_workspace_bytes(q_heads, kv_heads, head_dim))
 
 
-def _paged_workspace(q: torch.Tensor, handle: int, stream, nbytes: int) -> torch.Tensor:
-    key = (q.get_device(), handle)
-    ws = _paged_ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with _ws_lock, torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(q.device)):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-            ws[:PAGED_WORKSPACE_ZEROED].zero_()
-            _paged_ws_cache[key] = ws
+def _paged_workspace(q: torch.Tensor, handle: int, stream) -> torch.Tensor:
+    """A new workspace for any heads, kept for the stream's later calls unless it is capturing (what is
+    allocated then belongs to the graph, and is zeroed by its replays only)."""
+    with _ws_lock, torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(q.device)):
+        ws = torch.empty(paged_workspace_bytes(1, 1, 128), dtype=torch.uint8, device=q.device)
+        ws[:PAGED_WORKSPACE_ZEROED].zero_()
+        if not torch.cuda.is_current_stream_capturing():
+            _paged_ws_cache[q.get_device(), handle] = ws
     return ws
 
 
@@ -713,35 +642,16 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     chunk's own tokens (appended before, see paged_kv_append) included: causal, grouped heads, with
     `window` > 0 only the last `window` positions of each token (paged_attention in include/asv.h).
     cache_len [B] counts the tokens before the chunk; scale defaults to head_dim ** -0.5."""
-    if q.dim() != 3:
-        raise AsvError(2, "q must be [N, q_heads, head_dim]")
-    N, Hq, D = q.shape
-    cache, batch, B, dtype, cs = _paged_args(k_cache, v_cache, block_table, cache_len, indptr, N)
-    shape = (N, Hq, cs[3])
-    qr = _packed_rows(q, "q", shape, dtype)
+    handle = _raw_stream(q, stream)
     if out is None:
         dev = q.device
-        out = PagedAttentionOutput(torch.empty(q.shape, dtype=dtype, device=dev),
-                                   torch.empty(N, Hq, dtype=torch.float32, device=dev),
-                                   torch.zeros(B, dtype=torch.int32, device=dev))
-    rows = _packed_rows(out.out, "out.out", shape, dtype)
-    status, lse = _status_ptr(out.req_status, B), out.lse
-    if lse is not None:
-        if lse.dtype != torch.float32 or lse.shape != (N, Hq):
-            raise AsvError(2, "out.lse must be float32 [N, q_heads]")
-        if not lse.is_cuda:
-            _need_cuda(lse)
-        _contig(lse, "out.lse")
-        lse = lse.data_ptr()
-    L = _lib or library()
-    handle = _raw_stream(q, stream)
+        out = PagedAttentionOutput(torch.empty(q.shape, dtype=q.dtype, device=dev),
+                                   torch.empty(q.shape[:2], dtype=torch.float32, device=dev),
+                                   torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))
     if workspace is None:
-        workspace = _paged_workspace(q, handle, stream, paged_workspace_bytes(Hq, cs[2], D))
-    try:
-        st = L.paged_attention(cache, batch, qr, rows, Hq, D ** -0.5 if scale is None else scale, window, lse,
-                               status, workspace.data_ptr(), workspace.nbytes, handle)
-    except (C.ArgumentError, TypeError) as e:
-        raise AsvError(5, f"scale must be a number and window a 32-bit whole number ({e})") from None
-    if st:
-        _check(st, "paged_attention")
+        workspace = _paged_ws_cache.get((q.get_device(), handle))
+        if workspace is None:
+            workspace = _paged_workspace(q, handle, stream)
+    (_ext or _paged_ext()).paged_attention(q, k_cache, v_cache, block_table, cache_len, indptr, scale, window,
+                                           out.out, out.lse, out.req_status, workspace, handle)
     return out

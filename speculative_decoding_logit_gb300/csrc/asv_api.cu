@@ -215,8 +215,8 @@ const char* asv_status_string(asv_status s) {
   switch (s) {
     case ASV_OK: return "ASV_OK";
     case ASV_ERR_NULL: return "ASV_ERR_NULL: a required pointer is NULL";
-    case ASV_ERR_SHAPE: return "ASV_ERR_SHAPE: invalid B, K or V";
-    case ASV_ERR_ALIGN: return "ASV_ERR_ALIGN: misaligned pointer";
+    case ASV_ERR_SHAPE: return "ASV_ERR_SHAPE: a size is out of range";
+    case ASV_ERR_ALIGN: return "ASV_ERR_ALIGN: misaligned pointer or stride";
     case ASV_ERR_DTYPE: return "ASV_ERR_DTYPE: unsupported element type";
     case ASV_ERR_PARAM: return "ASV_ERR_PARAM: scalar parameter out of range";
     case ASV_ERR_WORKSPACE: return "ASV_ERR_WORKSPACE: workspace missing or too small";

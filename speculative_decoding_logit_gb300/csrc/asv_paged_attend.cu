@@ -1211,14 +1211,6 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, int d
   auto kernel = paged_attention_kernel<BF16, DP, NT>;
   constexpr int kSmem = 1024 + (2 + kRingSlots<DP>) * kTile * DP * 2 + int(sizeof(Misc));
   static_assert(kSmem <= 232448, "shared memory");
-  // the limit is raised once per device
-  static std::atomic<uint64_t> raised{0};
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(raised.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_relaxed);
-  }
   // a programmatic launch: the set-up runs while the launch before it ends
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid), 1, 1);
@@ -1230,6 +1222,17 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, int d
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // the limit is raised once per device, and again should a launch fail (a device reset forgets it)
+  static std::atomic<uint64_t> raised{0};
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (raised.load(std::memory_order_relaxed) & bit) {
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, maps[0], maps[1], maps[2]);
+    if (e != cudaErrorInvalidValue) return e;
+    cudaGetLastError();
+  }
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  raised.fetch_or(bit, std::memory_order_relaxed);
   return cudaLaunchKernelEx(&cfg, kernel, a, maps[0], maps[1], maps[2]);
 }
 

@@ -17,6 +17,9 @@ LIB = os.path.join(BUILD, "libasv.so")
 # The checked build: the same sources with -DASV_CHECKED (every kernel index tested against its
 # buffer, failures counted in the workspace's check log, the access skipped).
 LIB_CHECKED = os.path.join(BUILD, "libasv_checked.so")
+# The binding's compiled part (a CPython module over PyTorch's C++ tensors, no device code).
+TORCH_EXT = os.path.join(BUILD, "asv_torch.so")
+TORCH_EXT_SRC = os.path.join(CSRC, "asv_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -46,8 +49,44 @@ def build_checked(force: bool = False, verbose: bool = False) -> str:
     return build(force=force, verbose=verbose, extra_flags=("-DASV_CHECKED",), lib=LIB_CHECKED)
 
 
+def build_torch_ext(force: bool = False) -> str:
+    """Compile the binding's module (_build/asv_torch.so) with the host compiler."""
+    deps = [TORCH_EXT_SRC, os.path.join(INCLUDE, "asv.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(TORCH_EXT) and all(
+            os.path.getmtime(d) <= os.path.getmtime(TORCH_EXT) for d in deps):
+        return TORCH_EXT
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = TORCH_EXT + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", *[f"-I{i}" for i in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", TORCH_EXT_SRC, "-o", tmp,
+           f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding's module failed to compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_EXT)
+    return TORCH_EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib: str = LIB) -> str:
-    """Compile csrc/*.cu and link `lib` (default _build/libasv.so); returns the library path."""
+    """Compile csrc/*.cu and link `lib` (default _build/libasv.so), and with the default library the
+    binding's module; returns the library path."""
+    if lib != LIB:
+        return _build_library(force, verbose, extra_flags, lib)
+    with cf.ThreadPoolExecutor(1) as ex:
+        ext = ex.submit(build_torch_ext, force)
+        path = _build_library(force, verbose, extra_flags, lib)
+        ext.result()
+    return path
+
+
+def _build_library(force: bool, verbose: bool, extra_flags, lib: str) -> str:
     if not force and up_to_date(lib):
         return lib
     os.makedirs(BUILD, exist_ok=True)

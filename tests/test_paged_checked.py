@@ -60,9 +60,16 @@ def test_no_index_leaves_its_buffer(libs, dtype, q_lens, past, heads, dim, page,
     need = lib.asv_paged_workspace_bytes(heads[0], heads[1], dim)
     ws = Guarded(torch.zeros(need, dtype=torch.uint8, device="cuda"))
     assert ws.raw.data_ptr() % 256 == 0
-    cache, batch, _, _, _ = m._paged_args(kc.t, vc.t, b.table, b.cache_len, b.indptr, b.N)
-    rows = lambda x: m._pack_rows(x.data_ptr(), x.stride(0), x.stride(1))
-    rot = m._pack_rotary(table.data_ptr(), table.shape[1], table.shape[0], 0)
+    keep = [m._PagedCacheC(kc.t.data_ptr(), vc.t.data_ptr(), m.ASV_BF16 if dtype == torch.bfloat16 else m.ASV_F16,
+                           *kc.t.shape, *kc.t.stride()[:3], *vc.t.stride()[:3]),
+            m._PagedBatchC(b.B, b.N, b.indptr.data_ptr(), b.cache_len.data_ptr(), b.table.data_ptr(), b.table.shape[1],
+                           b.table.stride(0)),
+            m._RotaryC(table.data_ptr(), table.shape[1], table.shape[0], 0)]
+    cache, batch, rot = (C.addressof(x) for x in keep)
+
+    def rows(x):
+        keep.append(m._RowsC(x.data_ptr(), x.stride(0), x.stride(1)))
+        return C.addressof(keep[-1])
     sh = torch.cuda.current_stream().cuda_stream
     assert lib.paged_kv_append(cache, batch, rows(k), rows(v), rows(b.qd), rows(q.t), heads[0], rot,
                                status.t.data_ptr(), sh) == 0

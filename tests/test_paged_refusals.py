@@ -132,16 +132,6 @@ def test_attention_scalars(m):
     assert m.library().paged_kv_append(None, None, None, None, None, None, 4, None, None, None) == NULL
 
 
-def test_packed_forms_match_the_structures(m):
-    cache = (BASE, BASE + 16, 1, 4, 16, 2, 64, 1, 2, 3, 4, 5, 1 << 40)
-    batch = (2, 3, BASE, BASE + 4, BASE + 8, 5, 1 << 33)
-    for cls, pack, values in ((m._PagedCacheC, m._pack_cache, cache), (m._PagedBatchC, m._pack_batch, batch),
-                              (m._RowsC, m._pack_rows, (BASE, -5, 1 << 35)), (m._RotaryC, m._pack_rotary, (BASE, 64, 9, 1))):
-        got = cls.from_buffer_copy(pack(*values))
-        assert len(pack(*values)) == C.sizeof(cls)
-        assert tuple(getattr(got, f[0]) for f in cls._fields_) == values
-
-
 def test_workspace_size(m):
     n = m.paged_workspace_bytes(32, 8, 128)
     assert n > 0
