@@ -45,9 +45,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   const int tid = threadIdx.x, token0 = blockIdx.x * TOKENS;
   const long long limit = a.rotary != nullptr ? min((long long)a.max_position, table_positions(c)) : table_positions(c);
 
-  // What came before on the stream is needed from here on; what comes after may set itself up.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // What comes after on the stream may set itself up; what came before is needed from here on.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the tokens' requests and places
   int before = 0;

@@ -152,20 +152,11 @@ __device__ Items load_items(const PagedView& c, int b, int T) {
   return it;
 }
 
-// The item that a run starts in: units before it, its request, its place among the request's, head and key tiles.
-struct Start {
-  long long item0;
-  Items it;
-  int request, i, h, n;
-};
-
 struct Misc {
   uint64_t kv_full[10], kv_empty[10];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[4], pv_done[2], o_full[2], o_empty[2];
   uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
   Piece piece[kQueue];
-  long long warp_sum[12];
-  Start start;
   uint32_t tmem;
   int abort;
   int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
@@ -314,7 +305,6 @@ template <bool BF16, int DP, int NT>
 __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  constexpr int kThreads = kThreadsOf<NT>;
   constexpr int kCost = kItemCost<NT>;
   constexpr int kRing = kRingSlots<DP>;
   constexpr int kHalves = DP / 64;                // 64-element column blocks, 128 bytes a row
@@ -360,76 +350,64 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     prefetch_map(&map_k);
     prefetch_map(&map_v);
   }
-  // What came before on the stream is needed from here on; what comes after may set itself up.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // units of this thread's requests, and of all
-  const int per_thread = (c.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per_thread, c.B), b1 = min(b0 + per_thread, c.B);
-  long long own = 0;
-  Items it;
-  for (int b = b0; b < b1; ++b) {
-    it = load_items(c, b, T);
-    if (!it.r.ok && blockIdx.x == 0) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
-    own += it.units(a.window, kCost, c.kv_heads);
-  }
-  long long incl = own;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) ms.warp_sum[warp] = incl;
+  fence_before();
   __syncthreads();
-  long long before = incl - own, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += ms.warp_sum[w];
-    total += ms.warp_sum[w];
-  }
-  const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
-  const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
-  if (u0 >= before && u0 < before + own) {
-    long long x = before;
+  fence_after();
+  const uint32_t tmem = ms.tmem;
+  // What comes after on the stream may set itself up; what came before is needed from here on.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (warp == kWalkWarp) {
+    // ---- scheduler: the lanes sum up their shares of the requests; the one whose share the run starts in walks it
+    const int per_lane = (c.B + 31) / 32, b0 = min(lane * per_lane, c.B), b1 = min(b0 + per_lane, c.B);
+    long long own = 0;
+    Items it;
     for (int b = b0; b < b1; ++b) {
-      if (per_thread > 1) it = load_items(c, b, T);
-      const long long n = per_thread > 1 ? it.units(a.window, kCost, c.kv_heads) : own;
-      if (u0 < x + n) {
-        const long long rel = u0 - x;
-        int i = 0;  // the item that holds unit u0: the last with no more than rel units before it
+      it = load_items(c, b, T);
+      if (!it.r.ok && blockIdx.x == 0) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
+      own += it.units(a.window, kCost, c.kv_heads);
+    }
+    long long before = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    const long long total = __shfl_sync(0xffffffffu, before, 31);
+    before -= own;
+    const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
+    const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
+    if (u0 < u1 ? u0 >= before && u0 < before + own : lane == 0) {
+      int b = c.B, i = 0, n = 0, h = 0;
+      long long item0 = u0;
+      if (u0 < u1) {
+        for (b = b0;; ++b) {
+          if (per_lane > 1) {
+            it = load_items(c, b, T);
+            own = it.units(a.window, kCost, c.kv_heads);
+          }
+          if (u0 < before + own) break;
+          before += own;
+        }
+        // the item that holds unit u0: the last with no more than rel units before it
+        const long long rel = u0 - before;
         for (int hi = it.n; hi - i > 1;) {
           const int mid = (i + hi) / 2;
           if (c.kv_heads * it.before(a.window, kCost, mid) <= rel) i = mid;
           else hi = mid;
         }
-        const int tiles = it.tiles(a.window, i);
-        const long long item = x + c.kv_heads * it.before(a.window, kCost, i);
-        const int h = int(quotient(u0 - item, tiles + kCost));
-        ms.start = Start{item + (long long)h * (tiles + kCost), it, b, i, h, tiles};
-        break;
+        n = it.tiles(a.window, i);
+        item0 = before + c.kv_heads * it.before(a.window, kCost, i);
+        h = int(quotient(u0 - item0, n + kCost));
+        item0 += (long long)h * (n + kCost);
       }
-      x += n;
-    }
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = ms.tmem;
-  const bool idle = u0 >= u1;
-
-  if (idle) {
-  } else if (warp == kWalkWarp) {
-    // ---- scheduler
-    if (lane == 0) {
-      int b = ms.start.request, i = ms.start.i, n = ms.start.n, h = ms.start.h;
-      long long item0 = ms.start.item0;
-      Items it = ms.start.it;
       Ring ring_p;
-      for (bool end = false; !end;) {
+      for (;;) {
         // its first kCost units are its own, then one for each key tile
         const int ta = int(max(u0 - item0 - kCost, 0ll));
         const int tb = int(min(max(u1 - item0 - kCost, 0ll), (long long)n));
-        end = b >= c.B || item0 >= u1;
+        const bool end = b >= c.B || item0 >= u1;
         if (end || tb > ta) {
           if (!bar_wait(at(ms.piece_empty, ring_p.slot), ring_p.phase ^ 1, abort)) break;
           Piece& p = ms.piece[ring_p.slot];
@@ -454,6 +432,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           bar_arrive(at(ms.piece_full, ring_p.slot));
           ring_p.next(kQueue);
         }
+        if (end) break;
         item0 += n + kCost;
         if (++h == c.kv_heads) {
           h = 0;
@@ -1057,7 +1036,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
 
       // The last to file joins the parts, in CTA order.  The warps' writes come before the ticket through the
       // barrier and the ticket's release, the other CTAs' before the reads through its acquire and the barrier.
-      if (!wg_sync()) break;
+      // (Rows of the first warp alone need no barrier.)
+      if (n_rows > 32 && !wg_sync()) break;
+      __syncwarp();
       if (row == 0 && ASV_GUARD(a, p.first_cta + p.n_parts <= int(gridDim.x))) {
         const uint32_t old = atom_add_acq_rel_gpu(a.tickets + 2 * p.first_cta + wg, 1u);
         ms.last[wg][sync_phase] = old == uint32_t(p.n_parts - 1);
@@ -1090,7 +1071,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       float m = -INFINITY, l = 0.0f;
       // The parts in order, `kIn` at a time with all their loads in flight.  Few rows: a thread has one vector of
       // four columns and everything of a part at once.  Many: the rows' sums first, then eight vectors a time.
-      constexpr int kIn = 8, kCols = 8;
+      constexpr int kIn = 16, kCols = 8;
       if (cols4 <= step) {
         float4 acc = zero;
         for (int k0 = 0; k0 < p.n_parts; k0 += kIn) {
