@@ -67,9 +67,13 @@ struct Piece {
   int kind;        // 0: a piece; 1: the end of the run
 };
 
-// a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.
+// a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.  (What is
+// rare is out of line here and below: a short call runs most of its instructions for the first time, and fetching
+// them is a good part of its time.)
+__device__ __noinline__ long long quotient_64(long long a, long long b) { return a / b; }
+
 __device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : quotient_64(a, b);
 }
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0: each round takes out the whole parts of a / m and b / m
@@ -98,7 +102,7 @@ __device__ __noinline__ long long floor_sum(long long n, long long m, long long 
 }
 
 // sum_{i < n} floor((T i + b) / 128) for b >= 0; `shift` is log2 T where T is a power of two, else -1.
-__device__ __forceinline__ long long tile_sum(long long n, int T, int shift, long long b) {
+__device__ __noinline__ long long tile_sum(long long n, int T, int shift, long long b) {
   if (shift < 0) return floor_sum(n, kTile, T, b);
   if (shift >= 7) return n * (b >> 7) + ((n * (n - 1) / 2) << (shift - 7));
   // floor((floor(b / T) + i) / r), r = 128 / T: differences of sum_{m < x} floor(m / r)
@@ -109,6 +113,17 @@ __device__ __forceinline__ long long tile_sum(long long n, int T, int shift, lon
   };
   const long long c = b >> shift;
   return below(c + n) - below(c);
+}
+
+// Key tiles of the first i items of T tokens behind `past` tokens.
+__device__ __noinline__ long long sum_before(int past, int T, int shift, int window, int i) {
+  long long sum = tile_sum(i, T, shift, (long long)past + T + kTile - 1);
+  if (window > 0) {
+    // items before z start at position 0
+    const long long z = past >= window - 1 ? 0 : quotient((long long)window - 1 - past + T - 1, T);
+    if (i > z) sum -= tile_sum(i - z, T, shift, past + z * T - window + 1);
+  }
+  return sum;
 }
 
 // A request's items of one key head: n of them, item r with the tokens from r * T.
@@ -124,15 +139,7 @@ struct Items {
   }
   // key tiles of the items before i (i < n)
   __device__ long long tiles_before(int window, int i) const {
-    if (i == 0) return 0;
-    if (!r.ok) return i;
-    long long sum = tile_sum(i, T, shift, (long long)r.past + T + kTile - 1);
-    if (window > 0) {
-      // items before z start at position 0
-      const long long z = r.past >= window - 1 ? 0 : quotient((long long)window - 1 - r.past + T - 1, T);
-      if (i > z) sum -= tile_sum(i - z, T, shift, r.past + z * T - window + 1);
-    }
-    return sum;
+    return i == 0 ? 0 : r.ok ? sum_before(r.past, T, shift, window, i) : i;
   }
   // units of one key head before item i
   __device__ long long before(int window, int cost, int i) const { return tiles_before(window, i) + (long long)cost * i; }

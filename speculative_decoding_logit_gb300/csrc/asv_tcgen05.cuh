@@ -58,13 +58,17 @@ __device__ __forceinline__ unsigned long long now_ns() {
 constexpr unsigned long long kWaitNs = 2000000000ull;  // far above any wait that can end
 
 // Slow part of a wait: until the phase of parity `parity` completes, `abort` is raised or the time is
-// up (which raises it).
+// up (which raises it).  The global timer is read now and then only: a read takes longer than most waits.
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
-  const unsigned long long t0 = now_ns();
-  for (;;) {
+  unsigned long long t0 = 0;
+  for (uint32_t n = 1;; ++n) {
     if (bar_try(bar, parity)) return true;
+    if (n % 64 != 0) continue;
     if (*abort) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    const unsigned long long t = now_ns();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > kWaitNs) {
       *abort = 1;
       return false;
     }
