@@ -63,8 +63,9 @@ struct Piece {
   int kv_lo;       // first position that any of the tokens attends to
   int t0, t1;      // key tiles [t0, t1); none: a request left out, whose outputs are zero
   int part;        // -1: the whole item; else the slot of its partial result
-  int first_cta, n_parts;
+  int item_tiles;  // key tiles of the item
   int kind;        // 0: a piece; 1: the end of the run
+  long long item;  // units before the item's first key tile
 };
 
 // a / b for a >= 0, b > 0; in 32 bits where that will do (all but always), at a fraction of the time.  (What is
@@ -164,6 +165,7 @@ struct Misc {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[4], pv_done[2], o_full[2], o_empty[2];
   uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
   Piece piece[kQueue];
+  long long per_cta;  // units of a run
   uint32_t tmem;
   int abort;
   int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
@@ -385,6 +387,8 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     before -= own;
     const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
     const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
+    if (lane == 0) ms.per_cta = per_cta;
+    __syncwarp();
     if (u0 < u1 ? u0 >= before && u0 < before + own : lane == 0) {
       int b = c.B, i = 0, n = 0, h = 0;
       long long item0 = u0;
@@ -429,12 +433,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
             const int tile0 = p.kv_lo / kTile;
             p.t0 = it.r.ok ? tile0 + ta : 0;
             p.t1 = it.r.ok ? tile0 + tb : 0;
-            p.part = -1;
-            if (tb - ta < n) {
-              p.first_cta = int(quotient(item0 + kCost, per_cta));
-              p.n_parts = int(quotient(item0 + kCost + n - 1, per_cta)) - p.first_cta + 1;
-              p.part = 2 * int(blockIdx.x) + (ta == 0 ? 1 : 0);
-            }
+            p.part = tb - ta == n ? -1 : 2 * int(blockIdx.x) + (ta == 0 ? 1 : 0);
+            p.item_tiles = n;
+            p.item = item0 + kCost;
           }
           bar_arrive(at(ms.piece_full, ring_p.slot));
           ring_p.next(kQueue);
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       }
     }
   } else if (warp == kCopyWarp || warp == kCopyWarp + 1) {
-    // ---- copies: one warp for keys and queries, one for values; a copy takes its warp about 50 cycles
+    // ---- copies: one warp for keys, one for queries and values; a copy takes its warp about 50 cycles
     const bool values = warp == kCopyWarp + 1;
     // 32 lanes hold the pages of up to 32 boxes, a window of one or more tiles; the next window's entries of
     // the block table are on their way while this one's tiles are copied.
@@ -540,20 +541,18 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     };
     Window w, ahead;
     ahead.n = 0;
-    bool run = true, begun = false;
+    bool run = true;
     while (run) {
       if (ahead.n == 0 && (!next_window(true, ahead) || ahead.n == 0)) break;
       w = ahead;
+      ahead.n = 0;
+      if (values && w.first) run = copy_queries(w);
       const bool ok = w.need && w.entry >= 0 && w.entry < c.num_pages;
-      if (w.need && !ok) atomicOr(a.status + w.request, ASV_REQ_BAD_PAGE);
+      if (w.need && !ok && !values) atomicOr(a.status + w.request, ASV_REQ_BAD_PAGE);
       const int page = ok ? w.entry : c.num_pages;
-      next_window(false, ahead);
       for (int i = 0; i < w.n && run; ++i) {
-        // an item's queries after its first keys, which need not wait for the item before (the run's first: before)
-        if (!begun && !values) run = copy_queries(w);
-        run = run && copy_tile(w.head, i, page, w.slot);
-        if (i == 0 && w.first && begun && !values) run = run && copy_queries(w);
-        begun = true;
+        run = copy_tile(w.head, i, page, w.slot);
+        if (i == 0) next_window(false, ahead);
       }
     }
     if (*abort) {  // leave with no copy in flight: the slots still being written, for a while
@@ -744,21 +743,18 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           if (last) ring_q.next(2);
           return true;
         };
-        const bool early = more && (!first || __all_sync(0xffffffffu, bar_test(at(ms.kv_full, ring_k.slot), ring_k.phase) &&
-                                                                          bar_test(at(ms.q_full, ring_q.slot), ring_q.phase)));
-        if (early) ok = qk_tile();
-        if (ok && have_prev) {
-          // the output buffer (and its poison mark) is free; the weights come in two halves (qk_tile counted a use
-          // of the other buffer, so prev's parity is its own)
-          if (prev_first) ok = warp_wait(at(ms.o_empty, prev_ob), (items[prev_ob] & 1) ^ 1, abort);
-          ok = ok && take_values(ring_v, prev, prev_ob, prev_ob);
+        // the output buffer (and its poison mark) is free; the weights come in two halves (qk_tile counts a use of
+        // the other buffer, so prev's parity is its own)
+        auto pv_tile = [&]() {
+          if (prev_first && !warp_wait(at(ms.o_empty, prev_ob), (items[prev_ob] & 1) ^ 1, abort)) return false;
+          if (!take_values(ring_v, prev, prev_ob, prev_ob)) return false;
           const uint32_t p_phase = (used[prev_sb] & 1) ^ 1;
           const bool whole = prev.whole();
-          if (!ok || !warp_wait(at(ms.p_full, 2 * prev_sb), p_phase, abort)) break;
+          if (!warp_wait(at(ms.p_full, 2 * prev_sb), p_phase, abort)) return false;
           fence_after();
           if (whole && elect()) pv_run(prev_ob, prev_sb, ring_v.slot, 0, prev_first, std::integral_constant<int, 4>());
           __syncwarp();
-          if (!warp_wait(at(ms.p_full, 2 * prev_sb + 1), p_phase, abort)) break;
+          if (!warp_wait(at(ms.p_full, 2 * prev_sb + 1), p_phase, abort)) return false;
           fence_after();
           if (elect()) {
             if (whole) pv_run(prev_ob, prev_sb, ring_v.slot, 4, false, std::integral_constant<int, 4>());
@@ -770,8 +766,19 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           __syncwarp();
           if (prev_last) ++items[prev_ob];
           ring_v.next(kRing, 2);
+          return true;
+        };
+        const bool early = more && (!first || __all_sync(0xffffffffu, bar_test(at(ms.kv_full, ring_k.slot), ring_k.phase) &&
+                                                                          bar_test(at(ms.q_full, ring_q.slot), ring_q.phase)));
+#pragma unroll 1
+        for (int step = 0; step < 2 && ok; ++step) {
+          if ((step == 0) == early) {
+            if (more) ok = qk_tile();
+          } else if (have_prev) {
+            ok = pv_tile();
+          }
         }
-        if (ok && more && !early) ok = qk_tile();
+        if (!ok) break;
         if (!more) break;
         prev = Span{t * kTile, p.pos0, p.kv_lo, p.pos0 + p.ntok};
         prev_sb = sb;
@@ -932,6 +939,12 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       if (!run) break;
 
       // ---- epilogue
+      int first_cta = 0, n_parts = 1;  // the CTAs that have parts of the item
+      if (p.part >= 0) {
+        const long long per_cta = ms.per_cta;
+        first_cta = int(quotient(p.item, per_cta));
+        n_parts = int(quotient(p.item + p.item_tiles - 1, per_cta)) - first_cta + 1;
+      }
       const int n_rows = ntok * a.group;
       const int tok_row = p.tok0 + first_tok + tok;
       const int head = p.head * a.group + g;
@@ -1046,20 +1059,20 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       // (Rows of the first warp alone need no barrier.)
       if (n_rows > 32 && !wg_sync()) break;
       __syncwarp();
-      if (row == 0 && ASV_GUARD(a, p.first_cta + p.n_parts <= int(gridDim.x))) {
-        const uint32_t old = atom_add_acq_rel_gpu(a.tickets + 2 * p.first_cta + wg, 1u);
-        ms.last[wg][sync_phase] = old == uint32_t(p.n_parts - 1);
+      if (row == 0 && ASV_GUARD(a, first_cta + n_parts <= int(gridDim.x))) {
+        const uint32_t old = atom_add_acq_rel_gpu(a.tickets + 2 * first_cta + wg, 1u);
+        ms.last[wg][sync_phase] = old == uint32_t(n_parts - 1);
       }
       const uint32_t which = sync_phase;
       if (!wg_sync()) break;
       if (*reinterpret_cast<volatile int*>(&ms.last[wg][which]) == 0) continue;
-      if (row == 0) a.tickets[2 * p.first_cta + wg] = 0;
+      if (row == 0) a.tickets[2 * first_cta + wg] = 0;
       // A thread keeps one row: `span` threads side by side have the rows, the others further columns.
       const int span = n_rows <= 1 ? 1 : 1 << (32 - __clz(n_rows - 1)), r = row & (span - 1);
       const int cols4 = c.head_dim / 4, step = kTile / span;
       if (r >= n_rows) continue;
       auto part_of = [&](int k) {
-        const int slot = k == 0 ? 2 * p.first_cta + 1 : 2 * (p.first_cta + k);
+        const int slot = k == 0 ? 2 * first_cta + 1 : 2 * (first_cta + k);
         return a.parts + (size_t(slot) * 2 + wg) * part_floats;
       };
       auto stats_of = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part_of(k) + kTile * DP) + r); };
@@ -1081,14 +1094,14 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       constexpr int kIn = 16, kCols = 8;
       if (cols4 <= step) {
         float4 acc = zero;
-        for (int k0 = 0; k0 < p.n_parts; k0 += kIn) {
+        for (int k0 = 0; k0 < n_parts; k0 += kIn) {
           float2 ml[kIn];
           float4 o[kIn];
 #pragma unroll
           for (int k = 0; k < kIn; ++k) {
             ml[k] = make_float2(-INFINITY, 0.0f);
             o[k] = zero;
-            if (k0 + k < p.n_parts && col0 < cols4) {
+            if (k0 + k < n_parts && col0 < cols4) {
               ml[k] = stats_of(k0 + k);
               o[k] = __ldcg(reinterpret_cast<const float4*>(part_of(k0 + k)) + col0 * kTile + r);
             }
@@ -1111,7 +1124,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         if (col0 < cols4) put(col0, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
       } else {
 #pragma unroll 8
-        for (int k = 0; k < p.n_parts; ++k) {
+        for (int k = 0; k < n_parts; ++k) {
           const float2 ml = stats_of(k);
           const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
           l = l * ex2_approx(m - base) + ml.y * ex2_approx(ml.x - base);
@@ -1122,15 +1135,15 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           float4 acc[kCols];
 #pragma unroll
           for (int i = 0; i < kCols; ++i) acc[i] = zero;
-          for (int k = 0; k < p.n_parts; k += 2) {
+          for (int k = 0; k < n_parts; k += 2) {
             float4 o[2][kCols];
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               // (what is past the last is read again, with no weight)
-              const int at = min(k + e, p.n_parts - 1);
+              const int at = min(k + e, n_parts - 1);
               const float4* part = reinterpret_cast<const float4*>(part_of(at)) + r;
-              w[e] = k + e < p.n_parts ? stats_of(at).x : -INFINITY;
+              w[e] = k + e < n_parts ? stats_of(at).x : -INFINITY;
 #pragma unroll
               for (int i = 0; i < kCols; ++i) o[e][i] = ld_cg_f4(part + min(c0 + i, cols4 - 1) * kTile);
             }
