@@ -40,7 +40,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;  // rows of a row tile; positions of a key tile
-constexpr int kQueue = 4;
+constexpr int kQueue = 16;  // pieces ahead: of 4, short items left the copies waiting for the scheduler (2 % at 6 prompts)
 constexpr uint32_t kTmemColumns = 512;  // S buffers at 0 and 128, outputs at 256 and 384
 // Key tiles that an item's own work (queries in, outputs out, the pipeline's fill) is worth in the split.
 template <int NT>
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     Window w, ahead;
     ahead.n = 0;
     bool run = true;
-    while (run) {
+    for (int late = 1; run; late = 0) {
       if (ahead.n == 0 && (!next_window(true, ahead) || ahead.n == 0)) break;
       w = ahead;
       ahead.n = 0;
@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       if (w.need && !ok && !values) atomicOr(a.status + w.request, ASV_REQ_BAD_PAGE);
       const int page = ok ? w.entry : c.num_pages;
       for (int i = 0; i < w.n && run; ++i) {
+        if (i == late) next_window(false, ahead);
         run = copy_tile(w.head, i, page, w.slot);
-        if (i == 0) next_window(false, ahead);
       }
     }
     if (*abort) {  // leave with no copy in flight: the slots still being written, for a while
@@ -588,6 +588,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) step(i);
       } else {
+#pragma unroll 1
         for (int i = 0; i < k_steps; ++i) step(i);
       }
     };
@@ -600,6 +601,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     };
     auto pv_steps = [&](int ob, int sb, int slot, bool first, int i0, int i1) {
       const uint64_t vd = v_desc + slot * (kTileBytes / 16);
+#pragma unroll 1
       for (int i = i0; i < i1; ++i)
         mma_ts(tmem + 256 + ob * 128, tmem + sb * 128 + i * 8, vd + i * (2048 / 16), id_pv, !(first && i == i0));
     };
@@ -770,14 +772,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         };
         const bool early = more && (!first || __all_sync(0xffffffffu, bar_test(at(ms.kv_full, ring_k.slot), ring_k.phase) &&
                                                                           bar_test(at(ms.q_full, ring_q.slot), ring_q.phase)));
-#pragma unroll 1
-        for (int step = 0; step < 2 && ok; ++step) {
-          if ((step == 0) == early) {
-            if (more) ok = qk_tile();
-          } else if (have_prev) {
-            ok = pv_tile();
-          }
-        }
+        if (early) ok = qk_tile();
+        if (ok && have_prev) ok = pv_tile();
+        if (ok && more && !early) ok = qk_tile();
         if (!ok) break;
         if (!more) break;
         prev = Span{t * kTile, p.pos0, p.kv_lo, p.pos0 + p.ntok};
