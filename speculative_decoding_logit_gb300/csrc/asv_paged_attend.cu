@@ -42,9 +42,15 @@ using namespace tc;
 constexpr int kTile = 128;  // rows of a row tile; positions of a key tile
 constexpr int kQueue = 16;  // pieces ahead: of 4, short items left the copies waiting for the scheduler (2 % at 6 prompts)
 constexpr uint32_t kTmemColumns = 512;  // S buffers at 0 and 128, outputs at 256 and 384
-// Key tiles that an item's own work (queries in, outputs out, the pipeline's fill) is worth in the split.
+// Units of the split that a key tile is worth, and an item's own work (queries in, outputs out, the pipeline's
+// fill): two tiles where a CTA has an item or so, which keeps the cuts at whole tiles (one request, one token: 11.1 us,
+// with 7 units 11.6); a little less where it has many short ones (256 requests, one token: 105 us, 107.7 with 8, 110
+// with 5 or 10).
+constexpr int kTileCost = 4;
 template <int NT>
-constexpr int kItemCost = 2;
+__device__ int item_cost(const PagedView& c) {
+  return NT == 1 && (long long)c.B * c.kv_heads > gridDim.x ? 7 : 8;
+}
 constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
 
 // Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler.
@@ -143,9 +149,9 @@ struct Items {
     return i == 0 ? 0 : r.ok ? sum_before(r.past, T, shift, window, i) : i;
   }
   // units of one key head before item i
-  __device__ long long before(int window, int cost, int i) const { return tiles_before(window, i) + (long long)cost * i; }
+  __device__ long long before(int window, int cost, int i) const { return kTileCost * tiles_before(window, i) + (long long)cost * i; }
   __device__ long long units(int window, int cost, int kv_heads) const {
-    return n == 0 ? 0 : kv_heads * (before(window, cost, n - 1) + tiles(window, n - 1) + cost);
+    return n == 0 ? 0 : kv_heads * (before(window, cost, n - 1) + kTileCost * (long long)tiles(window, n - 1) + cost);
   }
 };
 
@@ -314,7 +320,6 @@ template <bool BF16, int DP, int NT>
 __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  constexpr int kCost = kItemCost<NT>;
   constexpr int kRing = kRingSlots<DP>;
   constexpr int kHalves = DP / 64;                // 64-element column blocks, 128 bytes a row
   constexpr uint32_t kTileBytes = kTile * DP * 2;
@@ -368,6 +373,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == kWalkWarp) {
+    const int cost = item_cost<NT>(c);
     // ---- scheduler: the lanes sum up their shares of the requests; the one whose share the run starts in walks it
     const int per_lane = (c.B + 31) / 32, b0 = min(lane * per_lane, c.B), b1 = min(b0 + per_lane, c.B);
     long long own = 0;
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     for (int b = b0; b < b1; ++b) {
       it = load_items(c, b, T);
       if (!it.r.ok && blockIdx.x == 0) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
-      own += it.units(a.window, kCost, c.kv_heads);
+      own += it.units(a.window, cost, c.kv_heads);
     }
     long long before = own;
 #pragma unroll
@@ -385,7 +391,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     }
     const long long total = __shfl_sync(0xffffffffu, before, 31);
     before -= own;
-    const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
+    // (whole tiles: where a run has few of them, an item begins that much sooner)
+    const long long per_cta =
+        max(quotient(total + gridDim.x * kTileCost - 1, gridDim.x * kTileCost), 1ll) * kTileCost;
     const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
     if (lane == 0) ms.per_cta = per_cta;
     __syncwarp();
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         for (b = b0;; ++b) {
           if (per_lane > 1) {
             it = load_items(c, b, T);
-            own = it.units(a.window, kCost, c.kv_heads);
+            own = it.units(a.window, cost, c.kv_heads);
           }
           if (u0 < before + own) break;
           before += own;
@@ -405,19 +413,20 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         const long long rel = u0 - before;
         for (int hi = it.n; hi - i > 1;) {
           const int mid = (i + hi) / 2;
-          if (c.kv_heads * it.before(a.window, kCost, mid) <= rel) i = mid;
+          if (c.kv_heads * it.before(a.window, cost, mid) <= rel) i = mid;
           else hi = mid;
         }
         n = it.tiles(a.window, i);
-        item0 = before + c.kv_heads * it.before(a.window, kCost, i);
-        h = int(quotient(u0 - item0, n + kCost));
-        item0 += (long long)h * (n + kCost);
+        item0 = before + c.kv_heads * it.before(a.window, cost, i);
+        const long long units = (long long)n * kTileCost + cost;
+        h = int(quotient(u0 - item0, units));
+        item0 += h * units;
       }
       Ring ring_p;
       for (;;) {
-        // its first kCost units are its own, then one for each key tile
-        const int ta = int(max(u0 - item0 - kCost, 0ll));
-        const int tb = int(min(max(u1 - item0 - kCost, 0ll), (long long)n));
+        // its first `cost` units are its own, then come its key tiles': a tile is the CTA's that has its last unit
+        const int ta = int(max(u0 - item0 - cost, 0ll) / kTileCost);
+        const int tb = int(min(max(u1 - item0 - cost, 0ll) / kTileCost, (long long)n));
         const bool end = b >= c.B || item0 >= u1;
         if (end || tb > ta) {
           if (!bar_wait(at(ms.piece_empty, ring_p.slot), ring_p.phase ^ 1, abort)) break;
@@ -435,13 +444,13 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
             p.t1 = it.r.ok ? tile0 + tb : 0;
             p.part = tb - ta == n ? -1 : 2 * int(blockIdx.x) + (ta == 0 ? 1 : 0);
             p.item_tiles = n;
-            p.item = item0 + kCost;
+            p.item = item0 + cost;
           }
           bar_arrive(at(ms.piece_full, ring_p.slot));
           ring_p.next(kQueue);
         }
         if (end) break;
-        item0 += n + kCost;
+        item0 += (long long)n * kTileCost + cost;
         if (++h == c.kv_heads) {
           h = 0;
           if (++i == it.n) {
@@ -939,8 +948,8 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       int first_cta = 0, n_parts = 1;  // the CTAs that have parts of the item
       if (p.part >= 0) {
         const long long per_cta = ms.per_cta;
-        first_cta = int(quotient(p.item, per_cta));
-        n_parts = int(quotient(p.item + p.item_tiles - 1, per_cta)) - first_cta + 1;
+        first_cta = int(quotient(p.item + kTileCost - 1, per_cta));
+        n_parts = int(quotient(p.item + (long long)p.item_tiles * kTileCost - 1, per_cta)) - first_cta + 1;
       }
       const int n_rows = ntok * a.group;
       const int tok_row = p.tok0 + first_tok + tok;
