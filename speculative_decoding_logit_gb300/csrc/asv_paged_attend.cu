@@ -57,8 +57,13 @@ constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the r
 template <int NT>
 constexpr int kThreadsOf = 32 * (4 * NT + 4);
 
-template <int DP>
-constexpr int kRingSlots = DP == 128 ? 5 : 10;
+// Slots of the ring of keys and values: what shared memory holds next to two tiles of queries (and the weights that the
+// warps of a divided row tile exchange).
+template <int DP, bool DIV>
+constexpr int kRingSlots = DP == 128 ? (DIV ? 4 : 5) : (DIV ? 8 : 10);
+constexpr uint32_t kChunkBytes = 32 * 32 * 2;  // weights of 32 rows for 32 positions: [8 positions][row] vectors
+template <bool DIV>
+constexpr uint32_t kExchangeBytes = DIV ? 2 * 4 * kChunkBytes : 0;
 
 // A run of key tiles of one item.
 struct Piece {
@@ -176,6 +181,13 @@ struct Misc {
   int abort;
   int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
   int last[2][2];
+};
+
+// What the warps of a divided row tile tell each other, for odd and even tiles: whether the reference has to move, the
+// maxima; the sums of a piece.
+struct Divided {
+  int vote[2][4];
+  float top[2][4][32], sum[4][32];
 };
 
 // Counters of a ring of `n` barriers: slot and phase of the i-th use.
@@ -316,18 +328,22 @@ __device__ __noinline__ void add_poison(const PagedView& c, int request, int hea
   }
 }
 
-template <bool BF16, int DP, int NT>
+template <bool BF16, int DP, int NT, bool DIV>
 __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  constexpr int kRing = kRingSlots<DP>;
+  static_assert(NT == 1 || !DIV);
+  constexpr int kRing = kRingSlots<DP, DIV>;
   constexpr int kHalves = DP / 64;                // 64-element column blocks, 128 bytes a row
   constexpr uint32_t kTileBytes = kTile * DP * 2;
   constexpr uint32_t kHalfBytes = kTile * 128;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t smem0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_tiles = smem0, ring = smem0 + 2 * kTileBytes;
-  Misc& ms = *reinterpret_cast<Misc*>(smem_raw + (smem0 - smem_addr(smem_raw)) + (2 + kRing) * kTileBytes);
+  const uint32_t exchange = ring + kRing * kTileBytes;
+  unsigned char* rest = smem_raw + (smem0 - smem_addr(smem_raw)) + (2 + kRing) * kTileBytes + kExchangeBytes<DIV>;
+  Misc& ms = *reinterpret_cast<Misc*>(rest);
+  Divided& dv = *reinterpret_cast<Divided*>(rest + sizeof(Misc));  // (only where DIV)
   const PagedView& c = a.c;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   constexpr int kMmaWarp = 4 * NT, kCopyWarp = 4 * NT + 1, kWalkWarp = 4 * NT + 3;
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       bar_init(at(ms.q_empty, i), 1);
       bar_init(at(ms.s_full, i), 1);
       bar_init(at(ms.p_full, 2 * i), 4);
-      bar_init(at(ms.p_full, 2 * i + 1), 4);
+      bar_init(at(ms.p_full, 2 * i + 1), DIV ? 1 : 4);
       bar_init(at(ms.pv_done, i), 1);
       bar_init(at(ms.o_full, i), 1);
       bar_init(at(ms.o_empty, i), 4);
@@ -538,11 +554,11 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       if (lane == 0) {
         const int tiles = NT == 1 || w.ntok <= a.tile_tokens ? 1 : 2;
         const uint32_t bar = at(ms.q_full, ring_q.slot);
-        bar_expect(bar, tiles * kHalves * a.tile_tokens * a.group * 128);
-        for (int i = 0; i < tiles; ++i)
+        bar_expect(bar, (DIV ? 4 : tiles) * kHalves * a.tile_tokens * a.group * 128);
+        for (int i = 0; i < (DIV ? 4 : tiles); ++i)
           for (int h = 0; h < kHalves; ++h)
-            copy_3d(q_tiles + (NT == 1 ? ring_q.slot : i) * kTileBytes + h * kHalfBytes, &map_q, h * 64,
-                    w.head * a.group, w.tok0 + i * a.tile_tokens, bar);
+            copy_3d(q_tiles + (NT == 1 ? ring_q.slot * kTileBytes + i * 32 * 128 : i * kTileBytes) + h * kHalfBytes, &map_q,
+                    h * 64, w.head * a.group, w.tok0 + (DIV ? 0 : i * a.tile_tokens), bar);
       }
       __syncwarp();
       ring_q.next(3 - NT);
@@ -761,14 +777,18 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           if (!take_values(ring_v, prev, prev_ob, prev_ob)) return false;
           const uint32_t p_phase = (used[prev_sb] & 1) ^ 1;
           const bool whole = prev.whole();
-          if (!warp_wait(at(ms.p_full, 2 * prev_sb), p_phase, abort)) return false;
-          fence_after();
-          if (whole && elect()) pv_run(prev_ob, prev_sb, ring_v.slot, 0, prev_first, std::integral_constant<int, 4>());
-          __syncwarp();
+          constexpr int kFirst = DIV ? 0 : 4;  // steps taken with the first half
+          if constexpr (!DIV) {
+            if (!warp_wait(at(ms.p_full, 2 * prev_sb), p_phase, abort)) return false;
+            fence_after();
+            if (whole && elect()) pv_run(prev_ob, prev_sb, ring_v.slot, 0, prev_first, std::integral_constant<int, kFirst>());
+            __syncwarp();
+          }
           if (!warp_wait(at(ms.p_full, 2 * prev_sb + 1), p_phase, abort)) return false;
           fence_after();
           if (elect()) {
-            if (whole) pv_run(prev_ob, prev_sb, ring_v.slot, 4, false, std::integral_constant<int, 4>());
+            if (whole)
+              pv_run(prev_ob, prev_sb, ring_v.slot, kFirst, DIV && prev_first, std::integral_constant<int, 8 - kFirst>());
             else pv_steps(prev_ob, prev_sb, ring_v.slot, prev_first, prev.first_step(), prev.end_step());
             commit(at(ms.pv_done, prev_sb));
             commit(at(ms.kv_empty, ring_v.slot));
@@ -800,7 +820,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     // ---- softmax: thread = row
     const int wg = warp / 4, row = (warp % 4) * 32 + lane;
     const uint32_t lanes = uint32_t((warp % 4) * 32) << 16;
-    const int tok = row / a.group, g = row - tok * a.group;
+    const int part32 = DIV ? warp % 4 : 0;  // the warp's 32 positions of a tile, where it is divided by positions
+    const int tok = (DIV ? lane : row) / a.group, g = (DIV ? lane : row) - tok * a.group;
+    const bool stores = part32 == 0;  // the warp has outputs in its rows
     const float scale2 = a.scale * kLog2e;
     Ring ring_p;
     uint32_t used = 0, pieces = 0, sync_phase = 0;
@@ -837,6 +859,25 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       const int ob = NT == 1 ? int(pieces & 1) : wg;
       const uint32_t o_addr = tmem + 256 + ob * 128 + lanes;
       float ref = -INFINITY, sum = 0.0f;
+      // the outputs so far, once the previous product is in them
+      auto rescale = [&](float keep) {
+        __syncwarp();
+        if (NT == 1) {
+          const uint32_t w = used - 1;
+          if (!warp_wait(at(ms.pv_done, int(w & 1)), (w >> 1) & 1, abort)) return false;
+          fence_after();
+        }
+#pragma unroll 1
+        for (int i = 0; i < DP / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + i * 32, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+          tmem_st32(o_addr + i * 32, o);
+        }
+        return true;
+      };
       for (int t = p.t0; t < p.t1; ++t) {
         const int sb = NT == 1 ? int(used & 1) : wg;
         const uint32_t s_addr = tmem + sb * 128 + lanes;
@@ -844,7 +885,95 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           run = false;
           break;
         }
-        if (any) {
+        if constexpr (DIV) {
+          fence_after();
+          __syncwarp();
+          const int base = t * kTile + part32 * 32, buf = used & 1;
+          uint32_t s[32];
+          tmem_ld32(s_addr + part32 * 32, s);
+          tmem_wait_ld(s);
+          fence_before();
+          if (base + 32 > all_hi || base < all_lo) {
+            const int b0 = lo - base, b1 = hi - base;
+            const uint32_t from = b0 <= 0 ? ~0u : b0 >= 32 ? 0u : ~0u << b0;
+            const uint32_t keep = b1 >= 32 ? from : b1 <= 0 ? 0u : from & ((1u << b1) - 1);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((keep >> j) & 1u)) s[j] = 0xff800000u;
+          }
+          float m[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[30]), __uint_as_float(s[31])};
+#pragma unroll
+          for (int j = 2; j < 30; j += 2) m[(j / 2) & 3] = max3(m[(j / 2) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          const float top = valid ? fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale2 : -INFINITY;
+          // The weights by the reference so far, which holds for most tiles; should a row have passed it (and for a
+          // piece's first tile), once more by the reference that the warps' maxima give.
+          const uint32_t mine = exchange + (buf * 4 + part32) * kChunkBytes + lane * 16;
+          float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+          for (int pass = t == p.t0 ? 1 : 0; pass < 2; ++pass) {
+            if (pass == 1) {
+              dv.top[buf][part32][lane] = top;
+              if (!wg_sync()) {
+                run = false;
+                break;
+              }
+              const float all = fmaxf(max3(dv.top[buf][0][lane], dv.top[buf][1][lane], dv.top[buf][2][lane]), dv.top[buf][3][lane]);
+              const bool move = all > ref + kLazy;
+              const float keep = move ? ex2_approx(ref - all) : 1.0f;
+              if (move) {
+                ref = all;
+                sum *= keep;
+              }
+              if (t > p.t0 && stores && !rescale(keep)) {
+                run = false;
+                break;
+              }
+            }
+            const float shift = ref == -INFINITY ? 0.0f : -ref;
+            const float2 sc = make_float2(scale2, scale2), sh = make_float2(shift, shift);
+            part = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float2 x = ffma2(make_float2(__uint_as_float(s[8 * v + 2 * j]), __uint_as_float(s[8 * v + 2 * j + 1])), sc, sh);
+                x.x = ex2_approx(x.x);
+                x.y = ex2_approx(x.y);
+                part = fadd2(part, x);
+                w[j] = pack2<BF16>(x.x, x.y);
+              }
+              sts16(mine + v * 512, make_uint4(w[0], w[1], w[2], w[3]));
+            }
+            const bool passed = __any_sync(0xffffffffu, top > ref + kLazy);
+            if (lane == 0) dv.vote[buf][part32] = passed;
+            if (!wg_sync()) {
+              run = false;
+              break;
+            }
+            if (pass == 0 && (dv.vote[buf][0] | dv.vote[buf][1] | dv.vote[buf][2] | dv.vote[buf][3]) == 0) break;
+          }
+          if (!run) break;
+          sum += part.x + part.y;
+          if (stores) {
+            // all of the rows' weights, from the four warps
+            const uint32_t theirs = exchange + buf * 4 * kChunkBytes + lane * 16;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t w[32];
+#pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                const uint4 x = lds16(theirs + (half * 8 + v) * 512);
+                w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+              }
+              tmem_st32(s_addr + half * 32, w);
+            }
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(at(ms.p_full, 2 * sb + 1));
+          }
+        } else if (any) {
           fence_after();
           __syncwarp();
           const int base = t * kTile;
@@ -888,26 +1017,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
               ref = top;
               sum *= keep;
             }
-            if (t > p.t0) {
-              // the outputs so far, once the previous product is in them
-              __syncwarp();
-              if (NT == 1) {
-                const uint32_t w = used - 1;
-                if (!warp_wait(at(ms.pv_done, int(w & 1)), (w >> 1) & 1, abort)) {
-                  run = false;
-                  break;
-                }
-                fence_after();
-              }
-#pragma unroll 1
-              for (int i = 0; i < DP / 32; ++i) {
-                uint32_t o[32];
-                tmem_ld32(o_addr + i * 32, o);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-                tmem_st32(o_addr + i * 32, o);
-              }
+            if (t > p.t0 && !rescale(keep)) {
+              run = false;
+              break;
             }
           }
           __syncwarp();
@@ -944,6 +1056,14 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       }
       if (!run) break;
 
+      if constexpr (DIV) {
+        if (p.t1 > p.t0) {
+          dv.sum[part32][lane] = sum;
+          if (!wg_sync()) break;
+          sum = dv.sum[0][lane] + dv.sum[1][lane] + (dv.sum[2][lane] + dv.sum[3][lane]);
+        }
+      }
+
       // ---- epilogue
       int first_cta = 0, n_parts = 1;  // the CTAs that have parts of the item
       if (p.part >= 0) {
@@ -976,9 +1096,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       const size_t part_floats = size_t(kTile) * DP + 2 * kTile;
       if (p.part < 0) {
         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-        const bool store = valid && ASV_GUARD(a, tok_row >= 0 && tok_row < c.N && head < a.q_heads);
+        const bool store = valid && stores && ASV_GUARD(a, tok_row >= 0 && tok_row < c.N && head < a.q_heads);
         uint16_t* out = a.out.p + tok_row * a.out.tok + head * a.out.head;
-        if (any) {
+        if (any && stores) {
           constexpr int kCols = NT == 1 ? 32 : 64;
 #pragma unroll 1
           for (int i = 0; i < DP; i += kCols) {
@@ -1025,7 +1145,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       } else {
         // file the partial result: [column / 4][row] float4, then (reference, sum) per row
         float* part = a.parts + (size_t(p.part) * 2 + wg) * part_floats;
-        if (any) {
+        if (any && stores) {
 #pragma unroll 1
           for (int i = 0; i < DP / 32; ++i) {
             __syncwarp();
@@ -1043,7 +1163,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
                        make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]));
             }
           }
-          if (valid && ASV_GUARD(a, p.part < kPagedSlots))
+          if (valid && stores && ASV_GUARD(a, p.part < kPagedSlots))
             __stcg(reinterpret_cast<float2*>(part + kTile * DP) + row, make_float2(ref, sum));
         }
       }
@@ -1213,10 +1333,11 @@ cudaError_t make_map(CUtensorMap* m, bool bf16, void* base, int rank, const cuui
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool BF16, int DP, int NT>
+template <bool BF16, int DP, int NT, bool DIV>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, int dev, cudaStream_t s) {
-  auto kernel = paged_attention_kernel<BF16, DP, NT>;
-  constexpr int kSmem = 1024 + (2 + kRingSlots<DP>) * kTile * DP * 2 + int(sizeof(Misc));
+  auto kernel = paged_attention_kernel<BF16, DP, NT, DIV>;
+  constexpr int kSmem = 1024 + (2 + kRingSlots<DP, DIV>) * kTile * DP * 2 + int(kExchangeBytes<DIV>) +
+                        int(sizeof(Misc) + (DIV ? sizeof(Divided) : 0));
   static_assert(kSmem <= 232448, "shared memory");
   // a programmatic launch: the set-up runs while the launch before it ends
   cudaLaunchConfig_t cfg = {};
@@ -1254,7 +1375,11 @@ cudaError_t launch_paged_attention(const AttendArgs& args, int dtype, cudaStream
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64) return cudaErrorInvalidDevice;
-  a.tile_tokens = kTile / a.group;
+  // two row tiles to an item where the average chunk has more rows than one tile holds; a divided one where (as far as
+  // the host can tell) every chunk has at most 32 rows
+  const bool two = (long long)c.N * a.group > (long long)kTile * c.B;
+  const bool div = c.N % c.B == 0 && (long long)c.N * a.group <= 32ll * c.B;
+  a.tile_tokens = (div ? 32 : kTile) / a.group;
   a.box = std::min(kTile, c.page_size & -c.page_size);
   CUtensorMap maps[3];
   const cuuint64_t qd[3] = {cuuint64_t(c.head_dim), cuuint64_t(a.q_heads), cuuint64_t(c.N)};
@@ -1268,18 +1393,20 @@ cudaError_t launch_paged_attention(const AttendArgs& args, int dtype, cudaStream
   if ((e = make_map(&maps[1], bf16, c.k, 4, kd, ks, kb)) != cudaSuccess) return e;
   if ((e = make_map(&maps[2], bf16, c.v, 4, kd, vs, kb)) != cudaSuccess) return e;
   const int grid = std::min(sms, kPagedMaxGrid);
-  // two row tiles to an item where the average chunk has more rows than one tile holds
-  const bool two = (long long)c.N * a.group > (long long)kTile * c.B;
-  const int which = (bf16 ? 4 : 0) + (c.head_dim > 64 ? 2 : 0) + (two ? 1 : 0);
+  const int which = (bf16 ? 6 : 0) + (c.head_dim > 64 ? 3 : 0) + (two ? 1 : div ? 2 : 0);
   switch (which) {
-    case 0: return launch<false, 64, 1>(a, maps, grid, dev, s);
-    case 1: return launch<false, 64, 2>(a, maps, grid, dev, s);
-    case 2: return launch<false, 128, 1>(a, maps, grid, dev, s);
-    case 3: return launch<false, 128, 2>(a, maps, grid, dev, s);
-    case 4: return launch<true, 64, 1>(a, maps, grid, dev, s);
-    case 5: return launch<true, 64, 2>(a, maps, grid, dev, s);
-    case 6: return launch<true, 128, 1>(a, maps, grid, dev, s);
-    default: return launch<true, 128, 2>(a, maps, grid, dev, s);
+    case 0: return launch<false, 64, 1, false>(a, maps, grid, dev, s);
+    case 1: return launch<false, 64, 2, false>(a, maps, grid, dev, s);
+    case 2: return launch<false, 64, 1, true>(a, maps, grid, dev, s);
+    case 3: return launch<false, 128, 1, false>(a, maps, grid, dev, s);
+    case 4: return launch<false, 128, 2, false>(a, maps, grid, dev, s);
+    case 5: return launch<false, 128, 1, true>(a, maps, grid, dev, s);
+    case 6: return launch<true, 64, 1, false>(a, maps, grid, dev, s);
+    case 7: return launch<true, 64, 2, false>(a, maps, grid, dev, s);
+    case 8: return launch<true, 64, 1, true>(a, maps, grid, dev, s);
+    case 9: return launch<true, 128, 1, false>(a, maps, grid, dev, s);
+    case 10: return launch<true, 128, 2, false>(a, maps, grid, dev, s);
+    default: return launch<true, 128, 1, true>(a, maps, grid, dev, s);
   }
 }
 
