@@ -57,10 +57,11 @@ constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the r
 template <int NT>
 constexpr int kThreadsOf = 32 * (4 * NT + 4);
 
-// Slots of the ring of keys and values: what shared memory holds next to two tiles of queries (and the weights that the
-// warps of a divided row tile exchange).
-template <int DP, bool DIV>
-constexpr int kRingSlots = DP == 128 ? (DIV ? 4 : 5) : (DIV ? 8 : 10);
+// Slots of the ring of keys and values.  Five of 32 KB are what shared memory holds next to two tiles of queries; where
+// the copies are what bounds (NT = 1), two tiles ahead are enough and go faster (256 requests, one token: 102.6 us, 105
+// with five; NT = 2, 4 x 2048 tokens: 5 % slower with four).
+template <int DP, int NT>
+constexpr int kRingSlots = (NT == 1 ? 4 : 5) * (128 / DP);
 constexpr uint32_t kChunkBytes = 32 * 32 * 2;  // weights of 32 rows for 32 positions: [8 positions][row] vectors
 template <bool DIV>
 constexpr uint32_t kExchangeBytes = DIV ? 2 * 4 * kChunkBytes : 0;
@@ -155,8 +156,10 @@ struct Items {
   }
   // units of one key head before item i
   __device__ long long before(int window, int cost, int i) const { return kTileCost * tiles_before(window, i) + (long long)cost * i; }
+  // units of all (most requests have one item to a key head, or none)
   __device__ long long units(int window, int cost, int kv_heads) const {
-    return n == 0 ? 0 : kv_heads * (before(window, cost, n - 1) + kTileCost * (long long)tiles(window, n - 1) + cost);
+    const long long last = kTileCost * (long long)tiles(window, max(n - 1, 0)) + cost;
+    return n == 0 ? 0 : kv_heads * (n == 1 ? last : last + before(window, cost, n - 1));
   }
 };
 
@@ -167,7 +170,8 @@ __device__ Items load_items(const PagedView& c, int b, int T) {
   it.shift = (T & (T - 1)) == 0 ? 31 - __clz(T) : -1;
   // the rows of a request that is left out are still zeroed, where they are rows
   const bool rows = it.r.start >= 0 && it.r.start <= it.r.end && it.r.end <= c.N;
-  it.n = rows ? (it.r.end - it.r.start + T - 1) / T : 0;
+  const int len = rows ? it.r.end - it.r.start : 0;
+  it.n = len <= T ? (len > 0 ? 1 : 0) : it.shift >= 0 ? ((len - 1) >> it.shift) + 1 : (len - 1) / T + 1;
   return it;
 }
 
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   static_assert(NT == 1 || !DIV);
-  constexpr int kRing = kRingSlots<DP, DIV>;
+  constexpr int kRing = kRingSlots<DP, NT>;
   constexpr int kHalves = DP / 64;                // 64-element column blocks, 128 bytes a row
   constexpr uint32_t kTileBytes = kTile * DP * 2;
   constexpr uint32_t kHalfBytes = kTile * 128;
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
 
   if (warp == kWalkWarp) {
     const int cost = item_cost<NT>(c);
-    // ---- scheduler: the lanes sum up their shares of the requests; the one whose share the run starts in walks it
+    // ---- scheduler: the lanes sum up their shares of the requests, find where the run starts, and one walks it
     const int per_lane = (c.B + 31) / 32, b0 = min(lane * per_lane, c.B), b1 = min(b0 + per_lane, c.B);
     long long own = 0;
     Items it;
@@ -413,31 +417,37 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
     if (lane == 0) ms.per_cta = per_cta;
     __syncwarp();
-    if (u0 < u1 ? u0 >= before && u0 < before + own : lane == 0) {
-      int b = c.B, i = 0, n = 0, h = 0;
-      long long item0 = u0;
-      if (u0 < u1) {
-        for (b = b0;; ++b) {
-          if (per_lane > 1) {
-            it = load_items(c, b, T);
-            own = it.units(a.window, cost, c.kv_heads);
-          }
-          if (u0 < before + own) break;
-          before += own;
+    // the request and the item that hold unit u0 (none: the end of the run)
+    int b = c.B, i = 0, n = 0, h = 0;
+    long long item0 = u0;
+    const uint32_t has = __ballot_sync(0xffffffffu, u0 < u1 && u0 >= before && u0 < before + own);
+    if (has != 0) {
+      const int lane_of = __ffs(has) - 1;
+      if (lane == lane_of) {
+        for (b = b0; b + 1 < b1; ++b) {
+          const long long units = load_items(c, b, T).units(a.window, cost, c.kv_heads);
+          if (u0 < before + units) break;
+          before += units;
         }
-        // the item that holds unit u0: the last with no more than rel units before it
-        const long long rel = u0 - before;
-        for (int hi = it.n; hi - i > 1;) {
-          const int mid = (i + hi) / 2;
-          if (c.kv_heads * it.before(a.window, cost, mid) <= rel) i = mid;
-          else hi = mid;
-        }
-        n = it.tiles(a.window, i);
-        item0 = before + c.kv_heads * it.before(a.window, cost, i);
-        const long long units = (long long)n * kTileCost + cost;
-        h = int(quotient(u0 - item0, units));
-        item0 += h * units;
       }
+      b = __shfl_sync(0xffffffffu, b, lane_of);
+      before = __shfl_sync(0xffffffffu, before, lane_of);
+      it = load_items(c, b, T);
+      // the last item with no more than rel units before it: 32 candidates at a time
+      const long long rel = u0 - before;
+      for (int end = it.n; end - i > 1;) {
+        const int step = (end - i + 31) / 32, k = i + lane * step;
+        const bool below = k < end && c.kv_heads * it.before(a.window, cost, min(k, end - 1)) <= rel;
+        i += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
+        end = min(i + step, end);
+      }
+      n = it.tiles(a.window, i);
+      item0 = before + c.kv_heads * it.before(a.window, cost, i);
+      const long long units = (long long)n * kTileCost + cost;
+      h = int(quotient(u0 - item0, units));
+      item0 += h * units;
+    }
+    if (lane == 0) {
       Ring ring_p;
       for (;;) {
         // its first `cost` units are its own, then come its key tiles': a tile is the CTA's that has its last unit
@@ -1336,7 +1346,7 @@ cudaError_t make_map(CUtensorMap* m, bool bf16, void* base, int rank, const cuui
 template <bool BF16, int DP, int NT, bool DIV>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap* maps, int grid, int dev, cudaStream_t s) {
   auto kernel = paged_attention_kernel<BF16, DP, NT, DIV>;
-  constexpr int kSmem = 1024 + (2 + kRingSlots<DP, DIV>) * kTile * DP * 2 + int(kExchangeBytes<DIV>) +
+  constexpr int kSmem = 1024 + (2 + kRingSlots<DP, NT>) * kTile * DP * 2 + int(kExchangeBytes<DIV>) +
                         int(sizeof(Misc) + (DIV ? sizeof(Divided) : 0));
   static_assert(kSmem <= 232448, "shared memory");
   // a programmatic launch: the set-up runs while the launch before it ends
