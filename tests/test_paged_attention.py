@@ -70,6 +70,17 @@ def test_ragged_batches(asv, seed):
                       dtype=[torch.bfloat16, torch.float16][seed % 2]))
 
 
+@pytest.mark.parametrize("group,q_lens,past", [
+    (32, [1, 1], [257, 0]), (10, [3, 3, 3], [130, 1200, 61]), (10, [6, 0, 3, 3], [130, 5, 0, 1000]), (1, [40, 24], [0, 300]),
+    (5, [7, 5, 6], [96, 129, 31]), (31, [1] * 5, [0, 31, 32, 33, 640]), (12, [2, 2], [2000, 127]), (3, [10], [4000]),
+])
+@pytest.mark.parametrize("window", [0, 70])
+def test_few_rows(asv, group, q_lens, past, window):
+    """At most 32 rows to an item on average: the warps divide a tile's positions among them."""
+    for dim, dtype in ((128, torch.bfloat16), (64, torch.float16), (40, torch.bfloat16)):
+        _check(asv, Batch(q_lens, past, heads=(2 * group, 2), dim=dim, page=24, dtype=dtype, seed=group), window=window)
+
+
 def test_long_split_context(asv):
     """Few rows over many keys: the work of one request is split and joined."""
     _check(asv, Batch([2], [9000], heads=(2, 1), dim=128, page=64, seed=1))
@@ -91,8 +102,9 @@ def test_peaked_and_flat_scores(asv, gain, scale):
     _check(asv, Batch([4, 40], [500, 260], heads=(4, 2), dim=64, gain=gain, seed=9), scale=scale)
 
 
-def test_rising_scores_move_the_maximum_in_every_tile(asv):
-    b = Batch([3], [1200], heads=(4, 2), dim=64, seed=11)
+@pytest.mark.parametrize("heads", [(4, 2), (20, 2), (64, 2)])
+def test_rising_scores_move_the_maximum_in_every_tile(asv, heads):
+    b = Batch([3], [1200], heads=heads, dim=64, seed=11)
     ramp = torch.linspace(0, 8, 1203)[:, None, None]
     b.q = b.q.abs().clamp(min=0.25)
     b.k[0] = (b.k[0].abs().float() * ramp).to(b.dtype)
@@ -144,7 +156,8 @@ def test_nan_where_no_token_looks(asv):
             assert_within(got.out[other], want[0][other], want[2][other], "the other request")
 
 
-@pytest.mark.parametrize("heads,q_lens", [((4, 1), [300, 20, 150]), ((2, 2), [260, 257, 5, 390])])
+@pytest.mark.parametrize("heads,q_lens", [((4, 1), [300, 20, 150]), ((2, 2), [260, 257, 5, 390]), ((4, 1), [6, 6, 3, 9]),
+                                          ((30, 2), [2, 2])])
 def test_nan_in_later_tokens_of_long_chunks(asv, heads, q_lens):
     """The last third of every chunk holds NaN keys and values: the tokens before it are left alone, whichever
     row tiles and items they share with it, and every one from there on is NaN."""
