@@ -7,25 +7,33 @@
 // Rows.  The query heads of a key head read the same keys, so a row tile of 128 rows holds
 // floor(128 / G) tokens x G heads, and an item is (request, NT row tiles, key head): NT = 1 where a
 // request's chunk fits one tile, NT = 2 for longer chunks (each key and value tile then serves 256 rows,
-// which halves what a CTA reads from L2 per multiplication).
+// which halves what a CTA reads from L2 per multiplication).  With at most 32 rows to an item the row tile is
+// divided (DIV): it holds the 32 rows four times, and each softmax warp takes 32 of a tile's 128 positions
+// instead of one warp all of them (a warp can only reach 32 rows of tensor memory).
 //
-// Split.  An item costs as many units as it has key tiles of 128 positions.  The units of all items, in
-// order, are cut into equal runs, one for each CTA (one CTA per SM), so a batch of any lengths keeps every
-// SM busy to the end; the prefix sums need only indptr and cache_len and a closed form per request, and
-// every CTA computes them.  An item that a cut goes through is finished from partial results (unnormalised
-// outputs, reference, sum) in the workspace by the CTA that files the last of them, in CTA order, so the
-// result does not depend on timing.
+// Split.  An item costs units: four for each key tile of 128 positions and about two tiles' for itself.  The
+// units of all items, in order, are cut into equal runs, one for each CTA (one CTA per SM), so a batch of any
+// lengths keeps every SM busy to the end; the prefix sums need only indptr and cache_len and a closed form per
+// request, and a warp of every CTA computes them.  An item that a cut goes through is finished from partial
+// results (unnormalised outputs, reference, sum) in the workspace by the CTA that files the last of them, in CTA
+// order, so the result does not depend on timing.
 //
 // In a CTA, warps take roles that hand over through mbarriers:
-//   scheduler  walks the CTA's run and describes its pieces in a queue
-//   copies     one box of the tensor map per page (part), 128-byte swizzled, into a ring of key / value
-//              tiles; positions that no row of the item attends to are not read (zero fill)
+//   scheduler  finds the CTA's run, walks it and describes its pieces in a queue
+//   copies     (two warps: keys; queries and values) one box of the tensor map per page (part), 128-byte swizzled,
+//              into a ring of key / value tiles; positions that no row of the item attends to are not read (zero
+//              fill)
 //   matrices   S = Q K^T into tensor memory; out += P V with P taken from tensor memory
 //   softmax    one thread per row: S to registers, reference, 2^x, P back over S in the 16-bit type; the
 //              outputs are rescaled only when the reference moves by more than 2^8, so seldom after the
 //              first tiles; the epilogue divides and stores
 // NT = 1 keeps two S and two output buffers, so the next tile's S is formed while the softmax runs; NT = 2
 // gives each row tile one, and the two tiles alternate.
+//
+// Measured (bf16, heads of 128, one call among others): 64 requests x 3 tokens over 500 .. 12,000, 64 / 8 heads,
+// 147 - 150 us, bound by HBM (6.2 TB/s); 256 x 1 token over 1 .. 4096 (fp16) 99 us, 506 MB, items of four tiles;
+// 4 x 2048 tokens over 8192, 32 / 8 heads, 620 - 690 us by the clock that the power limit leaves, 1.5 PFLOP/s at the
+// best, bound by each row tile's chain S, softmax, P V; 1 token over 4096, 10.7 us, all latency.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
