@@ -11,7 +11,7 @@
 // divided (DIV): it holds the 32 rows four times, and each softmax warp takes 32 of a tile's 128 positions
 // instead of one warp all of them (a warp can only reach 32 rows of tensor memory).
 //
-// Split.  An item costs units: four for each key tile of 128 positions and about two tiles' for itself.  The
+// Split.  An item costs as many units as it has key tiles of 128 positions, and one or two for itself.  The
 // units of all items, in order, are cut into equal runs, one for each CTA (one CTA per SM), so a batch of any
 // lengths keeps every SM busy to the end; the prefix sums need only indptr and cache_len and a closed form per
 // request, and a warp of every CTA computes them.  An item that a cut goes through is finished from partial
@@ -50,14 +50,12 @@ using namespace tc;
 constexpr int kTile = 128;  // rows of a row tile; positions of a key tile
 constexpr int kQueue = 16;  // pieces ahead: of 4, short items left the copies waiting for the scheduler (2 % at 6 prompts)
 constexpr uint32_t kTmemColumns = 512;  // S buffers at 0 and 128, outputs at 256 and 384
-// Units of the split that a key tile is worth, and an item's own work (queries in, outputs out, the pipeline's
-// fill): two tiles where a CTA has an item or so, which keeps the cuts at whole tiles (one request, one token: 11.1 us,
-// with 7 units 11.6); a little less where it has many short ones (256 requests, one token: 105 us, 107.7 with 8, 110
-// with 5 or 10).
-constexpr int kTileCost = 4;
-template <int NT>
+// Key tiles that an item's own work (queries in, outputs out, the pipeline's fill) is worth in the split: one for the
+// divided row tile of many short items (256 requests, one token: 95.3 us, 100 with 1.75, 97.5 with 1.5; undivided it
+// took 107 with two, 121 with one), else two (one request, one token: 10.6 us, 11.1 with one).
+template <bool DIV>
 __device__ int item_cost(const PagedView& c) {
-  return NT == 1 && (long long)c.B * c.kv_heads > gridDim.x ? 7 : 8;
+  return DIV && (long long)c.B * c.kv_heads > gridDim.x ? 1 : 2;
 }
 constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
 
@@ -163,10 +161,10 @@ struct Items {
     return i == 0 ? 0 : r.ok ? sum_before(r.past, T, shift, window, i) : i;
   }
   // units of one key head before item i
-  __device__ long long before(int window, int cost, int i) const { return kTileCost * tiles_before(window, i) + (long long)cost * i; }
+  __device__ long long before(int window, int cost, int i) const { return tiles_before(window, i) + (long long)cost * i; }
   // units of all (most requests have one item to a key head, or none)
   __device__ long long units(int window, int cost, int kv_heads) const {
-    const long long last = kTileCost * (long long)tiles(window, max(n - 1, 0)) + cost;
+    const long long last = (long long)tiles(window, max(n - 1, 0)) + cost;
     return n == 0 ? 0 : kv_heads * (n == 1 ? last : last + before(window, cost, n - 1));
   }
 };
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == kWalkWarp) {
-    const int cost = item_cost<NT>(c);
+    const int cost = item_cost<DIV>(c);
     // ---- scheduler: the lanes sum up their shares of the requests, find where the run starts, and one walks it
     const int per_lane = (c.B + 31) / 32, b0 = min(lane * per_lane, c.B), b1 = min(b0 + per_lane, c.B);
     long long own = 0;
@@ -419,9 +417,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     }
     const long long total = __shfl_sync(0xffffffffu, before, 31);
     before -= own;
-    // (whole tiles: where a run has few of them, an item begins that much sooner)
-    const long long per_cta =
-        max(quotient(total + gridDim.x * kTileCost - 1, gridDim.x * kTileCost), 1ll) * kTileCost;
+    const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
     const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
     if (lane == 0) ms.per_cta = per_cta;
     __syncwarp();
@@ -451,16 +447,16 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       }
       n = it.tiles(a.window, i);
       item0 = before + c.kv_heads * it.before(a.window, cost, i);
-      const long long units = (long long)n * kTileCost + cost;
+      const long long units = (long long)n + cost;
       h = int(quotient(u0 - item0, units));
       item0 += h * units;
     }
     if (lane == 0) {
       Ring ring_p;
       for (;;) {
-        // its first `cost` units are its own, then come its key tiles': a tile is the CTA's that has its last unit
-        const int ta = int(max(u0 - item0 - cost, 0ll) / kTileCost);
-        const int tb = int(min(max(u1 - item0 - cost, 0ll) / kTileCost, (long long)n));
+        // its first `cost` units are its own, then one for each key tile
+        const int ta = int(max(u0 - item0 - cost, 0ll));
+        const int tb = int(min(max(u1 - item0 - cost, 0ll), (long long)n));
         const bool end = b >= c.B || item0 >= u1;
         if (end || tb > ta) {
           if (!bar_wait(at(ms.piece_empty, ring_p.slot), ring_p.phase ^ 1, abort)) break;
@@ -484,7 +480,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
           ring_p.next(kQueue);
         }
         if (end) break;
-        item0 += (long long)n * kTileCost + cost;
+        item0 += n + cost;
         if (++h == c.kv_heads) {
           h = 0;
           if (++i == it.n) {
@@ -1086,8 +1082,8 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       int first_cta = 0, n_parts = 1;  // the CTAs that have parts of the item
       if (p.part >= 0) {
         const long long per_cta = ms.per_cta;
-        first_cta = int(quotient(p.item + kTileCost - 1, per_cta));
-        n_parts = int(quotient(p.item + (long long)p.item_tiles * kTileCost - 1, per_cta)) - first_cta + 1;
+        first_cta = int(quotient(p.item, per_cta));
+        n_parts = int(quotient(p.item + p.item_tiles - 1, per_cta)) - first_cta + 1;
       }
       const int n_rows = ntok * a.group;
       const int tok_row = p.tok0 + first_tok + tok;
