@@ -186,7 +186,7 @@ struct Misc {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[4], pv_done[2], o_full[2], o_empty[2];
   uint64_t piece_full[kQueue], piece_empty[kQueue], wg_sync[2];
   Piece piece[kQueue];
-  long long per_cta;  // units of a run
+  long long units;  // of all runs
   uint32_t tmem;
   int abort;
   int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
@@ -417,9 +417,20 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     }
     const long long total = __shfl_sync(0xffffffffu, before, 31);
     before -= own;
-    const long long per_cta = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
-    const long long u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, total);
-    if (lane == 0) ms.per_cta = per_cta;
+    // The runs: c * units / grid up to (c + 1) * units / grid, rounded down.  Short ones are made of one length (units
+    // rounded up), which cuts the items into fewer parts (one request, one token: 10.7 us, 11.8 with runs of one and
+    // two units); long ones would leave the last CTAs idle (256 requests: 94.1 us, 95.4).
+    const int grid = gridDim.x;
+    const long long run = quotient(max(total, 1ll) + grid - 1, grid);
+    long long units = run * grid, u0 = blockIdx.x * run, u1 = u0 + run;
+    if (run > 16) {
+      units = total;
+      u0 = quotient(blockIdx.x * units, grid);
+      u1 = quotient((blockIdx.x + 1) * units, grid);
+    }
+    u0 = min(u0, total);
+    u1 = min(u1, total);
+    if (lane == 0) ms.units = units;
     __syncwarp();
     // the request and the item that hold unit u0 (none: the end of the run)
     int b = c.B, i = 0, n = 0, h = 0;
@@ -1081,9 +1092,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       // ---- epilogue
       int first_cta = 0, n_parts = 1;  // the CTAs that have parts of the item
       if (p.part >= 0) {
-        const long long per_cta = ms.per_cta;
-        first_cta = int(quotient(p.item, per_cta));
-        n_parts = int(quotient(p.item + p.item_tiles - 1, per_cta)) - first_cta + 1;
+        const long long units = ms.units;
+        first_cta = int(quotient((p.item + 1) * gridDim.x - 1, units));
+        n_parts = int(quotient((p.item + p.item_tiles) * gridDim.x - 1, units)) - first_cta + 1;
       }
       const int n_rows = ntok * a.group;
       const int tok_row = p.tok0 + first_tok + tok;
