@@ -27,8 +27,8 @@
 //   softmax    one thread per row: S to registers, reference, 2^x, P back over S in the 16-bit type; the
 //              outputs are rescaled only when the reference moves by more than 2^8, so seldom after the
 //              first tiles; the epilogue divides and stores
-// NT = 1 keeps two S and two output buffers, so the next tile's S is formed while the softmax runs; NT = 2
-// gives each row tile one, and the two tiles alternate.
+// NT = 1 keeps two S and two output buffers, so the next tile's S is formed while the softmax runs, and has a warp
+// for each kind of product; NT = 2 gives each row tile one, and the two tiles alternate.
 //
 // Measured (bf16, heads of 128, one call among others): 64 requests x 3 tokens over 500 .. 12,000, 64 / 8 heads,
 // 147 - 150 us, bound by HBM (6.2 TB/s); 256 x 1 token over 1 .. 4096 (fp16) 99 us, 506 MB, items of four tiles;
@@ -59,9 +59,10 @@ __device__ int item_cost(const PagedView& c) {
 }
 constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
 
-// Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler.
+// Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler; with one row tile
+// the products P V have a warp of their own.
 template <int NT>
-constexpr int kThreadsOf = 32 * (4 * NT + 4);
+constexpr int kThreadsOf = 32 * (4 * NT + 4 + (NT == 1 ? 1 : 0));
 
 // Slots of the ring of keys and values.  Five of 32 KB are what shared memory holds next to two tiles of queries; where
 // the copies are what bounds (NT = 1), two tiles ahead are enough and go faster (256 requests, one token: 102.6 us, 105
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       bar_init(at(ms.piece_full, i), 1);
-      bar_init(at(ms.piece_empty, i), 3 + 4 * NT);
+      bar_init(at(ms.piece_empty, i), 3 + 4 * NT + (NT == 1 ? 1 : 0));
     }
     ms.abort = 0;
     fence_barrier_init();
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         }
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp || warp > kWalkWarp) {
     // ---- matrices
     Ring ring_p, ring_k, ring_v, ring_q;  // a tile's keys and values take two slots of the ring, one after the other
     ring_v.next(kRing);
@@ -757,88 +758,68 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         ring_q.next(1);
       }
     } else {
-      // Tile by tile over the pieces: S of the next tile before the product of this one, unless a new item's keys
-      // are still on their way.
-      int used[2] = {0, 0};   // S / P buffer uses so far
-      int items[2] = {0, 0};  // output buffer uses so far
-      int ob = 1, tile_no = 0;
-      Span prev = {0, 0, 0, 0};
-      int prev_ob = 0, prev_sb = 0;
-      bool have_prev = false, prev_first = false, prev_last = false, ok = true;
+      // One warp forms S of every tile, the other its product: a tile costs a warp three waits and as many signals
+      // next to its instructions (one warp in turn for both: 2100 cycles a tile, of which instructions run 1024).
       Piece p;
-      p.t0 = p.t1 = p.kind = 0;
-      int t = 0;
-      while (ok) {
-        while (t == p.t1 && p.kind == 0 && ok) {
-          ok = next_piece(p);
-          t = p.t0;
-        }
-        if (!ok) break;
-        const bool more = p.kind == 0, first = t == p.t0, last = t == p.t1 - 1;
-        const int sb = tile_no & 1;
-        auto qk_tile = [&]() {
-          if (!warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort)) return false;
-          if (first) {
-            if (!warp_wait(at(ms.q_full, ring_q.slot), ring_q.phase, abort)) return false;
-            ob ^= 1;
-          }
-          fence_after();
-          if (elect()) {
-            qk(sb, ring_q.slot, ring_k.slot);
-            commit(at(ms.s_full, sb));
-            commit(at(ms.kv_empty, ring_k.slot));
-            if (last) commit(at(ms.q_empty, ring_q.slot));
-          }
-          __syncwarp();
-          ++used[sb];
-          ring_k.next(kRing, 2);
-          if (last) ring_q.next(2);
-          return true;
-        };
-        // the output buffer (and its poison mark) is free; the weights come in two halves (qk_tile counts a use of
-        // the other buffer, so prev's parity is its own)
-        auto pv_tile = [&]() {
-          if (prev_first && !warp_wait(at(ms.o_empty, prev_ob), (items[prev_ob] & 1) ^ 1, abort)) return false;
-          if (!take_values(ring_v, prev, prev_ob, prev_ob)) return false;
-          const uint32_t p_phase = (used[prev_sb] & 1) ^ 1;
-          const bool whole = prev.whole();
-          constexpr int kFirst = DIV ? 0 : 4;  // steps taken with the first half
-          if constexpr (!DIV) {
-            if (!warp_wait(at(ms.p_full, 2 * prev_sb), p_phase, abort)) return false;
+      uint32_t tiles = 0, pieces = 0;
+      if (warp == kMmaWarp) {
+        for (bool ok = true; ok && next_piece(p) && p.kind == 0;) {
+          for (int t = p.t0; t < p.t1; ++t) {
+            const int sb = tiles & 1;
+            ok = warp_wait(at(ms.kv_full, ring_k.slot), ring_k.phase, abort) &&
+                 (t > p.t0 || warp_wait(at(ms.q_full, ring_q.slot), ring_q.phase, abort)) &&
+                 warp_wait(at(ms.pv_done, sb), ((tiles >> 1) & 1) ^ 1, abort);  // the weights there before are used
+            if (!ok) break;
             fence_after();
-            if (whole && elect()) pv_run(prev_ob, prev_sb, ring_v.slot, 0, prev_first, std::integral_constant<int, kFirst>());
+            if (elect()) {
+              qk(sb, ring_q.slot, ring_k.slot);
+              commit(at(ms.s_full, sb));
+              commit(at(ms.kv_empty, ring_k.slot));
+              if (t == p.t1 - 1) commit(at(ms.q_empty, ring_q.slot));
+            }
             __syncwarp();
+            ++tiles;
+            ring_k.next(kRing, 2);
           }
-          if (!warp_wait(at(ms.p_full, 2 * prev_sb + 1), p_phase, abort)) return false;
-          fence_after();
-          if (elect()) {
-            if (whole)
-              pv_run(prev_ob, prev_sb, ring_v.slot, kFirst, DIV && prev_first, std::integral_constant<int, 8 - kFirst>());
-            else pv_steps(prev_ob, prev_sb, ring_v.slot, prev_first, prev.first_step(), prev.end_step());
-            commit(at(ms.pv_done, prev_sb));
-            commit(at(ms.kv_empty, ring_v.slot));
-            if (prev_last) commit(at(ms.o_full, prev_ob));
+          if (p.t0 < p.t1) ring_q.next(2);
+        }
+      } else {
+        for (bool ok = true; ok && next_piece(p) && p.kind == 0;) {
+          const int ob = pieces & 1;
+          // the output buffer (and its poison mark) is free
+          if (p.t0 < p.t1) {
+            ok = warp_wait(at(ms.o_empty, ob), ((pieces >> 1) & 1) ^ 1, abort);
+            ++pieces;
           }
-          __syncwarp();
-          if (prev_last) ++items[prev_ob];
-          ring_v.next(kRing, 2);
-          return true;
-        };
-        const bool early = more && (!first || __all_sync(0xffffffffu, bar_test(at(ms.kv_full, ring_k.slot), ring_k.phase) &&
-                                                                          bar_test(at(ms.q_full, ring_q.slot), ring_q.phase)));
-        if (early) ok = qk_tile();
-        if (ok && have_prev) ok = pv_tile();
-        if (ok && more && !early) ok = qk_tile();
-        if (!ok) break;
-        if (!more) break;
-        prev = Span{t * kTile, p.pos0, p.kv_lo, p.pos0 + p.ntok};
-        prev_sb = sb;
-        prev_ob = ob;
-        prev_first = first;
-        prev_last = last;
-        have_prev = true;
-        ++tile_no;
-        ++t;
+          for (int t = p.t0; t < p.t1 && ok; ++t) {
+            const int sb = tiles & 1;
+            const bool first = t == p.t0;
+            const Span g = {t * kTile, p.pos0, p.kv_lo, p.pos0 + p.ntok};
+            constexpr int kFirst = DIV ? 0 : 4;  // steps taken with the first half of the weights
+            const bool whole = g.whole();
+            ok = take_values(ring_v, g, ob, ob);
+            if constexpr (!DIV) {
+              ok = ok && warp_wait(at(ms.p_full, 2 * sb), (tiles >> 1) & 1, abort);
+              if (!ok) break;
+              fence_after();
+              if (whole && elect()) pv_run(ob, sb, ring_v.slot, 0, first, std::integral_constant<int, kFirst>());
+              __syncwarp();
+            }
+            ok = ok && warp_wait(at(ms.p_full, 2 * sb + 1), (tiles >> 1) & 1, abort);
+            if (!ok) break;
+            fence_after();
+            if (elect()) {
+              if (whole) pv_run(ob, sb, ring_v.slot, kFirst, DIV && first, std::integral_constant<int, 8 - kFirst>());
+              else pv_steps(ob, sb, ring_v.slot, first, g.first_step(), g.end_step());
+              commit(at(ms.pv_done, sb));
+              commit(at(ms.kv_empty, ring_v.slot));
+              if (t == p.t1 - 1) commit(at(ms.o_full, ob));
+            }
+            __syncwarp();
+            ++tiles;
+            ring_v.next(kRing, 2);
+          }
+        }
       }
     }
   } else {
