@@ -26,7 +26,8 @@ constexpr int kThreads = 256;
 enum Pairing {
   kPlain,     // a vector a task; pairs lie within it (interleaved), or nothing is rotated
   kHalves,    // vectors j and j + dim / 2 a task, and the vectors from dim on one by one
-  kScattered  // a vector a task, its partners fetched one by one (dim / 2 not whole vectors)
+  kFours,  // a vector a task, its partners fetched by four (dim / 2 a multiple of 4)
+  kScattered  // a vector a task, its partners fetched one by one
 };
 
 struct TokenPlace {
@@ -127,6 +128,23 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
           w[e] = pack2<BF16>(second_of(p0.x, p1.x, co.x, si.x), second_of(p0.y, p1.y, co.y, si.y));
         }
         *reinterpret_cast<uint4*>(dst + half + d) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if (PAIRING == kFours && d < a.rot_dim) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int at = d + 4 * g;
+          if (at < a.rot_dim) {
+            const bool low = at < half;
+            const int q = low ? at : at - half;
+            const uint2 y = __ldg(reinterpret_cast<const uint2*>(src + (low ? at + half : q)));
+            const float4 co = *reinterpret_cast<const float4*>(cs + q), si = *reinterpret_cast<const float4*>(cs + half + q);
+            auto turn = [&](float2 own, float2 other, float c0, float c1, float s0, float s1) {
+              return low ? pack2<BF16>(first_of(own.x, other.x, c0, s0), first_of(own.y, other.y, c1, s1))
+                         : pack2<BF16>(second_of(other.x, own.x, c0, s0), second_of(other.y, own.y, c1, s1));
+            };
+            u[2 * g] = turn(unpack2<BF16>(u[2 * g]), unpack2<BF16>(y.x), co.x, co.y, si.x, si.y);
+            u[2 * g + 1] = turn(unpack2<BF16>(u[2 * g + 1]), unpack2<BF16>(y.y), co.z, co.w, si.z, si.w);
+          }
+        }
       } else if (PAIRING != kHalves && d < a.rot_dim) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -193,11 +211,15 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-  const int pairing = a.rotary == nullptr || a.interleaved ? kPlain : a.rot_dim % 16 == 0 ? kHalves : kScattered;
+  const int pairing = a.rotary == nullptr || a.interleaved ? kPlain
+                      : a.rot_dim % 16 == 0                ? kHalves
+                      : a.rot_dim % 8 == 0                 ? kFours
+                                                           : kScattered;
   const bool bf16 = dtype == ASV_BF16;
   switch (pairing) {
     case kPlain: return bf16 ? launch<true, kPlain>(a, s) : launch<false, kPlain>(a, s);
     case kHalves: return bf16 ? launch<true, kHalves>(a, s) : launch<false, kHalves>(a, s);
+    case kFours: return bf16 ? launch<true, kFours>(a, s) : launch<false, kFours>(a, s);
     default: return bf16 ? launch<true, kScattered>(a, s) : launch<false, kScattered>(a, s);
   }
 }

@@ -58,7 +58,7 @@ def _check(asv, b, *, rot=None, interleaved=False, with_q=True, views=False, str
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("rot,interleaved", [(None, False), (64, False), (64, True), (32, False), (16, True),
-                                             (10, False), (6, True), (30, False), (2, False)])
+                                             (10, False), (6, True), (30, False), (2, False), (24, False), (56, False), (8, False)])
 def test_rotations(asv, dtype, rot, interleaved):
     b = Batch([3, 1, 0, 18, 40], [5, 0, 9, 16, 31], heads=(6, 2), dim=64, page=16, dtype=dtype, seed=3)
     _check(asv, b, rot=rot, interleaved=interleaved)
