@@ -200,12 +200,22 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // one token to a CTA until every SM has a dozen, then more of them share the search and the chain of loads
-  // (9216 tokens: 37 us at eight to a CTA, 45 at one)
-  const int tokens = a.c.N <= 2048 ? 1 : 8;
-  cfg.gridDim = dim3(unsigned((a.c.N + tokens - 1) / tokens), 1, 1);
-  return tokens == 1 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 1>, a)
-                     : cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 8>, a);
+  // More tokens to a CTA share the search and the chain of loads, fewer have more loads in flight: doubled up to eight
+  // while there are more than 13 CTAs to an SM, and up to sixteen while there are more than 8 and a CTA's threads have
+  // less than four vectors each (9216 tokens of 576 vectors: 44 us at one token to a CTA, 34 at eight; 3995 of 525: 21,
+  // 18.6 at two, 26 at eight; 15,713 of 60: 70, 17.8 at eight, 14.2 at sixteen).
+  const long long vectors = (long long)(a.q_heads + 2 * a.c.kv_heads) * (a.c.head_dim / 8);
+  int tokens = 1;
+  auto ctas = [&]() { return (a.c.N + tokens - 1) / tokens; };
+  while ((tokens < 8 && ctas() > 2048) || (tokens < 16 && ctas() > 1216 && tokens * vectors < 4 * kThreads)) tokens *= 2;
+  cfg.gridDim = dim3(unsigned(ctas()), 1, 1);
+  switch (tokens) {
+    case 1: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 1>, a);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 2>, a);
+    case 4: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 4>, a);
+    case 8: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 8>, a);
+    default: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 16>, a);
+  }
 }
 
 }  // namespace

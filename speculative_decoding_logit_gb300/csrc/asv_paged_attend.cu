@@ -23,17 +23,17 @@
 //   copies     (two warps: keys; queries and values) one box of the tensor map per page (part), 128-byte swizzled,
 //              into a ring of key / value tiles; positions that no row of the item attends to are not read (zero
 //              fill)
-//   matrices   S = Q K^T into tensor memory; out += P V with P taken from tensor memory
+//   matrices   S = Q K^T into tensor memory; out += P V with P taken from tensor memory (NT = 1: a warp each)
 //   softmax    one thread per row: S to registers, reference, 2^x, P back over S in the 16-bit type; the
 //              outputs are rescaled only when the reference moves by more than 2^8, so seldom after the
 //              first tiles; the epilogue divides and stores
-// NT = 1 keeps two S and two output buffers, so the next tile's S is formed while the softmax runs, and has a warp
-// for each kind of product; NT = 2 gives each row tile one, and the two tiles alternate.
+// NT = 1 keeps two S and two output buffers, so the next tile's S is formed while the softmax runs; NT = 2
+// gives each row tile one, and the two tiles alternate.
 //
 // Measured (bf16, heads of 128, one call among others): 64 requests x 3 tokens over 500 .. 12,000, 64 / 8 heads,
-// 147 - 150 us, bound by HBM (6.2 TB/s); 256 x 1 token over 1 .. 4096 (fp16) 99 us, 506 MB, items of four tiles;
-// 4 x 2048 tokens over 8192, 32 / 8 heads, 620 - 690 us by the clock that the power limit leaves, 1.5 PFLOP/s at the
-// best, bound by each row tile's chain S, softmax, P V; 1 token over 4096, 10.7 us, all latency.
+// 146 - 148 us, bound by HBM (6.3 TB/s); 256 x 1 token over 1 .. 4096 (fp16) 94 us, 507 MB; 4 x 2048 tokens over
+// 8192, 32 / 8 heads, 620 - 690 us by the clock that the power limit leaves, 1.5 PFLOP/s at the best, bound by each row
+// tile's chain S, softmax, P V; 1 token over 4096, 10.7 us, all latency.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

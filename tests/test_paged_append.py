@@ -73,6 +73,15 @@ def test_head_layouts(asv, dim, heads):
     _check(asv, b, rot=max(2, dim // 4 // 2 * 2), interleaved=True)
 
 
+@pytest.mark.parametrize("n", [1300, 2500, 5000, 10000])
+def test_many_tokens_of_few_heads(asv, n):
+    """From one to sixteen tokens to a CTA, which take in one request's end and several others."""
+    q_lens = [1, 0, 7, 2, 31, 3, 0, 0, 5, 1]
+    q_lens += [n - sum(q_lens) - 40, 37, 3]
+    b = Batch(q_lens, [(53 * i) % 90 for i in range(len(q_lens))], heads=(1, 1), dim=16, page=16, seed=n)
+    _check(asv, b, rot=8)
+
+
 @pytest.mark.parametrize("page", [8, 16, 48, 128, 256])
 def test_pages_and_single_tokens(asv, page):
     b = Batch([1] * 300, [(37 * i) % 300 for i in range(300)], heads=(2, 1), dim=16, page=page, seed=page)
