@@ -57,7 +57,7 @@ template <bool DIV>
 __device__ int item_cost(const PagedView& c) {
   return DIV && (long long)c.B * c.kv_heads > gridDim.x ? 1 : 2;
 }
-constexpr float kLazy = 8.0f;           // log2 units the maximum may pass the reference by
+constexpr float kLazy = 8.0f;  // log2 units the maximum may pass the reference by
 
 // Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler; with one row tile
 // the products P V have a warp of their own.
