@@ -1272,15 +1272,16 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              // (what is past the last is read again, with no weight)
+              // (what is past the last is read again and left out)
               const int at = min(k + e, n_parts - 1);
               const float4* part = reinterpret_cast<const float4*>(part_of(at)) + r;
-              w[e] = k + e < n_parts ? stats_of(at).x : -INFINITY;
+              w[e] = stats_of(at).x;
 #pragma unroll
               for (int i = 0; i < kCols; ++i) o[e][i] = ld_cg_f4(part + min(c0 + i, cols4 - 1) * kTile);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+              if (k + e >= n_parts) break;  // (not a weight of zero: the outputs may be infinite)
               w[e] = ex2_approx(w[e] - base) * inv;
 #pragma unroll
               for (int i = 0; i < kCols; ++i) acc[i] = add(acc[i], o[e][i], w[e]);
