@@ -592,6 +592,21 @@ def _raw_stream(t: torch.Tensor, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _made_on(stream, make):
+    """The tensors that make() allocates for a call on `stream` (None: the current one).  They are made there, so
+    that a zero-fill comes before the call and no block is taken that work on another stream still uses, and are
+    marked as used by the caller's stream, which will read them."""
+    if stream is None:
+        return make()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in made:
+        if t is not None:
+            t.record_stream(caller)
+    return made
+
+
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     block_table: torch.Tensor, cache_len: torch.Tensor, indptr: torch.Tensor, *,
                     q: Optional[torch.Tensor] = None, rotary: Optional[torch.Tensor] = None,
@@ -605,8 +620,9 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     handle = _raw_stream(k, stream)
     if out is None:
         dev = k.device
-        out = PagedAppendOutput(None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
-                                torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))
+        out = PagedAppendOutput(*_made_on(stream, lambda: (
+            None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
+            torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))))
     (_ext or _paged_ext()).paged_kv_append(k, v, k_cache, v_cache, block_table, cache_len, indptr, q, rotary,
                                            interleaved, out.q, out.req_status, handle)
     return out
@@ -645,9 +661,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     handle = _raw_stream(q, stream)
     if out is None:
         dev = q.device
-        out = PagedAttentionOutput(torch.empty(q.shape, dtype=q.dtype, device=dev),
-                                   torch.empty(q.shape[:2], dtype=torch.float32, device=dev),
-                                   torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))
+        out = PagedAttentionOutput(*_made_on(stream, lambda: (
+            torch.empty(q.shape, dtype=q.dtype, device=dev),
+            torch.empty(q.shape[:2], dtype=torch.float32, device=dev),
+            torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))))
     if workspace is None:
         workspace = _paged_ws_cache.get((q.get_device(), handle))
         if workspace is None:
