@@ -583,13 +583,17 @@ def _paged_ext():
     return _ext
 
 
-def _raw_stream(t: torch.Tensor, stream) -> int:
-    """The CUDA stream handle of `stream`, or of the current stream of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    if not t.is_cuda:
+def _raw_stream(t: torch.Tensor, stream) -> Optional[int]:
+    """The CUDA stream handle of `stream`, or of the current stream of t's device; None where that device is not the
+    current one (a launch goes to the current device)."""
+    dev = t.get_device()
+    if dev < 0:
         _need_cuda(t)
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream is not None and stream.device != t.device:
+        raise AsvError(2, "the stream must be one of the tensors' device")
+    if dev != torch._C._cuda_getDevice():
+        return None
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _made_on(stream, make):
@@ -618,6 +622,10 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     are rotated on the way, and the queries `q` into out.q (paged_kv_append in include/asv.h).
     cache_len is not advanced.  The caches take any strides with head rows contiguous."""
     handle = _raw_stream(k, stream)
+    if handle is None:
+        with torch.cuda.device(k.device):
+            return paged_kv_append(k, v, k_cache, v_cache, block_table, cache_len, indptr, q=q, rotary=rotary,
+                                   interleaved=interleaved, out=out, stream=stream)
     if out is None:
         dev = k.device
         out = PagedAppendOutput(*_made_on(stream, lambda: (
@@ -659,6 +667,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     `window` > 0 only the last `window` positions of each token (paged_attention in include/asv.h).
     cache_len [B] counts the tokens before the chunk; scale defaults to head_dim ** -0.5."""
     handle = _raw_stream(q, stream)
+    if handle is None:
+        with torch.cuda.device(q.device):
+            return paged_attention(q, k_cache, v_cache, block_table, cache_len, indptr, scale=scale, window=window,
+                                   out=out, workspace=workspace, stream=stream)
     if out is None:
         dev = q.device
         out = PagedAttentionOutput(*_made_on(stream, lambda: (

@@ -29,6 +29,8 @@ def traced(monkeypatch):
     monkeypatch.setattr(torch, "zeros", noting(torch.zeros))
     monkeypatch.setattr(torch, "empty", noting(torch.empty))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log.append(("record", s.name)))
+    monkeypatch.setattr(_binding, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
     call = lambda *a: log.append(("call", a[-1]))
     monkeypatch.setattr(_binding, "_ext", SimpleNamespace(paged_attention=call, paged_kv_append=call))
     return _binding, log
