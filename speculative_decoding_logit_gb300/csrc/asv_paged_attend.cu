@@ -58,6 +58,11 @@ __device__ int item_cost(const PagedView& c) {
   return DIV && (long long)c.B * c.kv_heads > gridDim.x ? 1 : 2;
 }
 constexpr float kLazy = 8.0f;  // log2 units the maximum may pass the reference by
+// Weights are 2^kLift times 2^(s - reference).  fp16 has no step below 2^-24, so next to a largest weight of 1 those below
+// 2^-25 would vanish from the product with the values (20 thousand of 2^-25.6 are 4e-4 of the sum); lifted by 2^7 the
+// largest, 2^(kLazy + 7), is still in range and they vanish below 2^-32.  bf16 has fp32's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
 
 // Warps: four of softmax for each row tile, matrices, copies of keys, copies of values, scheduler; with one row tile
 // the products P V have a warp of their own.
@@ -935,7 +940,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
                 break;
               }
             }
-            const float shift = ref == -INFINITY ? 0.0f : -ref;
+            const float shift = ref == -INFINITY ? 0.0f : kLift<BF16> - ref;
             const float2 sc = make_float2(scale2, scale2), sh = make_float2(shift, shift);
             part = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -1029,7 +1034,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
             }
           }
           __syncwarp();
-          const float shift = ref == -INFINITY ? 0.0f : -ref;
+          const float shift = ref == -INFINITY ? 0.0f : kLift<BF16> - ref;
           const float2 sc = make_float2(scale2, scale2), sh = make_float2(shift, shift);
           float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
@@ -1146,7 +1151,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
             }
           }
           if (store && a.lse != nullptr)
-            a.lse[(long long)tok_row * a.q_heads + head] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2f;
+            a.lse[(long long)tok_row * a.q_heads + head] = sum == 0.0f ? -INFINITY : (ref + (log2f(sum) - kLift<BF16>)) * kLn2f;
         }
       } else {
         // file the partial result: [column / 4][row] float4, then (reference, sum) per row
@@ -1296,7 +1301,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         }
       }
       if (row < span && a.lse != nullptr)
-        a.lse[(long long)dst * a.q_heads + hd] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
+        a.lse[(long long)dst * a.q_heads + hd] = l == 0.0f ? -INFINITY : (m + (log2f(l) - kLift<BF16>)) * kLn2f;
     }
     if (*abort && lane == 0) {
       for (int b = 0; b < c.B; ++b) atomicOr(a.status + b, ASV_REQ_TIMEOUT);
