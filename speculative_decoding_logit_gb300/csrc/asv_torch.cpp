@@ -126,6 +126,15 @@ long long whole_number(PyObject* o, const char* name) {
   return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) {
+    PyErr_Clear();
+    refuse(ASV_ERR_PARAM, "%s must be true or false", name);
+  }
+  return t != 0;
+}
+
 cudaStream_t stream_of(PyObject* o) { return reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(whole_number(o, "stream"))); }
 
 PyObject* result(asv_status st, const char* what) {
@@ -197,6 +206,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // None), req_status, stream
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_kv_append", n, 13, [&]() -> PyObject* {
+    const bool interleaved = truth(a[9], "interleaved");
     const at::Tensor& k = tensor(a[0], "k");
     if (k.dim() != 3) refuse(ASV_ERR_SHAPE, "k and v must be [N, kv_heads, head_dim]");
     const Paged p = paged(tensor(a[2], "k_cache"), tensor(a[3], "v_cache"), tensor(a[4], "block_table"),
@@ -220,7 +230,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t.scalar_type() != at::kFloat || t.dim() != 2 || !t.is_contiguous() || t.device() != p.device)
         refuse(ASV_ERR_SHAPE, "rotary must be a contiguous float32 [max_position, dim] table");
       rot = {static_cast<const float*>(t.data_ptr()), extent(t.size(1), "the rotation's dim"),
-             extent(t.size(0), "max_position"), PyObject_IsTrue(a[9]) == 1};
+             extent(t.size(0), "max_position"), interleaved};
     }
     return result(g_append(&p.cache, &p.batch, &kr, &vr, with_q ? &qr : nullptr, with_q ? &oq : nullptr, heads,
                            rotate ? &rot : nullptr, status_of(tensor(a[11], "req_status"), p), stream_of(a[12])),
