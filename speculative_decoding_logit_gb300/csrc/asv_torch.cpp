@@ -143,6 +143,16 @@ PyObject* result(asv_status st, const char* what) {
   refuse(st, "%s: %s", what, g_status_string(st));
 }
 
+// f(), a call of the library, with the interpreter's lock released: a launch waits while the stream's queue is full, and
+// what drains it may need the lock (a host function in Python).  Nothing in the library throws.
+template <class F>
+asv_status unlocked(F f) {
+  PyThreadState* state = PyEval_SaveThread();
+  const asv_status st = f();
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 // Nothing but a Python exception leaves a call.
 template <class F>
 PyObject* guarded(const char* what, Py_ssize_t n, Py_ssize_t expected, F f) {
@@ -196,8 +206,14 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const at::Tensor& ws = tensor(a[11], "workspace");
     if (!ws.is_contiguous() || ws.device() != p.device) refuse(ASV_ERR_WORKSPACE, "workspace must be contiguous, on the tensors' device");
-    return result(g_attention(&p.cache, &p.batch, &qr, &out, heads, float(scale), int(window), lse,
-                              status_of(tensor(a[10], "req_status"), p), ws.data_ptr(), ws.nbytes(), stream_of(a[12])),
+    uint32_t* status = status_of(tensor(a[10], "req_status"), p);
+    void* const room = ws.data_ptr();
+    const size_t bytes = ws.nbytes();
+    const cudaStream_t stream = stream_of(a[12]);
+    return result(unlocked([&]() {
+                    return g_attention(&p.cache, &p.batch, &qr, &out, heads, float(scale), int(window), lse, status, room,
+                                       bytes, stream);
+                  }),
                   "paged_attention");
   });
 }
@@ -232,8 +248,12 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       rot = {static_cast<const float*>(t.data_ptr()), extent(t.size(1), "the rotation's dim"),
              extent(t.size(0), "max_position"), interleaved};
     }
-    return result(g_append(&p.cache, &p.batch, &kr, &vr, with_q ? &qr : nullptr, with_q ? &oq : nullptr, heads,
-                           rotate ? &rot : nullptr, status_of(tensor(a[11], "req_status"), p), stream_of(a[12])),
+    uint32_t* status = status_of(tensor(a[11], "req_status"), p);
+    const cudaStream_t stream = stream_of(a[12]);
+    return result(unlocked([&]() {
+                    return g_append(&p.cache, &p.batch, &kr, &vr, with_q ? &qr : nullptr, with_q ? &oq : nullptr, heads,
+                                    rotate ? &rot : nullptr, status, stream);
+                  }),
                   "paged_kv_append");
   });
 }
