@@ -574,6 +574,8 @@ def _paged_ext():
         if _ext is None:
             if not os.path.exists(_build.TORCH_EXT):
                 raise AsvError(-1, f"asv_torch.so not built ({_build.TORCH_EXT}); call speculative_decoding_logit_gb300.build()")
+            if not _build.torch_ext_fits():
+                raise AsvError(-1, f"{_build.TORCH_EXT} was built for another PyTorch; call speculative_decoding_logit_gb300.build()")
             loader = importlib.machinery.ExtensionFileLoader("asv_torch", _build.TORCH_EXT)
             ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("asv_torch", loader))
             loader.exec_module(ext)

@@ -49,10 +49,26 @@ def build_checked(force: bool = False, verbose: bool = False) -> str:
     return build(force=force, verbose=verbose, extra_flags=("-DASV_CHECKED",), lib=LIB_CHECKED)
 
 
+def torch_ext_fits() -> bool:
+    """Whether the binding's module was built for the PyTorch and the Python that run (noted beside it)."""
+    try:
+        with open(TORCH_EXT + ".for") as f:
+            return f.read() == _running()
+    except OSError:
+        return False
+
+
+def _running() -> str:
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def build_torch_ext(force: bool = False) -> str:
-    """Compile the binding's module (_build/asv_torch.so) with the host compiler."""
+    """Compile the binding's module (_build/asv_torch.so) with the host compiler, for the PyTorch that runs."""
     deps = [TORCH_EXT_SRC, os.path.join(INCLUDE, "asv.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(TORCH_EXT) and all(
+    if not force and torch_ext_fits() and os.path.exists(TORCH_EXT) and all(
             os.path.getmtime(d) <= os.path.getmtime(TORCH_EXT) for d in deps):
         return TORCH_EXT
     import sysconfig
@@ -71,6 +87,9 @@ def build_torch_ext(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"the binding's module failed to compile:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, TORCH_EXT)
+    with open(tmp, "w") as f:
+        f.write(_running())
+    os.replace(tmp, TORCH_EXT + ".for")
     return TORCH_EXT
 
 
