@@ -7,6 +7,7 @@ import glob
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -83,9 +84,15 @@ def build_torch_ext(force: bool = False) -> str:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", *[f"-I{i}" for i in inc],
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", TORCH_EXT_SRC, "-o", tmp,
            f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"the binding's module failed to compile:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.returncode != 0 and f"{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        if os.path.exists(TORCH_EXT):   # of older sources, or for another PyTorch
+            os.remove(TORCH_EXT)
+        raise RuntimeError(f"the binding's module failed to compile:\n{failed}")
     os.replace(tmp, TORCH_EXT)
     with open(tmp, "w") as f:
         f.write(_running())
@@ -95,13 +102,17 @@ def build_torch_ext(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib: str = LIB) -> str:
     """Compile csrc/*.cu and link `lib` (default _build/libasv.so), and with the default library the
-    binding's module; returns the library path."""
+    binding's module; returns the library path.  Only the paged calls need the module: where it does not
+    compile that is a warning here, and they refuse."""
     if lib != LIB:
         return _build_library(force, verbose, extra_flags, lib)
     with cf.ThreadPoolExecutor(1) as ex:
         ext = ex.submit(build_torch_ext, force)
         path = _build_library(force, verbose, extra_flags, lib)
+    try:
         ext.result()
+    except RuntimeError as e:
+        warnings.warn(f"paged_kv_append and paged_attention are not available: {e}", RuntimeWarning, stacklevel=2)
     return path
 
 

@@ -44,3 +44,22 @@ def test_a_module_of_another_torch_is_not_loaded(b, monkeypatch, tmp_path):
     monkeypatch.setattr(torch, "__version__", "99.0")
     with pytest.raises(_binding.AsvError, match="another PyTorch"):
         _binding._paged_ext()
+
+
+def test_the_library_is_built_without_the_module(b, monkeypatch, tmp_path):
+    """The verification needs no compiled module: where the host compiler fails, build() says so and the paged calls
+    refuse, with a module of older sources out of the way."""
+    from speculative_decoding_logit_gb300 import _binding
+    _compiler(monkeypatch, tmp_path)
+    b.build_torch_ext()
+    os.utime(b.TORCH_EXT, (1, 1))   # older than its sources
+    _compiler(monkeypatch, tmp_path, works=False)
+    with pytest.warns(RuntimeWarning, match="no headers"):
+        assert b.build() == b.LIB
+    assert os.path.exists(b.LIB) and not os.path.exists(b.TORCH_EXT)
+    monkeypatch.setattr(_binding, "_ext", None)
+    with pytest.raises(_binding.AsvError, match="not built"):
+        _binding._paged_ext()
+    assert _binding.workspace_bytes(0, 1, 2, 4096, 0) > 0
+    with pytest.raises(RuntimeError, match="no headers"):   # asked for by itself it is an error
+        b.build_torch_ext()
