@@ -84,9 +84,10 @@ typedef enum {
 /* Per-request status bits written by the kernels (never a trap). */
 #define ASV_REQ_NONFINITE 1u /* a row holds NaN or +inf, or is entirely -inf */
 #define ASV_REQ_BAD_DRAFT 2u /* a draft id lies outside [0, V) */
-#define ASV_REQ_TIMEOUT 4u   /* a bounded wait of the staged kernel expired (its launch keeps every CTA
-                                resident, so this marks a fault, not a load condition): the request's
-                                outputs are unspecified and the workspace must be zero-filled again */
+#define ASV_REQ_TIMEOUT 4u   /* a bounded wait of the staged kernel or of paged_attention expired (the staged launch
+                                keeps every CTA resident, and no CTA of paged_attention waits for another, so
+                                this marks a fault, not a load condition): the request's outputs are
+                                unspecified and the workspace must be zero-filled again */
 #define ASV_REQ_BAD_PAGE 8u  /* a block-table entry the request needs lies outside [0, num_pages) */
 #define ASV_REQ_BAD_LEN 16u  /* indptr is not 0 <= start <= end <= N, cache_len is negative, or the tokens go
                                 past the block table's last page or the rotation table's last row */

@@ -644,6 +644,21 @@ _paged_ws_cache: dict = {}
 PAGED_WORKSPACE_ZEROED = 4096
 
 
+def clear_workspaces():
+    """Zero-fills the workspaces that calls without workspace= keep for each stream, in place, when everything queued on
+    their devices is done.  To be called after a request came back with REQ_TIMEOUT: the call that gave up may have
+    left its workspace dirty, which later calls would count on."""
+    with _ws_lock:
+        kept = list(_ws_cache.values()) + [ws[:PAGED_WORKSPACE_ZEROED] for ws in _paged_ws_cache.values()]
+        devices = {ws.device for ws in kept}
+        for d in devices:
+            torch.cuda.synchronize(d)
+        for ws in kept:
+            ws.zero_()
+        for d in devices:
+            torch.cuda.synchronize(d)
+
+
 def paged_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
     """Bytes of workspace one paged_attention call with these heads needs, for any batch."""
     return int(library().asv_paged_workspace_bytes(q_heads, kv_heads, head_dim))
