@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "asv_paged_device.cuh"
+#include "asv_ring.h"
 #include "asv_tcgen05.cuh"
 
 namespace asv {
@@ -197,6 +198,9 @@ struct Misc {
   int abort;
   int poison[2];  // a value that some rows of the item in this output buffer do not attend to is not finite
   int last[2][2];
+  // for a launch that gives up: where the copies of keys, values and queries ended, the matrix instructions' end
+  Ring copied[2], queries;
+  uint64_t drained[2];
 };
 
 // What the warps of a divided row tile tell each other, for odd and even tiles: whether the reference has to move, the
@@ -204,19 +208,6 @@ struct Misc {
 struct Divided {
   int vote[2][4];
   float top[2][4][32], sum[4][32];
-};
-
-// Counters of a ring of `n` barriers: slot and phase of the i-th use.
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ void next(int n, int by = 1) {
-    slot += by;
-    if (slot >= n) {
-      slot -= n;
-      phase ^= 1;
-    }
-  }
 };
 
 __device__ __forceinline__ uint32_t at(const uint64_t* bars, int i) { return smem_addr(bars + i); }
@@ -384,6 +375,7 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
       bar_init(at(ms.o_full, i), 1);
       bar_init(at(ms.o_empty, i), 4);
       bar_init(at(ms.wg_sync, i), 4);
+      bar_init(at(ms.drained, i), 1);
       ms.poison[i] = 0;
     }
     for (int i = 0; i < kQueue; ++i) {
@@ -611,13 +603,9 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
         run = copy_tile(w.head, i, page, w.slot);
       }
     }
-    if (*abort) {  // leave with no copy in flight: the slots still being written, for a while
-      for (int i = 0; i < kRing; ++i) {
-        const unsigned long long t0 = now_ns();
-        const uint32_t parity = i < ring_kv.slot ? ring_kv.phase : ring_kv.phase ^ 1;
-        while (!bar_try(at(ms.kv_full, i), parity) && now_ns() - t0 < kWaitNs / 100) {
-        }
-      }
+    if (lane == 0) {
+      ms.copied[values] = ring_kv;
+      if (values) ms.queries = ring_q;
     }
   } else if (warp == kMmaWarp || warp > kWalkWarp) {
     // ---- matrices
@@ -1309,6 +1297,32 @@ __global__ void __launch_bounds__(kThreadsOf<NT>, 1)
   }
   fence_before();
   __syncthreads();
+  if (*abort) {
+    // A wait ran out.  Nothing waits any more, so all warps see it: leave with no copy, matrix instruction or store to
+    // tensor memory in flight (each waited for, a while).
+    if (warp == kCopyWarp || warp == kCopyWarp + 1) {
+      // Its last tiles: before it copied them, the ones before were used.
+      Ring r = ms.copied[warp - kCopyWarp];
+      for (int i = 0; i < (kRing + 1) / 2; ++i) {
+        r.back(kRing, 2);
+        wait_a_while(at(ms.kv_full, r.slot), r.phase);
+      }
+      r = ms.queries;
+      for (int i = 0; warp != kCopyWarp && i < 3 - NT; ++i) {
+        r.back(3 - NT);
+        wait_a_while(at(ms.q_full, r.slot), r.phase);
+      }
+    } else if (warp == kMmaWarp || warp > kWalkWarp) {
+      const int which = warp == kMmaWarp ? 0 : 1;
+      if (elect()) commit(at(ms.drained, which));
+      __syncwarp();
+      wait_a_while(at(ms.drained, which), 0);
+    } else if (warp != kWalkWarp) {
+      tmem_wait_st();
+    }
+    fence_before();
+    __syncthreads();
+  }
   if (warp == kMmaWarp) tmem_free(tmem, kTmemColumns);
 }
 

@@ -80,7 +80,14 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   return bar_wait_slow(bar, parity, abort);
 }
 
-// The same by a whole warp, one answer for every lane.
+// Until the phase completes or a hundredth of a wait's limit is over (for what a launch that gives up has in flight).
+__device__ __noinline__ void wait_a_while(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = now_ns();
+  while (!bar_try(bar, parity) && now_ns() - t0 < kWaitNs / 100) {
+  }
+}
+
+// A wait by a whole warp, one answer for every lane.
 __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, bar_wait_slow(bar, parity, abort));
 }
