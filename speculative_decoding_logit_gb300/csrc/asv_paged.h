@@ -36,7 +36,7 @@ struct AppendArgs {
   const float* rotary;  // nullptr: no rotation
   int rot_dim, max_position, interleaved;
   uint32_t* status;
-  uint32_t* check_log;  // always nullptr: the append has no workspace to keep a log in
+  uint32_t* check_log;  // of the checked build: the append has no workspace, its log is the library's
 };
 
 struct AttendArgs {

@@ -60,12 +60,12 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     while (b < c.B && c.indptr[b + 1] <= token) ++b;
     if (token < c.N && b < c.B) {
       const Request r = load_request(c, b, limit);
-      if (r.ok && token >= r.start && token < r.end && ASV_GUARD(a, token < c.N)) {
+      if (r.ok && token >= r.start && token < r.end) {
         p.request = b;
         p.pos = r.past + (token - r.start);
         const int entry = p.pos / c.page_size;
         p.slot = p.pos - entry * c.page_size;
-        p.page = c.table[b * c.table_stride + entry];
+        if (ASV_GUARD(a, entry >= 0 && entry < c.max_pages)) p.page = c.table[b * c.table_stride + entry];
         if (p.page < 0 || p.page >= c.num_pages) {
           atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
           p.page = -1;
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   if (a.rotary != nullptr) {
     for (int i = tid; i < TOKENS * a.rot_dim; i += kThreads) {
       const int t = i / a.rot_dim, j = i - t * a.rot_dim;
-      if (s_place[t].request >= 0) s_cs[t][j] = a.rotary[(long long)s_place[t].pos * a.rot_dim + j];
+      if (s_place[t].request >= 0 && ASV_GUARD(a, s_place[t].pos >= 0 && s_place[t].pos < a.max_position && j < 128))
+        s_cs[t][j] = a.rotary[(long long)s_place[t].pos * a.rot_dim + j];
     }
     __syncthreads();
   }
@@ -109,6 +110,11 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
       const bool is_q = h < a.q_heads;
       if (p.request < 0 || (!is_q && p.page < 0)) continue;
       const long long token = token0 + t;
+      // the row, the vector and its partners within it, the slot
+      if (!ASV_GUARD(a, token < c.N && p.request < c.B && h < heads && d + 8 <= c.head_dim &&
+                            (PAIRING == kHalves && pair ? half + d + 8 <= a.rot_dim : PAIRING == kPlain || a.rot_dim <= c.head_dim) &&
+                            (is_q || (p.page < c.num_pages && p.slot >= 0 && p.slot < c.page_size))))
+        continue;
       const uint16_t* src = is_q ? a.q.p + token * a.q.tok + h * a.q.head
                                  : a.k.p + token * a.k.tok + (h - a.q_heads) * a.k.head;
       uint16_t* dst = is_q ? a.out_q.p + token * a.out_q.tok + h * a.out_q.head
@@ -184,6 +190,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     if (t >= TOKENS) break;
     const TokenPlace p = s_place[t];
     if (p.request < 0 || p.page < 0) continue;
+    if (!ASV_GUARD(a, token0 + t < c.N && h < c.kv_heads && d + 8 <= c.head_dim && p.page < c.num_pages && p.slot >= 0 &&
+                          p.slot < c.page_size))
+      continue;
     *reinterpret_cast<uint4*>(c.v + p.page * c.v_page + p.slot * c.v_slot + h * c.v_head + d) =
         __ldg(reinterpret_cast<const uint4*>(a.v.p + (long long)(token0 + t) * a.v.tok + h * a.v.head + d));
   }
@@ -218,9 +227,22 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
   }
 }
 
+#ifdef ASV_CHECKED
+__device__ uint32_t g_check_log[2];  // the append has no workspace to keep a log in
+#endif
+
 }  // namespace
 
-cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s) {
+cudaError_t launch_paged_append(const AppendArgs& args, int dtype, cudaStream_t s) {
+#ifdef ASV_CHECKED
+  AppendArgs a = args;
+  void* log = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&log, g_check_log);
+  if (e != cudaSuccess) return e;
+  a.check_log = static_cast<uint32_t*>(log);
+#else
+  const AppendArgs& a = args;
+#endif
   const int pairing = a.rotary == nullptr || a.interleaved ? kPlain
                       : a.rot_dim % 16 == 0                ? kHalves
                       : a.rot_dim % 8 == 0                 ? kFours
@@ -235,3 +257,12 @@ cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s) 
 }
 
 }  // namespace asv
+
+#ifdef ASV_CHECKED
+// The append's check log (the count and the line of the first failure), when the device's work is done.  Returns a
+// cudaError.
+extern "C" int asv_paged_append_check_log(uint32_t* out) {
+  const cudaError_t e = cudaDeviceSynchronize();
+  return int(e != cudaSuccess ? e : cudaMemcpyFromSymbol(out, asv::g_check_log, sizeof(asv::g_check_log)));
+}
+#endif
