@@ -463,8 +463,9 @@ typedef struct {
 /*
  * paged_kv_append -- the chunk's keys (rotated) and values (as they are) into their slots of the cache,
  * and the rotated queries to out_q.  rotary NULL: no rotation.  q and out_q both NULL: keys and values
- * only (q_heads is then not looked at); out_q must not overlap q.  Two requests that share a page must not write
- * the same slot.  One launch.
+ * only (q_heads is then not looked at); out_q must not overlap q.  The queries of a token whose page is bad are
+ * rotated all the same, those of a request that is left out are not written.  Two requests that share a page
+ * must not write the same slot.  One launch.
  * Checks, in this order, before anything is queued: sizes (ASV_ERR_SHAPE), element type
  * (ASV_ERR_DTYPE), for B > 0 and N > 0: the rotation's sizes (ASV_ERR_PARAM), alignment of pointers
  * and strides (ASV_ERR_ALIGN; NULL counts as aligned), the required pointers (ASV_ERR_NULL).
@@ -479,7 +480,8 @@ asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* 
  * j <= p, with window > 0 only to j > p - window; query head h reads key head h / (q_heads / kv_heads).
  *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j)
  * Products take the 16-bit inputs exactly and accumulate in fp32; the softmax is fp32, its weights are
- * rounded to the cache's type for the product with v (their sum is not), and out is rounded once.
+ * rounded to the cache's type for the product with v (their sum is not; in fp16 those below 2^-32 of a large
+ * one are lost to it), and out is rounded once.
  * What a slot outside every attended position holds (a page's unwritten tail, an evicted page's entry)
  * does not matter, NaN included.
  * out must not overlap q or the cache.  q_heads is a multiple of kv_heads, at most 128 to one key head; scale is finite and > 0; window >= 0

@@ -59,6 +59,7 @@ from ._binding import (  # noqa: F401
     host_arena_bytes,
     library,
     library_path,
+    PAGED_WORKSPACE_ZEROED,
     clear_workspaces,
     paged_attention,
     paged_kv_append,

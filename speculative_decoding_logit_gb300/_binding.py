@@ -621,8 +621,10 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     """Appends the packed new tokens' keys and values ([N, kv_heads, head_dim]; request b's are rows
     indptr[b]..indptr[b+1]) to the paged caches at positions cache_len[b] onwards; with `rotary`
     ([max_position, dim] float32: cos of the dim/2 angles of each position, then their sines) the keys
-    are rotated on the way, and the queries `q` into out.q (paged_kv_append in include/asv.h).
-    cache_len is not advanced.  The caches take any strides with head rows contiguous."""
+    are rotated on the way, and the queries `q` into out.q, which must not overlap them (paged_kv_append in
+    include/asv.h).  cache_len is not advanced.  The caches take any positive strides that are multiples of 8 elements,
+    head rows contiguous.  With `stream`, the call's order with other streams' work is the caller's business; what it
+    makes for `out` belongs to that stream."""
     handle = _raw_stream(k, stream)
     if handle is None:
         with torch.cuda.device(k.device):
@@ -682,7 +684,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Attention of the packed chunks of new tokens q [N, q_heads, head_dim] over the paged caches, the
     chunk's own tokens (appended before, see paged_kv_append) included: causal, grouped heads, with
     `window` > 0 only the last `window` positions of each token (paged_attention in include/asv.h).
-    cache_len [B] counts the tokens before the chunk; scale defaults to head_dim ** -0.5."""
+    cache_len [B] counts the tokens before the chunk; scale defaults to head_dim ** -0.5.  `stream` as for
+    paged_kv_append.  Without `workspace` the call uses one kept for its stream (40 MB), and so does a graph captured
+    there: give a workspace of its own (paged_workspace_bytes, its first PAGED_WORKSPACE_ZEROED bytes zero) to a graph
+    that may be replayed next to the stream's other calls."""
     handle = _raw_stream(q, stream)
     if handle is None:
         with torch.cuda.device(q.device):

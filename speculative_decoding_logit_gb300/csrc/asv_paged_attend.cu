@@ -31,9 +31,9 @@
 // gives each row tile one, and the two tiles alternate.
 //
 // Measured (bf16, heads of 128, one call among others): 64 requests x 3 tokens over 500 .. 12,000, 64 / 8 heads,
-// 146 - 148 us, bound by HBM (6.3 TB/s); 256 x 1 token over 1 .. 4096 (fp16) 94 us, 507 MB; 4 x 2048 tokens over
-// 8192, 32 / 8 heads, 620 - 690 us by the clock that the power limit leaves, 1.5 PFLOP/s at the best, bound by each row
-// tile's chain S, softmax, P V; 1 token over 4096, 10.7 us, all latency.
+// 148 us, bound by HBM (6.2 TB/s); 256 x 1 token over 1 .. 4096 (fp16) 94 us, 507 MB; 4 x 2048 tokens over
+// 8192, 32 / 8 heads, 715 - 721 us at the clock that the power limit leaves (1.34 PFLOP/s; a single launch 630), bound by
+// each row tile's chain S, softmax, P V; 1 token over 4096, 10.5 us, all latency.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
