@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import importlib.machinery
 import importlib.util
 import os
@@ -175,6 +176,40 @@ def _stream_handle(device: torch.device, stream=None):
     return s.cuda_stream
 
 
+def _mark_used(tensors, caller):
+    """Keeps the memory of a call's outputs from reuse until the caller's stream, which reads them, is done too."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(caller)
+
+
+def _made_on(stream, make):
+    """The tensors that make() allocates for a call on `stream` (None: the current one).  They are made there, so
+    that a zero-fill comes before the call and no block is taken that work on another stream still uses."""
+    if stream is None:
+        return make()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        made = make()
+    _mark_used(made, caller)
+    return made
+
+
+def _all_on_stream(call):
+    """`call` with its `stream` current, so that its outputs and a new workspace are made there (see _made_on)."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            got = call(*args, stream=stream, **kw)
+        if kw.get("out") is None:
+            _mark_used(vars(got).values(), caller)
+        return got
+    return on_stream
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return ASV_F32
@@ -195,7 +230,8 @@ def _contig(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-# Workspace cache: one zero-initialised buffer per (device, stream); every call leaves it zeroed.
+# Workspace cache: one zero-initialised buffer per (device, stream); every call leaves it zeroed.  One made
+# while the stream is capturing belongs to the graph, whose replays zero-fill it, and is not kept.
 _ws_cache: dict = {}
 _ws_lock = threading.Lock()
 
@@ -206,7 +242,8 @@ def _workspace(device: torch.device, stream_handle: int, nbytes: int) -> torch.T
         ws = _ws_cache.get(key)
         if ws is None or ws.numel() < nbytes:
             ws = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=device)
-            _ws_cache[key] = ws
+            if not torch.cuda.is_current_stream_capturing():
+                _ws_cache[key] = ws
     return ws
 
 
@@ -247,6 +284,7 @@ class AsymSpecOutput:
     req_status: torch.Tensor   # [B] int32 (ASV_REQ_* bits)
 
 
+@_all_on_stream
 def asymspec_verify(a: torch.Tensor, b: torch.Tensor, t: torch.Tensor, draft_ids: torch.Tensor,
                     beta: float = 1.0, gamma: float = 0.5, *, delta_source: int = DELTA_A_MINUS_B,
                     out: Optional[AsymSpecOutput] = None, workspace: Optional[torch.Tensor] = None,
@@ -322,6 +360,7 @@ def _check_asym_inputs(a, b, t, draft_ids):
     return B, R1 - 1, V
 
 
+@_all_on_stream
 def asymspec_verify_sweep(a: torch.Tensor, b: torch.Tensor, t: torch.Tensor, draft_ids: torch.Tensor, betas,
                           gammas, *, workspace: Optional[torch.Tensor] = None, stream=None) -> SweepOutput:
     """AsymSpec for every (beta, gamma) of a grid from one read of a, b, t (asymspec_verify_sweep)."""
@@ -360,6 +399,7 @@ class AsymSciOutput:
     req_status: torch.Tensor      # [B]
 
 
+@_all_on_stream
 def asymspec_sci_verify(a: torch.Tensor, b: torch.Tensor, t: torch.Tensor, draft_ids: torch.Tensor, beta: float,
                         gamma: float, r_hat: torch.Tensor, params: "SciParams" = None, *,
                         workspace: Optional[torch.Tensor] = None, stream=None) -> AsymSciOutput:
@@ -414,6 +454,7 @@ TAIL_KEEP_P = 0          # tail entries keep p, the head is rescaled (rapid_veri
 TAIL_RENORMALISE_ALL = 1  # p substitutes phat on the tail, then every entry is renormalised
 
 
+@_all_on_stream
 def rapid_verify(z: torch.Tensor, q: torch.Tensor, draft_ids: torch.Tensor, T: float = 1.0, eta: float = 10.0,
                  tail_frac: float = 0.1, seed: int = 1234, offset: int = 0, *, tail_mode: int = TAIL_KEEP_P,
                  out: Optional[RapidOutput] = None, workspace: Optional[torch.Tensor] = None,
@@ -490,6 +531,7 @@ def sci_state_decode(state: torch.Tensor):
     return h[:, :2].contiguous().view(torch.float64).reshape(-1), h[:, 2].clone(), h[:, 3].clone()
 
 
+@_all_on_stream
 def sci_verify(draft: torch.Tensor, target: torch.Tensor, draft_ids: torch.Tensor, r_hat: torch.Tensor,
                params: SciParams = SciParams(), *, stabilisers: Optional[SciStabilisers] = None,
                state: Optional[torch.Tensor] = None, prehit: bool = False, out: Optional[SciOutput] = None,
@@ -596,21 +638,6 @@ def _raw_stream(t: torch.Tensor, stream) -> Optional[int]:
     if dev != torch._C._cuda_getDevice():
         return None
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _made_on(stream, make):
-    """The tensors that make() allocates for a call on `stream` (None: the current one).  They are made there, so
-    that a zero-fill comes before the call and no block is taken that work on another stream still uses, and are
-    marked as used by the caller's stream, which will read them."""
-    if stream is None:
-        return make()
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        made = make()
-    for t in made:
-        if t is not None:
-            t.record_stream(caller)
-    return made
 
 
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
