@@ -172,8 +172,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream_handle(device: torch.device, stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None and stream.device != device:
+        raise AsvError(2, "the stream must be one of the tensors' device")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _mark_used(tensors, caller):
@@ -195,10 +196,15 @@ def _made_on(stream, make):
     return made
 
 
-def _all_on_stream(call):
-    """`call` with its `stream` current, so that its outputs and a new workspace are made there (see _made_on)."""
+def _in_place(call):
+    """`call` with its first argument's device current, where the launch goes, and with its `stream` current, so that
+    its outputs and a new workspace are made there (see _made_on)."""
     @functools.wraps(call)
-    def on_stream(*args, stream=None, **kw):
+    def placed(*args, stream=None, **kw):
+        first = args[0] if args else next(iter(kw.values()), None)
+        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch._C._cuda_getDevice():
+            with torch.cuda.device(first.device):
+                return placed(*args, stream=stream, **kw)
         if stream is None:
             return call(*args, **kw)
         caller = torch.cuda.current_stream(stream.device)
@@ -207,7 +213,7 @@ def _all_on_stream(call):
         if kw.get("out") is None:
             _mark_used(vars(got).values(), caller)
         return got
-    return on_stream
+    return placed
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -284,7 +290,7 @@ class AsymSpecOutput:
     req_status: torch.Tensor   # [B] int32 (ASV_REQ_* bits)
 
 
-@_all_on_stream
+@_in_place
 def asymspec_verify(a: torch.Tensor, b: torch.Tensor, t: torch.Tensor, draft_ids: torch.Tensor,
                     beta: float = 1.0, gamma: float = 0.5, *, delta_source: int = DELTA_A_MINUS_B,
                     out: Optional[AsymSpecOutput] = None, workspace: Optional[torch.Tensor] = None,
@@ -360,7 +366,7 @@ def _check_asym_inputs(a, b, t, draft_ids):
     return B, R1 - 1, V
 
 
-@_all_on_stream
+@_in_place
 def asymspec_verify_sweep(a: torch.Tensor, b: torch.Tensor, t: torch.Tensor, draft_ids: torch.Tensor, betas,
                           gammas, *, workspace: Optional[torch.Tensor] = None, stream=None) -> SweepOutput:
     """AsymSpec for every (beta, gamma) of a grid from one read of a, b, t (asymspec_verify_sweep)."""
@@ -399,7 +405,7 @@ class AsymSciOutput:
     req_status: torch.Tensor      # [B]
 
 
-@_all_on_stream
+@_in_place
 def asymspec_sci_verify(a: torch.Tensor, b: torch.Tensor, t: torch.Tensor, draft_ids: torch.Tensor, beta: float,
                         gamma: float, r_hat: torch.Tensor, params: "SciParams" = None, *,
                         workspace: Optional[torch.Tensor] = None, stream=None) -> AsymSciOutput:
@@ -432,6 +438,10 @@ def asymspec_verify_host(a, b, t, draft_ids, beta, gamma, arena: torch.Tensor, o
                          out_req_status, dtype: int, stream=None):
     """AsymSpec verification over host (pinned) buffers: raw addresses of CPU tensors; `arena`
     is a zeroed device uint8 tensor of host_arena_bytes() bytes.  Asynchronous on the stream."""
+    if arena.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(arena.device):
+            return asymspec_verify_host(a, b, t, draft_ids, beta, gamma, arena, out_accept_len, out_tokens, out_D,
+                                        out_req_status, dtype, stream)
     B, R1, V = a.shape
     K = R1 - 1
     sh = _stream_handle(arena.device, stream)
@@ -454,7 +464,7 @@ TAIL_KEEP_P = 0          # tail entries keep p, the head is rescaled (rapid_veri
 TAIL_RENORMALISE_ALL = 1  # p substitutes phat on the tail, then every entry is renormalised
 
 
-@_all_on_stream
+@_in_place
 def rapid_verify(z: torch.Tensor, q: torch.Tensor, draft_ids: torch.Tensor, T: float = 1.0, eta: float = 10.0,
                  tail_frac: float = 0.1, seed: int = 1234, offset: int = 0, *, tail_mode: int = TAIL_KEEP_P,
                  out: Optional[RapidOutput] = None, workspace: Optional[torch.Tensor] = None,
@@ -531,7 +541,7 @@ def sci_state_decode(state: torch.Tensor):
     return h[:, :2].contiguous().view(torch.float64).reshape(-1), h[:, 2].clone(), h[:, 3].clone()
 
 
-@_all_on_stream
+@_in_place
 def sci_verify(draft: torch.Tensor, target: torch.Tensor, draft_ids: torch.Tensor, r_hat: torch.Tensor,
                params: SciParams = SciParams(), *, stabilisers: Optional[SciStabilisers] = None,
                state: Optional[torch.Tensor] = None, prehit: bool = False, out: Optional[SciOutput] = None,

@@ -49,6 +49,7 @@ def test_outputs_and_workspace_are_made_on_the_calls_stream(monkeypatch, name):
     monkeypatch.setattr(torch.cuda, "stream", stream_context)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: SimpleNamespace(name=current[-1], cuda_stream=1))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
     monkeypatch.setattr(torch, "zeros", noting(torch.zeros))
     monkeypatch.setattr(torch, "empty", noting(torch.empty))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log.append(("record", s.name)))
