@@ -90,7 +90,8 @@ typedef enum {
                                 unspecified and the workspace must be zero-filled again */
 #define ASV_REQ_BAD_PAGE 8u  /* a block-table entry the request needs lies outside [0, num_pages) */
 #define ASV_REQ_BAD_LEN 16u  /* indptr is not 0 <= start <= end <= N, cache_len is negative, or the tokens go
-                                past the block table's last page or the rotation table's last row */
+                                past the block table's last page or the rotation table's last row; a position
+                                given for the rotation lies outside its table */
 
 /* Human-readable name of a status code (static string). */
 const char* asv_status_string(asv_status s);
@@ -460,6 +461,19 @@ typedef struct {
   int interleaved;
 } asv_rotary;
 
+/* Positions for the rotation that are not the slots': `at` [axes, N] int32 on the device, axis i's N in a row
+ * stride_axis elements behind the one before it (any stride for one axis), 1 <= axes <= ASV_MAX_AXES.  Pair j of row n
+ * is turned by entry j of the table's row at[axis_of_pair[j], n]; axis_of_pair is a HOST array of dim / 2 axes, read
+ * during the call (NULL: every pair on axis 0).  Text has the same position on every axis; an image's rows and columns
+ * count on axes of their own (AsymSpec's cross-modal drafter: [ASYM] sec. 4.3). */
+#define ASV_MAX_AXES 8
+typedef struct {
+  const int32_t* at;
+  int axes;
+  int64_t stride_axis;
+  const uint8_t* axis_of_pair;
+} asv_positions;
+
 /*
  * paged_kv_append -- the chunk's keys (rotated) and values (as they are) into their slots of the cache,
  * and the rotated queries to out_q.  rotary NULL: no rotation.  q and out_q both NULL: keys and values
@@ -473,6 +487,18 @@ typedef struct {
 asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* k,
                            const asv_rows* v, const asv_rows* q, const asv_rows* out_q, int q_heads,
                            const asv_rotary* rotary, uint32_t* out_req_status, cudaStream_t stream);
+
+/*
+ * paged_kv_append_ex -- paged_kv_append with `positions` (NULL: the slots' positions, as paged_kv_append has them).
+ * Slots stay cache_len[b] + i.  A token one of whose positions, on any of the axes, is negative or past the table's
+ * last row is left out (its query too) and its request flagged ASV_REQ_BAD_LEN; rows that belong to no request may hold
+ * anything.  Further checks: positions without a rotation, `axes` or an entry of axis_of_pair out of range
+ * (ASV_ERR_PARAM), at 4-byte aligned (ASV_ERR_ALIGN), at given (ASV_ERR_NULL).
+ */
+asv_status paged_kv_append_ex(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* k,
+                              const asv_rows* v, const asv_rows* q, const asv_rows* out_q, int q_heads,
+                              const asv_rotary* rotary, const asv_positions* positions, uint32_t* out_req_status,
+                              cudaStream_t stream);
 
 /*
  * paged_attention -- attention of the chunk's queries over the cache, the chunk's own tokens (already

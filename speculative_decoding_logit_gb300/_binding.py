@@ -101,6 +101,10 @@ class _RowsC(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_token", C.c_int64), ("stride_head", C.c_int64)]
 
 
+class _PositionsC(C.Structure):
+    _fields_ = [("at", C.c_void_p), ("axes", C.c_int), ("stride_axis", C.c_int64), ("axis_of_pair", C.c_char_p)]
+
+
 class _RotaryC(C.Structure):
     _fields_ = [("table", C.c_void_p), ("dim", C.c_int), ("max_position", C.c_int), ("interleaved", C.c_int)]
 
@@ -152,6 +156,8 @@ def _declare(L):
     L.sci_verify_ex.restype = _i
     L.paged_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp]
     L.paged_kv_append.restype = _i
+    L.paged_kv_append_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]
+    L.paged_kv_append_ex.restype = _i
     L.asv_paged_workspace_bytes.argtypes = [_i, _i, _i]
     L.asv_paged_workspace_bytes.restype = _sz
     L.paged_attention.argtypes = [_vp, _vp, _vp, _vp, _i, _f, _i, _vp, _vp, _vp, _sz, _vp]
@@ -631,7 +637,7 @@ def _paged_ext():
             loader = importlib.machinery.ExtensionFileLoader("asv_torch", _build.TORCH_EXT)
             ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("asv_torch", loader))
             loader.exec_module(ext)
-            ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append,
+            ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append_ex,
                                                                         L.asv_status_string, L.asv_last_cuda_error)))
             _ext = ext
     return _ext
@@ -653,27 +659,34 @@ def _raw_stream(t: torch.Tensor, stream) -> Optional[int]:
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     block_table: torch.Tensor, cache_len: torch.Tensor, indptr: torch.Tensor, *,
                     q: Optional[torch.Tensor] = None, rotary: Optional[torch.Tensor] = None,
-                    interleaved: bool = False, out: Optional[PagedAppendOutput] = None,
-                    stream=None) -> PagedAppendOutput:
+                    interleaved: bool = False, positions: Optional[torch.Tensor] = None, axes=None,
+                    out: Optional[PagedAppendOutput] = None, stream=None) -> PagedAppendOutput:
     """Appends the packed new tokens' keys and values ([N, kv_heads, head_dim]; request b's are rows
     indptr[b]..indptr[b+1]) to the paged caches at positions cache_len[b] onwards; with `rotary`
     ([max_position, dim] float32: cos of the dim/2 angles of each position, then their sines) the keys
     are rotated on the way, and the queries `q` into out.q, which must not overlap them (paged_kv_append in
-    include/asv.h).  cache_len is not advanced.  The caches take any positive strides that are multiples of 8 elements,
+    include/asv.h).  cache_len is not advanced.  With `positions` ([axes, N] int32, or [N] for one axis) the rotation
+    takes those instead of the slots' positions, pair j of a head that on axis axes[j] (`axes`: bytes or a sequence of
+    dim / 2 numbers; paged_kv_append_ex).  The caches take any positive strides that are multiples of 8 elements,
     head rows contiguous.  With `stream`, the call's order with other streams' work is the caller's business; what it
     makes for `out` belongs to that stream."""
     handle = _raw_stream(k, stream)
     if handle is None:
         with torch.cuda.device(k.device):
             return paged_kv_append(k, v, k_cache, v_cache, block_table, cache_len, indptr, q=q, rotary=rotary,
-                                   interleaved=interleaved, out=out, stream=stream)
+                                   interleaved=interleaved, positions=positions, axes=axes, out=out, stream=stream)
+    if axes is not None and not isinstance(axes, bytes):
+        try:
+            axes = bytes(list(axes))
+        except (TypeError, ValueError):
+            raise AsvError(5, "axes must be whole numbers from 0 on, one for each pair") from None
     if out is None:
         dev = k.device
         out = PagedAppendOutput(*_made_on(stream, lambda: (
             None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
             torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))))
     (_ext or _paged_ext()).paged_kv_append(k, v, k_cache, v_cache, block_table, cache_len, indptr, q, rotary,
-                                           interleaved, out.q, out.req_status, handle)
+                                           interleaved, out.q, out.req_status, handle, positions, axes)
     return out
 
 

@@ -35,6 +35,10 @@ struct AppendArgs {
   int q_heads;
   const float* rotary;  // nullptr: no rotation
   int rot_dim, max_position, interleaved;
+  const int32_t* positions;  // [axes, N]; nullptr: the slots' positions
+  int axes;
+  long long axis_stride;
+  uint8_t axis[64];  // axis of each pair
   uint32_t* status;
   uint32_t* check_log;  // of the checked build: the append has no workspace, its log is the library's
 };

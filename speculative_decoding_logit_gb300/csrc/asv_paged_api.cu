@@ -75,6 +75,13 @@ extern "C" {
 asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* k,
                            const asv_rows* v, const asv_rows* q, const asv_rows* out_q, int q_heads,
                            const asv_rotary* rotary, uint32_t* out_req_status, cudaStream_t stream) {
+  return paged_kv_append_ex(cache, batch, k, v, q, out_q, q_heads, rotary, nullptr, out_req_status, stream);
+}
+
+asv_status paged_kv_append_ex(const asv_paged_cache* cache, const asv_paged_batch* batch, const asv_rows* k,
+                              const asv_rows* v, const asv_rows* q, const asv_rows* out_q, int q_heads,
+                              const asv_rotary* rotary, const asv_positions* positions, uint32_t* out_req_status,
+                              cudaStream_t stream) {
   if (!cache || !batch) return ASV_ERR_NULL;
   const asv_paged_cache& c = *cache;
   const asv_paged_batch& b = *batch;
@@ -85,11 +92,17 @@ asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* 
   if (rotary && (rotary->dim < 2 || rotary->dim % 2 != 0 || rotary->dim > c.head_dim || rotary->max_position < 1 ||
                  (rotary->interleaved != 0 && rotary->interleaved != 1)))
     return ASV_ERR_PARAM;
+  if (positions) {
+    if (!rotary || positions->axes < 1 || positions->axes > ASV_MAX_AXES) return ASV_ERR_PARAM;
+    for (int j = 0; positions->axis_of_pair && j < rotary->dim / 2; ++j)
+      if (positions->axis_of_pair[j] >= positions->axes) return ASV_ERR_PARAM;
+  }
   if (!cache_ok(c, b) || !rows_ok(k, b.N, c.kv_heads) || !rows_ok(v, b.N, c.kv_heads) || !rows_ok(q, b.N, q_heads) ||
-      !rows_ok(out_q, b.N, q_heads) || (rotary && !aligned(rotary->table, 4)) || !aligned(out_req_status, 4))
+      !rows_ok(out_q, b.N, q_heads) || (rotary && !aligned(rotary->table, 4)) || (positions && !aligned(positions->at, 4)) ||
+      !aligned(out_req_status, 4))
     return ASV_ERR_ALIGN;
   if (!cache_given(c, b) || !k || !k->data || !v || !v->data || (!q) != (!out_q) || (q && !q->data) ||
-      (out_q && !out_q->data) || (rotary && !rotary->table) || !out_req_status)
+      (out_q && !out_q->data) || (rotary && !rotary->table) || (positions && !positions->at) || !out_req_status)
     return ASV_ERR_NULL;
   asv::AppendArgs a = {};
   a.c = paged_view(c, b);
@@ -105,6 +118,12 @@ asv_status paged_kv_append(const asv_paged_cache* cache, const asv_paged_batch* 
     a.rot_dim = rotary->dim;
     a.max_position = rotary->max_position;
     a.interleaved = rotary->interleaved;
+  }
+  if (positions) {
+    a.positions = positions->at;
+    a.axes = positions->axes;
+    a.axis_stride = positions->axes > 1 ? positions->stride_axis : 0;
+    for (int j = 0; positions->axis_of_pair && j < a.rot_dim / 2; ++j) a.axis[j] = positions->axis_of_pair[j];
   }
   a.status = out_req_status;
   cudaError_t e = asv::launch_paged_append(a, c.dtype, stream);

@@ -42,9 +42,11 @@ template <bool BF16, int PAIRING, int TOKENS>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ __align__(16) float s_cs[TOKENS][128];  // cos of the positions' angles, then their sines
   __shared__ TokenPlace s_place[TOKENS];
+  __shared__ int s_at[TOKENS][ASV_MAX_AXES];  // (positions of several axes)
   const PagedView& c = a.c;
   const int tid = threadIdx.x, token0 = blockIdx.x * TOKENS;
-  const long long limit = a.rotary != nullptr ? min((long long)a.max_position, table_positions(c)) : table_positions(c);
+  const long long limit = a.rotary != nullptr && a.positions == nullptr ? min((long long)a.max_position, table_positions(c))
+                                                                        : table_positions(c);
 
   // What comes after on the stream may set itself up; what came before is needed from here on.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -70,6 +72,16 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
           atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
           p.page = -1;
         }
+        bool there = true;
+        for (int i = 0; i < a.axes; ++i) {
+          const int at = a.positions[i * a.axis_stride + token];
+          there = there && at >= 0 && at < a.max_position;
+          s_at[tid][i] = at;
+        }
+        if (!there) {
+          atomicOr(a.status + b, ASV_REQ_BAD_LEN);
+          p.request = -1;
+        }
       }
     }
     s_place[tid] = p;
@@ -81,8 +93,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   if (a.rotary != nullptr) {
     for (int i = tid; i < TOKENS * a.rot_dim; i += kThreads) {
       const int t = i / a.rot_dim, j = i - t * a.rot_dim;
-      if (s_place[t].request >= 0 && ASV_GUARD(a, s_place[t].pos >= 0 && s_place[t].pos < a.max_position && j < 128))
-        s_cs[t][j] = a.rotary[(long long)s_place[t].pos * a.rot_dim + j];
+      if (s_place[t].request < 0) continue;
+      const int half = a.rot_dim / 2;
+      const int pos = a.positions == nullptr ? s_place[t].pos : s_at[t][a.axis[j < half ? j : j - half]];
+      if (ASV_GUARD(a, pos >= 0 && pos < a.max_position && j < 128)) s_cs[t][j] = a.rotary[(long long)pos * a.rot_dim + j];
     }
     __syncthreads();
   }

@@ -19,7 +19,7 @@ namespace {
 
 PyObject* g_error = nullptr;  // AsvError(status, message)
 decltype(&paged_attention) g_attention = nullptr;
-decltype(&paged_kv_append) g_append = nullptr;
+decltype(&paged_kv_append_ex) g_append = nullptr;
 decltype(&asv_status_string) g_status_string = nullptr;
 decltype(&asv_last_cuda_error) g_last_cuda_error = nullptr;
 
@@ -219,9 +219,9 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // k, v, k_cache, v_cache, block_table, cache_len, indptr, q (or None), rotary (or None), interleaved, out_q (or
-// None), req_status, stream
+// None), req_status, stream, and with them or not: positions (or None), axes (bytes, or None)
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("paged_kv_append", n, 13, [&]() -> PyObject* {
+  return guarded("paged_kv_append", n, n == 13 ? 13 : 15, [&]() -> PyObject* {
     const bool interleaved = truth(a[9], "interleaved");
     const at::Tensor& k = tensor(a[0], "k");
     if (k.dim() != 3) refuse(ASV_ERR_SHAPE, "k and v must be [N, kv_heads, head_dim]");
@@ -248,11 +248,32 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       rot = {static_cast<const float*>(t.data_ptr()), extent(t.size(1), "the rotation's dim"),
              extent(t.size(0), "max_position"), interleaved};
     }
+    asv_positions at = {};
+    const bool placed = n > 13 && a[13] != Py_None;
+    if (placed) {
+      const at::Tensor& t = tensor(a[13], "positions");
+      if (t.scalar_type() != at::kInt) refuse(ASV_ERR_DTYPE, "positions must be int32");
+      if ((t.dim() != 1 && t.dim() != 2) || t.size(-1) != p.batch.N || (t.size(-1) > 1 && t.stride(-1) != 1) ||
+          t.device() != p.device)
+        refuse(ASV_ERR_SHAPE, "positions must be [axes, %d] or [%d], each axis's contiguous, on the tensors' device", p.batch.N,
+               p.batch.N);
+      at.at = static_cast<const int32_t*>(t.data_ptr());
+      at.axes = t.dim() == 1 ? 1 : extent(t.size(0), "axes");
+      at.stride_axis = t.dim() == 1 ? 0 : t.stride(0);
+    }
+    if (n > 13 && a[14] != Py_None) {
+      if (!placed || !rotate) refuse(ASV_ERR_PARAM, "axes go with positions and a rotation");
+      if (!PyBytes_Check(a[14]) || PyBytes_GET_SIZE(a[14]) != rot.dim / 2)
+        refuse(ASV_ERR_PARAM, "axes must be the axis of each of the rotation's %d pairs", rot.dim / 2);
+      at.axis_of_pair = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[14]));
+    } else if (placed && at.axes != 1) {
+      refuse(ASV_ERR_PARAM, "positions of several axes need axes=, the axis of each pair");
+    }
     uint32_t* status = status_of(tensor(a[11], "req_status"), p);
     const cudaStream_t stream = stream_of(a[12]);
     return result(unlocked([&]() {
                     return g_append(&p.cache, &p.batch, &kr, &vr, with_q ? &qr : nullptr, with_q ? &oq : nullptr, heads,
-                                    rotate ? &rot : nullptr, status, stream);
+                                    rotate ? &rot : nullptr, placed ? &at : nullptr, status, stream);
                   }),
                   "paged_kv_append");
   });
