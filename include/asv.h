@@ -88,10 +88,13 @@ typedef enum {
                                 keeps every CTA resident, and no CTA of paged_attention waits for another, so
                                 this marks a fault, not a load condition): the request's outputs are
                                 unspecified and the workspace must be zero-filled again */
-#define ASV_REQ_BAD_PAGE 8u  /* a block-table entry the request needs lies outside [0, num_pages) */
+#define ASV_REQ_BAD_PAGE 8u  /* a block-table entry the request needs lies outside [0, num_pages); paged_plan: an
+                                entry is negative, or the pool's count or the pages given back do not fit the pool */
 #define ASV_REQ_BAD_LEN 16u  /* indptr is not 0 <= start <= end <= N, cache_len is negative, or the tokens go
                                 past the block table's last page or the rotation table's last row; a position
-                                given for the rotation lies outside its table */
+                                given for the rotation lies outside its table; paged_plan: a length is negative
+                                or needs more pages than are held (what is cached) or fit the table (what is new) */
+#define ASV_REQ_NO_ROOM 32u  /* paged_plan: the pool has no pages, or the step no rows, for the request's new tokens */
 
 /* Human-readable name of a status code (static string). */
 const char* asv_status_string(asv_status s);
@@ -499,6 +502,43 @@ asv_status paged_kv_append_ex(const asv_paged_cache* cache, const asv_paged_batc
                               const asv_rows* v, const asv_rows* q, const asv_rows* out_q, int q_heads,
                               const asv_rotary* rotary, const asv_positions* positions, uint32_t* out_req_status,
                               cudaStream_t stream);
+
+/* The pages of a cache and who holds them, all on the device and all updated by paged_plan.  Request b holds the pages
+ * block_table[b, 0 .. held[b] - 1]; the pool is a stack, free_pages[0 .. free_count[0] - 1] of its pool_size entries.
+ * A new pool: held 0, every page in free_pages, free_count their number. */
+typedef struct {
+  int32_t* block_table;
+  int max_pages;
+  int64_t block_table_stride; /* at least max_pages */
+  int page_size;              /* 1 or more */
+  int32_t* held;              /* [B] */
+  int32_t* free_pages;        /* [pool_size] */
+  int pool_size;
+  int32_t* free_count;        /* [1] */
+} asv_page_pool;
+
+/*
+ * paged_plan -- pages for a step's new tokens, and where its packed rows go: what paged_kv_append and paged_attention
+ * take, without a host round trip.  For each request, in order:
+ *  - release (may be NULL) [b] not 0: its former occupant has ended.  The pages held go onto the pool, in request and
+ *    table order, their entries become -1, and nothing is held; cache_len[b] is the new occupant's, 0.
+ *  - it needs max(0, ceil((cache_len[b] + new_len[b]) / page_size) - held[b]) pages.  Requests are served first come
+ *    first served: b is, where what requests 0 .. b need together fits the pool (or b needs none) and their new tokens
+ *    fit N rows.  Served requests' pages come from the pool's top, in request and table order.  One that is not is
+ *    flagged ASV_REQ_NO_ROOM, takes no rows and no pages and keeps what it holds (room asked for is not passed on to
+ *    requests behind it).  Pages already held for more tokens (rejected drafts') stay.
+ *  - 0 <= cache_len[b] <= held[b] * page_size and new_len[b] >= 0, with all its tokens within max_pages; otherwise it is
+ *    flagged ASV_REQ_BAD_LEN and left out in the same way.
+ * out_indptr [B + 1]: the packed rows of the served requests.  For each of the N rows out_slots (page * page_size + slot
+ * within it), out_positions (cache_len[b] + i) and out_requests (b), -1 in all three for rows behind the last; each may
+ * be NULL.  cache_len and new_len are not changed.  ASV_REQ_* bits are ORed into out_req_status [B].  A pool whose count is
+ * not within [0, pool_size] flags every request ASV_REQ_BAD_PAGE and changes nothing.  The buffers must not overlap.
+ * B <= 16384.  One launch.  Checks: sizes (ASV_ERR_SHAPE); for B > 0 alignment (4 bytes, out_slots 8: ASV_ERR_ALIGN), the
+ * required pointers (ASV_ERR_NULL).
+ */
+asv_status paged_plan(const int32_t* cache_len, const int32_t* new_len, int B, const asv_page_pool* pool,
+                      const uint8_t* release, int N, int32_t* out_indptr, int64_t* out_slots, int32_t* out_positions,
+                      int32_t* out_requests, uint32_t* out_req_status, cudaStream_t stream);
 
 /*
  * paged_attention -- attention of the chunk's queries over the cache, the chunk's own tokens (already

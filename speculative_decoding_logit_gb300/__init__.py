@@ -17,6 +17,8 @@ Entry points (same names as the C ABI):
                          Inference with Retrieval-Augmented Speculative Decoding", Key designs 2-4)
   sci_verify             E2-SCI JSD test against an adaptive threshold ("E2-SCI: Elastic
                          Edge-Cloud Speculative Decoding via Credit Inertia", Key design 3)
+  paged_plan             pages for a step's new tokens out of a pool on the device, block tables, the packed rows'
+                         slots and positions
   paged_kv_append        the new tokens' keys and values into a paged cache, rotated on the way
   paged_attention        attention of a chunk of new tokens (one, K + 1 drafts, a prompt) over that
                          cache: the forwards whose logits the verification takes
@@ -41,9 +43,11 @@ from ._binding import (  # noqa: F401
     asymspec_verify_sweep,
     PagedAppendOutput,
     PagedAttentionOutput,
+    PagedPlanOutput,
     REQ_BAD_DRAFT,
     REQ_BAD_LEN,
     REQ_BAD_PAGE,
+    REQ_NO_ROOM,
     REQ_NONFINITE,
     REQ_TIMEOUT,
     AsvError,
@@ -63,6 +67,7 @@ from ._binding import (  # noqa: F401
     clear_workspaces,
     paged_attention,
     paged_kv_append,
+    paged_plan,
     paged_workspace_bytes,
     query_plan,
     rapid_verify,

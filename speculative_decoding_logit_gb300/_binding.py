@@ -25,6 +25,7 @@ REQ_BAD_DRAFT = 2
 REQ_TIMEOUT = 4
 REQ_BAD_PAGE = 8
 REQ_BAD_LEN = 16
+REQ_NO_ROOM = 32
 
 _STATUS = {0: "ASV_OK", 1: "ASV_ERR_NULL", 2: "ASV_ERR_SHAPE", 3: "ASV_ERR_ALIGN", 4: "ASV_ERR_DTYPE",
            5: "ASV_ERR_PARAM", 6: "ASV_ERR_WORKSPACE", 7: "ASV_ERR_CUDA"}
@@ -101,6 +102,12 @@ class _RowsC(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_token", C.c_int64), ("stride_head", C.c_int64)]
 
 
+class _PagePoolC(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("max_pages", C.c_int), ("block_table_stride", C.c_int64),
+                ("page_size", C.c_int), ("held", C.c_void_p), ("free_pages", C.c_void_p), ("pool_size", C.c_int),
+                ("free_count", C.c_void_p)]
+
+
 class _PositionsC(C.Structure):
     _fields_ = [("at", C.c_void_p), ("axes", C.c_int), ("stride_axis", C.c_int64), ("axis_of_pair", C.c_char_p)]
 
@@ -158,6 +165,8 @@ def _declare(L):
     L.paged_kv_append.restype = _i
     L.paged_kv_append_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]
     L.paged_kv_append_ex.restype = _i
+    L.paged_plan.argtypes = [_vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.paged_plan.restype = _i
     L.asv_paged_workspace_bytes.argtypes = [_i, _i, _i]
     L.asv_paged_workspace_bytes.restype = _sz
     L.paged_attention.argtypes = [_vp, _vp, _vp, _vp, _i, _f, _i, _vp, _vp, _vp, _sz, _vp]
@@ -639,6 +648,7 @@ def _paged_ext():
             loader.exec_module(ext)
             ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append_ex,
                                                                         L.asv_status_string, L.asv_last_cuda_error)))
+            ext.bind_step(C.cast(L.paged_plan, C.c_void_p).value)
             _ext = ext
     return _ext
 
@@ -686,7 +696,50 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
             None if q is None else torch.empty(q.shape, dtype=q.dtype, device=dev),
             torch.zeros(cache_len.shape, dtype=torch.int32, device=dev))))
     (_ext or _paged_ext()).paged_kv_append(k, v, k_cache, v_cache, block_table, cache_len, indptr, q, rotary,
-                                           interleaved, out.q, out.req_status, handle, positions, axes)
+                                           interleaved, out.q, out.req_status, positions, axes, handle)
+    return out
+
+
+@dataclass
+class PagedPlanOutput:
+    indptr: torch.Tensor               # [B + 1] int32
+    slots: Optional[torch.Tensor]      # [N] int64: page * page_size + slot within it (-1 behind the last row; may be None)
+    positions: Optional[torch.Tensor]  # [N] int32 (the same)
+    requests: Optional[torch.Tensor]   # [N] int32 (the same)
+    req_status: torch.Tensor           # [B] int32 (ASV_REQ_* bits, ORed in)
+
+
+def paged_plan(cache_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, held: torch.Tensor,
+               free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, *,
+               release: Optional[torch.Tensor] = None, max_tokens: Optional[int] = None,
+               out: Optional[PagedPlanOutput] = None, stream=None) -> PagedPlanOutput:
+    """Pages for new_len[b] tokens behind cache_len[b] of every request, out of a pool on the device, and the packed
+    rows' places (paged_plan in include/asv.h): block_table [B, max_pages], held [B], the stack free_pages and its
+    free_count [1] (all int32) are updated in place, `release` [B] bool first gives back what ended requests hold.  The
+    rows are `max_tokens`, or those of `out`.  cache_len is not advanced.  `stream` as for paged_kv_append."""
+    handle = _raw_stream(block_table, stream)
+    if handle is None:
+        with torch.cuda.device(block_table.device):
+            return paged_plan(cache_len, new_len, block_table, held, free_pages, free_count, page_size,
+                              release=release, max_tokens=max_tokens, out=out, stream=stream)
+    if out is None:
+        if max_tokens is None:
+            raise AsvError(5, "max_tokens (the rows of the step) or out must be given")
+        if not isinstance(max_tokens, int) or max_tokens < 0:
+            raise AsvError(2, "max_tokens must be a whole number, 0 or more")
+        i32 = dict(dtype=torch.int32, device=block_table.device)
+        B = block_table.shape[0]
+        out = PagedPlanOutput(*_made_on(stream, lambda: (
+            torch.zeros(B + 1, **i32), torch.empty(max_tokens, dtype=torch.int64, device=block_table.device),
+            torch.empty(max_tokens, **i32), torch.empty(max_tokens, **i32), torch.zeros(B, **i32))))
+    elif max_tokens is None:
+        rows = next((t for t in (out.slots, out.positions, out.requests) if t is not None), None)
+        if rows is None:
+            raise AsvError(5, "max_tokens must be given where out has no rows")
+        max_tokens = rows.shape[0] if rows.dim() else 0
+    (_ext or _paged_ext()).paged_plan(cache_len, new_len, block_table, held, free_pages, free_count, page_size, release,
+                                      out.indptr, out.slots, out.positions, out.requests, out.req_status, max_tokens,
+                                      handle)
     return out
 
 

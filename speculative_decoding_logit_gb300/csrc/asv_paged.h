@@ -58,6 +58,27 @@ struct AttendArgs {
   uint32_t* check_log;
 };
 
+struct PlanArgs {
+  const int32_t* cache_len;
+  const int32_t* new_len;
+  int B, N;
+  int32_t* table;
+  int max_pages;
+  long long table_stride;
+  int page_size;
+  int32_t* held;
+  int32_t* free_pages;
+  int pool;  // entries of free_pages
+  int32_t* free_count;
+  const uint8_t* release;  // nullptr: none
+  int32_t* indptr;
+  int64_t* slots;       // these three: nullptr, not wanted
+  int32_t* positions;
+  int32_t* requests;
+  uint32_t* status;
+  uint32_t* check_log;  // of the checked build: the plan has no workspace, its log is the library's
+};
+
 // paged_attention's workspace: tickets (zero between calls), then each CTA's two partial results of up
 // to two row tiles (unnormalised outputs, then row maxima and sums).
 constexpr int kPagedMaxGrid = 152;
@@ -68,6 +89,8 @@ inline size_t paged_workspace_bytes(int head_dim) {
   return kPagedTicketBytes + kPagedSlots * 2 * paged_part_floats(head_dim <= 64 ? 64 : 128) * sizeof(float);
 }
 
+constexpr int kPlanMaxRequests = 16384;  // three words each in one CTA's shared memory
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_paged_attention(const AttendArgs& a, int dtype, cudaStream_t s);
 

@@ -130,6 +130,46 @@ asv_status paged_kv_append_ex(const asv_paged_cache* cache, const asv_paged_batc
   return e == cudaSuccess ? ASV_OK : asv::record_cuda_error(e);
 }
 
+asv_status paged_plan(const int32_t* cache_len, const int32_t* new_len, int B, const asv_page_pool* pool,
+                      const uint8_t* release, int N, int32_t* out_indptr, int64_t* out_slots, int32_t* out_positions,
+                      int32_t* out_requests, uint32_t* out_req_status, cudaStream_t stream) {
+  if (!pool) return ASV_ERR_NULL;
+  const asv_page_pool& p = *pool;
+  if (B < 0 || B > asv::kPlanMaxRequests || N < 0 || p.max_pages < 0 || p.pool_size < 0 || p.page_size < 1 ||
+      (long long)p.max_pages * p.page_size > 0x7fff0000LL)
+    return ASV_ERR_SHAPE;
+  if (B == 0) return ASV_OK;
+  if (B > 1 && p.max_pages > 0 && p.block_table_stride < p.max_pages) return ASV_ERR_SHAPE;  // rows that overlap
+  if (!aligned(cache_len, 4) || !aligned(new_len, 4) || !aligned(p.block_table, 4) || !aligned(p.held, 4) ||
+      !aligned(p.free_pages, 4) || !aligned(p.free_count, 4) || !aligned(out_indptr, 4) || !aligned(out_slots, 8) ||
+      !aligned(out_positions, 4) || !aligned(out_requests, 4) || !aligned(out_req_status, 4))
+    return ASV_ERR_ALIGN;
+  if (!cache_len || !new_len || (p.max_pages > 0 && !p.block_table) || !p.held || (p.pool_size > 0 && !p.free_pages) ||
+      !p.free_count || !out_indptr || !out_req_status)
+    return ASV_ERR_NULL;
+  asv::PlanArgs a = {};
+  a.cache_len = cache_len;
+  a.new_len = new_len;
+  a.B = B;
+  a.N = N;
+  a.table = p.block_table;
+  a.max_pages = p.max_pages;
+  a.table_stride = p.block_table_stride;
+  a.page_size = p.page_size;
+  a.held = p.held;
+  a.free_pages = p.free_pages;
+  a.pool = p.pool_size;
+  a.free_count = p.free_count;
+  a.release = release;
+  a.indptr = out_indptr;
+  a.slots = out_slots;
+  a.positions = out_positions;
+  a.requests = out_requests;
+  a.status = out_req_status;
+  cudaError_t e = asv::launch_paged_plan(a, stream);
+  return e == cudaSuccess ? ASV_OK : asv::record_cuda_error(e);
+}
+
 size_t asv_paged_workspace_bytes(int q_heads, int kv_heads, int head_dim) {
   if (kv_heads < 1 || q_heads < kv_heads || head_dim < 1 || head_dim > 128) return 0;
   return asv::paged_workspace_bytes(head_dim) + asv::kCheckLogBytes;

@@ -1,7 +1,7 @@
-// asv_torch.cpp -- the paged-cache calls of the Python binding: checks of the tensors and their marshalling to
-// the C entry points, in C++ because they are made for every layer of every step (as Python code over ctypes the
-// two took 6 us a call, of 10 in all).  A CPython module: asv_torch.paged_attention(...) and
-// asv_torch.paged_kv_append(...), positional arguments only; failures raise the binding's AsvError.
+// asv_torch.cpp -- the paged-cache calls of the Python binding, and the sampling's: checks of the tensors and their
+// marshalling to the C entry points, in C++ because they are made for every layer of every step (as Python code over
+// ctypes the first two took 6 us a call, of 10 in all).  A CPython module: asv_torch.paged_attention(...),
+// paged_kv_append(...) and so on, positional arguments only; failures raise the binding's AsvError.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -20,6 +20,7 @@ namespace {
 PyObject* g_error = nullptr;  // AsvError(status, message)
 decltype(&paged_attention) g_attention = nullptr;
 decltype(&paged_kv_append_ex) g_append = nullptr;
+decltype(&paged_plan) g_plan = nullptr;
 decltype(&asv_status_string) g_status_string = nullptr;
 decltype(&asv_last_cuda_error) g_last_cuda_error = nullptr;
 
@@ -219,7 +220,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // k, v, k_cache, v_cache, block_table, cache_len, indptr, q (or None), rotary (or None), interleaved, out_q (or
-// None), req_status, stream, and with them or not: positions (or None), axes (bytes, or None)
+// None), req_status, (these two or neither: positions (or None), axes (bytes, or None)), stream
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_kv_append", n, n == 13 ? 13 : 15, [&]() -> PyObject* {
     const bool interleaved = truth(a[9], "interleaved");
@@ -249,9 +250,9 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
              extent(t.size(0), "max_position"), interleaved};
     }
     asv_positions at = {};
-    const bool placed = n > 13 && a[13] != Py_None;
+    const bool placed = n > 13 && a[12] != Py_None;
     if (placed) {
-      const at::Tensor& t = tensor(a[13], "positions");
+      const at::Tensor& t = tensor(a[12], "positions");
       if (t.scalar_type() != at::kInt) refuse(ASV_ERR_DTYPE, "positions must be int32");
       if ((t.dim() != 1 && t.dim() != 2) || t.size(-1) != p.batch.N || (t.size(-1) > 1 && t.stride(-1) != 1) ||
           t.device() != p.device)
@@ -261,21 +262,80 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       at.axes = t.dim() == 1 ? 1 : extent(t.size(0), "axes");
       at.stride_axis = t.dim() == 1 ? 0 : t.stride(0);
     }
-    if (n > 13 && a[14] != Py_None) {
+    if (n > 13 && a[13] != Py_None) {
       if (!placed || !rotate) refuse(ASV_ERR_PARAM, "axes go with positions and a rotation");
-      if (!PyBytes_Check(a[14]) || PyBytes_GET_SIZE(a[14]) != rot.dim / 2)
+      if (!PyBytes_Check(a[13]) || PyBytes_GET_SIZE(a[13]) != rot.dim / 2)
         refuse(ASV_ERR_PARAM, "axes must be the axis of each of the rotation's %d pairs", rot.dim / 2);
-      at.axis_of_pair = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[14]));
+      at.axis_of_pair = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[13]));
     } else if (placed && at.axes != 1) {
       refuse(ASV_ERR_PARAM, "positions of several axes need axes=, the axis of each pair");
     }
     uint32_t* status = status_of(tensor(a[11], "req_status"), p);
-    const cudaStream_t stream = stream_of(a[12]);
+    const cudaStream_t stream = stream_of(a[n - 1]);
     return result(unlocked([&]() {
                     return g_append(&p.cache, &p.batch, &kr, &vr, with_q ? &qr : nullptr, with_q ? &oq : nullptr, heads,
                                     rotate ? &rot : nullptr, placed ? &at : nullptr, status, stream);
                   }),
                   "paged_kv_append");
+  });
+}
+
+// A tensor of `type` on `device` with `n` entries in a row; None: nullptr.
+void* entries(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t n, at::Device device) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != type) refuse(ASV_ERR_DTYPE, "%s must be %s", name, type_name);
+  if (t.dim() != 1 || t.size(0) != n || (n > 1 && t.stride(0) != 1))
+    refuse(ASV_ERR_SHAPE, "%s must be contiguous, [%lld]", name, (long long)n);
+  if (t.device() != device) refuse(ASV_ERR_SHAPE, "the tensors must be on one device");
+  return t.data_ptr();
+}
+
+// cache_len, new_len, block_table, held, free_pages, free_count, page_size, release (or None), indptr, slots (or None),
+// positions (or None), requests (or None), req_status, N, stream
+PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("paged_plan", n, 15, [&]() -> PyObject* {
+    const at::Tensor& table = tensor(a[2], "block_table");
+    if (table.scalar_type() != at::kInt) refuse(ASV_ERR_DTYPE, "block_table must be int32");
+    if (table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
+      refuse(ASV_ERR_SHAPE, "block_table must be [B, max_pages], its rows contiguous");
+    const at::Device dev = table.device();
+    const int64_t B = table.size(0);
+    const at::Tensor& pool = tensor(a[4], "free_pages");
+    const long long page = whole_number(a[6], "page_size"), rows = whole_number(a[13], "max_tokens");
+    if (rows < 0 || rows > 0x7fffffff) refuse(ASV_ERR_SHAPE, "max_tokens must be a whole number of 32 bits, 0 or more");
+    if (page < 1 || page > 0x7fffffff) refuse(ASV_ERR_SHAPE, "page_size must be a whole number of 32 bits, 1 or more");
+    auto ints = [&](int i, const char* name, int64_t len) {
+      return static_cast<int32_t*>(entries(a[i], name, at::kInt, "int32", len, dev));
+    };
+    auto present = [&](int i, const char* name, int64_t len) {
+      int32_t* p = ints(i, name, len);
+      if (a[i] == Py_None) refuse(ASV_ERR_NULL, "%s is missing", name);
+      return p;
+    };
+    const asv_page_pool p = {static_cast<int32_t*>(table.data_ptr()),
+                             extent(table.size(1), "max_pages"),
+                             table.stride(0),
+                             int(page),
+                             present(3, "held", B),
+                             present(4, "free_pages", pool.dim() == 1 ? pool.size(0) : -1),
+                             extent(pool.dim() == 1 ? pool.size(0) : 0, "free_pages"),
+                             present(5, "free_count", 1)};
+    const int32_t* len = present(0, "cache_len", B);
+    const int32_t* grow = present(1, "new_len", B);
+    const uint8_t* release = static_cast<const uint8_t*>(entries(a[7], "release", at::kBool, "bool", B, dev));
+    int32_t* indptr = present(8, "out.indptr", B + 1);
+    int64_t* slots = static_cast<int64_t*>(entries(a[9], "out.slots", at::kLong, "int64", rows, dev));
+    int32_t* positions = ints(10, "out.positions", rows);
+    int32_t* requests = ints(11, "out.requests", rows);
+    uint32_t* status = reinterpret_cast<uint32_t*>(present(12, "out.req_status", B));
+    const int requests_in = extent(B, "B");
+    const cudaStream_t stream = stream_of(a[14]);
+    return result(unlocked([&]() {
+                    return g_plan(len, grow, requests_in, &p, release, int(rows), indptr, slots, positions, requests, status,
+                                  stream);
+                  }),
+                  "paged_plan");
   });
 }
 
@@ -294,8 +354,18 @@ PyObject* py_bind(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+// the address of paged_plan
+PyObject* py_bind_step(PyObject*, PyObject* args) {
+  unsigned long long f[1];
+  if (!PyArg_ParseTuple(args, "K", &f[0])) return nullptr;
+  g_plan = reinterpret_cast<decltype(g_plan)>(f[0]);
+  Py_RETURN_NONE;
+}
+
 PyMethodDef kMethods[] = {
     {"bind", py_bind, METH_VARARGS, nullptr},
+    {"bind_step", py_bind_step, METH_VARARGS, nullptr},
+    {"paged_plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_plan)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_attention)), METH_FASTCALL, nullptr},
     {"paged_kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_append)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
