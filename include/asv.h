@@ -96,6 +96,8 @@ typedef enum {
                                 or needs more pages than are held (what is cached) or fit the table (what is new) */
 #define ASV_REQ_NO_ROOM 32u  /* paged_plan: the pool has no pages, or the step no rows, for the request's new tokens */
 
+#define ASV_REQ_BAD_PARAM 64u /* sample_tokens: the request's own temperature, top-k, top-p or min-p is out of range */
+
 /* Human-readable name of a status code (static string). */
 const char* asv_status_string(asv_status s);
 
@@ -401,6 +403,65 @@ asv_status asymspec_sci_verify(const void* a, const void* b, const void* t, int 
                                float* out_lse, int32_t* out_sci_accept_len, int32_t* out_sci_tokens, float* out_jsd,
                                float* out_T, uint32_t* out_req_status, void* workspace, size_t ws_bytes,
                                cudaStream_t stream);
+
+/* ------------------------------------------------------------------ token sampling
+ *
+ * What a drafter does with its logits: the tokens that the verification checks, and for RAPID ([RAPID] Workflow: drafts are
+ * drawn from q) the distribution they were drawn from.
+ */
+
+/* Rows of V contiguous logits (ASV_F32 or ASV_BF16, any alignment of the element): B requests of n positions each, strides
+ * in elements, 0 or more (not looked at for an extent of 1). */
+typedef struct {
+  const void* data;
+  int dtype;
+  int B, n, V;
+  int64_t stride_request, stride_position;
+} asv_logits;
+
+/* A [B, n] field of 4-byte elements, or rows of V of them, at strides in elements. */
+typedef struct {
+  void* data;
+  int64_t stride_request, stride_position;
+} asv_field;
+
+/* temperature: 0 (the largest logit, the lowest index among equals) or 2^-64 .. 2^64; top_k: 0 (off) or more; top_p: 0 .. 1
+ * (1: off); min_p: 0 (off) .. 1. */
+typedef struct {
+  float temperature;
+  int top_k;
+  float top_p, min_p;
+} asv_sampling;
+
+/* The same for each request: [B] on the device, NULL: the call's one value. */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} asv_sampling_each;
+
+/*
+ * sample_tokens -- a token for every row x of logits.  With w_i = exp((x_i - max x) / temperature) and the entries in order
+ * (value descending, index ascending among equal values):
+ *   top_k  keeps the first top_k;
+ *   top_p  of these the ones before which less than top_p of their mass lies;
+ *   min_p  those with w_i >= min_p;
+ * the first is always kept.  The token is the lowest kept index i with  sum of w over kept indices <= i  >  u * W,  W the
+ * kept mass; u is a number from [0, 1) that the caller draws (one outside counts as the nearest in it, NaN as 0).  Sums are
+ * exact to about 2^-39 of the largest weight, so a token differs from exact arithmetic's only where a border is that near;
+ * the result does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.  out_probs
+ * (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere.  With temperature 0: 0, and 1 at the token.
+ * Inputs may share memory, outputs not with anything; rows of out_probs need no alignment but the element's.
+ * A row with NaN or +inf, or all -inf, flags its request ASV_REQ_NONFINITE (a single -inf is probability 0), a request's
+ * own parameter out of range ASV_REQ_BAD_PARAM; the row's token is then -1, its log-probability -inf, its distribution 0.
+ * Flags are ORed into out_req_status [B].  V <= 2^19.  No workspace.
+ * Checks: sizes and strides (ASV_ERR_SHAPE; outputs whose rows overlap among them), the element type (ASV_ERR_DTYPE), for
+ * B > 0 and n > 0: parameters (ASV_ERR_PARAM), alignment (ASV_ERR_ALIGN), the required pointers (ASV_ERR_NULL).
+ */
+asv_status sample_tokens(const asv_logits* logits, const asv_field* u, const asv_sampling* params,
+                         const asv_sampling_each* each, const asv_field* out_tokens, const asv_field* out_logprobs,
+                         const asv_field* out_probs, uint32_t* out_req_status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------ paged key/value cache
  *

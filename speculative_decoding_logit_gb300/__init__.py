@@ -17,6 +17,8 @@ Entry points (same names as the C ABI):
                          Inference with Retrieval-Augmented Speculative Decoding", Key designs 2-4)
   sci_verify             E2-SCI JSD test against an adaptive threshold ("E2-SCI: Elastic
                          Edge-Cloud Speculative Decoding via Credit Inertia", Key design 3)
+  sample_tokens          tokens drawn from logits by given random numbers (temperature, top-k, top-p, min-p), and the
+                         distributions they are drawn from
   paged_plan             pages for a step's new tokens out of a pool on the device, block tables, the packed rows'
                          slots and positions
   paged_kv_append        the new tokens' keys and values into a paged cache, rotated on the way
@@ -47,6 +49,7 @@ from ._binding import (  # noqa: F401
     REQ_BAD_DRAFT,
     REQ_BAD_LEN,
     REQ_BAD_PAGE,
+    REQ_BAD_PARAM,
     REQ_NO_ROOM,
     REQ_NONFINITE,
     REQ_TIMEOUT,
@@ -54,6 +57,7 @@ from ._binding import (  # noqa: F401
     AsymSpecOutput,
     RapidOutput,
     SciOutput,
+    SampleOutput,
     SciParams,
     SciStabilisers,
     TAIL_KEEP_P,
@@ -71,6 +75,7 @@ from ._binding import (  # noqa: F401
     paged_workspace_bytes,
     query_plan,
     rapid_verify,
+    sample_tokens,
     sci_state_decode,
     sci_state_new,
     sci_verify,

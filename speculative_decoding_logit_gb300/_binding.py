@@ -26,6 +26,7 @@ REQ_TIMEOUT = 4
 REQ_BAD_PAGE = 8
 REQ_BAD_LEN = 16
 REQ_NO_ROOM = 32
+REQ_BAD_PARAM = 64
 
 _STATUS = {0: "ASV_OK", 1: "ASV_ERR_NULL", 2: "ASV_ERR_SHAPE", 3: "ASV_ERR_ALIGN", 4: "ASV_ERR_DTYPE",
            5: "ASV_ERR_PARAM", 6: "ASV_ERR_WORKSPACE", 7: "ASV_ERR_CUDA"}
@@ -102,6 +103,23 @@ class _RowsC(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_token", C.c_int64), ("stride_head", C.c_int64)]
 
 
+class _LogitsC(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("dtype", C.c_int), ("B", C.c_int), ("n", C.c_int), ("V", C.c_int),
+                ("stride_request", C.c_int64), ("stride_position", C.c_int64)]
+
+
+class _FieldC(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_request", C.c_int64), ("stride_position", C.c_int64)]
+
+
+class _SamplingC(C.Structure):
+    _fields_ = [("temperature", C.c_float), ("top_k", C.c_int), ("top_p", C.c_float), ("min_p", C.c_float)]
+
+
+class _SamplingEachC(C.Structure):
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p)]
+
+
 class _PagePoolC(C.Structure):
     _fields_ = [("block_table", C.c_void_p), ("max_pages", C.c_int), ("block_table_stride", C.c_int64),
                 ("page_size", C.c_int), ("held", C.c_void_p), ("free_pages", C.c_void_p), ("pool_size", C.c_int),
@@ -165,6 +183,8 @@ def _declare(L):
     L.paged_kv_append.restype = _i
     L.paged_kv_append_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]
     L.paged_kv_append_ex.restype = _i
+    L.sample_tokens.argtypes = [_vp] * 9
+    L.sample_tokens.restype = _i
     L.paged_plan.argtypes = [_vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]
     L.paged_plan.restype = _i
     L.asv_paged_workspace_bytes.argtypes = [_i, _i, _i]
@@ -615,6 +635,39 @@ def sci_verify(draft: torch.Tensor, target: torch.Tensor, draft_ids: torch.Tenso
     return out
 
 
+# ------------------------------------------------------------------ token sampling
+
+@dataclass
+class SampleOutput:
+    tokens: torch.Tensor              # [B, n] (or [B], as the logits) int32, -1 where the row's request is flagged for it
+    logprobs: Optional[torch.Tensor]  # [B, n] float32: the tokens' log-probabilities (may be None)
+    probs: Optional[torch.Tensor]     # [B, n, V] float32: the distributions drawn from (may be None)
+    req_status: torch.Tensor          # [B] int32 (ASV_REQ_* bits, ORed in)
+
+
+def sample_tokens(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                  probs: bool = False, out: Optional[SampleOutput] = None, stream=None) -> SampleOutput:
+    """A token for every row of logits [B, n, V] (or [B, V]; float32 or bfloat16, rows contiguous at any strides), drawn by
+    the given uniform numbers u [B, n] ([B]) float32 after temperature, top-k, top-p and min-p (sample_tokens in
+    include/asv.h).  Each parameter is a number or a tensor [B] (int32 top_k, else float32) on the logits' device.
+    `probs` makes room for the distributions too; the tensors of `out` may have any strides, so RAPID's q and draft ids can
+    be filled a position at a time.  `stream` as for paged_kv_append."""
+    handle = _raw_stream(logits, stream)
+    if handle is None:
+        with torch.cuda.device(logits.device):
+            return sample_tokens(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, probs=probs,
+                                 out=out, stream=stream)
+    if out is None:
+        dev, rows = logits.device, logits.shape[:-1]
+        out = SampleOutput(*_made_on(stream, lambda: (
+            torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev),
+            torch.empty(logits.shape, dtype=torch.float32, device=dev) if probs else None,
+            torch.zeros(logits.shape[:1], dtype=torch.int32, device=dev))))
+    (_ext or _paged_ext()).sample_tokens(logits, u, temperature, top_k, top_p, min_p, out.tokens, out.logprobs, out.probs,
+                                         out.req_status, handle)
+    return out
+
+
 # ------------------------------------------------------------------ paged key/value cache
 
 @dataclass
@@ -648,7 +701,7 @@ def _paged_ext():
             loader.exec_module(ext)
             ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append_ex,
                                                                         L.asv_status_string, L.asv_last_cuda_error)))
-            ext.bind_step(C.cast(L.paged_plan, C.c_void_p).value)
+            ext.bind_step(*(C.cast(f, C.c_void_p).value for f in (L.paged_plan, L.sample_tokens)))
             _ext = ext
     return _ext
 

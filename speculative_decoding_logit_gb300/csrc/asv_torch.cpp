@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <exception>
 #include <initializer_list>
+#include <type_traits>
 
 #include "asv.h"
 
@@ -21,6 +22,7 @@ PyObject* g_error = nullptr;  // AsvError(status, message)
 decltype(&paged_attention) g_attention = nullptr;
 decltype(&paged_kv_append_ex) g_append = nullptr;
 decltype(&paged_plan) g_plan = nullptr;
+decltype(&sample_tokens) g_sample = nullptr;
 decltype(&asv_status_string) g_status_string = nullptr;
 decltype(&asv_last_cuda_error) g_last_cuda_error = nullptr;
 
@@ -354,17 +356,98 @@ PyObject* py_bind(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
-// the address of paged_plan
+// A [B, n] or [B] field (or with V > 0 rows of V: one dimension more) of `type`.
+asv_field field(const at::Tensor& t, const char* name, at::ScalarType type, const char* type_name, int64_t dims, int64_t B,
+                int64_t n, int64_t V, at::Device device) {
+  if (t.scalar_type() != type) refuse(ASV_ERR_DTYPE, "%s must be %s", name, type_name);
+  const int64_t d = dims + (V > 0 ? 1 : 0);
+  if (t.dim() != d || t.size(0) != B || (dims == 2 && t.size(1) != n) || (V > 0 && t.size(d - 1) != V))
+    refuse(ASV_ERR_SHAPE, "%s has the wrong shape: one entry%s for each row of logits", name, V > 0 ? " of the vocabulary" : "");
+  if (V > 1 && t.stride(d - 1) != 1) refuse(ASV_ERR_SHAPE, "the last dimension of %s must be contiguous", name);
+  if (t.device() != device) refuse(ASV_ERR_SHAPE, "the tensors must be on one device");
+  return {t.data_ptr(), t.stride(0), dims == 2 ? t.stride(1) : 0};
+}
+
+// A number, or a tensor [B] of its own for each request.
+template <class Number>
+void parameter(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t B, at::Device device,
+               Number* one, const Number** each) {
+  if (THPVariable_Check(o)) {
+    *each = static_cast<const Number*>(entries(o, name, type, type_name, B, device));
+    return;
+  }
+  if constexpr (std::is_integral_v<Number>) {
+    const long long v = whole_number(o, name);
+    if (v < 0 || v > 0x7fffffff) refuse(ASV_ERR_PARAM, "%s must be a whole number of 32 bits, 0 or more", name);
+    *one = Number(v);
+  } else {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse(ASV_ERR_PARAM, "%s must be a number or a tensor", name);
+    }
+    *one = Number(v);
+  }
+}
+
+// logits, u, temperature, top_k, top_p, min_p (each a number or a tensor [B]), tokens, logprobs (or None), probs (or
+// None), req_status, stream
+PyObject* py_sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("sample_tokens", n, 11, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[0], "logits");
+    const int64_t dims = x.dim() - 1;
+    if (dims != 1 && dims != 2) refuse(ASV_ERR_SHAPE, "logits must be [B, n, V] or [B, V]");
+    const at::Device dev = x.device();
+    const int64_t B = x.size(0), rows = dims == 2 ? x.size(1) : 1, V = x.size(dims);
+    asv_logits l = {};
+    if (x.scalar_type() == at::kFloat) l.dtype = ASV_F32;
+    else if (x.scalar_type() == at::kBFloat16) l.dtype = ASV_BF16;
+    else refuse(ASV_ERR_DTYPE, "logits must be float32 or bfloat16");
+    if (V < 1 || (V > 1 && x.stride(dims) != 1)) refuse(ASV_ERR_SHAPE, "the last dimension of logits must be contiguous and not empty");
+    l.data = x.data_ptr();
+    l.B = extent(B, "B");
+    l.n = extent(rows, "n");
+    l.V = extent(V, "V");
+    l.stride_request = x.stride(0);
+    l.stride_position = dims == 2 ? x.stride(1) : 0;
+    const asv_field u = field(tensor(a[1], "u"), "u", at::kFloat, "float32", dims, B, rows, 0, dev);
+    asv_sampling one = {1.0f, 0, 1.0f, 0.0f};
+    asv_sampling_each each = {};
+    parameter(a[2], "temperature", at::kFloat, "float32", B, dev, &one.temperature, &each.temperature);
+    parameter(a[3], "top_k", at::kInt, "int32", B, dev, &one.top_k, &each.top_k);
+    parameter(a[4], "top_p", at::kFloat, "float32", B, dev, &one.top_p, &each.top_p);
+    parameter(a[5], "min_p", at::kFloat, "float32", B, dev, &one.min_p, &each.min_p);
+    const asv_field tokens = field(tensor(a[6], "out.tokens"), "out.tokens", at::kInt, "int32", dims, B, rows, 0, dev);
+    asv_field logprobs = {}, probs = {};
+    if (a[7] != Py_None)
+      logprobs = field(tensor(a[7], "out.logprobs"), "out.logprobs", at::kFloat, "float32", dims, B, rows, 0, dev);
+    if (a[8] != Py_None)
+      probs = field(tensor(a[8], "out.probs"), "out.probs", at::kFloat, "float32", dims, B, rows, V, dev);
+    if (a[9] == Py_None) refuse(ASV_ERR_NULL, "out.req_status is missing");
+    uint32_t* status = static_cast<uint32_t*>(entries(a[9], "out.req_status", at::kInt, "int32", B, dev));
+    const bool with_logprobs = a[7] != Py_None, with_probs = a[8] != Py_None;
+    const cudaStream_t stream = stream_of(a[10]);
+    return result(unlocked([&]() {
+                    return g_sample(&l, &u, &one, &each, &tokens, with_logprobs ? &logprobs : nullptr,
+                                    with_probs ? &probs : nullptr, status, stream);
+                  }),
+                  "sample_tokens");
+  });
+}
+
+// the addresses of paged_plan and sample_tokens
 PyObject* py_bind_step(PyObject*, PyObject* args) {
-  unsigned long long f[1];
-  if (!PyArg_ParseTuple(args, "K", &f[0])) return nullptr;
+  unsigned long long f[2];
+  if (!PyArg_ParseTuple(args, "KK", &f[0], &f[1])) return nullptr;
   g_plan = reinterpret_cast<decltype(g_plan)>(f[0]);
+  g_sample = reinterpret_cast<decltype(g_sample)>(f[1]);
   Py_RETURN_NONE;
 }
 
 PyMethodDef kMethods[] = {
     {"bind", py_bind, METH_VARARGS, nullptr},
     {"bind_step", py_bind_step, METH_VARARGS, nullptr},
+    {"sample_tokens", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_sample)), METH_FASTCALL, nullptr},
     {"paged_plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_plan)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_attention)), METH_FASTCALL, nullptr},
     {"paged_kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_append)), METH_FASTCALL, nullptr},

@@ -102,8 +102,8 @@ def build_torch_ext(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib: str = LIB) -> str:
     """Compile csrc/*.cu and link `lib` (default _build/libasv.so), and with the default library the
-    binding's module; returns the library path.  Only the paged calls need the module: where it does not
-    compile that is a warning here, and they refuse."""
+    binding's module; returns the library path.  Only the paged calls and the sampling need the module: where
+    it does not compile that is a warning here, and they refuse."""
     if lib != LIB:
         return _build_library(force, verbose, extra_flags, lib)
     with cf.ThreadPoolExecutor(1) as ex:
@@ -112,7 +112,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib: str =
     try:
         ext.result()
     except RuntimeError as e:
-        warnings.warn(f"paged_kv_append and paged_attention are not available: {e}", RuntimeWarning, stacklevel=2)
+        warnings.warn(f"the paged calls and sample_tokens are not available: {e}", RuntimeWarning, stacklevel=2)
     return path
 
 

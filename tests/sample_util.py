@@ -1,0 +1,56 @@
+"""What sample_tokens draws, in 64 bits, and the error bounds of its numbers."""
+import math
+
+import numpy as np
+
+
+def sample64(x, u, T, k, p, least):
+    """(token, log-probability, distribution, margin) of one row x (float64 values of its stored type): from the
+    definition, sorted.  `margin`: how far, relative to the largest weight, the nearest decision was from its border (the
+    nucleus' border against p, the draw's against u)."""
+    V = len(x)
+    order = np.lexsort((np.arange(V), -x))          # value descending, index ascending
+    dist = np.zeros(V)
+    if T == 0:
+        dist[order[0]] = 1
+        return int(order[0]), 0.0, dist, math.inf
+    if k > 0:
+        order = order[:k]
+    w = np.exp((x[order] - x[order[0]]) / T)
+    margin = math.inf
+    keep = np.ones(len(order), bool)
+    if p < 1:
+        before = np.array([0.0] + [math.fsum(w[:i]) for i in range(1, len(w))]) if len(w) < 400 else \
+            np.concatenate([[0.0], np.cumsum(w.astype(np.longdouble))[:-1]]).astype(float)
+        target = p * math.fsum(w)
+        keep &= before < target
+        margin = min(margin, np.abs(before[1:] - target).min(initial=math.inf))
+    keep &= w >= least
+    keep[0] = True
+    kept = order[keep]
+    mass = np.zeros(V)
+    mass[kept] = w[keep]
+    total = math.fsum(mass)
+    upto = np.cumsum(mass.astype(np.longdouble)).astype(float)
+    token = int(np.searchsorted(upto, u * total, side="right"))
+    at = np.flatnonzero(mass)
+    margin = min(margin, np.abs(upto[at] - u * total)[:-1].min(initial=math.inf))
+    token = min(token, int(at[-1]))
+    return token, math.log(mass[token] / total), mass / total, margin
+
+
+# Borders nearer than this (of the largest weight, 1) are not judged: weights come to about 2^-39 and are summed in
+# units of 2^-44, so 2^17 of them are off by 2^-30 at most, by 2^-37 as errors of either sign add up.
+BORDER = 2.0 ** -30
+
+
+def logprob_bound(lp):
+    """Of ln((W - w) / w + 1) in fp32: three roundings of the quotient (2^-24 each), the logarithm's own two last places;
+    a kept mass summed from fp32 weights is off by 2^-21 at most."""
+    return 2.0 ** -20 + 2.0 ** -22 * abs(lp)
+
+
+def probs_bound(p):
+    """Weight (2^-22, the special-function unit's), kept mass (2^-21) and their quotient (four roundings of 2^-24); what is
+    below the weights' unit."""
+    return 2.0 ** -20 * p + 2.0 ** -38
