@@ -114,7 +114,7 @@ asv_status asv_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t str
  * Tuning override for the launch plan: cluster size (CTAs per row, 1..16; 0
  * restores the automatic choice).  threads_per_cta must be 0 or 256, the size
  * the kernels are compiled for (anything else is ASV_ERR_PARAM).  Applies to
- * later calls from any thread.
+ * later calls from any thread (sample_tokens takes at most 8).
  */
 asv_status asv_set_tuning(int cluster_ctas, int threads_per_cta);
 
@@ -449,9 +449,9 @@ typedef struct {
  *   min_p  those with w_i >= min_p;
  * the first is always kept.  The token is the lowest kept index i with  sum of w over kept indices <= i  >  u * W,  W the
  * kept mass; u is a number from [0, 1) that the caller draws (one outside counts as the nearest in it, NaN as 0).  Sums are
- * exact to about 2^-39 of the largest weight, so a token differs from exact arithmetic's only where a border is that near;
- * the result does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.  out_probs
- * (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere.  With temperature 0: 0, and 1 at the token.
+ * exact to about 2^-39 of the largest weight where a border is near, so a token differs from exact arithmetic's only where
+ * one is that near, and does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.
+ * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere; both to 2^-18 (typically 2^-23).  With temperature 0: 0, and 1 at the token.
  * Inputs may share memory, outputs not with anything; rows of out_probs need no alignment but the element's.
  * A row with NaN or +inf, or all -inf, flags its request ASV_REQ_NONFINITE (a single -inf is probability 0), a request's
  * own parameter out of range ASV_REQ_BAD_PARAM; the row's token is then -1, its log-probability -inf, its distribution 0.

@@ -184,6 +184,8 @@ namespace asv {
 
 asv_status record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
+int tuned_cluster() { return g_tune_cluster.load(); }
+
 // Argument checks of asymspec_verify, in the order they are applied: shapes and element type, then
 // (for B > 0) the scalar parameters, the alignment of every pointer given (NULL counts as
 // aligned), and last the required pointers.  A call that fails any of them touches neither the

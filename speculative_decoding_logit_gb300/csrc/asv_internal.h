@@ -181,6 +181,8 @@ constexpr size_t kCheckLogBytes = 256;
 constexpr size_t kCheckLogBytes = 0;
 #endif
 
+int tuned_cluster();  // the cluster size of asv_set_tuning, 0: none
+
 // Kernel launchers (return the cudaError_t of the launch).
 cudaError_t launch_jsd_family(int mode, int dtype, const JsdArgs& args, const LaunchPlan& plan, cudaStream_t s);
 cudaError_t launch_rapid(const RapidArgs& args, const LaunchPlan& plan, cudaStream_t s);

@@ -6,12 +6,20 @@
 // entry.  The token is the first kept index whose cumulative mass (over kept entries, by index) passes u times the
 // kept mass; the distribution is w over the kept mass.
 //
-// Whole numbers come out, so a border must fall where exact arithmetic has it: weights are worked out as (hi, lo) pairs to
-// about 2^-39 and summed in units of 2^-44 in 64-bit integers, which makes every sum exact in any order: the same token
-// for any number of CTAs.
+// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out as (hi, lo) pairs to
+// about 2^-39 and summed in units of 2^-44 in 64-bit integers, which makes their sums exact in any order.  That costs 50
+// operations an entry, so few are weighed so:
+//   - The row streams once, for the maxima of the threads' vectors and, where the whole row's mass counts, a running sum of
+//     fp32 weights (two operations and ex2).  Its error is bounded; a border within the bound counts as undecided.
+//   - Where the n largest maxima of threads bound the kept set from below (top-k; a nucleus, by trial; min-p's border),
+//     the vectors of the threads that reach the bound are read again, out of L2, and the few entries from it on are
+//     compared pair by pair: rank and mass before each, then the draw.
+//   - A draw from the whole row finds the warp's run that u falls into by the fp32 sums and weighs that run alone.
+//   - What stays undecided, or has too many candidates, goes by histograms of exact masses over the row, level by level
+//     until the rest fits the pairwise comparison.
 //
-// A cluster of CTAs has a row; each a run of its vectors, each warp a run of the CTA's.  The row streams from HBM once
-// for its maximum and is read again from L2.
+// A cluster of CTAs has a row, each a run of its vectors, each warp a run of the CTA's.  All CTAs come to the same
+// decisions from the same exchanged numbers.
 #include <algorithm>
 #include <climits>
 
@@ -24,27 +32,39 @@ namespace {
 
 #include "exp2_table.inc"
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;
+constexpr int kList = 512;               // candidates that are compared pair by pair
+constexpr int kNucleus = 64;             // maxima of threads that a nucleus is first looked for above
+constexpr int kBins = 2048, kOwnBins = kBins / kThreads;
 constexpr int kMaxCtas = 8;
 constexpr uint64_t kOne = uint64_t(1) << kSampleUnitBits;  // the largest weight
 
 template <class T>
 constexpr int kVec = 16 / int(sizeof(T));  // entries of a 16-byte vector
 
-struct Shared {
+struct Cut {
+  uint32_t key;   // entries with larger keys are kept, and those of this key up to the index
+  int index;
+  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
+};
+
+struct __align__(16) Shared {
+  uint4 list[kList];                             // candidates of the row: key, index, weight
+  uint32_t bin_lo[kBins], bin_hi[kBins];         // a histogram's 64-bit sums
+  uint64_t before[kList];                        // mass before each candidate, by value and then by index
+  uint2 own[kList];                              // this CTA's candidates: key, index
+  float tops[kThreads];                          // the threads' maxima
   float2 table[64];
-  uint32_t bin_lo[kBins], bin_hi[kBins];   // a histogram's 64-bit sums
-  uint64_t chunk[kWarps];                  // sums of the warps' runs
-  uint64_t all[kMaxCtas * kWarps];         // ... of all CTAs'
+  uint64_t chunk[kWarps];                        // sums of the warps' runs
   uint64_t room[kWarps], room2[kWarps];
-  float top;
-  int bad;
-  int first;   // lowest index of the maximum
-  int found;
-  int pick;
-  uint64_t pick_before, pick_sum;
+  uint64_t pick_before, pick_sum, total;
+  uint16_t rank[kList];
+  uint16_t scan[kThreads];                       // threads whose vectors are read again
+  Cut cut;
+  float top, tau;
+  int bad, n_scan, n_own, last, found, pick;
 };
 
 // ------------------------------------------------------------------ a row
@@ -54,9 +74,15 @@ struct Row {
   const T* base;     // the 16-byte vector with the first entry
   int off;           // entries of it before the first
   int V, vectors;
+  int rank, ctas, per_cta, per_warp;
   int v0, v1;        // this warp's vectors
   __device__ __forceinline__ bool whole(int v) const {
     return (v > 0 || off == 0) && (long long)(v + 1) * kVec<T> - off <= V;
+  }
+  // the vectors of warp w of CTA c
+  __device__ __forceinline__ int run_start(int c, int w) const { return min(c * per_cta + w * per_warp, vectors); }
+  __device__ __forceinline__ int run_end(int c, int w) const {
+    return max(min(min(c * per_cta + (w + 1) * per_warp, (c + 1) * per_cta), vectors), run_start(c, w));
   }
 };
 
@@ -76,21 +102,51 @@ __device__ __forceinline__ float entry(const Row<T>& r, int i) {
   return widen(r.base[r.off + i]);
 }
 
-// f(x, index) for the entries of the warp's vectors.
-template <class T, class F>
-__device__ __forceinline__ void sweep(const Row<T>& r, F f) {
-  const int lane = threadIdx.x % 32;
-  for (int v = r.v0 + lane; v < r.v1; v += 32) {
-    const int i0 = v * kVec<T> - r.off;
-    if (r.whole(v)) {
-      float x[kVec<T>];
-      unpack(__ldg(reinterpret_cast<const uint4*>(r.base) + v), x);
-#pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) f(x[e], i0 + e);
+// A vector; entries that are not the row's are -inf.
+template <class T>
+__device__ __noinline__ uint4 edge_vector(const Row<T>& r, int v) {
+  uint32_t w[4];
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80u : 0xff800000u;
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t half[2];
+      for (int h = 0; h < 2; ++h) {
+        const int i = v * 8 - r.off + 2 * e + h;
+        half[h] = i >= 0 && i < r.V ? r.base[r.off + i].bits : kNone;
+      }
+      w[e] = half[0] | (half[1] << 16);
     } else {
-      for (int i = max(i0, 0); i < min(i0 + kVec<T>, r.V); ++i) f(entry(r, i), i);
+      const int i = v * 4 - r.off + e;
+      w[e] = i >= 0 && i < r.V ? __float_as_uint(r.base[r.off + i]) : kNone;
     }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <class T>
+__device__ __forceinline__ uint4 load_vector(const Row<T>& r, int v) {
+  return r.whole(v) ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : edge_vector(r, v);
+}
+
+// f(vector, number) for the warp's vectors, kAhead of them a lane in flight.
+template <int kAhead, class T, class F>
+__device__ __forceinline__ void stream(const Row<T>& r, F f) {
+  const int lane = threadIdx.x % 32;
+  const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;  // whole vectors
+  const uint4* p = reinterpret_cast<const uint4*>(r.base);
+  const int end = min(r.v1, w1);
+  int v = max(r.v0, w0) + lane;
+  for (; v + 32 * (kAhead - 1) < end; v += 32 * kAhead) {
+    uint4 w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) w[i] = __ldg(p + v + 32 * i);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f(w[i], v + 32 * i);
+  }
+  for (; v < end; v += 32) f(__ldg(p + v), v);
+  // the row's ends
+  if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) f(edge_vector(r, 0), 0);
+  if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) f(edge_vector(r, w1), w1);
 }
 
 // Keys in the order of the values (equal for -0 and 0); 0 is no value's.
@@ -111,19 +167,33 @@ struct Scale {
 
 // exp((x - M) / T) in units of 2^-44, rounded, to about 2^-39.  x - M as the sum s + err (Knuth's TwoSum), times
 // log2(e) / T as the sum th + tl; 2^th by the table (k / 64 next to th, r the rest, |r| <= 2^-7) and Taylor's terms of
-// exp(z) - 1, z = r ln 2; what is below fp32's last place is carried in a second float throughout.
-__device__ __noinline__ uint64_t weight(float x, const Scale sc, const float2* table) {
+// exp(z) - 1, z = r ln 2; what is below fp32's last place is carried in a second float throughout.  Below 2^-24 a weight of
+// fp32's accuracy is within half a unit.
+struct Exponent {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Exponent exponent(float x, const Scale& sc) {
   const float s = x - sc.M, bb = s - x, err = (x - (s - bb)) + (-sc.M - bb);
-  const float th = s * sc.c;
-  if (!(th > -float(kSampleUnitBits + 2))) return 0;
-  const float tl = fmaf(s, sc.c, -th) + fmaf(s, sc.c_lo, err * sc.c);
+  const float hi = s * sc.c;
+  return {hi, fmaf(s, sc.c, -hi) + fmaf(s, sc.c_lo, err * sc.c)};
+}
+
+constexpr float kNoWeight = -float(kSampleUnitBits + 2), kLight = -24.0f;
+
+__device__ __forceinline__ uint64_t light_weight(Exponent t) {
+  const float w = ex2_approx(t.hi);
+  return uint64_t(uint32_t(__float2int_rn(fmaf(w, t.lo * kLn2Hi, w) * float(kOne))));
+}
+
+__device__ __forceinline__ uint64_t full_weight(Exponent x, const float2* table) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
-  const float m = fmaf(th, 64.0f, kMagic), kf = m - kMagic;
+  const float m = fmaf(x.hi, 64.0f, kMagic), kf = m - kMagic;
   const int k = __float_as_int(m) - __float_as_int(kMagic);
-  const float r = fmaf(kf, -0.015625f, th);
+  const float r = fmaf(kf, -0.015625f, x.hi);
   const float2 t = table[k & 63];
   const float zh = r * kLn2Hi;
-  const float zl = fmaf(tl, kLn2Hi, fmaf(r, kLn2Lo, fmaf(r, kLn2Hi, -zh)));
+  const float zl = fmaf(x.lo, kLn2Hi, fmaf(r, kLn2Lo, fmaf(r, kLn2Hi, -zh)));
   const float p = fmaf(fmaf(fmaf(zh, 1.0f / 120.0f, 1.0f / 24.0f), zh, 1.0f / 6.0f), zh, 0.5f) * (zh * zh);
   const float q = fmaf(zl, zh, zl) + p;
   const float mh = t.x * zh;
@@ -133,6 +203,36 @@ __device__ __noinline__ uint64_t weight(float x, const Scale sc, const float2* t
   const float yh = sh * unit, a = (yh + kMagic) - kMagic;
   const float low = ((yh - a) + sl * unit) * 4194304.0f;
   return uint64_t((long long)(int(a)) * 4194304 + __float2int_rn(low));
+}
+
+__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const float2* table) {
+  const Exponent t = exponent(x, sc);
+  return !(t.hi > kNoWeight) ? 0 : t.hi < kLight ? light_weight(t) : full_weight(t, table);
+}
+
+// A vector's, the same numbers.
+template <int N>
+__device__ __forceinline__ void weights(const float (&x)[N], const Scale& sc, const float2* table, uint64_t (&w)[N]) {
+  float top = x[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
+  const float t = (top - sc.M) * sc.c;  // (the largest entry's exponent)
+#pragma unroll
+  for (int e = 0; e < N; ++e) w[e] = 0;
+  if (!(t > kNoWeight)) return;
+  Exponent x2[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    x2[e] = exponent(x[e], sc);
+    if (x2[e].hi > kNoWeight) w[e] = light_weight(x2[e]);
+  }
+  if (t < kLight) return;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const bool full = x2[e].hi >= kLight;
+    const uint64_t f = full_weight({full ? x2[e].hi : 0.0f, x2[e].lo}, table);
+    if (full) w[e] = f;
+  }
 }
 
 // ------------------------------------------------------------------ sums over the row
@@ -176,50 +276,304 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* room) {
   return x;
 }
 
-// The sum f(x, index) of the whole row's entries passes target(total) at the returned index: the first whose inclusive
-// sum, by index, is above it.  Every CTA returns it.
-template <class T, class F, class G>
-__device__ __noinline__ int locate(Shared& sh, const Row<T>& r, int rank, int ctas, int per_cta, int per_warp, F f, G target,
-                                   uint64_t& total) {
+// ------------------------------------------------------------------ fast sums
+
+// The sums that stream with the row are of fp32 weights 2^t, t = fma(x, c, -ref).  With D = (max - x) c a term is off by
+// the rounding of c (D 2^-24 in t), of t ((D + 8) 2^-24, a reference is at most 8 below what it met) and ex2 (2^-22), a
+// thread's sum by its move to the row's maximum (ex2 again) and the additions (three within a vector; the running sum
+// carries its own errors).  Averaged over the mass, D is at most the entropy, log2 V <= 19: in all
+// (ln 2 (2 * 19 + 8) + 4 + 4 + 4 + 3) 2^-24 < 2^-18 of the sum.
+// References are whole parts of what fp32 holds exactly next to a term only within +-2^20: what lies below is left out, and
+// a row whose maximum is not well above that, or lies above the range, does without these sums.
+constexpr int kFastBits = 18;
+constexpr float kFastRange = 1048576.0f;
+
+struct Partial {
+  float ref = -INFINITY;  // log2 units
+  float hi = 0.0f, lo = 0.0f;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float vector_max(const uint4& w, bf16_t*) {
+  uint32_t m, n;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w.x), "r"(w.y));
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(w.z), "r"(w.w));
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+  return max_nan(bf16_lo(m), bf16_hi(m));
+}
+__device__ __forceinline__ float vector_max(const uint4& w, float*) {
+  return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+
+// One vector's weights onto a running sum.
+template <int N>
+__device__ __forceinline__ void add_weights(Partial& s, const float (&x)[N], float top, float c) {
+  const float t = top * c;
+  if (!(t > -kFastRange)) return;
+  if (t > s.ref + 8.0f) {
+    const float keep = ex2_approx(s.ref - t);
+    s.hi *= keep;
+    s.lo *= keep;
+    s.ref = t;
+  }
+  const float2 cc = make_float2(c, c), rr = make_float2(-s.ref, -s.ref);
+  float2 w[N / 2];
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    w[e] = ffma2(make_float2(x[2 * e], x[2 * e + 1]), cc, rr);
+    w[e].x = ex2_approx(w[e].x);
+    w[e].y = ex2_approx(w[e].y);
+  }
+#pragma unroll
+  for (int n = N / 2; n > 1; n /= 2)
+#pragma unroll
+    for (int e = 0; e < n / 2; ++e) w[e] = fadd2(w[2 * e], w[2 * e + 1]);
+  const float v = w[0].x + w[0].y;
+  const float sum = s.hi + v, bb = sum - s.hi;
+  s.lo += (s.hi - (sum - bb)) + (v - bb);
+  s.hi = sum;
+}
+
+// ------------------------------------------------------------------ candidates
+
+// The block's sum.
+__device__ __forceinline__ uint64_t block_sum(uint64_t x, uint64_t* room) {
+  x = warp_sum(x);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) room[threadIdx.x / 32] = x;
+  __syncthreads();
+  x = 0;
+  for (int i = 0; i < kWarps; ++i) x += room[i];
+  return x;
+}
+
+// The n-th largest of the threads' values (1 <= n <= kThreads), to sh.tau.
+__device__ __forceinline__ void nth_largest(Shared& sh, float x, int n) {
+  const int tid = threadIdx.x;
+  sh.tops[tid] = x;
+  __syncthreads();
+  int larger = 0;
+#pragma unroll 4
+  for (int i = 0; i < kThreads; i += 4) {
+    const float4 y = *reinterpret_cast<const float4*>(sh.tops + i);
+    larger += (y.x > x || (y.x == x && i < tid)) + (y.y > x || (y.y == x && i + 1 < tid)) +
+              (y.z > x || (y.z == x && i + 2 < tid)) + (y.w > x || (y.w == x && i + 3 < tid));
+  }
+  if (larger == n - 1) sh.tau = x;
+}
+
+// The CTA's entries from tau on, out of the vectors of the threads whose maximum reaches it, to sh.own (those that have
+// room; sh.n_own counts them all).
+template <class T>
+__device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float own_top, float tau) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  uint64_t own = 0;
-  sweep(r, [&](float x, int i) { own += f(x, i); });
-  own = warp_sum(own);
-  if (lane == 0) sh.chunk[warp] = own;
-  row_sync();
-  if (tid < ctas * kWarps) sh.all[tid] = ld_peer_u64(sh.chunk + tid % kWarps, tid / kWarps);
-  const int chunks = ctas * kWarps;
+  if (tid == 0) sh.n_scan = sh.n_own = 0;
   __syncthreads();
-  uint64_t incl = tid < chunks ? sh.all[tid] : 0;
-  const uint64_t mine = incl;
-  incl = block_scan(incl, sh.room);
-  if (tid == kThreads - 1) sh.pick_sum = incl;
+  const bool again = own_top >= tau;
+  const uint32_t votes = __ballot_sync(0xffffffffu, again);
+  int at = 0;
+  if (lane == 0 && votes != 0) at = atomicAdd(&sh.n_scan, __popc(votes));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1u));
+  if (again) sh.scan[at] = uint16_t(tid);
   __syncthreads();
-  total = sh.pick_sum;
-  const uint64_t at = target(total);
-  if (tid < chunks && incl > at && incl - mine <= at) {
+  const int n = sh.n_scan;
+  // a thread's vectors are 32 apart; all of them are shared out, a vector a lane
+  const int per_thread = (r.per_warp + 31) / 32;
+  for (int x = warp * 32 + lane; x < n * per_thread; x += kThreads) {
+    const int k = x / per_thread, q = x - k * per_thread, t = sh.scan[k];
+    const int v0 = r.run_start(r.rank, t / 32), v1 = r.run_end(r.rank, t / 32);
+    // (the row's ends are with the first two lanes of their warp, whichever they would fall to)
+    const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;
+    const int first = max(v0, w0) + t % 32, v = first + 32 * q;
+    auto take = [&](int v) {
+      const uint4 w = load_vector(r, v);
+      float x[kVec<T>];
+      unpack(w, x);
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) {
+        const int i = v * kVec<T> - r.off + e;
+        if (x[e] >= tau && i >= 0 && i < r.V) {
+          const int to = atomicAdd(&sh.n_own, 1);
+          if (to < kList) sh.own[to] = make_uint2(key_of(x[e]), uint32_t(i));
+        }
+      }
+    };
+    if (v < min(v1, w1)) take(v);
+    if (q == 0 && t % 32 == 0 && v0 == 0 && w0 == 1 && v1 > 0) take(0);
+    if (q == 0 && t % 32 == 1 && w1 >= w0 && w1 < r.vectors && w1 >= v0 && w1 < v1) take(w1);
+  }
+}
+
+// The row's candidates of all CTAs, with their weights, to sh.list; their number, or -1 if there is no room.
+__device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, bool weights) {
+  int n = 0;
+  for (int c = 0; c < ctas; ++c) {
+    const int m = int(ld_peer_u32(&sh.n_own, c));
+    if (n + m > kList) return -1;
+    for (int i = threadIdx.x; i < m; i += kThreads) {
+      const uint64_t e = ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.own + i), c);
+      const uint32_t key = uint32_t(e), index = uint32_t(e >> 32);
+      const uint64_t w = weights ? weight(value_of(key), sc, sh.table) : kOne;
+      sh.list[n + i] = make_uint4(key, index, uint32_t(w), uint32_t(w >> 32));
+    }
+    n += m;
+  }
+  __syncthreads();
+  return n;
+}
+
+__device__ __forceinline__ uint64_t weight_in(const uint4& e) { return (uint64_t(e.w) << 32) | e.z; }
+
+// p of a mass, p as a fraction of 2^64, rounded up.
+__device__ __forceinline__ uint64_t part_of(uint64_t part, uint64_t mass) {
+  return __umul64hi(part, mass) + (part * mass != 0 ? 1 : 0);
+}
+
+// For all candidates: the mass and the number of the others y with before(y, candidate), to sh.before and sh.rank.  A
+// group of threads has one where there are few.
+template <class F>
+__device__ __forceinline__ void all_pairs(Shared& sh, int n, F before) {
+  const int tid = threadIdx.x;
+  int g = 1;
+  while (g < 32 && 2 * g * n <= kThreads) g *= 2;
+  for (int e0 = 0; e0 < n; e0 += kThreads / g) {
+    const int e = e0 + tid / g;
+    const uint4 mine = sh.list[min(e, n - 1)];
+    uint64_t mass = 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int j = tid % g; j < n; j += g) {
+      const uint4 y = sh.list[j];
+      if (before(y, mine)) {
+        mass += weight_in(y);
+        ++rank;
+      }
+    }
+    for (int o = 1; o < g; o *= 2) {
+      mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    }
+    if (tid % g == 0 && e < n) {
+      sh.before[e] = mass;
+      sh.rank[e] = uint16_t(rank);
+    }
+  }
+  __syncthreads();
+}
+
+struct Drawn {
+  int token;
+  uint64_t weight, total;  // of the token, of all that is kept
+};
+
+// Settles a row by its n candidates, which are all its entries from some value on: its first k where k > 0, else all that
+// can be kept (`closed`: nothing else is, for its weight; if not, the list has to reach past the nucleus).  `mass`, off by
+// `off` at most: of the row, where k = 0 and p < 1.  False: the list does not settle it (sh.cut and the result are then
+// nothing).
+__device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t least, bool closed, uint64_t mass,
+                                    uint64_t off, uint64_t draw, Drawn& d) {
+  const int tid = threadIdx.x;
+  all_pairs(sh, n, [](const uint4& y, const uint4& e) { return y.x > e.x || (y.x == e.x && y.y < e.y); });
+  uint64_t sum = 0;
+  for (int e = tid; e < n; e += kThreads)
+    if (k == 0 || sh.rank[e] < k) sum += weight_in(sh.list[e]);
+  sum = block_sum(sum, sh.room);
+  if (k > 0) {
+    mass = sum;
+    off = 0;
+  }
+  uint64_t low = ~uint64_t(0), high = ~uint64_t(0);
+  if (p < 1.0f) {
+    const uint64_t part = uint64_t(p * 18446744073709551616.0f);
+    low = max(part_of(part, mass - min(off, mass)), uint64_t(1));
+    high = max(part_of(part, mass + off), uint64_t(1));
+  }
+  bool unsure = k == 0 && p < 1.0f && !closed && sum < high;
+  if (tid == 0) sh.last = 0;
+  __syncthreads();
+  uint64_t kept = 0;
+  for (int e = tid; e < n; e += kThreads) {
+    const uint64_t w = weight_in(sh.list[e]), b = sh.before[e];
+    const int rank = sh.rank[e];
+    bool keep = (k == 0 || rank < k) && w >= least;
+    unsure = unsure || (keep && b >= low && b < high);
+    keep = rank == 0 || (keep && b < low);
+    if (keep) {
+      kept += w;
+      atomicMax(&sh.last, rank);
+    } else {
+      sh.list[e].z = sh.list[e].w = 0;
+    }
+  }
+  if (__syncthreads_or(unsure)) return false;
+  for (int e = tid; e < n; e += kThreads)
+    if (sh.rank[e] == sh.last) sh.cut = {sh.list[e].x, int(sh.list[e].y)};
+  d.total = block_sum(kept, sh.room);
+  const uint64_t at = __umul64hi(draw, d.total);
+  all_pairs(sh, n, [](const uint4& y, const uint4& e) { return y.y < e.y; });
+  for (int e = tid; e < n; e += kThreads) {
+    const uint64_t w = weight_in(sh.list[e]), b = sh.before[e];
+    if (b <= at && at < b + w) {
+      sh.found = int(sh.list[e].y);
+      sh.pick_sum = w;
+    }
+  }
+  __syncthreads();
+  d.token = sh.found;
+  d.weight = sh.pick_sum;
+  return true;
+}
+
+// ------------------------------------------------------------------ the row in general
+
+// Where the draw's share `at` of the warps' sums (in sh.chunk, behind a row_sync) falls: the run that passes it and the sum
+// before it, to sh.pick and sh.pick_before; the sum of all to sh.total.  at = draw / 2^64 of `total`, or of the sum where
+// total is 0.
+template <class T>
+__device__ __forceinline__ uint64_t find_run(Shared& sh, const Row<T>& r, uint64_t draw, uint64_t total) {
+  const int tid = threadIdx.x, runs = r.ctas * kWarps;
+  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % kWarps, tid / kWarps) : 0;
+  const uint64_t incl = block_scan(mine, sh.room);
+  if (tid == kThreads - 1) sh.total = incl;
+  __syncthreads();
+  const uint64_t at = __umul64hi(draw, total > 0 ? total : sh.total);
+  if (tid < runs && incl > at && incl - mine <= at) {
     sh.pick = tid;
     sh.pick_before = incl - mine;
   }
+  return at;
+}
+
+// The entry of run sh.pick that `at` falls into, f(x, index) entry by entry: to sh.found of the CTA that owns the run (-1:
+// within `margin` of the entry's ends, or in none), read from there by all.
+template <class T, class F>
+__device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t at, uint64_t margin, F f) {
+  const int tid = threadIdx.x;
+  if (tid == 0) sh.found = -1;
   __syncthreads();
   const int pick = sh.pick, owner = pick / kWarps;
-  if (rank == owner) {
-    // the run of the warp that passes it, its entries shared out to all threads in order
-    const int v0 = min(rank * per_cta + (pick % kWarps) * per_warp, r.vectors);
-    const int v1 = min(min(v0 + per_warp, (rank + 1) * per_cta), r.vectors);
+  if (r.rank == owner) {
+    const int v0 = r.run_start(owner, pick % kWarps), v1 = r.run_end(owner, pick % kWarps);
     const int i0 = max(v0 * kVec<T> - r.off, 0), i1 = min(v1 * kVec<T> - r.off, r.V);
     const int per = (i1 - i0 + kThreads - 1) / kThreads, a = min(i0 + tid * per, i1), b = min(a + per, i1);
     uint64_t sum = 0;
     for (int i = a; i < b; ++i) sum += f(entry(r, i), i);
     const uint64_t upto = sh.pick_before + block_scan(sum, sh.room2);
-    if (upto > at && upto - sum <= at) {
-      uint64_t before = upto - sum;
+    uint64_t before = upto - sum;
+    if (upto > at && before <= at) {
       for (int i = a; i < b; ++i) {
-        before += f(entry(r, i), i);
-        if (before > at) {
-          sh.found = i;
+        const uint64_t w = f(entry(r, i), i);
+        if (before + w > at) {
+          // (before the row's first weight there is nothing to be off by)
+          if ((before == 0 || at - before >= margin) && before + w - at > margin) sh.found = i;
           break;
         }
+        before += w;
       }
     }
   }
@@ -229,64 +583,137 @@ __device__ __noinline__ int locate(Shared& sh, const Row<T>& r, int rank, int ct
   return found;
 }
 
-struct Cut {
-  uint32_t key;   // entries with larger keys are kept, and those of this key up to the index
-  int index;
-  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
-};
+// The index of the n-th entry with this key (n >= 1).
+template <class T>
+__device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key, uint64_t n) {
+  uint32_t own = 0;
+  stream<4>(r, [&](const uint4& w, int v) {
+    float x[kVec<T>];
+    unpack(w, x);
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) {
+      const int i = v * kVec<T> - r.off + e;
+      own += key_of(x[e]) == key && i >= 0 && i < r.V;
+    }
+  });
+  const uint64_t sum = warp_sum(own);
+  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = sum;
+  row_sync();
+  // (the share n - 1 of the count, as find_run takes it: it is looked for in units, not in parts of 2^64)
+  const int tid = threadIdx.x, runs = r.ctas * kWarps;
+  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % kWarps, tid / kWarps) : 0;
+  const uint64_t incl = block_scan(mine, sh.room);
+  if (tid < runs && incl >= n && incl - mine < n) {
+    sh.pick = tid;
+    sh.pick_before = incl - mine;
+  }
+  return find_entry(sh, r, n - 1, 0, [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); });
+}
 
-// The cut that keeps entries, in order, until their measures f(x, key, index) add up to target(total): the last is the
-// first with target <= the inclusive sum.  A histogram by value over the weights' range, then by key within the bin, each
-// level a sweep; then the index among equal values.
-template <class T, class F, class G>
-__device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc, int rank, int ctas, int per_cta,
-                                   int per_warp, F f, G target_of) {
+// The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
+// target_of(all): the last is the first with target <= the inclusive sum, which goes to `kept`.  A histogram by value
+// over the weights' range, then by key within the bin, each level a sweep, until what is left fits the list.
+template <bool MASS, class T, class G>
+__device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of,
+                                   uint64_t& kept) {
   const int tid = threadIdx.x;
   // bins of equal width down to where weights vanish; the last takes the rest
   const float width = float(kBins - 1) / float(kSampleUnitBits + 3) * sc.c;
   auto bin_of = [&](float x) { return min(int((sc.M - x) * width), kBins - 1); };
+  auto add = [&](int bin, uint64_t m) {
+    const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bin_lo[bin], low);
+    const uint32_t high = uint32_t(m >> 32) + (old + low < old ? 1u : 0u);
+    if (high) atomicAdd(&sh.bin_hi[bin], high);
+  };
   uint32_t lo = 1, hi = key_of(sc.M);
-  int level = 0, shift = 32, first_bin = 0;
+  int shift = 32, first_bin = 0;
   uint64_t above = 0, target = 0, in_bin = 0;
-  while (shift > 0) {
+  for (int level = 0; shift > 0; ++level) {
     if (level > 0) {
       const uint32_t span = hi - lo;
       shift = 0;
       while ((span >> shift) >= uint32_t(kBins)) ++shift;
     }
-    sh.bin_lo[tid] = 0;
-    sh.bin_hi[tid] = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.bin_lo[i] = sh.bin_hi[i] = 0;
+    if (tid == 0) sh.n_own = 0;
     __syncthreads();
-    sweep(r, [&](float x, int i) {
-      const uint32_t key = key_of(x);
-      int bin = bin_of(x);
-      if (level > 0) {
-        if (bin != first_bin || key < lo || key > hi) return;
-        bin = int((hi - key) >> shift);
-      }
-      const uint64_t m = f(x, key, i);
-      if (m == 0) return;
-      const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bin_lo[bin], low);
-      const uint32_t high = uint32_t(m >> 32) + (old + low < old ? 1u : 0u);
-      if (high) atomicAdd(&sh.bin_hi[bin], high);
-    });
-    row_sync();
-    uint64_t own = 0;
-    for (int c = 0; c < ctas; ++c)
-      own += (uint64_t(ld_peer_u32(&sh.bin_hi[tid], c)) << 32) + ld_peer_u32(&sh.bin_lo[tid], c);
-    uint64_t incl = block_scan(own, sh.room);
-    if (tid == kThreads - 1) sh.pick_sum = incl;
-    __syncthreads();
-    if (level == 0) target = target_of(sh.pick_sum);
-    if (own > 0 && above + incl >= target && above + incl - own < target) {
-      sh.pick = tid;
-      sh.pick_before = incl - own;
+    if (level == 0) {
+      stream<2>(r, [&](const uint4& w, int v) {
+        float x[kVec<T>];
+        unpack(w, x);
+        uint64_t m[kVec<T>];
+        if constexpr (MASS) weights(x, sc, sh.table, m);
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) {
+          const int i = v * kVec<T> - r.off + e;
+          if constexpr (!MASS) m[e] = i >= 0 && i < r.V;
+          if (m[e] != 0 && within.keeps(key_of(x[e]), i)) add(bin_of(x[e]), m[e]);
+        }
+      });
+    } else {
+      const float least = value_of(lo);
+      stream<4>(r, [&](const uint4& w, int v) {
+        if (vector_max(w, static_cast<T*>(nullptr)) < least) return;
+        float x[kVec<T>];
+        unpack(w, x);
+#pragma unroll 1
+        for (int e = 0; e < kVec<T>; ++e) {
+          const int i = v * kVec<T> - r.off + e;
+          const uint32_t key = key_of(x[e]);
+          if (key < lo || key > hi || bin_of(x[e]) != first_bin || i < 0 || i >= r.V || !within.keeps(key, i)) continue;
+          const uint64_t m = MASS ? weight(x[e], sc, sh.table) : 1;
+          if (m == 0) continue;
+          add(int((hi - key) >> shift), m);
+          const int to = atomicAdd(&sh.n_own, 1);
+          if (to < kList) sh.own[to] = make_uint2(key, uint32_t(i));
+        }
+      });
     }
+    row_sync();
+    const int n = level > 0 ? share_out(sh, sc, r.ctas, MASS) : -1;
+    if (n > 0) {
+      all_pairs(sh, n, [](const uint4& y, const uint4& e) { return y.x > e.x || (y.x == e.x && y.y < e.y); });
+      for (int e = tid; e < n; e += kThreads) {
+        const uint64_t m = MASS ? weight_in(sh.list[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(sh.rank[e]));
+        if (b < target && target <= b + m) {
+          sh.cut = {sh.list[e].x, int(sh.list[e].y)};
+          sh.total = b + m;
+        }
+      }
+      row_sync();
+      kept = sh.total;
+      return sh.cut;
+    }
+    uint64_t own[kOwnBins], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kOwnBins; ++i) own[i] = 0;
+    for (int c = 0; c < r.ctas; ++c)
+#pragma unroll
+      for (int i = 0; i < kOwnBins; ++i)
+        own[i] += (uint64_t(ld_peer_u32(sh.bin_hi + tid * kOwnBins + i, c)) << 32) +
+                  ld_peer_u32(sh.bin_lo + tid * kOwnBins + i, c);
+#pragma unroll
+    for (int i = 0; i < kOwnBins; ++i) sum += own[i];
+    const uint64_t incl = block_scan(sum, sh.room);
+    if (tid == kThreads - 1) sh.total = incl;
     __syncthreads();
+    if (level == 0) target = target_of(sh.total);
+    uint64_t b = above + incl - sum;
+    if (b < target && target <= above + incl) {
+#pragma unroll
+      for (int i = 0; i < kOwnBins; ++i) {
+        if (b < target && target <= b + own[i]) {
+          sh.pick = tid * kOwnBins + i;
+          sh.pick_before = b;
+          sh.pick_sum = own[i];
+        }
+        b += own[i];
+      }
+    }
+    row_sync();  // (and the peers have read the bins)
     const int bin = sh.pick;
-    above += sh.pick_before;
-    __syncthreads();
-    if (tid == bin) sh.pick_sum = own;
+    above = sh.pick_before;
+    in_bin = sh.pick_sum;
     if (level == 0) {
       // keys that the bin's values may have (its own test stays)
       first_bin = bin;
@@ -298,158 +725,290 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       hi -= uint32_t(bin) << shift;
       lo = max(lo, hi - ((1u << shift) - 1u));
     }
-    ++level;
-    row_sync();  // (the peers have read the bins)
-    in_bin = sh.pick_sum;
+    __syncthreads();
   }
-  const uint32_t key = hi;
-  const float value = value_of(key);
-  // of equal values the lowest indices
-  const uint64_t each = f(value, key, 0);
+  // one value, and more entries with it than the list holds: of equal values the lowest indices
+  const uint64_t each = MASS ? weight(value_of(hi), sc, sh.table) : 1;
   const uint64_t want = (target - above + each - 1) / each;
-  Cut cut = {key, INT_MAX};
-  if (want < in_bin / each) {
-    uint64_t n;
-    cut.index = locate(
-        sh, r, rank, ctas, per_cta, per_warp, [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); },
-        [&](uint64_t) { return want - 1; }, n);
-  }
+  kept = above + want * each;
+  Cut cut = {hi, INT_MAX};
+  if (want < in_bin / each) cut.index = nth_equal(sh, r, hi, want);
   return cut;
+}
+
+// The smallest key whose weight is at least `least`, by a warp: 32 candidates at a time.
+__device__ __noinline__ uint32_t least_key(Shared& sh, const Scale& sc, uint64_t least) {
+  uint32_t lo = 1, hi = key_of(sc.M);
+  __syncthreads();  // (sh.cut's last readers are done)
+  if (threadIdx.x < 32) {
+    while (lo < hi) {
+      const uint32_t step = (hi - lo + 31) / 32, key = min(lo + step * threadIdx.x, hi);
+      const uint32_t reach = __ballot_sync(0xffffffffu, key == hi || weight(value_of(key), sc, sh.table) >= least);
+      const int f = reach != 0 ? __ffs(reach) - 1 : 32;
+      const uint32_t below = lo;
+      if (f < 32) hi = min(below + step * f, hi);
+      if (f > 0) lo = min(below + step * (f - 1) + 1, hi);
+    }
+    if (threadIdx.x == 0) sh.cut.key = hi;
+  }
+  __syncthreads();
+  return sh.cut.key;
+}
+
+struct Kept {
+  Cut cut;
+  float value;  // the cut's
+  __device__ __forceinline__ bool operator()(float x, int i) const { return x > value || (x == value && i <= cut.index); }
+};
+
+// A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync); total: the kept mass, 0: that
+// of the sums.  A token < 0: too near a border to say.
+template <class T>
+__device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw,
+                                        uint64_t total) {
+  const uint64_t at = find_run(sh, r, draw, total);
+  __syncthreads();
+  Drawn d;
+  d.total = total > 0 ? total : sh.total;
+  d.token = find_entry(sh, r, at, 2 * ((sh.total >> kFastBits) + 1),
+                       [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
+  d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, sh.table) : 0;
+  return d;
+}
+
+// The warps' fast sums of the kept entries, to sh.chunk.
+template <class T>
+__device__ __noinline__ void fast_sums(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep) {
+  const float ref = -sc.M * sc.c;
+  Partial s;
+  s.ref = 0.0f;
+  stream<4>(r, [&](const uint4& w, int v) {
+    float x[kVec<T>];
+    unpack(w, x);
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+      if (keep(x[e], v * kVec<T> - r.off + e)) sum += ex2_approx(fmaf(x[e], sc.c, ref));
+    const float all = s.hi + sum, bb = all - s.hi;
+    s.lo += (s.hi - (all - bb)) + (sum - bb);
+    s.hi = all;
+  });
+  // (every reference is the maximum's: what fma leaves of it, the maximum itself has too)
+  const float own = (s.hi + s.lo) * ex2_approx(-fmaf(sc.M, sc.c, ref));
+  const uint64_t w = warp_sum(uint64_t(own * float(kOne)));
+  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = w;
+}
+
+// The same by exact sums.
+template <class T>
+__device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw) {
+  uint64_t own = 0;
+  stream<2>(r, [&](const uint4& w, int v) {
+    float x[kVec<T>];
+    unpack(w, x);
+    uint64_t m[kVec<T>];
+    weights(x, sc, sh.table, m);
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+      if (keep(x[e], v * kVec<T> - r.off + e)) own += m[e];
+  });
+  own = warp_sum(own);
+  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
+  row_sync();
+  const uint64_t at = find_run(sh, r, draw, 0);
+  __syncthreads();
+  Drawn d;
+  d.total = sh.total;
+  d.token = find_entry(sh, r, at, 0, [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
+  d.weight = weight(entry(r, d.token), sc, sh.table);
+  return d;
 }
 
 // ------------------------------------------------------------------ the kernel
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int ctas = int(cluster_size()), rank = int(cluster_rank());
-  const long long row = blockIdx.x / ctas;
+  Row<T> r;
+  r.ctas = int(cluster_size());
+  r.rank = int(cluster_rank());
+  const long long row = blockIdx.x / r.ctas;
   const int b = int(row / a.n), n = int(row - (long long)b * a.n);
   if (tid < 64) sh.table[tid] = kExp2Table[tid];
   if (tid == 0) {
-    sh.first = INT_MAX;
-    sh.found = 0;
-    sh.pick = 0;
-    sh.pick_before = 0;
+    sh.found = sh.pick = 0;
+    sh.pick_before = sh.pick_sum = sh.total = 0;
+    sh.tau = -INFINITY;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the request's parameters
   const float T_ = a.temperature != nullptr ? a.temperature[b] : a.one.temperature;
-  const int top_k = a.top_k != nullptr ? a.top_k[b] : a.one.top_k;
   const float top_p = a.top_p != nullptr ? a.top_p[b] : a.one.top_p;
   const float min_p = a.min_p != nullptr ? a.min_p[b] : a.one.min_p;
-  const bool params_ok = sampling_ok(T_, top_k, top_p, min_p);
+  int k = a.top_k != nullptr ? a.top_k[b] : a.one.top_k;
+  const bool params_ok = sampling_ok(T_, k, top_p, min_p);
   float u = a.u[b * a.u_b + n * a.u_n];
   u = u >= 0.0f ? fminf(u, 0.99999994f) : 0.0f;
+  const bool greedy = T_ == 0.0f;
+  k = greedy ? 1 : k >= a.V ? 0 : k;
 
-  Row<T> r;
   const T* first = static_cast<const T*>(a.x) + b * a.x_b + n * a.x_n;
   r.off = int((reinterpret_cast<uintptr_t>(first) % 16) / sizeof(T));
   r.base = first - r.off;
   r.V = a.V;
   r.vectors = (r.off + a.V + kVec<T> - 1) / kVec<T>;
-  const int per_cta = (r.vectors + ctas - 1) / ctas, per_warp = (per_cta + kWarps - 1) / kWarps;
-  r.v0 = min(rank * per_cta + warp * per_warp, r.vectors);
-  r.v1 = min(min(r.v0 + per_warp, (rank + 1) * per_cta), r.vectors);
+  r.per_cta = (r.vectors + r.ctas - 1) / r.ctas;
+  r.per_warp = (r.per_cta + kWarps - 1) / kWarps;
+  r.v0 = r.run_start(r.rank, warp);
+  r.v1 = r.run_end(r.rank, warp);
+  Scale sc;
+  sc.c = greedy || !params_ok ? 1.0f : kLog2eHi / T_;
+  sc.c_lo = greedy || !params_ok ? 0.0f : (fmaf(-sc.c, T_, kLog2eHi) + kLog2eLo) / T_;
 
-  // ---- the maximum
+  // ---- the row streams once: the threads' maxima, and the mass where it is needed
+  const bool nucleus = !greedy && top_p < 1.0f;
+  const bool sums = k == 0 && (nucleus || min_p == 0.0f);
   float top = -INFINITY;
-  bool bad = false;
-  sweep(r, [&](float x, int) {
-    bad = bad || x != x;
-    top = fmaxf(top, x);
-  });
-  bad = __syncthreads_or(bad || top == INFINITY);
-  top = warp_max(top);
-  if (lane == 0) sh.chunk[warp] = __float_as_uint(top);
+  Partial part;
+  if (sums) {
+    stream<4>(r, [&](const uint4& w, int) {
+      const float m = vector_max(w, static_cast<T*>(nullptr));
+      float x[kVec<T>];
+      unpack(w, x);
+      top = max_nan(top, m);
+      add_weights(part, x, m, sc.c);
+    });
+  } else {
+    stream<4>(r, [&](const uint4& w, int) { top = max_nan(top, vector_max(w, static_cast<T*>(nullptr))); });
+  }
+  bool bad = __syncthreads_or(!(top < INFINITY));
+  // Candidates are looked for from tau on: the row's k-th largest is at least the least of the CTAs' (k / ctas)-th
+  // largest maxima of threads.
+  const int nth = k > 0 ? (k + r.ctas - 1) / r.ctas : nucleus ? max(kNucleus / r.ctas, 1) : kThreads + 1;
+  if (nth <= kThreads) nth_largest(sh, top, nth);
+  float m = warp_max(top);
+  if (lane == 0) sh.chunk[warp] = __float_as_uint(m);
   __syncthreads();
   if (tid == 0) {
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, __uint_as_float(uint32_t(sh.chunk[w])));
-    sh.top = top;
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, __uint_as_float(uint32_t(sh.chunk[w])));
+    sh.top = m;
     sh.bad = bad;
   }
   row_sync();
-  Scale sc;
+  float tau = INFINITY;
   sc.M = -INFINITY;
-  for (int c = 0; c < ctas; ++c) {
+  for (int c = 0; c < r.ctas; ++c) {
     sc.M = fmaxf(sc.M, __uint_as_float(ld_peer_u32(&sh.top, c)));
+    tau = fminf(tau, __uint_as_float(ld_peer_u32(&sh.tau, c)));
     bad = bad || ld_peer_u32(&sh.bad, c) != 0;
   }
   bad = bad || sc.M == -INFINITY;
-  int token = -1;
-  float logprob = -INFINITY;
-  uint64_t total = 0;
+
+  Drawn d = {-1, 0, 0};
   Cut cut = {0u, INT_MAX};
   uint64_t least = 0;
-
-  // (params_ok and bad are the whole cluster's)
-  const bool greedy = T_ == 0.0f;
-  if (params_ok && !bad) {
+  if (params_ok && !bad) {  // (for all CTAs of the row)
+    least = greedy ? 0 : uint64_t(ceilf(min_p * float(kOne)));
+    const uint64_t draw = greedy ? 0 : uint64_t(u * 18446744073709551616.0f);
+    if (sums) {
+      const float own = !(part.ref > -INFINITY) ? 0.0f : (part.hi + part.lo) * ex2_approx(fmaf(-sc.M, sc.c, part.ref));
+      const uint64_t w = warp_sum(uint64_t(own * float(kOne)));
+      if (lane == 0) sh.chunk[warp] = w;
+    }
+    // Where nothing depends on the mass below min-p's border, candidates end there (a little below it, for the roundings).
+    bool closed = false;
     if (greedy) {
-      const uint32_t key = key_of(sc.M);
-      token = locate(
-          sh, r, rank, ctas, per_cta, per_warp, [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); },
-          [&](uint64_t) { return uint64_t(0); }, total);
-      cut = {key, token};
-      logprob = 0.0f;
-    } else {
-      sc.c = kLog2eHi / T_;
-      sc.c_lo = (fmaf(-sc.c, T_, kLog2eHi) + kLog2eLo) / T_;
-      if (top_k > 0 && top_k < a.V)
-        cut = search(
-            sh, r, sc, rank, ctas, per_cta, per_warp, [&](float, uint32_t, int) { return uint64_t(1); },
-            [&](uint64_t) { return uint64_t(top_k); });
-      if (top_p < 1.0f) {
-        const Cut k = cut;
-        const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
-        cut = search(
-            sh, r, sc, rank, ctas, per_cta, per_warp,
-            [&](float x, uint32_t key, int i) { return k.keeps(key, i) ? weight(x, sc, sh.table) : uint64_t(0); },
-            [&](uint64_t all) {
-              const uint64_t whole = __umul64hi(part, all) + (part * all != 0 ? 1 : 0);  // p times the mass, up
-              return whole > 0 ? whole : uint64_t(1);
-            });
-        if (cut.key == k.key) cut.index = min(cut.index, k.index);
+      tau = sc.M;
+    } else if (min_p > 0.0f && (k == 0 || !nucleus)) {
+      const float span = T_ * logf(min_p), border = sc.M + span - 1e-5f * (fabsf(sc.M) - span);
+      if (!(tau > border) || nth > kThreads) {
+        tau = border;
+        closed = true;
       }
-      least = uint64_t(ceilf(min_p * float(kOne)));
-      const uint64_t draw = uint64_t(u * 18446744073709551616.0f);
-      token = locate(
-          sh, r, rank, ctas, per_cta, per_warp,
-          [&](float x, int i) {
-            if (!cut.keeps(key_of(x), i)) return uint64_t(0);
-            const uint64_t w = weight(x, sc, sh.table);
-            return w >= least ? w : uint64_t(0);
-          },
-          [&](uint64_t all) { return __umul64hi(draw, all); }, total);
-      const uint64_t w = weight(entry(r, token), sc, sh.table);
-      logprob = -log1pf(float(total - w) / float(w));
+    }
+    const bool trusted = !sums || fabsf(sc.M * sc.c) < kFastRange - 128.0f;
+    const bool by_list = trusted && (nth <= kThreads || closed);
+    bool settled = false;
+    if (by_list) {
+      collect(sh, r, top, tau);
+      row_sync();
+      const int found = share_out(sh, sc, r.ctas, !greedy);
+      uint64_t mass = 0;
+      if (sums)
+        for (int i = 0; i < r.ctas * kWarps; ++i) mass += ld_peer_u64(sh.chunk + i % kWarps, i / kWarps);
+      if (found > 0) settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, d);
+      if (settled) cut = sh.cut;
+      row_sync();  // (the peers have read the candidates)
+    } else if (trusted && sums && !nucleus) {
+      row_sync();
+      d = draw_fast(sh, r, sc, Kept{cut, -INFINITY}, draw, 0);
+      settled = d.token >= 0;
+    }
+    if (!settled) {
+      uint64_t kept = 0;
+      if (k > 0) cut = search<false>(sh, r, sc, cut, [&](uint64_t) { return uint64_t(k); }, kept);
+      kept = 0;
+      if (nucleus) {
+        const Cut first_k = cut;
+        const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
+        cut = search<true>(sh, r, sc, first_k, [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); }, kept);
+        if (cut.key == first_k.key) cut.index = min(cut.index, first_k.index);
+      }
+      if (least > 0) {
+        const uint32_t key = least_key(sh, sc, least);
+        if (key > cut.key) {
+          cut = {key, INT_MAX};
+          kept = 0;
+        }
+      }
+      const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
+      d.token = -1;
+      if (fabsf(sc.M * sc.c) < kFastRange && !(sums && !nucleus && trusted)) {
+        fast_sums(sh, r, sc, keep);
+        row_sync();
+        d = draw_fast(sh, r, sc, keep, draw, kept);
+      }
+      if (d.token < 0) d = draw_exact(sh, r, sc, keep, draw);
     }
   }
-  if (rank == 0 && tid == 0) {
+  if (r.rank == 0 && tid == 0) {
     if (!params_ok) atomicOr(a.status + b, ASV_REQ_BAD_PARAM);
     if (bad) atomicOr(a.status + b, ASV_REQ_NONFINITE);
-    a.tokens[b * a.tokens_b + n * a.tokens_n] = token;
-    if (a.logprobs != nullptr) a.logprobs[b * a.logprobs_b + n * a.logprobs_n] = logprob;
+    a.tokens[b * a.tokens_b + n * a.tokens_n] = d.token;
+    if (a.logprobs != nullptr)
+      a.logprobs[b * a.logprobs_b + n * a.logprobs_n] =
+          d.token < 0 ? -INFINITY : -log1pf(float(d.total - min(d.total, d.weight)) / float(d.weight));
   }
 
   // ---- the distribution
   if (a.probs != nullptr) {
     float* to = a.probs + b * a.probs_b + n * a.probs_n;
-    const float inv = token >= 0 && !greedy ? float(kOne) / float(total) : 1.0f;
-    sweep(r, [&](float x, int i) {
-      float p = 0.0f;
-      if (token >= 0 && cut.keeps(key_of(x), i)) {
-        if (greedy) {
-          p = 1.0f;
-        } else {
-          const uint64_t w = weight(x, sc, sh.table);
-          if (w >= least) p = float(w) * (1.0f / float(kOne)) * inv;
-        }
+    const float inv = d.token >= 0 ? float(kOne) / float(d.total) : 0.0f;
+    const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
+    const bool vectors = (reinterpret_cast<uintptr_t>(to) / 4 + kVec<T> - r.off) % 4 == 0;
+    const float far = -200.0f / sc.c;  // (what is further below has no weight)
+    stream<2>(r, [&](const uint4& w, int v) {
+      float x[kVec<T>], p[kVec<T>];
+      unpack(w, x);
+      const int i0 = v * kVec<T> - r.off;
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) {
+        const float s = fmaxf(x[e] - sc.M, far), t = s * sc.c, lo = fmaf(s, sc.c, -t) + s * sc.c_lo;
+        const float q = ex2_approx(t) * inv;
+        p[e] = d.token >= 0 && keep(x[e], i0 + e) ? fmaf(q, lo * kLn2Hi, q) : 0.0f;
       }
-      to[i] = p;
+      if (vectors && i0 >= 0 && i0 + kVec<T> <= a.V) {
+#pragma unroll
+        for (int e = 0; e < kVec<T>; e += 4)
+          __stcs(reinterpret_cast<float4*>(to + i0 + e), make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e)
+          if (i0 + e >= 0 && i0 + e < a.V) to[i0 + e] = p[e];
+      }
     });
   }
   row_sync();  // (no CTA leaves while its peers read its shared memory)
@@ -457,8 +1016,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 // CTAs to a row: enough that all rows' together fill the GPU, each with enough of the row to be worth its exchanges.
 int sample_ctas(const SampleArgs& a) {
-  int ctas = 1;
-  while (ctas < kMaxCtas && 2ll * ctas * a.B * a.n <= 304 && a.V / (2 * ctas) >= 2048) ctas *= 2;
+  int ctas = tuned_cluster();
+  if (ctas > 0) return std::min(ctas, kMaxCtas);
+  ctas = 1;
+  while (ctas < kMaxCtas && 2ll * ctas * a.B * a.n <= 152 * kCtasPerSm && a.V / (2 * ctas) >= 2048) ctas *= 2;
   return ctas;
 }
 

@@ -44,13 +44,20 @@ def sample64(x, u, T, k, p, least):
 BORDER = 2.0 ** -30
 
 
+# The kept mass, where no border is near, may be the sum of fp32 weights 2^t, t = fma(x, c, -ref): with D = (max - x) c (in
+# log2 units) a term is off by the roundings of c and t, ln 2 (2 D + 8) 2^-24, and by ex2, 2^-22; a thread's sum by ex2 once
+# more, by its additions and by its rounding to whole units, 2^-22 each.  Averaged over the mass D is at most the
+# distribution's entropy in bits, 19 for 2^19 entries: (ln 2 (2 * 19 + 8) + 4 * 4) 2^-24 < 2^-18 in all.
+MASS = 2.0 ** -18
+
+
 def logprob_bound(lp):
-    """Of ln((W - w) / w + 1) in fp32: three roundings of the quotient (2^-24 each), the logarithm's own two last places;
-    a kept mass summed from fp32 weights is off by 2^-21 at most."""
-    return 2.0 ** -20 + 2.0 ** -22 * abs(lp)
+    """Of ln((W - w) / w + 1) in fp32: the mass W; three roundings of the quotient (2^-24 each), the logarithm's own two
+    last places."""
+    return MASS + 2.0 ** -22 + 2.0 ** -22 * abs(lp)
 
 
 def probs_bound(p):
-    """Weight (2^-22, the special-function unit's), kept mass (2^-21) and their quotient (four roundings of 2^-24); what is
-    below the weights' unit."""
-    return 2.0 ** -20 * p + 2.0 ** -38
+    """The mass; weight (2^-22, the special-function unit's) and quotient (four roundings of 2^-24); what is below the
+    weights' unit."""
+    return (MASS + 2.0 ** -20) * p + 2.0 ** -38

@@ -320,15 +320,36 @@ def test_two_dimensions_one_row_for_all_and_positions_in_turn(m):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_the_result_does_not_depend_on_the_batch(m, dtype):
-    """One row to a cluster of many CTAs and to one: the same token, log-probability and distribution, bit for bit."""
+    """One row to a cluster of many CTAs and to one: the same token and the same cut (entries that are kept), and numbers
+    within twice their bounds of each other."""
     V = 40000
     for kind in ("peaked", "flat"):
         x, u = _logits_of(1, 1, V, kind, dtype, 4).cuda(), _draws(1, 1, 4).cuda()
         for kw in (dict(), dict(top_k=40), dict(top_p=0.9), dict(top_p=0.95, min_p=0.01, temperature=0.6)):
             one = m.sample_tokens(x, u, probs=True, **kw)
             many = m.sample_tokens(x.expand(700, 1, V), u.expand(700, 1), probs=True, **kw)
-            assert bool((many.tokens == one.tokens).all()) and bool((many.logprobs == one.logprobs).all())
-            assert bool((many.probs == one.probs).all())
+            assert bool((many.tokens == one.tokens).all())
+            lp = float(one.logprobs)
+            assert float((many.logprobs - lp).abs().max()) <= 2 * logprob_bound(lp)
+            p = one.probs.double()
+            assert bool(((many.probs - p).abs() <= 2 * probs_bound(p)).all())
+            assert bool(((many.probs > 0) == (one.probs > 0)).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ctas", range(1, 9))
+def test_numbers_of_ctas(m, ctas):
+    """Rows cut into one to eight runs, the last ones short or empty."""
+    m.set_tuning(ctas, 0)
+    try:
+        for dtype, V, kind in ((BF, 3, "peaked"), (F32, 61, "ties"), (BF, 2047, "peaked"), (F32, 30001, "flat"), (BF, 30001, "ties")):
+            x, u = _logits_of(2, 2, V, kind, dtype, ctas), _draws(2, 2, ctas)
+            for T, k, p, least in ((1.0, 0, 1.0, 0.0), (0.9, 17, 0.95, 0.0), (1.0, 0, 0.9, 0.0), (0.0, 0, 1.0, 0.0),
+                                   (1.0, 1500, 0.9, 0.0), (1.0, 0, 0.99, 0.01)):
+                got = m.sample_tokens(x.cuda(), u.cuda(), temperature=T, top_k=k, top_p=p, min_p=least, probs=True)
+                _compare(x, u, got, T, k, p, least)
+    finally:
+        m.set_tuning(0, 0)
 
 
 @pytest.mark.gpu
