@@ -37,8 +37,11 @@ constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 512;               // candidates that are compared pair by pair
 constexpr int kNucleus = 64;             // maxima of threads that a nucleus is first looked for above
+constexpr int kGroups = 16;              // groups of a thread's vectors, at most
+constexpr int kScan = 1024;              // groups that are read again, at most
 constexpr int kBins = 2048, kOwnBins = kBins / kThreads;
 constexpr int kMaxCtas = 8;
+constexpr int kAhead = 4;                // vectors a lane has in flight
 constexpr uint64_t kOne = uint64_t(1) << kSampleUnitBits;  // the largest weight
 
 template <class T>
@@ -51,20 +54,25 @@ struct Cut {
 };
 
 struct __align__(16) Shared {
+  union {                                        // one after the other
+    float group[(kGroups + 1) * kThreads];       // maxima of groups of a thread's vectors; of the row's ends
+    struct {
+      uint32_t lo[kBins], hi[kBins];             // a histogram's 64-bit sums
+    } bin;
+    uint4 sorted[kList];                         // the candidates in order
+  };
   uint4 list[kList];                             // candidates of the row: key, index, weight
-  uint32_t bin_lo[kBins], bin_hi[kBins];         // a histogram's 64-bit sums
-  uint64_t before[kList];                        // mass before each candidate, by value and then by index
+  uint64_t before[kList];                        // mass before each, by value or by index
   uint2 own[kList];                              // this CTA's candidates: key, index
   float tops[kThreads];                          // the threads' maxima
+  uint16_t scan[kScan];                          // groups whose vectors are read again
   float2 table[64];
   uint64_t chunk[kWarps];                        // sums of the warps' runs
   uint64_t room[kWarps], room2[kWarps];
   uint64_t pick_before, pick_sum, total;
-  uint16_t rank[kList];
-  uint16_t scan[kThreads];                       // threads whose vectors are read again
+  float4 ends;                                   // of the CTA: maximum, bound of the candidates, whether it is bad
   Cut cut;
-  float top, tau;
-  int bad, n_scan, n_own, last, found, pick;
+  int n_scan, n_own, found, pick;
 };
 
 // ------------------------------------------------------------------ a row
@@ -129,7 +137,7 @@ __device__ __forceinline__ uint4 load_vector(const Row<T>& r, int v) {
 }
 
 // f(vector, number) for the warp's vectors, kAhead of them a lane in flight.
-template <int kAhead, class T, class F>
+template <class T, class F>
 __device__ __forceinline__ void stream(const Row<T>& r, F f) {
   const int lane = threadIdx.x % 32;
   const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;  // whole vectors
@@ -341,87 +349,134 @@ __device__ __forceinline__ void add_weights(Partial& s, const float (&x)[N], flo
 
 // ------------------------------------------------------------------ candidates
 
-// The block's sum.
-__device__ __forceinline__ uint64_t block_sum(uint64_t x, uint64_t* room) {
-  x = warp_sum(x);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) room[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = 0;
-  for (int i = 0; i < kWarps; ++i) x += room[i];
-  return x;
-}
-
-// The n-th largest of the threads' values (1 <= n <= kThreads), to sh.tau.
-__device__ __forceinline__ void nth_largest(Shared& sh, float x, int n) {
-  const int tid = threadIdx.x;
-  sh.tops[tid] = x;
-  __syncthreads();
-  int larger = 0;
-#pragma unroll 4
-  for (int i = 0; i < kThreads; i += 4) {
-    const float4 y = *reinterpret_cast<const float4*>(sh.tops + i);
-    larger += (y.x > x || (y.x == x && i < tid)) + (y.y > x || (y.y == x && i + 1 < tid)) +
-              (y.z > x || (y.z == x && i + 2 < tid)) + (y.w > x || (y.w == x && i + 3 < tid));
+// The n-th largest of sh.tops (1 <= n <= kThreads) and the largest, by a warp: the longest beginning of a key that n of
+// the keys reach, two bits a step.
+__device__ __forceinline__ void nth_largest(const Shared& sh, int n, float& nth, float& top) {
+  constexpr int kEach = kThreads / 32;
+  const int lane = threadIdx.x % 32;
+  uint32_t key[kEach], most = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; i += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(sh.tops + lane * kEach + i);
+    key[i] = key_of(x.x), key[i + 1] = key_of(x.y), key[i + 2] = key_of(x.z), key[i + 3] = key_of(x.w);
   }
-  if (larger == n - 1) sh.tau = x;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) most = max(most, key[i]);
+  most = __reduce_max_sync(0xffffffffu, most);
+  top = value_of(most);
+  uint32_t at = 0;
+  if (n == 1) at = most;
+  for (int bit = n == 1 ? -2 : 30; bit >= 0; bit -= 2) {
+    // how many reach each of the three next beginnings, 10 bits each
+    const uint32_t one = at + (1u << bit), two = at + (2u << bit), three = at + (3u << bit);
+    uint32_t count = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      count += (key[i] >= one ? 1u : 0u) + (key[i] >= two ? 1u << 10 : 0u) + (key[i] >= three ? 1u << 20 : 0u);
+    count = __reduce_add_sync(0xffffffffu, count);
+    at = int(count >> 20) >= n ? three : int((count >> 10) & 1023u) >= n ? two : int(count & 1023u) >= n ? one : at;
+  }
+  nth = value_of(at);
 }
 
-// The CTA's entries from tau on, out of the vectors of the threads whose maximum reaches it, to sh.own (those that have
+// Where the thread's groups of vectors lie: vector q of the thread is first + 32 q, and in group q / per_group.
+template <class T>
+struct Groups {
+  int per_group;
+  __device__ __forceinline__ explicit Groups(const Row<T>& r) {
+    const int each = (r.per_warp + 31) / 32;
+    per_group = ((each + kGroups - 1) / kGroups + kAhead - 1) / kAhead * kAhead;
+  }
+};
+
+// The CTA's entries from tau on, out of the groups of vectors whose maximum reaches it, to sh.own (those that have
 // room; sh.n_own counts them all).
 template <class T>
-__device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float own_top, float tau) {
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+__device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
+  const int tid = threadIdx.x;
   if (tid == 0) sh.n_scan = sh.n_own = 0;
   __syncthreads();
-  const bool again = own_top >= tau;
-  const uint32_t votes = __ballot_sync(0xffffffffu, again);
-  int at = 0;
-  if (lane == 0 && votes != 0) at = atomicAdd(&sh.n_scan, __popc(votes));
-  at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1u));
-  if (again) sh.scan[at] = uint16_t(tid);
+#pragma unroll
+  for (int g = 0; g <= kGroups; ++g) {
+    if (sh.group[g * kThreads + tid] >= tau) {
+      const int at = atomicAdd(&sh.n_scan, 1);
+      if (at < kScan) sh.scan[at] = uint16_t(g * kThreads + tid);
+    }
+  }
   __syncthreads();
-  const int n = sh.n_scan;
-  // a thread's vectors are 32 apart; all of them are shared out, a vector a lane
-  const int per_thread = (r.per_warp + 31) / 32;
-  for (int x = warp * 32 + lane; x < n * per_thread; x += kThreads) {
-    const int k = x / per_thread, q = x - k * per_thread, t = sh.scan[k];
-    const int v0 = r.run_start(r.rank, t / 32), v1 = r.run_end(r.rank, t / 32);
-    // (the row's ends are with the first two lanes of their warp, whichever they would fall to)
-    const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;
-    const int first = max(v0, w0) + t % 32, v = first + 32 * q;
-    auto take = [&](int v) {
-      const uint4 w = load_vector(r, v);
-      float x[kVec<T>];
-      unpack(w, x);
+  const int n = sh.n_scan, per_group = Groups<T>(r).per_group;
+  if (n > kScan) {
+    if (tid == 0) sh.n_own = kList + 1;
+    return;
+  }
+  const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;
+  // the vector that number x of all groups' is, < 0: none
+  auto vector_at = [&](int x) {
+    const int k = x / per_group, q = x - k * per_group;
+    if (k >= n) return -1;
+    const int g = sh.scan[k] / kThreads, t = sh.scan[k] % kThreads, warp = t / 32, lane = t % 32;
+    const int v0 = r.run_start(r.rank, warp), v1 = r.run_end(r.rank, warp);
+    if (g == kGroups) {  // the row's ends (stream)
+      if (q == 0 && lane == 0 && v0 == 0 && w0 == 1 && v1 > 0) return 0;
+      return q == 0 && lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= v0 && w1 < v1 ? w1 : -1;
+    }
+    const int v = max(v0, w0) + lane + 32 * (g * per_group + q);
+    return v < min(v1, w1) ? v : -1;
+  };
+  for (int x = tid; x < n * per_group; x += 4 * kThreads) {
+    int v[4];
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = vector_at(x + i * kThreads);
+      if (v[i] >= 0) w[i] = load_vector(r, v[i]);
+    }
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const uint4 ww = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+      const int vv = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+      if (vv < 0 || !(vector_max(ww, static_cast<T*>(nullptr)) >= tau)) continue;
+      float y[kVec<T>];
+      unpack(ww, y);
 #pragma unroll
       for (int e = 0; e < kVec<T>; ++e) {
-        const int i = v * kVec<T> - r.off + e;
-        if (x[e] >= tau && i >= 0 && i < r.V) {
+        const int index = vv * kVec<T> - r.off + e;
+        if (y[e] >= tau && index >= 0 && index < r.V) {
           const int to = atomicAdd(&sh.n_own, 1);
-          if (to < kList) sh.own[to] = make_uint2(key_of(x[e]), uint32_t(i));
+          if (to < kList) sh.own[to] = make_uint2(key_of(y[e]), uint32_t(index));
         }
       }
-    };
-    if (v < min(v1, w1)) take(v);
-    if (q == 0 && t % 32 == 0 && v0 == 0 && w0 == 1 && v1 > 0) take(0);
-    if (q == 0 && t % 32 == 1 && w1 >= w0 && w1 < r.vectors && w1 >= v0 && w1 < v1) take(w1);
+    }
   }
 }
 
-// The row's candidates of all CTAs, with their weights, to sh.list; their number, or -1 if there is no room.
-__device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, bool weights) {
-  int n = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const int m = int(ld_peer_u32(&sh.n_own, c));
-    if (n + m > kList) return -1;
-    for (int i = threadIdx.x; i < m; i += kThreads) {
-      const uint64_t e = ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.own + i), c);
-      const uint32_t key = uint32_t(e), index = uint32_t(e >> 32);
-      const uint64_t w = weights ? weight(value_of(key), sc, sh.table) : kOne;
-      sh.list[n + i] = make_uint4(key, index, uint32_t(w), uint32_t(w >> 32));
+// The row's candidates of all CTAs, with their weights (kOne each without), to sh.list; their number, or -1 if there is no
+// room.
+__device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, bool weigh) {
+  const int lane = threadIdx.x % 32;
+  const int own = lane < ctas ? int(ld_peer_u32(&sh.n_own, lane)) : 0;
+  int upto = own;
+#pragma unroll
+  for (int d = 1; d < kMaxCtas; d *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  if (__any_sync(0xffffffffu, lane < ctas && (own > kList || upto > kList))) return -1;
+  const int n = __shfl_sync(0xffffffffu, upto, kMaxCtas - 1);
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    int c = 0, start = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxCtas - 1; ++k) {
+      const int end = __shfl_sync(0xffffffffu, upto, k);
+      if (i >= end) c = k + 1, start = end;
     }
-    n += m;
+    if (i < n) {
+      const uint64_t e = ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.own + (i - start)), c);
+      const uint32_t key = uint32_t(e), index = uint32_t(e >> 32);
+      const uint64_t w = weigh ? weight(value_of(key), sc, sh.table) : kOne;
+      sh.list[i] = make_uint4(key, index, uint32_t(w), uint32_t(w >> 32));
+    }
   }
   __syncthreads();
   return n;
@@ -429,39 +484,116 @@ __device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, boo
 
 __device__ __forceinline__ uint64_t weight_in(const uint4& e) { return (uint64_t(e.w) << 32) | e.z; }
 
+// The warps' sums of all CTAs, added up by each warp.
+__device__ __forceinline__ uint64_t all_chunks(const Shared& sh, int ctas) {
+  uint64_t x = 0;
+  for (int i = threadIdx.x % 32; i < ctas * kWarps; i += 32) x += ld_peer_u64(sh.chunk + i % kWarps, i / kWarps);
+  return warp_sum(x);
+}
+
 // p of a mass, p as a fraction of 2^64, rounded up.
 __device__ __forceinline__ uint64_t part_of(uint64_t part, uint64_t mass) {
   return __umul64hi(part, mass) + (part * mass != 0 ? 1 : 0);
 }
 
-// For all candidates: the mass and the number of the others y with before(y, candidate), to sh.before and sh.rank.  A
-// group of threads has one where there are few.
-template <class F>
-__device__ __forceinline__ void all_pairs(Shared& sh, int n, F before) {
-  const int tid = threadIdx.x;
-  int g = 1;
-  while (g < 32 && 2 * g * n <= kThreads) g *= 2;
-  for (int e0 = 0; e0 < n; e0 += kThreads / g) {
-    const int e = e0 + tid / g;
-    const uint4 mine = sh.list[min(e, n - 1)];
-    uint64_t mass = 0;
-    int rank = 0;
-#pragma unroll 4
-    for (int j = tid % g; j < n; j += g) {
-      const uint4 y = sh.list[j];
-      if (before(y, mine)) {
-        mass += weight_in(y);
-        ++rank;
+// A warp sorts its 32 R numbers, the largest first, element lane * R + i in x[i]: a bitonic network.
+template <int R>
+__device__ __forceinline__ void sort_down(uint64_t (&x)[R]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int k = 2; k <= 32 * R; k *= 2) {
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2) {
+      if (j >= R) {
+        const int far = j / R;
+        // (of the pair the lower place keeps the larger where its block of k goes down)
+        const bool larger = ((lane & far) == 0) == ((lane * R & k) == 0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const uint64_t y = __shfl_xor_sync(0xffffffffu, x[i], far);
+          x[i] = (x[i] > y) == larger ? x[i] : y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if ((i & j) != 0) continue;
+          const bool down = ((lane * R + i) & k) == 0;
+          const uint64_t a = x[i], b = x[i | j];
+          const bool swap = (a < b) == down;
+          x[i] = swap ? b : a;
+          x[i | j] = swap ? a : b;
+        }
       }
     }
-    for (int o = 1; o < g; o *= 2) {
-      mass += __shfl_xor_sync(0xffffffffu, mass, o);
-      rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  }
+}
+
+template <int R>
+__device__ __noinline__ void sort_warp(Shared& sh, int n) {
+  const int lane = threadIdx.x % 32;
+  // key, index turned round, place in the list: 32, 19 and 9 bits
+  static_assert(kSampleMaxVocab == 1 << 19 && kList == 1 << 9);
+  uint64_t x[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = lane * R + i;
+    x[i] = 0;
+    if (e < n) {
+      const uint4 y = sh.list[e];
+      x[i] = (uint64_t(y.x) << 32) | (uint64_t(uint32_t(kSampleMaxVocab - 1) - y.y) << 9) | uint32_t(e);
     }
-    if (tid % g == 0 && e < n) {
-      sh.before[e] = mass;
-      sh.rank[e] = uint16_t(rank);
+  }
+  sort_down<R>(x);
+  uint64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (lane * R + i < n) sum += weight_in(sh.list[x[i] & (kList - 1)]);
+  uint64_t before = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint64_t y = shfl_up_u64(before, d);
+    if (lane >= d) before += y;
+  }
+  before -= sum;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = lane * R + i;
+    if (e < n) {
+      const uint4 y = sh.list[x[i] & (kList - 1)];
+      sh.sorted[e] = y;
+      sh.before[e] = before;
+      before += weight_in(y);
     }
+  }
+}
+
+// The candidates in order, to sh.sorted, and the mass before each, to sh.before.
+__device__ __forceinline__ void sort_list(Shared& sh, int n) {
+  if (threadIdx.x < 32) {
+    if (n <= 64) sort_warp<2>(sh, n);
+    else if (n <= 128) sort_warp<4>(sh, n);
+    else sort_warp<16>(sh, n);
+  }
+  __syncthreads();
+}
+
+// The mass of the first m candidates with lower indices than each, to sh.before.  A group of threads has one where there
+// are few.
+__device__ __forceinline__ void masses_by_index(Shared& sh, int m) {
+  const int tid = threadIdx.x;
+  int g = 1;
+  while (g < 32 && 2 * g * m <= kThreads) g *= 2;
+  for (int e0 = 0; e0 < m; e0 += kThreads / g) {
+    const int e = e0 + tid / g;
+    const uint32_t index = sh.sorted[min(e, m - 1)].y;
+    uint64_t mass = 0;
+#pragma unroll 4
+    for (int j = tid % g; j < m; j += g) {
+      const uint4 y = sh.sorted[j];
+      if (y.y < index) mass += weight_in(y);
+    }
+    for (int o = 1; o < g; o *= 2) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    if (tid % g == 0 && e < m) sh.before[e] = mass;
   }
   __syncthreads();
 }
@@ -478,11 +610,8 @@ struct Drawn {
 __device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t least, bool closed, uint64_t mass,
                                     uint64_t off, uint64_t draw, Drawn& d) {
   const int tid = threadIdx.x;
-  all_pairs(sh, n, [](const uint4& y, const uint4& e) { return y.x > e.x || (y.x == e.x && y.y < e.y); });
-  uint64_t sum = 0;
-  for (int e = tid; e < n; e += kThreads)
-    if (k == 0 || sh.rank[e] < k) sum += weight_in(sh.list[e]);
-  sum = block_sum(sum, sh.room);
+  sort_list(sh, n);
+  const uint64_t sum = k > 0 && k < n ? sh.before[k] : sh.before[n - 1] + weight_in(sh.sorted[n - 1]);
   if (k > 0) {
     mass = sum;
     off = 0;
@@ -494,32 +623,25 @@ __device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t 
     high = max(part_of(part, mass + off), uint64_t(1));
   }
   bool unsure = k == 0 && p < 1.0f && !closed && sum < high;
-  if (tid == 0) sh.last = 0;
-  __syncthreads();
-  uint64_t kept = 0;
-  for (int e = tid; e < n; e += kThreads) {
-    const uint64_t w = weight_in(sh.list[e]), b = sh.before[e];
-    const int rank = sh.rank[e];
-    bool keep = (k == 0 || rank < k) && w >= least;
-    unsure = unsure || (keep && b >= low && b < high);
-    keep = rank == 0 || (keep && b < low);
-    if (keep) {
-      kept += w;
-      atomicMax(&sh.last, rank);
-    } else {
-      sh.list[e].z = sh.list[e].w = 0;
-    }
+  // the kept ones are the first m
+  int m = 0;
+  for (int e0 = 0; e0 < n; e0 += kThreads) {
+    const int e = e0 + tid;
+    const uint64_t w = e < n ? weight_in(sh.sorted[e]) : 0, b = e < n ? sh.before[e] : 0;
+    const bool may = e < n && (k == 0 || e < k) && w >= least;
+    unsure = unsure || (may && b >= low && b < high);
+    m += __syncthreads_count(e == 0 || (may && b < low));
   }
   if (__syncthreads_or(unsure)) return false;
-  for (int e = tid; e < n; e += kThreads)
-    if (sh.rank[e] == sh.last) sh.cut = {sh.list[e].x, int(sh.list[e].y)};
-  d.total = block_sum(kept, sh.room);
+  d.total = m < n ? sh.before[m] : sh.before[n - 1] + weight_in(sh.sorted[n - 1]);
   const uint64_t at = __umul64hi(draw, d.total);
-  all_pairs(sh, n, [](const uint4& y, const uint4& e) { return y.y < e.y; });
-  for (int e = tid; e < n; e += kThreads) {
-    const uint64_t w = weight_in(sh.list[e]), b = sh.before[e];
+  if (tid == 0) sh.cut = {sh.sorted[m - 1].x, int(sh.sorted[m - 1].y)};
+  __syncthreads();  // (all have read what is before whom)
+  masses_by_index(sh, m);
+  for (int e = tid; e < m; e += kThreads) {
+    const uint64_t w = weight_in(sh.sorted[e]), b = sh.before[e];
     if (b <= at && at < b + w) {
-      sh.found = int(sh.list[e].y);
+      sh.found = int(sh.sorted[e].y);
       sh.pick_sum = w;
     }
   }
@@ -549,23 +671,33 @@ __device__ __forceinline__ uint64_t find_run(Shared& sh, const Row<T>& r, uint64
   return at;
 }
 
-// The entry of run sh.pick that `at` falls into, f(x, index) entry by entry: to sh.found of the CTA that owns the run (-1:
-// within `margin` of the entry's ends, or in none), read from there by all.
-template <class T, class F>
-__device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t at, uint64_t margin, F f) {
-  const int tid = threadIdx.x;
+// The entry of run sh.pick that `at` falls into: to sh.found of the CTA that owns the run (-1: within `margin` of the
+// entry's ends, or in none), read from there by all.  sum_of(v0, v1): a warp's sum of the entries of vectors [v0, v1), f(x,
+// index) one entry's.
+template <class T, class S, class F>
+__device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t at, uint64_t margin, S sum_of, F f) {
+  const int tid = threadIdx.x, warp = tid / 32;
   if (tid == 0) sh.found = -1;
   __syncthreads();
   const int pick = sh.pick, owner = pick / kWarps;
   if (r.rank == owner) {
+    // the part of the run that a warp has
     const int v0 = r.run_start(owner, pick % kWarps), v1 = r.run_end(owner, pick % kWarps);
-    const int i0 = max(v0 * kVec<T> - r.off, 0), i1 = min(v1 * kVec<T> - r.off, r.V);
+    const int each = (v1 - v0 + kWarps - 1) / kWarps;
+    uint64_t before = sh.pick_before;
+    const uint64_t own = sum_of(min(v0 + warp * each, v1), min(v0 + (warp + 1) * each, v1));
+    if (tid % 32 == 0) sh.room2[warp] = own;
+    __syncthreads();
+    int part = 0;
+    for (; part < kWarps - 1 && before + sh.room2[part] <= at; ++part) before += sh.room2[part];
+    // entry by entry, each thread a few
+    const int i0 = max(min(v0 + part * each, v1) * kVec<T> - r.off, 0);
+    const int i1 = min(min(v0 + (part + 1) * each, v1) * kVec<T> - r.off, r.V);
     const int per = (i1 - i0 + kThreads - 1) / kThreads, a = min(i0 + tid * per, i1), b = min(a + per, i1);
     uint64_t sum = 0;
     for (int i = a; i < b; ++i) sum += f(entry(r, i), i);
-    const uint64_t upto = sh.pick_before + block_scan(sum, sh.room2);
-    uint64_t before = upto - sum;
-    if (upto > at && before <= at) {
+    before += block_scan(sum, sh.room) - sum;
+    if (before <= at && at < before + sum) {
       for (int i = a; i < b; ++i) {
         const uint64_t w = f(entry(r, i), i);
         if (before + w > at) {
@@ -583,11 +715,23 @@ __device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t 
   return found;
 }
 
+// f(vector, number) for a warp's vectors [v0, v1), whole or not.
+template <class T, class F>
+__device__ __forceinline__ void few(const Row<T>& r, int v0, int v1, F f) {
+  for (int v = v0 + int(threadIdx.x % 32); v < v1; v += 64) {
+    const uint4 a = load_vector(r, v);
+    const bool two = v + 32 < v1;
+    const uint4 b = two ? load_vector(r, v + 32) : a;
+    f(a, v);
+    if (two) f(b, v + 32);
+  }
+}
+
 // The index of the n-th entry with this key (n >= 1).
 template <class T>
 __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key, uint64_t n) {
-  uint32_t own = 0;
-  stream<4>(r, [&](const uint4& w, int v) {
+  uint64_t own = 0;
+  auto count = [&](const uint4& w, int v) {
     float x[kVec<T>];
     unpack(w, x);
 #pragma unroll
@@ -595,9 +739,10 @@ __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key,
       const int i = v * kVec<T> - r.off + e;
       own += key_of(x[e]) == key && i >= 0 && i < r.V;
     }
-  });
-  const uint64_t sum = warp_sum(own);
-  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = sum;
+  };
+  stream(r, count);
+  own = warp_sum(own);
+  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
   row_sync();
   // (the share n - 1 of the count, as find_run takes it: it is looked for in units, not in parts of 2^64)
   const int tid = threadIdx.x, runs = r.ctas * kWarps;
@@ -607,7 +752,14 @@ __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key,
     sh.pick = tid;
     sh.pick_before = incl - mine;
   }
-  return find_entry(sh, r, n - 1, 0, [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); });
+  return find_entry(
+      sh, r, n - 1, 0,
+      [&](int v0, int v1) {
+        own = 0;
+        few(r, v0, v1, count);
+        return warp_sum(own);
+      },
+      [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); });
 }
 
 // The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
@@ -621,9 +773,9 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
   const float width = float(kBins - 1) / float(kSampleUnitBits + 3) * sc.c;
   auto bin_of = [&](float x) { return min(int((sc.M - x) * width), kBins - 1); };
   auto add = [&](int bin, uint64_t m) {
-    const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bin_lo[bin], low);
+    const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bin.lo[bin], low);
     const uint32_t high = uint32_t(m >> 32) + (old + low < old ? 1u : 0u);
-    if (high) atomicAdd(&sh.bin_hi[bin], high);
+    if (high) atomicAdd(&sh.bin.hi[bin], high);
   };
   uint32_t lo = 1, hi = key_of(sc.M);
   int shift = 32, first_bin = 0;
@@ -634,11 +786,11 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       shift = 0;
       while ((span >> shift) >= uint32_t(kBins)) ++shift;
     }
-    for (int i = tid; i < kBins; i += kThreads) sh.bin_lo[i] = sh.bin_hi[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.bin.lo[i] = sh.bin.hi[i] = 0;
     if (tid == 0) sh.n_own = 0;
     __syncthreads();
     if (level == 0) {
-      stream<2>(r, [&](const uint4& w, int v) {
+      stream(r, [&](const uint4& w, int v) {
         float x[kVec<T>];
         unpack(w, x);
         uint64_t m[kVec<T>];
@@ -652,7 +804,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       });
     } else {
       const float least = value_of(lo);
-      stream<4>(r, [&](const uint4& w, int v) {
+      stream(r, [&](const uint4& w, int v) {
         if (vector_max(w, static_cast<T*>(nullptr)) < least) return;
         float x[kVec<T>];
         unpack(w, x);
@@ -672,11 +824,11 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     row_sync();
     const int n = level > 0 ? share_out(sh, sc, r.ctas, MASS) : -1;
     if (n > 0) {
-      all_pairs(sh, n, [](const uint4& y, const uint4& e) { return y.x > e.x || (y.x == e.x && y.y < e.y); });
+      sort_list(sh, n);
       for (int e = tid; e < n; e += kThreads) {
-        const uint64_t m = MASS ? weight_in(sh.list[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(sh.rank[e]));
+        const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(e));
         if (b < target && target <= b + m) {
-          sh.cut = {sh.list[e].x, int(sh.list[e].y)};
+          sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
           sh.total = b + m;
         }
       }
@@ -690,8 +842,8 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     for (int c = 0; c < r.ctas; ++c)
 #pragma unroll
       for (int i = 0; i < kOwnBins; ++i)
-        own[i] += (uint64_t(ld_peer_u32(sh.bin_hi + tid * kOwnBins + i, c)) << 32) +
-                  ld_peer_u32(sh.bin_lo + tid * kOwnBins + i, c);
+        own[i] += (uint64_t(ld_peer_u32(sh.bin.hi + tid * kOwnBins + i, c)) << 32) +
+                  ld_peer_u32(sh.bin.lo + tid * kOwnBins + i, c);
 #pragma unroll
     for (int i = 0; i < kOwnBins; ++i) sum += own[i];
     const uint64_t incl = block_scan(sum, sh.room);
@@ -761,6 +913,25 @@ struct Kept {
   __device__ __forceinline__ bool operator()(float x, int i) const { return x > value || (x == value && i <= cut.index); }
 };
 
+// A vector's fast weights of kept entries onto a sum whose reference is the row's maximum.
+template <class T>
+__device__ __forceinline__ void add_kept(Partial& s, const uint4& w, int v, const Row<T>& r, const Scale& sc, const Kept& keep) {
+  const float ref = -sc.M * sc.c;
+  float x[kVec<T>], sum = 0.0f;
+  unpack(w, x);
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e)
+    if (keep(x[e], v * kVec<T> - r.off + e)) sum += ex2_approx(fmaf(x[e], sc.c, ref));
+  const float all = s.hi + sum, bb = all - s.hi;
+  s.lo += (s.hi - (all - bb)) + (sum - bb);
+  s.hi = all;
+}
+
+__device__ __forceinline__ uint64_t units_of(const Partial& s, const Scale& sc) {
+  // (what the rounding of the reference leaves the maximum itself has too)
+  return uint64_t((s.hi + s.lo) * ex2_approx(-fmaf(sc.M, sc.c, -sc.M * sc.c)) * float(kOne));
+}
+
 // A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync); total: the kept mass, 0: that
 // of the sums.  A token < 0: too near a border to say.
 template <class T>
@@ -770,8 +941,15 @@ __device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale
   __syncthreads();
   Drawn d;
   d.total = total > 0 ? total : sh.total;
-  d.token = find_entry(sh, r, at, 2 * ((sh.total >> kFastBits) + 1),
-                       [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
+  // (the sums before the run, those within it, and where the total is theirs the draw's place)
+  d.token = find_entry(
+      sh, r, at, 3 * ((sh.total >> kFastBits) + 1),
+      [&](int v0, int v1) {
+        Partial s;
+        few(r, v0, v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
+        return warp_sum(units_of(s, sc));
+      },
+      [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
   d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, sh.table) : 0;
   return d;
 }
@@ -779,23 +957,9 @@ __device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale
 // The warps' fast sums of the kept entries, to sh.chunk.
 template <class T>
 __device__ __noinline__ void fast_sums(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep) {
-  const float ref = -sc.M * sc.c;
   Partial s;
-  s.ref = 0.0f;
-  stream<4>(r, [&](const uint4& w, int v) {
-    float x[kVec<T>];
-    unpack(w, x);
-    float sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kVec<T>; ++e)
-      if (keep(x[e], v * kVec<T> - r.off + e)) sum += ex2_approx(fmaf(x[e], sc.c, ref));
-    const float all = s.hi + sum, bb = all - s.hi;
-    s.lo += (s.hi - (all - bb)) + (sum - bb);
-    s.hi = all;
-  });
-  // (every reference is the maximum's: what fma leaves of it, the maximum itself has too)
-  const float own = (s.hi + s.lo) * ex2_approx(-fmaf(sc.M, sc.c, ref));
-  const uint64_t w = warp_sum(uint64_t(own * float(kOne)));
+  stream(r, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
+  const uint64_t w = warp_sum(units_of(s, sc));
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = w;
 }
 
@@ -803,7 +967,7 @@ __device__ __noinline__ void fast_sums(Shared& sh, const Row<T>& r, const Scale&
 template <class T>
 __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw) {
   uint64_t own = 0;
-  stream<2>(r, [&](const uint4& w, int v) {
+  auto add = [&](const uint4& w, int v) {
     float x[kVec<T>];
     unpack(w, x);
     uint64_t m[kVec<T>];
@@ -811,7 +975,8 @@ __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scal
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e)
       if (keep(x[e], v * kVec<T> - r.off + e)) own += m[e];
-  });
+  };
+  stream(r, add);
   own = warp_sum(own);
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
   row_sync();
@@ -819,7 +984,14 @@ __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scal
   __syncthreads();
   Drawn d;
   d.total = sh.total;
-  d.token = find_entry(sh, r, at, 0, [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
+  d.token = find_entry(
+      sh, r, at, 0,
+      [&](int v0, int v1) {
+        own = 0;
+        few(r, v0, v1, add);
+        return warp_sum(own);
+      },
+      [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
   d.weight = weight(entry(r, d.token), sc, sh.table);
   return d;
 }
@@ -839,7 +1011,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
   if (tid == 0) {
     sh.found = sh.pick = 0;
     sh.pick_before = sh.pick_sum = sh.total = 0;
-    sh.tau = -INFINITY;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -873,37 +1044,74 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
   const bool sums = k == 0 && (nucleus || min_p == 0.0f);
   float top = -INFINITY;
   Partial part;
-  if (sums) {
-    stream<4>(r, [&](const uint4& w, int) {
+  {
+    const int per_group = Groups<T>(r).per_group;
+    float most = -INFINITY;  // of the group
+    int g = 0, left = per_group;
+    auto one = [&](const uint4& w) {
       const float m = vector_max(w, static_cast<T*>(nullptr));
-      float x[kVec<T>];
-      unpack(w, x);
-      top = max_nan(top, m);
-      add_weights(part, x, m, sc.c);
-    });
-  } else {
-    stream<4>(r, [&](const uint4& w, int) { top = max_nan(top, vector_max(w, static_cast<T*>(nullptr))); });
+      if (sums) {
+        float x[kVec<T>];
+        unpack(w, x);
+        add_weights(part, x, m, sc.c);
+      }
+      return m;
+    };
+    auto close = [&]() {
+      sh.group[g * kThreads + tid] = most;
+      top = max_nan(top, most);
+      most = -INFINITY;
+      ++g;
+      left = per_group;
+    };
+    const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>, end = min(r.v1, w1);  // whole vectors
+    const uint4* p = reinterpret_cast<const uint4*>(r.base);
+    int v = max(r.v0, w0) + lane;
+    for (; v + 32 * (kAhead - 1) < end; v += 32 * kAhead) {
+      uint4 w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) w[i] = __ldg(p + v + 32 * i);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) most = max_nan(most, one(w[i]));
+      left -= kAhead;
+      if (left == 0) close();
+    }
+    for (; v < end; v += 32) most = max_nan(most, one(__ldg(p + v)));
+    while (g < kGroups) close();
+    // the row's ends (as in stream)
+    if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) most = one(edge_vector(r, 0));
+    if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) most = one(edge_vector(r, w1));
+    close();
   }
-  bool bad = __syncthreads_or(!(top < INFINITY));
+  bool bad = __any_sync(0xffffffffu, !(top < INFINITY));
   // Candidates are looked for from tau on: the row's k-th largest is at least the least of the CTAs' (k / ctas)-th
   // largest maxima of threads.
   const int nth = k > 0 ? (k + r.ctas - 1) / r.ctas : nucleus ? max(kNucleus / r.ctas, 1) : kThreads + 1;
-  if (nth <= kThreads) nth_largest(sh, top, nth);
-  float m = warp_max(top);
-  if (lane == 0) sh.chunk[warp] = __float_as_uint(m);
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, __uint_as_float(uint32_t(sh.chunk[w])));
-    sh.top = m;
-    sh.bad = bad;
+  sh.tops[tid] = top;
+  bad = __syncthreads_or(bad);
+  if (warp == 0) {
+    float least_top = -INFINITY, most = -INFINITY;
+    nth_largest(sh, min(nth, kThreads), least_top, most);
+    if (lane == 0) sh.ends = make_float4(most, nth <= kThreads ? least_top : -INFINITY, bad ? 1.0f : 0.0f, 0.0f);
   }
   row_sync();
-  float tau = INFINITY;
-  sc.M = -INFINITY;
-  for (int c = 0; c < r.ctas; ++c) {
-    sc.M = fmaxf(sc.M, __uint_as_float(ld_peer_u32(&sh.top, c)));
-    tau = fminf(tau, __uint_as_float(ld_peer_u32(&sh.tau, c)));
-    bad = bad || ld_peer_u32(&sh.bad, c) != 0;
+  float tau;
+  {
+    float4 e = make_float4(-INFINITY, INFINITY, 0.0f, 0.0f);
+    if (lane < r.ctas) {
+      const uint64_t ab = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends), lane);
+      e.x = __uint_as_float(uint32_t(ab));
+      e.y = __uint_as_float(uint32_t(ab >> 32));
+      e.z = __uint_as_float(ld_peer_u32(&sh.ends.z, lane));
+    }
+    bad = __any_sync(0xffffffffu, e.z != 0.0f);
+#pragma unroll
+    for (int o = 1; o < kMaxCtas; o *= 2) {
+      e.x = fmaxf(e.x, __shfl_xor_sync(0xffffffffu, e.x, o));
+      e.y = fminf(e.y, __shfl_xor_sync(0xffffffffu, e.y, o));
+    }
+    sc.M = __shfl_sync(0xffffffffu, e.x, 0);
+    tau = __shfl_sync(0xffffffffu, e.y, 0);
   }
   bad = bad || sc.M == -INFINITY;
 
@@ -933,12 +1141,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
     const bool by_list = trusted && (nth <= kThreads || closed);
     bool settled = false;
     if (by_list) {
-      collect(sh, r, top, tau);
+      collect(sh, r, tau);
       row_sync();
       const int found = share_out(sh, sc, r.ctas, !greedy);
-      uint64_t mass = 0;
-      if (sums)
-        for (int i = 0; i < r.ctas * kWarps; ++i) mass += ld_peer_u64(sh.chunk + i % kWarps, i / kWarps);
+      const uint64_t mass = sums ? all_chunks(sh, r.ctas) : 0;
       if (found > 0) settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, d);
       if (settled) cut = sh.cut;
       row_sync();  // (the peers have read the candidates)
@@ -990,7 +1196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
     const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
     const bool vectors = (reinterpret_cast<uintptr_t>(to) / 4 + kVec<T> - r.off) % 4 == 0;
     const float far = -200.0f / sc.c;  // (what is further below has no weight)
-    stream<2>(r, [&](const uint4& w, int v) {
+    stream(r, [&](const uint4& w, int v) {
       float x[kVec<T>], p[kVec<T>];
       unpack(w, x);
       const int i0 = v * kVec<T> - r.off;
