@@ -6,9 +6,9 @@
 // entry.  The token is the first kept index whose cumulative mass (over kept entries, by index) passes u times the
 // kept mass; the distribution is w over the kept mass.
 //
-// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out as (hi, lo) pairs to
-// about 2^-39 and summed in units of 2^-44 in 64-bit integers, which makes their sums exact in any order.  That costs 50
-// operations an entry, so few are weighed so:
+// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out to 2^-35 of themselves
+// and summed in units of 2^-44 in 64-bit integers, which makes their sums exact in any order.  That costs 40 operations an
+// entry, so few are weighed so:
 //   - The row streams once, for the maxima of the threads' vectors and, where the whole row's mass counts, a running sum of
 //     fp32 weights (two operations and ex2).  Its error is bounded; a border within the bound counts as undecided.
 //   - Where the n largest maxima of threads bound the kept set from below (top-k; a nucleus, by trial; min-p's border),
@@ -16,7 +16,7 @@
 //     compared pair by pair: rank and mass before each, then the draw.
 //   - A draw from the whole row finds the warp's run that u falls into by the fp32 sums and weighs that run alone.
 //   - What stays undecided, or has too many candidates, goes by histograms of exact masses over the row, level by level
-//     until the rest fits the pairwise comparison.
+//     until the rest fits the comparison.
 //
 // A cluster of CTAs has a row, each a run of its vectors, each warp a run of the CTA's.  All CTAs come to the same
 // decisions from the same exchanged numbers.
@@ -39,7 +39,7 @@ constexpr int kList = 512;               // candidates that are compared pair by
 constexpr int kNucleus = 64;             // maxima of threads that a nucleus is first looked for above
 constexpr int kGroups = 16;              // groups of a thread's vectors, at most
 constexpr int kScan = 1024;              // groups that are read again, at most
-constexpr int kBins = 2048, kOwnBins = kBins / kThreads;
+constexpr int kBins = 2048;
 constexpr int kMaxCtas = 8;
 constexpr int kAhead = 4;                // vectors a lane has in flight
 constexpr uint64_t kOne = uint64_t(1) << kSampleUnitBits;  // the largest weight
@@ -56,17 +56,18 @@ struct Cut {
 struct __align__(16) Shared {
   union {                                        // one after the other
     float group[(kGroups + 1) * kThreads];       // maxima of groups of a thread's vectors; of the row's ends
+    uint2 bins[kBins];                           // a histogram's 64-bit sums
     struct {
-      uint32_t lo[kBins], hi[kBins];             // a histogram's 64-bit sums
-    } bin;
-    uint4 sorted[kList];                         // the candidates in order
+      uint64_t place[kList];                     // the candidates' places in the order
+      uint4 sorted[kList];                       // the candidates in order
+    };
   };
   uint4 list[kList];                             // candidates of the row: key, index, weight
   uint64_t before[kList];                        // mass before each, by value or by index
   uint2 own[kList];                              // this CTA's candidates: key, index
   float tops[kThreads];                          // the threads' maxima
   uint16_t scan[kScan];                          // groups whose vectors are read again
-  float2 table[64];
+  uint64_t table[1024];                          // kExp2Table, where the whole row is weighed
   uint64_t chunk[kWarps];                        // sums of the warps' runs
   uint64_t room[kWarps], room2[kWarps];
   uint64_t pick_before, pick_sum, total;
@@ -173,10 +174,9 @@ struct Scale {
   float c, c_lo;   // log2(e) / T
 };
 
-// exp((x - M) / T) in units of 2^-44, rounded, to about 2^-39.  x - M as the sum s + err (Knuth's TwoSum), times
-// log2(e) / T as the sum th + tl; 2^th by the table (k / 64 next to th, r the rest, |r| <= 2^-7) and Taylor's terms of
-// exp(z) - 1, z = r ln 2; what is below fp32's last place is carried in a second float throughout.  Below 2^-24 a weight of
-// fp32's accuracy is within half a unit.
+// exp((x - M) / T) in units of 2^-44.  x - M as the sum s + err (Knuth's TwoSum), times log2(e) / T as the sum hi + lo;
+// 2^hi+lo by the table (k / 1024 next to hi, r the rest, |r| <= 2^-11) and Taylor's first terms of 2^r - 1 in fp32, which
+// are off by 2^-35 of the weight; the rest is whole numbers.
 struct Exponent {
   float hi, lo;
 };
@@ -187,59 +187,36 @@ __device__ __forceinline__ Exponent exponent(float x, const Scale& sc) {
   return {hi, fmaf(s, sc.c, -hi) + fmaf(s, sc.c_lo, err * sc.c)};
 }
 
-constexpr float kNoWeight = -float(kSampleUnitBits + 2), kLight = -24.0f;
+constexpr float kNoWeight = -float(kSampleUnitBits + 2);
 
-__device__ __forceinline__ uint64_t light_weight(Exponent t) {
-  const float w = ex2_approx(t.hi);
-  return uint64_t(uint32_t(__float2int_rn(fmaf(w, t.lo * kLn2Hi, w) * float(kOne))));
-}
-
-__device__ __forceinline__ uint64_t full_weight(Exponent x, const float2* table) {
+// (hi above kNoWeight)
+__device__ __forceinline__ uint64_t units_of(Exponent t, const uint64_t* table) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
-  const float m = fmaf(x.hi, 64.0f, kMagic), kf = m - kMagic;
+  const float m = fmaf(t.hi, 1024.0f, kMagic);
   const int k = __float_as_int(m) - __float_as_int(kMagic);
-  const float r = fmaf(kf, -0.015625f, x.hi);
-  const float2 t = table[k & 63];
-  const float zh = r * kLn2Hi;
-  const float zl = fmaf(x.lo, kLn2Hi, fmaf(r, kLn2Lo, fmaf(r, kLn2Hi, -zh)));
-  const float p = fmaf(fmaf(fmaf(zh, 1.0f / 120.0f, 1.0f / 24.0f), zh, 1.0f / 6.0f), zh, 0.5f) * (zh * zh);
-  const float q = fmaf(zl, zh, zl) + p;
-  const float mh = t.x * zh;
-  const float ml = fmaf(t.y, zh, fmaf(t.x, q, fmaf(t.x, zh, -mh) + t.y));
-  const float sh = t.x + mh, sl = (mh - (sh - t.x)) + ml;
-  const float unit = __int_as_float(((k >> 6) + 22 + 127) << 23);  // 2^(e + 22)
-  const float yh = sh * unit, a = (yh + kMagic) - kMagic;
-  const float low = ((yh - a) + sl * unit) * 4194304.0f;
-  return uint64_t((long long)(int(a)) * 4194304 + __float2int_rn(low));
+  const float z = (fmaf(m - kMagic, -1.0f / 1024.0f, t.hi) + t.lo) * kLn2Hi;
+  const float more = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z);                   // 2^r - 1
+  const int more40 = __float2int_rn(more * 1099511627776.0f);                      // in units of 2^-40
+  const long long base = (long long)table[k & 1023];
+  const long long w = base + (((long long)int(base >> 14) * more40 + (1 << 25)) >> 26);
+  const int down = -(k >> 10);
+  return uint64_t((w + ((1ll << down) >> 1)) >> down);
 }
 
-__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const float2* table) {
+__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const uint64_t* table) {
   const Exponent t = exponent(x, sc);
-  return !(t.hi > kNoWeight) ? 0 : t.hi < kLight ? light_weight(t) : full_weight(t, table);
+  return t.hi > kNoWeight ? units_of(t, table) : 0;
 }
 
 // A vector's, the same numbers.
 template <int N>
-__device__ __forceinline__ void weights(const float (&x)[N], const Scale& sc, const float2* table, uint64_t (&w)[N]) {
-  float top = x[0];
-#pragma unroll
-  for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
-  const float t = (top - sc.M) * sc.c;  // (the largest entry's exponent)
-#pragma unroll
-  for (int e = 0; e < N; ++e) w[e] = 0;
-  if (!(t > kNoWeight)) return;
-  Exponent x2[N];
+__device__ __forceinline__ void weights(const float (&x)[N], const Scale& sc, const uint64_t* table, uint64_t (&w)[N]) {
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    x2[e] = exponent(x[e], sc);
-    if (x2[e].hi > kNoWeight) w[e] = light_weight(x2[e]);
-  }
-  if (t < kLight) return;
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const bool full = x2[e].hi >= kLight;
-    const uint64_t f = full_weight({full ? x2[e].hi : 0.0f, x2[e].lo}, table);
-    if (full) w[e] = f;
+    const Exponent t = exponent(x[e], sc);
+    const bool some = t.hi > kNoWeight;
+    const uint64_t u = units_of({some ? t.hi : 0.0f, some ? t.lo : 0.0f}, table);
+    w[e] = some ? u : 0;
   }
 }
 
@@ -349,8 +326,13 @@ __device__ __forceinline__ void add_weights(Partial& s, const float (&x)[N], flo
 
 // ------------------------------------------------------------------ candidates
 
-// The n-th largest of sh.tops (1 <= n <= kThreads) and the largest, by a warp: the longest beginning of a key that n of
-// the keys reach, two bits a step.
+// A running sum in units, once the row's maximum is known.
+__device__ __forceinline__ uint64_t units_of_sum(const Partial& s, const Scale& sc) {
+  return s.ref > -INFINITY ? uint64_t((s.hi + s.lo) * ex2_approx(fmaf(-sc.M, sc.c, s.ref)) * float(kOne)) : 0;
+}
+
+// A bound of the n-th largest of sh.tops (1 <= n <= kThreads) from below, to sixteen bits, and the largest, by a warp: the
+// longest beginning of a key that n of the keys reach, two bits a step.
 __device__ __forceinline__ void nth_largest(const Shared& sh, int n, float& nth, float& top) {
   constexpr int kEach = kThreads / 32;
   const int lane = threadIdx.x % 32;
@@ -364,9 +346,8 @@ __device__ __forceinline__ void nth_largest(const Shared& sh, int n, float& nth,
   for (int i = 0; i < kEach; ++i) most = max(most, key[i]);
   most = __reduce_max_sync(0xffffffffu, most);
   top = value_of(most);
-  uint32_t at = 0;
-  if (n == 1) at = most;
-  for (int bit = n == 1 ? -2 : 30; bit >= 0; bit -= 2) {
+  uint32_t at = n == 1 ? most : 0;
+  for (int bit = n == 1 ? 0 : 30; bit >= 16; bit -= 2) {
     // how many reach each of the three next beginnings, 10 bits each
     const uint32_t one = at + (1u << bit), two = at + (2u << bit), three = at + (3u << bit);
     uint32_t count = 0;
@@ -376,7 +357,7 @@ __device__ __forceinline__ void nth_largest(const Shared& sh, int n, float& nth,
     count = __reduce_add_sync(0xffffffffu, count);
     at = int(count >> 20) >= n ? three : int((count >> 10) & 1023u) >= n ? two : int(count & 1023u) >= n ? one : at;
   }
-  nth = value_of(at);
+  nth = at < key_of(-INFINITY) ? -INFINITY : value_of(at);
 }
 
 // Where the thread's groups of vectors lie: vector q of the thread is first + 32 q, and in group q / per_group.
@@ -397,7 +378,7 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
   if (tid == 0) sh.n_scan = sh.n_own = 0;
   __syncthreads();
 #pragma unroll
-  for (int g = 0; g <= kGroups; ++g) {
+  for (int g = 0; g < kGroups; ++g) {
     if (sh.group[g * kThreads + tid] >= tau) {
       const int at = atomicAdd(&sh.n_scan, 1);
       if (at < kScan) sh.scan[at] = uint16_t(g * kThreads + tid);
@@ -409,44 +390,40 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
     if (tid == 0) sh.n_own = kList + 1;
     return;
   }
+  auto take = [&](const uint4& w, int v) {
+    if (!(vector_max(w, static_cast<T*>(nullptr)) >= tau)) return;
+    float x[kVec<T>];
+    unpack(w, x);
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) {
+      const int index = v * kVec<T> - r.off + e;
+      if (x[e] >= tau && index >= 0 && index < r.V) {
+        const int to = atomicAdd(&sh.n_own, 1);
+        if (to < kList) sh.own[to] = make_uint2(key_of(x[e]), uint32_t(index));
+      }
+    }
+  };
   const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;
-  // the vector that number x of all groups' is, < 0: none
+  // the (whole) vector that number x of all groups' is, < 0: none
   auto vector_at = [&](int x) {
     const int k = x / per_group, q = x - k * per_group;
     if (k >= n) return -1;
-    const int g = sh.scan[k] / kThreads, t = sh.scan[k] % kThreads, warp = t / 32, lane = t % 32;
-    const int v0 = r.run_start(r.rank, warp), v1 = r.run_end(r.rank, warp);
-    if (g == kGroups) {  // the row's ends (stream)
-      if (q == 0 && lane == 0 && v0 == 0 && w0 == 1 && v1 > 0) return 0;
-      return q == 0 && lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= v0 && w1 < v1 ? w1 : -1;
-    }
-    const int v = max(v0, w0) + lane + 32 * (g * per_group + q);
-    return v < min(v1, w1) ? v : -1;
+    const int g = sh.scan[k] / kThreads, t = sh.scan[k] % kThreads, warp = t / 32;
+    const int v = max(r.run_start(r.rank, warp), w0) + t % 32 + 32 * (g * per_group + q);
+    return v < min(r.run_end(r.rank, warp), w1) ? v : -1;
   };
-  for (int x = tid; x < n * per_group; x += 4 * kThreads) {
-    int v[4];
-    uint4 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = vector_at(x + i * kThreads);
-      if (v[i] >= 0) w[i] = load_vector(r, v[i]);
-    }
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const uint4 ww = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
-      const int vv = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
-      if (vv < 0 || !(vector_max(ww, static_cast<T*>(nullptr)) >= tau)) continue;
-      float y[kVec<T>];
-      unpack(ww, y);
-#pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) {
-        const int index = vv * kVec<T> - r.off + e;
-        if (y[e] >= tau && index >= 0 && index < r.V) {
-          const int to = atomicAdd(&sh.n_own, 1);
-          if (to < kList) sh.own[to] = make_uint2(key_of(y[e]), uint32_t(index));
-        }
-      }
-    }
+  const uint4* p = reinterpret_cast<const uint4*>(r.base);
+  for (int x = tid; x < n * per_group; x += 2 * kThreads) {
+    const int a = vector_at(x), b = vector_at(x + kThreads);
+    const uint4 none = make_uint4(0, 0, 0, 0), u = a >= 0 ? __ldg(p + a) : none, v = b >= 0 ? __ldg(p + b) : none;
+    if (a >= 0) take(u, a);
+    if (b >= 0) take(v, b);
+  }
+  // the row's ends (as in stream)
+  if (sh.group[kGroups * kThreads + tid] >= tau) {
+    const int lane = tid % 32;
+    if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) take(edge_vector(r, 0), 0);
+    if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) take(edge_vector(r, w1), w1);
   }
 }
 
@@ -474,7 +451,7 @@ __device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, boo
     if (i < n) {
       const uint64_t e = ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.own + (i - start)), c);
       const uint32_t key = uint32_t(e), index = uint32_t(e >> 32);
-      const uint64_t w = weigh ? weight(value_of(key), sc, sh.table) : kOne;
+      const uint64_t w = weigh ? weight(value_of(key), sc, kExp2Table) : kOne;
       sh.list[i] = make_uint4(key, index, uint32_t(w), uint32_t(w >> 32));
     }
   }
@@ -496,84 +473,30 @@ __device__ __forceinline__ uint64_t part_of(uint64_t part, uint64_t mass) {
   return __umul64hi(part, mass) + (part * mass != 0 ? 1 : 0);
 }
 
-// A warp sorts its 32 R numbers, the largest first, element lane * R + i in x[i]: a bitonic network.
-template <int R>
-__device__ __forceinline__ void sort_down(uint64_t (&x)[R]) {
-  const int lane = threadIdx.x % 32;
-#pragma unroll
-  for (int k = 2; k <= 32 * R; k *= 2) {
-#pragma unroll
-    for (int j = k / 2; j > 0; j /= 2) {
-      if (j >= R) {
-        const int far = j / R;
-        // (of the pair the lower place keeps the larger where its block of k goes down)
-        const bool larger = ((lane & far) == 0) == ((lane * R & k) == 0);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const uint64_t y = __shfl_xor_sync(0xffffffffu, x[i], far);
-          x[i] = (x[i] > y) == larger ? x[i] : y;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if ((i & j) != 0) continue;
-          const bool down = ((lane * R + i) & k) == 0;
-          const uint64_t a = x[i], b = x[i | j];
-          const bool swap = (a < b) == down;
-          x[i] = swap ? b : a;
-          x[i | j] = swap ? a : b;
-        }
-      }
-    }
+// The candidates in order, to sh.sorted, and the mass before each, to sh.before: a candidate's rank is the number of those
+// before it, a group of threads counts for one where there are few.  (A warp's bitonic network took 1.6 us at 100
+// candidates, its shuffles one behind the other.)
+__device__ __noinline__ void sort_list(Shared& sh, int n) {
+  const int tid = threadIdx.x;
+  for (int e = tid; e < n; e += kThreads) sh.place[e] = (uint64_t(sh.list[e].x) << 32) | ~sh.list[e].y;
+  __syncthreads();
+  int g = 1;
+  while (g < 32 && 2 * g * n <= kThreads) g *= 2;
+  for (int e0 = 0; e0 < n; e0 += kThreads / g) {
+    const int e = e0 + tid / g;
+    const uint64_t mine = sh.place[min(e, n - 1)];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = tid % g; j < n; j += g) rank += sh.place[j] > mine;
+    for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (tid % g == 0 && e < n) sh.sorted[rank] = sh.list[e];
   }
-}
-
-template <int R>
-__device__ __noinline__ void sort_warp(Shared& sh, int n) {
-  const int lane = threadIdx.x % 32;
-  // key, index turned round, place in the list: 32, 19 and 9 bits
-  static_assert(kSampleMaxVocab == 1 << 19 && kList == 1 << 9);
-  uint64_t x[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int e = lane * R + i;
-    x[i] = 0;
-    if (e < n) {
-      const uint4 y = sh.list[e];
-      x[i] = (uint64_t(y.x) << 32) | (uint64_t(uint32_t(kSampleMaxVocab - 1) - y.y) << 9) | uint32_t(e);
-    }
-  }
-  sort_down<R>(x);
-  uint64_t sum = 0;
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (lane * R + i < n) sum += weight_in(sh.list[x[i] & (kList - 1)]);
-  uint64_t before = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const uint64_t y = shfl_up_u64(before, d);
-    if (lane >= d) before += y;
-  }
-  before -= sum;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int e = lane * R + i;
-    if (e < n) {
-      const uint4 y = sh.list[x[i] & (kList - 1)];
-      sh.sorted[e] = y;
-      sh.before[e] = before;
-      before += weight_in(y);
-    }
-  }
-}
-
-// The candidates in order, to sh.sorted, and the mass before each, to sh.before.
-__device__ __forceinline__ void sort_list(Shared& sh, int n) {
-  if (threadIdx.x < 32) {
-    if (n <= 64) sort_warp<2>(sh, n);
-    else if (n <= 128) sort_warp<4>(sh, n);
-    else sort_warp<16>(sh, n);
-  }
+  __syncthreads();
+  static_assert(kList == 2 * kThreads);
+  const uint64_t a = 2 * tid < n ? weight_in(sh.sorted[2 * tid]) : 0, b = 2 * tid + 1 < n ? weight_in(sh.sorted[2 * tid + 1]) : 0;
+  const uint64_t upto = block_scan(a + b, sh.room);
+  sh.before[2 * tid] = upto - a - b;
+  sh.before[2 * tid + 1] = upto - b;
   __syncthreads();
 }
 
@@ -653,17 +576,16 @@ __device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t 
 
 // ------------------------------------------------------------------ the row in general
 
-// Where the draw's share `at` of the warps' sums (in sh.chunk, behind a row_sync) falls: the run that passes it and the sum
-// before it, to sh.pick and sh.pick_before; the sum of all to sh.total.  at = draw / 2^64 of `total`, or of the sum where
-// total is 0.
+// Where the draw falls, draw / 2^64 of the warps' sums (in sh.chunk, behind a row_sync): the run that passes it and the sum
+// before it, to sh.pick and sh.pick_before; the sum of all to sh.total.
 template <class T>
-__device__ __forceinline__ uint64_t find_run(Shared& sh, const Row<T>& r, uint64_t draw, uint64_t total) {
+__device__ __forceinline__ uint64_t find_run(Shared& sh, const Row<T>& r, uint64_t draw) {
   const int tid = threadIdx.x, runs = r.ctas * kWarps;
   const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % kWarps, tid / kWarps) : 0;
   const uint64_t incl = block_scan(mine, sh.room);
   if (tid == kThreads - 1) sh.total = incl;
   __syncthreads();
-  const uint64_t at = __umul64hi(draw, total > 0 ? total : sh.total);
+  const uint64_t at = __umul64hi(draw, sh.total);
   if (tid < runs && incl > at && incl - mine <= at) {
     sh.pick = tid;
     sh.pick_before = incl - mine;
@@ -763,20 +685,22 @@ __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key,
 }
 
 // The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
-// target_of(all): the last is the first with target <= the inclusive sum, which goes to `kept`.  A histogram by value
-// over the weights' range, then by key within the bin, each level a sweep, until what is left fits the list.
+// target_of(all): the last is the first with target <= the inclusive sum.  A histogram by value over the weights' range,
+// then by key within the bin, each level a sweep, until what is left fits the list.  The bins are added up a part by each
+// CTA.
 template <bool MASS, class T, class G>
-__device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of,
-                                   uint64_t& kept) {
-  const int tid = threadIdx.x;
+__device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of) {
+  const int tid = threadIdx.x, lane = tid % 32;
   // bins of equal width down to where weights vanish; the last takes the rest
   const float width = float(kBins - 1) / float(kSampleUnitBits + 3) * sc.c;
   auto bin_of = [&](float x) { return min(int((sc.M - x) * width), kBins - 1); };
   auto add = [&](int bin, uint64_t m) {
-    const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bin.lo[bin], low);
+    const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bins[bin].x, low);
     const uint32_t high = uint32_t(m >> 32) + (old + low < old ? 1u : 0u);
-    if (high) atomicAdd(&sh.bin.hi[bin], high);
+    if (high) atomicAdd(&sh.bins[bin].y, high);
   };
+  const bool all = within.key == 0;
+  const int part = (kBins + r.ctas - 1) / r.ctas, part0 = min(r.rank * part, kBins), part1 = min(part0 + part, kBins);
   uint32_t lo = 1, hi = key_of(sc.M);
   int shift = 32, first_bin = 0;
   uint64_t above = 0, target = 0, in_bin = 0;
@@ -786,7 +710,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       shift = 0;
       while ((span >> shift) >= uint32_t(kBins)) ++shift;
     }
-    for (int i = tid; i < kBins; i += kThreads) sh.bin.lo[i] = sh.bin.hi[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = make_uint2(0, 0);
     if (tid == 0) sh.n_own = 0;
     __syncthreads();
     if (level == 0) {
@@ -794,12 +718,15 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
         float x[kVec<T>];
         unpack(w, x);
         uint64_t m[kVec<T>];
-        if constexpr (MASS) weights(x, sc, sh.table, m);
+        if constexpr (MASS) {
+          if (!((vector_max(w, static_cast<T*>(nullptr)) - sc.M) * sc.c > kNoWeight)) return;
+          weights(x, sc, sh.table, m);
+        }
 #pragma unroll
         for (int e = 0; e < kVec<T>; ++e) {
           const int i = v * kVec<T> - r.off + e;
           if constexpr (!MASS) m[e] = i >= 0 && i < r.V;
-          if (m[e] != 0 && within.keeps(key_of(x[e]), i)) add(bin_of(x[e]), m[e]);
+          if (m[e] != 0 && (all || within.keeps(key_of(x[e]), i))) add(bin_of(x[e]), m[e]);
         }
       });
     } else {
@@ -808,11 +735,13 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
         if (vector_max(w, static_cast<T*>(nullptr)) < least) return;
         float x[kVec<T>];
         unpack(w, x);
-#pragma unroll 1
+        const float most = value_of(hi);
+#pragma unroll
         for (int e = 0; e < kVec<T>; ++e) {
+          if (x[e] < least || x[e] > most || bin_of(x[e]) != first_bin) continue;
           const int i = v * kVec<T> - r.off + e;
           const uint32_t key = key_of(x[e]);
-          if (key < lo || key > hi || bin_of(x[e]) != first_bin || i < 0 || i >= r.V || !within.keeps(key, i)) continue;
+          if (i < 0 || i >= r.V || !within.keeps(key, i)) continue;
           const uint64_t m = MASS ? weight(x[e], sc, sh.table) : 1;
           if (m == 0) continue;
           add(int((hi - key) >> shift), m);
@@ -827,62 +756,75 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       sort_list(sh, n);
       for (int e = tid; e < n; e += kThreads) {
         const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(e));
-        if (b < target && target <= b + m) {
-          sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
-          sh.total = b + m;
-        }
+        if (b < target && target <= b + m) sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
       }
       row_sync();
-      kept = sh.total;
       return sh.cut;
     }
-    uint64_t own[kOwnBins], sum = 0;
+    // this CTA's part of the bins, of all CTAs, in place (nobody else reads them here), and their sum
+    uint64_t sum = 0;
+    for (int i = part0 + tid; i < part1; i += kThreads) {
+      uint64_t own = 0;
+      for (int c = 0; c < r.ctas; ++c) own += ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.bins + i), c);
+      *reinterpret_cast<uint64_t*>(sh.bins + i) = own;
+      sum += own;
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) sh.chunk[tid / 32] = sum;
+    if (tid == 0) sh.pick = -1;
+    row_sync();
+    uint64_t mine = 0;
+    if (lane < r.ctas)
+      for (int i = 0; i < kWarps; ++i) mine += ld_peer_u64(sh.chunk + i, lane);
+    uint64_t upto = mine;
 #pragma unroll
-    for (int i = 0; i < kOwnBins; ++i) own[i] = 0;
-    for (int c = 0; c < r.ctas; ++c)
-#pragma unroll
-      for (int i = 0; i < kOwnBins; ++i)
-        own[i] += (uint64_t(ld_peer_u32(sh.bin.hi + tid * kOwnBins + i, c)) << 32) +
-                  ld_peer_u32(sh.bin.lo + tid * kOwnBins + i, c);
-#pragma unroll
-    for (int i = 0; i < kOwnBins; ++i) sum += own[i];
-    const uint64_t incl = block_scan(sum, sh.room);
-    if (tid == kThreads - 1) sh.total = incl;
-    __syncthreads();
-    if (level == 0) target = target_of(sh.total);
-    uint64_t b = above + incl - sum;
-    if (b < target && target <= above + incl) {
-#pragma unroll
-      for (int i = 0; i < kOwnBins; ++i) {
-        if (b < target && target <= b + own[i]) {
-          sh.pick = tid * kOwnBins + i;
-          sh.pick_before = b;
-          sh.pick_sum = own[i];
+    for (int d = 1; d < kMaxCtas; d *= 2) {
+      const uint64_t y = shfl_up_u64(upto, d);
+      if (lane >= d) upto += y;
+    }
+    if (level == 0) target = target_of(__shfl_sync(0xffffffffu, upto, kMaxCtas - 1));
+    upto += above;
+    const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && upto - mine < target && target <= upto);
+    const int owner = __ffs(holds) - 1;
+    const uint64_t start = __shfl_sync(0xffffffffu, upto - mine, owner);
+    if (r.rank == owner) {
+      // the bin, each thread looking through a few
+      const int few = (part + kThreads - 1) / kThreads, i0 = min(part0 + tid * few, part1), i1 = min(i0 + few, part1);
+      uint64_t s = 0;
+      for (int i = i0; i < i1; ++i) s += *reinterpret_cast<const uint64_t*>(sh.bins + i);
+      uint64_t b = start + block_scan(s, sh.room) - s;
+      if (b < target && target <= b + s) {
+        for (int i = i0; i < i1; ++i) {
+          const uint64_t own = *reinterpret_cast<const uint64_t*>(sh.bins + i);
+          if (b < target && target <= b + own) {
+            sh.pick = i;
+            sh.pick_before = b;
+            sh.pick_sum = own;
+          }
+          b += own;
         }
-        b += own[i];
       }
     }
-    row_sync();  // (and the peers have read the bins)
-    const int bin = sh.pick;
-    above = sh.pick_before;
-    in_bin = sh.pick_sum;
+    row_sync();
+    const int bin = int(ld_peer_u32(&sh.pick, owner));
+    above = ld_peer_u64(&sh.pick_before, owner);
+    in_bin = ld_peer_u64(&sh.pick_sum, owner);
     if (level == 0) {
       // keys that the bin's values may have (its own test stays)
       first_bin = bin;
       const float from = sc.M - float(bin) / width, to = sc.M - float(bin + 1) / width;
       const float slack = (fabsf(sc.M) + fabsf(to)) * 1e-5f;
       hi = min(hi, key_of(from + slack));
-      lo = bin == kBins - 1 || !(to - slack > -INFINITY) ? 1u : key_of(to - slack);
+      lo = bin == kBins - 1 || !(to - slack > -INFINITY) ? key_of(-INFINITY) : key_of(to - slack);
     } else {
       hi -= uint32_t(bin) << shift;
       lo = max(lo, hi - ((1u << shift) - 1u));
     }
-    __syncthreads();
+    row_sync();  // (all have read what the owner found)
   }
   // one value, and more entries with it than the list holds: of equal values the lowest indices
   const uint64_t each = MASS ? weight(value_of(hi), sc, sh.table) : 1;
   const uint64_t want = (target - above + each - 1) / each;
-  kept = above + want * each;
   Cut cut = {hi, INT_MAX};
   if (want < in_bin / each) cut.index = nth_equal(sh, r, hi, want);
   return cut;
@@ -913,61 +855,37 @@ struct Kept {
   __device__ __forceinline__ bool operator()(float x, int i) const { return x > value || (x == value && i <= cut.index); }
 };
 
-// A vector's fast weights of kept entries onto a sum whose reference is the row's maximum.
+// A draw from the whole row by the warps' fast sums (sh.chunk, behind a row_sync).  A token < 0: too near a border to say.
 template <class T>
-__device__ __forceinline__ void add_kept(Partial& s, const uint4& w, int v, const Row<T>& r, const Scale& sc, const Kept& keep) {
-  const float ref = -sc.M * sc.c;
-  float x[kVec<T>], sum = 0.0f;
-  unpack(w, x);
-#pragma unroll
-  for (int e = 0; e < kVec<T>; ++e)
-    if (keep(x[e], v * kVec<T> - r.off + e)) sum += ex2_approx(fmaf(x[e], sc.c, ref));
-  const float all = s.hi + sum, bb = all - s.hi;
-  s.lo += (s.hi - (all - bb)) + (sum - bb);
-  s.hi = all;
-}
-
-__device__ __forceinline__ uint64_t units_of(const Partial& s, const Scale& sc) {
-  // (what the rounding of the reference leaves the maximum itself has too)
-  return uint64_t((s.hi + s.lo) * ex2_approx(-fmaf(sc.M, sc.c, -sc.M * sc.c)) * float(kOne));
-}
-
-// A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync); total: the kept mass, 0: that
-// of the sums.  A token < 0: too near a border to say.
-template <class T>
-__device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw,
-                                        uint64_t total) {
-  const uint64_t at = find_run(sh, r, draw, total);
+__device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale& sc, uint64_t draw) {
+  const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
-  d.total = total > 0 ? total : sh.total;
-  // (the sums before the run, those within it, and where the total is theirs the draw's place)
+  d.total = sh.total;
+  // (the sums before the run, those within it, and by the total the draw's place are off)
   d.token = find_entry(
       sh, r, at, 3 * ((sh.total >> kFastBits) + 1),
       [&](int v0, int v1) {
         Partial s;
-        few(r, v0, v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
-        return warp_sum(units_of(s, sc));
+        few(r, v0, v1, [&](const uint4& w, int) {
+          float x[kVec<T>];
+          unpack(w, x);
+          add_weights(s, x, vector_max(w, static_cast<T*>(nullptr)), sc.c);
+        });
+        return warp_sum(units_of_sum(s, sc));
       },
-      [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
-  d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, sh.table) : 0;
+      [&](float x, int) { return weight(x, sc, kExp2Table); });
+  d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, kExp2Table) : 0;
   return d;
 }
 
-// The warps' fast sums of the kept entries, to sh.chunk.
-template <class T>
-__device__ __noinline__ void fast_sums(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep) {
-  Partial s;
-  stream(r, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
-  const uint64_t w = warp_sum(units_of(s, sc));
-  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = w;
-}
-
-// The same by exact sums.
+// A draw from the kept entries by exact sums.
 template <class T>
 __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw) {
   uint64_t own = 0;
   auto add = [&](const uint4& w, int v) {
+    const float top = vector_max(w, static_cast<T*>(nullptr));
+    if (top < keep.value || !((top - sc.M) * sc.c > kNoWeight)) return;
     float x[kVec<T>];
     unpack(w, x);
     uint64_t m[kVec<T>];
@@ -980,7 +898,7 @@ __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scal
   own = warp_sum(own);
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
   row_sync();
-  const uint64_t at = find_run(sh, r, draw, 0);
+  const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
   d.total = sh.total;
@@ -1007,7 +925,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
   r.rank = int(cluster_rank());
   const long long row = blockIdx.x / r.ctas;
   const int b = int(row / a.n), n = int(row - (long long)b * a.n);
-  if (tid < 64) sh.table[tid] = kExp2Table[tid];
   if (tid == 0) {
     sh.found = sh.pick = 0;
     sh.pick_before = sh.pick_sum = sh.total = 0;
@@ -1122,8 +1039,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
     least = greedy ? 0 : uint64_t(ceilf(min_p * float(kOne)));
     const uint64_t draw = greedy ? 0 : uint64_t(u * 18446744073709551616.0f);
     if (sums) {
-      const float own = !(part.ref > -INFINITY) ? 0.0f : (part.hi + part.lo) * ex2_approx(fmaf(-sc.M, sc.c, part.ref));
-      const uint64_t w = warp_sum(uint64_t(own * float(kOne)));
+      const uint64_t w = warp_sum(units_of_sum(part, sc));
       if (lane == 0) sh.chunk[warp] = w;
     }
     // Where nothing depends on the mass below min-p's border, candidates end there (a little below it, for the roundings).
@@ -1150,34 +1066,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
       row_sync();  // (the peers have read the candidates)
     } else if (trusted && sums && !nucleus) {
       row_sync();
-      d = draw_fast(sh, r, sc, Kept{cut, -INFINITY}, draw, 0);
+      d = draw_fast(sh, r, sc, draw);
       settled = d.token >= 0;
     }
     if (!settled) {
-      uint64_t kept = 0;
-      if (k > 0) cut = search<false>(sh, r, sc, cut, [&](uint64_t) { return uint64_t(k); }, kept);
-      kept = 0;
+      for (int i = tid; i < 1024; i += kThreads) sh.table[i] = kExp2Table[i];
+      __syncthreads();
+      if (k > 0) cut = search<false>(sh, r, sc, cut, [&](uint64_t) { return uint64_t(k); });
       if (nucleus) {
         const Cut first_k = cut;
         const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
-        cut = search<true>(sh, r, sc, first_k, [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); }, kept);
+        cut = search<true>(sh, r, sc, first_k, [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); });
         if (cut.key == first_k.key) cut.index = min(cut.index, first_k.index);
       }
       if (least > 0) {
         const uint32_t key = least_key(sh, sc, least);
-        if (key > cut.key) {
-          cut = {key, INT_MAX};
-          kept = 0;
-        }
+        if (key > cut.key) cut = {key, INT_MAX};
       }
-      const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
-      d.token = -1;
-      if (fabsf(sc.M * sc.c) < kFastRange && !(sums && !nucleus && trusted)) {
-        fast_sums(sh, r, sc, keep);
-        row_sync();
-        d = draw_fast(sh, r, sc, keep, draw, kept);
-      }
-      if (d.token < 0) d = draw_exact(sh, r, sc, keep, draw);
+      d = draw_exact(sh, r, sc, Kept{cut, cut.key == 0 ? -INFINITY : value_of(cut.key)}, draw);
     }
   }
   if (r.rank == 0 && tid == 0) {

@@ -6,8 +6,8 @@ import numpy as np
 
 def sample64(x, u, T, k, p, least):
     """(token, log-probability, distribution, margin) of one row x (float64 values of its stored type): from the
-    definition, sorted.  `margin`: how far, relative to the largest weight, the nearest decision was from its border (the
-    nucleus' border against p, the draw's against u)."""
+    definition, sorted.  `margin`: how far, relative to the mass it is decided within, the nearest decision was from its
+    border (the nucleus' border against p, the draw's against u)."""
     V = len(x)
     order = np.lexsort((np.arange(V), -x))          # value descending, index ascending
     dist = np.zeros(V)
@@ -24,7 +24,7 @@ def sample64(x, u, T, k, p, least):
             np.concatenate([[0.0], np.cumsum(w.astype(np.longdouble))[:-1]]).astype(float)
         target = p * math.fsum(w)
         keep &= before < target
-        margin = min(margin, np.abs(before[1:] - target).min(initial=math.inf))
+        margin = min(margin, np.abs(before[1:] - target).min(initial=math.inf) / math.fsum(w))
     keep &= w >= least
     keep[0] = True
     kept = order[keep]
@@ -34,14 +34,15 @@ def sample64(x, u, T, k, p, least):
     upto = np.cumsum(mass.astype(np.longdouble)).astype(float)
     token = int(np.searchsorted(upto, u * total, side="right"))
     at = np.flatnonzero(mass)
-    margin = min(margin, np.abs(upto[at] - u * total)[:-1].min(initial=math.inf))
+    margin = min(margin, np.abs(upto[at] - u * total)[:-1].min(initial=math.inf) / total)
     token = min(token, int(at[-1]))
     return token, math.log(mass[token] / total), mass / total, margin
 
 
-# Borders nearer than this (of the largest weight, 1) are not judged: weights come to about 2^-39 and are summed in
-# units of 2^-44, so 2^17 of them are off by 2^-30 at most, by 2^-37 as errors of either sign add up.
-BORDER = 2.0 ** -30
+# Borders nearer than this are not judged: a weight is off by 2^-34 of itself at most (its fp32 part, 2^r - 1 <= 2^-11.5, by
+# three roundings; its exponent by 2^-35) and by half a unit of 2^-45 of the largest, of which there are 2^18 at most in
+# these tests; both sides of a comparison are sums of such.
+BORDER = 2.0 ** -32 + 2.0 ** -26 * 2.0 ** -8
 
 
 # The kept mass, where no border is near, may be the sum of fp32 weights 2^t, t = fma(x, c, -ref): with D = (max - x) c (in
