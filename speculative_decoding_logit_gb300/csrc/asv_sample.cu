@@ -42,6 +42,7 @@ constexpr int kScan = 1024;              // groups that are read again, at most
 constexpr int kBins = 2048;
 constexpr int kMaxCtas = 8;
 constexpr int kAhead = 4;                // vectors a lane has in flight
+constexpr int kFirstAhead = 8;           // the same, when the row streams from HBM
 constexpr uint64_t kOne = uint64_t(1) << kSampleUnitBits;  // the largest weight
 
 template <class T>
@@ -169,56 +170,64 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // ------------------------------------------------------------------ weights
 
+// How weights follow from values: exponents are x c in log2 units, of which k_top / 1024 + rest is the maximum's; where
+// that is beyond +-4000 (`far`), (x - M) c.
 struct Scale {
   float M;         // the row's maximum
   float c, c_lo;   // log2(e) / T
+  float rest;
+  int k_top;
+  bool far;
 };
 
-// exp((x - M) / T) in units of 2^-44.  x - M as the sum s + err (Knuth's TwoSum), times log2(e) / T as the sum hi + lo;
-// 2^hi+lo by the table (k / 1024 next to hi, r the rest, |r| <= 2^-11) and Taylor's first terms of 2^r - 1 in fp32, which
-// are off by 2^-35 of the weight; the rest is whole numbers.
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
+constexpr int kNoWeight = -(kSampleUnitBits + 2) * 1024;
+
 struct Exponent {
   float hi, lo;
 };
 
 __device__ __forceinline__ Exponent exponent(float x, const Scale& sc) {
+  if (!sc.far) {
+    const float hi = x * sc.c;
+    return {hi, fmaf(x, sc.c_lo, -sc.rest) + fmaf(x, sc.c, -hi)};
+  }
+  // x - M as a sum of two floats (Knuth's TwoSum)
   const float s = x - sc.M, bb = s - x, err = (x - (s - bb)) + (-sc.M - bb);
   const float hi = s * sc.c;
   return {hi, fmaf(s, sc.c, -hi) + fmaf(s, sc.c_lo, err * sc.c)};
 }
 
-constexpr float kNoWeight = -float(kSampleUnitBits + 2);
-
-// (hi above kNoWeight)
-__device__ __forceinline__ uint64_t units_of(Exponent t, const uint64_t* table) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
-  const float m = fmaf(t.hi, 1024.0f, kMagic);
-  const int k = __float_as_int(m) - __float_as_int(kMagic);
+// exp((x - M) / T) in units of 2^-44: 2^(hi + lo) by the table (k / 1024 next to hi, r the rest, |r| <= 2^-11) and Taylor's
+// first terms of 2^r - 1 in fp32, which are off by 2^-34 of the weight; what follows is whole numbers.
+__device__ __forceinline__ uint64_t units_of(float x, const Scale& sc, const uint64_t* table) {
+  const Exponent t = exponent(x, sc);
+  const float m = fmaf(fmaxf(t.hi, -4090.0f), 1024.0f, kMagic);
+  const int k = __float_as_int(m) - __float_as_int(kMagic) - sc.k_top;
   const float z = (fmaf(m - kMagic, -1.0f / 1024.0f, t.hi) + t.lo) * kLn2Hi;
   const float more = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z);                   // 2^r - 1
   const int more40 = __float2int_rn(more * 1099511627776.0f);                      // in units of 2^-40
   const long long base = (long long)table[k & 1023];
   const long long w = base + (((long long)int(base >> 14) * more40 + (1 << 25)) >> 26);
-  const int down = -(k >> 10);
-  return uint64_t((w + ((1ll << down) >> 1)) >> down);
+  const int down = -(k >> 10) & 63;
+  return k > kNoWeight ? uint64_t((w + ((1ll << down) >> 1)) >> down) : 0;
 }
 
-__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const uint64_t* table) {
-  const Exponent t = exponent(x, sc);
-  return t.hi > kNoWeight ? units_of(t, table) : 0;
-}
-
-// A vector's, the same numbers.
-template <int N>
-__device__ __forceinline__ void weights(const float (&x)[N], const Scale& sc, const uint64_t* table, uint64_t (&w)[N]) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const Exponent t = exponent(x[e], sc);
-    const bool some = t.hi > kNoWeight;
-    const uint64_t u = units_of({some ? t.hi : 0.0f, some ? t.lo : 0.0f}, table);
-    w[e] = some ? u : 0;
+__device__ __forceinline__ Scale scale_of(float M, float c, float c_lo) {
+  Scale sc = {M, c, c_lo, 0.0f, 0, !(fabsf(M * c) < 4000.0f)};
+  if (!sc.far) {
+    const Exponent t = exponent(M, sc);
+    const float m = fmaf(t.hi, 1024.0f, kMagic);
+    sc.k_top = __float_as_int(m) - __float_as_int(kMagic);
+    sc.rest = fmaf(m - kMagic, -1.0f / 1024.0f, t.hi) + t.lo;
   }
+  return sc;
 }
+
+__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const uint64_t* table) { return units_of(x, sc, table); }
+
+// Whether a vector whose largest entry is x has weights that count.
+__device__ __forceinline__ bool weighs(float x, const Scale& sc) { return (x - sc.M) * sc.c > -float(kSampleUnitBits + 3); }
 
 // ------------------------------------------------------------------ sums over the row
 
@@ -366,7 +375,7 @@ struct Groups {
   int per_group;
   __device__ __forceinline__ explicit Groups(const Row<T>& r) {
     const int each = (r.per_warp + 31) / 32;
-    per_group = ((each + kGroups - 1) / kGroups + kAhead - 1) / kAhead * kAhead;
+    per_group = ((each + kGroups - 1) / kGroups + kFirstAhead - 1) / kFirstAhead * kFirstAhead;
   }
 };
 
@@ -685,15 +694,18 @@ __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key,
 }
 
 // The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
-// target_of(all): the last is the first with target <= the inclusive sum.  A histogram by value over the weights' range,
-// then by key within the bin, each level a sweep, until what is left fits the list.  The bins are added up a part by each
-// CTA.
+// target_of(all): the last is the first with target <= the inclusive sum.  A histogram by value over the larger weights'
+// range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
+// on.  The bins are added up a part by each CTA.
 template <bool MASS, class T, class G>
 __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of) {
   const int tid = threadIdx.x, lane = tid % 32;
-  // bins of equal width down to where weights vanish; the last takes the rest
-  const float width = float(kBins - 1) / float(kSampleUnitBits + 3) * sc.c;
-  auto bin_of = [&](float x) { return min(int((sc.M - x) * width), kBins - 1); };
+  // bins of equal width down to weights of 2^-24, the last takes the rest (7 % of a weight's width each: of 152 thousand
+  // flat entries 250 at most fall into one)
+  const float width = float(kBins - 1) / 24.0f * sc.c;
+  auto bin_of = [&](float x) {
+    return __float_as_int(fminf((sc.M - x) * width, float(kBins - 1)) + kMagic) - __float_as_int(kMagic);
+  };
   auto add = [&](int bin, uint64_t m) {
     const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bins[bin].x, low);
     const uint32_t high = uint32_t(m >> 32) + (old + low < old ? 1u : 0u);
@@ -710,8 +722,42 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       shift = 0;
       while ((span >> shift) >= uint32_t(kBins)) ++shift;
     }
+    // what the entries of the bracket do
+    auto each_entry = [&](auto f) {
+      const float least = value_of(lo), most = value_of(hi);
+      stream(r, [&](const uint4& w, int v) {
+        if (vector_max(w, static_cast<T*>(nullptr)) < least) return;
+        float x[kVec<T>];
+        unpack(w, x);
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) {
+          if (x[e] < least || x[e] > most || bin_of(x[e]) != first_bin) continue;
+          const int i = v * kVec<T> - r.off + e;
+          const uint32_t key = key_of(x[e]);
+          if (i >= 0 && i < r.V && within.keeps(key, i)) f(x[e], key, i);
+        }
+      });
+    };
+    if (level > 0) {
+      if (tid == 0) sh.n_own = 0;
+      __syncthreads();
+      each_entry([&](float, uint32_t key, int i) {
+        const int to = atomicAdd(&sh.n_own, 1);
+        if (to < kList) sh.own[to] = make_uint2(key, uint32_t(i));
+      });
+      row_sync();
+      const int n = share_out(sh, sc, r.ctas, MASS);
+      if (n > 0) {
+        sort_list(sh, n);
+        for (int e = tid; e < n; e += kThreads) {
+          const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(e));
+          if (b < target && target <= b + m) sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
+        }
+        row_sync();
+        return sh.cut;
+      }
+    }
     for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = make_uint2(0, 0);
-    if (tid == 0) sh.n_own = 0;
     __syncthreads();
     if (level == 0) {
       stream(r, [&](const uint4& w, int v) {
@@ -719,8 +765,9 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
         unpack(w, x);
         uint64_t m[kVec<T>];
         if constexpr (MASS) {
-          if (!((vector_max(w, static_cast<T*>(nullptr)) - sc.M) * sc.c > kNoWeight)) return;
-          weights(x, sc, sh.table, m);
+          if (!weighs(vector_max(w, static_cast<T*>(nullptr)), sc)) return;
+#pragma unroll
+          for (int e = 0; e < kVec<T>; ++e) m[e] = units_of(x[e], sc, sh.table);
         }
 #pragma unroll
         for (int e = 0; e < kVec<T>; ++e) {
@@ -730,37 +777,12 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
         }
       });
     } else {
-      const float least = value_of(lo);
-      stream(r, [&](const uint4& w, int v) {
-        if (vector_max(w, static_cast<T*>(nullptr)) < least) return;
-        float x[kVec<T>];
-        unpack(w, x);
-        const float most = value_of(hi);
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) {
-          if (x[e] < least || x[e] > most || bin_of(x[e]) != first_bin) continue;
-          const int i = v * kVec<T> - r.off + e;
-          const uint32_t key = key_of(x[e]);
-          if (i < 0 || i >= r.V || !within.keeps(key, i)) continue;
-          const uint64_t m = MASS ? weight(x[e], sc, sh.table) : 1;
-          if (m == 0) continue;
-          add(int((hi - key) >> shift), m);
-          const int to = atomicAdd(&sh.n_own, 1);
-          if (to < kList) sh.own[to] = make_uint2(key, uint32_t(i));
-        }
+      each_entry([&](float x, uint32_t key, int) {
+        const uint64_t m = MASS ? weight(x, sc, sh.table) : 1;
+        if (m != 0) add(int((hi - key) >> shift), m);
       });
     }
     row_sync();
-    const int n = level > 0 ? share_out(sh, sc, r.ctas, MASS) : -1;
-    if (n > 0) {
-      sort_list(sh, n);
-      for (int e = tid; e < n; e += kThreads) {
-        const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(e));
-        if (b < target && target <= b + m) sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
-      }
-      row_sync();
-      return sh.cut;
-    }
     // this CTA's part of the bins, of all CTAs, in place (nobody else reads them here), and their sum
     uint64_t sum = 0;
     for (int i = part0 + tid; i < part1; i += kThreads) {
@@ -812,7 +834,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     if (level == 0) {
       // keys that the bin's values may have (its own test stays)
       first_bin = bin;
-      const float from = sc.M - float(bin) / width, to = sc.M - float(bin + 1) / width;
+      const float from = sc.M - (float(bin) - 0.5f) / width, to = sc.M - (float(bin) + 0.5f) / width;
       const float slack = (fabsf(sc.M) + fabsf(to)) * 1e-5f;
       hi = min(hi, key_of(from + slack));
       lo = bin == kBins - 1 || !(to - slack > -INFINITY) ? key_of(-INFINITY) : key_of(to - slack);
@@ -862,9 +884,13 @@ __device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale
   __syncthreads();
   Drawn d;
   d.total = sh.total;
-  // (the sums before the run, those within it, and by the total the draw's place are off)
+  // Of sums b before a border and a behind it the draw u compares (1 - u) b with u a.  Next to the border both are u (1 - u)
+  // of the mass, 1/4 at most, and each is off by 2^-18 of itself; the run's own sum counts once as the rows streamed and
+  // once as it is taken apart here, each off by 2^-18 too.
+  const int run = sh.pick;
+  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % kWarps, run / kWarps)) >> kFastBits) + 64;
   d.token = find_entry(
-      sh, r, at, 3 * ((sh.total >> kFastBits) + 1),
+      sh, r, at, margin,
       [&](int v0, int v1) {
         Partial s;
         few(r, v0, v1, [&](const uint4& w, int) {
@@ -885,14 +911,14 @@ __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scal
   uint64_t own = 0;
   auto add = [&](const uint4& w, int v) {
     const float top = vector_max(w, static_cast<T*>(nullptr));
-    if (top < keep.value || !((top - sc.M) * sc.c > kNoWeight)) return;
+    if (top < keep.value || !weighs(top, sc)) return;
     float x[kVec<T>];
     unpack(w, x);
-    uint64_t m[kVec<T>];
-    weights(x, sc, sh.table, m);
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e)
-      if (keep(x[e], v * kVec<T> - r.off + e)) own += m[e];
+    for (int e = 0; e < kVec<T>; ++e) {
+      const uint64_t u = units_of(x[e], sc, sh.table);
+      own += keep(x[e], v * kVec<T> - r.off + e) ? u : 0;
+    }
   };
   stream(r, add);
   own = warp_sum(own);
@@ -952,9 +978,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
   r.per_warp = (r.per_cta + kWarps - 1) / kWarps;
   r.v0 = r.run_start(r.rank, warp);
   r.v1 = r.run_end(r.rank, warp);
-  Scale sc;
-  sc.c = greedy || !params_ok ? 1.0f : kLog2eHi / T_;
-  sc.c_lo = greedy || !params_ok ? 0.0f : (fmaf(-sc.c, T_, kLog2eHi) + kLog2eLo) / T_;
+  const float c = greedy || !params_ok ? 1.0f : kLog2eHi / T_;
+  const float c_lo = greedy || !params_ok ? 0.0f : (fmaf(-c, T_, kLog2eHi) + kLog2eLo) / T_;
 
   // ---- the row streams once: the threads' maxima, and the mass where it is needed
   const bool nucleus = !greedy && top_p < 1.0f;
@@ -970,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
       if (sums) {
         float x[kVec<T>];
         unpack(w, x);
-        add_weights(part, x, m, sc.c);
+        add_weights(part, x, m, c);
       }
       return m;
     };
@@ -984,16 +1009,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
     const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>, end = min(r.v1, w1);  // whole vectors
     const uint4* p = reinterpret_cast<const uint4*>(r.base);
     int v = max(r.v0, w0) + lane;
-    for (; v + 32 * (kAhead - 1) < end; v += 32 * kAhead) {
-      uint4 w[kAhead];
+    for (; v + 32 * (kFirstAhead - 1) < end; v += 32 * kFirstAhead) {
+      uint4 w[kFirstAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) w[i] = __ldg(p + v + 32 * i);
+      for (int i = 0; i < kFirstAhead; ++i) w[i] = __ldg(p + v + 32 * i);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) most = max_nan(most, one(w[i]));
-      left -= kAhead;
+      for (int i = 0; i < kFirstAhead; ++i) most = max_nan(most, one(w[i]));
+      left -= kFirstAhead;
       if (left == 0) close();
     }
-    for (; v < end; v += 32) most = max_nan(most, one(__ldg(p + v)));
+    if (v < end) {  // (the last ones, together too)
+      uint4 w[kFirstAhead - 1];
+#pragma unroll
+      for (int i = 0; i < kFirstAhead - 1; ++i)
+        if (v + 32 * i < end) w[i] = __ldg(p + v + 32 * i);
+#pragma unroll
+      for (int i = 0; i < kFirstAhead - 1; ++i)
+        if (v + 32 * i < end) most = max_nan(most, one(w[i]));
+    }
     while (g < kGroups) close();
     // the row's ends (as in stream)
     if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) most = one(edge_vector(r, 0));
@@ -1012,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
     if (lane == 0) sh.ends = make_float4(most, nth <= kThreads ? least_top : -INFINITY, bad ? 1.0f : 0.0f, 0.0f);
   }
   row_sync();
-  float tau;
+  float tau, M;
   {
     float4 e = make_float4(-INFINITY, INFINITY, 0.0f, 0.0f);
     if (lane < r.ctas) {
@@ -1027,16 +1060,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
       e.x = fmaxf(e.x, __shfl_xor_sync(0xffffffffu, e.x, o));
       e.y = fminf(e.y, __shfl_xor_sync(0xffffffffu, e.y, o));
     }
-    sc.M = __shfl_sync(0xffffffffu, e.x, 0);
+    M = __shfl_sync(0xffffffffu, e.x, 0);
     tau = __shfl_sync(0xffffffffu, e.y, 0);
   }
-  bad = bad || sc.M == -INFINITY;
+  bad = bad || M == -INFINITY;
+  const Scale sc = scale_of(M, c, c_lo);
 
   Drawn d = {-1, 0, 0};
   Cut cut = {0u, INT_MAX};
   uint64_t least = 0;
   if (params_ok && !bad) {  // (for all CTAs of the row)
-    least = greedy ? 0 : uint64_t(ceilf(min_p * float(kOne)));
+    if (!greedy && min_p > 0.0f) {
+      const uint64_t most = weight(M, sc, kExp2Table);
+      least = min_p < 1.0f ? part_of(uint64_t(min_p * 18446744073709551616.0f), most) : most;
+    }
     const uint64_t draw = greedy ? 0 : uint64_t(u * 18446744073709551616.0f);
     if (sums) {
       const uint64_t w = warp_sum(units_of_sum(part, sc));
