@@ -6,7 +6,7 @@
 // entry.  The token is the first kept index whose cumulative mass (over kept entries, by index) passes u times the
 // kept mass; the distribution is w over the kept mass.
 //
-// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out to 2^-35 of themselves
+// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out to 2^-30 of themselves
 // and summed in units of 2^-44 in 64-bit integers, which makes their sums exact in any order.  That costs 40 operations an
 // entry, so few are weighed so:
 //   - The row streams once, for the maxima of the threads' vectors and, where the whole row's mass counts, a running sum of
@@ -68,7 +68,7 @@ struct __align__(16) Shared {
   uint2 own[kList];                              // this CTA's candidates: key, index
   float tops[kThreads];                          // the threads' maxima
   uint16_t scan[kScan];                          // groups whose vectors are read again
-  uint64_t table[1024];                          // kExp2Table, where the whole row is weighed
+  uint32_t table[1024];                          // kExp2Table, where the whole row is weighed
   uint64_t chunk[kWarps];                        // sums of the warps' runs
   uint64_t room[kWarps], room2[kWarps];
   uint64_t pick_before, pick_sum, total;
@@ -105,6 +105,14 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
 __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
   x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
   x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+}
+
+// Entry e of a vector.
+template <class T>
+__device__ __forceinline__ float entry_of(const uint4& w, int e) {
+  const int i = sizeof(T) == 2 ? e / 2 : e;
+  const uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+  return sizeof(T) == 4 ? __uint_as_float(x) : e % 2 ? bf16_hi(x) : bf16_lo(x);
 }
 
 template <class T>
@@ -181,7 +189,6 @@ struct Scale {
 };
 
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
-constexpr int kNoWeight = -(kSampleUnitBits + 2) * 1024;
 
 struct Exponent {
   float hi, lo;
@@ -198,19 +205,34 @@ __device__ __forceinline__ Exponent exponent(float x, const Scale& sc) {
   return {hi, fmaf(s, sc.c, -hi) + fmaf(s, sc.c_lo, err * sc.c)};
 }
 
-// exp((x - M) / T) in units of 2^-44: 2^(hi + lo) by the table (k / 1024 next to hi, r the rest, |r| <= 2^-11) and Taylor's
-// first terms of 2^r - 1 in fp32, which are off by 2^-34 of the weight; what follows is whole numbers.
-__device__ __forceinline__ uint64_t units_of(float x, const Scale& sc, const uint64_t* table) {
+// Shifts whose amounts may be any: 32 and more, and below 0, leave nothing.
+__device__ __forceinline__ uint32_t shift_right(uint32_t x, int by) {
+  uint32_t y;
+  asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(by));
+  return y;
+}
+__device__ __forceinline__ uint32_t shift_left(uint32_t x, int by) {
+  uint32_t y;
+  asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(by));
+  return y;
+}
+
+// exp((x - M) / T) in units of 2^-44, rounded down: 2^(hi + lo) by the table (k / 1024 next to hi, r the rest, |r| <= 2^-11)
+// and Taylor's first terms of 2^r - 1 in fp32; the rest is whole numbers, to 2^-30 of the weight.  (As pairs of floats, to
+// 2^-39, it took 50 instructions, and with 64-bit whole numbers, to 2^-34, as many cycles; 32-bit ones run at half the rate
+// of fp32's, 64-bit ones at a quarter.)
+__device__ __forceinline__ uint64_t units_of(float x, const Scale& sc, const uint32_t* table) {
   const Exponent t = exponent(x, sc);
   const float m = fmaf(fmaxf(t.hi, -4090.0f), 1024.0f, kMagic);
   const int k = __float_as_int(m) - __float_as_int(kMagic) - sc.k_top;
   const float z = (fmaf(m - kMagic, -1.0f / 1024.0f, t.hi) + t.lo) * kLn2Hi;
-  const float more = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z);                   // 2^r - 1
-  const int more40 = __float2int_rn(more * 1099511627776.0f);                      // in units of 2^-40
-  const long long base = (long long)table[k & 1023];
-  const long long w = base + (((long long)int(base >> 14) * more40 + (1 << 25)) >> 26);
-  const int down = -(k >> 10) & 63;
-  return k > kNoWeight ? uint64_t((w + ((1ll << down) >> 1)) >> down) : 0;
+  const float more = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z);                                             // 2^r - 1
+  const int more32 = __float_as_int(fmaf(more, 4294967296.0f, kMagic)) - __float_as_int(kMagic);  // in units of 2^-32
+  const int base = int(table[k & 1023]);
+  const uint32_t w = uint32_t(base + __mulhi(base, more32));  // in units of 2^-30
+  const int down = -(k >> 10) - (kSampleUnitBits - 30);
+  const uint32_t low = shift_right(w, down) | shift_left(w, -down), high = shift_right(w, down + 32);
+  return (uint64_t(high) << 32) | low;
 }
 
 __device__ __forceinline__ Scale scale_of(float M, float c, float c_lo) {
@@ -224,7 +246,7 @@ __device__ __forceinline__ Scale scale_of(float M, float c, float c_lo) {
   return sc;
 }
 
-__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const uint64_t* table) { return units_of(x, sc, table); }
+__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const uint32_t* table) { return units_of(x, sc, table); }
 
 // Whether a vector whose largest entry is x has weights that count.
 __device__ __forceinline__ bool weighs(float x, const Scale& sc) { return (x - sc.M) * sc.c > -float(kSampleUnitBits + 3); }
@@ -621,23 +643,18 @@ __device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t 
     __syncthreads();
     int part = 0;
     for (; part < kWarps - 1 && before + sh.room2[part] <= at; ++part) before += sh.room2[part];
-    // entry by entry, each thread a few
+    // entry by entry, one a thread
     const int i0 = max(min(v0 + part * each, v1) * kVec<T> - r.off, 0);
     const int i1 = min(min(v0 + (part + 1) * each, v1) * kVec<T> - r.off, r.V);
-    const int per = (i1 - i0 + kThreads - 1) / kThreads, a = min(i0 + tid * per, i1), b = min(a + per, i1);
-    uint64_t sum = 0;
-    for (int i = a; i < b; ++i) sum += f(entry(r, i), i);
-    before += block_scan(sum, sh.room) - sum;
-    if (before <= at && at < before + sum) {
-      for (int i = a; i < b; ++i) {
-        const uint64_t w = f(entry(r, i), i);
-        if (before + w > at) {
-          // (before the row's first weight there is nothing to be off by)
-          if ((before == 0 || at - before >= margin) && before + w - at > margin) sh.found = i;
-          break;
-        }
-        before += w;
-      }
+    for (int first = i0; first < i1 && before <= at; first += kThreads) {
+      const int i = first + tid;
+      const uint64_t own = i < i1 ? f(entry(r, i), i) : 0;
+      const uint64_t upto = before + block_scan(own, sh.room);
+      // (before the row's first weight there is nothing to be off by)
+      if (upto > at && upto - own <= at && (upto == own || at - (upto - own) >= margin) && upto - at > margin) sh.found = i;
+      if (tid == kThreads - 1) sh.pick_sum = upto;
+      __syncthreads();
+      before = sh.pick_sum;
     }
   }
   row_sync();
@@ -649,13 +666,19 @@ __device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t 
 // f(vector, number) for a warp's vectors [v0, v1), whole or not.
 template <class T, class F>
 __device__ __forceinline__ void few(const Row<T>& r, int v0, int v1, F f) {
-  for (int v = v0 + int(threadIdx.x % 32); v < v1; v += 64) {
-    const uint4 a = load_vector(r, v);
-    const bool two = v + 32 < v1;
-    const uint4 b = two ? load_vector(r, v + 32) : a;
-    f(a, v);
-    if (two) f(b, v + 32);
+  const uint4* p = reinterpret_cast<const uint4*>(r.base);
+  const int w0 = max(v0, r.off > 0 ? 1 : 0), w1 = min(v1, (r.off + r.V) / kVec<T>), lane = threadIdx.x % 32;  // whole ones
+  for (int v = w0 + lane; v < w1; v += 32 * kAhead) {
+    uint4 w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (v + 32 * i < w1) w[i] = __ldg(p + v + 32 * i);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (v + 32 * i < w1) f(w[i], v + 32 * i);
   }
+  if (lane == 0 && v0 < min(w0, v1)) f(edge_vector(r, v0), v0);
+  if (lane == 1 && w1 < v1 && w1 >= w0) f(edge_vector(r, w1), w1);
 }
 
 // The index of the n-th entry with this key (n >= 1).
@@ -726,15 +749,16 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     auto each_entry = [&](auto f) {
       const float least = value_of(lo), most = value_of(hi);
       stream(r, [&](const uint4& w, int v) {
-        if (vector_max(w, static_cast<T*>(nullptr)) < least) return;
         float x[kVec<T>];
         unpack(w, x);
+        uint32_t some = 0;
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) {
-          if (x[e] < least || x[e] > most || bin_of(x[e]) != first_bin) continue;
-          const int i = v * kVec<T> - r.off + e;
-          const uint32_t key = key_of(x[e]);
-          if (i >= 0 && i < r.V && within.keeps(key, i)) f(x[e], key, i);
+        for (int e = 0; e < kVec<T>; ++e) some |= (x[e] >= least && x[e] <= most ? 1u : 0u) << e;
+        for (; some != 0; some &= some - 1) {
+          const int e = __ffs(some) - 1, i = v * kVec<T> - r.off + e;
+          const float y = entry_of<T>(w, e);
+          const uint32_t key = key_of(y);
+          if (bin_of(y) == first_bin && i >= 0 && i < r.V && within.keeps(key, i)) f(y, key, i);
         }
       });
     };

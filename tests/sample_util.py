@@ -6,8 +6,8 @@ import numpy as np
 
 def sample64(x, u, T, k, p, least):
     """(token, log-probability, distribution, margin) of one row x (float64 values of its stored type): from the
-    definition, sorted.  `margin`: how far, relative to the mass it is decided within, the nearest decision was from its
-    border (the nucleus' border against p, the draw's against u)."""
+    definition, sorted.  `margin`: how far the nearest decision was from its border (the nucleus' border against p, the
+    draw's against u), in what the sums of weights may be off by."""
     V = len(x)
     order = np.lexsort((np.arange(V), -x))          # value descending, index ascending
     dist = np.zeros(V)
@@ -24,7 +24,7 @@ def sample64(x, u, T, k, p, least):
             np.concatenate([[0.0], np.cumsum(w.astype(np.longdouble))[:-1]]).astype(float)
         target = p * math.fsum(w)
         keep &= before < target
-        margin = min(margin, np.abs(before[1:] - target).min(initial=math.inf) / math.fsum(w))
+        margin = min(margin, np.abs(before[1:] - target).min(initial=math.inf) / off(math.fsum(w), V))
     keep &= w >= least
     keep[0] = True
     kept = order[keep]
@@ -34,15 +34,16 @@ def sample64(x, u, T, k, p, least):
     upto = np.cumsum(mass.astype(np.longdouble)).astype(float)
     token = int(np.searchsorted(upto, u * total, side="right"))
     at = np.flatnonzero(mass)
-    margin = min(margin, np.abs(upto[at] - u * total)[:-1].min(initial=math.inf) / total)
+    margin = min(margin, np.abs(upto[at] - u * total)[:-1].min(initial=math.inf) / off(total, V))
     token = min(token, int(at[-1]))
     return token, math.log(mass[token] / total), mass / total, margin
 
 
-# Borders nearer than this are not judged: a weight is off by 2^-34 of itself at most (its fp32 part, 2^r - 1 <= 2^-11.5, by
-# three roundings; its exponent by 2^-35) and by half a unit of 2^-45 of the largest, of which there are 2^18 at most in
-# these tests; both sides of a comparison are sums of such.
-BORDER = 2.0 ** -32 + 2.0 ** -26 * 2.0 ** -8
+def off(mass, V):
+    """What a border between sums of weights may be off by.  A weight is off by 2^-29 of itself (its table's entry 2^-31, its
+    whole part 2^-30 rounded down, 2^r - 1 in fp32 2^-34), and is rounded down to units of 2^-44 of the largest; the two
+    sides of a comparison together are the whole mass."""
+    return 2.0 ** -29 * mass + 2.0 ** -44 * V
 
 
 # The kept mass, where no border is near, may be the sum of fp32 weights 2^t, t = fma(x, c, -ref): with D = (max - x) c (in

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import test_paged_refusals as host
-from sample_util import BORDER, logprob_bound, probs_bound, sample64
+from sample_util import logprob_bound, probs_bound, sample64
 
 NULL, SHAPE, ALIGN, DTYPE, PARAM = 1, 2, 3, 4, 5
 m = host.m
@@ -136,7 +136,7 @@ def _compare(x, u, got, T, k, p, least, probs=True):
         for i in range(n):
             token, lp, dist, margin = sample64(x[b, i].double().numpy(), float(u[b, i]), f32(each(T, b)), each(k, b),
                                                f32(each(p, b)), f32(each(least, b)))
-            if margin < BORDER:
+            if margin < 1:
                 left += 1
                 continue
             assert int(got.tokens[b, i]) == token, (b, i, margin)
@@ -145,7 +145,7 @@ def _compare(x, u, got, T, k, p, least, probs=True):
                 have = got.probs[b, i].double().cpu().numpy()
                 far = np.abs(have - dist) > probs_bound(dist)
                 assert not far.any(), (b, i, int(far.argmax()), have[far][0], dist[far][0])
-    assert left <= B * n // 50
+    assert left <= 1 + B * n // 50   # (of 50 thousand borders one is that near in 2e-4 of the rows)
     assert not got.req_status.any()
 
 
