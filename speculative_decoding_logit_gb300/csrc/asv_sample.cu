@@ -32,10 +32,6 @@ namespace {
 
 #include "exp2_table.inc"
 
-constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;
-constexpr int kWarps = kThreads / 32;
-constexpr int kList = 512;               // candidates that are compared pair by pair
 constexpr int kNucleus = 64;             // maxima of threads that a nucleus is first looked for above
 constexpr int kGroups = 16;              // groups of a thread's vectors, at most
 constexpr int kScan = 1024;              // groups that are read again, at most
@@ -54,25 +50,30 @@ struct Cut {
   __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
 };
 
+// WHOLE: with what the general way needs.
+template <int THREADS, bool WHOLE>
 struct __align__(16) Shared {
-  union {                                        // one after the other
-    float group[(kGroups + 1) * kThreads];       // maxima of groups of a thread's vectors; of the row's ends
-    uint2 bins[kBins];                           // a histogram's 64-bit sums
+  static constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+  static constexpr int kList = 2 * THREADS;        // candidates that are compared with each other
+  union {                                          // one after the other
+    float group[(kGroups + 1) * THREADS];          // maxima of groups of a thread's vectors; of the row's ends
+    uint2 bins[WHOLE ? kBins : 1];                 // a histogram's 64-bit sums
     struct {
-      uint64_t place[kList];                     // the candidates' places in the order
-      uint4 sorted[kList];                       // the candidates in order
+      uint64_t place[kList];                       // the candidates' places in the order
+      uint4 sorted[kList];                         // the candidates in order
     };
   };
-  uint4 list[kList];                             // candidates of the row: key, index, weight
-  uint64_t before[kList];                        // mass before each, by value or by index
-  uint2 own[kList];                              // this CTA's candidates: key, index
-  float tops[kThreads];                          // the threads' maxima
-  uint16_t scan[kScan];                          // groups whose vectors are read again
-  uint32_t table[1024];                          // kExp2Table, where the whole row is weighed
-  uint64_t chunk[kWarps];                        // sums of the warps' runs
+  uint4 list[kList];                               // candidates of the row: key, index, weight
+  uint64_t before[kList];                          // mass before each, by value or by index
+  uint2 own[kList];                                // this CTA's candidates: key, index
+  float tops[THREADS];                             // the threads' maxima
+  uint16_t scan[kScan];                            // groups whose vectors are read again
+  uint32_t table[WHOLE ? 1024 : 1];                // kExp2Table, where the whole row is weighed
+  uint64_t chunk[kWarps];                          // sums of the warps' runs
   uint64_t room[kWarps], room2[kWarps];
   uint64_t pick_before, pick_sum, total;
-  float4 ends;                                   // of the CTA: maximum, bound of the candidates, whether it is bad
+  float2 sums[kWarps];                             // the warps' maxima and fast sums next to them
+  float4 ends;                                     // of the CTA: maximum, bound of the candidates, whether it is bad, sum
   Cut cut;
   int n_scan, n_own, found, pick;
 };
@@ -255,7 +256,8 @@ __device__ __forceinline__ bool weighs(float x, const Scale& sc) { return (x - s
 
 __device__ __forceinline__ void row_sync() {  // all threads of the row's CTAs
   __syncwarp();
-  cluster_sync();
+  if (cluster_size() > 1) cluster_sync();
+  else __syncthreads();
 }
 
 __device__ __forceinline__ uint64_t ld_peer_u64(const uint64_t* p, int rank) {
@@ -307,6 +309,10 @@ constexpr float kFastRange = 1048576.0f;
 struct Partial {
   float ref = -INFINITY;  // log2 units
   float hi = 0.0f, lo = 0.0f;
+  // the sum with `top` (log2 units, at least any term's) for reference
+  __device__ __forceinline__ float next_to(float top) const {
+    return ref > -INFINITY ? (hi + lo) * ex2_approx(ref - top) : 0.0f;
+  }
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -364,8 +370,9 @@ __device__ __forceinline__ uint64_t units_of_sum(const Partial& s, const Scale& 
 
 // A bound of the n-th largest of sh.tops (1 <= n <= kThreads) from below, to sixteen bits, and the largest, by a warp: the
 // longest beginning of a key that n of the keys reach, two bits a step.
-__device__ __forceinline__ void nth_largest(const Shared& sh, int n, float& nth, float& top) {
-  constexpr int kEach = kThreads / 32;
+template <class S>
+__device__ __forceinline__ void nth_largest(const S& sh, int n, float& nth, float& top) {
+  constexpr int kEach = S::kThreads / 32;
   const int lane = threadIdx.x % 32;
   uint32_t key[kEach], most = 0;
 #pragma unroll
@@ -403,22 +410,22 @@ struct Groups {
 
 // The CTA's entries from tau on, out of the groups of vectors whose maximum reaches it, to sh.own (those that have
 // room; sh.n_own counts them all).
-template <class T>
-__device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
+template <class S, class T>
+__device__ __noinline__ void collect(S& sh, const Row<T>& r, float tau) {
   const int tid = threadIdx.x;
   if (tid == 0) sh.n_scan = sh.n_own = 0;
   __syncthreads();
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    if (sh.group[g * kThreads + tid] >= tau) {
+    if (sh.group[g * S::kThreads + tid] >= tau) {
       const int at = atomicAdd(&sh.n_scan, 1);
-      if (at < kScan) sh.scan[at] = uint16_t(g * kThreads + tid);
+      if (at < kScan) sh.scan[at] = uint16_t(g * S::kThreads + tid);
     }
   }
   __syncthreads();
   const int n = sh.n_scan, per_group = Groups<T>(r).per_group;
   if (n > kScan) {
-    if (tid == 0) sh.n_own = kList + 1;
+    if (tid == 0) sh.n_own = S::kList + 1;
     return;
   }
   auto take = [&](const uint4& w, int v) {
@@ -430,7 +437,7 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
       const int index = v * kVec<T> - r.off + e;
       if (x[e] >= tau && index >= 0 && index < r.V) {
         const int to = atomicAdd(&sh.n_own, 1);
-        if (to < kList) sh.own[to] = make_uint2(key_of(x[e]), uint32_t(index));
+        if (to < S::kList) sh.own[to] = make_uint2(key_of(x[e]), uint32_t(index));
       }
     }
   };
@@ -439,19 +446,19 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
   auto vector_at = [&](int x) {
     const int k = x / per_group, q = x - k * per_group;
     if (k >= n) return -1;
-    const int g = sh.scan[k] / kThreads, t = sh.scan[k] % kThreads, warp = t / 32;
+    const int g = sh.scan[k] / S::kThreads, t = sh.scan[k] % S::kThreads, warp = t / 32;
     const int v = max(r.run_start(r.rank, warp), w0) + t % 32 + 32 * (g * per_group + q);
     return v < min(r.run_end(r.rank, warp), w1) ? v : -1;
   };
   const uint4* p = reinterpret_cast<const uint4*>(r.base);
-  for (int x = tid; x < n * per_group; x += 2 * kThreads) {
-    const int a = vector_at(x), b = vector_at(x + kThreads);
+  for (int x = tid; x < n * per_group; x += 2 * S::kThreads) {
+    const int a = vector_at(x), b = vector_at(x + S::kThreads);
     const uint4 none = make_uint4(0, 0, 0, 0), u = a >= 0 ? __ldg(p + a) : none, v = b >= 0 ? __ldg(p + b) : none;
     if (a >= 0) take(u, a);
     if (b >= 0) take(v, b);
   }
   // the row's ends (as in stream)
-  if (sh.group[kGroups * kThreads + tid] >= tau) {
+  if (sh.group[kGroups * S::kThreads + tid] >= tau) {
     const int lane = tid % 32;
     if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) take(edge_vector(r, 0), 0);
     if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) take(edge_vector(r, w1), w1);
@@ -460,7 +467,8 @@ __device__ __noinline__ void collect(Shared& sh, const Row<T>& r, float tau) {
 
 // The row's candidates of all CTAs, with their weights (kOne each without), to sh.list; their number, or -1 if there is no
 // room.
-__device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, bool weigh) {
+template <class S>
+__device__ __noinline__ int share_out(S& sh, const Scale& sc, int ctas, bool weigh) {
   const int lane = threadIdx.x % 32;
   const int own = lane < ctas ? int(ld_peer_u32(&sh.n_own, lane)) : 0;
   int upto = own;
@@ -469,9 +477,9 @@ __device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, boo
     const int x = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += x;
   }
-  if (__any_sync(0xffffffffu, lane < ctas && (own > kList || upto > kList))) return -1;
+  if (__any_sync(0xffffffffu, lane < ctas && (own > S::kList || upto > S::kList))) return -1;
   const int n = __shfl_sync(0xffffffffu, upto, kMaxCtas - 1);
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
+  for (int i0 = 0; i0 < n; i0 += S::kThreads) {
     const int i = i0 + threadIdx.x;
     int c = 0, start = 0;
 #pragma unroll
@@ -493,9 +501,10 @@ __device__ __noinline__ int share_out(Shared& sh, const Scale& sc, int ctas, boo
 __device__ __forceinline__ uint64_t weight_in(const uint4& e) { return (uint64_t(e.w) << 32) | e.z; }
 
 // The warps' sums of all CTAs, added up by each warp.
-__device__ __forceinline__ uint64_t all_chunks(const Shared& sh, int ctas) {
+template <class S>
+__device__ __forceinline__ uint64_t all_chunks(const S& sh, int ctas) {
   uint64_t x = 0;
-  for (int i = threadIdx.x % 32; i < ctas * kWarps; i += 32) x += ld_peer_u64(sh.chunk + i % kWarps, i / kWarps);
+  for (int i = threadIdx.x % 32; i < ctas * S::kWarps; i += 32) x += ld_peer_u64(sh.chunk + i % S::kWarps, i / S::kWarps);
   return warp_sum(x);
 }
 
@@ -507,13 +516,14 @@ __device__ __forceinline__ uint64_t part_of(uint64_t part, uint64_t mass) {
 // The candidates in order, to sh.sorted, and the mass before each, to sh.before: a candidate's rank is the number of those
 // before it, a group of threads counts for one where there are few.  (A warp's bitonic network took 1.6 us at 100
 // candidates, its shuffles one behind the other.)
-__device__ __noinline__ void sort_list(Shared& sh, int n) {
+template <class S>
+__device__ __noinline__ void sort_list(S& sh, int n) {
   const int tid = threadIdx.x;
-  for (int e = tid; e < n; e += kThreads) sh.place[e] = (uint64_t(sh.list[e].x) << 32) | ~sh.list[e].y;
+  for (int e = tid; e < n; e += S::kThreads) sh.place[e] = (uint64_t(sh.list[e].x) << 32) | ~sh.list[e].y;
   __syncthreads();
   int g = 1;
-  while (g < 32 && 2 * g * n <= kThreads) g *= 2;
-  for (int e0 = 0; e0 < n; e0 += kThreads / g) {
+  while (g < 32 && 2 * g * n <= S::kThreads) g *= 2;
+  for (int e0 = 0; e0 < n; e0 += S::kThreads / g) {
     const int e = e0 + tid / g;
     const uint64_t mine = sh.place[min(e, n - 1)];
     int rank = 0;
@@ -523,7 +533,7 @@ __device__ __noinline__ void sort_list(Shared& sh, int n) {
     if (tid % g == 0 && e < n) sh.sorted[rank] = sh.list[e];
   }
   __syncthreads();
-  static_assert(kList == 2 * kThreads);
+  static_assert(S::kList == 2 * S::kThreads);
   const uint64_t a = 2 * tid < n ? weight_in(sh.sorted[2 * tid]) : 0, b = 2 * tid + 1 < n ? weight_in(sh.sorted[2 * tid + 1]) : 0;
   const uint64_t upto = block_scan(a + b, sh.room);
   sh.before[2 * tid] = upto - a - b;
@@ -533,11 +543,12 @@ __device__ __noinline__ void sort_list(Shared& sh, int n) {
 
 // The mass of the first m candidates with lower indices than each, to sh.before.  A group of threads has one where there
 // are few.
-__device__ __forceinline__ void masses_by_index(Shared& sh, int m) {
+template <class S>
+__device__ __forceinline__ void masses_by_index(S& sh, int m) {
   const int tid = threadIdx.x;
   int g = 1;
-  while (g < 32 && 2 * g * m <= kThreads) g *= 2;
-  for (int e0 = 0; e0 < m; e0 += kThreads / g) {
+  while (g < 32 && 2 * g * m <= S::kThreads) g *= 2;
+  for (int e0 = 0; e0 < m; e0 += S::kThreads / g) {
     const int e = e0 + tid / g;
     const uint32_t index = sh.sorted[min(e, m - 1)].y;
     uint64_t mass = 0;
@@ -561,7 +572,8 @@ struct Drawn {
 // can be kept (`closed`: nothing else is, for its weight; if not, the list has to reach past the nucleus).  `mass`, off by
 // `off` at most: of the row, where k = 0 and p < 1.  False: the list does not settle it (sh.cut and the result are then
 // nothing).
-__device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t least, bool closed, uint64_t mass,
+template <class S>
+__device__ __noinline__ bool settle(S& sh, int n, int k, float p, uint64_t least, bool closed, uint64_t mass,
                                     uint64_t off, uint64_t draw, Drawn& d) {
   const int tid = threadIdx.x;
   sort_list(sh, n);
@@ -579,7 +591,7 @@ __device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t 
   bool unsure = k == 0 && p < 1.0f && !closed && sum < high;
   // the kept ones are the first m
   int m = 0;
-  for (int e0 = 0; e0 < n; e0 += kThreads) {
+  for (int e0 = 0; e0 < n; e0 += S::kThreads) {
     const int e = e0 + tid;
     const uint64_t w = e < n ? weight_in(sh.sorted[e]) : 0, b = e < n ? sh.before[e] : 0;
     const bool may = e < n && (k == 0 || e < k) && w >= least;
@@ -592,7 +604,7 @@ __device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t 
   if (tid == 0) sh.cut = {sh.sorted[m - 1].x, int(sh.sorted[m - 1].y)};
   __syncthreads();  // (all have read what is before whom)
   masses_by_index(sh, m);
-  for (int e = tid; e < m; e += kThreads) {
+  for (int e = tid; e < m; e += S::kThreads) {
     const uint64_t w = weight_in(sh.sorted[e]), b = sh.before[e];
     if (b <= at && at < b + w) {
       sh.found = int(sh.sorted[e].y);
@@ -609,12 +621,15 @@ __device__ __noinline__ bool settle(Shared& sh, int n, int k, float p, uint64_t 
 
 // Where the draw falls, draw / 2^64 of the warps' sums (in sh.chunk, behind a row_sync): the run that passes it and the sum
 // before it, to sh.pick and sh.pick_before; the sum of all to sh.total.
-template <class T>
-__device__ __forceinline__ uint64_t find_run(Shared& sh, const Row<T>& r, uint64_t draw) {
-  const int tid = threadIdx.x, runs = r.ctas * kWarps;
-  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % kWarps, tid / kWarps) : 0;
+template <class S, class T>
+__device__ __forceinline__ uint64_t find_run(S& sh, const Row<T>& r, uint64_t draw) {
+  const int tid = threadIdx.x, runs = r.ctas * S::kWarps;
+  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % S::kWarps, tid / S::kWarps) : 0;
   const uint64_t incl = block_scan(mine, sh.room);
-  if (tid == kThreads - 1) sh.total = incl;
+  if (tid == S::kThreads - 1) {
+    sh.total = incl;
+    sh.pick = 0;
+  }
   __syncthreads();
   const uint64_t at = __umul64hi(draw, sh.total);
   if (tid < runs && incl > at && incl - mine <= at) {
@@ -627,32 +642,32 @@ __device__ __forceinline__ uint64_t find_run(Shared& sh, const Row<T>& r, uint64
 // The entry of run sh.pick that `at` falls into: to sh.found of the CTA that owns the run (-1: within `margin` of the
 // entry's ends, or in none), read from there by all.  sum_of(v0, v1): a warp's sum of the entries of vectors [v0, v1), f(x,
 // index) one entry's.
-template <class T, class S, class F>
-__device__ __forceinline__ int find_entry(Shared& sh, const Row<T>& r, uint64_t at, uint64_t margin, S sum_of, F f) {
+template <class S, class T, class Sum, class F>
+__device__ __forceinline__ int find_entry(S& sh, const Row<T>& r, uint64_t at, uint64_t margin, Sum sum_of, F f) {
   const int tid = threadIdx.x, warp = tid / 32;
   if (tid == 0) sh.found = -1;
   __syncthreads();
-  const int pick = sh.pick, owner = pick / kWarps;
+  const int pick = sh.pick, owner = pick / S::kWarps;
   if (r.rank == owner) {
     // the part of the run that a warp has
-    const int v0 = r.run_start(owner, pick % kWarps), v1 = r.run_end(owner, pick % kWarps);
-    const int each = (v1 - v0 + kWarps - 1) / kWarps;
+    const int v0 = r.run_start(owner, pick % S::kWarps), v1 = r.run_end(owner, pick % S::kWarps);
+    const int each = (v1 - v0 + S::kWarps - 1) / S::kWarps;
     uint64_t before = sh.pick_before;
     const uint64_t own = sum_of(min(v0 + warp * each, v1), min(v0 + (warp + 1) * each, v1));
     if (tid % 32 == 0) sh.room2[warp] = own;
     __syncthreads();
     int part = 0;
-    for (; part < kWarps - 1 && before + sh.room2[part] <= at; ++part) before += sh.room2[part];
+    for (; part < S::kWarps - 1 && before + sh.room2[part] <= at; ++part) before += sh.room2[part];
     // entry by entry, one a thread
     const int i0 = max(min(v0 + part * each, v1) * kVec<T> - r.off, 0);
     const int i1 = min(min(v0 + (part + 1) * each, v1) * kVec<T> - r.off, r.V);
-    for (int first = i0; first < i1 && before <= at; first += kThreads) {
+    for (int first = i0; first < i1 && before <= at; first += S::kThreads) {
       const int i = first + tid;
       const uint64_t own = i < i1 ? f(entry(r, i), i) : 0;
       const uint64_t upto = before + block_scan(own, sh.room);
       // (before the row's first weight there is nothing to be off by)
       if (upto > at && upto - own <= at && (upto == own || at - (upto - own) >= margin) && upto - at > margin) sh.found = i;
-      if (tid == kThreads - 1) sh.pick_sum = upto;
+      if (tid == S::kThreads - 1) sh.pick_sum = upto;
       __syncthreads();
       before = sh.pick_sum;
     }
@@ -682,8 +697,8 @@ __device__ __forceinline__ void few(const Row<T>& r, int v0, int v1, F f) {
 }
 
 // The index of the n-th entry with this key (n >= 1).
-template <class T>
-__device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key, uint64_t n) {
+template <class S, class T>
+__device__ __noinline__ int nth_equal(S& sh, const Row<T>& r, uint32_t key, uint64_t n) {
   uint64_t own = 0;
   auto count = [&](const uint4& w, int v) {
     float x[kVec<T>];
@@ -699,9 +714,11 @@ __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key,
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
   row_sync();
   // (the share n - 1 of the count, as find_run takes it: it is looked for in units, not in parts of 2^64)
-  const int tid = threadIdx.x, runs = r.ctas * kWarps;
-  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % kWarps, tid / kWarps) : 0;
+  const int tid = threadIdx.x, runs = r.ctas * S::kWarps;
+  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % S::kWarps, tid / S::kWarps) : 0;
   const uint64_t incl = block_scan(mine, sh.room);
+  if (tid == 0) sh.pick = 0;
+  __syncthreads();
   if (tid < runs && incl >= n && incl - mine < n) {
     sh.pick = tid;
     sh.pick_before = incl - mine;
@@ -720,8 +737,8 @@ __device__ __noinline__ int nth_equal(Shared& sh, const Row<T>& r, uint32_t key,
 // target_of(all): the last is the first with target <= the inclusive sum.  A histogram by value over the larger weights'
 // range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
 // on.  The bins are added up a part by each CTA.
-template <bool MASS, class T, class G>
-__device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of) {
+template <bool MASS, class S, class T, class G>
+__device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of) {
   const int tid = threadIdx.x, lane = tid % 32;
   // bins of equal width down to weights of 2^-24, the last takes the rest (7 % of a weight's width each: of 152 thousand
   // flat entries 250 at most fall into one)
@@ -767,13 +784,13 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       __syncthreads();
       each_entry([&](float, uint32_t key, int i) {
         const int to = atomicAdd(&sh.n_own, 1);
-        if (to < kList) sh.own[to] = make_uint2(key, uint32_t(i));
+        if (to < S::kList) sh.own[to] = make_uint2(key, uint32_t(i));
       });
       row_sync();
       const int n = share_out(sh, sc, r.ctas, MASS);
       if (n > 0) {
         sort_list(sh, n);
-        for (int e = tid; e < n; e += kThreads) {
+        for (int e = tid; e < n; e += S::kThreads) {
           const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(e));
           if (b < target && target <= b + m) sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
         }
@@ -781,7 +798,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
         return sh.cut;
       }
     }
-    for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = make_uint2(0, 0);
+    for (int i = tid; i < kBins; i += S::kThreads) sh.bins[i] = make_uint2(0, 0);
     __syncthreads();
     if (level == 0) {
       stream(r, [&](const uint4& w, int v) {
@@ -809,7 +826,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     row_sync();
     // this CTA's part of the bins, of all CTAs, in place (nobody else reads them here), and their sum
     uint64_t sum = 0;
-    for (int i = part0 + tid; i < part1; i += kThreads) {
+    for (int i = part0 + tid; i < part1; i += S::kThreads) {
       uint64_t own = 0;
       for (int c = 0; c < r.ctas; ++c) own += ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.bins + i), c);
       *reinterpret_cast<uint64_t*>(sh.bins + i) = own;
@@ -821,7 +838,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     row_sync();
     uint64_t mine = 0;
     if (lane < r.ctas)
-      for (int i = 0; i < kWarps; ++i) mine += ld_peer_u64(sh.chunk + i, lane);
+      for (int i = 0; i < S::kWarps; ++i) mine += ld_peer_u64(sh.chunk + i, lane);
     uint64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < kMaxCtas; d *= 2) {
@@ -831,11 +848,11 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
     if (level == 0) target = target_of(__shfl_sync(0xffffffffu, upto, kMaxCtas - 1));
     upto += above;
     const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && upto - mine < target && target <= upto);
-    const int owner = __ffs(holds) - 1;
+    const int owner = max(__ffs(holds) - 1, 0);
     const uint64_t start = __shfl_sync(0xffffffffu, upto - mine, owner);
     if (r.rank == owner) {
       // the bin, each thread looking through a few
-      const int few = (part + kThreads - 1) / kThreads, i0 = min(part0 + tid * few, part1), i1 = min(i0 + few, part1);
+      const int few = (part + S::kThreads - 1) / S::kThreads, i0 = min(part0 + tid * few, part1), i1 = min(i0 + few, part1);
       uint64_t s = 0;
       for (int i = i0; i < i1; ++i) s += *reinterpret_cast<const uint64_t*>(sh.bins + i);
       uint64_t b = start + block_scan(s, sh.room) - s;
@@ -852,7 +869,7 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
       }
     }
     row_sync();
-    const int bin = int(ld_peer_u32(&sh.pick, owner));
+    const int bin = max(int(ld_peer_u32(&sh.pick, owner)), 0);
     above = ld_peer_u64(&sh.pick_before, owner);
     in_bin = ld_peer_u64(&sh.pick_sum, owner);
     if (level == 0) {
@@ -877,7 +894,8 @@ __device__ __noinline__ Cut search(Shared& sh, const Row<T>& r, const Scale& sc,
 }
 
 // The smallest key whose weight is at least `least`, by a warp: 32 candidates at a time.
-__device__ __noinline__ uint32_t least_key(Shared& sh, const Scale& sc, uint64_t least) {
+template <class S>
+__device__ __noinline__ uint32_t least_key(S& sh, const Scale& sc, uint64_t least) {
   uint32_t lo = 1, hi = key_of(sc.M);
   __syncthreads();  // (sh.cut's last readers are done)
   if (threadIdx.x < 32) {
@@ -902,8 +920,8 @@ struct Kept {
 };
 
 // A draw from the whole row by the warps' fast sums (sh.chunk, behind a row_sync).  A token < 0: too near a border to say.
-template <class T>
-__device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale& sc, uint64_t draw) {
+template <class S, class T>
+__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T>& r, const Scale& sc, uint64_t draw) {
   const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
@@ -912,7 +930,7 @@ __device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale
   // of the mass, 1/4 at most, and each is off by 2^-18 of itself; the run's own sum counts once as the rows streamed and
   // once as it is taken apart here, each off by 2^-18 too.
   const int run = sh.pick;
-  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % kWarps, run / kWarps)) >> kFastBits) + 64;
+  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % S::kWarps, run / S::kWarps)) >> kFastBits) + 64;
   d.token = find_entry(
       sh, r, at, margin,
       [&](int v0, int v1) {
@@ -930,8 +948,8 @@ __device__ __noinline__ Drawn draw_fast(Shared& sh, const Row<T>& r, const Scale
 }
 
 // A draw from the kept entries by exact sums.
-template <class T>
-__device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw) {
+template <class S, class T>
+__device__ __noinline__ Drawn draw_exact(S& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw) {
   uint64_t own = 0;
   auto add = [&](const uint4& w, int v) {
     const float top = vector_max(w, static_cast<T*>(nullptr));
@@ -964,23 +982,17 @@ __device__ __noinline__ Drawn draw_exact(Shared& sh, const Row<T>& r, const Scal
   return d;
 }
 
-// ------------------------------------------------------------------ the kernel
+// ------------------------------------------------------------------ the kernels
 
-template <class T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
-  __shared__ Shared sh;
+// What a launch does with its rows: all of it; the first way alone, leaving what that does not settle marked in the
+// tokens; or those rows in general.
+enum Part { kAll, kFirst, kRest };
+constexpr int kLeft = INT_MIN;
+
+template <Part PART, class S, class T>
+__device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r, long long row) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  Row<T> r;
-  r.ctas = int(cluster_size());
-  r.rank = int(cluster_rank());
-  const long long row = blockIdx.x / r.ctas;
   const int b = int(row / a.n), n = int(row - (long long)b * a.n);
-  if (tid == 0) {
-    sh.found = sh.pick = 0;
-    sh.pick_before = sh.pick_sum = sh.total = 0;
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the request's parameters
   const float T_ = a.temperature != nullptr ? a.temperature[b] : a.one.temperature;
@@ -999,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
   r.V = a.V;
   r.vectors = (r.off + a.V + kVec<T> - 1) / kVec<T>;
   r.per_cta = (r.vectors + r.ctas - 1) / r.ctas;
-  r.per_warp = (r.per_cta + kWarps - 1) / kWarps;
+  r.per_warp = (r.per_cta + S::kWarps - 1) / S::kWarps;
   r.v0 = r.run_start(r.rank, warp);
   r.v1 = r.run_end(r.rank, warp);
   const float c = greedy || !params_ok ? 1.0f : kLog2eHi / T_;
@@ -1007,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
 
   // ---- the row streams once: the threads' maxima, and the mass where it is needed
   const bool nucleus = !greedy && top_p < 1.0f;
-  const bool sums = k == 0 && (nucleus || min_p == 0.0f);
+  const bool sums = PART != kRest && k == 0 && (nucleus || min_p == 0.0f);
   float top = -INFINITY;
   Partial part;
   {
@@ -1023,8 +1035,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
       }
       return m;
     };
-    auto close = [&]() {
-      sh.group[g * kThreads + tid] = most;
+    auto close = [&]() {  // (a group without vectors has no maximum)
+      if (PART != kRest) sh.group[g * S::kThreads + tid] = left < per_group ? most : NAN;
       top = max_nan(top, most);
       most = -INFINITY;
       ++g;
@@ -1050,42 +1062,63 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < kFirstAhead - 1; ++i)
         if (v + 32 * i < end) most = max_nan(most, one(w[i]));
+      --left;
     }
     while (g < kGroups) close();
     // the row's ends (as in stream)
-    if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) most = one(edge_vector(r, 0));
-    if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) most = one(edge_vector(r, w1));
+    if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) {
+      most = one(edge_vector(r, 0));
+      --left;
+    }
+    if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) {
+      most = one(edge_vector(r, w1));
+      --left;
+    }
     close();
   }
-  bool bad = __any_sync(0xffffffffu, !(top < INFINITY));
   // Candidates are looked for from tau on: the row's k-th largest is at least the least of the CTAs' (k / ctas)-th
   // largest maxima of threads.
-  const int nth = k > 0 ? (k + r.ctas - 1) / r.ctas : nucleus ? max(kNucleus / r.ctas, 1) : kThreads + 1;
+  const int nth = k > 0 ? (k + r.ctas - 1) / r.ctas : nucleus ? max(kNucleus / r.ctas, 1) : S::kThreads + 1;
   sh.tops[tid] = top;
-  bad = __syncthreads_or(bad);
+  if (sums) {
+    const float most = warp_max(top), s = most > -kFastRange ? part.next_to(most * c) : 0.0f;
+    float all = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) sh.sums[warp] = make_float2(most, all);
+  }
+  bool bad = __syncthreads_or(!(top < INFINITY));
   if (warp == 0) {
     float least_top = -INFINITY, most = -INFINITY;
-    nth_largest(sh, min(nth, kThreads), least_top, most);
-    if (lane == 0) sh.ends = make_float4(most, nth <= kThreads ? least_top : -INFINITY, bad ? 1.0f : 0.0f, 0.0f);
+    nth_largest(sh, min(nth, S::kThreads), least_top, most);
+    float all = 0.0f;
+    if (sums)
+      for (int w = 0; w < S::kWarps; ++w) all += sh.sums[w].y * ex2_approx((sh.sums[w].x - most) * c);
+    if (lane == 0) sh.ends = make_float4(most, nth <= S::kThreads ? least_top : -INFINITY, bad ? 1.0f : 0.0f, all);
   }
   row_sync();
-  float tau, M;
+  float tau, M, about;  // about: the row's mass, roughly
   {
     float4 e = make_float4(-INFINITY, INFINITY, 0.0f, 0.0f);
     if (lane < r.ctas) {
       const uint64_t ab = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends), lane);
-      e.x = __uint_as_float(uint32_t(ab));
-      e.y = __uint_as_float(uint32_t(ab >> 32));
-      e.z = __uint_as_float(ld_peer_u32(&sh.ends.z, lane));
+      const uint64_t cd = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends) + 1, lane);
+      e = make_float4(__uint_as_float(uint32_t(ab)), __uint_as_float(uint32_t(ab >> 32)), __uint_as_float(uint32_t(cd)),
+                      __uint_as_float(uint32_t(cd >> 32)));
     }
     bad = __any_sync(0xffffffffu, e.z != 0.0f);
+    M = e.x;
 #pragma unroll
     for (int o = 1; o < kMaxCtas; o *= 2) {
-      e.x = fmaxf(e.x, __shfl_xor_sync(0xffffffffu, e.x, o));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       e.y = fminf(e.y, __shfl_xor_sync(0xffffffffu, e.y, o));
     }
-    M = __shfl_sync(0xffffffffu, e.x, 0);
+    M = __shfl_sync(0xffffffffu, M, 0);
     tau = __shfl_sync(0xffffffffu, e.y, 0);
+    about = e.w > 0.0f ? e.w * ex2_approx((e.x - M) * c) : 0.0f;
+#pragma unroll
+    for (int o = 1; o < kMaxCtas; o *= 2) about += __shfl_xor_sync(0xffffffffu, about, o);
+    about = __shfl_sync(0xffffffffu, about, 0);
   }
   bad = bad || M == -INFINITY;
   const Scale sc = scale_of(M, c, c_lo);
@@ -1099,52 +1132,64 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
       least = min_p < 1.0f ? part_of(uint64_t(min_p * 18446744073709551616.0f), most) : most;
     }
     const uint64_t draw = greedy ? 0 : uint64_t(u * 18446744073709551616.0f);
-    if (sums) {
-      const uint64_t w = warp_sum(units_of_sum(part, sc));
-      if (lane == 0) sh.chunk[warp] = w;
-    }
-    // Where nothing depends on the mass below min-p's border, candidates end there (a little below it, for the roundings).
-    bool closed = false;
-    if (greedy) {
-      tau = sc.M;
-    } else if (min_p > 0.0f && (k == 0 || !nucleus)) {
-      const float span = T_ * logf(min_p), border = sc.M + span - 1e-5f * (fabsf(sc.M) - span);
-      if (!(tau > border) || nth > kThreads) {
-        tau = border;
-        closed = true;
-      }
-    }
-    const bool trusted = !sums || fabsf(sc.M * sc.c) < kFastRange - 128.0f;
-    const bool by_list = trusted && (nth <= kThreads || closed);
     bool settled = false;
-    if (by_list) {
-      collect(sh, r, tau);
-      row_sync();
-      const int found = share_out(sh, sc, r.ctas, !greedy);
-      const uint64_t mass = sums ? all_chunks(sh, r.ctas) : 0;
-      if (found > 0) settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, d);
-      if (settled) cut = sh.cut;
-      row_sync();  // (the peers have read the candidates)
-    } else if (trusted && sums && !nucleus) {
-      row_sync();
-      d = draw_fast(sh, r, sc, draw);
-      settled = d.token >= 0;
+    if constexpr (PART != kRest) {
+      if (sums) {
+        const uint64_t w = warp_sum(units_of_sum(part, sc));
+        if (lane == 0) sh.chunk[warp] = w;
+      }
+      // Where nothing depends on the mass below min-p's border, candidates end there (a little below it, for the
+      // roundings).
+      bool closed = false;
+      if (greedy) {
+        tau = sc.M;
+      } else if (min_p > 0.0f && (k == 0 || !nucleus)) {
+        const float span = T_ * logf(min_p), border = sc.M + span - 1e-5f * (fabsf(sc.M) - span);
+        if (!(tau > border) || nth > S::kThreads) {
+          tau = border;
+          closed = true;
+        }
+      }
+      const bool trusted = !sums || fabsf(sc.M * sc.c) < kFastRange - 128.0f;
+      // (a weight is 1 at most, so a nucleus has p times the mass entries at least)
+      const bool hopeless = sums && nucleus && !closed && top_p * about > 1.5f * kNucleus;
+      const bool by_list = trusted && !hopeless && (nth <= S::kThreads || closed);
+      if (by_list) {
+        collect(sh, r, tau);
+        row_sync();
+        const int found = share_out(sh, sc, r.ctas, !greedy);
+        const uint64_t mass = sums ? all_chunks(sh, r.ctas) : 0;
+        if (found > 0)
+          settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, d);
+        if (settled) cut = sh.cut;
+        row_sync();  // (the peers have read the candidates)
+      } else if (trusted && sums && !nucleus) {
+        row_sync();
+        d = draw_fast(sh, r, sc, draw);
+        settled = d.token >= 0;
+      }
     }
-    if (!settled) {
-      for (int i = tid; i < 1024; i += kThreads) sh.table[i] = kExp2Table[i];
-      __syncthreads();
-      if (k > 0) cut = search<false>(sh, r, sc, cut, [&](uint64_t) { return uint64_t(k); });
-      if (nucleus) {
-        const Cut first_k = cut;
-        const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
-        cut = search<true>(sh, r, sc, first_k, [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); });
-        if (cut.key == first_k.key) cut.index = min(cut.index, first_k.index);
+    if constexpr (PART != kFirst) {
+      if (!settled) {
+        for (int i = tid; i < 1024; i += S::kThreads) sh.table[i] = kExp2Table[i];
+        __syncthreads();
+        if (k > 0) cut = search<false>(sh, r, sc, cut, [&](uint64_t) { return uint64_t(k); });
+        if (nucleus) {
+          const Cut first_k = cut;
+          const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
+          cut = search<true>(sh, r, sc, first_k, [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); });
+          if (cut.key == first_k.key) cut.index = min(cut.index, first_k.index);
+        }
+        if (least > 0) {
+          const uint32_t key = least_key(sh, sc, least);
+          if (key > cut.key) cut = {key, INT_MAX};
+        }
+        d = draw_exact(sh, r, sc, Kept{cut, cut.key == 0 ? -INFINITY : value_of(cut.key)}, draw);
       }
-      if (least > 0) {
-        const uint32_t key = least_key(sh, sc, least);
-        if (key > cut.key) cut = {key, INT_MAX};
-      }
-      d = draw_exact(sh, r, sc, Kept{cut, cut.key == 0 ? -INFINITY : value_of(cut.key)}, draw);
+    } else if (!settled) {
+      if (r.rank == 0 && tid == 0) a.tokens[b * a.tokens_b + n * a.tokens_n] = kLeft;
+      row_sync();
+      return;
     }
   }
   if (r.rank == 0 && tid == 0) {
@@ -1184,24 +1229,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const __gr
       }
     });
   }
-  row_sync();  // (no CTA leaves while its peers read its shared memory)
+  row_sync();  // (no CTA goes on while its peers read its shared memory)
 }
 
-// CTAs to a row: enough that all rows' together fill the GPU, each with enough of the row to be worth its exchanges.
-int sample_ctas(const SampleArgs& a) {
-  int ctas = tuned_cluster();
-  if (ctas > 0) return std::min(ctas, kMaxCtas);
-  ctas = 1;
-  while (ctas < kMaxCtas && 2ll * ctas * a.B * a.n <= 152 * kCtasPerSm && a.V / (2 * ctas) >= 2048) ctas *= 2;
-  return ctas;
+// A cluster for each row.
+template <Part PART, class T, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) sample_kernel(const __grid_constant__ SampleArgs a) {
+  __shared__ Shared<THREADS, PART != kFirst> sh;
+  Row<T> r;
+  r.ctas = int(cluster_size());
+  r.rank = int(cluster_rank());
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  sample_row<PART>(a, sh, r, blockIdx.x / r.ctas);
 }
 
-template <class T>
-cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
+// The rows that the first way left, by the clusters in turn.  (A row's mark goes only when all of its cluster's CTAs have
+// seen it: its token is written behind their first row_sync.)
+template <class T, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) sample_rest_kernel(const __grid_constant__ SampleArgs a) {
+  __shared__ Shared<THREADS, true> sh;
+  Row<T> r;
+  r.ctas = int(cluster_size());
+  r.rank = int(cluster_rank());
+  const long long rows = (long long)a.B * a.n, clusters = gridDim.x / r.ctas, mine = blockIdx.x / r.ctas;
+  const int lane = threadIdx.x % 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (long long q = 0; mine + q * clusters < rows; q += 32) {
+    const long long row = mine + (q + lane) * clusters;
+    bool left = false;
+    if (row < rows) {
+      const long long b = row / a.n;
+      left = __ldcg(a.tokens + b * a.tokens_b + (row - b * a.n) * a.tokens_n) == kLeft;
+    }
+    for (uint32_t some = __ballot_sync(0xffffffffu, left); some != 0; some &= some - 1)
+      sample_row<kRest>(a, sh, r, mine + (q + __ffs(some) - 1) * clusters);
+  }
+}
+
+constexpr int kAllThreads = 256, kAllCtas = 4, kFirstThreads = 128, kFirstCtas = 8;  // of a CTA; CTAs to an SM
+constexpr int kSms = 152;
+
+template <class Kernel>
+cudaError_t launch(Kernel kernel, const SampleArgs& a, long long clusters, int ctas, int threads, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int ctas = sample_ctas(a);
-  cfg.gridDim = dim3(unsigned((long long)a.B * a.n * ctas), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.gridDim = dim3(unsigned(clusters * ctas), 1, 1);
+  cfg.blockDim = dim3(unsigned(threads), 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1211,7 +1285,27 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <class T>
+cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
+  const long long rows = (long long)a.B * a.n;
+  const int tuned = std::min(tuned_cluster(), kMaxCtas);
+  // CTAs to a row: as many as all rows together leave room for, each with enough of the row to be worth its exchanges.
+  auto ctas_of = [&](int slots) {
+    if (tuned > 0) return tuned;
+    return int(std::clamp(std::min(slots / rows, (long long)a.V / 2048), 1ll, (long long)kMaxCtas));
+  };
+  if (rows <= kSms / 2)
+    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(kSms * kAllCtas), kAllThreads, s);
+  // Many rows: small CTAs whose chains of exchanges overlap, and the few rows that need it in general behind them, where
+  // large clusters have them at once.
+  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(kSms * kFirstCtas),
+                               kFirstThreads, s);
+  if (e != cudaSuccess) return e;
+  return launch(sample_rest_kernel<T, kAllThreads, kAllCtas>, a, std::min(rows, (long long)kSms * kAllCtas / kMaxCtas),
+                kMaxCtas, kAllThreads, s);
 }
 
 #ifdef ASV_CHECKED
@@ -1228,7 +1322,7 @@ cudaError_t launch_sample(const SampleArgs& args, int dtype, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   a.check_log = static_cast<uint32_t*>(log);
 #endif
-  return dtype == ASV_BF16 ? launch<bf16_t>(a, s) : launch<float>(a, s);
+  return dtype == ASV_BF16 ? launch_rows<bf16_t>(a, s) : launch_rows<float>(a, s);
 }
 
 }  // namespace asv

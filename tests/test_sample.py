@@ -384,3 +384,21 @@ def test_frequencies(m):
     seen = torch.bincount(got.tokens.flatten().cpu().long(), minlength=16).double()
     chi = float(((seen - rows * p) ** 2 / (rows * p)).sum())
     assert chi < 44.0    # 15 degrees of freedom: 44 is passed with probability 1e-4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [(77, 1), (40, 5), (1300, 1)])
+def test_many_rows(m, dtype, rows):
+    """More rows than are taken whole by one launch: settled by the first or left to the one behind it, mixed."""
+    B, n, V = *rows, 5003
+    x, u = _logits_of(B, n, V, "peaked", dtype, B), _draws(B, n, B)
+    flat = torch.arange(B) % 3 == 0
+    x[flat] = _logits_of(int(flat.sum()), n, V, "flat", dtype, 1)
+    x[1] = 0.5                                         # all equal
+    for T, k, p, least in ((1.0, 0, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (0.9, 30, 0.95, 0.02), (1.0, 1500, 0.9, 0.0), (0.0, 0, 1.0, 0.0)):
+        got = m.sample_tokens(x.cuda(), u.cuda(), temperature=T, top_k=k, top_p=p, min_p=least, probs=B == 77)
+        _compare(x, u, got, T, k, p, least, probs=B == 77)
+    x[5, 0, 17], x[6, 0, 3] = math.nan, math.inf
+    got = m.sample_tokens(x.cuda(), u.cuda(), top_p=0.9)
+    assert got.req_status.nonzero().flatten().tolist() == [5, 6] and int(got.tokens.min()) == -1
