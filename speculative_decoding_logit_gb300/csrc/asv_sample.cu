@@ -33,7 +33,7 @@ namespace {
 #include "exp2_table.inc"
 
 constexpr int kNucleus = 64;             // maxima of threads that a nucleus is first looked for above
-constexpr int kGroups = 16;              // groups of a thread's vectors, at most
+constexpr int kGroups = 20;              // groups of a thread's vectors, at most
 constexpr int kScan = 1024;              // groups that are read again, at most
 constexpr int kBins = 2048;
 constexpr int kMaxCtas = 8;
@@ -50,14 +50,18 @@ struct Cut {
   __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
 };
 
-// WHOLE: with what the general way needs.
-template <int THREADS, bool WHOLE>
+// What a launch does with its rows: all of it; the first way alone, leaving what that does not settle marked in the
+// tokens; or those rows in general.
+enum Part { kAll, kFirst, kRest };
+constexpr int kLeft = INT_MIN;
+
+template <int THREADS, Part PART>
 struct __align__(16) Shared {
   static constexpr int kThreads = THREADS, kWarps = THREADS / 32;
-  static constexpr int kList = 2 * THREADS;        // candidates that are compared with each other
+  static constexpr int kList = THREADS < 256 ? 256 : 512;  // candidates that are compared with each other
   union {                                          // one after the other
-    float group[(kGroups + 1) * THREADS];          // maxima of groups of a thread's vectors; of the row's ends
-    uint2 bins[WHOLE ? kBins : 1];                 // a histogram's 64-bit sums
+    float group[PART != kRest ? (kGroups + 1) * THREADS : 1];  // maxima of groups of a thread's vectors; of the row's ends
+    uint2 bins[PART != kFirst ? kBins : 1];        // a histogram's 64-bit sums
     struct {
       uint64_t place[kList];                       // the candidates' places in the order
       uint4 sorted[kList];                         // the candidates in order
@@ -68,7 +72,7 @@ struct __align__(16) Shared {
   uint2 own[kList];                                // this CTA's candidates: key, index
   float tops[THREADS];                             // the threads' maxima
   uint16_t scan[kScan];                            // groups whose vectors are read again
-  uint32_t table[WHOLE ? 1024 : 1];                // kExp2Table, where the whole row is weighed
+  uint32_t table[PART != kFirst ? 1024 : 1];       // kExp2Table, where the whole row is weighed
   uint64_t chunk[kWarps];                          // sums of the warps' runs
   uint64_t room[kWarps], room2[kWarps];
   uint64_t pick_before, pick_sum, total;
@@ -123,20 +127,24 @@ __device__ __forceinline__ float entry(const Row<T>& r, int i) {
 
 // A vector; entries that are not the row's are -inf.
 template <class T>
-__device__ __noinline__ uint4 edge_vector(const Row<T>& r, int v) {
+__device__ __forceinline__ uint4 edge_vector(const Row<T>& r, int v) {
   uint32_t w[4];
-  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80u : 0xff800000u;
+  const int i0 = v * kVec<T> - r.off;
+#pragma unroll
   for (int e = 0; e < 4; ++e) {
     if constexpr (sizeof(T) == 2) {
       uint32_t half[2];
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int i = v * 8 - r.off + 2 * e + h;
-        half[h] = i >= 0 && i < r.V ? r.base[r.off + i].bits : kNone;
+        const int i = i0 + 2 * e + h;
+        half[h] = 0xff80u;
+        if (i >= 0 && i < r.V) half[h] = r.base[r.off + i].bits;
       }
       w[e] = half[0] | (half[1] << 16);
     } else {
-      const int i = v * 4 - r.off + e;
-      w[e] = i >= 0 && i < r.V ? __float_as_uint(r.base[r.off + i]) : kNone;
+      const int i = i0 + e;
+      w[e] = 0xff800000u;
+      if (i >= 0 && i < r.V) w[e] = __float_as_uint(r.base[r.off + i]);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -147,25 +155,21 @@ __device__ __forceinline__ uint4 load_vector(const Row<T>& r, int v) {
   return r.whole(v) ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : edge_vector(r, v);
 }
 
-// f(vector, number) for the warp's vectors, kAhead of them a lane in flight.
+// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; one instance of f.
 template <class T, class F>
-__device__ __forceinline__ void stream(const Row<T>& r, F f) {
-  const int lane = threadIdx.x % 32;
-  const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;  // whole vectors
-  const uint4* p = reinterpret_cast<const uint4*>(r.base);
-  const int end = min(r.v1, w1);
-  int v = max(r.v0, w0) + lane;
-  for (; v + 32 * (kAhead - 1) < end; v += 32 * kAhead) {
-    uint4 w[kAhead];
+__device__ __forceinline__ void stream(const Row<T>& r, int v0, int v1, F f) {
+  int v = v0 + int(threadIdx.x % 32);
+  uint4 w[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) w[i] = __ldg(p + v + 32 * i);
+  for (int i = 0; i < kAhead; ++i) w[i] = v + 32 * i < v1 ? load_vector(r, v + 32 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (; v < v1; v += 32) {
+    const uint4 now = w[0];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) f(w[i], v + 32 * i);
+    for (int i = 1; i < kAhead; ++i) w[i - 1] = w[i];
+    if (v + 32 * kAhead < v1) w[kAhead - 1] = load_vector(r, v + 32 * kAhead);
+    f(now, v);
   }
-  for (; v < end; v += 32) f(__ldg(p + v), v);
-  // the row's ends
-  if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) f(edge_vector(r, 0), 0);
-  if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) f(edge_vector(r, w1), w1);
 }
 
 // Keys in the order of the values (equal for -0 and 0); 0 is no value's.
@@ -247,7 +251,7 @@ __device__ __forceinline__ Scale scale_of(float M, float c, float c_lo) {
   return sc;
 }
 
-__device__ __noinline__ uint64_t weight(float x, const Scale& sc, const uint32_t* table) { return units_of(x, sc, table); }
+__device__ __noinline__ uint64_t weight(float x, const Scale sc, const uint32_t* table) { return units_of(x, sc, table); }
 
 // Whether a vector whose largest entry is x has weights that count.
 __device__ __forceinline__ bool weighs(float x, const Scale& sc) { return (x - sc.M) * sc.c > -float(kSampleUnitBits + 3); }
@@ -411,7 +415,7 @@ struct Groups {
 // The CTA's entries from tau on, out of the groups of vectors whose maximum reaches it, to sh.own (those that have
 // room; sh.n_own counts them all).
 template <class S, class T>
-__device__ __noinline__ void collect(S& sh, const Row<T>& r, float tau) {
+__device__ __noinline__ void collect(S& sh, const Row<T> r, float tau) {
   const int tid = threadIdx.x;
   if (tid == 0) sh.n_scan = sh.n_own = 0;
   __syncthreads();
@@ -429,16 +433,16 @@ __device__ __noinline__ void collect(S& sh, const Row<T>& r, float tau) {
     return;
   }
   auto take = [&](const uint4& w, int v) {
-    if (!(vector_max(w, static_cast<T*>(nullptr)) >= tau)) return;
     float x[kVec<T>];
     unpack(w, x);
+    uint32_t some = 0;
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) {
-      const int index = v * kVec<T> - r.off + e;
-      if (x[e] >= tau && index >= 0 && index < r.V) {
-        const int to = atomicAdd(&sh.n_own, 1);
-        if (to < S::kList) sh.own[to] = make_uint2(key_of(x[e]), uint32_t(index));
-      }
+    for (int e = 0; e < kVec<T>; ++e) some |= (x[e] >= tau ? 1u : 0u) << e;
+    for (; some != 0; some &= some - 1) {
+      const int e = __ffs(some) - 1, index = v * kVec<T> - r.off + e;
+      if (index < 0 || index >= r.V) continue;
+      const int to = atomicAdd(&sh.n_own, 1);
+      if (to < S::kList) sh.own[to] = make_uint2(key_of(entry_of<T>(w, e)), uint32_t(index));
     }
   };
   const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;
@@ -451,24 +455,29 @@ __device__ __noinline__ void collect(S& sh, const Row<T>& r, float tau) {
     return v < min(r.run_end(r.rank, warp), w1) ? v : -1;
   };
   const uint4* p = reinterpret_cast<const uint4*>(r.base);
-  for (int x = tid; x < n * per_group; x += 2 * S::kThreads) {
-    const int a = vector_at(x), b = vector_at(x + S::kThreads);
-    const uint4 none = make_uint4(0, 0, 0, 0), u = a >= 0 ? __ldg(p + a) : none, v = b >= 0 ? __ldg(p + b) : none;
-    if (a >= 0) take(u, a);
-    if (b >= 0) take(v, b);
+  for (int x = tid; x < n * per_group; x += kAhead * S::kThreads) {
+    int v[kAhead];
+    uint4 w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      v[i] = vector_at(x + i * S::kThreads);
+      w[i] = v[i] >= 0 ? __ldg(p + v[i]) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (v[i] >= 0) take(w[i], v[i]);
   }
-  // the row's ends (as in stream)
+  // the row's ends (as they were streamed)
   if (sh.group[kGroups * S::kThreads + tid] >= tau) {
-    const int lane = tid % 32;
-    if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) take(edge_vector(r, 0), 0);
-    if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) take(edge_vector(r, w1), w1);
+    const int edge = tid % 32 == 0 ? 0 : w1;
+    take(edge_vector(r, edge), edge);
   }
 }
 
 // The row's candidates of all CTAs, with their weights (kOne each without), to sh.list; their number, or -1 if there is no
 // room.
 template <class S>
-__device__ __noinline__ int share_out(S& sh, const Scale& sc, int ctas, bool weigh) {
+__device__ __noinline__ int share_out(S& sh, const Scale sc, int ctas, bool weigh) {
   const int lane = threadIdx.x % 32;
   const int own = lane < ctas ? int(ld_peer_u32(&sh.n_own, lane)) : 0;
   int upto = own;
@@ -533,11 +542,19 @@ __device__ __noinline__ void sort_list(S& sh, int n) {
     if (tid % g == 0 && e < n) sh.sorted[rank] = sh.list[e];
   }
   __syncthreads();
-  static_assert(S::kList == 2 * S::kThreads);
-  const uint64_t a = 2 * tid < n ? weight_in(sh.sorted[2 * tid]) : 0, b = 2 * tid + 1 < n ? weight_in(sh.sorted[2 * tid + 1]) : 0;
-  const uint64_t upto = block_scan(a + b, sh.room);
-  sh.before[2 * tid] = upto - a - b;
-  sh.before[2 * tid + 1] = upto - b;
+  constexpr int kEach = S::kList / S::kThreads;
+  uint64_t w[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    w[i] = kEach * tid + i < n ? weight_in(sh.sorted[kEach * tid + i]) : 0;
+    sum += w[i];
+  }
+  uint64_t upto = block_scan(sum, sh.room) - sum;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    sh.before[kEach * tid + i] = upto;
+    upto += w[i];
+  }
   __syncthreads();
 }
 
@@ -640,36 +657,61 @@ __device__ __forceinline__ uint64_t find_run(S& sh, const Row<T>& r, uint64_t dr
 }
 
 // The entry of run sh.pick that `at` falls into: to sh.found of the CTA that owns the run (-1: within `margin` of the
-// entry's ends, or in none), read from there by all.  sum_of(v0, v1): a warp's sum of the entries of vectors [v0, v1), f(x,
-// index) one entry's.
-template <class S, class T, class Sum, class F>
-__device__ __forceinline__ int find_entry(S& sh, const Row<T>& r, uint64_t at, uint64_t margin, Sum sum_of, F f) {
+// entry's ends, or in none), read from there by all.  The run is shared out to the warps, the part that `at` falls into to
+// the threads, a thread's vectors entry by entry.  run_sum(v0, v1): a warp's sum of the entries of vectors [v0, v1);
+// vector_sum(vector, number); f(x, index): an entry's.
+template <class S, class T, class Run, class Vector, class F>
+__device__ __forceinline__ int find_entry(S& sh, const Row<T>& r, uint64_t at, uint64_t margin, Run run_sum,
+                                          Vector vector_sum, F f) {
   const int tid = threadIdx.x, warp = tid / 32;
-  if (tid == 0) sh.found = -1;
+  if (tid == 0) {
+    sh.found = -1;
+    sh.pick_sum = 0;
+  }
   __syncthreads();
   const int pick = sh.pick, owner = pick / S::kWarps;
   if (r.rank == owner) {
-    // the part of the run that a warp has
     const int v0 = r.run_start(owner, pick % S::kWarps), v1 = r.run_end(owner, pick % S::kWarps);
-    const int each = (v1 - v0 + S::kWarps - 1) / S::kWarps;
     uint64_t before = sh.pick_before;
-    const uint64_t own = sum_of(min(v0 + warp * each, v1), min(v0 + (warp + 1) * each, v1));
+    const int each = (v1 - v0 + S::kWarps - 1) / S::kWarps;
+    const uint64_t own = run_sum(min(v0 + warp * each, v1), min(v0 + (warp + 1) * each, v1));
     if (tid % 32 == 0) sh.room2[warp] = own;
     __syncthreads();
     int part = 0;
     for (; part < S::kWarps - 1 && before + sh.room2[part] <= at; ++part) before += sh.room2[part];
-    // entry by entry, one a thread
-    const int i0 = max(min(v0 + part * each, v1) * kVec<T> - r.off, 0);
-    const int i1 = min(min(v0 + (part + 1) * each, v1) * kVec<T> - r.off, r.V);
-    for (int first = i0; first < i1 && before <= at; first += S::kThreads) {
-      const int i = first + tid;
-      const uint64_t own = i < i1 ? f(entry(r, i), i) : 0;
-      const uint64_t upto = before + block_scan(own, sh.room);
-      // (before the row's first weight there is nothing to be off by)
-      if (upto > at && upto - own <= at && (upto == own || at - (upto - own) >= margin) && upto - at > margin) sh.found = i;
-      if (tid == S::kThreads - 1) sh.pick_sum = upto;
-      __syncthreads();
+    const int p0 = min(v0 + part * each, v1), p1 = min(p0 + each, v1), few = (p1 - p0 + S::kThreads - 1) / S::kThreads;
+    {
+      const int a = min(p0 + tid * few, p1), b = min(a + few, p1);
+      uint64_t sum = 0;
+      for (int v = a; v < b; v += 2) {
+        const bool two = v + 1 < b;
+        const uint4 w = load_vector(r, v), x = two ? load_vector(r, v + 1) : w;
+        sum += vector_sum(w, v);
+        if (two) sum += vector_sum(x, v + 1);
+      }
+      const uint64_t upto = before + block_scan(sum, sh.room);
+      if (upto > at && upto - sum <= at) {
+        sh.pick_sum = upto - sum;
+        sh.pick = a;
+        sh.found = -2;
+      }
+    }
+    __syncthreads();
+    if (sh.found == -2) {
       before = sh.pick_sum;
+      const int a = sh.pick, i0 = max(a * kVec<T> - r.off, 0), i1 = min(min(a + few, p1) * kVec<T> - r.off, r.V);
+      __syncthreads();
+      if (tid == 0) sh.found = -1;
+      for (int first = i0; first < i1 && before <= at; first += S::kThreads) {
+        const int i = first + tid;
+        const uint64_t own = i < i1 ? f(entry(r, i), i) : 0;
+        const uint64_t upto = before + block_scan(own, sh.room);
+        // (before the row's first weight there is nothing to be off by)
+        if (upto > at && upto - own <= at && (upto == own || at - (upto - own) >= margin) && upto - at > margin) sh.found = i;
+        if (tid == S::kThreads - 1) sh.pick_sum = upto;
+        __syncthreads();
+        before = sh.pick_sum;
+      }
     }
   }
   row_sync();
@@ -678,38 +720,22 @@ __device__ __forceinline__ int find_entry(S& sh, const Row<T>& r, uint64_t at, u
   return found;
 }
 
-// f(vector, number) for a warp's vectors [v0, v1), whole or not.
-template <class T, class F>
-__device__ __forceinline__ void few(const Row<T>& r, int v0, int v1, F f) {
-  const uint4* p = reinterpret_cast<const uint4*>(r.base);
-  const int w0 = max(v0, r.off > 0 ? 1 : 0), w1 = min(v1, (r.off + r.V) / kVec<T>), lane = threadIdx.x % 32;  // whole ones
-  for (int v = w0 + lane; v < w1; v += 32 * kAhead) {
-    uint4 w[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (v + 32 * i < w1) w[i] = __ldg(p + v + 32 * i);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (v + 32 * i < w1) f(w[i], v + 32 * i);
-  }
-  if (lane == 0 && v0 < min(w0, v1)) f(edge_vector(r, v0), v0);
-  if (lane == 1 && w1 < v1 && w1 >= w0) f(edge_vector(r, w1), w1);
-}
-
 // The index of the n-th entry with this key (n >= 1).
 template <class S, class T>
-__device__ __noinline__ int nth_equal(S& sh, const Row<T>& r, uint32_t key, uint64_t n) {
+__device__ __noinline__ int nth_equal(S& sh, const Row<T> r, uint32_t key, uint64_t n) {
   uint64_t own = 0;
   auto count = [&](const uint4& w, int v) {
     float x[kVec<T>];
     unpack(w, x);
+    uint32_t n = 0;
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e) {
       const int i = v * kVec<T> - r.off + e;
-      own += key_of(x[e]) == key && i >= 0 && i < r.V;
+      n += key_of(x[e]) == key && i >= 0 && i < r.V;
     }
+    return uint64_t(n);
   };
-  stream(r, count);
+  stream(r, r.v0, r.v1, [&](const uint4& w, int v) { own += count(w, v); });
   own = warp_sum(own);
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
   row_sync();
@@ -727,10 +753,10 @@ __device__ __noinline__ int nth_equal(S& sh, const Row<T>& r, uint32_t key, uint
       sh, r, n - 1, 0,
       [&](int v0, int v1) {
         own = 0;
-        few(r, v0, v1, count);
+        stream(r, v0, v1, [&](const uint4& w, int v) { own += count(w, v); });
         return warp_sum(own);
       },
-      [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); });
+      count, [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); });
 }
 
 // The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
@@ -738,7 +764,7 @@ __device__ __noinline__ int nth_equal(S& sh, const Row<T>& r, uint32_t key, uint
 // range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
 // on.  The bins are added up a part by each CTA.
 template <bool MASS, class S, class T, class G>
-__device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, const Cut within, G target_of) {
+__device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const Cut within, G target_of) {
   const int tid = threadIdx.x, lane = tid % 32;
   // bins of equal width down to weights of 2^-24, the last takes the rest (7 % of a weight's width each: of 152 thousand
   // flat entries 250 at most fall into one)
@@ -765,7 +791,7 @@ __device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, cons
     // what the entries of the bracket do
     auto each_entry = [&](auto f) {
       const float least = value_of(lo), most = value_of(hi);
-      stream(r, [&](const uint4& w, int v) {
+      stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
         float x[kVec<T>];
         unpack(w, x);
         uint32_t some = 0;
@@ -801,7 +827,8 @@ __device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, cons
     for (int i = tid; i < kBins; i += S::kThreads) sh.bins[i] = make_uint2(0, 0);
     __syncthreads();
     if (level == 0) {
-      stream(r, [&](const uint4& w, int v) {
+      uint64_t rest = 0;  // the last bin's, which most entries of a peaked row fall into
+      stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
         float x[kVec<T>];
         unpack(w, x);
         uint64_t m[kVec<T>];
@@ -814,9 +841,15 @@ __device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, cons
         for (int e = 0; e < kVec<T>; ++e) {
           const int i = v * kVec<T> - r.off + e;
           if constexpr (!MASS) m[e] = i >= 0 && i < r.V;
-          if (m[e] != 0 && (all || within.keeps(key_of(x[e]), i))) add(bin_of(x[e]), m[e]);
+          if (m[e] != 0 && (all || within.keeps(key_of(x[e]), i))) {
+            const int bin = bin_of(x[e]);
+            if (bin < kBins - 1) add(bin, m[e]);
+            else rest += m[e];
+          }
         }
       });
+      rest = warp_sum(rest);
+      if (lane == 0 && rest != 0) add(kBins - 1, rest);
     } else {
       each_entry([&](float x, uint32_t key, int) {
         const uint64_t m = MASS ? weight(x, sc, sh.table) : 1;
@@ -828,17 +861,17 @@ __device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, cons
     uint64_t sum = 0;
     for (int i = part0 + tid; i < part1; i += S::kThreads) {
       uint64_t own = 0;
-      for (int c = 0; c < r.ctas; ++c) own += ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.bins + i), c);
+#pragma unroll
+      for (int c = 0; c < kMaxCtas; ++c)
+        if (c < r.ctas) own += ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.bins + i), c);
       *reinterpret_cast<uint64_t*>(sh.bins + i) = own;
       sum += own;
     }
-    sum = warp_sum(sum);
-    if (lane == 0) sh.chunk[tid / 32] = sum;
+    sum = block_scan(sum, sh.room);
+    if (tid == S::kThreads - 1) sh.total = sum;
     if (tid == 0) sh.pick = -1;
     row_sync();
-    uint64_t mine = 0;
-    if (lane < r.ctas)
-      for (int i = 0; i < S::kWarps; ++i) mine += ld_peer_u64(sh.chunk + i, lane);
+    const uint64_t mine = lane < r.ctas ? ld_peer_u64(&sh.total, lane) : 0;
     uint64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < kMaxCtas; d *= 2) {
@@ -895,7 +928,7 @@ __device__ __noinline__ Cut search(S& sh, const Row<T>& r, const Scale& sc, cons
 
 // The smallest key whose weight is at least `least`, by a warp: 32 candidates at a time.
 template <class S>
-__device__ __noinline__ uint32_t least_key(S& sh, const Scale& sc, uint64_t least) {
+__device__ __noinline__ uint32_t least_key(S& sh, const Scale sc, uint64_t least) {
   uint32_t lo = 1, hi = key_of(sc.M);
   __syncthreads();  // (sh.cut's last readers are done)
   if (threadIdx.x < 32) {
@@ -919,9 +952,40 @@ struct Kept {
   __device__ __forceinline__ bool operator()(float x, int i) const { return x > value || (x == value && i <= cut.index); }
 };
 
-// A draw from the whole row by the warps' fast sums (sh.chunk, behind a row_sync).  A token < 0: too near a border to say.
+// The sum of a vector's kept entries.
+template <class T>
+__device__ __forceinline__ uint64_t kept_sum(const uint4& w, int v, const Row<T>& r, const Scale& sc, const Kept& keep,
+                                             const uint32_t* table) {
+  const float top = vector_max(w, static_cast<T*>(nullptr));
+  if (top < keep.value || !weighs(top, sc)) return 0;
+  float x[kVec<T>];
+  unpack(w, x);
+  uint64_t sum = 0;
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e) {
+    const uint64_t u = units_of(x[e], sc, table);
+    sum += keep(x[e], v * kVec<T> - r.off + e) ? u : 0;
+  }
+  return sum;
+}
+
+// The same by fast sums.
+template <class T>
+__device__ __forceinline__ void add_kept(Partial& s, const uint4& w, int v, const Row<T>& r, const Scale& sc, const Kept& keep) {
+  const float top = vector_max(w, static_cast<T*>(nullptr));
+  if (top < keep.value) return;
+  float x[kVec<T>];
+  unpack(w, x);
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e)
+    if (!keep(x[e], v * kVec<T> - r.off + e)) x[e] = -INFINITY;
+  add_weights(s, x, top, sc.c);
+}
+
+// A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync).  A token < 0: too near a
+// border to say.
 template <class S, class T>
-__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T>& r, const Scale& sc, uint64_t draw) {
+__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, const Kept keep, uint64_t draw) {
   const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
@@ -935,34 +999,30 @@ __device__ __noinline__ Drawn draw_fast(S& sh, const Row<T>& r, const Scale& sc,
       sh, r, at, margin,
       [&](int v0, int v1) {
         Partial s;
-        few(r, v0, v1, [&](const uint4& w, int) {
-          float x[kVec<T>];
-          unpack(w, x);
-          add_weights(s, x, vector_max(w, static_cast<T*>(nullptr)), sc.c);
-        });
+        stream(r, v0, v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
         return warp_sum(units_of_sum(s, sc));
       },
-      [&](float x, int) { return weight(x, sc, kExp2Table); });
+      [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, kExp2Table); },
+      [&](float x, int i) { return keep(x, i) ? weight(x, sc, kExp2Table) : uint64_t(0); });
   d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, kExp2Table) : 0;
   return d;
 }
 
+// The warps' fast sums of the kept entries, to sh.chunk.
+template <class S, class T>
+__device__ __noinline__ void fast_sums(S& sh, const Row<T> r, const Scale sc, const Kept keep) {
+  Partial s;
+  stream(r, r.v0, r.v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
+  const uint64_t w = warp_sum(units_of_sum(s, sc));
+  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = w;
+}
+
 // A draw from the kept entries by exact sums.
 template <class S, class T>
-__device__ __noinline__ Drawn draw_exact(S& sh, const Row<T>& r, const Scale& sc, const Kept& keep, uint64_t draw) {
+__device__ __noinline__ Drawn draw_exact(S& sh, const Row<T> r, const Scale sc, const Kept keep, uint64_t draw) {
   uint64_t own = 0;
-  auto add = [&](const uint4& w, int v) {
-    const float top = vector_max(w, static_cast<T*>(nullptr));
-    if (top < keep.value || !weighs(top, sc)) return;
-    float x[kVec<T>];
-    unpack(w, x);
-#pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) {
-      const uint64_t u = units_of(x[e], sc, sh.table);
-      own += keep(x[e], v * kVec<T> - r.off + e) ? u : 0;
-    }
-  };
-  stream(r, add);
+  auto sum = [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, sh.table); };
+  stream(r, r.v0, r.v1, [&](const uint4& w, int v) { own += sum(w, v); });
   own = warp_sum(own);
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
   row_sync();
@@ -974,20 +1034,15 @@ __device__ __noinline__ Drawn draw_exact(S& sh, const Row<T>& r, const Scale& sc
       sh, r, at, 0,
       [&](int v0, int v1) {
         own = 0;
-        few(r, v0, v1, add);
+        stream(r, v0, v1, [&](const uint4& w, int v) { own += sum(w, v); });
         return warp_sum(own);
       },
-      [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
+      sum, [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
   d.weight = weight(entry(r, d.token), sc, sh.table);
   return d;
 }
 
 // ------------------------------------------------------------------ the kernels
-
-// What a launch does with its rows: all of it; the first way alone, leaving what that does not settle marked in the
-// tokens; or those rows in general.
-enum Part { kAll, kFirst, kRest };
-constexpr int kLeft = INT_MIN;
 
 template <Part PART, class S, class T>
 __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r, long long row) {
@@ -1045,33 +1100,24 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>, end = min(r.v1, w1);  // whole vectors
     const uint4* p = reinterpret_cast<const uint4*>(r.base);
     int v = max(r.v0, w0) + lane;
-    for (; v + 32 * (kFirstAhead - 1) < end; v += 32 * kFirstAhead) {
+    for (; v - lane < end; v += 32 * kFirstAhead) {
+      constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
       uint4 w[kFirstAhead];
 #pragma unroll
-      for (int i = 0; i < kFirstAhead; ++i) w[i] = __ldg(p + v + 32 * i);
+      for (int i = 0; i < kFirstAhead; ++i)
+        w[i] = v + 32 * i < end ? __ldg(p + v + 32 * i) : make_uint4(kNone, kNone, kNone, kNone);
 #pragma unroll
       for (int i = 0; i < kFirstAhead; ++i) most = max_nan(most, one(w[i]));
       left -= kFirstAhead;
       if (left == 0) close();
     }
-    if (v < end) {  // (the last ones, together too)
-      uint4 w[kFirstAhead - 1];
-#pragma unroll
-      for (int i = 0; i < kFirstAhead - 1; ++i)
-        if (v + 32 * i < end) w[i] = __ldg(p + v + 32 * i);
-#pragma unroll
-      for (int i = 0; i < kFirstAhead - 1; ++i)
-        if (v + 32 * i < end) most = max_nan(most, one(w[i]));
-      --left;
-    }
     while (g < kGroups) close();
-    // the row's ends (as in stream)
-    if (lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0) {
-      most = one(edge_vector(r, 0));
-      --left;
-    }
-    if (lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1) {
-      most = one(edge_vector(r, w1));
+    // the row's ends
+    const int edge = lane == 0 && r.v0 == 0 && w0 == 1 && r.v1 > 0                                  ? 0
+                     : lane == 1 && w1 >= w0 && w1 < r.vectors && w1 >= r.v0 && w1 < r.v1 ? w1
+                                                                                            : -1;
+    if (edge >= 0) {
+      most = one(edge_vector(r, edge));
       --left;
     }
     close();
@@ -1090,7 +1136,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   bool bad = __syncthreads_or(!(top < INFINITY));
   if (warp == 0) {
     float least_top = -INFINITY, most = -INFINITY;
-    nth_largest(sh, min(nth, S::kThreads), least_top, most);
+    nth_largest(sh, PART == kRest ? 1 : min(nth, S::kThreads), least_top, most);
     float all = 0.0f;
     if (sums)
       for (int w = 0; w < S::kWarps; ++w) all += sh.sums[w].y * ex2_approx((sh.sums[w].x - most) * c);
@@ -1165,7 +1211,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         row_sync();  // (the peers have read the candidates)
       } else if (trusted && sums && !nucleus) {
         row_sync();
-        d = draw_fast(sh, r, sc, draw);
+        d = draw_fast(sh, r, sc, Kept{cut, -INFINITY}, draw);
         settled = d.token >= 0;
       }
     }
@@ -1184,7 +1230,14 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
           const uint32_t key = least_key(sh, sc, least);
           if (key > cut.key) cut = {key, INT_MAX};
         }
-        d = draw_exact(sh, r, sc, Kept{cut, cut.key == 0 ? -INFINITY : value_of(cut.key)}, draw);
+        const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
+        d.token = -1;
+        if (cut.key != 0 && fabsf(sc.M * sc.c) < kFastRange - 128.0f) {
+          fast_sums(sh, r, sc, keep);
+          row_sync();
+          d = draw_fast(sh, r, sc, keep, draw);
+        }
+        if (d.token < 0) d = draw_exact(sh, r, sc, keep, draw);
       }
     } else if (!settled) {
       if (r.rank == 0 && tid == 0) a.tokens[b * a.tokens_b + n * a.tokens_n] = kLeft;
@@ -1208,7 +1261,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
     const bool vectors = (reinterpret_cast<uintptr_t>(to) / 4 + kVec<T> - r.off) % 4 == 0;
     const float far = -200.0f / sc.c;  // (what is further below has no weight)
-    stream(r, [&](const uint4& w, int v) {
+    stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
       float x[kVec<T>], p[kVec<T>];
       unpack(w, x);
       const int i0 = v * kVec<T> - r.off;
@@ -1235,7 +1288,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
 // A cluster for each row.
 template <Part PART, class T, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) sample_kernel(const __grid_constant__ SampleArgs a) {
-  __shared__ Shared<THREADS, PART != kFirst> sh;
+  __shared__ Shared<THREADS, PART> sh;
   Row<T> r;
   r.ctas = int(cluster_size());
   r.rank = int(cluster_rank());
@@ -1248,7 +1301,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) sample_kernel(const __grid_cons
 // seen it: its token is written behind their first row_sync.)
 template <class T, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) sample_rest_kernel(const __grid_constant__ SampleArgs a) {
-  __shared__ Shared<THREADS, true> sh;
+  __shared__ Shared<THREADS, kRest> sh;
   Row<T> r;
   r.ctas = int(cluster_size());
   r.rank = int(cluster_rank());
@@ -1269,6 +1322,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) sample_rest_kernel(const __grid
 }
 
 constexpr int kAllThreads = 256, kAllCtas = 4, kFirstThreads = 128, kFirstCtas = 8;  // of a CTA; CTAs to an SM
+constexpr int kRestThreads = 512, kRestCtas = 2;
 constexpr int kSms = 152;
 
 template <class Kernel>
@@ -1304,8 +1358,8 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
   const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(kSms * kFirstCtas),
                                kFirstThreads, s);
   if (e != cudaSuccess) return e;
-  return launch(sample_rest_kernel<T, kAllThreads, kAllCtas>, a, std::min(rows, (long long)kSms * kAllCtas / kMaxCtas),
-                kMaxCtas, kAllThreads, s);
+  return launch(sample_rest_kernel<T, kRestThreads, kRestCtas>, a, std::min(rows, (long long)kSms * kRestCtas / kMaxCtas),
+                kMaxCtas, kRestThreads, s);
 }
 
 #ifdef ASV_CHECKED
