@@ -47,7 +47,7 @@ constexpr int kVec = 16 / int(sizeof(T));  // entries of a 16-byte vector
 struct Cut {
   uint32_t key;   // entries with larger keys are kept, and those of this key up to the index
   int index;
-  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
+  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return (k > key) | ((k == key) & (i <= index)); }
 };
 
 // What a launch does with its rows: all of it; the first way alone, leaving what that does not settle marked in the
@@ -155,20 +155,35 @@ __device__ __forceinline__ uint4 load_vector(const Row<T>& r, int v) {
   return r.whole(v) ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : edge_vector(r, v);
 }
 
-// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; one instance of f.
+// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; the loop has eight entries' worth of f.
 template <class T, class F>
 __device__ __forceinline__ void stream(const Row<T>& r, int v0, int v1, F f) {
+  constexpr int kEach = 8 / kVec<T>;
+  const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;  // whole ones
+  const uint4* p = reinterpret_cast<const uint4*>(r.base);
   int v = v0 + int(threadIdx.x % 32);
+  auto load = [&](int v) { return (v >= w0) & (v < w1) ? __ldg(p + v) : edge_vector(r, v); };
   uint4 w[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) w[i] = v + 32 * i < v1 ? load_vector(r, v + 32 * i) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kAhead; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (v + 32 * i < v1) w[i] = load(v + 32 * i);
+  }
 #pragma unroll 1
-  for (; v < v1; v += 32) {
-    const uint4 now = w[0];
+  for (; v < v1; v += 32 * kEach) {
+    uint4 now[kEach];
 #pragma unroll
-    for (int i = 1; i < kAhead; ++i) w[i - 1] = w[i];
-    if (v + 32 * kAhead < v1) w[kAhead - 1] = load_vector(r, v + 32 * kAhead);
-    f(now, v);
+    for (int i = 0; i < kEach; ++i) now[i] = w[i];
+#pragma unroll
+    for (int i = kEach; i < kAhead; ++i) w[i - kEach] = w[i];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int next = v + 32 * (kAhead + i);
+      if (next < v1) w[kAhead - kEach + i] = load(next);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (i == 0 || v + 32 * i < v1) f(now[i], v + 32 * i);
   }
 }
 
@@ -796,7 +811,7 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
         unpack(w, x);
         uint32_t some = 0;
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) some |= (x[e] >= least && x[e] <= most ? 1u : 0u) << e;
+        for (int e = 0; e < kVec<T>; ++e) some |= uint32_t((x[e] >= least) & (x[e] <= most)) << e;
         for (; some != 0; some &= some - 1) {
           const int e = __ffs(some) - 1, i = v * kVec<T> - r.off + e;
           const float y = entry_of<T>(w, e);
@@ -829,23 +844,19 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
     if (level == 0) {
       uint64_t rest = 0;  // the last bin's, which most entries of a peaked row fall into
       stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
+        if (MASS && !weighs(vector_max(w, static_cast<T*>(nullptr)), sc)) return;
         float x[kVec<T>];
         unpack(w, x);
-        uint64_t m[kVec<T>];
-        if constexpr (MASS) {
-          if (!weighs(vector_max(w, static_cast<T*>(nullptr)), sc)) return;
-#pragma unroll
-          for (int e = 0; e < kVec<T>; ++e) m[e] = units_of(x[e], sc, sh.table);
-        }
 #pragma unroll
         for (int e = 0; e < kVec<T>; ++e) {
           const int i = v * kVec<T> - r.off + e;
-          if constexpr (!MASS) m[e] = i >= 0 && i < r.V;
-          if (m[e] != 0 && (all || within.keeps(key_of(x[e]), i))) {
-            const int bin = bin_of(x[e]);
-            if (bin < kBins - 1) add(bin, m[e]);
-            else rest += m[e];
-          }
+          uint64_t m;
+          if constexpr (MASS) m = units_of(x[e], sc, sh.table);
+          else m = (i >= 0) & (i < r.V);
+          if (!all) m = within.keeps(key_of(x[e]), i) ? m : 0;
+          const int bin = m != 0 ? bin_of(x[e]) : kBins - 1;
+          if (bin < kBins - 1) add(bin, m);
+          else rest += m;
         }
       });
       rest = warp_sum(rest);
@@ -949,7 +960,7 @@ __device__ __noinline__ uint32_t least_key(S& sh, const Scale sc, uint64_t least
 struct Kept {
   Cut cut;
   float value;  // the cut's
-  __device__ __forceinline__ bool operator()(float x, int i) const { return x > value || (x == value && i <= cut.index); }
+  __device__ __forceinline__ bool operator()(float x, int i) const { return (x > value) | ((x == value) & (i <= cut.index)); }
 };
 
 // The sum of a vector's kept entries.
