@@ -38,7 +38,7 @@ constexpr int kScan = 1024;              // groups that are read again, at most
 constexpr int kBins = 2048;
 constexpr int kMaxCtas = 8;
 constexpr int kAhead = 4;                // vectors a lane has in flight
-constexpr int kFirstAhead = 8;           // the same, when the row streams from HBM
+constexpr int kMostAhead = 8;            // the same at most, when the row streams from HBM
 constexpr uint64_t kOne = uint64_t(1) << kSampleUnitBits;  // the largest weight
 
 template <class T>
@@ -78,6 +78,7 @@ struct __align__(16) Shared {
   uint64_t pick_before, pick_sum, total;
   float2 sums[kWarps];                             // the warps' maxima and fast sums next to them
   float4 ends;                                     // of the CTA: maximum, bound of the candidates, whether it is bad, sum
+  float lead;                                      // the sum of threads' maxima from the bound on
   Cut cut;
   int n_scan, n_own, found, pick;
 };
@@ -120,6 +121,21 @@ __device__ __forceinline__ float entry_of(const uint4& w, int e) {
   return sizeof(T) == 4 ? __uint_as_float(x) : e % 2 ? bf16_hi(x) : bf16_lo(x);
 }
 
+// f(entries e and e + 1 of a vector, e), two at a time: a loop, whose instructions are fetched once.
+template <class T, class F>
+__device__ __forceinline__ void pairs(uint4 w, F f) {
+#pragma unroll 1
+  for (int e = 0; e < kVec<T>; e += 2) {
+    if constexpr (sizeof(T) == 2) {
+      f(bf16_lo(w.x), bf16_hi(w.x), e);
+      w = make_uint4(w.y, w.z, w.w, 0);
+    } else {
+      f(__uint_as_float(w.x), __uint_as_float(w.y), e);
+      w = make_uint4(w.z, w.w, 0, 0);
+    }
+  }
+}
+
 template <class T>
 __device__ __forceinline__ float entry(const Row<T>& r, int i) {
   return widen(r.base[r.off + i]);
@@ -128,26 +144,19 @@ __device__ __forceinline__ float entry(const Row<T>& r, int i) {
 // A vector; entries that are not the row's are -inf.
 template <class T>
 __device__ __forceinline__ uint4 edge_vector(const Row<T>& r, int v) {
-  uint32_t w[4];
-  const int i0 = v * kVec<T> - r.off;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t half[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = i0 + 2 * e + h;
-        half[h] = 0xff80u;
-        if (i >= 0 && i < r.V) half[h] = r.base[r.off + i].bits;
-      }
-      w[e] = half[0] | (half[1] << 16);
-    } else {
-      const int i = i0 + e;
-      w[e] = 0xff800000u;
-      if (i >= 0 && i < r.V) w[e] = __float_as_uint(r.base[r.off + i]);
-    }
+  constexpr int kBits = 8 * int(sizeof(T));
+  uint4 w = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int e = kVec<T> - 1; e >= 0; --e) {  // the last entry first, moved up by those before it
+    const int i = v * kVec<T> - r.off + e;
+    uint32_t x = kBits == 16 ? 0xff80u : 0xff800000u;
+    if (i >= 0 && i < r.V) memcpy(&x, r.base + r.off + i, sizeof(T));
+    if constexpr (kBits == 16)
+      w = make_uint4((w.x << 16) | x, __funnelshift_l(w.x, w.y, 16), __funnelshift_l(w.y, w.z, 16), __funnelshift_l(w.z, w.w, 16));
+    else
+      w = make_uint4(x, w.x, w.y, w.z);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return w;
 }
 
 template <class T>
@@ -155,35 +164,28 @@ __device__ __forceinline__ uint4 load_vector(const Row<T>& r, int v) {
   return r.whole(v) ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : edge_vector(r, v);
 }
 
-// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; the loop has eight entries' worth of f.
+// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; one instance of f.
 template <class T, class F>
 __device__ __forceinline__ void stream(const Row<T>& r, int v0, int v1, F f) {
-  constexpr int kEach = 8 / kVec<T>;
   const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;  // whole ones
   const uint4* p = reinterpret_cast<const uint4*>(r.base);
   int v = v0 + int(threadIdx.x % 32);
-  auto load = [&](int v) { return (v >= w0) & (v < w1) ? __ldg(p + v) : edge_vector(r, v); };
   uint4 w[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
-    if (v + 32 * i < v1) w[i] = load(v + 32 * i);
+    const int at = v + 32 * i;
+    if ((at < v1) & (at >= w0) & (at < w1)) w[i] = __ldg(p + at);
   }
 #pragma unroll 1
-  for (; v < v1; v += 32 * kEach) {
-    uint4 now[kEach];
+  for (; v < v1; v += 32) {
+    uint4 now = w[0];
+    if ((v < w0) | (v >= w1)) now = edge_vector(r, v);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) now[i] = w[i];
-#pragma unroll
-    for (int i = kEach; i < kAhead; ++i) w[i - kEach] = w[i];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int next = v + 32 * (kAhead + i);
-      if (next < v1) w[kAhead - kEach + i] = load(next);
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i == 0 || v + 32 * i < v1) f(now[i], v + 32 * i);
+    for (int i = 1; i < kAhead; ++i) w[i - 1] = w[i];
+    const int at = v + 32 * kAhead;
+    if ((at < v1) & (at >= w0) & (at < w1)) w[kAhead - 1] = __ldg(p + at);
+    f(now, v);
   }
 }
 
@@ -423,18 +425,18 @@ struct Groups {
   int per_group;
   __device__ __forceinline__ explicit Groups(const Row<T>& r) {
     const int each = (r.per_warp + 31) / 32;
-    per_group = ((each + kGroups - 1) / kGroups + kFirstAhead - 1) / kFirstAhead * kFirstAhead;
+    per_group = ((each + kGroups - 1) / kGroups + kMostAhead - 1) / kMostAhead * kMostAhead;
   }
 };
 
 // The CTA's entries from tau on, out of the groups of vectors whose maximum reaches it, to sh.own (those that have
 // room; sh.n_own counts them all).
-template <class S, class T>
+template <int AHEAD, class S, class T>
 __device__ __noinline__ void collect(S& sh, const Row<T> r, float tau) {
   const int tid = threadIdx.x;
   if (tid == 0) sh.n_scan = sh.n_own = 0;
   __syncthreads();
-#pragma unroll
+#pragma unroll 4
   for (int g = 0; g < kGroups; ++g) {
     if (sh.group[g * S::kThreads + tid] >= tau) {
       const int at = atomicAdd(&sh.n_scan, 1);
@@ -470,16 +472,17 @@ __device__ __noinline__ void collect(S& sh, const Row<T> r, float tau) {
     return v < min(r.run_end(r.rank, warp), w1) ? v : -1;
   };
   const uint4* p = reinterpret_cast<const uint4*>(r.base);
-  for (int x = tid; x < n * per_group; x += kAhead * S::kThreads) {
-    int v[kAhead];
-    uint4 w[kAhead];
+#pragma unroll 1
+  for (int x = tid; x < n * per_group; x += AHEAD * S::kThreads) {
+    int v[AHEAD];
+    uint4 w[AHEAD];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       v[i] = vector_at(x + i * S::kThreads);
       w[i] = v[i] >= 0 ? __ldg(p + v[i]) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
+    for (int i = 0; i < AHEAD; ++i)
       if (v[i] >= 0) take(w[i], v[i]);
   }
   // the row's ends (as they were streamed)
@@ -551,7 +554,7 @@ __device__ __noinline__ void sort_list(S& sh, int n) {
     const int e = e0 + tid / g;
     const uint64_t mine = sh.place[min(e, n - 1)];
     int rank = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int j = tid % g; j < n; j += g) rank += sh.place[j] > mine;
     for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (tid % g == 0 && e < n) sh.sorted[rank] = sh.list[e];
@@ -845,19 +848,20 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
       uint64_t rest = 0;  // the last bin's, which most entries of a peaked row fall into
       stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
         if (MASS && !weighs(vector_max(w, static_cast<T*>(nullptr)), sc)) return;
-        float x[kVec<T>];
-        unpack(w, x);
+        pairs<T>(w, [&](float x0, float x1, int e) {
+          const float x[2] = {x0, x1};
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) {
-          const int i = v * kVec<T> - r.off + e;
-          uint64_t m;
-          if constexpr (MASS) m = units_of(x[e], sc, sh.table);
-          else m = (i >= 0) & (i < r.V);
-          if (!all) m = within.keeps(key_of(x[e]), i) ? m : 0;
-          const int bin = m != 0 ? bin_of(x[e]) : kBins - 1;
-          if (bin < kBins - 1) add(bin, m);
-          else rest += m;
-        }
+          for (int h = 0; h < 2; ++h) {
+            const int i = v * kVec<T> - r.off + e + h;
+            uint64_t m;
+            if constexpr (MASS) m = units_of(x[h], sc, sh.table);
+            else m = (i >= 0) & (i < r.V);
+            if (!all) m = within.keeps(key_of(x[h]), i) ? m : 0;
+            const int bin = m != 0 ? bin_of(x[h]) : kBins - 1;
+            if (bin < kBins - 1) add(bin, m);
+            else rest += m;
+          }
+        });
       });
       rest = warp_sum(rest);
       if (lane == 0 && rest != 0) add(kBins - 1, rest);
@@ -969,14 +973,12 @@ __device__ __forceinline__ uint64_t kept_sum(const uint4& w, int v, const Row<T>
                                              const uint32_t* table) {
   const float top = vector_max(w, static_cast<T*>(nullptr));
   if (top < keep.value || !weighs(top, sc)) return 0;
-  float x[kVec<T>];
-  unpack(w, x);
   uint64_t sum = 0;
-#pragma unroll
-  for (int e = 0; e < kVec<T>; ++e) {
-    const uint64_t u = units_of(x[e], sc, table);
-    sum += keep(x[e], v * kVec<T> - r.off + e) ? u : 0;
-  }
+  pairs<T>(w, [&](float a, float b, int e) {
+    const uint64_t u = units_of(a, sc, table), w = units_of(b, sc, table);
+    const int i = v * kVec<T> - r.off + e;
+    sum += (keep(a, i) ? u : 0) + (keep(b, i + 1) ? w : 0);
+  });
   return sum;
 }
 
@@ -1084,6 +1086,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   const float c_lo = greedy || !params_ok ? 0.0f : (fmaf(-c, T_, kLog2eHi) + kLog2eLo) / T_;
 
   // ---- the row streams once: the threads' maxima, and the mass where it is needed
+  constexpr int kFirstAhead = PART == kFirst ? kMostAhead : kAhead;  // (few CTAs to a row have more to do each)
   const bool nucleus = !greedy && top_p < 1.0f;
   const bool sums = PART != kRest && k == 0 && (nucleus || min_p == 0.0f);
   float top = -INFINITY;
@@ -1151,17 +1154,27 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     float all = 0.0f;
     if (sums)
       for (int w = 0; w < S::kWarps; ++w) all += sh.sums[w].y * ex2_approx((sh.sums[w].x - most) * c);
+    float lead = 0.0f;
+    if (sums) {
+#pragma unroll 4
+      for (int i = lane; i < S::kThreads; i += 32) lead += sh.tops[i] >= least_top ? ex2_approx((sh.tops[i] - most) * c) : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) lead += __shfl_xor_sync(0xffffffffu, lead, o);
+    }
+    if (lane == 0) sh.lead = lead;
     if (lane == 0) sh.ends = make_float4(most, nth <= S::kThreads ? least_top : -INFINITY, bad ? 1.0f : 0.0f, all);
   }
   row_sync();
-  float tau, M, about;  // about: the row's mass, roughly
+  float tau, M, about, lead;  // about, lead: the row's mass and the largest maxima's, roughly
   {
+    float leads = 0.0f;
     float4 e = make_float4(-INFINITY, INFINITY, 0.0f, 0.0f);
     if (lane < r.ctas) {
       const uint64_t ab = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends), lane);
       const uint64_t cd = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends) + 1, lane);
       e = make_float4(__uint_as_float(uint32_t(ab)), __uint_as_float(uint32_t(ab >> 32)), __uint_as_float(uint32_t(cd)),
                       __uint_as_float(uint32_t(cd >> 32)));
+      leads = __uint_as_float(ld_peer_u32(&sh.lead, lane));
     }
     bad = __any_sync(0xffffffffu, e.z != 0.0f);
     M = e.x;
@@ -1172,10 +1185,16 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     }
     M = __shfl_sync(0xffffffffu, M, 0);
     tau = __shfl_sync(0xffffffffu, e.y, 0);
-    about = e.w > 0.0f ? e.w * ex2_approx((e.x - M) * c) : 0.0f;
+    const float scale = e.w > 0.0f ? ex2_approx((e.x - M) * c) : 0.0f;
+    about = e.w * scale;
+    lead = leads * scale;
 #pragma unroll
-    for (int o = 1; o < kMaxCtas; o *= 2) about += __shfl_xor_sync(0xffffffffu, about, o);
+    for (int o = 1; o < kMaxCtas; o *= 2) {
+      about += __shfl_xor_sync(0xffffffffu, about, o);
+      lead += __shfl_xor_sync(0xffffffffu, lead, o);
+    }
     about = __shfl_sync(0xffffffffu, about, 0);
+    lead = __shfl_sync(0xffffffffu, lead, 0);
   }
   bad = bad || M == -INFINITY;
   const Scale sc = scale_of(M, c, c_lo);
@@ -1208,11 +1227,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         }
       }
       const bool trusted = !sums || fabsf(sc.M * sc.c) < kFastRange - 128.0f;
-      // (a weight is 1 at most, so a nucleus has p times the mass entries at least)
-      const bool hopeless = sums && nucleus && !closed && top_p * about > 1.5f * kNucleus;
+      // (the candidates are half as many again as the maxima they are found by, so twice those' mass they hardly reach)
+      const bool hopeless = sums && nucleus && !closed && top_p * about > 2.0f * lead;
       const bool by_list = trusted && !hopeless && (nth <= S::kThreads || closed);
       if (by_list) {
-        collect(sh, r, tau);
+        collect<PART == kFirst ? kAhead : 1>(sh, r, tau);
         row_sync();
         const int found = share_out(sh, sc, r.ctas, !greedy);
         const uint64_t mass = sums ? all_chunks(sh, r.ctas) : 0;
