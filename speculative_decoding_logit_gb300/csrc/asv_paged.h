@@ -75,6 +75,7 @@ struct PlanArgs {
   int64_t* slots;       // these three: nullptr, not wanted
   int32_t* positions;
   int32_t* requests;
+  bool rows_behind;  // the rows are placed by the launch behind
   uint32_t* status;
   uint32_t* check_log;  // of the checked build: the plan has no workspace, its log is the library's
 };

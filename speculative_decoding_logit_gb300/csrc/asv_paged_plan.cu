@@ -24,36 +24,52 @@ namespace asv {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kKept = 4;  // requests of a thread whose lengths stay in registers
+constexpr int kRows = 4;  // rows of a thread at a time
+constexpr int kRowThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
+// Sums that stay at the largest number of 31 bits once they reach it: none of the limits they are held against is larger.
 struct Sums {
-  long long back, need, rows;
+  uint32_t back, need, rows;
 };
 
-__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.back + b.back, a.need + b.need, a.rows + b.rows}; }
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+  constexpr uint32_t kMost = 0x7fffffffu;
+  return {min(a.back + b.back, kMost), min(a.need + b.need, kMost), min(a.rows + b.rows, kMost)};
+}
 
-__device__ __forceinline__ long long shfl_up(long long x, int d) { return __shfl_up_sync(0xffffffffu, x, d); }
+// The sums of the lanes up to this one.
+__device__ __forceinline__ Sums warp_scan(Sums x) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const Sums y = {__shfl_up_sync(0xffffffffu, x.back, d), __shfl_up_sync(0xffffffffu, x.need, d),
+                    __shfl_up_sync(0xffffffffu, x.rows, d)};
+    if (lane >= d) x = x + y;
+  }
+  return x;
+}
+
+__device__ __forceinline__ Sums lane_before(Sums x) {
+  const Sums y = {__shfl_up_sync(0xffffffffu, x.back, 1), __shfl_up_sync(0xffffffffu, x.need, 1),
+                  __shfl_up_sync(0xffffffffu, x.rows, 1)};
+  return threadIdx.x % 32 == 0 ? Sums{0, 0, 0} : y;
+}
 
 // The sums of the threads before this one, and of all; `room` is [kWarps].
 __device__ __forceinline__ Sums scan(Sums own, Sums* room, Sums& all) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  Sums incl = own;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const Sums x = {shfl_up(incl.back, d), shfl_up(incl.need, d), shfl_up(incl.rows, d)};
-    if (lane >= d) incl = incl + x;
-  }
+  const Sums upto = warp_scan(own), inner = lane_before(upto);
   __syncthreads();  // (the room's last readers are done)
-  if (lane == 31) room[warp] = incl;
+  if (lane == 31) room[warp] = upto;
   __syncthreads();
-  Sums before = {0, 0, 0};
-  all = before;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before = before + room[w];
-    all = all + room[w];
-  }
-  return before + Sums{incl.back - own.back, incl.need - own.need, incl.rows - own.rows};
+  const Sums warps = warp_scan(lane < kWarps ? room[lane] : Sums{0, 0, 0}), outer = lane_before(warps);
+  auto of = [&](const Sums& x, int l) {
+    return Sums{__shfl_sync(0xffffffffu, x.back, l), __shfl_sync(0xffffffffu, x.need, l), __shfl_sync(0xffffffffu, x.rows, l)};
+  };
+  all = of(warps, 31);
+  return of(outer, warp) + inner;
 }
 
 // What a request asks for.
@@ -79,7 +95,52 @@ __device__ __forceinline__ Want load_want(const PlanArgs& a, int b) {
   return w;
 }
 
-__global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+// The rows' requests, positions and slots; `first` [B + 1] the requests' first rows.  A few of a thread at a time (the
+// searches one behind the other took most of the launch).
+__device__ __forceinline__ void place_rows(const PlanArgs& a, const int* first, int total, int tid, int threads) {
+  int steps = 0;
+  while ((1 << steps) < a.B) ++steps;
+  for (int x0 = tid; x0 < a.N; x0 += kRows * threads) {
+    int lo[kRows], hi[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      lo[i] = 0;
+      hi[i] = a.B;
+    }
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int mid = (lo[i] + hi[i]) / 2;
+        const bool up = first[mid] <= x0 + i * threads;
+        lo[i] = up ? mid : lo[i];
+        hi[i] = up ? hi[i] : mid;
+      }
+    }
+    int pos[kRows], page[kRows], slot[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int x = x0 + i * threads;
+      page[i] = pos[i] = -1;
+      if (x < total) {
+        pos[i] = a.cache_len[lo[i]] + (x - first[lo[i]]);
+        const int entry = pos[i] / a.page_size;
+        slot[i] = pos[i] - entry * a.page_size;
+        if (ASV_GUARD(a, entry >= 0 && entry < a.max_pages)) page[i] = __ldcg(a.table + lo[i] * a.table_stride + entry);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int x = x0 + i * threads;
+      if (x >= a.N) break;
+      if (x < total && page[i] < 0) atomicOr(a.status + lo[i], ASV_REQ_BAD_PAGE);
+      if (a.slots != nullptr) a.slots[x] = page[i] >= 0 ? (long long)page[i] * a.page_size + slot[i] : -1;
+      if (a.positions != nullptr) a.positions[x] = pos[i];
+      if (a.requests != nullptr) a.requests[x] = x < total ? lo[i] : -1;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ __align__(16) int s_dyn[];
   __shared__ Sums s_room[kWarps];
   // Of the requests, in order: the first row; pages given back, pages taken (exclusive sums).  (Ends behind the last.)
@@ -93,42 +154,55 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 
   // ---- the sums: a thread has consecutive requests
   const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  Want kept[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (b0 + i < b1) kept[i] = load_want(a, b0 + i);
+  // f(request, what it asks for) for the thread's requests
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+      if (b0 + i < b1) f(b0 + i, kept[i]);
+    for (int b = b0 + kKept; b < b1; ++b) f(b, load_want(a, b));
+  };
   const int count0 = a.free_count[0];
   const bool pool_ok = count0 >= 0 && count0 <= a.pool;
   Sums own = {0, 0, 0}, all;
-  for (int b = b0; b < b1; ++b) {
-    const Want w = load_want(a, b);
-    own = own + Sums{w.back, w.need, w.grow};
+  each([&](int b, const Want& w) {
+    own = own + Sums{uint32_t(w.back), uint32_t(w.need), uint32_t(w.grow)};
     if (rank == 0 && !w.ok) atomicOr(a.status + b, ASV_REQ_BAD_LEN);
     if (rank == 0 && !pool_ok) atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
-  }
-  Sums before = scan(own, s_room, all);
+  });
+  const Sums first = scan(own, s_room, all);
+  const uint32_t given_all = all.back;
   // (pages beyond the pool's end are not there: the pool was handed more pages than it holds)
   const long long count = pool_ok ? min((long long)count0 + all.back, (long long)a.pool) : 0;
-  Sums take = {0, 0, 0};
-  const Sums first = before;
-  for (int pass = 0; pass < 2; ++pass) {
-    Sums at = first, got = take;  // (second pass: the served requests' own sums before this thread's)
-    for (int b = b0; b < b1; ++b) {
-      const Want w = load_want(a, b);
-      const bool served = pool_ok && (w.need == 0 || at.need + w.need <= count) && at.rows + w.grow <= a.N;
-      if (pass == 1) {
-        s_back[b] = int(min(at.back, (long long)INT_MAX));
-        s_take[b] = int(got.need);
-        s_row[b] = int(got.rows);
-        if (rank == 0) {
-          a.indptr[b] = int(got.rows);
-          if (w.ok && pool_ok && !served) atomicOr(a.status + b, ASV_REQ_NO_ROOM);
-        }
-      }
-      at = at + Sums{w.back, w.need, w.grow};
-      if (served) got = got + Sums{0, w.need, w.grow};
+  auto served = [&](const Sums& at, const Want& w) {
+    return pool_ok && (w.need == 0 || (long long)at.need + w.need <= count) && (long long)at.rows + w.grow <= a.N;
+  };
+  Sums at = first, got = {0, 0, 0};
+  each([&](int, const Want& w) {
+    if (served(at, w)) got = got + Sums{0, uint32_t(w.need), uint32_t(w.grow)};
+    at = at + Sums{uint32_t(w.back), uint32_t(w.need), uint32_t(w.grow)};
+  });
+  got = scan(got, s_room, all);  // the served requests' own sums before this thread's
+  at = first;
+  each([&](int b, const Want& w) {
+    const bool is = served(at, w);
+    s_back[b] = int(at.back);
+    s_take[b] = int(got.need);
+    s_row[b] = int(got.rows);
+    if (rank == 0) {
+      a.indptr[b] = int(got.rows);
+      if (w.ok && pool_ok && !is) atomicOr(a.status + b, ASV_REQ_NO_ROOM);
     }
-    if (pass == 0) take = scan(got, s_room, all);
-  }
+    at = at + Sums{uint32_t(w.back), uint32_t(w.need), uint32_t(w.grow)};
+    if (is) got = got + Sums{0, uint32_t(w.need), uint32_t(w.grow)};
+  });
   if (tid == 0) {
     s_row[a.B] = int(all.rows);
     s_take[a.B] = int(all.need);
+    s_back[a.B] = int(given_all);
     if (rank == 0) a.indptr[a.B] = int(all.rows);
   }
   __syncthreads();
@@ -145,29 +219,19 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     return lo;
   };
 
-  // ---- pages given back, by warps in turn (few requests have any)
-  const int warp = rank * kWarps + tid / 32, warps = ctas * kWarps, lane = tid % 32;
-  if (a.release != nullptr && pool_ok) {
-    for (int g = warp; g * 32 < a.B; g += warps) {
-      const int mine = g * 32 + lane;
-      const int back = mine < a.B ? load_want(a, mine).back : 0;
-      for (uint32_t some = __ballot_sync(0xffffffffu, back > 0); some != 0; some &= some - 1) {
-        const int b = g * 32 + __ffs(some) - 1, n = __shfl_sync(0xffffffffu, back, __ffs(some) - 1);
-        int32_t* row = a.table + b * a.table_stride;
-        for (int j = lane; j < n; j += 32) {
-          const long long to = (long long)count0 + s_back[b] + j;
-          if (to < a.pool) a.free_pages[to] = row[j];
-          else atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
-          row[j] = -1;
-        }
-      }
-    }
+  // ---- pages given back
+  const int tid_all = rank * kThreads + tid, threads = ctas * kThreads, given = pool_ok ? s_back[a.B] : 0;
+  for (int x = tid_all; x < given; x += threads) {
+    const int b = owner(s_back, x);
+    int32_t* entry = a.table + b * a.table_stride + (x - s_back[b]);
+    if (x < a.pool - count0) a.free_pages[count0 + x] = *entry;
+    else atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
+    *entry = -1;
   }
   if (ctas > 1) cluster_sync();
   else __syncthreads();
 
   // ---- pages taken
-  const int tid_all = rank * kThreads + tid, threads = ctas * kThreads;
   for (int x = tid_all; x < taken; x += threads) {
     const int b = owner(s_take, x), i = x - s_take[b];
     const Want w = load_want(a, b);
@@ -177,21 +241,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
   else __syncthreads();
 
   // ---- rows
-  for (int x = tid_all; x < a.N; x += threads) {
-    int request = -1, pos = -1;
-    long long slot = -1;
-    if (x < total) {
-      request = owner(s_row, x);
-      pos = a.cache_len[request] + (x - s_row[request]);
-      const int entry = pos / a.page_size;
-      const int page = ASV_GUARD(a, entry >= 0 && entry < a.max_pages) ? __ldcg(a.table + request * a.table_stride + entry) : -1;
-      if (page >= 0) slot = (long long)page * a.page_size + (pos - entry * a.page_size);
-      else atomicOr(a.status + request, ASV_REQ_BAD_PAGE);
-    }
-    if (a.slots != nullptr) a.slots[x] = slot;
-    if (a.positions != nullptr) a.positions[x] = pos;
-    if (a.requests != nullptr) a.requests[x] = request;
-  }
+  if (!a.rows_behind) place_rows(a, s_row, total, tid_all, threads);
 
   // ---- what is held now (nobody reads it any more)
   if (rank == 0) {
@@ -203,16 +253,24 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
   }
 }
 
+// The rows of a long step, by a launch of their own.
+__global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const __grid_constant__ PlanArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  place_rows(a, a.indptr, a.indptr[a.B], blockIdx.x * kRowThreads + threadIdx.x, gridDim.x * kRowThreads);
+}
+
 #ifdef ASV_CHECKED
 __device__ uint32_t g_check_log[2];  // the plan has no workspace to keep a log in
 #endif
 
-// More CTAs where there are rows for them.
-int plan_ctas(const PlanArgs& a) { return a.N > 2048 ? 8 : 1; }
-
-cudaError_t launch(const PlanArgs& a, cudaStream_t s) {
+cudaError_t launch(const PlanArgs& args, cudaStream_t s) {
+  PlanArgs a = args;
+  // More CTAs where there are rows for them (192 rows: 4.5 us with one; 24 thousand: 26 with one, 12 with eight), and for
+  // many rows a launch behind this one, of as many CTAs as they need.
+  a.rows_behind = a.N > 8192;
+  const int ctas = a.N > 2048 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
-  const int ctas = plan_ctas(a);
   cfg.gridDim = dim3(unsigned(ctas), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = 3 * sizeof(int) * size_t(a.B + 1);
@@ -230,7 +288,13 @@ cudaError_t launch(const PlanArgs& a, cudaStream_t s) {
                                                int(cfg.dynamicSmemBytes));
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
+  if (e != cudaSuccess || !a.rows_behind) return e;
+  cfg.gridDim = dim3(unsigned((a.N + kRows * kRowThreads - 1) / (kRows * kRowThreads)), 1, 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_rows_kernel, a);
 }
 
 }  // namespace
