@@ -594,7 +594,7 @@ typedef struct {
  * within it), out_positions (cache_len[b] + i) and out_requests (b), -1 in all three for rows behind the last; each may
  * be NULL.  cache_len and new_len are not changed.  ASV_REQ_* bits are ORed into out_req_status [B].  A pool whose count is
  * not within [0, pool_size] flags every request ASV_REQ_BAD_PAGE and changes nothing.  The buffers must not overlap.
- * B <= 16384.  One launch.  Checks: sizes (ASV_ERR_SHAPE); for B > 0 alignment (4 bytes, out_slots 8: ASV_ERR_ALIGN), the
+ * B <= 16384.  One launch, or two where N > 8192.  Checks: sizes (ASV_ERR_SHAPE); for B > 0 alignment (4 bytes, out_slots 8: ASV_ERR_ALIGN), the
  * required pointers (ASV_ERR_NULL).
  */
 asv_status paged_plan(const int32_t* cache_len, const int32_t* new_len, int B, const asv_page_pool* pool,

@@ -73,10 +73,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
           p.page = -1;
         }
         bool there = true;
-        for (int i = 0; i < a.axes; ++i) {
-          const int at = a.positions[i * a.axis_stride + token];
-          there = there && at >= 0 && at < a.max_position;
-          s_at[tid][i] = at;
+        int at[ASV_MAX_AXES];
+#pragma unroll
+        for (int i = 0; i < ASV_MAX_AXES; ++i) at[i] = i < a.axes ? a.positions[i * a.axis_stride + token] : 0;
+#pragma unroll
+        for (int i = 0; i < ASV_MAX_AXES; ++i) {
+          there = there && (i >= a.axes || (at[i] >= 0 && at[i] < a.max_position));
+          s_at[tid][i] = at[i];
         }
         if (!there) {
           atomicOr(a.status + b, ASV_REQ_BAD_LEN);

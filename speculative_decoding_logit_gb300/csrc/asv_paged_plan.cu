@@ -9,10 +9,11 @@
 //   place  row r belongs to the last request that starts at or before it; its position and slot follow
 // so four prefix sums place every write by itself, and the result does not depend on timing.
 //
-// One launch of one cluster (CTAs of 512 threads; one of them where there is little to write): every CTA works the
+// A launch of one cluster (CTAs of 512 threads; one of them where there is little to write): every CTA works the
 // sums out for itself from the requests' lengths (a few KB, from L2), the CTAs share the pages and the rows, and two
 // cluster barriers keep them in step: between pushes and pops (a released request's old entries are read before its new
 // ones are written, and pushed pages may be popped), and before the lengths, which all have read, are brought up to date.
+// Long steps' rows are placed by a second launch over as many CTAs as they need.
 // Next to nothing is moved (16 bytes a row), so the launch is bound by its chain of dependent loads and barriers.
 #include <algorithm>
 #include <climits>
