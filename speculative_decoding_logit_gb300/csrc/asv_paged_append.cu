@@ -228,12 +228,13 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   // More tokens to a CTA share the search and the chain of loads, fewer have more loads in flight: doubled up to eight
   // while there are more than 13 CTAs to an SM, and up to sixteen while there are more than 8 and a CTA's threads have
-  // less than four vectors each (9216 tokens of 576 vectors: 44 us at one token to a CTA, 34 at eight; 3995 of 525: 21,
-  // 18.6 at two, 26 at eight; 15,713 of 60: 70, 17.8 at eight, 14.2 at sixteen).
+  // less than four vectors each, but not past four when its threads have ten each (9216 tokens of 576 vectors: 44 us at
+  // one token to a CTA, 36 at four, 34.7 at eight; 16,883 of 768: 77 at two, 73 at four, 77 at eight, with positions of
+  // three axes 83.5, 79, 85; 3995 of 525: 21, 18.6 at two, 26 at eight; 15,713 of 60: 70, 17.8 at eight, 14.2 at sixteen).
   const long long vectors = (long long)(a.q_heads + 2 * a.c.kv_heads) * (a.c.head_dim / 8);
   int tokens = 1;
   auto ctas = [&]() { return (a.c.N + tokens - 1) / tokens; };
-  while ((tokens < 8 && ctas() > 2048) || (tokens < 16 && ctas() > 1216 && tokens * vectors < 4 * kThreads)) tokens *= 2;
+  while ((tokens < 8 && ctas() > 2048 && (tokens < 4 || tokens * vectors < 10 * kThreads)) || (tokens < 16 && ctas() > 1216 && tokens * vectors < 4 * kThreads)) tokens *= 2;
   cfg.gridDim = dim3(unsigned(ctas()), 1, 1);
   switch (tokens) {
     case 1: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 1>, a);

@@ -53,7 +53,7 @@ struct Cut {
 // What a launch does with its rows: all of it; the first way alone, leaving what that does not settle marked in the
 // tokens; or those rows in general.
 enum Part { kAll, kFirst, kRest };
-constexpr int kLeft = INT_MIN;
+constexpr int kLeft = INT_MIN, kTaken = INT_MIN + 1;
 
 template <int THREADS, Part PART>
 struct __align__(16) Shared {
@@ -80,7 +80,8 @@ struct __align__(16) Shared {
   float4 ends;                                     // of the CTA: maximum, bound of the candidates, whether it is bad, sum
   float lead;                                      // the sum of threads' maxima from the bound on
   Cut cut;
-  int n_scan, n_own, found, pick;
+  int n_scan, n_own, found, pick, first;
+  long long row;                                   // the next one
 };
 
 // ------------------------------------------------------------------ a row
@@ -164,28 +165,31 @@ __device__ __forceinline__ uint4 load_vector(const Row<T>& r, int v) {
   return r.whole(v) ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : edge_vector(r, v);
 }
 
-// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; one instance of f.
-template <class T, class F>
+// f(vector, number) for a warp's vectors [v0, v1), kAhead of them a lane in flight; one instance of f.  BACK: from the last
+// on (what was read last is likeliest still in L2).
+template <bool BACK = false, class T, class F>
 __device__ __forceinline__ void stream(const Row<T>& r, int v0, int v1, F f) {
   const int w0 = r.off > 0 ? 1 : 0, w1 = (r.off + r.V) / kVec<T>;  // whole ones
   const uint4* p = reinterpret_cast<const uint4*>(r.base);
   int v = v0 + int(threadIdx.x % 32);
+  auto number = [&](int v) { return BACK ? v0 + v1 - 1 - v : v; };
+  auto whole = [&](int v) { return (number(v) >= w0) & (number(v) < w1); };
   uint4 w[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
     const int at = v + 32 * i;
-    if ((at < v1) & (at >= w0) & (at < w1)) w[i] = __ldg(p + at);
+    if ((at < v1) & whole(at)) w[i] = __ldg(p + number(at));
   }
 #pragma unroll 1
   for (; v < v1; v += 32) {
     uint4 now = w[0];
-    if ((v < w0) | (v >= w1)) now = edge_vector(r, v);
+    if (!whole(v)) now = edge_vector(r, number(v));
 #pragma unroll
     for (int i = 1; i < kAhead; ++i) w[i - 1] = w[i];
     const int at = v + 32 * kAhead;
-    if ((at < v1) & (at >= w0) & (at < w1)) w[kAhead - 1] = __ldg(p + at);
-    f(now, v);
+    if ((at < v1) & whole(at)) w[kAhead - 1] = __ldg(p + number(at));
+    f(now, number(v));
   }
 }
 
@@ -384,9 +388,51 @@ __device__ __forceinline__ void add_weights(Partial& s, const float (&x)[N], flo
 
 // ------------------------------------------------------------------ candidates
 
+// The same where the whole row's mass is drawn from, and fp32's errors are what leaves a draw undecided: exponents as sums of
+// two floats next to a whole reference.  What is left is ex2 (2^-22), a product, three additions within the vector, and the
+// move to the maximum (ex2 and two products): 15 * 2^-24 < 2^-20.
+constexpr int kFineBits = 20;
+
+template <int N>
+__device__ __forceinline__ void add_weights_fine(Partial& s, const float (&x)[N], float top, float c, float c_lo) {
+  const float most = top * c;
+  if (!(most > -kFastRange)) return;
+  if (most > s.ref + 8.0f) {
+    const float ref = rintf(most), keep = ex2_approx(s.ref - ref);  // (a power of two)
+    s.hi *= keep;
+    s.lo *= keep;
+    s.ref = ref;
+  }
+  const float2 cc = make_float2(c, c), cl = make_float2(c_lo, c_lo), rr = make_float2(-s.ref, -s.ref);
+  const float2 one = make_float2(1.0f, 1.0f), ln2 = make_float2(kLn2Hi, kLn2Hi), far = make_float2(-120.0f, -120.0f);
+  float2 w[N / 2];
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    const float2 y = make_float2(x[2 * e], x[2 * e + 1]);
+    const float2 p = fmul2(y, cc), low = ffma2(y, cl, ffma2(y, cc, make_float2(-p.x, -p.y)));
+    const float2 t = fadd2(p, rr), bb = fsub2(t, p), err = fadd2(fsub2(p, fsub2(t, bb)), fsub2(rr, bb));
+    // (what is too far below to count may be -inf, and its errors nothing)
+    const bool a = t.x > far.x, b = t.y > far.y;
+    const float2 v = make_float2(a ? ex2_approx(t.x) : 0.0f, b ? ex2_approx(t.y) : 0.0f);
+    const float2 l = fadd2(low, err), more = fmul2(make_float2(a ? l.x : 0.0f, b ? l.y : 0.0f), ln2);
+    w[e] = ffma2(v, more, v);
+  }
+#pragma unroll
+  for (int n = N / 2; n > 1; n /= 2)
+#pragma unroll
+    for (int e = 0; e < n / 2; ++e) w[e] = fadd2(w[2 * e], w[2 * e + 1]);
+  const float v = w[0].x + w[0].y;
+  const float sum = s.hi + v, bb = sum - s.hi;
+  s.lo += (s.hi - (sum - bb)) + (v - bb);
+  s.hi = sum;
+}
+
 // A running sum in units, once the row's maximum is known.
-__device__ __forceinline__ uint64_t units_of_sum(const Partial& s, const Scale& sc) {
-  return s.ref > -INFINITY ? uint64_t((s.hi + s.lo) * ex2_approx(fmaf(-sc.M, sc.c, s.ref)) * float(kOne)) : 0;
+__device__ __forceinline__ uint64_t units_of_sum(const Partial& s, const Scale& sc, bool fine) {
+  if (!(s.ref > -INFINITY)) return 0;
+  const float shift = fine ? ex2_approx(s.ref - float(sc.k_top) * (1.0f / 1024.0f)) : ex2_approx(fmaf(-sc.M, sc.c, s.ref));
+  const float v = (s.hi + s.lo) * shift;
+  return uint64_t((fine ? fmaf(v, -sc.rest * kLn2Hi, v) : v) * float(kOne));
 }
 
 // A bound of the n-th largest of sh.tops (1 <= n <= kThreads) from below, to sixteen bits, and the largest, by a warp: the
@@ -995,25 +1041,33 @@ __device__ __forceinline__ void add_kept(Partial& s, const uint4& w, int v, cons
   add_weights(s, x, top, sc.c);
 }
 
-// A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync).  A token < 0: too near a
-// border to say.
+// A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync); fine: from all of them, by
+// their finer sums.  A token < 0: too near a border to say.
 template <class S, class T>
-__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, const Kept keep, uint64_t draw) {
+__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, const Kept keep, bool fine, uint64_t draw) {
   const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
   d.total = sh.total;
   // Of sums b before a border and a behind it the draw u compares (1 - u) b with u a.  Next to the border both are u (1 - u)
-  // of the mass, 1/4 at most, and each is off by 2^-18 of itself; the run's own sum counts once as the rows streamed and
-  // once as it is taken apart here, each off by 2^-18 too.
+  // of the mass, 1/4 at most, and each is off by 2^-18 (2^-20) of itself; the run's own sum counts once as the rows streamed
+  // and once as it is taken apart here, each off by as much too.
   const int run = sh.pick;
-  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % S::kWarps, run / S::kWarps)) >> kFastBits) + 64;
+  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % S::kWarps, run / S::kWarps)) >> (fine ? kFineBits : kFastBits)) + 64;
   d.token = find_entry(
       sh, r, at, margin,
       [&](int v0, int v1) {
         Partial s;
-        stream(r, v0, v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
-        return warp_sum(units_of_sum(s, sc));
+        stream(r, v0, v1, [&](const uint4& w, int v) {
+          if (fine) {
+            float x[kVec<T>];
+            unpack(w, x);
+            add_weights_fine(s, x, vector_max(w, static_cast<T*>(nullptr)), sc.c, sc.c_lo);
+          } else {
+            add_kept(s, w, v, r, sc, keep);
+          }
+        });
+        return warp_sum(units_of_sum(s, sc, fine));
       },
       [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, kExp2Table); },
       [&](float x, int i) { return keep(x, i) ? weight(x, sc, kExp2Table) : uint64_t(0); });
@@ -1026,7 +1080,7 @@ template <class S, class T>
 __device__ __noinline__ void fast_sums(S& sh, const Row<T> r, const Scale sc, const Kept keep) {
   Partial s;
   stream(r, r.v0, r.v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
-  const uint64_t w = warp_sum(units_of_sum(s, sc));
+  const uint64_t w = warp_sum(units_of_sum(s, sc, false));
   if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = w;
 }
 
@@ -1089,6 +1143,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   constexpr int kFirstAhead = PART == kFirst ? kMostAhead : kAhead;  // (few CTAs to a row have more to do each)
   const bool nucleus = !greedy && top_p < 1.0f;
   const bool sums = PART != kRest && k == 0 && (nucleus || min_p == 0.0f);
+  const bool fine = sizeof(T) == 4 && sums && !nucleus;  // (16-bit rows would be bound by it)
   float top = -INFINITY;
   Partial part;
   {
@@ -1100,7 +1155,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
       if (sums) {
         float x[kVec<T>];
         unpack(w, x);
-        add_weights(part, x, m, c);
+        if (fine) add_weights_fine(part, x, m, c, c_lo);
+        else add_weights(part, x, m, c);
       }
       return m;
     };
@@ -1211,7 +1267,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     bool settled = false;
     if constexpr (PART != kRest) {
       if (sums) {
-        const uint64_t w = warp_sum(units_of_sum(part, sc));
+        const uint64_t w = warp_sum(units_of_sum(part, sc, fine));
         if (lane == 0) sh.chunk[warp] = w;
       }
       // Where nothing depends on the mass below min-p's border, candidates end there (a little below it, for the
@@ -1226,7 +1282,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
           closed = true;
         }
       }
-      const bool trusted = !sums || fabsf(sc.M * sc.c) < kFastRange - 128.0f;
+      const bool trusted = !sums || (fine ? !sc.far : fabsf(sc.M * sc.c) < kFastRange - 128.0f);
       // (the candidates are half as many again as the maxima they are found by, so twice those' mass they hardly reach)
       const bool hopeless = sums && nucleus && !closed && top_p * about > 2.0f * lead;
       const bool by_list = trusted && !hopeless && (nth <= S::kThreads || closed);
@@ -1238,10 +1294,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         if (found > 0)
           settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, d);
         if (settled) cut = sh.cut;
-        row_sync();  // (the peers have read the candidates)
+        else row_sync();  // (the peers have read the candidates)
       } else if (trusted && sums && !nucleus) {
         row_sync();
-        d = draw_fast(sh, r, sc, Kept{cut, -INFINITY}, draw);
+        d = draw_fast(sh, r, sc, Kept{cut, -INFINITY}, true, draw);
         settled = d.token >= 0;
       }
     }
@@ -1265,7 +1321,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         if (cut.key != 0 && fabsf(sc.M * sc.c) < kFastRange - 128.0f) {
           fast_sums(sh, r, sc, keep);
           row_sync();
-          d = draw_fast(sh, r, sc, keep, draw);
+          d = draw_fast(sh, r, sc, keep, false, draw);
         }
         if (d.token < 0) d = draw_exact(sh, r, sc, keep, draw);
       }
@@ -1291,7 +1347,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
     const bool vectors = (reinterpret_cast<uintptr_t>(to) / 4 + kVec<T> - r.off) % 4 == 0;
     const float far = -200.0f / sc.c;  // (what is further below has no weight)
-    stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
+    stream<true>(r, r.v0, r.v1, [&](const uint4& w, int v) {
       float x[kVec<T>], p[kVec<T>];
       unpack(w, x);
       const int i0 = v * kVec<T> - r.off;
@@ -1327,27 +1383,53 @@ __global__ void __launch_bounds__(THREADS, CTAS) sample_kernel(const __grid_cons
   sample_row<PART>(a, sh, r, blockIdx.x / r.ctas);
 }
 
-// The rows that the first way left, by the clusters in turn.  (A row's mark goes only when all of its cluster's CTAs have
-// seen it: its token is written behind their first row_sync.)
+// The rows that the first way left.  Each cluster goes through all rows once, from a place of its own, and takes those
+// that no other has taken (an exchange of the mark; by turns, two of a few rows often came to one cluster).
 template <class T, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) sample_rest_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ Shared<THREADS, kRest> sh;
   Row<T> r;
   r.ctas = int(cluster_size());
   r.rank = int(cluster_rank());
+  const int tid = threadIdx.x;
   const long long rows = (long long)a.B * a.n, clusters = gridDim.x / r.ctas, mine = blockIdx.x / r.ctas;
-  const int lane = threadIdx.x % 32;
+  const long long chunks = (rows + THREADS - 1) / THREADS, start = mine * chunks / clusters;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (long long q = 0; mine + q * clusters < rows; q += 32) {
-    const long long row = mine + (q + lane) * clusters;
-    bool left = false;
-    if (row < rows) {
-      const long long b = row / a.n;
-      left = __ldcg(a.tokens + b * a.tokens_b + (row - b * a.n) * a.tokens_n) == kLeft;
+  auto token_of = [&](long long row) {
+    const long long b = row / a.n;
+    return a.tokens + b * a.tokens_b + (row - b * a.n) * a.tokens_n;
+  };
+  long long chunk = 0;
+  for (;;) {
+    if (r.rank == 0) {
+      // the next row that can be taken, or none
+      if (tid == 0) sh.row = -1;
+      while (chunk < chunks) {
+        const long long row = (start + chunk) % chunks * THREADS + tid;
+        // (in an order of its own within the chunk too)
+        const int place = int((tid + THREADS - mine * 13 % THREADS) % THREADS);
+        const bool left = row < rows && __ldcg(token_of(row)) == kLeft;
+        if (tid == 0) sh.first = THREADS;
+        __syncthreads();
+        if (left) atomicMin(&sh.first, place);
+        __syncthreads();
+        const int first = sh.first;
+        if (first == THREADS) {
+          ++chunk;
+          __syncthreads();
+          continue;
+        }
+        if (left && place == first && atomicCAS(token_of(row), kLeft, kTaken) == kLeft) sh.row = row;
+        __syncthreads();
+        if (sh.row >= 0) break;
+      }
     }
-    for (uint32_t some = __ballot_sync(0xffffffffu, left); some != 0; some &= some - 1)
-      sample_row<kRest>(a, sh, r, mine + (q + __ffs(some) - 1) * clusters);
+    row_sync();
+    const long long row = (long long)ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.row), 0);
+    row_sync();
+    if (row < 0) break;
+    sample_row<kRest>(a, sh, r, row);
   }
 }
 
