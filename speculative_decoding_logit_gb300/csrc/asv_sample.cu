@@ -93,6 +93,12 @@ struct Row {
   int V, vectors;
   int rank, ctas, per_cta, per_warp;
   int v0, v1;        // this warp's vectors
+#ifdef ASV_CHECKED
+  uint32_t* check_log;
+#endif
+  __device__ __forceinline__ bool holds(int v) const {  // a whole vector of the row
+    return v >= 0 && (long long)v * kVec<T> >= off && (long long)(v + 1) * kVec<T> - off <= V;
+  }
   __device__ __forceinline__ bool whole(int v) const {
     return (v > 0 || off == 0) && (long long)(v + 1) * kVec<T> - off <= V;
   }
@@ -139,6 +145,7 @@ __device__ __forceinline__ void pairs(uint4 w, F f) {
 
 template <class T>
 __device__ __forceinline__ float entry(const Row<T>& r, int i) {
+  if (!ASV_GUARD(r, i >= 0 && i < r.V)) return -INFINITY;
   return widen(r.base[r.off + i]);
 }
 
@@ -179,7 +186,7 @@ __device__ __forceinline__ void stream(const Row<T>& r, int v0, int v1, F f) {
   for (int i = 0; i < kAhead; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
     const int at = v + 32 * i;
-    if ((at < v1) & whole(at)) w[i] = __ldg(p + number(at));
+    if (((at < v1) & whole(at)) && ASV_GUARD(r, r.holds(number(at)))) w[i] = __ldg(p + number(at));
   }
 #pragma unroll 1
   for (; v < v1; v += 32) {
@@ -188,7 +195,7 @@ __device__ __forceinline__ void stream(const Row<T>& r, int v0, int v1, F f) {
 #pragma unroll
     for (int i = 1; i < kAhead; ++i) w[i - 1] = w[i];
     const int at = v + 32 * kAhead;
-    if ((at < v1) & whole(at)) w[kAhead - 1] = __ldg(p + number(at));
+    if (((at < v1) & whole(at)) && ASV_GUARD(r, r.holds(number(at)))) w[kAhead - 1] = __ldg(p + number(at));
     f(now, number(v));
   }
 }
@@ -513,6 +520,7 @@ __device__ __noinline__ void collect(S& sh, const Row<T> r, float tau) {
   auto vector_at = [&](int x) {
     const int k = x / per_group, q = x - k * per_group;
     if (k >= n) return -1;
+    if (!ASV_GUARD(r, k >= 0 && k < kScan)) return -1;
     const int g = sh.scan[k] / S::kThreads, t = sh.scan[k] % S::kThreads, warp = t / 32;
     const int v = max(r.run_start(r.rank, warp), w0) + t % 32 + 32 * (g * per_group + q);
     return v < min(r.run_end(r.rank, warp), w1) ? v : -1;
@@ -525,7 +533,7 @@ __device__ __noinline__ void collect(S& sh, const Row<T> r, float tau) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       v[i] = vector_at(x + i * S::kThreads);
-      w[i] = v[i] >= 0 ? __ldg(p + v[i]) : make_uint4(0, 0, 0, 0);
+      w[i] = v[i] >= 0 && ASV_GUARD(r, r.holds(v[i])) ? __ldg(p + v[i]) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
@@ -603,7 +611,7 @@ __device__ __noinline__ void sort_list(S& sh, int n) {
 #pragma unroll 4
     for (int j = tid % g; j < n; j += g) rank += sh.place[j] > mine;
     for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (tid % g == 0 && e < n) sh.sorted[rank] = sh.list[e];
+    if (tid % g == 0 && e < n && rank < S::kList) sh.sorted[rank] = sh.list[e];
   }
   __syncthreads();
   constexpr int kEach = S::kList / S::kThreads;
@@ -837,6 +845,7 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
     return __float_as_int(fminf((sc.M - x) * width, float(kBins - 1)) + kMagic) - __float_as_int(kMagic);
   };
   auto add = [&](int bin, uint64_t m) {
+    if (!ASV_GUARD(r, bin >= 0 && bin < kBins)) return;
     const uint32_t low = uint32_t(m), old = atomicAdd(&sh.bins[bin].x, low);
     const uint32_t high = uint32_t(m >> 32) + (old + low < old ? 1u : 0u);
     if (high) atomicAdd(&sh.bins[bin].y, high);
@@ -1131,6 +1140,9 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   r.off = int((reinterpret_cast<uintptr_t>(first) % 16) / sizeof(T));
   r.base = first - r.off;
   r.V = a.V;
+#ifdef ASV_CHECKED
+  r.check_log = a.check_log;
+#endif
   r.vectors = (r.off + a.V + kVec<T> - 1) / kVec<T>;
   r.per_cta = (r.vectors + r.ctas - 1) / r.ctas;
   r.per_warp = (r.per_cta + S::kWarps - 1) / S::kWarps;
@@ -1175,7 +1187,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
       uint4 w[kFirstAhead];
 #pragma unroll
       for (int i = 0; i < kFirstAhead; ++i)
-        w[i] = v + 32 * i < end ? __ldg(p + v + 32 * i) : make_uint4(kNone, kNone, kNone, kNone);
+        w[i] = v + 32 * i < end && ASV_GUARD(r, r.holds(v + 32 * i)) ? __ldg(p + v + 32 * i)
+                                                                   : make_uint4(kNone, kNone, kNone, kNone);
 #pragma unroll
       for (int i = 0; i < kFirstAhead; ++i) most = max_nan(most, one(w[i]));
       left -= kFirstAhead;
@@ -1331,7 +1344,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
       return;
     }
   }
-  if (r.rank == 0 && tid == 0) {
+  if (r.rank == 0 && tid == 0 && ASV_GUARD(a, b >= 0 && b < a.B && n >= 0 && n < a.n && d.token >= -1 && d.token < a.V)) {
     if (!params_ok) atomicOr(a.status + b, ASV_REQ_BAD_PARAM);
     if (bad) atomicOr(a.status + b, ASV_REQ_NONFINITE);
     a.tokens[b * a.tokens_b + n * a.tokens_n] = d.token;
@@ -1357,7 +1370,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         const float q = ex2_approx(t) * inv;
         p[e] = d.token >= 0 && keep(x[e], i0 + e) ? fmaf(q, lo * kLn2Hi, q) : 0.0f;
       }
-      if (vectors && i0 >= 0 && i0 + kVec<T> <= a.V) {
+      if (vectors && i0 >= 0 && i0 + kVec<T> <= a.V && ASV_GUARD(a, b < a.B && n < a.n)) {
 #pragma unroll
         for (int e = 0; e < kVec<T>; e += 4)
           __stcs(reinterpret_cast<float4*>(to + i0 + e), make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]));
@@ -1458,10 +1471,13 @@ template <class T>
 cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.B * a.n;
   const int tuned = std::min(tuned_cluster(), kMaxCtas);
-  // CTAs to a row: as many as all rows together leave room for, each with enough of the row to be worth its exchanges.
+  // CTAs to a row: as many as all rows together leave room for, each with enough of the row to be worth its exchanges; the
+  // most where distributions are wanted and the rows in hand would not stay in L2 until they are written (352 fp32 rows of
+  // 128,256: 179 us with three, 169 with eight).
   auto ctas_of = [&](int slots) {
     if (tuned > 0) return tuned;
-    return int(std::clamp(std::min(slots / rows, (long long)a.V / 2048), 1ll, (long long)kMaxCtas));
+    const bool large = a.probs != nullptr && rows * a.V * (long long)sizeof(T) > (80ll << 20);
+    return int(std::clamp(std::min(large ? kMaxCtas : slots / rows, (long long)a.V / 2048), 1ll, (long long)kMaxCtas));
   };
   if (rows <= kSms / 2)
     return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(kSms * kAllCtas), kAllThreads, s);
