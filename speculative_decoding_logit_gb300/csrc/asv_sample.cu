@@ -74,6 +74,7 @@ struct __align__(16) Shared {
   uint16_t scan[kScan];                            // groups whose vectors are read again
   uint32_t table[PART != kFirst ? 1024 : 1];       // kExp2Table, where the whole row is weighed
   uint64_t chunk[kWarps];                          // sums of the warps' runs
+  uint64_t run_mass[PART != kFirst ? kWarps : 1], count[PART != kFirst ? kWarps : 1];  // the same of all, and counts
   uint64_t room[kWarps], room2[kWarps];
   uint64_t pick_before, pick_sum, total;
   float2 sums[kWarps];                             // the warps' maxima and fast sums next to them
@@ -81,6 +82,7 @@ struct __align__(16) Shared {
   float lead;                                      // the sum of threads' maxima from the bound on
   Cut cut;
   int n_scan, n_own, found, pick, first;
+  uint32_t least_key, most_key;                    // of what was collected
   long long row;                                   // the next one
 };
 
@@ -792,9 +794,9 @@ __device__ __forceinline__ int find_entry(S& sh, const Row<T>& r, uint64_t at, u
   return found;
 }
 
-// The index of the n-th entry with this key (n >= 1).
+// The index of the n-th entry with this key (n >= 1).  counted: the runs' counts are in sh.count already.
 template <class S, class T>
-__device__ __noinline__ int nth_equal(S& sh, const Row<T> r, uint32_t key, uint64_t n) {
+__device__ __noinline__ int nth_equal(S& sh, const Row<T> r, uint32_t key, uint64_t n, bool counted) {
   uint64_t own = 0;
   auto count = [&](const uint4& w, int v) {
     float x[kVec<T>];
@@ -807,13 +809,15 @@ __device__ __noinline__ int nth_equal(S& sh, const Row<T> r, uint32_t key, uint6
     }
     return uint64_t(n);
   };
-  stream(r, r.v0, r.v1, [&](const uint4& w, int v) { own += count(w, v); });
-  own = warp_sum(own);
-  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
-  row_sync();
+  if (!counted) {
+    stream(r, r.v0, r.v1, [&](const uint4& w, int v) { own += count(w, v); });
+    own = warp_sum(own);
+    if (threadIdx.x % 32 == 0) sh.count[threadIdx.x / 32] = own;
+    row_sync();
+  }
   // (the share n - 1 of the count, as find_run takes it: it is looked for in units, not in parts of 2^64)
   const int tid = threadIdx.x, runs = r.ctas * S::kWarps;
-  const uint64_t mine = tid < runs ? ld_peer_u64(sh.chunk + tid % S::kWarps, tid / S::kWarps) : 0;
+  const uint64_t mine = tid < runs ? ld_peer_u64(sh.count + tid % S::kWarps, tid / S::kWarps) : 0;
   const uint64_t incl = block_scan(mine, sh.room);
   if (tid == 0) sh.pick = 0;
   __syncthreads();
@@ -831,9 +835,230 @@ __device__ __noinline__ int nth_equal(S& sh, const Row<T> r, uint32_t key, uint6
       count, [&](float x, int) { return uint64_t(key_of(x) == key ? 1 : 0); });
 }
 
+// Where `target` = target_of(all) falls among bins, each CTA adding up a part of them over all CTAs (add_up(bin): to its own,
+// in place; mass(bin): it again).  To all: the bin (-1: none), the mass before it (`above` and the bins'), its own.
+struct Bin {
+  int bin;
+  uint64_t target, above, in, all;
+};
+
+template <class S, class T, class Add, class Mass, class G>
+__device__ __forceinline__ Bin find_bin(S& sh, const Row<T>& r, int bins, uint64_t above, Add add_up, Mass mass, G target_of) {
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int part = (bins + r.ctas - 1) / r.ctas, part0 = min(r.rank * part, bins), part1 = min(part0 + part, bins);
+  row_sync();
+  uint64_t sum = 0;
+  for (int i = part0 + tid; i < part1; i += S::kThreads) sum += add_up(i);
+  sum = block_scan(sum, sh.room);
+  if (tid == S::kThreads - 1) sh.total = sum;
+  if (tid == 0) sh.pick = -1;
+  row_sync();
+  const uint64_t mine = lane < r.ctas ? ld_peer_u64(&sh.total, lane) : 0;
+  uint64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < kMaxCtas; d *= 2) {
+    const uint64_t y = shfl_up_u64(upto, d);
+    if (lane >= d) upto += y;
+  }
+  Bin found;
+  found.all = __shfl_sync(0xffffffffu, upto, kMaxCtas - 1);
+  const uint64_t target = found.target = target_of(found.all);
+  upto += above;
+  const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && upto - mine < target && target <= upto);
+  const int owner = max(__ffs(holds) - 1, 0);
+  const uint64_t start = __shfl_sync(0xffffffffu, upto - mine, owner);
+  if (r.rank == owner) {
+    // the bin, each thread looking through a few
+    const int few = (part + S::kThreads - 1) / S::kThreads, i0 = min(part0 + tid * few, part1), i1 = min(i0 + few, part1);
+    uint64_t s = 0;
+    for (int i = i0; i < i1; ++i) s += mass(i);
+    uint64_t b = start + block_scan(s, sh.room) - s;
+    if (b < target && target <= b + s) {
+      for (int i = i0; i < i1; ++i) {
+        const uint64_t own = mass(i);
+        if (b < target && target <= b + own) {
+          sh.pick = i;
+          sh.pick_before = b;
+          sh.pick_sum = own;
+        }
+        b += own;
+      }
+    }
+  }
+  row_sync();
+  found.bin = int(ld_peer_u32(&sh.pick, owner));
+  found.above = ld_peer_u64(&sh.pick_before, owner);
+  found.in = ld_peer_u64(&sh.pick_sum, owner);
+  row_sync();  // (all have read what the owner found)
+  return found;
+}
+
 // The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
-// target_of(all): the last is the first with target <= the inclusive sum.  A histogram by value over the larger weights'
-// range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
+// target_of(all): the last is the first with target <= the inclusive sum.  Where that lies is estimated first: a histogram
+// by value, each weight as its bin's times 4096 (1 - d ln 2 width), d its distance from the bin's middle, in 32 bits and
+// without an exponential.  The bin (two, near a border) is a bracket, and one pass over the row weighs exactly: all, what is
+// above the bracket, a sum for each warp; and collects what is in it.  The sums say whether the target is in the bracket;
+// then the cut is among its entries, or, where they are more than the list holds and equal, the first so many of
+// them by index.  False: it is not, or they are not.
+// `sums`: the warps' masses of what is kept are left in sh.chunk (behind a row_sync).
+// (64 flat fp32 rows of 151,936: an exact histogram first, then the bin's entries, then two draws took 116 us.)
+template <bool MASS, class S, class T, class G>
+__device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, const Cut within, G target_of, bool sums,
+                                         Cut& cut) {
+  constexpr int kNear = 2 * kBins;            // 32-bit ones; the last takes what counts for nothing
+  constexpr float kSpan = 36.0f;              // log2 units down from the maximum (152 thousand entries below: 2^-18 of it)
+  constexpr float kStep = kSpan / float(kNear - 1);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  uint32_t* bins = reinterpret_cast<uint32_t*>(sh.bins);
+  const float width = float(kNear - 1) / kSpan * sc.c;
+  const bool all = within.key == 0;
+  auto place = [&](float x) { return __fmul_rn(sc.M - x, width); };  // (rounded alike in both passes)
+  for (int i = tid; i < kNear; i += S::kThreads) bins[i] = 0;
+  if (tid == 0) {
+    sh.n_own = 0;
+    sh.least_key = ~0u;
+    sh.most_key = 0;
+  }
+  __syncthreads();
+  stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
+    if (!(place(vector_max(w, static_cast<T*>(nullptr))) < float(kNear - 1))) return;
+    float x[kVec<T>];
+    unpack(w, x);
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) {
+      const float t = fminf(place(x[e]), float(kNear - 1)), m = __fadd_rn(t, kMagic);
+      const int bin = __float_as_int(m) - __float_as_int(kMagic);
+      const float d = t - (m - kMagic);
+      const uint32_t q = MASS ? uint32_t(__float_as_int(fmaf(d, -4096.0f * kLn2Hi * kStep, kMagic + 4096.0f)) - __float_as_int(kMagic)) : 1u;
+      bool counts = bin < kNear - 1;
+      if (!all) counts = counts && within.keeps(key_of(x[e]), v * kVec<T> - r.off + e);
+      if (counts && ASV_GUARD(r, bin >= 0 && bin < kNear)) atomicAdd(bins + bin, q);
+    }
+  });
+  // (a bin's sum over all CTAs, 2^19 entries of 4109 at most, has room too)
+  auto mass = [&](int i) {
+    return MASS ? uint64_t(float(bins[i]) * ex2_approx(float(i) * -kStep) * 1048576.0f) : uint64_t(bins[i]);
+  };
+  const Bin near = find_bin(
+      sh, r, kNear - 1, 0,
+      [&](int i) {
+        uint32_t own = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCtas; ++c)
+          if (c < r.ctas) own += ld_peer_u32(bins + i, c);
+        bins[i] = own;
+        return mass(i);
+      },
+      mass, target_of);
+  if (near.bin < 0) return false;
+  const uint64_t margin = MASS ? near.all >> 16 : 0;
+  const int b0 = max(near.bin - int(near.target - near.above <= margin), 0);
+  const int b1 = min(near.bin + int(near.above + near.in - near.target < margin), kNear - 2);
+
+  // ---- exactly
+  const float m0 = kMagic + float(b0), m1 = kMagic + float(b1);
+  const bool weigh = MASS || sums;
+  uint64_t total = 0, above = 0;
+  uint32_t count = 0, low = ~0u, high = 0;
+  stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
+    const float most = vector_max(w, static_cast<T*>(nullptr));
+    if (MASS ? !weighs(most, sc) : __fadd_rn(place(most), kMagic) > m1) return;
+    pairs<T>(w, [&](float x0, float x1, int e) {
+      const float x[2] = {x0, x1};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = v * kVec<T> - r.off + e + h;
+        const float m = __fadd_rn(place(x[h]), kMagic);
+        uint64_t u = weigh ? units_of(x[h], sc, sh.table) : 0;
+        bool in = (m >= m0) & (m <= m1);  // (an entry that is not the row's is far below)
+        if (!all) {
+          const bool keeps = within.keeps(key_of(x[h]), i);
+          u = keeps ? u : 0;
+          in = in && keeps;
+        }
+        if (MASS) total += u;
+        above += m < m0 ? u : 0;
+        if (in) {
+          const uint32_t key = key_of(x[h]);
+          ++count;
+          low = min(low, key);
+          high = max(high, key);
+          const int to = atomicAdd(&sh.n_own, 1);
+          if (to < S::kList) sh.own[to] = make_uint2(key, uint32_t(i));
+        }
+      }
+    });
+  });
+  total = warp_sum(total);
+  above = warp_sum(above);
+  count = __reduce_add_sync(0xffffffffu, count);
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    sh.run_mass[warp] = total;
+    sh.chunk[warp] = above;
+    sh.count[warp] = count;
+    atomicMin(&sh.least_key, low);
+    atomicMax(&sh.most_key, high);
+  }
+  row_sync();
+  uint64_t before = near.above, target = near.target;  // (counts are exact)
+  if (MASS) {
+    uint64_t x = 0;
+    for (int i = lane; i < r.ctas * S::kWarps; i += 32) x += ld_peer_u64(sh.run_mass + i % S::kWarps, i / S::kWarps);
+    target = target_of(warp_sum(x));
+    before = all_chunks(sh, r.ctas);
+  }
+  low = lane < r.ctas ? ld_peer_u32(&sh.least_key, lane) : ~0u;
+  high = lane < r.ctas ? ld_peer_u32(&sh.most_key, lane) : 0;
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  const int n = share_out(sh, sc, r.ctas, true);
+  const int runs = r.ctas * S::kWarps;
+  const uint64_t mine = tid < runs ? ld_peer_u64(sh.count + tid % S::kWarps, tid / S::kWarps) : 0;
+  row_sync();  // (all have read the masses above)
+  if (target <= before || n == 0) return false;
+  if (n > 0) {
+    sort_list(sh, n);
+    if (tid == 0) sh.first = -1;
+    __syncthreads();
+    for (int e = tid; e < n; e += S::kThreads) {
+      const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = before + (MASS ? sh.before[e] : uint64_t(e));
+      if (b < target && target <= b + m) {
+        sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
+        sh.first = e;
+      }
+    }
+    __syncthreads();
+    const int last = sh.first;
+    if (last < 0) return false;
+    cut = sh.cut;
+    for (int e = tid; e <= last; e += S::kThreads) {
+      const int v = int(sh.sorted[e].y + uint32_t(r.off)) / kVec<T>, c = v / r.per_cta, run = (v - c * r.per_cta) / r.per_warp;
+      if (c == r.rank && ASV_GUARD(r, run >= 0 && run < S::kWarps))
+        atomicAdd(reinterpret_cast<unsigned long long*>(sh.chunk + run), (unsigned long long)weight_in(sh.sorted[e]));
+    }
+  } else {
+    if (low != high) return false;
+    const uint64_t each = weight(value_of(low), sc, sh.table), step = MASS ? each : 1;
+    const uint64_t upto = block_scan(mine, sh.room);
+    if (tid == S::kThreads - 1) sh.total = upto;
+    __syncthreads();
+    const uint64_t have = sh.total;
+    if (step == 0 || target - before > have * step) return false;
+    const uint64_t want = (target - before + step - 1) / step;
+    if (tid / S::kWarps == r.rank && tid < runs)
+      sh.chunk[tid % S::kWarps] += min(want - min(want, upto - mine), mine) * each;
+    cut = {low, INT_MAX};
+    if (want < have) cut.index = nth_equal(sh, r, low, want, true);
+  }
+  row_sync();
+  return true;
+}
+
+// The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
+// target_of(all): the last is the first with target <= the inclusive sum.  For rows that search_near does not settle.  A
+// histogram by value over the larger weights' range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
 // on.  The bins are added up a part by each CTA.
 template <bool MASS, class S, class T, class G>
 __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const Cut within, G target_of) {
@@ -851,7 +1076,6 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
     if (high) atomicAdd(&sh.bins[bin].y, high);
   };
   const bool all = within.key == 0;
-  const int part = (kBins + r.ctas - 1) / r.ctas, part0 = min(r.rank * part, kBins), part1 = min(part0 + part, kBins);
   uint32_t lo = 1, hi = key_of(sc.M);
   int shift = 32, first_bin = 0;
   uint64_t above = 0, target = 0, in_bin = 0;
@@ -926,55 +1150,22 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
         if (m != 0) add(int((hi - key) >> shift), m);
       });
     }
-    row_sync();
-    // this CTA's part of the bins, of all CTAs, in place (nobody else reads them here), and their sum
-    uint64_t sum = 0;
-    for (int i = part0 + tid; i < part1; i += S::kThreads) {
-      uint64_t own = 0;
+    auto mass = [&](int i) { return *reinterpret_cast<const uint64_t*>(sh.bins + i); };
+    const Bin found = find_bin(
+        sh, r, kBins, above,
+        [&](int i) {
+          uint64_t own = 0;
 #pragma unroll
-      for (int c = 0; c < kMaxCtas; ++c)
-        if (c < r.ctas) own += ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.bins + i), c);
-      *reinterpret_cast<uint64_t*>(sh.bins + i) = own;
-      sum += own;
-    }
-    sum = block_scan(sum, sh.room);
-    if (tid == S::kThreads - 1) sh.total = sum;
-    if (tid == 0) sh.pick = -1;
-    row_sync();
-    const uint64_t mine = lane < r.ctas ? ld_peer_u64(&sh.total, lane) : 0;
-    uint64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < kMaxCtas; d *= 2) {
-      const uint64_t y = shfl_up_u64(upto, d);
-      if (lane >= d) upto += y;
-    }
-    if (level == 0) target = target_of(__shfl_sync(0xffffffffu, upto, kMaxCtas - 1));
-    upto += above;
-    const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && upto - mine < target && target <= upto);
-    const int owner = max(__ffs(holds) - 1, 0);
-    const uint64_t start = __shfl_sync(0xffffffffu, upto - mine, owner);
-    if (r.rank == owner) {
-      // the bin, each thread looking through a few
-      const int few = (part + S::kThreads - 1) / S::kThreads, i0 = min(part0 + tid * few, part1), i1 = min(i0 + few, part1);
-      uint64_t s = 0;
-      for (int i = i0; i < i1; ++i) s += *reinterpret_cast<const uint64_t*>(sh.bins + i);
-      uint64_t b = start + block_scan(s, sh.room) - s;
-      if (b < target && target <= b + s) {
-        for (int i = i0; i < i1; ++i) {
-          const uint64_t own = *reinterpret_cast<const uint64_t*>(sh.bins + i);
-          if (b < target && target <= b + own) {
-            sh.pick = i;
-            sh.pick_before = b;
-            sh.pick_sum = own;
-          }
-          b += own;
-        }
-      }
-    }
-    row_sync();
-    const int bin = max(int(ld_peer_u32(&sh.pick, owner)), 0);
-    above = ld_peer_u64(&sh.pick_before, owner);
-    in_bin = ld_peer_u64(&sh.pick_sum, owner);
+          for (int c = 0; c < kMaxCtas; ++c)
+            if (c < r.ctas) own += ld_peer_u64(reinterpret_cast<const uint64_t*>(sh.bins + i), c);
+          *reinterpret_cast<uint64_t*>(sh.bins + i) = own;
+          return own;
+        },
+        mass, [&](uint64_t sum) { return level == 0 ? target_of(sum) : target; });
+    const int bin = max(found.bin, 0);
+    target = found.target;
+    above = found.above;
+    in_bin = found.in;
     if (level == 0) {
       // keys that the bin's values may have (its own test stays)
       first_bin = bin;
@@ -986,13 +1177,12 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
       hi -= uint32_t(bin) << shift;
       lo = max(lo, hi - ((1u << shift) - 1u));
     }
-    row_sync();  // (all have read what the owner found)
   }
   // one value, and more entries with it than the list holds: of equal values the lowest indices
   const uint64_t each = MASS ? weight(value_of(hi), sc, sh.table) : 1;
   const uint64_t want = (target - above + each - 1) / each;
   Cut cut = {hi, INT_MAX};
-  if (want < in_bin / each) cut.index = nth_equal(sh, r, hi, want);
+  if (want < in_bin / each) cut.index = nth_equal(sh, r, hi, want, false);
   return cut;
 }
 
@@ -1037,71 +1227,47 @@ __device__ __forceinline__ uint64_t kept_sum(const uint4& w, int v, const Row<T>
   return sum;
 }
 
-// The same by fast sums.
-template <class T>
-__device__ __forceinline__ void add_kept(Partial& s, const uint4& w, int v, const Row<T>& r, const Scale& sc, const Kept& keep) {
-  const float top = vector_max(w, static_cast<T*>(nullptr));
-  if (top < keep.value) return;
-  float x[kVec<T>];
-  unpack(w, x);
-#pragma unroll
-  for (int e = 0; e < kVec<T>; ++e)
-    if (!keep(x[e], v * kVec<T> - r.off + e)) x[e] = -INFINITY;
-  add_weights(s, x, top, sc.c);
-}
-
-// A draw from the kept entries by the warps' fast sums of them (sh.chunk, behind a row_sync); fine: from all of them, by
-// their finer sums.  A token < 0: too near a border to say.
+// A draw from the whole row by the warps' finer sums (sh.chunk, behind a row_sync).  A token < 0: too near a border to say.
 template <class S, class T>
-__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, const Kept keep, bool fine, uint64_t draw) {
+__device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, uint64_t draw) {
   const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
   d.total = sh.total;
   // Of sums b before a border and a behind it the draw u compares (1 - u) b with u a.  Next to the border both are u (1 - u)
-  // of the mass, 1/4 at most, and each is off by 2^-18 (2^-20) of itself; the run's own sum counts once as the rows streamed
-  // and once as it is taken apart here, each off by as much too.
+  // of the mass, 1/4 at most, and each is off by 2^-20 of itself; the run's own sum counts once as the rows streamed and
+  // once as it is taken apart here, each off by as much too.
   const int run = sh.pick;
-  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % S::kWarps, run / S::kWarps)) >> (fine ? kFineBits : kFastBits)) + 64;
+  const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % S::kWarps, run / S::kWarps)) >> kFineBits) + 64;
+  const Kept keep = {{0u, INT_MAX}, -INFINITY};
   d.token = find_entry(
       sh, r, at, margin,
       [&](int v0, int v1) {
         Partial s;
         stream(r, v0, v1, [&](const uint4& w, int v) {
-          if (fine) {
-            float x[kVec<T>];
-            unpack(w, x);
-            add_weights_fine(s, x, vector_max(w, static_cast<T*>(nullptr)), sc.c, sc.c_lo);
-          } else {
-            add_kept(s, w, v, r, sc, keep);
-          }
+          float x[kVec<T>];
+          unpack(w, x);
+          add_weights_fine(s, x, vector_max(w, static_cast<T*>(nullptr)), sc.c, sc.c_lo);
         });
-        return warp_sum(units_of_sum(s, sc, fine));
+        return warp_sum(units_of_sum(s, sc, true));
       },
       [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, kExp2Table); },
-      [&](float x, int i) { return keep(x, i) ? weight(x, sc, kExp2Table) : uint64_t(0); });
+      [&](float x, int) { return weight(x, sc, kExp2Table); });
   d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, kExp2Table) : 0;
   return d;
 }
 
-// The warps' fast sums of the kept entries, to sh.chunk.
+// A draw from the kept entries by exact sums.  summed: the warps' are in sh.chunk already.
 template <class S, class T>
-__device__ __noinline__ void fast_sums(S& sh, const Row<T> r, const Scale sc, const Kept keep) {
-  Partial s;
-  stream(r, r.v0, r.v1, [&](const uint4& w, int v) { add_kept(s, w, v, r, sc, keep); });
-  const uint64_t w = warp_sum(units_of_sum(s, sc, false));
-  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = w;
-}
-
-// A draw from the kept entries by exact sums.
-template <class S, class T>
-__device__ __noinline__ Drawn draw_exact(S& sh, const Row<T> r, const Scale sc, const Kept keep, uint64_t draw) {
+__device__ __noinline__ Drawn draw_exact(S& sh, const Row<T> r, const Scale sc, const Kept keep, bool summed, uint64_t draw) {
   uint64_t own = 0;
   auto sum = [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, sh.table); };
-  stream(r, r.v0, r.v1, [&](const uint4& w, int v) { own += sum(w, v); });
-  own = warp_sum(own);
-  if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
-  row_sync();
+  if (!summed) {
+    stream(r, r.v0, r.v1, [&](const uint4& w, int v) { own += sum(w, v); });
+    own = warp_sum(own);
+    if (threadIdx.x % 32 == 0) sh.chunk[threadIdx.x / 32] = own;
+    row_sync();
+  }
   const uint64_t at = find_run(sh, r, draw);
   __syncthreads();
   Drawn d;
@@ -1310,7 +1476,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         else row_sync();  // (the peers have read the candidates)
       } else if (trusted && sums && !nucleus) {
         row_sync();
-        d = draw_fast(sh, r, sc, Kept{cut, -INFINITY}, true, draw);
+        d = draw_fast(sh, r, sc, draw);
         settled = d.token >= 0;
       }
     }
@@ -1318,25 +1484,28 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
       if (!settled) {
         for (int i = tid; i < 1024; i += S::kThreads) sh.table[i] = kExp2Table[i];
         __syncthreads();
-        if (k > 0) cut = search<false>(sh, r, sc, cut, [&](uint64_t) { return uint64_t(k); });
+        bool summed = false;  // what is kept, for each warp
+        if (k > 0) {
+          auto target = [&](uint64_t) { return uint64_t(k); };
+          summed = search_near<false>(sh, r, sc, cut, target, !nucleus, cut);
+          if (!summed) cut = search<false>(sh, r, sc, Cut{0u, INT_MAX}, target);
+        }
         if (nucleus) {
           const Cut first_k = cut;
           const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
-          cut = search<true>(sh, r, sc, first_k, [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); });
+          auto target = [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); };
+          summed = search_near<true>(sh, r, sc, first_k, target, true, cut);
+          if (!summed) cut = search<true>(sh, r, sc, first_k, target);
           if (cut.key == first_k.key) cut.index = min(cut.index, first_k.index);
         }
         if (least > 0) {
           const uint32_t key = least_key(sh, sc, least);
-          if (key > cut.key) cut = {key, INT_MAX};
+          if (key > cut.key) {
+            cut = {key, INT_MAX};
+            summed = false;
+          }
         }
-        const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
-        d.token = -1;
-        if (cut.key != 0 && fabsf(sc.M * sc.c) < kFastRange - 128.0f) {
-          fast_sums(sh, r, sc, keep);
-          row_sync();
-          d = draw_fast(sh, r, sc, keep, false, draw);
-        }
-        if (d.token < 0) d = draw_exact(sh, r, sc, keep, draw);
+        d = draw_exact(sh, r, sc, Kept{cut, cut.key == 0 ? -INFINITY : value_of(cut.key)}, summed, draw);
       }
     } else if (!settled) {
       if (r.rank == 0 && tid == 0) a.tokens[b * a.tokens_b + n * a.tokens_n] = kLeft;
