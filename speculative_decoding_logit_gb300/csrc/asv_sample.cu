@@ -82,6 +82,7 @@ struct __align__(16) Shared {
   float lead;                                      // the sum of threads' maxima from the bound on
   Cut cut;
   int n_scan, n_own, found, pick, first;
+  int first_own;                                   // of the list's, this CTA's first
   uint32_t least_key, most_key;                    // of what was collected
   long long row;                                   // the next one
 };
@@ -562,6 +563,7 @@ __device__ __noinline__ int share_out(S& sh, const Scale sc, int ctas, bool weig
   }
   if (__any_sync(0xffffffffu, lane < ctas && (own > S::kList || upto > S::kList))) return -1;
   const int n = __shfl_sync(0xffffffffu, upto, kMaxCtas - 1);
+  if (threadIdx.x == int(cluster_rank())) sh.first_own = upto - own;
   for (int i0 = 0; i0 < n; i0 += S::kThreads) {
     const int i = i0 + threadIdx.x;
     int c = 0, start = 0;
@@ -1019,24 +1021,38 @@ __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, 
   row_sync();  // (all have read the masses above)
   if (target <= before || n == 0) return false;
   if (n > 0) {
-    sort_list(sh, n);
+    // each CTA has its own candidates, a group of threads for one: the mass before it, and whether it is the last
+    const int first = sh.first_own, m = sh.n_own;
     if (tid == 0) sh.first = -1;
     __syncthreads();
-    for (int e = tid; e < n; e += S::kThreads) {
-      const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = before + (MASS ? sh.before[e] : uint64_t(e));
-      if (b < target && target <= b + m) {
-        sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
+    int g = 1;
+    while (g < 32 && 2 * g * m <= S::kThreads) g *= 2;
+    for (int e0 = 0; e0 < m; e0 += S::kThreads / g) {
+      const int e = e0 + tid / g;
+      const uint4 y = sh.list[first + min(e, m - 1)];
+      uint64_t b = 0;
+#pragma unroll 4
+      for (int j = tid % g; j < n; j += g) {
+        const uint4 z = sh.list[j];
+        if ((z.x > y.x) | ((z.x == y.x) & (z.y < y.y))) b += MASS ? weight_in(z) : 1;
+      }
+      for (int o = 1; o < g; o *= 2) b += __shfl_xor_sync(0xffffffffu, b, o);
+      b += before;
+      if (tid % g == 0 && e < m && b < target && target <= b + (MASS ? weight_in(y) : 1)) {
+        sh.cut = {y.x, int(y.y)};
         sh.first = e;
       }
     }
-    __syncthreads();
-    const int last = sh.first;
-    if (last < 0) return false;
-    cut = sh.cut;
-    for (int e = tid; e <= last; e += S::kThreads) {
-      const int v = int(sh.sorted[e].y + uint32_t(r.off)) / kVec<T>, c = v / r.per_cta, run = (v - c * r.per_cta) / r.per_warp;
-      if (c == r.rank && ASV_GUARD(r, run >= 0 && run < S::kWarps))
-        atomicAdd(reinterpret_cast<unsigned long long*>(sh.chunk + run), (unsigned long long)weight_in(sh.sorted[e]));
+    row_sync();
+    const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && int(ld_peer_u32(&sh.first, min(lane, r.ctas - 1))) >= 0);
+    if (holds == 0) return false;
+    const int owner = __ffs(holds) - 1;
+    cut = {ld_peer_u32(&sh.cut.key, owner), int(ld_peer_u32(&sh.cut.index, owner))};
+    for (int e = tid; e < m; e += S::kThreads) {
+      const uint4 y = sh.list[first + e];
+      const int v = int(y.y + uint32_t(r.off)) / kVec<T>, run = (v - r.rank * r.per_cta) / r.per_warp;
+      if (cut.keeps(y.x, int(y.y)) && ASV_GUARD(r, run >= 0 && run < S::kWarps))
+        atomicAdd(reinterpret_cast<unsigned long long*>(sh.chunk + run), (unsigned long long)weight_in(y));
     }
   } else {
     if (low != high) return false;
