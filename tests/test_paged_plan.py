@@ -29,7 +29,7 @@ def _plan(m, pool=None, B=2, N=3, **kw):
 
 
 def test_sizes(m):
-    for kw in (dict(B=-1), dict(B=16385), dict(N=-1)):
+    for kw in (dict(B=-1), dict(B=16385), dict(N=-1), dict(N=(1 << 30) + 1)):
         assert _plan(m, **kw) == SHAPE
     for kw in (dict(max_pages=-1), dict(pool_size=-1), dict(page_size=0), dict(max_pages=1 << 28),
                dict(block_table_stride=3), dict(block_table_stride=-4)):
@@ -291,6 +291,18 @@ def test_slots_past_32_bits(m):
     s.free[:3] = torch.tensor([4000, 2047, 4096], dtype=torch.int32)
     got = m.paged_plan(s.cache_len, s.new_len, s.table, s.held, s.free, s.count, 1 << 20, max_tokens=3)
     assert got.slots.tolist() == [(4096 << 20) + i for i in range(3)]
+
+
+@pytest.mark.gpu
+def test_no_requests(m):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = m.PagedPlanOutput(torch.full((1,), 7, **i32), torch.full((5,), 7, dtype=torch.int64, device="cuda"),
+                            torch.full((5,), 7, **i32), torch.full((5,), 7, **i32), torch.zeros(0, **i32))
+    none, count = torch.zeros(0, **i32), torch.tensor([3], **i32)
+    m.paged_plan(none, none, torch.zeros(0, 4, **i32), none, torch.arange(3, **i32), count, 16, out=out)
+    assert out.indptr.tolist() == [0] and int(count) == 3
+    for t in (out.slots, out.positions, out.requests):
+        assert t.tolist() == [-1] * 5
 
 
 @pytest.mark.gpu

@@ -402,3 +402,32 @@ def test_many_rows(m, dtype, rows):
     x[5, 0, 17], x[6, 0, 3] = math.nan, math.inf
     got = m.sample_tokens(x.cuda(), u.cuda(), top_p=0.9)
     assert got.req_status.nonzero().flatten().tolist() == [5, 6] and int(got.tokens.min()) == -1
+
+
+def _in_general(V, kind):
+    g = torch.Generator().manual_seed(V)
+    if kind == "pairs":          # two values next to each other, each many times
+        return 1.0 + 1e-4 * torch.randint(0, 2, (V,), generator=g)
+    if kind == "steps":          # equal values that a border falls among
+        return torch.randint(-40, 0, (V,), generator=g) / 16.0
+    if kind == "wide":           # more decades than weights have
+        return -200 * torch.rand(V, generator=g)
+    return 2 * torch.randn(V, generator=g)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 80])
+@pytest.mark.parametrize("kind", ["pairs", "steps", "wide", "flat"])
+def test_borders_of_rows_in_general(m, dtype, rows, kind):
+    """Rows whose kept set is too large to be listed: borders among equal values, among values that no histogram by value
+    tells apart, of a nucleus within a top-k, and min-p's within them."""
+    V = 30011
+    few = [0, rows // 2, rows - 1][:1 if rows == 1 else 3]
+    x = _in_general(V, kind).to(dtype).expand(rows, 1, V).contiguous()
+    u = _draws(rows, 1, V)
+    for T, k, p, least in ((1.0, 0, 0.5, 0.0), (1.0, 0, 0.97, 0.0), (1000.0, 0, 0.9, 0.0), (1.0, 9000, 1.0, 0.0),
+                           (1.0, 20000, 0.6, 0.0), (0.7, 0, 0.9, 0.02), (1000.0, 15000, 1.0, 0.9), (1e-3, 12000, 0.999, 0.0)):
+        got = m.sample_tokens(x.cuda(), u.cuda(), temperature=T, top_k=k, top_p=p, min_p=least, probs=True)
+        got = m.SampleOutput(*(t.cpu()[few] for t in (got.tokens, got.logprobs, got.probs, got.req_status)))
+        _compare(x[few], u[few], got, T, k, p, least)
