@@ -594,8 +594,8 @@ typedef struct {
  * within it), out_positions (cache_len[b] + i) and out_requests (b), -1 in all three for rows behind the last; each may
  * be NULL.  cache_len and new_len are not changed.  ASV_REQ_* bits are ORed into out_req_status [B].  A pool whose count is
  * not within [0, pool_size] flags every request ASV_REQ_BAD_PAGE and changes nothing.  The buffers must not overlap.
- * B <= 16384.  One launch, or two where N > 8192.  Checks: sizes (ASV_ERR_SHAPE); for B > 0 alignment (4 bytes, out_slots 8: ASV_ERR_ALIGN), the
- * required pointers (ASV_ERR_NULL).
+ * B <= 16384, N <= 2^30.  One launch, or two where N > 8192.  Checks: sizes (ASV_ERR_SHAPE); for B > 0 alignment (4 bytes,
+ * out_slots 8: ASV_ERR_ALIGN), the required pointers (ASV_ERR_NULL).
  */
 asv_status paged_plan(const int32_t* cache_len, const int32_t* new_len, int B, const asv_page_pool* pool,
                       const uint8_t* release, int N, int32_t* out_indptr, int64_t* out_slots, int32_t* out_positions,

@@ -91,6 +91,7 @@ inline size_t paged_workspace_bytes(int head_dim) {
 }
 
 constexpr int kPlanMaxRequests = 16384;  // three words each in one CTA's shared memory
+constexpr int kPlanMaxRows = 1 << 30;  // (a thread's next rows are still numbers of 32 bits)
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_paged_attention(const AttendArgs& a, int dtype, cudaStream_t s);

@@ -135,10 +135,20 @@ asv_status paged_plan(const int32_t* cache_len, const int32_t* new_len, int B, c
                       int32_t* out_requests, uint32_t* out_req_status, cudaStream_t stream) {
   if (!pool) return ASV_ERR_NULL;
   const asv_page_pool& p = *pool;
-  if (B < 0 || B > asv::kPlanMaxRequests || N < 0 || p.max_pages < 0 || p.pool_size < 0 || p.page_size < 1 ||
+  if (B < 0 || B > asv::kPlanMaxRequests || N < 0 || N > asv::kPlanMaxRows || p.max_pages < 0 || p.pool_size < 0 || p.page_size < 1 ||
       (long long)p.max_pages * p.page_size > 0x7fff0000LL)
     return ASV_ERR_SHAPE;
-  if (B == 0) return ASV_OK;
+  if (B == 0) {  // no rows but those behind the last
+    cudaError_t e = cudaSuccess;
+    auto fill = [&](void* to, int byte, size_t bytes) {
+      if (e == cudaSuccess && to && bytes > 0) e = cudaMemsetAsync(to, byte, bytes, stream);
+    };
+    fill(out_indptr, 0, sizeof(int32_t));
+    fill(out_slots, 0xff, N * sizeof(int64_t));
+    fill(out_positions, 0xff, N * sizeof(int32_t));
+    fill(out_requests, 0xff, N * sizeof(int32_t));
+    return e == cudaSuccess ? ASV_OK : asv::record_cuda_error(e);
+  }
   if (B > 1 && p.max_pages > 0 && p.block_table_stride < p.max_pages) return ASV_ERR_SHAPE;  // rows that overlap
   if (!aligned(cache_len, 4) || !aligned(new_len, 4) || !aligned(p.block_table, 4) || !aligned(p.held, 4) ||
       !aligned(p.free_pages, 4) || !aligned(p.free_count, 4) || !aligned(out_indptr, 4) || !aligned(out_slots, 8) ||
