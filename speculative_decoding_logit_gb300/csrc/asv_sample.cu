@@ -35,6 +35,7 @@ namespace {
 constexpr int kNucleus = 64;             // maxima of threads that a nucleus is first looked for above
 constexpr int kGroups = 20;              // groups of a thread's vectors, at most
 constexpr int kScan = 1024;              // groups that are read again, at most
+constexpr int kFew = 128;                // candidates up to which each is compared with each
 constexpr int kBins = 2048;
 constexpr int kMaxCtas = 8;
 constexpr int kAhead = 4;                // vectors a lane has in flight
@@ -58,13 +59,16 @@ constexpr int kLeft = INT_MIN, kTaken = INT_MIN + 1;
 template <int THREADS, Part PART>
 struct __align__(16) Shared {
   static constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+  static constexpr int kBuckets = THREADS < 256 ? THREADS : 256;
   static constexpr int kList = THREADS < 256 ? 256 : 512;  // candidates that are compared with each other
   union {                                          // one after the other
     float group[PART != kRest ? (kGroups + 1) * THREADS : 1];  // maxima of groups of a thread's vectors; of the row's ends
     uint2 bins[PART != kFirst ? kBins : 1];        // a histogram's 64-bit sums
     struct {
-      uint64_t place[kList];                       // the candidates' places in the order
       uint4 sorted[kList];                         // the candidates in order
+      uint64_t place[kFew];                        // the candidates' places in the order, where there are few
+      uint64_t bin_mass[kBuckets];
+      uint32_t bin_start[kBuckets];
     };
   };
   uint4 list[kList];                               // candidates of the row: key, index, weight
@@ -79,12 +83,13 @@ struct __align__(16) Shared {
   uint64_t pick_before, pick_sum, total;
   float2 sums[kWarps];                             // the warps' maxima and fast sums next to them
   float4 ends;                                     // of the CTA: maximum, bound of the candidates, whether it is bad, sum
-  float lead;                                      // the sum of threads' maxima from the bound on
+  float2 lead[2];                                  // a bound, and the sum of threads' maxima from it on; a lower one
   Cut cut;
   int n_scan, n_own, found, pick, first;
   int first_own;                                   // of the list's, this CTA's first
   uint32_t least_key, most_key;                    // of what was collected
   long long row;                                   // the next one
+  __device__ __forceinline__ uint32_t* bin_ends() { return reinterpret_cast<uint32_t*>(tops); }  // (read by then)
 };
 
 // ------------------------------------------------------------------ a row
@@ -598,24 +603,62 @@ __device__ __forceinline__ uint64_t part_of(uint64_t part, uint64_t mass) {
   return __umul64hi(part, mass) + (part * mass != 0 ? 1 : 0);
 }
 
-// The candidates in order, to sh.sorted, and the mass before each, to sh.before: a candidate's rank is the number of those
-// before it, a group of threads counts for one where there are few.  (A warp's bitonic network took 1.6 us at 100
-// candidates, its shuffles one behind the other.)
-template <class S>
-__device__ __noinline__ void sort_list(S& sh, int n) {
+// Numbers 0 .. n - 1 (n <= kList) by bins: bin b has sh.scan[bin_start[b]] up to sh.scan[bin_ends()[b] - 1], in any order.
+// (Each candidate against each takes 1 us at 75 of them, this 2.5; at 350 they take 12 and 4.)
+template <class S, class F>
+__device__ __forceinline__ void by_bins(S& sh, int n, F bin_of) {
   const int tid = threadIdx.x;
-  for (int e = tid; e < n; e += S::kThreads) sh.place[e] = (uint64_t(sh.list[e].x) << 32) | ~sh.list[e].y;
+  uint32_t *count = sh.bin_ends(), *start = sh.bin_start;
+  if (tid < S::kBuckets) count[tid] = 0;
+  __syncthreads();
+  for (int e = tid; e < n; e += S::kThreads) atomicAdd(count + bin_of(e), 1u);
+  __syncthreads();
+  const uint64_t own = tid < S::kBuckets ? count[tid] : 0;
+  const uint32_t upto = uint32_t(block_scan(own, sh.room) - own);
+  if (tid < S::kBuckets) start[tid] = count[tid] = upto;
+  __syncthreads();
+  for (int e = tid; e < n; e += S::kThreads) sh.scan[atomicAdd(count + bin_of(e), 1u)] = uint16_t(e);
+  __syncthreads();
+}
+
+// Few candidates' ranks: a group of threads counts for one those before it.
+template <class S>
+__device__ __forceinline__ void sort_few(S& sh, int n) {
+  const int tid = threadIdx.x;
+  if (tid < n) sh.place[tid] = (uint64_t(sh.list[tid].x) << 32) | ~sh.list[tid].y;
   __syncthreads();
   int g = 1;
   while (g < 32 && 2 * g * n <= S::kThreads) g *= 2;
-  for (int e0 = 0; e0 < n; e0 += S::kThreads / g) {
-    const int e = e0 + tid / g;
-    const uint64_t mine = sh.place[min(e, n - 1)];
-    int rank = 0;
+  const int e = tid / g;  // (n <= kFew <= kThreads)
+  const uint64_t mine = sh.place[min(e, n - 1)];
+  int rank = 0;
 #pragma unroll 4
-    for (int j = tid % g; j < n; j += g) rank += sh.place[j] > mine;
-    for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (tid % g == 0 && e < n && rank < S::kList) sh.sorted[rank] = sh.list[e];
+  for (int j = tid % g; j < n; j += g) rank += sh.place[j] > mine;
+  for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  if (tid % g == 0 && e < n) sh.sorted[rank] = sh.list[e];
+}
+
+// The candidates in order, to sh.sorted, and the mass before each, to sh.before.  Where they are many, by bins of their
+// values, from `top` down to `low`, and within a bin by comparison.
+template <class S>
+__device__ __noinline__ void sort_list(S& sh, int n, float top, float low) {
+  const int tid = threadIdx.x;
+  if (n <= kFew) {
+    sort_few(sh, n);
+  } else {
+    const float scale = top > low ? float(S::kBuckets) / (top - low) : 0.0f;
+    auto bin_of = [&](int e) { return int(fminf((top - value_of(sh.list[e].x)) * scale, float(S::kBuckets - 1))); };
+    by_bins(sh, n, bin_of);
+    for (int e = tid; e < n; e += S::kThreads) {
+      const uint4 mine = sh.list[e];
+      const int bin = bin_of(e), end = int(sh.bin_ends()[bin]);
+      int rank = int(sh.bin_start[bin]);
+      for (int q = rank; q < end; ++q) {
+        const uint4& other = sh.list[sh.scan[q]];
+        rank += (other.x > mine.x) | ((other.x == mine.x) & (other.y < mine.y));
+      }
+      sh.sorted[rank] = mine;
+    }
   }
   __syncthreads();
   constexpr int kEach = S::kList / S::kThreads;
@@ -634,15 +677,15 @@ __device__ __noinline__ void sort_list(S& sh, int n) {
   __syncthreads();
 }
 
-// The mass of the first m candidates with lower indices than each, to sh.before.  A group of threads has one where there
-// are few.
+// The mass of the first m candidates with lower indices than each, to sh.before.  Where they are many, by bins of the V
+// indices.
 template <class S>
-__device__ __forceinline__ void masses_by_index(S& sh, int m) {
+__device__ __forceinline__ void masses_by_index(S& sh, int m, int V) {
   const int tid = threadIdx.x;
-  int g = 1;
-  while (g < 32 && 2 * g * m <= S::kThreads) g *= 2;
-  for (int e0 = 0; e0 < m; e0 += S::kThreads / g) {
-    const int e = e0 + tid / g;
+  if (m <= kFew) {
+    int g = 1;
+    while (g < 32 && 2 * g * m <= S::kThreads) g *= 2;
+    const int e = tid / g;
     const uint32_t index = sh.sorted[min(e, m - 1)].y;
     uint64_t mass = 0;
 #pragma unroll 4
@@ -652,6 +695,28 @@ __device__ __forceinline__ void masses_by_index(S& sh, int m) {
     }
     for (int o = 1; o < g; o *= 2) mass += __shfl_xor_sync(0xffffffffu, mass, o);
     if (tid % g == 0 && e < m) sh.before[e] = mass;
+    __syncthreads();
+    return;
+  }
+  const uint32_t scale = uint32_t((uint64_t(S::kBuckets) << 32) / uint32_t(V + S::kBuckets));
+  auto bin_of = [&](int e) { return int(__umulhi(sh.sorted[e].y, scale)); };
+  by_bins(sh, m, bin_of);
+  uint64_t* mass = sh.bin_mass;
+  uint64_t own = 0;  // of the thread's bin
+  if (tid < S::kBuckets)
+    for (uint32_t q = sh.bin_start[tid]; q < sh.bin_ends()[tid]; ++q) own += weight_in(sh.sorted[sh.scan[q]]);
+  const uint64_t upto = block_scan(own, sh.room) - own;
+  if (tid < S::kBuckets) mass[tid] = upto;
+  __syncthreads();
+  for (int e = tid; e < m; e += S::kThreads) {
+    const uint32_t index = sh.sorted[e].y;
+    const int bin = bin_of(e);
+    uint64_t before = mass[bin];
+    for (uint32_t q = sh.bin_start[bin]; q < sh.bin_ends()[bin]; ++q) {
+      const uint4& other = sh.sorted[sh.scan[q]];
+      if (other.y < index) before += weight_in(other);
+    }
+    sh.before[e] = before;
   }
   __syncthreads();
 }
@@ -667,9 +732,9 @@ struct Drawn {
 // nothing).
 template <class S>
 __device__ __noinline__ bool settle(S& sh, int n, int k, float p, uint64_t least, bool closed, uint64_t mass,
-                                    uint64_t off, uint64_t draw, Drawn& d) {
+                                    uint64_t off, uint64_t draw, float M, float tau, int V, Drawn& d) {
   const int tid = threadIdx.x;
-  sort_list(sh, n);
+  sort_list(sh, n, M, tau);
   const uint64_t sum = k > 0 && k < n ? sh.before[k] : sh.before[n - 1] + weight_in(sh.sorted[n - 1]);
   if (k > 0) {
     mass = sum;
@@ -696,7 +761,7 @@ __device__ __noinline__ bool settle(S& sh, int n, int k, float p, uint64_t least
   const uint64_t at = __umul64hi(draw, d.total);
   if (tid == 0) sh.cut = {sh.sorted[m - 1].x, int(sh.sorted[m - 1].y)};
   __syncthreads();  // (all have read what is before whom)
-  masses_by_index(sh, m);
+  masses_by_index(sh, m, V);
   for (int e = tid; e < m; e += S::kThreads) {
     const uint64_t w = weight_in(sh.sorted[e]), b = sh.before[e];
     if (b <= at && at < b + w) {
@@ -1128,7 +1193,7 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
       row_sync();
       const int n = share_out(sh, sc, r.ctas, MASS);
       if (n > 0) {
-        sort_list(sh, n);
+        sort_list(sh, n, value_of(hi), value_of(lo));
         for (int e = tid; e < n; e += S::kThreads) {
           const uint64_t m = MASS ? weight_in(sh.sorted[e]) : 1, b = above + (MASS ? sh.before[e] : uint64_t(e));
           if (b < target && target <= b + m) sh.cut = {sh.sorted[e].x, int(sh.sorted[e].y)};
@@ -1399,9 +1464,12 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     if (lane == 0) sh.sums[warp] = make_float2(most, all);
   }
   bool bad = __syncthreads_or(!(top < INFINITY));
-  if (warp == 0) {
+  // (a lower bound by the next warp, for a nucleus that the first does not hold: by half as many maxima as the list has
+  // room, which 60 to 80 % as many candidates reach)
+  if (warp < (PART != kRest && sums && nucleus ? 2 : 1)) {
+    const int count = PART == kRest ? 1 : warp == 0 ? min(nth, S::kThreads) : min(S::kList / 2 / r.ctas, S::kThreads * 3 / 4);
     float least_top = -INFINITY, most = -INFINITY;
-    nth_largest(sh, PART == kRest ? 1 : min(nth, S::kThreads), least_top, most);
+    nth_largest(sh, count, least_top, most);
     float all = 0.0f;
     if (sums)
       for (int w = 0; w < S::kWarps; ++w) all += sh.sums[w].y * ex2_approx((sh.sums[w].x - most) * c);
@@ -1412,40 +1480,47 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) lead += __shfl_xor_sync(0xffffffffu, lead, o);
     }
-    if (lane == 0) sh.lead = lead;
-    if (lane == 0) sh.ends = make_float4(most, nth <= S::kThreads ? least_top : -INFINITY, bad ? 1.0f : 0.0f, all);
+    if (lane == 0) sh.lead[warp] = make_float2(nth <= S::kThreads ? least_top : -INFINITY, lead);
+    if (lane == 0 && warp == 0) sh.ends = make_float4(most, bad ? 1.0f : 0.0f, all, 0.0f);
   }
   row_sync();
   float tau, M, about, lead;  // about, lead: the row's mass and the largest maxima's, roughly
   {
-    float leads = 0.0f;
-    float4 e = make_float4(-INFINITY, INFINITY, 0.0f, 0.0f);
+    float4 e = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    float2 first = make_float2(INFINITY, 0.0f), second = first;
+    auto pair = [&](const void* p) {
+      const uint64_t x = ld_peer_u64(static_cast<const uint64_t*>(p), lane);
+      return make_float2(__uint_as_float(uint32_t(x)), __uint_as_float(uint32_t(x >> 32)));
+    };
     if (lane < r.ctas) {
-      const uint64_t ab = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends), lane);
-      const uint64_t cd = ld_peer_u64(reinterpret_cast<const uint64_t*>(&sh.ends) + 1, lane);
-      e = make_float4(__uint_as_float(uint32_t(ab)), __uint_as_float(uint32_t(ab >> 32)), __uint_as_float(uint32_t(cd)),
-                      __uint_as_float(uint32_t(cd >> 32)));
-      leads = __uint_as_float(ld_peer_u32(&sh.lead, lane));
+      const float2 ab = pair(&sh.ends), cd = pair(&sh.ends.z);
+      e = make_float4(ab.x, ab.y, cd.x, cd.y);
+      first = pair(sh.lead);
+      if (sums && nucleus) second = pair(sh.lead + 1);
     }
-    bad = __any_sync(0xffffffffu, e.z != 0.0f);
+    bad = __any_sync(0xffffffffu, e.y != 0.0f);
     M = e.x;
 #pragma unroll
     for (int o = 1; o < kMaxCtas; o *= 2) {
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      e.y = fminf(e.y, __shfl_xor_sync(0xffffffffu, e.y, o));
+      first.x = fminf(first.x, __shfl_xor_sync(0xffffffffu, first.x, o));
+      second.x = fminf(second.x, __shfl_xor_sync(0xffffffffu, second.x, o));
     }
     M = __shfl_sync(0xffffffffu, M, 0);
-    tau = __shfl_sync(0xffffffffu, e.y, 0);
-    const float scale = e.w > 0.0f ? ex2_approx((e.x - M) * c) : 0.0f;
-    about = e.w * scale;
-    lead = leads * scale;
+    const float scale = e.z > 0.0f ? ex2_approx((e.x - M) * c) : 0.0f;
+    about = e.z * scale;
+    first.y *= scale;
+    second.y *= scale;
 #pragma unroll
     for (int o = 1; o < kMaxCtas; o *= 2) {
       about += __shfl_xor_sync(0xffffffffu, about, o);
-      lead += __shfl_xor_sync(0xffffffffu, lead, o);
+      first.y += __shfl_xor_sync(0xffffffffu, first.y, o);
+      second.y += __shfl_xor_sync(0xffffffffu, second.y, o);
     }
+    if (sums && nucleus && top_p * about > first.y) first = second;
     about = __shfl_sync(0xffffffffu, about, 0);
-    lead = __shfl_sync(0xffffffffu, lead, 0);
+    tau = __shfl_sync(0xffffffffu, first.x, 0);
+    lead = __shfl_sync(0xffffffffu, first.y, 0);
   }
   bad = bad || M == -INFINITY;
   const Scale sc = scale_of(M, c, c_lo);
@@ -1472,14 +1547,14 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         tau = sc.M;
       } else if (min_p > 0.0f && (k == 0 || !nucleus)) {
         const float span = T_ * logf(min_p), border = sc.M + span - 1e-5f * (fabsf(sc.M) - span);
-        if (!(tau > border) || nth > S::kThreads) {
+        if (!(tau > border) || nth > S::kThreads || (nucleus && top_p * about > lead)) {
           tau = border;
           closed = true;
         }
       }
       const bool trusted = !sums || (fine ? !sc.far : fabsf(sc.M * sc.c) < kFastRange - 128.0f);
-      // (the candidates are half as many again as the maxima they are found by, so twice those' mass they hardly reach)
-      const bool hopeless = sums && nucleus && !closed && top_p * about > 2.0f * lead;
+      // (the candidates are half as many again as the maxima they are found by, but smaller ones: 1.0 to 1.2 times the mass)
+      const bool hopeless = sums && nucleus && !closed && top_p * about > 1.25f * lead;
       const bool by_list = trusted && !hopeless && (nth <= S::kThreads || closed);
       if (by_list) {
         collect<PART == kFirst ? kAhead : 1>(sh, r, tau);
@@ -1487,7 +1562,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         const int found = share_out(sh, sc, r.ctas, !greedy);
         const uint64_t mass = sums ? all_chunks(sh, r.ctas) : 0;
         if (found > 0)
-          settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, d);
+          settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, sc.M, tau, a.V, d);
         if (settled) cut = sh.cut;
         else row_sync();  // (the peers have read the candidates)
       } else if (trusted && sums && !nucleus) {
