@@ -139,7 +139,7 @@ __device__ __forceinline__ float entry_of(const uint4& w, int e) {
 // f(entries e and e + 1 of a vector, e), two at a time: a loop, whose instructions are fetched once.
 template <class T, class F>
 __device__ __forceinline__ void pairs(uint4 w, F f) {
-#pragma unroll 1
+#pragma unroll kVec<T> == 4 ? 2 : 1
   for (int e = 0; e < kVec<T>; e += 2) {
     if constexpr (sizeof(T) == 2) {
       f(bf16_lo(w.x), bf16_hi(w.x), e);
@@ -219,8 +219,8 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // ------------------------------------------------------------------ weights
 
-// How weights follow from values: exponents are x c in log2 units, of which k_top / 1024 + rest is the maximum's; where
-// that is beyond +-4000 (`far`), (x - M) c.
+// How weights follow from values.  k_top / 1024 + rest is the maximum's x c, which the fine sums' whole references are
+// next to, unless it is beyond +-4000 (`far`).
 struct Scale {
   float M;         // the row's maximum
   float c, c_lo;   // log2(e) / T
@@ -235,12 +235,8 @@ struct Exponent {
   float hi, lo;
 };
 
+// (x - M) / T in log2 units, x - M as a sum of two floats (Knuth's TwoSum).
 __device__ __forceinline__ Exponent exponent(float x, const Scale& sc) {
-  if (!sc.far) {
-    const float hi = x * sc.c;
-    return {hi, fmaf(x, sc.c_lo, -sc.rest) + fmaf(x, sc.c, -hi)};
-  }
-  // x - M as a sum of two floats (Knuth's TwoSum)
   const float s = x - sc.M, bb = s - x, err = (x - (s - bb)) + (-sc.M - bb);
   const float hi = s * sc.c;
   return {hi, fmaf(s, sc.c, -hi) + fmaf(s, sc.c_lo, err * sc.c)};
@@ -265,7 +261,7 @@ __device__ __forceinline__ uint32_t shift_left(uint32_t x, int by) {
 __device__ __forceinline__ uint64_t units_of(float x, const Scale& sc, const uint32_t* table) {
   const Exponent t = exponent(x, sc);
   const float m = fmaf(fmaxf(t.hi, -4090.0f), 1024.0f, kMagic);
-  const int k = __float_as_int(m) - __float_as_int(kMagic) - sc.k_top;
+  const int k = __float_as_int(m) - __float_as_int(kMagic);
   const float z = (fmaf(m - kMagic, -1.0f / 1024.0f, t.hi) + t.lo) * kLn2Hi;
   const float more = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z);                                             // 2^r - 1
   const int more32 = __float_as_int(fmaf(more, 4294967296.0f, kMagic)) - __float_as_int(kMagic);  // in units of 2^-32
@@ -279,10 +275,9 @@ __device__ __forceinline__ uint64_t units_of(float x, const Scale& sc, const uin
 __device__ __forceinline__ Scale scale_of(float M, float c, float c_lo) {
   Scale sc = {M, c, c_lo, 0.0f, 0, !(fabsf(M * c) < 4000.0f)};
   if (!sc.far) {
-    const Exponent t = exponent(M, sc);
-    const float m = fmaf(t.hi, 1024.0f, kMagic);
+    const float hi = M * c, lo = fmaf(M, c_lo, fmaf(M, c, -hi)), m = fmaf(hi, 1024.0f, kMagic);
     sc.k_top = __float_as_int(m) - __float_as_int(kMagic);
-    sc.rest = fmaf(m - kMagic, -1.0f / 1024.0f, t.hi) + t.lo;
+    sc.rest = fmaf(m - kMagic, -1.0f / 1024.0f, hi) + lo;
   }
   return sc;
 }
