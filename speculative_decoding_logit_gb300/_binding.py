@@ -699,9 +699,9 @@ def _paged_ext():
             loader = importlib.machinery.ExtensionFileLoader("asv_torch", _build.TORCH_EXT)
             ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("asv_torch", loader))
             loader.exec_module(ext)
-            ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append_ex,
+            ext.bind(AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append,
                                                                         L.asv_status_string, L.asv_last_cuda_error)))
-            ext.bind_step(*(C.cast(f, C.c_void_p).value for f in (L.paged_plan, L.sample_tokens)))
+            ext.bind_step(*(C.cast(f, C.c_void_p).value for f in (L.paged_kv_append_ex, L.paged_plan, L.sample_tokens)))
             _ext = ext
     return _ext
 

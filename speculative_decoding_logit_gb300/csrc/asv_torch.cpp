@@ -20,7 +20,8 @@ namespace {
 
 PyObject* g_error = nullptr;  // AsvError(status, message)
 decltype(&paged_attention) g_attention = nullptr;
-decltype(&paged_kv_append_ex) g_append = nullptr;
+decltype(&paged_kv_append) g_append = nullptr;
+decltype(&paged_kv_append_ex) g_append_ex = nullptr;
 decltype(&paged_plan) g_plan = nullptr;
 decltype(&sample_tokens) g_sample = nullptr;
 decltype(&asv_status_string) g_status_string = nullptr;
@@ -275,8 +276,10 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     uint32_t* status = status_of(tensor(a[11], "req_status"), p);
     const cudaStream_t stream = stream_of(a[n - 1]);
     return result(unlocked([&]() {
-                    return g_append(&p.cache, &p.batch, &kr, &vr, with_q ? &qr : nullptr, with_q ? &oq : nullptr, heads,
-                                    rotate ? &rot : nullptr, placed ? &at : nullptr, status, stream);
+                    const asv_rows *qs = with_q ? &qr : nullptr, *os = with_q ? &oq : nullptr;
+                    const asv_rotary* turn = rotate ? &rot : nullptr;
+                    return placed ? g_append_ex(&p.cache, &p.batch, &kr, &vr, qs, os, heads, turn, &at, status, stream)
+                                  : g_append(&p.cache, &p.batch, &kr, &vr, qs, os, heads, turn, status, stream);
                   }),
                   "paged_kv_append");
   });
@@ -435,12 +438,13 @@ PyObject* py_sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// the addresses of paged_plan and sample_tokens
+// the addresses of paged_kv_append_ex, paged_plan and sample_tokens
 PyObject* py_bind_step(PyObject*, PyObject* args) {
-  unsigned long long f[2];
-  if (!PyArg_ParseTuple(args, "KK", &f[0], &f[1])) return nullptr;
-  g_plan = reinterpret_cast<decltype(g_plan)>(f[0]);
-  g_sample = reinterpret_cast<decltype(g_sample)>(f[1]);
+  unsigned long long f[3];
+  if (!PyArg_ParseTuple(args, "KKK", &f[0], &f[1], &f[2])) return nullptr;
+  g_append_ex = reinterpret_cast<decltype(g_append_ex)>(f[0]);
+  g_plan = reinterpret_cast<decltype(g_plan)>(f[1]);
+  g_sample = reinterpret_cast<decltype(g_sample)>(f[2]);
   Py_RETURN_NONE;
 }
 

@@ -67,3 +67,28 @@ def test_rows_of_a_plan_that_are_no_number(traced, rows):
     with pytest.raises(m.AsvError):
         m.paged_plan(i, i, i[None], i, i, i, 16, max_tokens=rows,
                      stream=SimpleNamespace(name="s", cuda_stream=7, device=torch.device("cpu")))
+
+
+@pytest.mark.gpu
+def test_append_after_the_module_was_bound_again():
+    """bind() takes the entry points that it always took; positions have one of their own."""
+    import ctypes as C
+
+    import speculative_decoding_logit_gb300 as asv
+    from speculative_decoding_logit_gb300 import _binding as m
+    asv.build()
+    L = m.library()
+    m._paged_ext().bind(m.AsvError, *(C.cast(f, C.c_void_p).value for f in (L.paged_attention, L.paged_kv_append,
+                                                                            L.asv_status_string, L.asv_last_cuda_error)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.randn(3, 1, 16, device="cuda").bfloat16()
+    table, zero, indptr = torch.tensor([[1, 0]], **i32), torch.zeros(1, **i32), torch.tensor([0, 3], **i32)
+    rotary = torch.randn(16, 16, device="cuda")
+    caches = []
+    for kw in ({}, dict(positions=torch.arange(3, **i32))):
+        kc, vc = (torch.zeros(2, 8, 1, 16, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        app = asv.paged_kv_append(k, k, kc, vc, table, zero, indptr, rotary=rotary, **kw)
+        assert not app.req_status.any()
+        caches.append((kc, vc))
+    for a, b in zip(*caches):
+        assert torch.equal(a, b) and a[1, :3].any() and not a[0].any()
