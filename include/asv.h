@@ -451,7 +451,8 @@ typedef struct {
  * kept mass; u is a number from [0, 1) that the caller draws (one outside counts as the nearest in it, NaN as 0).  Sums are
  * exact to about 2^-30 of their size where a border is near, so a token differs from exact arithmetic's only where one is
  * that near, and does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.
- * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere; both to 2^-18 (typically 2^-23).  With temperature 0: 0, and 1 at the token.
+ * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere; both to 2^-18 (typically 2^-23).
+ * With temperature 0: 0, and 1 at the token.
  * Inputs may share memory, outputs not with anything; rows of out_probs need no alignment but the element's.
  * A row with NaN or +inf, or all -inf, flags its request ASV_REQ_NONFINITE (a single -inf is probability 0), a request's
  * own parameter out of range ASV_REQ_BAD_PARAM; the row's token is then -1, its log-probability -inf, its distribution 0.

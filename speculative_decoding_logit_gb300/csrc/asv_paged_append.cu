@@ -3,7 +3,7 @@
 //
 // Per token: R_p turns the pairs of every query and key head by the position's angles, cos and sin from
 // the caller's table (fp32); values are copied.  Each element is read once and written once and nothing
-// is used twice but the table's row, so the launch is bound by HBM for long batches and by its chain of
+// is used twice but the table's row (rows, where pairs turn by positions of axes of their own), so the launch is bound by HBM for long batches and by its chain of
 // dependent loads (indptr, cache_len, block table and table row, each an L2 or HBM latency) for short
 // ones.
 //
@@ -234,7 +234,9 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
   const long long vectors = (long long)(a.q_heads + 2 * a.c.kv_heads) * (a.c.head_dim / 8);
   int tokens = 1;
   auto ctas = [&]() { return (a.c.N + tokens - 1) / tokens; };
-  while ((tokens < 8 && ctas() > 2048 && (tokens < 4 || tokens * vectors < 10 * kThreads)) || (tokens < 16 && ctas() > 1216 && tokens * vectors < 4 * kThreads)) tokens *= 2;
+  while ((tokens < 8 && ctas() > 2048 && (tokens < 4 || tokens * vectors < 10 * kThreads)) ||
+         (tokens < 16 && ctas() > 1216 && tokens * vectors < 4 * kThreads))
+    tokens *= 2;
   cfg.gridDim = dim3(unsigned(ctas()), 1, 1);
   switch (tokens) {
     case 1: return cudaLaunchKernelEx(&cfg, paged_append_kernel<BF16, PAIRING, 1>, a);

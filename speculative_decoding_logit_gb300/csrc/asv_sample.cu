@@ -6,20 +6,29 @@
 // entry.  The token is the first kept index whose cumulative mass (over kept entries, by index) passes u times the
 // kept mass; the distribution is w over the kept mass.
 //
-// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out to 2^-30 of themselves
-// and summed in units of 2^-44 in 64-bit integers, which makes their sums exact in any order.  That costs 40 operations an
-// entry, so few are weighed so:
-//   - The row streams once, for the maxima of the threads' vectors and, where the whole row's mass counts, a running sum of
-//     fp32 weights (two operations and ex2).  Its error is bounded; a border within the bound counts as undecided.
-//   - Where the n largest maxima of threads bound the kept set from below (top-k; a nucleus, by trial; min-p's border),
-//     the vectors of the threads that reach the bound are read again, out of L2, and the few entries from it on are
-//     compared pair by pair: rank and mass before each, then the draw.
+// Whole numbers come out, so a border must fall where exact arithmetic has it.  Weights are worked out to 2^-29 of themselves
+// and summed in units of 2^-44 in 64-bit integers, which makes their sums exact in any order.  That costs some 40
+// instructions an entry, half of them at half the rate, so few are weighed so:
+//   - The row streams once, for the maxima of groups of the threads' vectors and, where the whole row's mass counts, a
+//     running sum of fp32 weights (two operations and ex2).  Its error is bounded; a border within the bound counts as
+//     undecided.
+//   - Where the n largest maxima of threads bound the kept set from below (top-k; a nucleus, by one of two trials; min-p's
+//     border), the groups that reach the bound are read again, out of L2, and the few entries from it on are put in order:
+//     rank and mass before each, then the draw.
 //   - A draw from the whole row finds the warp's run that u falls into by the fp32 sums and weighs that run alone.
-//   - What stays undecided, or has too many candidates, goes by histograms of exact masses over the row, level by level
-//     until the rest fits the comparison.
+//   - What stays undecided, or has too many candidates, takes an estimate of the border by a histogram and one pass that
+//     weighs the row exactly and collects what is near the border (search_near); where even that does not settle it, many
+//     values apart by less than a bin, histograms of exact masses level by level (search).
 //
 // A cluster of CTAs has a row, each a run of its vectors, each warp a run of the CTA's.  All CTAs come to the same
-// decisions from the same exchanged numbers.
+// decisions from the same exchanged numbers.  Up to 76 rows one launch does all; above, a launch of small CTAs whose chains
+// of exchanges overlap, and one that has the rows it left, a cluster of eight large CTAs each.
+//
+// What bounds it (one call among others; the row's bytes at 6.79 TB/s in brackets): one row of 32,000, top-k, 11.4 us: four
+// exchanges of a cluster and code that runs once, 42 % of its waits for instructions; 64 bf16 rows of 151,936, top-p,
+// 23.0 [2.9], of which a row's chain is 19; 64 flat fp32 rows 77 [5.7]: 48 million warp instructions, 54 % of the issue slots;
+// 352 fp32 rows of 128,256 with distributions 167 [53]; 1024 mixed rows of 151,936 148 [46]: 86 for the first launch, 58 for
+// the few rows of the second, each a chain of some 20 exchanges.
 #include <algorithm>
 #include <climits>
 
@@ -60,7 +69,7 @@ template <int THREADS, Part PART>
 struct __align__(16) Shared {
   static constexpr int kThreads = THREADS, kWarps = THREADS / 32;
   static constexpr int kBuckets = THREADS < 256 ? THREADS : 256;
-  static constexpr int kList = THREADS < 256 ? 256 : 512;  // candidates that are compared with each other
+  static constexpr int kList = THREADS < 256 ? 256 : 512;  // candidates that are put in order
   union {                                          // one after the other
     float group[PART != kRest ? (kGroups + 1) * THREADS : 1];  // maxima of groups of a thread's vectors; of the row's ends
     uint2 bins[PART != kFirst ? kBins : 1];        // a histogram's 64-bit sums
@@ -168,7 +177,8 @@ __device__ __forceinline__ uint4 edge_vector(const Row<T>& r, int v) {
     uint32_t x = kBits == 16 ? 0xff80u : 0xff800000u;
     if (i >= 0 && i < r.V) memcpy(&x, r.base + r.off + i, sizeof(T));
     if constexpr (kBits == 16)
-      w = make_uint4((w.x << 16) | x, __funnelshift_l(w.x, w.y, 16), __funnelshift_l(w.y, w.z, 16), __funnelshift_l(w.z, w.w, 16));
+      w = make_uint4((w.x << 16) | x, __funnelshift_l(w.x, w.y, 16), __funnelshift_l(w.y, w.z, 16),
+                     __funnelshift_l(w.z, w.w, 16));
     else
       w = make_uint4(x, w.x, w.y, w.z);
   }
@@ -905,7 +915,8 @@ struct Bin {
 };
 
 template <class S, class T, class Add, class Mass, class G>
-__device__ __forceinline__ Bin find_bin(S& sh, const Row<T>& r, int bins, uint64_t above, Add add_up, Mass mass, G target_of) {
+__device__ __forceinline__ Bin find_bin(S& sh, const Row<T>& r, int bins, uint64_t above, Add add_up, Mass mass,
+                                        G target_of) {
   const int tid = threadIdx.x, lane = tid % 32;
   const int part = (bins + r.ctas - 1) / r.ctas, part0 = min(r.rank * part, bins), part1 = min(part0 + part, bins);
   row_sync();
@@ -963,7 +974,8 @@ __device__ __forceinline__ Bin find_bin(S& sh, const Row<T>& r, int bins, uint64
 // then the cut is among its entries, or, where they are more than the list holds and equal, the first so many of
 // them by index.  False: it is not, or they are not.
 // `sums`: the warps' masses of what is kept are left in sh.chunk (behind a row_sync).
-// (64 flat fp32 rows of 151,936: an exact histogram first, then the bin's entries, then two draws took 116 us.)
+// (64 flat fp32 rows of 151,936: an exact histogram, the bin's entries, and a draw by fast sums before the exact one took
+// 116 us, this takes 77.)
 template <bool MASS, class S, class T, class G>
 __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, const Cut within, G target_of, bool sums,
                                          Cut& cut) {
@@ -991,7 +1003,8 @@ __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, 
       const float t = fminf(place(x[e]), float(kNear - 1)), m = __fadd_rn(t, kMagic);
       const int bin = __float_as_int(m) - __float_as_int(kMagic);
       const float d = t - (m - kMagic);
-      const uint32_t q = MASS ? uint32_t(__float_as_int(fmaf(d, -4096.0f * kLn2Hi * kStep, kMagic + 4096.0f)) - __float_as_int(kMagic)) : 1u;
+      const float relative = fmaf(d, -4096.0f * kLn2Hi * kStep, kMagic + 4096.0f);
+      const uint32_t q = MASS ? uint32_t(__float_as_int(relative) - __float_as_int(kMagic)) : 1u;
       bool counts = bin < kNear - 1;
       if (!all) counts = counts && within.keeps(key_of(x[e]), v * kVec<T> - r.off + e);
       if (counts && ASV_GUARD(r, bin >= 0 && bin < kNear)) atomicAdd(bins + bin, q);
@@ -1104,7 +1117,8 @@ __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, 
       }
     }
     row_sync();
-    const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && int(ld_peer_u32(&sh.first, min(lane, r.ctas - 1))) >= 0);
+    const int theirs = int(ld_peer_u32(&sh.first, min(lane, r.ctas - 1)));
+    const uint32_t holds = __ballot_sync(0xffffffffu, lane < r.ctas && theirs >= 0);
     if (holds == 0) return false;
     const int owner = __ffs(holds) - 1;
     cut = {ld_peer_u32(&sh.cut.key, owner), int(ld_peer_u32(&sh.cut.index, owner))};
@@ -1132,9 +1146,8 @@ __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, 
   return true;
 }
 
-// The cut that keeps entries of `within`, in order, until their measures (MASS: weights; else one each) add up to
-// target_of(all): the last is the first with target <= the inclusive sum.  For rows that search_near does not settle.  A
-// histogram by value over the larger weights' range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
+// The same cut for rows that search_near does not settle.  A histogram of exact masses by value over the larger weights'
+// range, then the bin's entries to the list; where there are more than it holds, a histogram by key within the bin, and so
 // on.  The bins are added up a part by each CTA.
 template <bool MASS, class S, class T, class G>
 __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const Cut within, G target_of) {
@@ -1471,7 +1484,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     float lead = 0.0f;
     if (sums) {
 #pragma unroll 4
-      for (int i = lane; i < S::kThreads; i += 32) lead += sh.tops[i] >= least_top ? ex2_approx((sh.tops[i] - most) * c) : 0.0f;
+      for (int i = lane; i < S::kThreads; i += 32)
+        lead += sh.tops[i] >= least_top ? ex2_approx((sh.tops[i] - most) * c) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) lead += __shfl_xor_sync(0xffffffffu, lead, o);
     }
@@ -1557,7 +1571,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         const int found = share_out(sh, sc, r.ctas, !greedy);
         const uint64_t mass = sums ? all_chunks(sh, r.ctas) : 0;
         if (found > 0)
-          settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, sc.M, tau, a.V, d);
+          settled = settle(sh, found, k, greedy ? 1.0f : top_p, least, closed, mass, (mass >> kFastBits) + 1, draw, sc.M,
+                           tau, a.V, d);
         if (settled) cut = sh.cut;
         else row_sync();  // (the peers have read the candidates)
       } else if (trusted && sums && !nucleus) {
