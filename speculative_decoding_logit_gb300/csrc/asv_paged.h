@@ -35,12 +35,16 @@ struct AppendArgs {
   int q_heads;
   const float* rotary;  // nullptr: no rotation
   int rot_dim, max_position, interleaved;
+  uint32_t* status;
+  uint32_t* check_log;  // of the checked build: the append has no workspace, its log is the library's
+};
+
+// The same with positions of their own for the rotation.
+struct PlacedArgs : AppendArgs {
   const int32_t* positions;  // [axes, N]; nullptr: the slots' positions
   int axes;
   long long axis_stride;
   uint8_t axis[64];  // axis of each pair
-  uint32_t* status;
-  uint32_t* check_log;  // of the checked build: the append has no workspace, its log is the library's
 };
 
 struct AttendArgs {
@@ -93,7 +97,7 @@ inline size_t paged_workspace_bytes(int head_dim) {
 constexpr int kPlanMaxRequests = 16384;  // three words each in one CTA's shared memory
 constexpr int kPlanMaxRows = 1 << 30;  // (a thread's next rows are still numbers of 32 bits)
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
-cudaError_t launch_paged_append(const AppendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_paged_append(const PlacedArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_paged_attention(const AttendArgs& a, int dtype, cudaStream_t s);
 
 // ASV_ERR_CUDA, with `e` kept for asv_last_cuda_error (asv_api.cu).

@@ -104,7 +104,7 @@ asv_status paged_kv_append_ex(const asv_paged_cache* cache, const asv_paged_batc
   if (!cache_given(c, b) || !k || !k->data || !v || !v->data || (!q) != (!out_q) || (q && !q->data) ||
       (out_q && !out_q->data) || (rotary && !rotary->table) || (positions && !positions->at) || !out_req_status)
     return ASV_ERR_NULL;
-  asv::AppendArgs a = {};
+  asv::PlacedArgs a = {};
   a.c = paged_view(c, b);
   a.k = rows_view(*k, b.N, c.kv_heads);
   a.v = rows_view(*v, b.N, c.kv_heads);
