@@ -1562,8 +1562,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         }
       }
       const bool trusted = !sums || (fine ? !sc.far : fabsf(sc.M * sc.c) < kFastRange - 128.0f);
-      // (the candidates are half as many again as the maxima they are found by, but smaller ones: 1.0 to 1.2 times the mass)
-      const bool hopeless = sums && nucleus && !closed && top_p * about > 1.25f * lead;
+      // (the candidates are half as many again as the maxima they are found by, but smaller ones: 1.0 to 1.2 times the mass,
+      // and more where threads have few entries, several of them candidates)
+      const float reach = 1.25f + 16.0f * float(S::kThreads * r.ctas) / float(a.V);
+      const bool hopeless = sums && nucleus && !closed && top_p * about > reach * lead;
       const bool by_list = trusted && !hopeless && (nth <= S::kThreads || closed);
       if (by_list) {
         collect<PART == kFirst ? kAhead : 1>(sh, r, tau);
@@ -1741,20 +1743,22 @@ template <class T>
 cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.B * a.n;
   const int tuned = std::min(tuned_cluster(), kMaxCtas);
-  // CTAs to a row: as many as all rows together leave room for, each with enough of the row to be worth its exchanges; the
-  // most where distributions are wanted and the rows in hand would not stay in L2 until they are written (352 fp32 rows of
-  // 128,256: 179 us with three, 169 with eight).
-  auto ctas_of = [&](int slots) {
+  // CTAs to a row: `share`, what all rows together leave room for, but no more than have enough of the row to be worth their
+  // exchanges; the most where distributions are wanted and the rows in hand would not stay in L2 until they are written
+  // (352 fp32 rows of 128,256: 179 us with three, 169 with eight).
+  auto ctas_of = [&](long long share, int least) {
     if (tuned > 0) return tuned;
     const bool large = a.probs != nullptr && rows * a.V * (long long)sizeof(T) > (80ll << 20);
-    return int(std::clamp(std::min(large ? kMaxCtas : slots / rows, (long long)a.V / 2048), 1ll, (long long)kMaxCtas));
+    return int(std::clamp(std::min(large ? kMaxCtas : share, (long long)a.V / least), 1ll, (long long)kMaxCtas));
   };
   if (rows <= kSms / 2)
-    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(kSms * kAllCtas), kAllThreads, s);
-  // Many rows: small CTAs whose chains of exchanges overlap, and the few rows that need it in general behind them, where
-  // large clusters have them at once.
-  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(kSms * kFirstCtas),
-                               kFirstThreads, s);
+    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(kSms * kAllCtas / rows, 2048), kAllThreads, s);
+  // Many rows: small CTAs whose chains of exchanges overlap, some half of those that there is room for, four to a row at
+  // most (300 rows of 151,936, top-p: 39 us with three, 49 with four; 150 rows 28.6 with four, 39 with eight; 600 58 with
+  // two, 68 with one and 70 with three); and the few rows that need it in general behind them, where large clusters have
+  // them at once.
+  const long long share = std::min((kSms * kFirstCtas * 9 / 16 + rows - 1) / rows, 4ll);
+  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(share, 1024), kFirstThreads, s);
   if (e != cudaSuccess) return e;
   return launch(sample_rest_kernel<T, kRestThreads, kRestCtas>, a, std::min(rows, (long long)kSms * kRestCtas / kMaxCtas),
                 kMaxCtas, kRestThreads, s);
