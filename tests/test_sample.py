@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import test_paged_refusals as host
-from sample_util import logprob_bound, probs_bound, sample64
+from sample_util import logprob_bound, off, probs_bound, sample64
 
 NULL, SHAPE, ALIGN, DTYPE, PARAM = 1, 2, 3, 4, 5
 m = host.m
@@ -431,3 +431,31 @@ def test_borders_of_rows_in_general(m, dtype, rows, kind):
         got = m.sample_tokens(x.cuda(), u.cuda(), temperature=T, top_k=k, top_p=p, min_p=least, probs=True)
         got = m.SampleOutput(*(t.cpu()[few] for t in (got.tokens, got.logprobs, got.probs, got.req_status)))
         _compare(x[few], u[few], got, T, k, p, least)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", ["flat", "peaked", "ties"])
+@pytest.mark.parametrize("V,B", [(20011, 60), (151936, 90)])
+def test_draws_next_to_borders(m, dtype, kind, V, B):
+    """u at the fp32 number nearest to where one token ends and the next begins, 2^-25 of the mass away at most.  Weights'
+    sums may be off by 2^-29 + V 2^-44 of it, 2^-26.7 at 151,936, so a good part of the draws is too near to tell the token;
+    theirs may be any that u falls into with that much to both sides (several, where a token's mass is less)."""
+    x = _logits_of(1, 1, V, kind, dtype, V)
+    for p in (1.0, 0.97):
+        y, p32 = x[0, 0].double().numpy(), float(np.float32(p))
+        dist = sample64(y, 0.5, 1.0, 0, p32, 0.0)[2]
+        upto = np.cumsum(dist)
+        at = np.searchsorted(upto, np.random.default_rng(V).uniform(0.001, 0.999, B))
+        u = torch.from_numpy(upto[at].astype(np.float32)).view(B, 1).clamp(max=1 - 2 ** -24)
+        got = m.sample_tokens(x.expand(B, 1, V).cuda(), u.cuda(), top_p=p)
+        assert not got.req_status.any()
+        for b in range(20):
+            token, lp, _, margin = sample64(y, float(u[b, 0]), 1.0, 0, p32, 0.0)
+            have = int(got.tokens[b, 0])
+            if margin >= 1:
+                assert have == token, (b, margin)
+                assert abs(float(got.logprobs[b, 0]) - lp) <= logprob_bound(lp)
+            else:
+                assert dist[have] > 0, b
+                assert upto[have] - dist[have] - off(1.0, V) <= float(u[b, 0]) <= upto[have] + off(1.0, V), (b, margin)
