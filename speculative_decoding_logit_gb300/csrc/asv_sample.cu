@@ -1754,8 +1754,16 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
     const bool large = a.probs != nullptr && rows * a.V * (long long)sizeof(T) > (80ll << 20);
     return int(std::clamp(std::min(large ? kMaxCtas : share, (long long)a.V / least), 1ll, (long long)kMaxCtas));
   };
-  if (rows <= kSms / 2)
-    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(kSms * kAllCtas / rows, 2048), kAllThreads, s);
+  if (rows <= kSms / 2) {
+    // One CTA to an SM, six to a row at most, where no row can have a large kept set (64 rows of 151,936, top-k 50: 15.6 us with
+    // two, 18.8 with eight; 16 rows 12.9 with six, 14.2 with eight); with a nucleus of any size four to an SM (64 flat rows: 77
+    // with eight, 111 with three).  Not quite all there is room for: 76 rows of eight take two turns, 33 us against 23.
+    const bool nucleus = a.top_p != nullptr || a.one.top_p < 1.0f, min_p = a.min_p != nullptr || a.one.min_p > 0.0f;
+    const bool few = (a.temperature == nullptr && a.one.temperature == 0.0f) ||
+                     (a.top_k == nullptr && (a.one.top_k > 0 ? a.one.top_k <= 256 : !nucleus && !min_p));
+    const long long share = few ? std::clamp(kSms / rows, 2ll, 6ll) : kSms * kAllCtas * 15 / 16 / rows;
+    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(share, 2048), kAllThreads, s);
+  }
   // Many rows: small CTAs whose chains of exchanges overlap, some half of those that there is room for, four to a row at
   // most (300 rows of 151,936, top-p: 39 us with three, 49 with four; 150 rows 28.6 with four, 39 with eight; 600 58 with
   // two, 68 with one and 70 with three); and the few rows that need it in general behind them, where large clusters have
