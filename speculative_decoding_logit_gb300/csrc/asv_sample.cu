@@ -27,7 +27,7 @@
 // What bounds it (one call among others; the row's bytes at 6.79 TB/s in brackets): one row of 32,000, top-k, 11.4 us: four
 // exchanges of a cluster and code that runs once, 42 % of its waits for instructions; 64 bf16 rows of 151,936, top-p,
 // 23.0 [2.9], of which a row's chain is 19; 64 flat fp32 rows 77 [5.7]: 48 million warp instructions, 54 % of the issue slots;
-// 352 fp32 rows of 128,256 with distributions 167 [53]; 1024 mixed rows of 151,936 148 [46]: 86 for the first launch, 58 for
+// 352 fp32 rows of 128,256 with distributions 168 [53]; 1024 mixed rows of 151,936 150 [46]: 86 for the first launch, 58 for
 // the few rows of the second, each a chain of some 20 exchanges.
 #include <algorithm>
 #include <climits>
@@ -1026,9 +1026,9 @@ __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, 
       },
       mass, target_of);
   if (near.bin < 0) return false;
-  const uint64_t margin = MASS ? near.all >> 16 : 0;
-  const int b0 = max(near.bin - int(near.target - near.above <= margin), 0);
-  const int b1 = min(near.bin + int(near.above + near.in - near.target < margin), kNear - 2);
+  const uint64_t margin = near.all >> 16;  // (counts have none: they are exact)
+  const int b0 = max(near.bin - int(MASS && near.target - near.above <= margin), 0);
+  const int b1 = min(near.bin + int(MASS && near.above + near.in - near.target < margin), kNear - 2);
 
   // ---- exactly
   const float m0 = kMagic + float(b0), m1 = kMagic + float(b1);
