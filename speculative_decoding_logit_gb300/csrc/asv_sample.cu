@@ -1325,8 +1325,10 @@ __device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, u
   d.total = sh.total;
   // Of sums b before a border and a behind it the draw u compares (1 - u) b with u a.  Next to the border both are u (1 - u)
   // of the mass, 1/4 at most, and each is off by 2^-20 (2^-18) of itself; the run's own sum counts once as the rows streamed
-  // and once as it is taken apart here, each off by as much too.
-  constexpr int kBits = sizeof(T) == 4 ? kFineBits : kFastBits;
+  // and once as it is taken apart here, each off by as much too.  (It is taken apart by the sums it was streamed with: the
+  // finer ones' references do not hold for 16-bit rows, which come here from further than +-4000 too.)
+  constexpr bool kFine = sizeof(T) == 4;
+  constexpr int kBits = kFine ? kFineBits : kFastBits;
   const int run = sh.pick;
   const uint64_t margin = ((sh.total / 2 + 2 * ld_peer_u64(sh.chunk + run % S::kWarps, run / S::kWarps)) >> kBits) + 64;
   const Kept keep = {{0u, INT_MAX}, -INFINITY};
@@ -1337,9 +1339,11 @@ __device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, u
         stream(r, v0, v1, [&](const uint4& w, int v) {
           float x[kVec<T>];
           unpack(w, x);
-          add_weights_fine(s, x, vector_max(w, static_cast<T*>(nullptr)), sc.c, sc.c_lo);
+          const float most = vector_max(w, static_cast<T*>(nullptr));
+          if constexpr (kFine) add_weights_fine(s, x, most, sc.c, sc.c_lo);
+          else add_weights(s, x, most, sc.c);
         });
-        return warp_sum(units_of_sum(s, sc, true));
+        return warp_sum(units_of_sum(s, sc, kFine));
       },
       [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, kExp2Table); },
       [&](float x, int) { return weight(x, sc, kExp2Table); });
