@@ -288,8 +288,9 @@ cudaError_t launch(const PlanArgs& args, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cfg.dynamicSmemBytes > 48 * 1024 - 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(cfg.dynamicSmemBytes));
+    // (always to the most: the limit is the function's, not the launch's, and another host thread may be between the two)
+    constexpr int kMost = 3 * int(sizeof(int)) * (kPlanMaxRequests + 1);
+    const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
