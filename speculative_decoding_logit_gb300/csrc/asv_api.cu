@@ -151,7 +151,7 @@ cudaError_t plan_rapid(int V, long long R, bool aligned, bool all_sums, LaunchPl
       while (C < asv::kMaxCluster && smem(C) > 52 * 1024) ++C;
     }
   }
-  if (smem(C) > 200 * 1024) return cudaErrorInvalidValue;  // V too large
+  if (smem(C) > asv::kRapidMostSmem) return cudaErrorInvalidValue;  // V too large
   out->cluster = C;
   out->threads = asv::rapid_threads();
   out->n_slice = n_slice(C);

@@ -1329,7 +1329,9 @@ template <typename K>
 cudaError_t prepare(K kern, const LaunchPlan& plan) {
   cudaError_t e = allow_cluster(kern, plan.cluster);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem);
+  // (always to the most a plan may have, here and for the draws: the limit is the function's, not the launch's, and another
+  // host thread may be between setting it and launching)
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRapidMostSmem);
 }
 
 template <bool AL, bool AE>
@@ -1377,7 +1379,7 @@ cudaError_t launch_rapid(const RapidArgs& a, const LaunchPlan& plan, cudaStream_
   const int parts = a.draw_ctas;
   b.n_slice = ((a.V + parts - 1) / parts + 3) / 4 * 4;
   const int smem = rapid_draw_smem_bytes(b.n_slice, a.bulk != 0);
-  e = cudaFuncSetAttribute(rapid_draw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(rapid_draw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDrawStage * 2 * kDrawThreads * 16);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.B) * unsigned(parts), 1, 1);
