@@ -222,12 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
     return lo;
   };
 
-  // ---- pages given back
-  const int tid_all = rank * kThreads + tid, threads = ctas * kThreads, given = pool_ok ? s_back[a.B] : 0;
-  for (int x = tid_all; x < given; x += threads) {
-    const int b = owner(s_back, x);
-    int32_t* entry = a.table + b * a.table_stride + (x - s_back[b]);
-    if (x < a.pool - count0) a.free_pages[count0 + x] = *entry;
+  // ---- pages given back (numbers of 32 bits without a sign: there may be almost 2^31 pages, and a thread's next is past them)
+  const uint32_t tid_all = rank * kThreads + tid, threads = ctas * kThreads, given = pool_ok ? uint32_t(s_back[a.B]) : 0;
+  for (uint32_t x = tid_all; x < given; x += threads) {
+    const int b = owner(s_back, int(x));
+    int32_t* entry = a.table + b * a.table_stride + (int(x) - s_back[b]);
+    if (x < uint32_t(a.pool - count0)) a.free_pages[count0 + int(x)] = *entry;
     else atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
     *entry = -1;
   }
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
   else __syncthreads();
 
   // ---- pages taken
-  for (int x = tid_all; x < taken; x += threads) {
-    const int b = owner(s_take, x), i = x - s_take[b];
+  for (uint32_t x = tid_all; x < uint32_t(taken); x += threads) {
+    const int b = owner(s_take, int(x)), i = int(x) - s_take[b];
     const Want w = load_want(a, b);
     if (ASV_GUARD(a, x < count && w.held + i < a.max_pages))
       a.table[b * a.table_stride + w.held + i] = __ldcg(a.free_pages + (count - 1 - x));
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
   else __syncthreads();
 
   // ---- rows
-  if (!a.rows_behind) place_rows(a, s_row, total, tid_all, threads);
+  if (!a.rows_behind) place_rows(a, s_row, total, int(tid_all), int(threads));
 
   // ---- what is held now (nobody reads it any more)
   if (rank == 0) {

@@ -40,3 +40,27 @@ def test_host_threads_plan_at_once(m):
     for one, _, held, _, count, out, _ in calls:
         assert torch.equal(held, one) and int(count) == 0
         assert torch.equal(out.positions, one) and not out.req_status.any()
+
+
+@pytest.mark.gpu
+def test_almost_all_pages_that_32_bits_can_number_given_back(m):
+    """2^31 - 1 pages held by 16,384 requests that have all ended: a thread's next page's number is past 31 bits."""
+    B, width = 16384, 131072
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.arange(width, **i32) + (torch.arange(B, **i32) * width)[:, None]
+    held, pool, count = torch.full((B,), width, **i32), torch.zeros(B * width - 1, **i32), torch.zeros(1, **i32)
+    held[-1] -= 1
+    new = torch.zeros(B, **i32)
+    new[7] = 3
+    plan = m.paged_plan(torch.zeros(B, **i32), new, table, held, pool, count, 16, max_tokens=2100,
+                        release=torch.ones(B, dtype=torch.bool, device="cuda"))
+    assert not plan.req_status.any() and int(count) == B * width - 2
+    top = B * width - 2
+    assert plan.slots[:4].tolist() == [top * 16, top * 16 + 1, top * 16 + 2, -1]
+    for i in range(0, B * width - 1, 1 << 28):
+        part = pool[i:i + (1 << 28)]
+        assert bool((part == torch.arange(i, i + part.shape[0], device="cuda")).all())
+    assert int(table[7, 0]) == top and int(table[-1, -1]) == B * width - 1
+    table[7, 0] = table[-1, -1] = -1
+    assert bool((table == -1).all())
+    assert held.tolist() == [0] * 7 + [1] + [0] * (B - 8)
