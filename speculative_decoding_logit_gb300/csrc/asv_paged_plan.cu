@@ -227,8 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
   for (uint32_t x = tid_all; x < given; x += threads) {
     const int b = owner(s_back, int(x));
     int32_t* entry = a.table + b * a.table_stride + (int(x) - s_back[b]);
-    if (x < uint32_t(a.pool - count0)) a.free_pages[count0 + int(x)] = *entry;
-    else atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
+    const int page = *entry;
+    const bool room = x < uint32_t(a.pool - count0);
+    if (room) a.free_pages[count0 + int(x)] = page;
+    if (!room || page < 0) atomicOr(a.status + b, ASV_REQ_BAD_PAGE);
     *entry = -1;
   }
   if (ctas > 1) cluster_sync();

@@ -64,3 +64,17 @@ def test_almost_all_pages_that_32_bits_can_number_given_back(m):
     table[7, 0] = table[-1, -1] = -1
     assert bool((table == -1).all())
     assert held.tolist() == [0] * 7 + [1] + [0] * (B - 8)
+
+
+@pytest.mark.gpu
+def test_negative_entries_among_the_pages_given_back(m):
+    """They are what the table holds, so they go onto the pool, and the request that held them is flagged."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.tensor([[4, 5, -9], [6, -2, 7]], **i32)
+    held, pool, count = torch.tensor([2, 3], **i32), torch.tensor([1, 0, 0, 0, 0, 0, 0], **i32), torch.tensor([1], **i32)
+    zero = torch.zeros(2, **i32)
+    plan = m.paged_plan(zero, zero, table, held, pool, count, 8, max_tokens=1,
+                        release=torch.ones(2, dtype=torch.bool, device="cuda"))
+    assert plan.req_status.tolist() == [0, m.REQ_BAD_PAGE] and held.tolist() == [0, 0]
+    assert pool.tolist() == [1, 4, 5, 6, -2, 7, 0] and count.tolist() == [6]
+    assert table.tolist() == [[-1, -1, -9], [-1, -1, -1]]
