@@ -96,7 +96,7 @@ struct __align__(16) Shared {
   Cut cut;
   int n_scan, n_own, found, pick, first;
   int first_own;                                   // of the list's, this CTA's first
-  uint32_t least_key, most_key;                    // of what was collected
+  uint32_t least_key, most_key, found_key;         // of what was collected; of the token
   long long row;                                   // the next one
   __device__ __forceinline__ uint32_t* bin_ends() { return reinterpret_cast<uint32_t*>(tops); }  // (read by then)
 };
@@ -728,7 +728,8 @@ __device__ __forceinline__ void masses_by_index(S& sh, int m, int V) {
 
 struct Drawn {
   int token;
-  uint64_t weight, total;  // of the token, of all that is kept
+  float value;     // its logit
+  uint64_t total;  // the mass of all that is kept
 };
 
 // Settles a row by its n candidates, which are all its entries from some value on: its first k where k > 0, else all that
@@ -771,12 +772,12 @@ __device__ __noinline__ bool settle(S& sh, int n, int k, float p, uint64_t least
     const uint64_t w = weight_in(sh.sorted[e]), b = sh.before[e];
     if (b <= at && at < b + w) {
       sh.found = int(sh.sorted[e].y);
-      sh.pick_sum = w;
+      sh.found_key = sh.sorted[e].x;
     }
   }
   __syncthreads();
   d.token = sh.found;
-  d.weight = sh.pick_sum;
+  d.value = value_of(sh.found_key);
   return true;
 }
 
@@ -1347,7 +1348,7 @@ __device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, u
       },
       [&](const uint4& w, int v) { return kept_sum(w, v, r, sc, keep, kExp2Table); },
       [&](float x, int) { return weight(x, sc, kExp2Table); });
-  d.weight = d.token >= 0 ? weight(entry(r, d.token), sc, kExp2Table) : 0;
+  d.value = d.token >= 0 ? entry(r, d.token) : -INFINITY;
   return d;
 }
 
@@ -1374,8 +1375,16 @@ __device__ __noinline__ Drawn draw_exact(S& sh, const Row<T> r, const Scale sc, 
         return warp_sum(own);
       },
       sum, [&](float x, int i) { return keep(x, i) ? weight(x, sc, sh.table) : uint64_t(0); });
-  d.weight = weight(entry(r, d.token), sc, sh.table);
+  d.value = entry(r, d.token);
   return d;
+}
+
+// (x - max x) / T - ln(kept mass): from the logit, as its weight in whole units has few digits where it is light.  Neither
+// part is above 0, so nothing cancels; the mass is the maximum's weight of 1 and the rest.
+__device__ __forceinline__ float log_probability(const Drawn& d, const Scale& sc) {
+  const Exponent t = exponent(d.value, sc);
+  const float rest = float(d.total - min(d.total, kOne)) * (1.0f / float(kOne));
+  return fmaf(t.hi, kLn2Hi, t.lo * kLn2Hi) - log1pf(rest);
 }
 
 // ------------------------------------------------------------------ the kernels
@@ -1541,7 +1550,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   bad = bad || M == -INFINITY;
   const Scale sc = scale_of(M, c, c_lo);
 
-  Drawn d = {-1, 0, 0};
+  Drawn d = {-1, -INFINITY, 0};
   Cut cut = {0u, INT_MAX};
   uint64_t least = 0;
   if (params_ok && !bad) {  // (for all CTAs of the row)
@@ -1628,8 +1637,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     if (bad) atomicOr(a.status + b, ASV_REQ_NONFINITE);
     a.tokens[b * a.tokens_b + n * a.tokens_n] = d.token;
     if (a.logprobs != nullptr)
-      a.logprobs[b * a.logprobs_b + n * a.logprobs_n] =
-          d.token < 0 ? -INFINITY : -log1pf(float(d.total - min(d.total, d.weight)) / float(d.weight));
+      a.logprobs[b * a.logprobs_b + n * a.logprobs_n] = d.token < 0 ? -INFINITY : log_probability(d, sc);
   }
 
   // ---- the distribution
