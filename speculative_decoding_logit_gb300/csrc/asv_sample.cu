@@ -1387,6 +1387,44 @@ __device__ __forceinline__ float log_probability(const Drawn& d, const Scale& sc
   return fmaf(t.hi, kLn2Hi, t.lo * kLn2Hi) - log1pf(rest);
 }
 
+// The kept entries' shares of the mass, 1 / inv, and 0 elsewhere (everywhere without a token).
+template <class T>
+__device__ __noinline__ void write_distribution(const SampleArgs& a, const Row<T> r, const Scale sc, const Cut cut, int token,
+                                                float inv, int b, int n) {
+  float* to = a.probs + b * a.probs_b + n * a.probs_n;
+  // (what is further below the maximum than 2^-200 has no weight; of a row without a token nothing has)
+  const float cut_at = cut.key == 0 ? -INFINITY : value_of(cut.key), least_value = sc.M - 200.0f / sc.c;
+  const Kept keep = {{0u, token < 0 ? -1 : cut_at < least_value ? INT_MAX : cut.index},
+                     token < 0 ? INFINITY : fmaxf(cut_at, least_value)};
+  const bool vectors = (reinterpret_cast<uintptr_t>(to) / 4 + kVec<T> - r.off) % 4 == 0;
+  const float2 cc = make_float2(sc.c, sc.c), cl = make_float2(sc.c_lo, sc.c_lo), mm = make_float2(-sc.M, -sc.M);
+  const float2 minus = make_float2(-sc.c, -sc.c), ii = make_float2(inv, inv), ln2 = make_float2(kLn2Hi, kLn2Hi);
+  stream<true>(r, r.v0, r.v1, [&](const uint4& w, int v) {
+    float x[kVec<T>], p[kVec<T>];
+    unpack(w, x);
+    const int i0 = v * kVec<T> - r.off;
+#pragma unroll
+    for (int e = 0; e < kVec<T>; e += 2) {
+      // exponents as sums of two floats, two entries at a time: x - M with its rounding (Knuth's TwoSum), its product with c
+      const float2 y = make_float2(x[e], x[e + 1]), s = fadd2(y, mm), bb = fsub2(s, y);
+      const float2 err = fadd2(fsub2(y, fsub2(s, bb)), fsub2(mm, bb)), down = fmul2(s, minus);
+      const float2 lo = ffma2(err, cc, ffma2(s, cl, ffma2(s, cc, down)));
+      const float2 q = fmul2(make_float2(ex2_approx(-down.x), ex2_approx(-down.y)), ii), more = ffma2(q, fmul2(lo, ln2), q);
+      p[e] = keep(x[e], i0 + e) ? more.x : 0.0f;
+      p[e + 1] = keep(x[e + 1], i0 + e + 1) ? more.y : 0.0f;
+    }
+    if (vectors && i0 >= 0 && i0 + kVec<T> <= a.V && ASV_GUARD(a, b < a.B && n < a.n)) {
+#pragma unroll
+      for (int e = 0; e < kVec<T>; e += 4)
+        __stcs(reinterpret_cast<float4*>(to + i0 + e), make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e)
+        if (i0 + e >= 0 && i0 + e < a.V) to[i0 + e] = p[e];
+    }
+  });
+}
+
 // ------------------------------------------------------------------ the kernels
 
 template <Part PART, class S, class T>
@@ -1641,33 +1679,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   }
 
   // ---- the distribution
-  if (a.probs != nullptr) {
-    float* to = a.probs + b * a.probs_b + n * a.probs_n;
-    const float inv = d.token >= 0 ? float(kOne) / float(d.total) : 0.0f;
-    const Kept keep = {cut, cut.key == 0 ? -INFINITY : value_of(cut.key)};
-    const bool vectors = (reinterpret_cast<uintptr_t>(to) / 4 + kVec<T> - r.off) % 4 == 0;
-    const float far = -200.0f / sc.c;  // (what is further below has no weight)
-    stream<true>(r, r.v0, r.v1, [&](const uint4& w, int v) {
-      float x[kVec<T>], p[kVec<T>];
-      unpack(w, x);
-      const int i0 = v * kVec<T> - r.off;
-#pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) {
-        const float s = fmaxf(x[e] - sc.M, far), t = s * sc.c, lo = fmaf(s, sc.c, -t) + s * sc.c_lo;
-        const float q = ex2_approx(t) * inv;
-        p[e] = d.token >= 0 && keep(x[e], i0 + e) ? fmaf(q, lo * kLn2Hi, q) : 0.0f;
-      }
-      if (vectors && i0 >= 0 && i0 + kVec<T> <= a.V && ASV_GUARD(a, b < a.B && n < a.n)) {
-#pragma unroll
-        for (int e = 0; e < kVec<T>; e += 4)
-          __stcs(reinterpret_cast<float4*>(to + i0 + e), make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e)
-          if (i0 + e >= 0 && i0 + e < a.V) to[i0 + e] = p[e];
-      }
-    });
-  }
+  if (a.probs != nullptr)
+    write_distribution(a, r, sc, cut, d.token, d.token >= 0 ? float(kOne) / float(d.total) : 0.0f, b, n);
   row_sync();  // (no CTA goes on while its peers read its shared memory)
 }
 

@@ -1,4 +1,5 @@
-"""The numbers of light tokens: log-probabilities of tokens whose weight is next to the sums' unit of 2^-44."""
+"""The numbers of light tokens: log-probabilities of tokens whose weight is next to the sums' unit of 2^-44, and entries of
+distributions as far down as fp32 holds them."""
 import math
 
 import numpy as np
@@ -40,3 +41,23 @@ def test_log_probabilities_of_light_tokens(m, dtype, rows, V, gap, T):
         if n > 1:
             p = got.probs.cpu().double().numpy().reshape(-1, V)[np.arange(B * n), have]
             assert (np.abs(np.log(p) - logs) <= MASS + logprob_bound(lp)).all(), (kw, p[:3], logs[:3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 90])
+@pytest.mark.parametrize("T,top", [(1.0, 10.3), (0.75, 10.3), (3.0, -200.7), (0.0075, 0.103), (1.0, 1e-3)])
+def test_distributions_far_below_the_maximum(m, dtype, rows, T, top):
+    """Entries down to 2^-125 of the maximum, each to 2^-18 of itself: the mass, 0.75 2^-18 (sample_util); ex2, 2^-22; the mass in
+    fp32 and its reciprocal, two products and a sum, 5 * 2^-24.  The exponents are sums of two floats, off by 2^-40."""
+    V = 7001
+    x = (top - T * 86.5 * torch.rand(V, generator=torch.Generator().manual_seed(7))).to(dtype)
+    x[4321] = top
+    got = m.sample_tokens(x.cuda().expand(rows, 1, V), torch.full((rows, 1), 0.5, device="cuda"), temperature=T, probs=True)
+    y, T = x.double().numpy(), float(np.float32(T))
+    w = np.exp((y - y.max()) / T)
+    want = w / math.fsum(w)
+    have = got.probs[:, 0].double().cpu().numpy()
+    bound = 2.0 ** -18 * want + 2.0 ** -149
+    worst = (np.abs(have - want) / bound).max()
+    assert worst <= 1, (worst, np.log2(want[(np.abs(have - want) / bound).argmax() % V]))
