@@ -1532,14 +1532,15 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     const int count = PART == kRest ? 1 : warp == 0 ? min(nth, S::kThreads) : min(S::kList / 2 / r.ctas, S::kThreads * 3 / 4);
     float least_top = -INFINITY, most = -INFINITY;
     nth_largest(sh, count, least_top, most);
+    const float next_to = most > -INFINITY ? most : 0.0f;  // (next to a maximum of -inf nothing has a weight)
     float all = 0.0f;
     if (sums)
-      for (int w = 0; w < S::kWarps; ++w) all += sh.sums[w].y * ex2_approx((sh.sums[w].x - most) * c);
+      for (int w = 0; w < S::kWarps; ++w) all += sh.sums[w].y * ex2_approx((sh.sums[w].x - next_to) * c);
     float lead = 0.0f;
     if (sums) {
 #pragma unroll 4
       for (int i = lane; i < S::kThreads; i += 32)
-        lead += sh.tops[i] >= least_top ? ex2_approx((sh.tops[i] - most) * c) : 0.0f;
+        lead += sh.tops[i] >= least_top ? ex2_approx((sh.tops[i] - next_to) * c) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) lead += __shfl_xor_sync(0xffffffffu, lead, o);
     }
@@ -1586,6 +1587,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
     lead = __shfl_sync(0xffffffffu, first.y, 0);
   }
   bad = bad || M == -INFINITY;
+  // (numbers, also where CTAs hold nothing but -inf: what follows chooses by them)
+  (void)ASV_GUARD(r, !sums || bad || !(fabsf(M * c) < kFastRange) || (about >= 0.0f && lead >= 0.0f));
   const Scale sc = scale_of(M, c, c_lo);
 
   Drawn d = {-1, -INFINITY, 0};
