@@ -450,8 +450,9 @@ typedef struct {
  * the first is always kept.  The token is the lowest kept index i with  sum of w over kept indices <= i  >  u * W,  W the
  * kept mass; u is a number from [0, 1) that the caller draws (one outside counts as the nearest in it, NaN as 0).  Sums are
  * exact to about 2^-30 of their size where a border is near, and what weighs less than 2^-44 of the largest counts for
- * nothing in them (top_p 0.5 of two equal entries and next to nothing besides: the first alone).  So a token differs from
- * exact arithmetic's only where a border is that near, and does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.
+ * nothing in them; only where top_p of the mass is a whole number of equal largest entries but for that, does it decide
+ * (down to 2^-53 of the mass) whether the next of them is kept.  So a token differs from exact arithmetic's only where a
+ * border is that near, and does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.
  * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere; both to 2^-18 (typically 2^-23).
  * With temperature 0: 0, and 1 at the token.
  * Inputs may share memory, outputs not with anything; rows of out_probs need no alignment but the element's.

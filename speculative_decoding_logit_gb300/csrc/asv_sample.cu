@@ -608,6 +608,19 @@ __device__ __forceinline__ uint64_t part_of(uint64_t part, uint64_t mass) {
   return __umul64hi(part, mass) + (part * mass != 0 ? 1 : 0);
 }
 
+// Whether p of a mass is a whole number of the largest weights.  The border is then right behind some of several equal largest
+// entries, whose sums are exact, and what weighs less than a unit decides whether the next one is in.
+__device__ __forceinline__ bool even_border(uint64_t part, uint64_t mass) {
+  return part > 0 && part * mass == 0 && part_of(part, mass) % kOne == 0;
+}
+
+// A weight below 2^-44, in units of 2^-88, and whether a sum of them is more than 2^-53 of the mass, which 64 bits see.
+__device__ __forceinline__ uint64_t light_units(float x, float M, float c) {
+  const float t = (x - M) * c;
+  return t < -float(kSampleUnitBits) ? uint64_t(ex2_approx(t + 88.0f)) : 0;
+}
+__device__ __forceinline__ bool light_counts(uint64_t sum, uint64_t mass) { return sum > mass >> 9; }
+
 // Numbers 0 .. n - 1 (n <= kList) by bins: bin b has sh.scan[bin_start[b]] up to sh.scan[bin_ends()[b] - 1], in any order.
 // (Each candidate against each takes 1 us at 75 of them, this 2.5; at 350 they take 12 and 4.)
 template <class S, class F>
@@ -750,7 +763,8 @@ __device__ __noinline__ bool settle(S& sh, int n, int k, float p, uint64_t least
   if (p < 1.0f) {
     const uint64_t part = uint64_t(p * 18446744073709551616.0f);
     low = max(part_of(part, mass - min(off, mass)), uint64_t(1));
-    high = max(part_of(part, mass + off), uint64_t(1));
+    high = max(part_of(part, mass + off), uint64_t(1)) + (off > 0 ? 1 : 0);  // (the border itself is undecided too)
+    if (k > 0 && even_border(part, mass)) return false;
   }
   bool unsure = k == 0 && p < 1.0f && !closed && sum < high;
   // the kept ones are the first m
@@ -1276,6 +1290,46 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
   return cut;
 }
 
+// Where the border of a nucleus of part / 2^64 of the mass is even: the next of the equal largest entries comes into the cut if
+// what weighs less than a unit, of the entries in `within`, counts next to it.  True: one did.
+template <class S, class T>
+__device__ __noinline__ bool one_more(S& sh, const Row<T> r, const Scale sc, const Cut within, uint64_t part,
+                                      uint64_t mass, Cut& cut) {
+  const uint32_t top = key_of(sc.M);
+  if (!even_border(part, mass) || cut.key != top) return false;
+  if (threadIdx.x == 0) sh.least_key = ~0u;
+  __syncthreads();
+  uint64_t sum = 0;
+  uint32_t next = ~0u;
+  stream(r, r.v0, r.v1, [&](const uint4& w, int v) {
+    pairs<T>(w, [&](float x0, float x1, int e) {
+      const float x[2] = {x0, x1};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = v * kVec<T> - r.off + e + h;  // (an entry that is not the row's is -inf)
+        if (!within.keeps(key_of(x[h]), i)) continue;
+        sum += light_units(x[h], sc.M, sc.c);
+        if (key_of(x[h]) == top && i > cut.index) next = min(next, uint32_t(i));
+      }
+    });
+  });
+  sum = warp_sum(sum);
+  next = __reduce_min_sync(0xffffffffu, next);
+  if (threadIdx.x % 32 == 0) {
+    sh.run_mass[threadIdx.x / 32] = sum;  // (sh.chunk is still needed)
+    atomicMin(&sh.least_key, next);
+  }
+  row_sync();
+  const int lane = threadIdx.x % 32;
+  sum = 0;
+  for (int i = lane; i < r.ctas * S::kWarps; i += 32) sum += ld_peer_u64(sh.run_mass + i % S::kWarps, i / S::kWarps);
+  next = __reduce_min_sync(0xffffffffu, lane < r.ctas ? ld_peer_u32(&sh.least_key, lane) : ~0u);
+  row_sync();
+  if (next == ~0u || !light_counts(warp_sum(sum), mass)) return false;
+  cut.index = int(next);
+  return true;
+}
+
 // The smallest key whose weight is at least `least`, by a warp: 32 candidates at a time.
 template <class S>
 __device__ __noinline__ uint32_t least_key(S& sh, const Scale sc, uint64_t least) {
@@ -1653,9 +1707,14 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         if (nucleus) {
           const Cut first_k = cut;
           const uint64_t part = uint64_t(top_p * 18446744073709551616.0f);
-          auto target = [&](uint64_t all) { return max(part_of(part, all), uint64_t(1)); };
+          uint64_t mass = 0;
+          auto target = [&](uint64_t all) {
+            mass = all;
+            return max(part_of(part, all), uint64_t(1));
+          };
           summed = search_near<true>(sh, r, sc, first_k, target, true, cut);
           if (!summed) cut = search<true>(sh, r, sc, first_k, target);
+          if (one_more(sh, r, sc, first_k, part, mass, cut)) summed = false;
           if (cut.key == first_k.key) cut.index = min(cut.index, first_k.index);
         }
         if (least > 0) {

@@ -15,7 +15,7 @@ BF, F32 = torch.bfloat16, torch.float32
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows", [1, 90])
 @pytest.mark.parametrize("V", [5, 517, 30011])
-@pytest.mark.parametrize("equal,p", [(2, 0.5), (4, 0.25), (4, 0.75), (2000, 0.5)])
+@pytest.mark.parametrize("equal,p", [(2, 0.5), (4, 0.25), (4, 0.75), (2000, 0.5), (3, 0.0), (2000, 0.0)])
 @pytest.mark.parametrize("log_rest", [45.5, 47.0, 50.0, None])
 def test_even_borders(m, dtype, rows, V, equal, p, log_rest):
     if equal >= V:
@@ -31,7 +31,7 @@ def test_even_borders(m, dtype, rows, V, equal, p, log_rest):
         x[at] = 0.0
         u = torch.full((rows, 1), 0.9995)
         got = m.sample_tokens(x.cuda().expand(rows, 1, V), u.cuda(), temperature=T, top_k=k, top_p=p, probs=True)
-        kept = int(p * equal) + int(rest)
+        kept = int(p * equal) + int(rest) if p > 0 else 1    # (the first always)
         want = torch.zeros(V)
         want[at[:kept]] = 1.0 / kept
         assert not got.req_status.any()
