@@ -448,13 +448,14 @@ typedef struct {
  *   top_p  of these the ones before which less than top_p of their mass lies;
  *   min_p  those with w_i >= min_p;
  * the first is always kept.  The token is the lowest kept index i with  sum of w over kept indices <= i  >  u * W,  W the
- * kept mass; u is a number from [0, 1) that the caller draws (one outside counts as the nearest in it, NaN as 0).  Sums are
- * exact to about 2^-30 of their size where a border is near, and what weighs less than 2^-44 of the largest counts for
- * nothing in them; only where top_p of the mass is a whole number of equal largest entries but for that, does it decide
- * (down to 2^-53 of the mass) whether the next of them is kept.  So a token differs from exact arithmetic's only where a
- * border is that near, and does not depend on how the row is cut up.  out_logprobs (may be NULL): ln(w / W) of the token.
- * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries and 0 elsewhere; both to 2^-18 (typically 2^-23).
- * With temperature 0: 0, and 1 at the token.
+ * kept mass; u is a number from [0, 1) that the caller draws (one outside counts as the nearest in it, NaN as 0).  Where a
+ * border is near, weights are good to 2^-29 of themselves and rounded down to units of 2^-44 of the largest, so it lies within
+ * 2^-29 + V 2^-44 of the mass.  What weighs less than a unit counts for nothing; only where top_p of the mass is a whole number
+ * of equal largest entries but for that, does it decide (down to 2^-53 of the mass) whether the next of them is kept.  So a
+ * token differs from exact arithmetic's only where a border is that near, and does not depend on how the row is cut up.
+ * out_logprobs (may be NULL): ln(w / W) of the token, to 2^-18 and 2^-22 of its size (typically 2^-23).
+ * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries, to 2^-18 of each (typically 2^-23) and 2^-149, and 0
+ * elsewhere.  With temperature 0: 0, and 1 at the token.
  * Inputs may share memory, outputs not with anything; rows of out_probs need no alignment but the element's.
  * A row with NaN or +inf, or all -inf, flags its request ASV_REQ_NONFINITE (a single -inf is probability 0), a request's
  * own parameter out of range ASV_REQ_BAD_PARAM; the row's token is then -1, its log-probability -inf, its distribution 0.
