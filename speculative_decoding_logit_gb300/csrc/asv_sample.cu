@@ -1661,12 +1661,12 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
         if (lane == 0) sh.chunk[warp] = w;
       }
       // Where nothing depends on the mass below min-p's border, candidates end there (a little below it, for the
-      // roundings).
+      // roundings: of the maximum, the span, and of weights, as which exact ones decide).
       bool closed = false;
       if (greedy) {
         tau = sc.M;
       } else if (min_p > 0.0f && (k == 0 || !nucleus)) {
-        const float span = T_ * logf(min_p), border = sc.M + span - 1e-5f * (fabsf(sc.M) - span);
+        const float span = T_ * logf(min_p), border = sc.M + span - 1e-5f * (fabsf(sc.M) - span + T_);
         if (!(tau > border) || nth > S::kThreads || (nucleus && top_p * about > lead)) {
           tau = border;
           closed = true;
