@@ -454,8 +454,8 @@ typedef struct {
  * of equal largest entries but for that, does it decide (down to 2^-53 of the mass) whether the next of them is kept.  So a
  * token differs from exact arithmetic's only where a border is that near, and does not depend on how the row is cut up.
  * out_logprobs (may be NULL): ln(w / W) of the token, to 2^-18 and 2^-22 of its size (typically 2^-23).
- * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries, to 2^-18 of each (typically 2^-23) and 2^-149, and 0
- * elsewhere.  With temperature 0: 0, and 1 at the token.
+ * out_probs (may be NULL): [B, n] rows of V, w / W on the kept entries, to 2^-18 of each (typically 2^-23), and 0 elsewhere and
+ * for weights below 2^-126 of the largest.  With temperature 0: 0, and 1 at the token.
  * Inputs may share memory, outputs not with anything; rows of out_probs need no alignment but the element's.
  * A row with NaN or +inf, or all -inf, flags its request ASV_REQ_NONFINITE (a single -inf is probability 0), a request's
  * own parameter out of range ASV_REQ_BAD_PARAM; the row's token is then -1, its log-probability -inf, its distribution 0.
