@@ -1834,12 +1834,16 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.B * a.n;
   const int tuned = std::min(tuned_cluster(), kMaxCtas);
   // CTAs to a row: `share`, what all rows together leave room for, but no more than have enough of the row to be worth their
-  // exchanges; the most where distributions are wanted and the rows in hand would not stay in L2 until they are written
-  // (352 fp32 rows of 128,256: 179 us with three, 169 with eight).
-  auto ctas_of = [&](long long share, int least) {
+  // exchanges; where distributions are wanted, as many more as leave the rows in hand (of `room` CTAs) small enough to stay in L2
+  // until they are written, about half of it (fp32 rows: 352 of 128,256 239 us with two, 169 with eight; 700 of 50,257 206 with
+  // one, 145 with four, 161 with eight; 1500 of 16,384 109, 107 with two, 196; 4000 of 8192 143 with one, 430 with eight).
+  auto ctas_of = [&](long long share, int least, int room) {
     if (tuned > 0) return tuned;
-    const bool large = a.probs != nullptr && rows * a.V * (long long)sizeof(T) > (80ll << 20);
-    return int(std::clamp(std::min(large ? kMaxCtas : share, (long long)a.V / least), 1ll, (long long)kMaxCtas));
+    auto in_hand = [&](long long ctas) { return std::min(rows, room / ctas) * a.V * (long long)sizeof(T); };
+    long long ctas = std::min(share, (long long)kMaxCtas);
+    if (a.probs != nullptr)
+      while (in_hand(ctas) > (60ll << 20) && in_hand(kMaxCtas) < in_hand(ctas)) ++ctas;
+    return int(std::clamp(std::min(ctas, (long long)a.V / least), 1ll, (long long)kMaxCtas));
   };
   if (rows <= kSms / 2) {
     // One CTA to an SM, six to a row at most, where no row can have a large kept set (64 rows of 151,936, top-k 50: 15.6 us with
@@ -1849,14 +1853,15 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
     const bool few = (a.temperature == nullptr && a.one.temperature == 0.0f) ||
                      (a.top_k == nullptr && (a.one.top_k > 0 ? a.one.top_k <= 256 : !nucleus && !min_p));
     const long long share = few ? std::clamp(kSms / rows, 2ll, 6ll) : kSms * kAllCtas * 15 / 16 / rows;
-    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(share, 2048), kAllThreads, s);
+    return launch(sample_kernel<kAll, T, kAllThreads, kAllCtas>, a, rows, ctas_of(share, 2048, kSms * kAllCtas), kAllThreads, s);
   }
   // Many rows: small CTAs whose chains of exchanges overlap, some half of those that there is room for, four to a row at
   // most (300 rows of 151,936, top-p: 39 us with three, 49 with four; 150 rows 28.6 with four, 39 with eight; 600 58 with
   // two, 68 with one and 70 with three); and the few rows that need it in general behind them, where large clusters have
   // them at once.
   const long long share = std::min((kSms * kFirstCtas * 9 / 16 + rows - 1) / rows, 4ll);
-  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(share, 1024), kFirstThreads, s);
+  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(share, 1024, kSms * kFirstCtas),
+                               kFirstThreads, s);
   if (e != cudaSuccess) return e;
   return launch(sample_rest_kernel<T, kRestThreads, kRestCtas>, a, std::min(rows, (long long)kSms * kRestCtas / kMaxCtas),
                 kMaxCtas, kRestThreads, s);
