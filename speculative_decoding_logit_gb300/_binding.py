@@ -781,7 +781,7 @@ def paged_plan(cache_len: torch.Tensor, new_len: torch.Tensor, block_table: torc
         if not isinstance(max_tokens, int) or max_tokens < 0:
             raise AsvError(2, "max_tokens must be a whole number, 0 or more")
         i32 = dict(dtype=torch.int32, device=block_table.device)
-        B = block_table.shape[0]
+        B = block_table.shape[0] if block_table.dim() else 0  # (refused below)
         out = PagedPlanOutput(*_made_on(stream, lambda: (
             torch.zeros(B + 1, **i32), torch.empty(max_tokens, dtype=torch.int64, device=block_table.device),
             torch.empty(max_tokens, **i32), torch.empty(max_tokens, **i32), torch.zeros(B, **i32))))

@@ -78,3 +78,11 @@ def test_negative_entries_among_the_pages_given_back(m):
     assert plan.req_status.tolist() == [0, m.REQ_BAD_PAGE] and held.tolist() == [0, 0]
     assert pool.tolist() == [1, 4, 5, 6, -2, 7, 0] and count.tolist() == [6]
     assert table.tolist() == [[-1, -1, -9], [-1, -1, -1]]
+
+
+@pytest.mark.gpu
+def test_a_block_table_without_dimensions_is_refused(m):
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(m.AsvError) as e:
+        m.paged_plan(i, i, i[0], i, i, i, 16, max_tokens=3)
+    assert e.value.status == 2
