@@ -238,7 +238,8 @@ cudaError_t launch(const ARGS& a, cudaStream_t s) {
   // while there are more than 13 CTAs to an SM, and up to sixteen while there are more than 8 and a CTA's threads have
   // less than four vectors each, but not past four when its threads have ten each (9216 tokens of 576 vectors: 44 us at
   // one token to a CTA, 36 at four, 34.7 at eight; 16,883 of 768: 77 at two, 73 at four, 77 at eight, with positions of
-  // three axes 83.5, 79, 85; 3995 of 525: 21, 18.6 at two, 26 at eight; 15,713 of 60: 70, 17.8 at eight, 14.2 at sixteen).
+  // three axes 83.5, 79, 85; on the far side of ten vectors, 640: 9216 tokens 38 at four, 42 at eight, 16,883 63 and 66,
+  // 12,000 47.8 and 47.3, 40,000 138.4 and 137.7, and of 704 in heads of 40/2 53 and 52, 153 and 151; 3995 of 525: 21, 18.6 at two, 26 at eight; 15,713 of 60: 70, 17.8 at eight, 14.2 at sixteen).
   const long long vectors = (long long)(a.q_heads + 2 * a.c.kv_heads) * (a.c.head_dim / 8);
   int tokens = 1;
   auto ctas = [&]() { return (a.c.N + tokens - 1) / tokens; };

@@ -24,11 +24,13 @@
 // decisions from the same exchanged numbers.  Up to 76 rows one launch does all; above, a launch of small CTAs whose chains
 // of exchanges overlap, and one that has the rows it left, a cluster of eight large CTAs each.
 //
-// What bounds it (one call among others; the row's bytes at 6.79 TB/s in brackets): one row of 32,000, top-k, 11.4 us: four
-// exchanges of a cluster and code that runs once, 42 % of its waits for instructions; 64 bf16 rows of 151,936, top-p,
-// 23.0 [2.9], of which a row's chain is 19; 64 flat fp32 rows 77 [5.7]: 48 million warp instructions, 54 % of the issue slots;
-// 352 fp32 rows of 128,256 with distributions 168 [53]; 1024 mixed rows of 151,936 150 [46]: 86 for the first launch, 58 for
+// What bounds it (one call among others; the row's bytes at 6.79 TB/s in brackets): one row of 32,000, top-k, 11.1 us: four
+// exchanges of a cluster and code that runs once, 43 % of its waits for instructions; 64 bf16 rows of 151,936, top-p,
+// 23.4 [2.9], of which a row's chain is 19; 64 flat fp32 rows 80 [5.7]: 48 million warp instructions, 54 % of the issue slots;
+// 352 fp32 rows of 128,256 with distributions 170 [53]; 1024 mixed rows of 151,936 150 [46]: 86 for the first launch, 58 for
 // the few rows of the second, each a chain of some 20 exchanges.
+// What the bound of the candidates lives on is that large entries lie anywhere: where whole runs are masked, or logits fall with
+// the index, it admits too many, and the row takes the general way (one row at top-p 0.9: 14 us, with its last third masked 79).
 #include <algorithm>
 #include <climits>
 
@@ -990,7 +992,7 @@ __device__ __forceinline__ Bin find_bin(S& sh, const Row<T>& r, int bins, uint64
 // them by index.  False: it is not, or they are not.
 // `sums`: the warps' masses of what is kept are left in sh.chunk (behind a row_sync).
 // (64 flat fp32 rows of 151,936: an exact histogram, the bin's entries, and a draw by fast sums before the exact one took
-// 116 us, this takes 77.)
+// 116 us, this takes 80.)
 template <bool MASS, class S, class T, class G>
 __device__ __noinline__ bool search_near(S& sh, const Row<T> r, const Scale sc, const Cut within, G target_of, bool sums,
                                          Cut& cut) {
@@ -1371,7 +1373,8 @@ __device__ __forceinline__ uint64_t kept_sum(const uint4& w, int v, const Row<T>
   return sum;
 }
 
-// A draw from the whole row by the warps' fast sums (finer ones of fp32; sh.chunk, behind a row_sync).  A token < 0: too near a border to say.
+// A draw from the whole row by the warps' fast sums (finer ones of fp32; sh.chunk, behind a row_sync).  A token < 0: too near
+// a border to say.
 template <class S, class T>
 __device__ __noinline__ Drawn draw_fast(S& sh, const Row<T> r, const Scale sc, uint64_t draw) {
   const uint64_t at = find_run(sh, r, draw);
@@ -1516,7 +1519,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, S& sh, Row<T>& r
   constexpr int kFirstAhead = PART == kFirst ? kMostAhead : kAhead;  // (few CTAs to a row have more to do each)
   const bool nucleus = !greedy && top_p < 1.0f;
   const bool sums = PART != kRest && k == 0 && (nucleus || min_p == 0.0f);
-  // (16-bit rows would be bound by it: 1024 of 151,936, drawn from whole, 153 -> 235 us; without, 2 % of rows like Zipf's are
+  // (16-bit rows would be bound by it: 1024 of 151,936, drawn from whole, 235 us, 135 without; so 2 % of rows like Zipf's are
   // too near a border instead of 1 %, and 24 % of flat ones instead of 10)
   const bool fine = sizeof(T) == 4 && sums && !nucleus;
   float top = -INFINITY;
@@ -1846,9 +1849,10 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
     return int(std::clamp(std::min(ctas, (long long)a.V / least), 1ll, (long long)kMaxCtas));
   };
   if (rows <= kSms / 2) {
-    // One CTA to an SM, six to a row at most, where no row can have a large kept set (64 rows of 151,936, top-k 50: 15.6 us with
-    // two, 18.8 with eight; 16 rows 12.9 with six, 14.2 with eight); with a nucleus of any size four to an SM (64 flat rows: 77
-    // with eight, 111 with three).  Not quite all there is room for: 76 rows of eight take two turns, 33 us against 23.
+    // One CTA to an SM, six to a row at most, where no row can have a large kept set (64 rows of 151,936, top-k 50, in L2: 15.6 us
+    // with two, 18.8 with eight, out of HBM 20.4, 18.4 with three and 20.2 with eight; 16 rows 12.9 with six, 14.2 with eight);
+    // with a nucleus of any size four to an SM (64 flat rows: 80 with eight, 111 with three).  Not quite all there is room for:
+    // 76 rows of eight take two turns, 33 us against 23.
     const bool nucleus = a.top_p != nullptr || a.one.top_p < 1.0f, min_p = a.min_p != nullptr || a.one.min_p > 0.0f;
     const bool few = (a.temperature == nullptr && a.one.temperature == 0.0f) ||
                      (a.top_k == nullptr && (a.one.top_k > 0 ? a.one.top_k <= 256 : !nucleus && !min_p));
@@ -1860,8 +1864,8 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
   // two, 68 with one and 70 with three); and the few rows that need it in general behind them, where large clusters have
   // them at once.
   const long long share = std::min((kSms * kFirstCtas * 9 / 16 + rows - 1) / rows, 4ll);
-  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows, ctas_of(share, 1024, kSms * kFirstCtas),
-                               kFirstThreads, s);
+  const cudaError_t e = launch(sample_kernel<kFirst, T, kFirstThreads, kFirstCtas>, a, rows,
+                               ctas_of(share, 1024, kSms * kFirstCtas), kFirstThreads, s);
   if (e != cudaSuccess) return e;
   return launch(sample_rest_kernel<T, kRestThreads, kRestCtas>, a, std::min(rows, (long long)kSms * kRestCtas / kMaxCtas),
                 kMaxCtas, kRestThreads, s);
