@@ -1204,7 +1204,9 @@ __device__ __noinline__ Cut search(S& sh, const Row<T> r, const Scale sc, const 
           const int e = __ffs(some) - 1, i = v * kVec<T> - r.off + e;
           const float y = entry_of<T>(w, e);
           const uint32_t key = key_of(y);
-          if (bin_of(y) == first_bin && i >= 0 && i < r.V && within.keeps(key, i)) f(y, key, i);
+          // (the keys are tested too: the one between 0's and the largest negative number's is no value's, and where the
+          // bracket ends with it, 0 is not below its value, -0, but above it)
+          if (key >= lo && key <= hi && bin_of(y) == first_bin && i >= 0 && i < r.V && within.keeps(key, i)) f(y, key, i);
         }
       });
     };
